@@ -12,6 +12,15 @@
  *   pa_swap_blocks  copy whole blocks between two pools (GPU memory and host
  *                   memory), the swap step of residency changes.
  *
+ * Around them, the other work of a serving step on the same cache:
+ *
+ *   pa_rope_append_kv  rotate queries and keys by their positions and append;
+ *   pa_decode_tree     attention of several drafted tokens per sequence (a
+ *                      tree), and pa_compact_kv to commit the accepted ones;
+ *   pa_decode_scored, pa_evict_select, pa_compact_kv  accumulate the attention
+ *                      each cached token gets, choose the tokens to keep, and
+ *                      move them together.
+ *
  * Sources (web pages on PagedAttention):
  *   [A] "PagedAttention: From Operating System Virtual Memory to Large
  *       Language Model Memory Systems", section 2 Background — the attention
@@ -108,6 +117,7 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT 0x8u   /* a pipeline wait gave up (about 2 s); the output is not valid */
 #define PA_DEVERR_BAD_LEN 0x10u  /* decode: context_lens[s] > max_blocks_per_seq * block_size; clamped to that */
 #define PA_DEVERR_BAD_LAUNCH 0x20u /* a kernel refused its launch configuration; the output is not valid */
+#define PA_DEVERR_BAD_INDEX 0x40u /* compact: a kept index outside the sequence, or below its place; the row was not moved */
 
 /*
  * Bytes of scratch pa_decode needs for split-context partials (0 when no
@@ -363,6 +373,191 @@ PA_API pa_status pa_swap_blocks_quant(const int64_t *src_dst_pairs, int num_pair
                                       const void *src_v, void *dst_k, void *dst_v, int src_num_blocks,
                                       int dst_num_blocks, int num_kv_heads, int head_dim, int block_size,
                                       uint32_t *err_word, pa_stream_t stream);
+
+/*
+ * Rotary positions.  A pair (x_a, x_b) of a row at position n turns by the
+ * angle n * freqs[i]:
+ *   y_a = mscale * (x_a cos - x_b sin),  y_b = mscale * (x_b cos + x_a sin)
+ * for i < rot_dim / 2, with (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1)
+ * when interleaved.  Elements from rot_dim on pass through unchanged (mscale
+ * does not apply to them).  The angle's fraction of a turn is formed in
+ * 64-bit fixed point, so positions up to 2^31 lose nothing; the sine, the
+ * cosine and the rotation are fp32, rounded once to dtype.
+ */
+typedef enum {
+    PA_ROPE_PLAIN = 0,  /* base^(-2i / rot_dim) */
+    PA_ROPE_LINEAR = 1, /* every frequency divided by factor (positions interpolated) */
+    PA_ROPE_BASE = 2,   /* the base enlarged to base * factor^(rot_dim / (rot_dim - 2)) */
+    PA_ROPE_RAMP = 3    /* by wavelength: pairs turning at least `high` times over original_len keep their
+                         * frequency, those turning at most `low` times have it divided by factor, linear
+                         * in the number of turns between */
+} pa_rope_scaling;
+
+/*
+ * The rotation frequencies (radians per position) of a scaled rotary scheme:
+ * writes rot_dim / 2 doubles to HOST memory, to be copied to the device by
+ * the caller.  rot_dim even and positive, base > 0, factor > 0;
+ * PA_ROPE_RAMP needs original_len > 0 and 0 <= low < high.
+ */
+PA_API pa_status pa_rope_frequencies(double *freqs, int rot_dim, double base, pa_rope_scaling scaling,
+                                     double factor, double original_len, double low, double high);
+
+/*
+ * Rotate rows: out[i][h][:] = the rotation above of x[i][h][:] at
+ * positions[i] (int32; negative positions turn backwards).
+ *   x, out        [num_tokens] rows of num_heads * head_dim elements of dtype,
+ *                 x_stride / out_stride elements apart (>= num_heads * head_dim);
+ *                 out may be x itself (with the same stride), and must not
+ *                 overlap it otherwise
+ *   freqs         device double [rot_dim / 2], finite
+ *   rot_dim       even, 2 .. head_dim
+ *   direction     1, or -1 to turn by the negated angle: the gradient of the
+ *                 rotation (out = gradient of x for x = gradient of out)
+ * num_tokens == 0 returns PA_OK without launching.
+ */
+PA_API pa_status pa_rope(void *out, const void *x, const int32_t *positions, const double *freqs, int num_tokens,
+                         int num_heads, int head_dim, int rot_dim, long long x_stride, long long out_stride,
+                         int interleaved, int direction, float mscale, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * pa_rope on the queries and pa_append_kv of the rotated keys and of the
+ * values, in one pass: for every token i
+ *   q_out[i][h][:] = rotation of q[i][h][:]
+ *   k_cache[slot / block_size][h][slot % block_size][:] = rotation of k[i][h][:]
+ *   v_cache[...] = v[i][h][:]
+ * with slot = slot_mapping[i]; a negative slot is padding (its query is
+ * rotated, nothing is appended), one outside the pool is skipped and flagged,
+ * and a slot named twice holds one of its rows, as for pa_append_kv.
+ *   q, k, v       rows of num_heads (q) or num_kv_heads (k, v) * head_dim
+ *                 elements of dtype, q_stride, k_stride, v_stride elements
+ *                 apart (slices of one fused projection, for instance)
+ *   q_out         densely packed [num_tokens][num_heads][head_dim]; may be q
+ *                 when q is dense
+ * The caches must be 16-byte aligned; rows and strides that are not a
+ * multiple of 16 bytes are accepted (and moved element by element).
+ */
+PA_API pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, const void *v,
+                                   const int32_t *positions, const int64_t *slot_mapping, const double *freqs,
+                                   void *k_cache, void *v_cache, int num_tokens, int num_heads, int num_kv_heads,
+                                   int head_dim, int rot_dim, long long q_stride, long long k_stride,
+                                   long long v_stride, int block_size, int num_blocks, int interleaved, float mscale,
+                                   pa_dtype dtype, uint32_t *err_word, pa_stream_t stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache: the check step of
+ * speculative decoding.  Sequence s holds context_lens[s] cached tokens, the
+ * last draft_lens[s] of them drafted (their K/V appended in draft order, like
+ * any token's); the ones before are committed.  Query i of the sequence (its
+ * i-th drafted token) attends every committed token, and drafted token j when
+ * bit j % 64 of tree_mask[s][i][j / 64] is set:
+ *   out[s][i][h] = sum_t exp(x_t - max x) v_t / sum_t exp(x_t - max x),
+ *   x_t = scale * <q[s][i][h], k_t>  over those tokens
+ * and 0 when there is none.  Rows i >= draft_lens[s] are padding: out is 0.
+ *   q, out        [num_seqs][num_draft][num_heads][head_dim]
+ *   draft_lens    int32 [num_seqs]; NULL: num_draft everywhere.  Values
+ *                 outside [0, min(num_draft, context_lens[s])] are clamped to
+ *                 it and flagged (PA_DEVERR_BAD_LEN)
+ *   tree_mask     uint64 [num_seqs][num_draft][ceil(num_draft / 64)] (bits
+ *                 from draft_lens[s] on are ignored); NULL: token j <= i, the
+ *                 drafted tokens are a chain
+ *   num_draft     1 .. 256
+ *   partition_size  as pa_decode; 0 = chosen from the batch size and
+ *                 max_blocks_per_seq so that every SM has work
+ *   workspace     pa_decode_tree_workspace_size() bytes, 16-byte aligned
+ *                 (may be NULL when that size is 0)
+ * A drafted token that some query does not attend has no influence on it,
+ * whatever its K and V hold (infinities and NaN too).  Other arguments and
+ * limits as pa_decode (window 0).
+ */
+PA_API pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, const int32_t *context_lens, const int32_t *draft_lens,
+                                const uint64_t *tree_mask, int num_seqs, int num_draft, int num_heads,
+                                int num_kv_heads, int head_dim, int block_size, float scale, pa_dtype dtype,
+                                pa_dtype out_dtype, int max_blocks_per_seq, int num_blocks, int partition_size,
+                                void *workspace, size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
+
+/* Bytes of workspace pa_decode_tree needs (0 when no sequence can span more
+ * than one partition, and for bad arguments). */
+PA_API size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num_heads, int num_kv_heads,
+                                            int head_dim, int block_size, int max_blocks_per_seq,
+                                            int partition_size);
+
+/*
+ * pa_decode that also accumulates how much attention each cached token gets,
+ * the score by which pa_evict_select chooses:
+ *   scores_out[s][kvh][t] = scores_in[s][kvh][t] + sum_h w[s][h][t]
+ * over the num_heads / num_kv_heads query heads h of kv head kvh, with w the
+ * softmax weight of token t (0 for a token left out because of a bad table
+ * entry), for t < context_lens[s]; entries from there on are left as they
+ * were.  The sum over heads is in a fixed order: the same inputs give the
+ * same bits.
+ *   scores_out, scores_in  fp32 [num_seqs][num_kv_heads][scores_stride],
+ *                 scores_stride >= max_blocks_per_seq * block_size; scores_in
+ *                 may be scores_out itself, or NULL (zeros)
+ *   workspace     pa_decode_scored_workspace_size() bytes, 16-byte aligned
+ *                 (the scores of every query head are kept there between the
+ *                 passes)
+ * Other arguments, limits and results as pa_decode with window 0.
+ */
+PA_API pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in, const void *q,
+                                  const void *k_cache, const void *v_cache, const int32_t *block_tables,
+                                  const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                  int head_dim, int block_size, float scale, long long scores_stride, pa_dtype dtype,
+                                  pa_dtype out_dtype, int max_blocks_per_seq, int num_blocks, int partition_size,
+                                  void *workspace, size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
+
+/* Bytes of workspace pa_decode_scored needs (0 for bad arguments). */
+PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int block_size,
+                                              int max_blocks_per_seq, int partition_size);
+
+/*
+ * Which cached tokens to keep.  With L = context_lens[s] and
+ * n = min(L, budget), for every kv head:
+ *   L <= budget: all tokens;
+ *   else the last `recent` tokens, and of the tokens before them the
+ *   budget - recent with the largest scores (of equal scores the lowest
+ *   index; a NaN counts as larger than any number).
+ *   keep          int32 [num_seqs][num_kv_heads][budget] (written): the kept
+ *                 tokens in ascending order, then -1
+ *   new_lens      int32 [num_seqs] (written): n
+ *   scores_out    fp32 [num_seqs][num_kv_heads][scores_stride] (written): the
+ *                 kept tokens' scores at 0 .. n - 1, then zeros to the end of
+ *                 the row.  May be scores itself; NULL: not written
+ *   scores        fp32, same shape
+ *   budget >= 1, 0 <= recent <= budget; a context longer than scores_stride
+ *   is clamped to it and flagged (PA_DEVERR_BAD_LEN)
+ */
+PA_API pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores_out, const float *scores,
+                                 const int32_t *context_lens, int num_seqs, int num_kv_heads, int budget, int recent,
+                                 long long scores_stride, uint32_t *err_word, pa_stream_t stream);
+
+/*
+ * Move kept rows to the front: for every sequence s, kv head h and
+ * i < keep_lens[s], with j = keep[s][h or 0][i] and b = base_lens[s],
+ *   token b + i (through the destination table) takes the K and V rows of
+ *   token b + j (through block_tables), kv head h: a bit-exact copy.
+ * The movement of an eviction (keep from pa_evict_select, base_lens NULL), and
+ * the commit of accepted drafted tokens (base_lens the committed lengths,
+ * keep the accepted drafted tokens of the sequence, keep_heads 1).
+ *   keep          int32 [num_seqs][keep_heads][keep_stride], keep_heads
+ *                 num_kv_heads or 1 (the same list for every kv head)
+ *   keep_lens     int32 [num_seqs], clamped to [0, keep_stride]
+ *   base_lens     int32 [num_seqs], or NULL (zeros)
+ *   dst_block_tables  int32 [num_seqs][dst_max_blocks_per_seq], or NULL: in
+ *                 place, through block_tables.  In place needs j >= i.  The
+ *                 destination blocks must not be read by the call otherwise
+ *                 (blocks shared with another sequence are sources only)
+ * An index outside [0, max_blocks_per_seq * block_size - b) or, in place,
+ * below i, and a place outside the destination table, move nothing and are
+ * flagged (PA_DEVERR_BAD_INDEX); a table entry outside the pool likewise
+ * (PA_DEVERR_BAD_BLOCK).
+ */
+PA_API pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep, const int32_t *keep_lens,
+                               const int32_t *base_lens, const int32_t *block_tables,
+                               const int32_t *dst_block_tables, int num_seqs, int keep_heads, int keep_stride,
+                               int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
+                               int dst_max_blocks_per_seq, int num_blocks, pa_dtype dtype, uint32_t *err_word,
+                               pa_stream_t stream);
 
 /* Static text for a status code. */
 PA_API const char *pa_status_string(pa_status status);

@@ -74,6 +74,19 @@ PA_API pa_status pa_bm_free_sequence(pa_bm *bm, int seq);
 PA_API pa_status pa_bm_append(pa_bm *bm, const int32_t *seqs, int n, int64_t *slots, int64_t *pairs,
                               int pairs_cap, int *num_pairs, int *placed);
 
+/* Cut a sequence to its first `length` tokens (at most its length): the blocks
+ * past them lose one reference.  Drafted tokens that were not accepted, or the
+ * rows behind an in-place pa_compact_kv.  Not available for window sequences. */
+PA_API pa_status pa_bm_truncate(pa_bm *bm, int seq, long long length);
+
+/* Give a sequence ceil(length / block_size) blocks from the free list in place
+ * of its own, and that length: the destination of a pa_compact_kv into other
+ * blocks.  The old blocks lose one reference (export the tables before this
+ * call: pa_compact_kv reads them, and nothing else may be enqueued that writes
+ * blocks handed out after it).  PA_ERR_NO_BLOCKS, with nothing changed, when
+ * the free list is too short.  Not available for window sequences. */
+PA_API pa_status pa_bm_renew(pa_bm *bm, int seq, long long length);
+
 /* Tokens held by a sequence (-1 if it does not exist). */
 PA_API long long pa_bm_length(const pa_bm *bm, int seq);
 

@@ -20,6 +20,10 @@ _lib.pa_bm_free_sequence.argtypes = [P, I]
 _lib.pa_bm_free_sequence.restype = I
 _lib.pa_bm_append.argtypes = [P, P, I, P, P, I, P, P]
 _lib.pa_bm_append.restype = I
+_lib.pa_bm_truncate.argtypes = [P, I, ctypes.c_longlong]
+_lib.pa_bm_truncate.restype = I
+_lib.pa_bm_renew.argtypes = [P, I, ctypes.c_longlong]
+_lib.pa_bm_renew.restype = I
 _lib.pa_bm_length.argtypes = [P, I]
 _lib.pa_bm_length.restype = ctypes.c_longlong
 _lib.pa_bm_tables.argtypes = [P, P, P]
@@ -85,6 +89,15 @@ class BlockManager:
     def extend(self, seq: int, ntokens: int):
         """Place ntokens tokens at the end of one sequence."""
         return self.append([seq] * ntokens)
+
+    def truncate(self, seq: int, length: int) -> None:
+        """Cut a sequence to its first `length` tokens; whole blocks past them are dropped."""
+        _check(_lib.pa_bm_truncate(self._h, seq, length))
+
+    def renew(self, seq: int, length: int) -> None:
+        """Replace a sequence's blocks by fresh ones for `length` tokens (the
+        destination of pa_compact_kv); its old blocks are dropped."""
+        _check(_lib.pa_bm_renew(self._h, seq, length))
 
     def length(self, seq: int) -> int:
         return int(_lib.pa_bm_length(self._h, seq))

@@ -180,6 +180,44 @@ pa_status pa_bm_append(pa_bm *bm, const int32_t *seqs, int n, int64_t *slots, in
     return st;
 }
 
+pa_status pa_bm_truncate(pa_bm *bm, int seq, long long length) {
+    if (!bm || !bm->valid(seq) || !bm->seqs[seq].live || bm->seqs[seq].ring || length < 0 ||
+        length > bm->seqs[seq].length)
+        return PA_ERR_INVALID_ARGUMENT;
+    pa_bm::Seq &s = bm->seqs[seq];
+    const size_t blocks = static_cast<size_t>((length + bm->block_size - 1) / bm->block_size);
+    while (s.table.size() > blocks) {
+        bm->drop(s.table.back());
+        s.table.pop_back();
+    }
+    s.length = length;
+    return PA_OK;
+}
+
+pa_status pa_bm_renew(pa_bm *bm, int seq, long long length) {
+    if (!bm || !bm->valid(seq) || !bm->seqs[seq].live || bm->seqs[seq].ring || length < 0)
+        return PA_ERR_INVALID_ARGUMENT;
+    const long long blocks = length / bm->block_size + (length % bm->block_size != 0);
+    if (blocks > bm->max_blocks)
+        return PA_ERR_INVALID_ARGUMENT;
+    if (blocks > static_cast<long long>(bm->free_list.size()))
+        return PA_ERR_NO_BLOCKS;
+    pa_bm::Seq &s = bm->seqs[seq];
+    std::vector<int32_t> fresh;
+    try {
+        fresh.resize(static_cast<size_t>(blocks));
+    } catch (...) {  // no exception crosses the C interface
+        return PA_ERR_NO_BLOCKS;
+    }
+    for (int32_t &b : fresh)
+        bm->take(&b);
+    for (int32_t b : s.table)
+        bm->drop(b);
+    s.table.swap(fresh);
+    s.length = length;
+    return PA_OK;
+}
+
 long long pa_bm_length(const pa_bm *bm, int seq) {
     if (!bm || !bm->valid(seq) || !bm->seqs[seq].live)
         return -1;

@@ -21,6 +21,7 @@
 #include "pa_decode_q8.cuh"
 #include "pa_decode_q8f.cuh"
 #include "pa_decode_q8t.cuh"
+#include "pa_host.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -35,8 +36,6 @@ const void *reduce_kernel(int head_dim, bool wide) {
     return nullptr;
 }
 
-namespace {
-
 thread_local std::string g_detail;
 
 pa_status fail(pa_status st, const std::string &why) {
@@ -48,13 +47,6 @@ pa_status cuda_fail(cudaError_t e, const char *what) {
     g_detail = std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")";
     return PA_ERR_CUDA;
 }
-
-int elt_bytes(int dtype) { return dtype == PA_F32 ? 4 : 2; }
-bool dtype_ok(int dtype) { return dtype == PA_F32 || dtype == PA_F16 || dtype == PA_BF16; }
-bool code_dtype_ok(int dtype) { return dtype == PA_I8 || dtype == PA_E4M3; }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool block_size_ok(int bs) { return bs == 8 || bs == 16 || bs == 32; }
-bool head_dim_ok(int d) { return d == 64 || d == 128; }
 
 // Per-device facts and per-kernel launch settings, filled on first use.
 std::mutex g_mu;
@@ -207,7 +199,7 @@ pa_status kv_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_
 // cache; a contiguous cache's tiles of one kv head are consecutive) and lands
 // in shared memory as 8-row groups of both 128-byte halves (128-byte swizzle).
 pa_status kv_tensor_map_groups(CUtensorMap *map, const void *base, int dtype, int block_size, long long tiles,
-                               int box_tiles = 1) {
+                               int box_tiles) {
     const TmKey key{2, base, dtype, block_size, tiles, box_tiles, 0};
     if (tm_lookup(key, map))
         return PA_OK;
@@ -283,12 +275,6 @@ pa_status q8_page_tensor_map(CUtensorMap *map, const void *base, int block_size,
     return PA_OK;
 }
 
-constexpr int kDefaultPartition = 512;
-// The tensor-core kernels (grouped heads over 16-bit K/V, and over E4M3
-// pages) pay more per item (query load, the merge of the quarters, partials):
-// their default partition is twice as long.  pa_decode_workspace_size(..., 0) sizes for the shorter one, which
-// needs at least as much.
-constexpr int kGqaDefaultPartition = 1024;
 // The block size contiguous caches are cut into (their tiles: TMA boxes).
 constexpr int kContiguousBlock = 16;
 constexpr int kQ8fStageBudget = 48 * 1024;
@@ -322,12 +308,6 @@ bool q8t_tensor_core_path(int num_heads, int num_kv_heads, int head_dim, int blo
            (q_dtype == PA_F16 || q_dtype == PA_BF16);
 }
 
-struct DecodePlan {
-    int bpp = 0;
-    int max_parts = 0;
-    size_t workspace = 0;
-};
-
 pa_status plan_decode(int num_seqs, int num_heads, int head_dim, int block_size, int max_blocks_per_seq,
                       int window, int partition_size, DecodePlan *plan) {
     if (num_seqs < 0 || num_heads <= 0 || max_blocks_per_seq <= 0 || window < 0)
@@ -353,8 +333,6 @@ pa_status plan_decode(int num_seqs, int num_heads, int head_dim, int block_size,
         plan->workspace = 0;
     return PA_OK;
 }
-
-}  // namespace
 
 void set_last_error_detail(const char *why) { g_detail = why; }
 
@@ -402,7 +380,7 @@ unsigned int *work_counter(int device, cudaStream_t stream) {
 
 // The partition reduce: a warp per row when there are rows enough to fill the
 // GPU and few partitions each, else a CTA per row.
-static cudaError_t launch_reduce(DecodeParams &p, int head_dim, long long rows, cudaStream_t cs) {
+cudaError_t launch_reduce(DecodeParams &p, int head_dim, long long rows, cudaStream_t cs) {
     int dev = 0, sms = 0;
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess)
@@ -437,7 +415,8 @@ pa_status launch_decode_kernel(DecodeParams &p, int dtype, int head_dim, int G, 
         return fail(PA_ERR_UNSUPPORTED, "contiguous caches take one query head per kv head, or 2, 4 or 8 with "
                                         "fp16 / bf16 K/V and head_dim 128");
     if (gqa_tc) {
-        fn = dtype == PA_F16 ? decode_gqa_kernel_f16(block_size, G) : decode_gqa_kernel_bf16(block_size, G);
+        fn = p.logits ? (dtype == PA_F16 ? scored_gqa_kernel_f16(block_size, G) : scored_gqa_kernel_bf16(block_size, G))
+                      : (dtype == PA_F16 ? decode_gqa_kernel_f16(block_size, G) : decode_gqa_kernel_bf16(block_size, G));
         p.stages = kGqaStages;
         smem = gqa_smem_layout(kGqaStages).total;
         threads = kGqaThreads;
@@ -457,9 +436,14 @@ pa_status launch_decode_kernel(DecodeParams &p, int dtype, int head_dim, int G, 
         if (ts != PA_OK)
             return ts;
     } else if (mha) {
-        fn = dtype == PA_F32   ? decode_mha_kernel_f32(head_dim, block_size)
-             : dtype == PA_F16 ? decode_mha_kernel_f16(head_dim, block_size)
-                               : decode_mha_kernel_bf16(head_dim, block_size);
+        if (p.logits)
+            fn = dtype == PA_F32   ? scored_mha_kernel_f32(head_dim, block_size)
+                 : dtype == PA_F16 ? scored_mha_kernel_f16(head_dim, block_size)
+                                   : scored_mha_kernel_bf16(head_dim, block_size);
+        else
+            fn = dtype == PA_F32   ? decode_mha_kernel_f32(head_dim, block_size)
+                 : dtype == PA_F16 ? decode_mha_kernel_f16(head_dim, block_size)
+                                   : decode_mha_kernel_bf16(head_dim, block_size);
         // the stages form one sub-ring per consumer warp: a multiple of their count
         int S = kMhaStageBudget / (2 * tile);
         S -= S % kMhaWarps;
@@ -473,9 +457,14 @@ pa_status launch_decode_kernel(DecodeParams &p, int dtype, int head_dim, int G, 
         if (ts != PA_OK)
             return ts;
     } else {
-        fn = dtype == PA_F32   ? decode_kernel_f32(head_dim, G)
-             : dtype == PA_F16 ? decode_kernel_f16(head_dim, G)
-                               : decode_kernel_bf16(head_dim, G);
+        if (p.logits)
+            fn = dtype == PA_F32   ? scored_kernel_f32(head_dim, G)
+                 : dtype == PA_F16 ? scored_kernel_f16(head_dim, G)
+                                   : scored_kernel_bf16(head_dim, G);
+        else
+            fn = dtype == PA_F32   ? decode_kernel_f32(head_dim, G)
+                 : dtype == PA_F16 ? decode_kernel_f16(head_dim, G)
+                                   : decode_kernel_bf16(head_dim, G);
         int S = kStageBudget / (2 * tile);
         S = S < 2 ? 2 : (S > 8 ? 8 : S);
         p.stages = S;

@@ -71,7 +71,18 @@ struct DecodeParams {
     // (s * num_kv_heads + h) * max_blocks_per_seq + b); the MHA and
     // tensor-core grouped-head kernels only
     int contiguous = 0;
+    // Scored decode (the kernels' Log variants) only: every attended token's
+    // score in base-2 units, [num_seqs][num_heads][logits_stride] (-inf for a
+    // token left out because of a bad table entry), for the pass that turns
+    // them into weights once the rows' maxima and denominators are known
+    float *logits = nullptr;
+    long long logits_stride = 0;
 };
+
+// A score of the scored decode (row = sequence * num_heads + head).
+__device__ inline void store_logit(const DecodeParams &p, long long row, int tok, float x) {
+    p.logits[row * p.logits_stride + tok] = x;
+}
 
 // Tile index (into the [tiles][block_size][D] view of a cache) of table entry
 // or logical block `pb` of sequence s and kv head h.
@@ -243,7 +254,7 @@ struct StageMeta {
     int slot;   // item slot (item counter mod stages)
     int lo;     // first attended row of the block
     int hi;     // one past the last attended row
-    int flags;  // kValid | kFirst | kLast | kEnd | kHasQ
+    int flags;  // kValid | kFirst | kLast | kEnd | kHasQ, and the block's index in its partition << 8
 };
 constexpr int kValid = 1, kFirst = 2, kLast = 4, kEnd = 8, kHasQ = 16;
 
@@ -426,7 +437,7 @@ __device__ inline void decode_producer(const DecodeParams &p, char *smem, const 
                 mt.hi = hi;
                 const bool with_q = (j == 0 && nb > 0);
                 mt.flags = (pb >= 0 ? kValid : 0) | (j == 0 ? kFirst : 0) | (j == nst - 1 ? kLast : 0) |
-                           (with_q ? kHasQ : 0);
+                           (with_q ? kHasQ : 0) | (j << 8);
                 meta[stage] = mt;
                 if (j == 0) {
                     ItemInfo it;
@@ -489,7 +500,7 @@ __device__ inline void decode_producer(const DecodeParams &p, char *smem, const 
     __syncwarp();
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool Log>
 __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const SmemLayout &L) {
     using C = DecodeCfg<T, D, G>;
     constexpr int E = C::kEpl;
@@ -514,6 +525,8 @@ __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const 
     float qf[G][E];
     float m[G], l[G], acc[G][E];
     ItemInfo cur = {0, 0, 0, 1};
+    // first token of a stage's block (Log variants: no window, so partitions start at token 0)
+    auto blk_tok0 = [&](const StageMeta &mt) { return (cur.part * p.bpp + (mt.flags >> 8)) * p.block_size; };
 
     uint32_t t = 0;
     int k = 0;
@@ -566,6 +579,14 @@ __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const 
                     sc[g] = x;
                 }
                 Elt<T>::unpack(ld_shared_v4(vb + r * C::kRow + li * 16), vf);
+                if constexpr (Log) {
+                    if (act && li == 0) {
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+                            store_logit(p, static_cast<long long>(cur.s) * p.num_heads + cur.kvh * G + g,
+                                        blk_tok0(mt) + r, sc[g]);
+                    }
+                }
                 if (act) {
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
@@ -579,6 +600,15 @@ __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const 
                         m[g] = mn;
                     }
                 }
+            }
+        }
+        if constexpr (Log) {
+            if (!(mt.flags & kValid)) {  // a block left out: no weight
+                for (int r = mt.lo + warp * 32 + lane; r < mt.hi; r += kConsumerWarps * 32)
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        store_logit(p, static_cast<long long>(cur.s) * p.num_heads + cur.kvh * G + g,
+                                    blk_tok0(mt) + r, -INFINITY);
             }
         }
         __syncwarp();
@@ -643,6 +673,13 @@ __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const 
                 }
                 const int h = cur.kvh * G + g;
                 const long long row = static_cast<long long>(cur.s) * p.num_heads + h;
+                if constexpr (Log) {
+                    if (dd == 0) {  // the score pass wants every row's state
+                        const long long pr = row * p.max_parts + cur.part;
+                        p.part_ml[pr * 2] = M;
+                        p.part_ml[pr * 2 + 1] = den;
+                    }
+                }
                 if (cur.nparts == 1 && !p.force_partial) {
                     store_out(p.out, p.out_dtype, row * D + dd, den > 0.f ? num / den : 0.f);
                 } else {
@@ -668,7 +705,7 @@ __device__ inline void decode_consumer(const DecodeParams &p, char *smem, const 
     }
 }
 
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool Log = false>
 __global__ void __launch_bounds__(kDecodeThreads) pa_decode_kernel(const DecodeParams p) {
     // the next kernel on the stream may be launched now (it waits for this
     // grid); this one waits for the kernel before it
@@ -697,7 +734,7 @@ __global__ void __launch_bounds__(kDecodeThreads) pa_decode_kernel(const DecodeP
     if ((threadIdx.x >> 5) == kConsumerWarps)
         decode_producer<T, D, G>(p, smem, L);
     else
-        decode_consumer<T, D, G>(p, smem, L);
+        decode_consumer<T, D, G, Log>(p, smem, L);
 }
 
 // Merge the partitions of every multi-partition (sequence, head):

@@ -605,7 +605,7 @@ __device__ inline bool gqa_exchange(const float *v, float *all, float *xbuf, uin
 }
 
 // Softmax and epilogue warps.
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool Log>
 __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaLayout &L, uint32_t tmem) {
     using C = GqaCfg<T, BS, G>;
     const int warp = threadIdx.x >> 5;
@@ -708,6 +708,13 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
                     den = fmaf(all[w * 2 * G + G + h], sc, den);
                 }
             }
+            if constexpr (Log) {
+                if (row == 0) {  // the score pass wants every row's state
+                    const long long pr = (row0 + h) * p.max_parts + it.part;
+                    p.part_ml[pr * 2] = M;
+                    p.part_ml[pr * 2 + 1] = den;
+                }
+            }
             if (it.nparts == 1 && !p.force_partial) {
                 store_out(p.out, p.out_dtype, (row0 + h) * C::kD + row, den > 0.f ? num / den : 0.f);
             } else {
@@ -785,6 +792,10 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 const float x = valid ? sc[h] * p.scale_log2 : -INFINITY;
+                if constexpr (Log) {
+                    if (tok >= it.tok_lo && tok < it.tok_hi)
+                        store_logit(p, static_cast<long long>(it.s) * p.num_heads + it.kvh * G + h, tok, x);
+                }
                 float mt = x;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
@@ -842,7 +853,7 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
     return true;
 }
 
-template <typename T, int BS, int G>
+template <typename T, int BS, int G, bool Log = false>
 __global__ void __launch_bounds__(kGqaThreads, 1)
     pa_decode_gqa_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq,
@@ -922,7 +933,7 @@ __global__ void __launch_bounds__(kGqaThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
     } else {
-        const bool ok = gqa_softmax<T, BS, G>(p, smem, L, tmem);
+        const bool ok = gqa_softmax<T, BS, G, Log>(p, smem, L, tmem);
         if (!ok && (threadIdx.x & 31) == 0 && p.err)
             atomicOr(p.err, PA_DEVERR_TIMEOUT);
         tc_fence_before();

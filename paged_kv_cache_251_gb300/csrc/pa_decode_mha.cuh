@@ -365,7 +365,7 @@ __device__ inline void mha_producer(const DecodeParams &p, const CUtensorMap *tm
     __syncwarp();
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, bool Log>
 __device__ inline void mha_consumer(const DecodeParams &p, char *smem, const MhaLayout &L) {
     using C = MhaCfg<T, D, BS>;
     constexpr int kDpl = C::kDpl;
@@ -448,6 +448,10 @@ __device__ inline void mha_consumer(const DecodeParams &p, char *smem, const Mha
                     for (int o = C::kTpr; o < 32; o <<= 1)
                         sc += __shfl_xor_sync(0xffffffffu, sc, o);
                     sc = (r >= lo && r < hi) ? sc * p.scale_log2 : -INFINITY;
+                    if constexpr (Log) {
+                        if (part == 0 && r >= lo && r < hi)
+                            store_logit(p, static_cast<long long>(it.s) * p.num_heads + it.kvh, blk * BS + r, sc);
+                    }
                     float mr = sc;
 #pragma unroll
                     for (int o = 1; o < C::kTpr; o <<= 1)
@@ -477,6 +481,10 @@ __device__ inline void mha_consumer(const DecodeParams &p, char *smem, const Mha
                         }
                     }
                 }
+            } else if constexpr (Log) {  // a block left out: no weight
+                const int tok = (it.blk_lo + j) * BS + lane;
+                if (lane < BS && tok >= it.tok_lo && tok < it.tok_hi)
+                    store_logit(p, static_cast<long long>(it.s) * p.num_heads + it.kvh, tok, -INFINITY);
             }
             __syncwarp();
             if (lane == 0)
@@ -522,6 +530,12 @@ __device__ inline void mha_consumer(const DecodeParams &p, char *smem, const Mha
             den = fmaf(mml[(b * kMhaWarps + w2) * 2 + 1], scl[w2], den);
         }
         const long long rowi = static_cast<long long>(it.s) * p.num_heads + it.kvh;
+        if constexpr (Log) {
+            if (warp == 0 && lane == 0) {  // the score pass wants every row's state
+                p.part_ml[(rowi * p.max_parts + it.part) * 2] = M;
+                p.part_ml[(rowi * p.max_parts + it.part) * 2 + 1] = den;
+            }
+        }
         for (int dd = warp * 32 + lane; dd < D; dd += kMhaWarps * 32) {
             float num = 0.f;
 #pragma unroll
@@ -546,7 +560,7 @@ __device__ inline void mha_consumer(const DecodeParams &p, char *smem, const Mha
         atomicOr(p.err, PA_DEVERR_TIMEOUT);
 }
 
-template <typename T, int D, int BS>
+template <typename T, int D, int BS, bool Log = false>
 __global__ void __launch_bounds__(kMhaThreads) pa_decode_mha_kernel(const DecodeParams p,
                                                                    const __grid_constant__ CUtensorMap tmk,
                                                                    const __grid_constant__ CUtensorMap tmv) {
@@ -590,7 +604,7 @@ __global__ void __launch_bounds__(kMhaThreads) pa_decode_mha_kernel(const Decode
     if ((threadIdx.x >> 5) == kMhaWarps)
         mha_producer<T, D, BS>(p, &tmk, &tmv, smem, L);
     else
-        mha_consumer<T, D, BS>(p, smem, L);
+        mha_consumer<T, D, BS, Log>(p, smem, L);
     __syncthreads();
     release_claims(p);
 }

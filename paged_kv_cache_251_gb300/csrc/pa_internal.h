@@ -47,6 +47,17 @@ const void *decode_mha_kernel_bf16(int head_dim, int block_size);
 const void *decode_gqa_kernel_f16(int block_size, int group);
 const void *decode_gqa_kernel_bf16(int block_size, int group);
 
+// The same kernels with every token's score written out (DecodeParams::logits),
+// for the scored decode.
+const void *scored_kernel_f32(int head_dim, int group);
+const void *scored_kernel_f16(int head_dim, int group);
+const void *scored_kernel_bf16(int head_dim, int group);
+const void *scored_mha_kernel_f32(int head_dim, int block_size);
+const void *scored_mha_kernel_f16(int head_dim, int block_size);
+const void *scored_mha_kernel_bf16(int head_dim, int block_size);
+const void *scored_gqa_kernel_f16(int block_size, int group);
+const void *scored_gqa_kernel_bf16(int block_size, int group);
+
 // General decode kernels for 8-bit caches (INT8 / E4M3 codes with row
 // scales), per head_dim and query group; nullptr if not built.
 const void *decode_q8_kernel_i8(int head_dim, int group);

@@ -1,0 +1,225 @@
+// Rotary positions, alone and fused with the KV append.
+//
+// y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t) with
+// t = position * freq_i.  The angle is kept as a fraction of a turn in 64-bit
+// fixed point: freq_i / 2 pi is a 0.64 fraction (from the caller's double),
+// and position times it wraps modulo one turn exactly, so a far position loses
+// nothing and no 64-bit floating arithmetic runs per position.  Its top 32
+// bits, as a signed fraction in [-1/2, 1/2) turn, go to sincospif: the angle
+// is off by at most 2^-33 turn plus one fp32 rounding.
+//
+// The rows are read once and written once: HBM-bound, or launch-bound for a
+// decode step.  A CTA takes `tok` tokens.  It first forms their rot / 2
+// (cos, sin) pairs once, in shared memory (every head of a token shares
+// them), then its threads are x lanes by y rows: lane x of a row holds the
+// same E elements of both halves (or E adjacent ones, interleaved) of every
+// row it takes, so its angles of a token stay in registers while it walks the
+// rows.
+#include <cuda_runtime.h>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_internal.h"
+#include "pa_rope.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxTok = 8;
+
+__device__ inline float load_f(const float *p) { return *p; }
+__device__ inline float load_f(const __half *p) { return __half2float(*p); }
+__device__ inline float load_f(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ inline void store_f(float *p, float v) { *p = v; }
+__device__ inline void store_f(__half *p, float v) { *p = __float2half_rn(v); }
+__device__ inline void store_f(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// E consecutive elements of T: one 16-byte access when E fills it, else one
+// element (E == 1).
+template <typename T, int E> struct Vec {
+    uint4 r;
+    __device__ inline void load(const T *p) { r = *reinterpret_cast<const uint4 *>(p); }
+    __device__ inline void store(T *p) const { *reinterpret_cast<uint4 *>(p) = r; }
+    __device__ inline void get(float *f) const { Elt<T>::unpack(r, f); }
+    __device__ inline void set(const float *f) {
+        T *t = reinterpret_cast<T *>(&r);
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            store_f(t + i, f[i]);
+    }
+};
+template <typename T> struct Vec<T, 1> {
+    T r;
+    __device__ inline void load(const T *p) { r = *p; }
+    __device__ inline void store(T *p) const { *p = r; }
+    __device__ inline void get(float *f) const { f[0] = load_f(&r); }
+    __device__ inline void set(const float *f) { store_f(&r, f[0]); }
+};
+
+// Lanes of a row: the pair lanes, then the lanes that copy the elements past
+// rot.  Half layout: a pair lane holds elements [E x, E x + E) of both halves.
+// Interleaved: E / 2 adjacent pairs (one pair when E == 1), in `P` elements.
+template <int E, bool Inter> struct RopeUnit {
+    static constexpr int kPairs = Inter ? (E == 1 ? 1 : E / 2) : E;  // pairs of a pair lane
+};
+
+template <typename T, int E, bool Inter>
+__device__ inline void rotate_unit(const T *src, T *dst, int x, int half, const float *c, const float *s) {
+    constexpr int P = RopeUnit<E, Inter>::kPairs;
+    if constexpr (!Inter) {
+        Vec<T, E> a, b;
+        a.load(src + x * E);
+        b.load(src + half + x * E);
+        float fa[E], fb[E], ya[E], yb[E];
+        a.get(fa);
+        b.get(fb);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            ya[i] = fa[i] * c[i] - fb[i] * s[i];
+            yb[i] = fb[i] * c[i] + fa[i] * s[i];
+        }
+        a.set(ya);
+        b.set(yb);
+        a.store(dst + x * E);
+        b.store(dst + half + x * E);
+    } else if constexpr (E == 1) {
+        const float a = load_f(src + 2 * x), b = load_f(src + 2 * x + 1);
+        store_f(dst + 2 * x, a * c[0] - b * s[0]);
+        store_f(dst + 2 * x + 1, b * c[0] + a * s[0]);
+    } else {
+        Vec<T, E> a;
+        a.load(src + x * E);
+        float f[E], y[E];
+        a.get(f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            y[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * s[i];
+            y[2 * i + 1] = f[2 * i + 1] * c[i] + f[2 * i] * s[i];
+        }
+        a.set(y);
+        a.store(dst + x * E);
+    }
+}
+
+template <typename T, int E, bool Inter>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+    constexpr int P = RopeUnit<E, Inter>::kPairs;
+    pdl_launch_dependents();
+    extern __shared__ float2 trig[];  // [tok][rot / 2]
+    pdl_wait();
+    const int half = p.rot / 2;
+    const long long tok0 = static_cast<long long>(blockIdx.x) * p.tok;
+    const int ntok = static_cast<int>(min(static_cast<long long>(p.tok), p.num_tokens - tok0));
+    for (int i = threadIdx.x; i < ntok * half; i += kRopeThreads) {
+        const int t = i / half, j = i - t * half;
+        // a fraction of a turn per position, in units of 2^-64 turn
+        double turns = p.freqs[j] * 0.15915494309189533577;
+        turns -= floor(turns);
+        const unsigned long long frac = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+        const long long pos = static_cast<long long>(p.positions[tok0 + t]) * p.direction;
+        const unsigned long long angle = frac * static_cast<unsigned long long>(pos);
+        float sn, cs;
+        sincospif(static_cast<float>(static_cast<int>((angle + 0x80000000ull) >> 32)) * 4.656612873077393e-10f, &sn,
+                  &cs);
+        trig[i] = make_float2(cs * p.mscale, sn * p.mscale);
+    }
+    __syncthreads();
+    const int pair_lanes = half / P;
+    const int lanes = pair_lanes + (p.head_dim - p.rot) / E;  // lanes of a row
+    const int rows_at_once = kRopeThreads / lanes;
+    const int y = threadIdx.x / lanes;
+    const int x = threadIdx.x - y * lanes;
+    if (y >= rows_at_once)
+        return;
+    const bool pair = x < pair_lanes;
+    const int copy_at = pair ? 0 : p.rot + (x - pair_lanes) * E;
+    const T *qg = static_cast<const T *>(p.q), *kg = static_cast<const T *>(p.k), *vg = static_cast<const T *>(p.v);
+    T *qo = static_cast<T *>(p.q_out), *kc = static_cast<T *>(p.k_cache), *vc = static_cast<T *>(p.v_cache);
+    const long long pool_slots = static_cast<long long>(p.num_blocks) * p.block_size;
+    for (int t = 0; t < ntok; ++t) {
+        const long long tok = tok0 + t;
+        float c[P], s[P];
+        if (pair) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 cs = trig[t * half + x * P + i];
+                c[i] = cs.x, s[i] = cs.y;
+            }
+        }
+        auto move = [&](const T *src, T *dst) {
+            if (pair) {
+                rotate_unit<T, E, Inter>(src, dst, x, half, c, s);
+            } else {
+                Vec<T, E> v;
+                v.load(src + copy_at);
+                v.store(dst + copy_at);
+            }
+        };
+#pragma unroll 2
+        for (int h = y; h < p.num_heads; h += rows_at_once)
+            move(qg + tok * p.q_stride + h * p.head_dim, qo + tok * p.q_out_stride + h * p.head_dim);
+        if (p.num_kv_heads == 0)
+            continue;
+        const long long slot = p.slots[tok];
+        if (slot < 0)
+            continue;  // padding
+        if (slot >= pool_slots) {
+            if (p.err && threadIdx.x == 0)
+                atomicOr(p.err, PA_DEVERR_BAD_SLOT);
+            continue;
+        }
+        const long long phys = slot / p.block_size;
+        const long long off = slot - phys * p.block_size;
+        const long long step = static_cast<long long>(p.block_size) * p.head_dim;  // kv head to kv head
+        const long long at = phys * p.num_kv_heads * step + off * p.head_dim;
+#pragma unroll 2
+        for (int h = y; h < p.num_kv_heads; h += rows_at_once)
+            move(kg + tok * p.k_stride + h * p.head_dim, kc + at + h * step);
+#pragma unroll 2
+        for (int h = y; h < p.num_kv_heads; h += rows_at_once) {
+            const T *src = vg + tok * p.v_stride + h * p.head_dim;
+            T *dst = vc + at + h * step;
+            for (int e = x * E; e < p.head_dim; e += lanes * E) {
+                Vec<T, E> v;
+                v.load(src + e);
+                v.store(dst + e);
+            }
+        }
+    }
+}
+
+template <typename T, int E> const void *rope_fn(bool inter) {
+    return inter ? reinterpret_cast<const void *>(&rope_kernel<T, E, true>)
+                 : reinterpret_cast<const void *>(&rope_kernel<T, E, false>);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(RopeParams p, int dtype, int interleaved, int num_sms, cudaStream_t stream) {
+    const int elt = elt_bytes(dtype), E = 16 / elt;
+    const auto wide = [&](const void *ptr, long long stride) { return aligned16(ptr) && stride % E == 0; };
+    // 16-byte accesses need every row and both halves of a row on a 16-byte
+    // boundary; anything else goes element by element
+    const bool vec = (interleaved ? p.rot % E == 0 : (p.rot / 2) % E == 0) && wide(p.q, p.q_stride) &&
+                     wide(p.q_out, p.q_out_stride) &&
+                     (p.num_kv_heads == 0 || (wide(p.k, p.k_stride) && wide(p.v, p.v_stride)));
+    const void *fn;
+    if (dtype == PA_F32)
+        fn = vec ? rope_fn<float, 4>(interleaved) : rope_fn<float, 1>(interleaved);
+    else if (dtype == PA_F16)
+        fn = vec ? rope_fn<__half, 8>(interleaved) : rope_fn<__half, 1>(interleaved);
+    else
+        fn = vec ? rope_fn<__nv_bfloat16, 8>(interleaved) : rope_fn<__nv_bfloat16, 1>(interleaved);
+    // tokens per CTA: enough CTAs for every SM first, then more work per CTA
+    long long tok = p.num_tokens / (8LL * num_sms);
+    tok = tok < 1 ? 1 : (tok > kRopeMaxTok ? kRopeMaxTok : tok);
+    p.tok = static_cast<int>(tok);
+    const long long grid = (p.num_tokens + tok - 1) / tok;
+    void *args[] = {&p};
+    return launch_dependent(fn, dim3(static_cast<unsigned>(grid)), dim3(kRopeThreads), args,
+                            static_cast<size_t>(p.tok) * (p.rot / 2) * sizeof(float2), stream);
+}
+
+}  // namespace pa

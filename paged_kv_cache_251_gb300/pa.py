@@ -18,8 +18,11 @@ LIB_PATH = Path(__file__).resolve().parent / "_lib" / "libpa.so"
 PA_OK, PA_ERR_INVALID_ARGUMENT, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA = range(5)
 PA_F32, PA_F16, PA_BF16, PA_I8, PA_E4M3 = 0, 1, 2, 3, 4
 DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_BAD_PAIR, DEVERR_TIMEOUT, DEVERR_BAD_LEN, DEVERR_BAD_LAUNCH = 1, 2, 4, 8, 16, 32
+DEVERR_BAD_INDEX = 64
 
 DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+# rotary frequency scalings of pa_rope_frequencies
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
 # 8-bit caches: code pools are int8 or float8_e4m3fn tensors, scales float32
 CODE_DTYPE = {torch.int8: PA_I8, torch.float8_e4m3fn: PA_E4M3}
 
@@ -65,6 +68,25 @@ def _load():
     lib.pa_copy_blocks_quant.restype = I
     lib.pa_swap_blocks_quant.argtypes = [P, I, P, P, P, P, I, I, I, I, I, P, P]
     lib.pa_swap_blocks_quant.restype = I
+    D, LL = ctypes.c_double, ctypes.c_longlong
+    lib.pa_rope_frequencies.argtypes = [P, I, D, I, D, D, D, D]
+    lib.pa_rope_frequencies.restype = I
+    lib.pa_rope.argtypes = [P, P, P, P, I, I, I, I, LL, LL, I, I, F, I, P]
+    lib.pa_rope.restype = I
+    lib.pa_rope_append_kv.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, LL, LL, LL, I, I, I, F, I, P, P]
+    lib.pa_rope_append_kv.restype = I
+    lib.pa_decode_tree.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_decode_tree.restype = I
+    lib.pa_decode_tree_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
+    lib.pa_decode_tree_workspace_size.restype = SZ
+    lib.pa_decode_scored.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, F, LL, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_decode_scored.restype = I
+    lib.pa_decode_scored_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.pa_decode_scored_workspace_size.restype = SZ
+    lib.pa_evict_select.argtypes = [P, P, P, P, P, I, I, I, I, LL, P, P]
+    lib.pa_evict_select.restype = I
+    lib.pa_compact_kv.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
+    lib.pa_compact_kv.restype = I
     lib.pa_status_string.argtypes = [I]
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_last_error_detail.argtypes = []
@@ -387,6 +409,312 @@ def pa_swap_blocks_quant(src_dst_pairs: torch.Tensor, src_k: torch.Tensor, src_v
     _check(_lib.pa_swap_blocks_quant(_ptr(src_dst_pairs), src_dst_pairs.numel() // 2, _ptr(src_k), _ptr(src_v),
                                      _ptr(dst_k), _ptr(dst_v), snb, dnb, hkv, d, bs, _ptr(err_word),
                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Serving-step operators (rotary positions, tree attention, scored decode,
+# eviction)
+
+
+def _one_device(*ts) -> torch.device:
+    """The tensors' common CUDA device; every tensor must be on it."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("every tensor must be on one device")
+    return dev
+
+
+def _call(fn, device: torch.device, stream, *args) -> None:
+    """Run a library call on `stream` (default: the device's current one) with
+    `device` current."""
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is on another device than the tensors")
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(stream)))
+
+
+def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _int32(**ts) -> None:
+    for name, t in ts.items():
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError(f"{name} must be int32")
+
+
+def _ws_bytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _ws(nbytes: int, device) -> torch.Tensor | None:
+    return torch.empty((nbytes + 15) // 16 * 4, dtype=torch.float32, device=device) if nbytes else None
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """The row stride, in elements, of a [tokens, heads, d] tensor whose rows are
+    dense (a slice of a wider projection, for instance)."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if n and ((h > 1 and t.stride(1) != d) or t.stride(2) != 1):
+        raise ValueError(f"{name}: each token's heads must be dense")
+    return t.stride(0) if n > 1 else h * d
+
+
+def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                        original_len: float = 0.0, low: float = 1.0, high: float = 4.0) -> torch.Tensor:
+    """Rotation frequencies (radians per position) as a CPU double tensor
+    [rot_dim / 2]: scaling "none", "linear", "base" or "ramp" (see
+    include/pa.h).  Copy it to the GPU once and pass it to the rope calls."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    out = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    _check(_lib.pa_rope_frequencies(_ptr(out), int(rot_dim), float(base), ROPE_SCALING[scaling], float(factor),
+                                    float(original_len), float(low), float(high)))
+    return out
+
+
+def pa_rope(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor,
+            interleaved: bool = False, inverse: bool = False, mscale: float = 1.0, stream=None) -> torch.Tensor:
+    """out[i, h] = x[i, h] rotated to positions[i] (back by it when inverse:
+    the gradient of the rotation).  rot_dim is 2 * freqs.numel(); out may be x."""
+    dev = _one_device(out, x, positions, freqs)
+    n, h, d = x.shape
+    _shape(out, x.shape, "out")
+    _shape(positions, (n,), "positions")
+    _int32(positions=positions)
+    if freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise TypeError("freqs must be a double vector")
+    if out.dtype != x.dtype:
+        raise TypeError("out and x must share one dtype")
+    _cuda(positions, freqs)
+    _call(_lib.pa_rope, dev, stream, _ptr(out), _ptr(x), _ptr(positions), _ptr(freqs), n, h, d, 2 * freqs.numel(),
+          _rows(x, "x"), _rows(out, "out"), int(interleaved), -1 if inverse else 1, float(mscale),
+          DTYPE_CODE[x.dtype])
+    return out
+
+
+def pa_rope_append_kv(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                      positions: torch.Tensor, slot_mapping: torch.Tensor, freqs: torch.Tensor,
+                      k_cache: torch.Tensor, v_cache: torch.Tensor, interleaved: bool = False, mscale: float = 1.0,
+                      err_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotate q into q_out and k into its cache slots, store v in its slots (see
+    include/pa.h).  q, k and v may be slices of one projection: their rows may
+    be any distance apart."""
+    dev = _one_device(q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, err_word)
+    n, h, d = q.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    _shape(q_out, q.shape, "q_out")
+    _shape(k, (n, hkv, d), "k")
+    _shape(v, (n, hkv, d), "v")
+    _shape(k_cache, (nb, hkv, bs, d), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(positions, (n,), "positions")
+    _shape(slot_mapping, (n,), "slot_mapping")
+    _int32(positions=positions)
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise TypeError("freqs must be a double vector")
+    if len({q_out.dtype, q.dtype, k.dtype, v.dtype, k_cache.dtype, v_cache.dtype}) != 1:
+        raise TypeError("q, k, v, q_out and the caches must share one dtype")
+    _cuda(q_out, positions, slot_mapping, freqs, k_cache, v_cache, err_word)
+    _call(_lib.pa_rope_append_kv, dev, stream, _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions),
+          _ptr(slot_mapping), _ptr(freqs), _ptr(k_cache), _ptr(v_cache), n, h, hkv, d, 2 * freqs.numel(),
+          _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), bs, nb, int(interleaved), float(mscale), DTYPE_CODE[q.dtype],
+          _ptr(err_word))
+    return q_out
+
+
+def pa_decode_tree_workspace_size(num_seqs: int, num_draft: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                  block_size: int, max_blocks_per_seq: int, partition_size: int = 0) -> int:
+    return int(_lib.pa_decode_tree_workspace_size(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size,
+                                                  max_blocks_per_seq, partition_size))
+
+
+def tree_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int,
+                       partition_size: int = 0) -> torch.Tensor | None:
+    """A workspace tensor for pa_decode_tree (None if 0 bytes)."""
+    n, t, h, d = q.shape
+    return _ws(pa_decode_tree_workspace_size(n, t, h, k_cache.shape[1], d, k_cache.shape[2], max_blocks_per_seq,
+                                             partition_size), q.device)
+
+
+def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
+    """The mask of pa_decode_tree for trees given by parents, an integer tensor
+    [N, T]: parents[s, i] < i is the drafted token before token i, or negative
+    when it follows the last committed token.  A token attends itself and its
+    ancestors.  Returns int64 [N, T, ceil(T / 64)] on the device of parents."""
+    n, t = parents.shape
+    p = parents.to("cpu", torch.int64)
+    if bool((p >= torch.arange(t)).any()):
+        raise ValueError("a token's parent must come before it")
+    seen = torch.zeros((n, t, t), dtype=torch.bool)
+    rows = torch.arange(n)
+    for i in range(t):
+        up = p[:, i]
+        seen[:, i] = seen[rows, up.clamp_min(0)] & (up >= 0)[:, None]
+        seen[:, i, i] = True
+    words = (t + 63) // 64
+    bits = torch.zeros((n, t, words * 64), dtype=torch.int64)
+    bits[:, :, :t] = seen
+    one = torch.ones(64, dtype=torch.int64) << torch.arange(64)
+    return (bits.view(n, t, words, 64) * one).sum(-1).to(parents.device)
+
+
+def _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d) -> tuple:
+    nb, hkv, bs, d2 = k_cache.shape
+    _shape(k_cache, (nb, hkv, bs, d), "k_cache")
+    _shape(v_cache, k_cache.shape, "v_cache")
+    _shape(context_lens, (n,), "context_lens")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [N, max_blocks_per_seq]")
+    _int32(block_tables=block_tables, context_lens=context_lens)
+    if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
+        raise TypeError("q, k_cache and v_cache must share one dtype")
+    return nb, hkv, bs
+
+
+def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_tables: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor | None = None,
+                   draft_lens: torch.Tensor | None = None, scale: float | None = None, partition_size: int = 0,
+                   workspace: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of each sequence's drafted tokens (q, out: [N, T, H, d]) over
+    its committed tokens and the drafted ones its mask names; the drafted
+    tokens are the last draft_lens[s] of the context_lens[s] cached ones.
+    tree_mask None: a chain (see include/pa.h)."""
+    dev = _one_device(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace,
+                      err_word)
+    _cuda(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, err_word)
+    n, t, h, d = q.shape
+    nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
+    _shape(out, q.shape, "out")
+    _int32(draft_lens=draft_lens)
+    if draft_lens is not None:
+        _shape(draft_lens, (n,), "draft_lens")
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int64:
+            raise TypeError("tree_mask must be int64 (64 bits a word)")
+        _shape(tree_mask, (n, t, (t + 63) // 64), "tree_mask")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = tree_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
+    _call(_lib.pa_decode_tree, dev, stream, _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+          _ptr(context_lens), _ptr(draft_lens), _ptr(tree_mask), n, t, h, hkv, d, bs, float(scale),
+          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, int(partition_size),
+          _ptr(workspace), _ws_bytes(workspace), _ptr(err_word))
+    return out
+
+
+def pa_decode_scored_workspace_size(num_seqs: int, num_heads: int, head_dim: int, block_size: int,
+                                    max_blocks_per_seq: int, partition_size: int = 0) -> int:
+    return int(_lib.pa_decode_scored_workspace_size(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq,
+                                                    partition_size))
+
+
+def scored_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int,
+                         partition_size: int = 0) -> torch.Tensor | None:
+    """A workspace tensor for pa_decode_scored (None if 0 bytes)."""
+    n, h, d = q.shape
+    return _ws(pa_decode_scored_workspace_size(n, h, d, k_cache.shape[2], max_blocks_per_seq, partition_size),
+               q.device)
+
+
+def pa_decode_scored(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     scores_in: torch.Tensor | None = None, scale: float | None = None, partition_size: int = 0,
+                     workspace: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """pa_decode, and scores_out[s, kvh, t] = scores_in[s, kvh, t] (None: 0) +
+    the softmax weights token t gets from the kv head's query heads (see
+    include/pa.h).  Scores are fp32 [N, H_kv, at least max_blocks * block_size]."""
+    dev = _one_device(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace,
+                      err_word)
+    _cuda(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace, err_word)
+    n, h, d = q.shape
+    nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
+    _shape(out, q.shape, "out")
+    if scores_out.dim() != 3 or tuple(scores_out.shape[:2]) != (n, hkv):
+        raise ValueError("scores_out must be [N, H_kv, tokens]")
+    if scores_in is not None:
+        _shape(scores_in, scores_out.shape, "scores_in")
+    for t in (scores_out, scores_in):
+        if t is not None and t.dtype != torch.float32:
+            raise TypeError("scores must be float32")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = scored_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
+    _call(_lib.pa_decode_scored, dev, stream, _ptr(out), _ptr(scores_out), _ptr(scores_in), _ptr(q), _ptr(k_cache),
+          _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), n, h, hkv, d, bs, float(scale),
+          scores_out.shape[2], DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb,
+          int(partition_size), _ptr(workspace), _ws_bytes(workspace), _ptr(err_word))
+    return out
+
+
+def pa_evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores_out: torch.Tensor | None,
+                    scores: torch.Tensor, context_lens: torch.Tensor, budget: int, recent: int,
+                    err_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The cached tokens every kv head keeps: its `recent` last ones and those of
+    the others with the largest scores, `budget` in all, ascending in keep
+    [N, H_kv, budget] (-1 past new_lens); their scores move to the front of
+    scores_out (which may be scores, or None).  See include/pa.h."""
+    dev = _one_device(keep, new_lens, scores_out, scores, context_lens, err_word)
+    _cuda(keep, new_lens, scores_out, scores, context_lens, err_word)
+    if scores.dim() != 3 or scores.dtype != torch.float32:
+        raise TypeError("scores must be float32 [N, H_kv, tokens]")
+    n, hkv, stride = scores.shape
+    if scores_out is not None:
+        _shape(scores_out, scores.shape, "scores_out")
+        if scores_out.dtype != torch.float32:
+            raise TypeError("scores_out must be float32")
+    _shape(keep, (n, hkv, budget), "keep")
+    _shape(new_lens, (n,), "new_lens")
+    _shape(context_lens, (n,), "context_lens")
+    _int32(keep=keep, new_lens=new_lens, context_lens=context_lens)
+    _call(_lib.pa_evict_select, dev, stream, _ptr(keep), _ptr(new_lens), _ptr(scores_out), _ptr(scores),
+          _ptr(context_lens), n, hkv, int(budget), int(recent), stride, _ptr(err_word))
+    return keep
+
+
+def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tensor, keep_lens: torch.Tensor,
+                  block_tables: torch.Tensor, dst_block_tables: torch.Tensor | None = None,
+                  base_lens: torch.Tensor | None = None, err_word: torch.Tensor | None = None, stream=None) -> None:
+    """Token base_lens[s] + i takes the K/V rows of token base_lens[s] +
+    keep[s, h, i], for i < keep_lens[s] (keep [N, H_kv or 1, n]): in place, or
+    into the blocks of dst_block_tables.  See include/pa.h."""
+    dev = _one_device(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
+    _cuda(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
+    nb, hkv, bs, d = k_cache.shape
+    _shape(v_cache, k_cache.shape, "v_cache")
+    if v_cache.dtype != k_cache.dtype:
+        raise TypeError("the caches must share one dtype")
+    if keep.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("keep must be [N, H_kv or 1, n] and block_tables [N, max_blocks_per_seq]")
+    n = keep.shape[0]
+    _int32(keep=keep, keep_lens=keep_lens, block_tables=block_tables, dst_block_tables=dst_block_tables,
+           base_lens=base_lens)
+    for name, t in (("block_tables", block_tables), ("dst_block_tables", dst_block_tables)):
+        if t is not None and (t.dim() != 2 or t.shape[0] != n):
+            raise ValueError(f"{name} must be [N, max_blocks_per_seq]")
+    for name, t in (("keep_lens", keep_lens), ("base_lens", base_lens)):
+        if t is not None:
+            _shape(t, (n,), name)
+    _call(_lib.pa_compact_kv, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(keep), _ptr(keep_lens),
+          _ptr(base_lens), _ptr(block_tables), _ptr(dst_block_tables), n, keep.shape[1], keep.shape[2], hkv, d, bs,
+          block_tables.shape[1], 0 if dst_block_tables is None else dst_block_tables.shape[1], nb,
+          DTYPE_CODE[k_cache.dtype], _ptr(err_word))
 
 
 def version() -> tuple[int, int, int]:
