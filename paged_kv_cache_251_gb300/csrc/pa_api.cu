@@ -193,14 +193,14 @@ pa_status kv_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_
     return PA_OK;
 }
 
-// 5-D view of a 16-bit K or V cache with head_dim 128 for the tensor-core
-// kernel: [tile = block * H_kv + head][row / 8][half][row % 8][64 elements];
+// 5-D view of a 16-bit K or V cache (head_dim 64 or 128) for the tensor-core
+// kernels: [tile = block * H_kv + head][row / 8][half][row % 8][64 elements];
 // one box is `box_tiles` consecutive whole (block, head) tiles (1 for a paged
 // cache; a contiguous cache's tiles of one kv head are consecutive) and lands
 // in shared memory as 8-row groups of both 128-byte halves (128-byte swizzle).
 pa_status kv_tensor_map_groups(CUtensorMap *map, const void *base, int dtype, int block_size, long long tiles,
-                               int box_tiles) {
-    const TmKey key{2, base, dtype, block_size, tiles, box_tiles, 0};
+                               int box_tiles, int head_dim) {
+    const TmKey key{2, base, dtype, block_size, tiles, box_tiles, head_dim};
     if (tm_lookup(key, map))
         return PA_OK;
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
@@ -208,10 +208,11 @@ pa_status kv_tensor_map_groups(CUtensorMap *map, const void *base, int dtype, in
     if (e != cudaSuccess || !enc)
         return cuda_fail(e == cudaSuccess ? cudaErrorSymbolNotFound : e, "cuTensorMapEncodeTiled lookup");
     const CUtensorMapDataType dt = dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const cuuint64_t row = 256;  // bytes per token row (128 x 2 bytes)
-    cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(block_size / 8), static_cast<cuuint64_t>(tiles)};
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+    const cuuint32_t halves = static_cast<cuuint32_t>(head_dim / 64);
+    cuuint64_t dims[5] = {64, 8, halves, static_cast<cuuint64_t>(block_size / 8), static_cast<cuuint64_t>(tiles)};
     cuuint64_t strides[4] = {row, 128, 8 * row, row * block_size};
-    cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(block_size / 8), static_cast<cuuint32_t>(box_tiles)};
+    cuuint32_t box[5] = {64, 8, halves, static_cast<cuuint32_t>(block_size / 8), static_cast<cuuint32_t>(box_tiles)};
     cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = enc(map, dt, 5, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -239,6 +240,34 @@ pa_status q_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_d
     cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elt), static_cast<cuuint32_t>(group)};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(PA_ERR_INVALID_ARGUMENT,
+                    "cuTensorMapEncodeTiled rejected the query layout (code " + std::to_string(static_cast<int>(r)) + ")");
+    tm_store(key, *map);
+    return PA_OK;
+}
+
+// 3-D view of the drafted tokens' queries [num_seqs * num_draft][num_heads][head_dim]
+// (16-bit) for the tree attention: a box is 64 elements x the `group` heads of
+// one kv head x 128 / group tokens, 128 rows of 128 bytes (128-byte swizzle).
+pa_status tree_q_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_dim, int heads, long long tokens,
+                            int group) {
+    const TmKey key{5, base, dtype, head_dim, heads, tokens, group};
+    if (tm_lookup(key, map))
+        return PA_OK;
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    cudaError_t e = tensor_map_encoder(&enc);
+    if (e != cudaSuccess || !enc)
+        return cuda_fail(e == cudaSuccess ? cudaErrorSymbolNotFound : e, "cuTensorMapEncodeTiled lookup");
+    const CUtensorMapDataType dt = dtype == PA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                          static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {row, row * heads};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(128 / group)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS)
         return fail(PA_ERR_INVALID_ARGUMENT,

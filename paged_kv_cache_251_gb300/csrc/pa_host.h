@@ -35,7 +35,9 @@ cudaError_t prepare_kernel(int dev, const void *fn, size_t smem, int threads, in
 pa_status kv_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_dim, int block_size,
                         long long tiles);
 pa_status kv_tensor_map_groups(CUtensorMap *map, const void *base, int dtype, int block_size, long long tiles,
-                               int box_tiles = 1);
+                               int box_tiles = 1, int head_dim = 128);
+pa_status tree_q_tensor_map(CUtensorMap *map, const void *base, int dtype, int head_dim, int heads, long long tokens,
+                            int group);
 
 // Context partitions of a decode.
 struct DecodePlan {

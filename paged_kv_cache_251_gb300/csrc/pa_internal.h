@@ -58,6 +58,11 @@ const void *scored_mha_kernel_bf16(int head_dim, int block_size);
 const void *scored_gqa_kernel_f16(int block_size, int group);
 const void *scored_gqa_kernel_bf16(int block_size, int group);
 
+// Tensor-core tree attention kernels (16-bit caches): per head_dim, parts of P
+// (1 or 2) and row tiles a CTA takes (1 or 2), with their shared memory.
+const void *tree_tc_kernel_f16(int head_dim, int parts, int units, size_t *smem);
+const void *tree_tc_kernel_bf16(int head_dim, int parts, int units, size_t *smem);
+
 // General decode kernels for 8-bit caches (INT8 / E4M3 codes with row
 // scales), per head_dim and query group; nullptr if not built.
 const void *decode_q8_kernel_i8(int head_dim, int group);

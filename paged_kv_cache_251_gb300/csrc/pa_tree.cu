@@ -1,5 +1,7 @@
 // Tree attention: launches (the kernels: pa_tree.cuh).
-#include "pa_tree.cuh"
+#include <climits>
+
+#include "pa_tree_tc.cuh"
 
 #include "pa_host.h"
 #include "pa_internal.h"
@@ -14,29 +16,75 @@ template <typename T> const void *tree_fn(int head_dim) {
                           : reinterpret_cast<const void *>(&pa_tree_kernel<T, 128>);
 }
 
-}  // namespace
-
-pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t stream) {
-    int dev = 0, sms = 0, per_sm = 0;
-    cudaError_t e = device_sms(&dev, &sms);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "device query");
+pa_status launch_general(TreeParams &p, int dtype, int head_dim, int dev, cudaStream_t stream) {
     const int G = p.num_heads / p.num_kv_heads;
     p.row_tiles = (p.num_draft * G + kTreeRows - 1) / kTreeRows;
     const void *fn = dtype == PA_F32   ? tree_fn<float>(head_dim)
                      : dtype == PA_F16 ? tree_fn<__half>(head_dim)
                                        : tree_fn<__nv_bfloat16>(head_dim);
     const size_t smem = static_cast<size_t>(2) * p.block_size * head_dim * sizeof(float);
-    e = prepare_kernel(dev, fn, smem, kTreeThreads, &per_sm);
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(dev, fn, smem, kTreeThreads, &per_sm);
     if (e != cudaSuccess)
         return cuda_fail(e, "tree kernel set-up");
-    const long long items =
-        static_cast<long long>(p.num_seqs) * p.max_parts * p.num_kv_heads * p.row_tiles;
+    const long long items = static_cast<long long>(p.num_seqs) * p.max_parts * p.num_kv_heads * p.row_tiles;
     const long long grid = items < (1 << 30) ? items : (1 << 30);
     void *args[] = {&p};
     e = launch_dependent(fn, dim3(static_cast<unsigned>(grid)), dim3(kTreeThreads), args, smem, stream);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "tree launch");
+}
+
+// 16-bit caches: the tensor-core kernel.  More than 128 rows a kv head: two
+// row tiles a CTA, which read each K/V tile once.
+pa_status launch_tc(TreeParams &p, int dtype, int head_dim, int dev, int sms, cudaStream_t stream) {
+    const int G = p.num_heads / p.num_kv_heads;
+    const int rows = p.num_draft * G;
+    const int units = rows > 128 ? 2 : 1;
+    p.row_tiles = (rows + 128 * units - 1) / (128 * units);
+    const int parts = p.out_dtype == PA_F32 ? 2 : 1;
+    size_t smem = 0;
+    const void *fn = dtype == PA_F16 ? tree_tc_kernel_f16(head_dim, parts, units, &smem)
+                                     : tree_tc_kernel_bf16(head_dim, parts, units, &smem);
+    if (!fn)
+        return fail(PA_ERR_UNSUPPORTED, "no tree kernel for this dtype / head_dim");
+    CUtensorMap tmk, tmv, tmq;
+    const long long tiles = static_cast<long long>(p.num_blocks) * p.num_kv_heads;
+    pa_status st = kv_tensor_map_groups(&tmk, p.k_cache, dtype, p.block_size, tiles, 1, head_dim);
+    if (st == PA_OK)
+        st = kv_tensor_map_groups(&tmv, p.v_cache, dtype, p.block_size, tiles, 1, head_dim);
+    if (st == PA_OK)
+        st = tree_q_tensor_map(&tmq, p.q, dtype, head_dim, p.num_heads,
+                               static_cast<long long>(p.num_seqs) * p.num_draft, G);
+    if (st != PA_OK)
+        return st;
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(dev, fn, smem, kTcThreads, &per_sm);
     if (e != cudaSuccess)
-        return cuda_fail(e, "tree launch");
+        return cuda_fail(e, "tree kernel set-up");
+    if (per_sm < 1)
+        return fail(PA_ERR_UNSUPPORTED, "tree kernel does not fit on an SM");
+    const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.max_parts * p.row_tiles;
+    const long long grid = items < sms ? (items < 1 ? 1 : items) : sms;
+    if (items > grid)
+        p.work = work_counter(dev, stream);
+    void *args[] = {&p, &tmk, &tmv, &tmq};
+    e = launch_dependent(fn, dim3(static_cast<unsigned>(grid)), dim3(kTcThreads), args, smem, stream);
+    return e == cudaSuccess ? PA_OK : cuda_fail(e, "tree launch");
+}
+
+}  // namespace
+
+pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "device query");
+    void *args[] = {&p};
+    const pa_status st = dtype != PA_F32 && static_cast<long long>(p.num_blocks) * p.num_kv_heads <= INT_MAX
+                             ? launch_tc(p, dtype, head_dim, dev, sms, stream)
+                             : launch_general(p, dtype, head_dim, dev, stream);
+    if (st != PA_OK)
+        return st;
     if (p.max_parts > 1) {
         const long long rows = static_cast<long long>(p.num_seqs) * p.num_draft * p.num_heads;
         constexpr int kRows = kTreeMergeThreads / 32;

@@ -1,0 +1,951 @@
+// Tree attention on the 5th-generation tensor cores (tcgen05, accumulators in
+// tensor memory), for 16-bit K/V.
+//
+// The T drafted tokens x G query heads of a (sequence, kv head) are the rows
+// of a 128-row operand (row r = i * G + g), a tile is 128 cached tokens:
+//   S = Q . K^T    M = 128 rows, N = 128 tokens, K = head_dim
+//   O += P . V     M = 128 rows, N = head_dim,   K = 128 tokens
+// Q, K, V come from shared memory, P from tensor memory (it overwrites S in
+// place), so shared memory feeds one operand of P V only.  A thread owns a row
+// of S: its softmax needs no exchange between lanes.  O accumulates in tensor
+// memory over the tiles of an item; a row whose maximum grows by more than 2^8
+// rescales its O (rare after the first tiles), a smaller growth is left in
+// the exponents (weights up to 2^8, fp32 sums), which changes nothing in the
+// quotient.
+//
+// Two softmax warpgroups, two S and two O buffers.  With at most 128 rows
+// (Units = 1) they take alternate tiles, each with its own running state and
+// O, merged once per item; with more (Units = 2) each takes one of two row
+// tiles on every K/V tile.  While one warpgroup computes, the other's P V and
+// next S run on the tensor cores.
+//
+// P's rounding (Parts): a 16-bit output takes P rounded once to the type of V
+// (the output is rounded as coarsely); an fp32 output takes hi + lo parts
+// (hi = round(p), lo = round(p - hi)), two accumulating products.
+//
+// Warp roles (384 threads, one CTA per SM, persistent over items (sequence,
+// partition, kv head, row tile)):
+//   warp 0      K producer: item ring, block-table slice in registers, K of
+//               each tile by TMA (one copy per block), and a record of the
+//               tile's blocks for the V producer;
+//   warp 1      V producer, from the records;
+//   warp 2      tensor-memory allocation and the thread that issues MMAs;
+//   warp 3      Q loader (the Q buffer is free once the item before it has
+//               issued and finished its last S);
+//   warps 4-7, 8-11  softmax and epilogue, warpgroups 0 and 1.
+//
+// Masks.  A tile whose blocks are all valid and whose tokens are all committed
+// needs none.  Elsewhere each row builds its 128 allowed bits from the
+// committed count, its mask words and the valid blocks, and masked scores are
+// replaced, never multiplied.  V rows of tokens outside the context or behind
+// a bad table entry are zeroed in shared memory (their weight is 0, and 0 x
+// NaN is not).  A drafted token whose V row holds an infinity or NaN must not
+// reach the rows that do not attend it: its contribution is added to the
+// attending rows' O by the softmax threads, and its V row is then zeroed.
+// Every wait is bounded (PA_DEVERR_TIMEOUT); bad table entries are never
+// dereferenced (PA_DEVERR_BAD_BLOCK).
+#pragma once
+
+#include "pa_decode_gqa.cuh"
+#include "pa_tree.cuh"
+
+namespace pa {
+
+constexpr int kTcThreads = 12 * 32;
+constexpr int kTcItems = 4;      // item ring
+constexpr int kTcRecords = 4;    // record ring of the V producer
+// valid-block masks of the last tiles: the K producer of tile t has seen S of tile t - kSK finish, which was issued
+// after the softmax of tile t - kSK - 2 was done, so no reader lags by more than kSK + 1 <= 7 tiles
+constexpr int kTcMeta = 8;
+constexpr int kTcNear = 4;       // tiles of an item still to issue when the next one is claimed
+constexpr int kTcMaxBpt = 16;    // blocks per tile at block size 8
+constexpr uint32_t kTcEnd = 0xFFFFFFFFu;
+constexpr float kTcLazy = 8.0f;  // growth of a row's maximum (base 2) that rescales its O
+
+template <int D, int Units> struct TcCfg {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kGroup = 1024 * kHalves;      // 8 token rows
+    static constexpr int kTile = 16 * kGroup;          // 128 tokens of K or V
+    static constexpr int kRow = D * 2;
+    static constexpr int kQ = 128 * kRow;              // one row tile of queries
+    // measured on the tree over long contexts and the ragged batch: as many
+    // tiles as shared memory holds beside the queries
+    static constexpr int kSK = D == 64 ? 6 : 3;
+    static constexpr int kSV = D == 64 ? 6 : (Units == 1 ? 3 : 2);
+    static constexpr int kOffK = Units * kQ;
+    static constexpr int kOffV = kOffK + kSK * kTile;
+    static constexpr int kOffMisc = kOffV + kSV * kTile;
+};
+
+struct TcItem {
+    int s, kvh, rt, part;
+    int nparts, nb, blk_lo, t_first;
+    int len, committed, drafted, end;
+};
+
+// Small shared-memory state, behind the operand buffers.
+struct TcMisc {
+    uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
+    uint64_t zfull[kTcRecords], zfree[kTcRecords];
+    uint64_t ifull[kTcItems], iempty[kTcItems];
+    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone[2], odone, ofree, xbar, pz[2], fin, done;
+    TcItem items[kTcItems];
+    uint32_t meta[kTcMeta];
+    uint32_t zmask[kTcRecords];
+    int32_t zid[kTcRecords][kTcMaxBpt];
+    uint32_t poison[2][4];
+    int oinit[2];
+    uint32_t tmem;
+    float2 ml[2][128];
+};
+
+template <int D, int Units> __host__ __device__ constexpr int tc_smem() {
+    return TcCfg<D, Units>::kOffMisc + static_cast<int>(sizeof(TcMisc));
+}
+static_assert(tc_smem<128, 1>() <= 232448 && tc_smem<128, 2>() <= 232448 && tc_smem<64, 2>() <= 232448,
+              "shared memory of one CTA");
+
+// D (tensor memory) += A (tensor memory) . B (shared memory)
+__device__ inline void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, int accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <> __device__ inline void tmem_ld<32>(uint32_t taddr, float *v) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = __uint_as_float(r[i]);
+}
+__device__ inline void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ inline void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ inline void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Two 16-bit values of one word (lo element first), rounded to nearest even.
+template <typename T> __device__ inline uint32_t pack2(float lo, float hi);
+template <> __device__ inline uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <> __device__ inline uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <typename T> __device__ inline void unpack2(uint32_t w, float &lo, float &hi);
+template <> __device__ inline void unpack2<__nv_bfloat16>(uint32_t w, float &lo, float &hi) {
+    lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xffff0000u);
+}
+template <> __device__ inline void unpack2<__half>(uint32_t w, float &lo, float &hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    lo = f.x, hi = f.y;
+}
+// Whether either 16-bit value of a word is an infinity or NaN.
+template <typename T> __device__ inline bool non_finite2(uint32_t w) {
+    constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+}
+
+// ---------------------------------------------------------------------------
+// Producers
+
+template <int D, int Units>
+__device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk, char *smem, TcMisc *M) {
+    using C = TcCfg<D, Units>;
+    const int lane = threadIdx.x & 31;
+    const int bs = p.block_size, bpt = 128 / bs;
+    const uint32_t block_bytes = static_cast<uint32_t>(bs) * C::kRow;
+    const uint64_t policy = policy_evict_first();
+    if (lane == 0)
+        prefetch_tensormap(tmk);
+    ItemScan scan;
+    ItemClaim claim;
+    claim.start();
+    NextItem cur, nxt;
+    const long long groups = static_cast<long long>(p.num_kv_heads) * p.row_tiles;
+    prepare_item(p, bs, scan, claim.w, groups, cur);
+    uint32_t t = 0;
+    bool ok = true;
+    for (uint32_t k = 0;; ++k) {
+        const int slot = static_cast<int>(k % kTcItems);
+        if (!mbar_wait_bounded(&M->iempty[slot], ((k / kTcItems) & 1u) ^ 1u)) {
+            ok = false;
+            break;
+        }
+        if (cur.s < 0) {
+            if (lane == 0) {
+                M->items[slot].end = 1;
+                mbar_arrive(&M->ifull[slot]);
+            }
+            __syncwarp();
+            break;
+        }
+        const int ntiles = (cur.nb + bpt - 1) / bpt;
+        const int kvh = cur.head / p.row_tiles;
+        if (lane == 0) {
+            const TreeSeq q = tree_seq(p, cur.s);
+            if (q.bad && cur.part == 0 && cur.head == 0 && p.err)
+                atomicOr(p.err, PA_DEVERR_BAD_LEN);
+            TcItem it;
+            it.s = cur.s;
+            it.kvh = kvh;
+            it.rt = cur.head - kvh * p.row_tiles;
+            it.part = cur.part;
+            it.nparts = cur.sp.nparts;
+            it.nb = cur.nb;
+            it.blk_lo = cur.blk_lo;
+            it.t_first = static_cast<int>(t);
+            it.len = q.len;
+            it.committed = q.len - q.drafted;
+            it.drafted = q.drafted;
+            it.end = 0;
+            M->items[slot] = it;
+            mbar_arrive(&M->ifull[slot]);
+        }
+        __syncwarp();
+        bool have_next = false;
+        for (int ti = 0; ti < ntiles; ++ti, ++t) {
+            const int stage = static_cast<int>(t % C::kSK), rec = static_cast<int>(t % kTcRecords);
+            if (!mbar_wait_bounded(&M->kempty[stage], ((t / C::kSK) & 1u) ^ 1u) ||
+                !mbar_wait_bounded(&M->zfree[rec], ((t / kTcRecords) & 1u) ^ 1u)) {
+                ok = false;
+                break;
+            }
+            // lane j takes block j of the tile: its entry is in lane (index % 32) of the slice registers
+            const int b0 = ti * bpt;  // (a tile's entries share one register: bpt divides 32)
+            int entry = -1;
+#pragma unroll
+            for (int i = 0; i < kMaxBpp / 32; ++i) {
+                const int e = __shfl_sync(0xffffffffu, cur.tb[i], (b0 + lane) & 31);
+                if (i == b0 >> 5)
+                    entry = e;
+            }
+            const bool in = lane < bpt && b0 + lane < cur.nb;
+            const bool mine = in && entry >= 0 && entry < p.num_blocks;
+            if (in && !mine && p.err)
+                atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+            const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+            const int z = mine ? entry * p.num_kv_heads + kvh : 0;
+            if (lane < kTcMaxBpt)
+                M->zid[rec][lane] = z;
+            if (lane == 0) {
+                M->meta[t % kTcMeta] = mask;
+                M->zmask[rec] = mask;
+                if (mask)
+                    mbar_arrive_expect_tx(&M->kfull[stage], __popc(mask) * block_bytes);
+                else
+                    mbar_arrive(&M->kfull[stage]);
+            }
+            __syncwarp();
+            if (mine)
+                tma_load_5d(smem + C::kOffK + stage * C::kTile + lane * block_bytes, tmk, z, &M->kfull[stage], policy);
+            if (lane == 0)
+                mbar_arrive(&M->zfull[rec]);
+            __syncwarp();
+            if (ti == max(0, ntiles - kTcNear)) {  // the next item, while copies are in flight
+                claim.next(p);
+                prepare_item(p, bs, scan, claim.w, groups, nxt);
+                have_next = true;
+            }
+        }
+        if (!ok)
+            break;
+        if (!have_next) {
+            claim.next(p);
+            prepare_item(p, bs, scan, claim.w, groups, nxt);
+        }
+        cur = nxt;
+    }
+    // no more tiles for the V producer (after a failed wait too)
+    if (lane == 0) {
+        const int rec = static_cast<int>(t % kTcRecords);
+        if (!mbar_wait_bounded(&M->zfree[rec], ((t / kTcRecords) & 1u) ^ 1u))
+            ok = false;
+        M->zmask[rec] = kTcEnd;
+        mbar_arrive(&M->zfull[rec]);
+    }
+    if (!ok && lane == 0) {
+        if (p.err)
+            atomicOr(p.err, PA_DEVERR_TIMEOUT);
+        const uint32_t first = t > static_cast<uint32_t>(C::kSK) ? t - C::kSK : 0;
+        for (uint32_t u = first; u < t; ++u)
+            (void)mbar_wait_bounded(&M->kfull[u % C::kSK], (u / C::kSK) & 1u);
+    }
+    claim.finish(p);
+    __syncwarp();
+}
+
+template <int D, int Units>
+__device__ inline void tc_vproducer(const TreeParams &p, const CUtensorMap *tmv, char *smem, TcMisc *M) {
+    using C = TcCfg<D, Units>;
+    const int lane = threadIdx.x & 31;
+    const uint32_t block_bytes = static_cast<uint32_t>(p.block_size) * C::kRow;
+    const uint64_t policy = policy_evict_first();
+    if (lane == 0)
+        prefetch_tensormap(tmv);
+    bool ok = true;
+    uint32_t t = 0;
+    for (;; ++t) {
+        const int stage = static_cast<int>(t % C::kSV), rec = static_cast<int>(t % kTcRecords);
+        if (!mbar_wait_bounded(&M->zfull[rec], (t / kTcRecords) & 1u)) {
+            ok = false;
+            break;
+        }
+        const uint32_t mask = M->zmask[rec];
+        if (mask == kTcEnd)
+            break;
+        const int z = lane < kTcMaxBpt ? M->zid[rec][lane] : 0;
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&M->zfree[rec]);  // the record is in registers
+        if (!mbar_wait_bounded(&M->vempty[stage], ((t / C::kSV) & 1u) ^ 1u)) {
+            ok = false;
+            break;
+        }
+        if (lane == 0) {
+            if (mask)
+                mbar_arrive_expect_tx(&M->vfull[stage], __popc(mask) * block_bytes);
+            else
+                mbar_arrive(&M->vfull[stage]);
+        }
+        __syncwarp();
+        if ((mask >> lane) & 1u)
+            tma_load_5d(smem + C::kOffV + stage * C::kTile + lane * block_bytes, tmv, z, &M->vfull[stage], policy);
+        __syncwarp();
+    }
+    if (!ok && lane == 0) {
+        if (p.err)
+            atomicOr(p.err, PA_DEVERR_TIMEOUT);
+        const uint32_t first = t > static_cast<uint32_t>(C::kSV) ? t - C::kSV : 0;
+        for (uint32_t u = first; u < t; ++u)
+            (void)mbar_wait_bounded(&M->vfull[u % C::kSV], (u / C::kSV) & 1u);
+    }
+    __syncwarp();
+}
+
+// The item's query rows (one thread): row tile(s) of 128 rows = 128 / G drafted
+// tokens x G heads; rows past the last drafted token of the batch read zeros,
+// rows of the next sequence are computed and never stored.
+template <int D, int Units>
+__device__ inline bool tc_qloader(const TreeParams &p, const CUtensorMap *tmq, char *smem, TcMisc *M) {
+    using C = TcCfg<D, Units>;
+    const int G = p.num_heads / p.num_kv_heads;
+    prefetch_tensormap(tmq);
+    uint32_t ke = 0;
+    for (uint32_t k = 0;; ++k) {
+        const int slot = static_cast<int>(k % kTcItems);
+        if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
+            return false;
+        const TcItem it = M->items[slot];
+        mbar_arrive(&M->iempty[slot]);
+        if (it.end)
+            return true;
+        if (it.nb == 0)
+            continue;
+        if (!mbar_wait_bounded(&M->qempty, (ke & 1u) ^ 1u))
+            return false;
+        mbar_arrive_expect_tx(&M->qfull, Units * C::kQ);
+#pragma unroll
+        for (int u = 0; u < Units; ++u) {
+            const int z = it.s * p.num_draft + (it.rt * Units + u) * (128 / G);
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+                tma_load_3d(smem + u * C::kQ + hf * (128 * 128), tmq, hf * 64, it.kvh * G, z, &M->qfull);
+        }
+        ++ke;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The MMA-issuing thread.  Unit g (a tile, or a tile and a row tile): S(g) is
+// issued before P V of unit g - 1, so a softmax always overlaps a product.
+
+template <typename T, int D, int Parts, int Units>
+__device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
+    using C = TcCfg<D, Units>;
+    // a negative scale is the sign of Q (bit 13: A negated), so the softmax
+    // takes maxima of raw scores
+    const uint32_t id_qk = idesc_f16<T>(128, 128, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t kIdPV = idesc_f16<T>(128, D, 0, 1);
+    uint32_t cnt[2] = {0, 0};  // units issued per buffer
+    uint32_t ke = 0;           // items with tiles
+    uint32_t g = 0;
+    uint32_t pvs[2] = {0, 0};
+    struct Pend {
+        int b, w;
+        uint32_t t;
+        bool first;  // the buffer's first unit of its item
+    } pend = {};
+    bool have = false;
+
+    auto pv = [&](const Pend &u) -> bool {
+        const int stage = static_cast<int>(u.t % C::kSV);
+        if (!mbar_wait_bounded(&M->pfull[u.b], pvs[u.b] & 1u))
+            return false;
+        ++pvs[u.b];
+        // O is free once the item before has been written out
+        if (u.first && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
+            return false;
+        if (!mbar_wait_bounded(&M->vfull[stage], (u.t / C::kSV) & 1u))
+            return false;
+        tc_fence_after();
+        const int keep = u.first ? *reinterpret_cast<volatile int *>(&M->oinit[u.b]) : 1;
+        const char *vt = smem + C::kOffV + stage * C::kTile;
+        const uint32_t o = tmem + 256 + u.b * D, pt = tmem + u.b * 128;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+            // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
+            const uint64_t bd = sdesc(vt + kk * 2 * C::kGroup, 1024, C::kGroup);
+#pragma unroll
+            for (int part = 0; part < Parts; ++part)
+                tc_mma_ts(o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd, kIdPV, (kk | part) ? 1 : keep);
+        }
+        tc_commit(&M->pvdone[u.b]);
+        if (u.w == Units - 1)
+            tc_commit(&M->vempty[stage]);
+        return true;
+    };
+
+    for (uint32_t k = 0;; ++k) {
+        const int slot = static_cast<int>(k % kTcItems);
+        if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
+            return false;
+        const TcItem it = M->items[slot];
+        mbar_arrive(&M->iempty[slot]);
+        if (it.end)
+            return true;
+        const int bpt = 128 / p.block_size;
+        const int ntiles = (it.nb + bpt - 1) / bpt;
+        if (ntiles == 0)
+            continue;
+        if (!mbar_wait_bounded(&M->qfull, ke & 1u))
+            return false;
+        bool first[2] = {true, true};
+        for (int ti = 0; ti < ntiles; ++ti) {
+            const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
+            const int stage = static_cast<int>(t % C::kSK);
+            if (!mbar_wait_bounded(&M->kfull[stage], (t / C::kSK) & 1u))
+                return false;
+#pragma unroll
+            for (int w = 0; w < Units; ++w, ++g) {
+                const int b = static_cast<int>(g & 1u);
+                // S shares its columns with the P of the buffer's last unit
+                if (cnt[b] > 0 && !mbar_wait_bounded(&M->pvdone[b], (cnt[b] - 1) & 1u))
+                    return false;
+                tc_fence_after();
+                const char *kt = smem + C::kOffK + stage * C::kTile, *qs = smem + w * C::kQ;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t ad = sdesc(qs + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
+                    const uint64_t bd = sdesc(kt + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::kGroup);
+                    tc_mma(tmem + b * 128, ad, bd, id_qk, kk > 0);
+                }
+                tc_commit(&M->sfull[b]);
+                ++cnt[b];
+                if (w == Units - 1)
+                    tc_commit(&M->kempty[stage]);
+                if (ti == ntiles - 1 && w == Units - 1)
+                    tc_commit(&M->qempty);
+                if (have && !pv(pend))
+                    return false;
+                pend.b = b, pend.w = w, pend.t = t, pend.first = first[b];
+                first[b] = false;
+                have = true;
+            }
+        }
+        // the item's last product before anything of the next item
+        if (!pv(pend))
+            return false;
+        have = false;
+        tc_commit(&M->odone);
+        ++ke;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Softmax and epilogue
+
+// 32 allowed bits of a row for cached tokens [tok, tok + 32): committed tokens,
+// then the row's drafted ones.
+__device__ inline uint32_t first_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+
+__device__ inline uint32_t tree_bits32(const TreeParams &p, const TcItem &it, int i, int tok) {
+    uint32_t bits = first_bits(it.committed - tok);
+    const int j = tok - it.committed;  // drafted index of the first token
+    if (j <= -32 || j >= it.drafted)
+        return bits;
+    uint32_t d;
+    if (!p.mask) {
+        d = first_bits(min(i + 1, it.drafted) - j);
+        if (j < 0)
+            d &= ~first_bits(-j);
+    } else {
+        const uint64_t *row = p.mask + (static_cast<long long>(it.s) * p.num_draft + i) * p.words;
+        const int j0 = max(j, 0);
+        uint64_t w = row[j0 >> 6] >> (j0 & 63);
+        if ((j0 & 63) > 32 && (j0 >> 6) + 1 < p.words)
+            w |= row[(j0 >> 6) + 1] << (64 - (j0 & 63));
+        d = static_cast<uint32_t>(w) & first_bits(it.drafted - j0);
+        if (j < 0)
+            d <<= -j;
+    }
+    return bits | d;
+}
+
+// 32 columns of an accumulator row to memory.
+__device__ inline void store_cols32(void *out, int dtype, long long idx, const float *v) {
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    if (dtype == PA_F32) {
+        float *o = static_cast<float *>(out) + idx;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            if (wide)
+                *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            else
+                o[i] = v[i], o[i + 1] = v[i + 1], o[i + 2] = v[i + 2], o[i + 3] = v[i + 3];
+        }
+        return;
+    }
+    uint16_t *o = static_cast<uint16_t *>(out) + idx;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = dtype == PA_F16 ? pack2<__half>(v[i + 2 * e], v[i + 2 * e + 1])
+                                   : pack2<__nv_bfloat16>(v[i + 2 * e], v[i + 2 * e + 1]);
+        if (wide) {
+            *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[i + 2 * e] = static_cast<uint16_t>(w[e]), o[i + 2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
+        }
+    }
+}
+
+template <typename T, int D, int Parts, int Units>
+__device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
+    using C = TcCfg<D, Units>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wg = (warp >> 2) - 1;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;  // row of the 128, and token of a tile
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + wg * 128, o_addr = tmem + lanes + 256 + wg * D;
+    const int bs = p.block_size, bpt = 128 / bs;
+    const int G = p.num_heads / p.num_kv_heads;
+    const int lg = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
+    const int lbs = bs == 8 ? 3 : (bs == 16 ? 4 : 5);
+    const float sc = fabsf(p.scale_log2);
+    uint64_t *pzbar = Units == 1 ? &M->pz[wg] : &M->pz[0];
+    uint32_t use = 0, pzc = 0, ke = 0, g = 0;
+
+    auto arrive_wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(bar);
+        return mbar_wait_bounded(bar, phase & 1u);
+    };
+
+    for (uint32_t k = 0;; ++k) {
+        const int slot = static_cast<int>(k % kTcItems);
+        if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
+            return false;
+        const TcItem it = M->items[slot];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&M->iempty[slot]);
+        if (it.end)
+            return true;
+        const int ntiles = (it.nb + bpt - 1) / bpt;
+        // this thread's row of the (sequence, kv head)
+        const int r = (it.rt * Units + (Units == 2 ? wg : 0)) * 128 + row;
+        const int i = r >> lg;
+        const bool stored = i < p.num_draft, live = i < it.drafted;
+        const bool warp_live = __any_sync(0xffffffffu, live);
+        const long long orow = (static_cast<long long>(it.s) * p.num_draft + i) * p.num_heads + it.kvh * G + (r & (G - 1));
+        float m = -INFINITY, l = 0.f;
+        bool first = true;
+        for (int ti = 0; ti < ntiles; ++ti, g += Units) {
+            if (Units == 1 && static_cast<int>(g & 1u) != wg)
+                continue;
+            const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
+            const int tok0 = (it.blk_lo << lbs) + ti * 128;
+            if (!mbar_wait_bounded(&M->sfull[wg], use & 1u))
+                return false;
+            ++use;
+            tc_fence_after();
+            const uint32_t blocks = M->meta[t % kTcMeta];
+            const bool whole = blocks == (1u << bpt) - 1u;
+            const bool drafts = it.drafted > 0 && tok0 + 128 > it.committed && tok0 < it.len;
+            const bool masked = !whole || tok0 + 128 > it.committed;
+            bool poisoned = false;
+            const int vstage = static_cast<int>(t % C::kSV);
+            char *vrow = smem + C::kOffV + vstage * C::kTile + (row >> 3) * C::kGroup + (row & 7) * 128;
+            bool drop = false;  // this thread's token has a V row that must not be multiplied
+            if (masked) {
+                const int tok = tok0 + row;
+                const bool valid = ((blocks >> (row >> lbs)) & 1u) && tok < it.len;
+                drop = !valid;
+                if (__any_sync(0xffffffffu, drop) || drafts)
+                    if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
+                        return false;
+                if (drafts) {
+                    bool bad = false;
+                    if (valid && tok >= it.committed) {
+#pragma unroll
+                        for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                const uint4 x = ld_shared_v4(vrow + hf * 1024 + ((c + row) & 7) * 16);
+                                bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
+                                      non_finite2<T>(x.w);
+                            }
+                    }
+                    const uint32_t votes = __ballot_sync(0xffffffffu, bad);
+                    if (lane == 0)
+                        M->poison[wg][quarter] = votes;
+                    if (!arrive_wait(pzbar, pzc++))
+                        return false;
+                    poisoned = (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
+                    drop = drop || bad;
+                }
+            }
+            uint32_t allow[4];
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t a = live ? tree_bits32(p, it, i, tok0 + 32 * c) : 0u;
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
+                            if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
+                                a &= ~(0xffu << (8 * e));
+                    }
+                    allow[c] = a;
+                }
+            }
+            if (warp_live) {
+                // the row's maximum (raw scores; sc >= 0)
+                float mt = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float s[32];
+                    tmem_ld<32>(s_addr + 32 * c, s);
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            s[e] = (allow[c] >> e) & 1u ? s[e] : -INFINITY;
+                    }
+                    float a = mt, b = s[0];
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2)
+                        a = fmaxf(a, s[e]), b = fmaxf(b, s[e + 1]);
+                    mt = fmaxf(fmaxf(a, s[31]), b);
+                }
+                mt = mt == -INFINITY ? -INFINITY : mt * sc;
+                // O scales with the maximum in use; it changes only when the row's
+                // maximum passed it by kTcLazy
+                const float mn = fmaxf(m, mt);
+                const bool grow = first ? false : mn > m + kTcLazy;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tmem_ld<16>(o_addr + c, o);
+                        tmem_wait_ld();
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = __float_as_uint(alpha == 1.f ? o[e] : o[e] * alpha);
+                        tmem_st16(o_addr + c, w);
+                    }
+                    l *= alpha;
+                    tmem_wait_st();
+                }
+                if (first || grow)
+                    m = mn;
+            }
+            const float me = m == -INFINITY ? 0.f : m;
+            if (poisoned) {
+                // drafted tokens with non-finite V: added here to the rows that attend them
+                if (warp_live) {
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        if (first) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = 0.f;
+                        } else {
+                            tmem_ld<16>(o_addr + c, o);
+                            tmem_wait_ld();
+                        }
+                        for (int u = 0; u < 128; ++u) {
+                            if (!((M->poison[wg][u >> 5] >> (u & 31)) & 1u))
+                                continue;
+                            float x[2];
+                            tmem_ld<2>(s_addr + (u & ~1), x);
+                            tmem_wait_ld();
+                            const float s = u & 1 ? x[1] : x[0];
+                            const uint32_t a = u < 64 ? (u < 32 ? allow[0] : allow[1]) : (u < 96 ? allow[2] : allow[3]);
+                            if ((a >> (u & 31)) & 1u) {
+                                const float pw = fast_exp2(fmaf(s, sc, -me));
+                                const char *vr = smem + C::kOffV + vstage * C::kTile + (u >> 3) * C::kGroup +
+                                                 (u & 7) * 128 + (c >> 6) * 1024;
+#pragma unroll
+                                for (int e = 0; e < 16; e += 2) {
+                                    const int ch = ((c & 63) + e) >> 3;  // 16-byte chunk, swizzled by the row
+                                    float v0, v1;
+                                    unpack2<T>(ld_shared_u32(vr + ((ch ^ (u & 7)) << 4) + (e & 7) * 2), v0, v1);
+                                    o[e] = fmaf(pw, v0, o[e]);
+                                    o[e + 1] = fmaf(pw, v1, o[e + 1]);
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = __float_as_uint(o[e]);
+                        tmem_st16(o_addr + c, w);
+                    }
+                    tmem_wait_st();
+                }
+                if (!arrive_wait(pzbar, pzc++))  // every row has read the V rows that are zeroed now
+                    return false;
+            }
+            if (first && quarter == 0 && lane == 0)
+                M->oinit[wg] = poisoned ? 1 : 0;
+            if (warp_live) {
+                float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float s[32];
+                    tmem_ld<32>(s_addr + 32 * c, s);
+                    tmem_wait_ld();
+                    uint32_t w[16], wl[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float p0 = fast_exp2(fmaf(s[e], sc, -me)), p1 = fast_exp2(fmaf(s[e + 1], sc, -me));
+                        if (masked) {
+                            p0 = (allow[c] >> e) & 1u ? p0 : 0.f;
+                            p1 = (allow[c] >> (e + 1)) & 1u ? p1 : 0.f;
+                        }
+                        l0 += p0, l1 += p1;
+                        w[e / 2] = pack2<T>(p0, p1);
+                        if constexpr (Parts == 2) {
+                            float h0, h1;
+                            unpack2<T>(w[e / 2], h0, h1);
+                            wl[e / 2] = pack2<T>(p0 - h0, p1 - h1);
+                        }
+                    }
+                    // in place: chunk c's columns were read just above
+                    tmem_st16(s_addr + 32 * c, w);
+                    if constexpr (Parts == 2)
+                        tmem_st16(s_addr + 32 * c + 16, wl);
+                }
+                l += l0 + l1;
+                tmem_wait_st();
+            }
+            if (drop) {
+#pragma unroll
+                for (int hf = 0; hf < C::kHalves; ++hf)
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        *reinterpret_cast<uint4 *>(vrow + hf * 1024 + ((c + row) & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            if (masked)
+                fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&M->pfull[wg]);
+            first = false;
+        }
+        // ---- the item's output: final rows, or a partial per row
+        const bool direct = it.nparts == 1;
+        if (!live)  // padding rows in a warp with live ones: they attend nothing
+            m = -INFINITY, l = 0.f;
+        float f0 = 1.f, f1 = 0.f, den = l, mx = m;
+        if (ntiles > 0) {
+            if (!mbar_wait_bounded(&M->odone, ke & 1u))
+                return false;
+            tc_fence_after();
+            if (Units == 1) {
+                // both warpgroups hold a state of the same rows: this one stores columns [wg D / 2, + D / 2)
+                M->ml[wg][row] = make_float2(m, l);
+                if (!arrive_wait(&M->xbar, ke))
+                    return false;
+                const float2 a = M->ml[0][row], b = M->ml[1][row];
+                mx = fmaxf(a.x, b.x);
+                // (a state that saw nothing has l == 0 and no accumulator; a NaN denominator stays)
+                f0 = a.y == 0.f ? 0.f : (a.x == mx ? 1.f : fast_exp2(a.x - mx));
+                f1 = b.y == 0.f ? 0.f : (b.x == mx ? 1.f : fast_exp2(b.x - mx));
+                den = a.y * f0 + b.y * f1;
+            }
+        }
+        const float inv = den == 0.f ? 0.f : 1.f / den;
+        constexpr int kCols = Units == 1 ? D / 2 : D;
+        const int col0 = Units == 1 ? wg * kCols : 0;
+        const long long pr = orow * p.max_parts + it.part;
+        for (int c = col0; c < col0 + kCols; c += 32) {
+            float o[32];
+            if (ntiles > 0 && warp_live) {
+                if (Units == 1) {
+                    float x[32];
+                    tmem_ld<32>(tmem + lanes + 256 + c, o);
+                    tmem_ld<32>(tmem + lanes + 256 + D + c, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : x[e] * f1);
+                } else {
+                    tmem_ld<32>(o_addr + c, o);
+                    tmem_wait_ld();
+                }
+            }
+            if (stored) {
+                if (direct) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = den == 0.f ? 0.f : o[e] * inv;
+                    store_cols32(p.out, p.out_dtype, orow * D + c, o);
+                } else if (den != 0.f) {
+                    store_cols32(p.part_acc, PA_F32, pr * D + c, o);
+                }
+            }
+        }
+        if (stored && !direct && col0 == 0) {
+            p.part_ml[pr * 2] = mx;
+            p.part_ml[pr * 2 + 1] = den;
+        }
+        if (ntiles > 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&M->ofree);
+            ++ke;
+        }
+    }
+}
+
+template <typename T, int D, int Parts, int Units>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    pa_tree_tc_kernel(const TreeParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
+    pdl_launch_dependents();
+    pdl_wait();
+    using C = TcCfg<D, Units>;
+    extern __shared__ __align__(1024) char smem_raw[];
+    char *smem = smem_raw;
+    // the operand buffers need 1024-byte alignment (the swizzle); dynamic
+    // shared memory starts there when a kernel has no other.  Refused otherwise.
+    if (smem_addr(smem) & 1023u) {
+        if (threadIdx.x == 0 && p.err)
+            atomicOr(p.err, PA_DEVERR_BAD_LAUNCH);
+        return;
+    }
+    TcMisc *M = reinterpret_cast<TcMisc *>(smem + C::kOffMisc);
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&M->kfull[i], 1);
+            mbar_init(&M->kempty[i], 1);
+            mbar_init(&M->vfull[i], 1);
+            mbar_init(&M->vempty[i], 1);
+        }
+        for (int i = 0; i < kTcRecords; ++i) {
+            mbar_init(&M->zfull[i], 1);
+            mbar_init(&M->zfree[i], 1);
+        }
+        for (int i = 0; i < kTcItems; ++i) {
+            mbar_init(&M->ifull[i], 1);
+            mbar_init(&M->iempty[i], 10);  // Q loader, MMA thread, softmax warps
+        }
+        mbar_init(&M->qfull, 1);
+        mbar_init(&M->qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&M->sfull[i], 1);
+            mbar_init(&M->pfull[i], 4);
+            mbar_init(&M->pvdone[i], 1);
+            mbar_init(&M->pz[i], Units == 1 ? 4 : 8);
+        }
+        mbar_init(&M->odone, 1);
+        mbar_init(&M->ofree, 8);
+        mbar_init(&M->xbar, 8);
+        mbar_init(&M->fin, 1);
+        mbar_init(&M->done, 8);
+        fence_mbar_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(&M->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
+
+    bool ok = true;
+    if (warp == 0) {
+        tc_kproducer<D, Units>(p, &tmk, smem, M);
+    } else if (warp == 1) {
+        tc_vproducer<D, Units>(p, &tmv, smem, M);
+    } else if (warp == 2) {
+        if ((threadIdx.x & 31) == 0) {
+            ok = tc_mma_warp<T, D, Parts, Units>(p, smem, M, tmem);
+            // every MMA has finished, and the softmax warps are done with tensor memory, before it goes
+            tc_commit(&M->fin);
+            (void)mbar_wait_bounded(&M->fin, 0);
+            (void)mbar_wait_bounded(&M->done, 0);
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    } else if (warp == 3) {
+        if ((threadIdx.x & 31) == 0)
+            ok = tc_qloader<D, Units>(p, &tmq, smem, M);
+        __syncwarp();
+    } else {
+        ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive(&M->done);
+    }
+    if (!ok && (threadIdx.x & 31) == 0 && p.err)
+        atomicOr(p.err, PA_DEVERR_TIMEOUT);
+    __syncthreads();
+    release_claims(p);
+}
+
+}  // namespace pa

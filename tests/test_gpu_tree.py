@@ -146,6 +146,22 @@ def test_ramps_and_dominant_keys(dtype):
         check(q, k, v, tables, lens_t, None, mask, out_dtype, partition=256)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, 0.3])
+def test_scales(dtype, scale):
+    """A negative scale, zero (the mean of V) and one larger than usual."""
+    from paged_kv_cache_251_gb300 import pa
+    lens, t, h, hkv, d = [300, 40], 20, 8, 2, 128
+    k, v, tables, lens_t = paged(13, lens, hkv, d, 16, dtype)
+    q = wl.normal_tensor(8, 3, (2, t, h, d), dtype=dtype).cuda()
+    mask = pa.tree_mask_from_parents(random_parents(2, 2, t)).cuda()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run(q, k, v, tables, lens_t, mask, None, torch.float32, partition=128, err=err, scale=scale)
+    ref, mag, dx = tree_oracle(q, k, v, tables, lens_t, [t, t], mask, scale)
+    assert err.item() == 0
+    check_within(out, ref, attention_bound(ref, mag, dx, dtype, torch.float32, 300))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_bad_tables_and_lengths(dtype):
     """Table entries outside the pool are left out and flagged; contexts beyond
