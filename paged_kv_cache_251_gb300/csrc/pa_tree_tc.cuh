@@ -105,12 +105,37 @@ template <int D, int Units> __host__ __device__ constexpr int tc_smem() {
 static_assert(tc_smem<128, 1>() <= 232448 && tc_smem<128, 2>() <= 232448 && tc_smem<64, 2>() <= 232448,
               "shared memory of one CTA");
 
-// D (tensor memory) += A (tensor memory) . B (shared memory)
-__device__ inline void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, int accumulate) {
+// MMAs issued by a converged warp, one elected lane executing (`lead`): the
+// operands stay warp-uniform, so the compiler keeps descriptors in uniform
+// registers (a divergent lane paid about 90 cycles an MMA for moving them).
+__device__ inline uint32_t elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+// D (tensor memory) (+)= A (shared memory) . B (shared memory)
+__device__ inline void tc_mma_ss(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                 int accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+// D (tensor memory) (+)= A (tensor memory) . B (shared memory)
+__device__ inline void tc_mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                 int accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ inline void tc_commit_lead(uint32_t lead, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"(lead)
         : "memory");
 }
 
@@ -166,6 +191,23 @@ template <> __device__ inline void unpack2<__half>(uint32_t w, float &lo, float 
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
     lo = f.x, hi = f.y;
 }
+// Two fp32 operations of one instruction.
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+          "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return d;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<uint64_t *>(&d))
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return d;
+}
+
 // Whether either 16-bit value of a word is an infinity or NaN.
 template <typename T> __device__ inline bool non_finite2(uint32_t w) {
     constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
@@ -383,7 +425,7 @@ __device__ inline bool tc_qloader(const TreeParams &p, const CUtensorMap *tmq, c
 }
 
 // ---------------------------------------------------------------------------
-// The MMA-issuing thread.  Unit g (a tile, or a tile and a row tile): S(g) is
+// The MMA-issuing warp.  Unit g (a tile, or a tile and a row tile): S(g) is
 // issued before P V of unit g - 1, so a softmax always overlaps a product.
 
 template <typename T, int D, int Parts, int Units>
@@ -393,42 +435,51 @@ __device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, u
     // takes maxima of raw scores
     const uint32_t id_qk = idesc_f16<T>(128, 128, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t kIdPV = idesc_f16<T>(128, D, 0, 1);
+    const uint32_t lead = elect_lane();
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    // descriptors of the first Q row tile and the first K and V stages; steps
+    // along a buffer are added to the address field (16-byte units)
+    const uint64_t q_desc = sdesc(smem, 16, 1024);
+    const uint64_t k_desc = sdesc(smem + C::kOffK, 16, C::kGroup);
+    // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
+    const uint64_t v_desc = sdesc(smem + C::kOffV, 1024, C::kGroup);
+    const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
     uint32_t cnt[2] = {0, 0};  // units issued per buffer
+    uint32_t pvs[2] = {0, 0};  // products issued per buffer
     uint32_t ke = 0;           // items with tiles
-    uint32_t g = 0;
-    uint32_t pvs[2] = {0, 0};
-    struct Pend {
-        int b, w;
-        uint32_t t;
-        bool first;  // the buffer's first unit of its item
-    } pend = {};
-    bool have = false;
+    uint32_t g = 0, t = 0;     // units, tiles
+    uint32_t kst = 0, kph = 0;  // K stage of tile t, phase of its use
+    uint32_t vst = 0, vph = 0;  // V stage of the next product, phase of its use
 
-    auto pv = [&](const Pend &u) -> bool {
-        const int stage = static_cast<int>(u.t % C::kSV);
-        if (!mbar_wait_bounded(&M->pfull[u.b], pvs[u.b] & 1u))
+    // P V of the unit in buffer b (row tile w); first: the buffer's first of its item
+    auto pv = [&](uint32_t b, int w, bool first) -> bool {
+        if (!mbar_wait_bounded(&M->pfull[b], (b ? pvs[1] : pvs[0]) & 1u))
             return false;
-        ++pvs[u.b];
+        if (b)
+            ++pvs[1];
+        else
+            ++pvs[0];
         // O is free once the item before has been written out
-        if (u.first && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
+        if (first && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
             return false;
-        if (!mbar_wait_bounded(&M->vfull[stage], (u.t / C::kSV) & 1u))
+        if (!mbar_wait_bounded(&M->vfull[vst], vph))
             return false;
         tc_fence_after();
-        const int keep = u.first ? *reinterpret_cast<volatile int *>(&M->oinit[u.b]) : 1;
-        const char *vt = smem + C::kOffV + stage * C::kTile;
-        const uint32_t o = tmem + 256 + u.b * D, pt = tmem + u.b * 128;
+        const int keep = first ? *reinterpret_cast<volatile int *>(&M->oinit[b]) : 1;
+        const uint64_t vd = v_desc + vst * (C::kTile >> 4);
+        const uint32_t o = tmem + 256 + b * D, pt = tmem + b * 128;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-            // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
-            const uint64_t bd = sdesc(vt + kk * 2 * C::kGroup, 1024, C::kGroup);
+        for (int kk = 0; kk < 8; ++kk)
 #pragma unroll
             for (int part = 0; part < Parts; ++part)
-                tc_mma_ts(o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, bd, kIdPV, (kk | part) ? 1 : keep);
+                tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, vd + kk * (2 * C::kGroup >> 4), kIdPV,
+                          (kk | part) ? 1 : keep);
+        tc_commit_lead(lead, &M->pvdone[b]);
+        if (w == Units - 1) {
+            tc_commit_lead(lead, &M->vempty[vst]);
+            if (++vst == C::kSV)
+                vst = 0, vph ^= 1u;
         }
-        tc_commit(&M->pvdone[u.b]);
-        if (u.w == Units - 1)
-            tc_commit(&M->vempty[stage]);
         return true;
     };
 
@@ -436,54 +487,55 @@ __device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, u
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
             return false;
-        const TcItem it = M->items[slot];
-        mbar_arrive(&M->iempty[slot]);
-        if (it.end)
+        const int nb = M->items[slot].nb, end = M->items[slot].end;
+        __syncwarp();
+        if (lane0)
+            mbar_arrive(&M->iempty[slot]);
+        if (end)
             return true;
-        const int bpt = 128 / p.block_size;
-        const int ntiles = (it.nb + bpt - 1) / bpt;
+        const int ntiles = (nb + (1 << lbpt) - 1) >> lbpt;
         if (ntiles == 0)
             continue;
         if (!mbar_wait_bounded(&M->qfull, ke & 1u))
             return false;
-        bool first[2] = {true, true};
-        for (int ti = 0; ti < ntiles; ++ti) {
-            const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
-            const int stage = static_cast<int>(t % C::kSK);
-            if (!mbar_wait_bounded(&M->kfull[stage], (t / C::kSK) & 1u))
+        const uint32_t g0 = g;
+        for (int ti = 0; ti < ntiles; ++ti, ++t) {
+            if (!mbar_wait_bounded(&M->kfull[kst], kph))
                 return false;
 #pragma unroll
             for (int w = 0; w < Units; ++w, ++g) {
-                const int b = static_cast<int>(g & 1u);
+                const uint32_t b = g & 1u;
                 // S shares its columns with the P of the buffer's last unit
-                if (cnt[b] > 0 && !mbar_wait_bounded(&M->pvdone[b], (cnt[b] - 1) & 1u))
+                const uint32_t used = b ? cnt[1] : cnt[0];
+                if (used > 0 && !mbar_wait_bounded(&M->pvdone[b], (used - 1) & 1u))
                     return false;
                 tc_fence_after();
-                const char *kt = smem + C::kOffK + stage * C::kTile, *qs = smem + w * C::kQ;
+                const uint64_t qd = q_desc + w * (C::kQ >> 4), kd = k_desc + kst * (C::kTile >> 4);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t ad = sdesc(qs + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024);
-                    const uint64_t bd = sdesc(kt + (kk >> 2) * 1024 + (kk & 3) * 32, 16, C::kGroup);
-                    tc_mma(tmem + b * 128, ad, bd, id_qk, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_ss(lead, tmem + b * 128, qd + ((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
+                              kd + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2), id_qk, kk > 0);
+                tc_commit_lead(lead, &M->sfull[b]);
+                if (b)
+                    ++cnt[1];
+                else
+                    ++cnt[0];
+                if (w == Units - 1) {
+                    tc_commit_lead(lead, &M->kempty[kst]);
+                    if (ti == ntiles - 1)
+                        tc_commit_lead(lead, &M->qempty);
                 }
-                tc_commit(&M->sfull[b]);
-                ++cnt[b];
-                if (w == Units - 1)
-                    tc_commit(&M->kempty[stage]);
-                if (ti == ntiles - 1 && w == Units - 1)
-                    tc_commit(&M->qempty);
-                if (have && !pv(pend))
+                // the product of the unit before (the first two units of an item are their buffers' first)
+                if (g > g0 && !pv(b ^ 1u, Units == 2 ? 1 - w : 0, g - g0 <= 2))
                     return false;
-                pend.b = b, pend.w = w, pend.t = t, pend.first = first[b];
-                first[b] = false;
-                have = true;
             }
+            if (++kst == C::kSK)
+                kst = 0, kph ^= 1u;
         }
         // the item's last product before anything of the next item
-        if (!pv(pend))
+        if (!pv((g - 1) & 1u, Units - 1, g - g0 <= 2))
             return false;
-        have = false;
-        tc_commit(&M->odone);
+        tc_commit_lead(lead, &M->odone);
         ++ke;
     }
 }
@@ -563,7 +615,8 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
     const int G = p.num_heads / p.num_kv_heads;
     const int lg = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
     const int lbs = bs == 8 ? 3 : (bs == 16 ? 4 : 5);
-    const float sc = fabsf(p.scale_log2);
+    // (a scale of 0 as one too small to matter: a masked -inf times 0 would be NaN)
+    const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
     uint64_t *pzbar = Units == 1 ? &M->pz[wg] : &M->pz[0];
     uint32_t use = 0, pzc = 0, ke = 0, g = 0;
 
@@ -638,39 +691,43 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     drop = drop || bad;
                 }
             }
-            uint32_t allow[4];
-            if (masked) {
+            // the tile's tokens 32 c .. 32 c + 31 that this row attends
+            auto allowed = [&](int c) -> uint32_t {
+                uint32_t a = live ? tree_bits32(p, it, i, tok0 + 32 * c) : 0u;
+                if (!whole) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t a = live ? tree_bits32(p, it, i, tok0 + 32 * c) : 0u;
-                    if (!whole) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
-                            if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
-                                a &= ~(0xffu << (8 * e));
-                    }
-                    allow[c] = a;
+                    for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
+                        if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
+                            a &= ~(0xffu << (8 * e));
                 }
-            }
+                return a;
+            };
+            float sv[128];
             if (warp_live) {
-                // the row's maximum (raw scores; sc >= 0)
-                float mt = -INFINITY;
+                // the row's scores, once into registers; their maximum (raw; sc >= 0)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    tmem_ld<32>(s_addr + 32 * c, s);
-                    tmem_wait_ld();
-                    if (masked) {
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld<32>(s_addr + 32 * c, sv + 32 * c);
+                tmem_wait_ld();
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t a = allowed(c);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            s[e] = (allow[c] >> e) & 1u ? s[e] : -INFINITY;
+                            sv[32 * c + e] = (a >> e) & 1u ? sv[32 * c + e] : -INFINITY;
                     }
-                    float a = mt, b = s[0];
-#pragma unroll
-                    for (int e = 1; e < 31; e += 2)
-                        a = fmaxf(a, s[e]), b = fmaxf(b, s[e + 1]);
-                    mt = fmaxf(fmaxf(a, s[31]), b);
                 }
+                float m4[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    m4[c] = sv[c];
+#pragma unroll
+                for (int e = 4; e < 128; e += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), e + 4 + c < 128 ? sv[e + 4 + c] : m4[c]);
+                float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 mt = mt == -INFINITY ? -INFINITY : mt * sc;
                 // O scales with the maximum in use; it changes only when the row's
                 // maximum passed it by kTcLazy
@@ -716,8 +773,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                             tmem_ld<2>(s_addr + (u & ~1), x);
                             tmem_wait_ld();
                             const float s = u & 1 ? x[1] : x[0];
-                            const uint32_t a = u < 64 ? (u < 32 ? allow[0] : allow[1]) : (u < 96 ? allow[2] : allow[3]);
-                            if ((a >> (u & 31)) & 1u) {
+                            if ((allowed(u >> 5) >> (u & 31)) & 1u) {
                                 const float pw = fast_exp2(fmaf(s, sc, -me));
                                 const char *vr = smem + C::kOffV + vstage * C::kTile + (u >> 3) * C::kGroup +
                                                  (u & 7) * 128 + (c >> 6) * 1024;
@@ -746,34 +802,29 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             if (first && quarter == 0 && lane == 0)
                 M->oinit[wg] = poisoned ? 1 : 0;
             if (warp_live) {
-                float l0 = 0.f, l1 = 0.f;
+                // (a masked score is -inf: its weight is exactly 0)
+                float2 l2 = make_float2(0.f, 0.f);
+                const float2 sc2 = make_float2(sc, sc), me2 = make_float2(-me, -me);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float s[32];
-                    tmem_ld<32>(s_addr + 32 * c, s);
-                    tmem_wait_ld();
                     uint32_t w[16], wl[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float p0 = fast_exp2(fmaf(s[e], sc, -me)), p1 = fast_exp2(fmaf(s[e + 1], sc, -me));
-                        if (masked) {
-                            p0 = (allow[c] >> e) & 1u ? p0 : 0.f;
-                            p1 = (allow[c] >> (e + 1)) & 1u ? p1 : 0.f;
-                        }
-                        l0 += p0, l1 += p1;
-                        w[e / 2] = pack2<T>(p0, p1);
+                        float2 x = fma2(make_float2(sv[32 * c + e], sv[32 * c + e + 1]), sc2, me2);
+                        x.x = fast_exp2(x.x), x.y = fast_exp2(x.y);
+                        l2 = add2(l2, x);
+                        w[e / 2] = pack2<T>(x.x, x.y);
                         if constexpr (Parts == 2) {
                             float h0, h1;
                             unpack2<T>(w[e / 2], h0, h1);
-                            wl[e / 2] = pack2<T>(p0 - h0, p1 - h1);
+                            wl[e / 2] = pack2<T>(x.x - h0, x.y - h1);
                         }
                     }
-                    // in place: chunk c's columns were read just above
                     tmem_st16(s_addr + 32 * c, w);
                     if constexpr (Parts == 2)
                         tmem_st16(s_addr + 32 * c + 16, wl);
                 }
-                l += l0 + l1;
+                l += l2.x + l2.y;
                 tmem_wait_st();
             }
             if (drop) {
@@ -915,27 +966,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
+    // registers: 384 x 168 = 128 x 72 + 256 x 216 (a softmax thread holds its row's 128 scores)
     bool ok = true;
-    if (warp == 0) {
-        tc_kproducer<D, Units>(p, &tmk, smem, M);
-    } else if (warp == 1) {
-        tc_vproducer<D, Units>(p, &tmv, smem, M);
-    } else if (warp == 2) {
-        if ((threadIdx.x & 31) == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            tc_kproducer<D, Units>(p, &tmk, smem, M);
+        } else if (warp == 1) {
+            tc_vproducer<D, Units>(p, &tmv, smem, M);
+        } else if (warp == 2) {
             ok = tc_mma_warp<T, D, Parts, Units>(p, smem, M, tmem);
             // every MMA has finished, and the softmax warps are done with tensor memory, before it goes
-            tc_commit(&M->fin);
+            tc_commit_lead(elect_lane(), &M->fin);
             (void)mbar_wait_bounded(&M->fin, 0);
             (void)mbar_wait_bounded(&M->done, 0);
+            __syncwarp();
+            tc_fence_after();
+            tmem_dealloc(tmem, 512);
+        } else {
+            if ((threadIdx.x & 31) == 0)
+                ok = tc_qloader<D, Units>(p, &tmq, smem, M);
+            __syncwarp();
         }
-        __syncwarp();
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    } else if (warp == 3) {
-        if ((threadIdx.x & 31) == 0)
-            ok = tc_qloader<D, Units>(p, &tmq, smem, M);
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
