@@ -543,62 +543,154 @@ __device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, u
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 
-// 32 allowed bits of a row for cached tokens [tok, tok + 32): committed tokens,
-// then the row's drafted ones.
+// The 128 cached tokens [tok, tok + 128) that a row attends, blocks aside:
+// committed tokens, then the row's drafted ones.  The mask words come in one
+// round trip (three 64-bit words cover 128 bits at any offset).
 __device__ inline uint32_t first_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
 
-__device__ inline uint32_t tree_bits32(const TreeParams &p, const TcItem &it, int i, int tok) {
-    uint32_t bits = first_bits(it.committed - tok);
-    const int j = tok - it.committed;  // drafted index of the first token
-    if (j <= -32 || j >= it.drafted)
-        return bits;
-    uint32_t d;
-    if (!p.mask) {
-        d = first_bits(min(i + 1, it.drafted) - j);
-        if (j < 0)
-            d &= ~first_bits(-j);
-    } else {
-        const uint64_t *row = p.mask + (static_cast<long long>(it.s) * p.num_draft + i) * p.words;
-        const int j0 = max(j, 0);
-        uint64_t w = row[j0 >> 6] >> (j0 & 63);
-        if ((j0 & 63) > 32 && (j0 >> 6) + 1 < p.words)
-            w |= row[(j0 >> 6) + 1] << (64 - (j0 & 63));
-        d = static_cast<uint32_t>(w) & first_bits(it.drafted - j0);
-        if (j < 0)
-            d <<= -j;
+__device__ inline void tree_bits128(const TreeParams &p, int s, int committed, int drafted, int i, int tok,
+                                    uint32_t *bits) {
+    const int j = tok - committed;  // drafted index of the first token (negative: committed tokens first)
+    uint64_t w[3] = {0, 0, 0};
+    const int j0 = max(j, 0);
+    if (j > -128 && j < drafted) {
+        if (p.mask) {
+            const uint64_t *row = p.mask + (static_cast<long long>(s) * p.num_draft + i) * p.words + (j0 >> 6);
+            const int left = p.words - (j0 >> 6);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < left)
+                    w[k] = row[k];
+        } else {  // a chain: bits 0 .. i
+            const int n = i + 1 - (j0 & ~63);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                w[k] = static_cast<uint64_t>(first_bits(n - 64 * k)) |
+                       static_cast<uint64_t>(first_bits(n - 64 * k - 32)) << 32;
+        }
     }
-    return bits | d;
+    // bit e of d: drafted token j0 + e
+    const int sh = j0 & 63;
+    uint64_t d[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        d[k] = sh ? (w[k] >> sh) | (w[k + 1] << (64 - sh)) : w[k];
+    uint32_t u[4] = {static_cast<uint32_t>(d[0]), static_cast<uint32_t>(d[0] >> 32), static_cast<uint32_t>(d[1]),
+                     static_cast<uint32_t>(d[1] >> 32)};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        u[c] &= first_bits(drafted - j0 - 32 * c);
+    // committed tokens below them: the drafted bits start at bit -j
+    const int up = max(-j, 0);  // 0 .. 128 and more
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t x = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // u[k] lands on bits [32 k + up, + 32)
+            const int at = 32 * k + up - 32 * c;
+            if (at >= 0 && at < 32)
+                x |= u[k] << at;
+            else if (at < 0 && at > -32)
+                x |= u[k] >> -at;
+        }
+        bits[c] = x | first_bits(up - 32 * c);
+    }
 }
 
-// 32 columns of an accumulator row to memory.
-__device__ inline void store_cols32(void *out, int dtype, long long idx, const float *v) {
-    const bool wide = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    if (dtype == PA_F32) {
-        float *o = static_cast<float *>(out) + idx;
+// 16 bytes to an address of any 2-byte alignment.
+template <typename E> __device__ inline void store16(E *p, const uint32_t *w) {
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+    if constexpr (sizeof(E) == 4) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            if (wide)
-                *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            else
-                o[i] = v[i], o[i + 1] = v[i + 1], o[i + 2] = v[i + 2], o[i + 3] = v[i + 3];
+        for (int e = 0; e < 4; ++e)
+            p[e] = __uint_as_float(w[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            p[2 * e] = static_cast<E>(w[e]), p[2 * e + 1] = static_cast<E>(w[e] >> 16);
+    }
+}
+
+// Exchange pieces among 4 adjacent lanes: v holds piece k (N words) of this
+// lane's own row; afterwards v holds piece (lane & 3) of the rows of lanes
+// (lane & ~3) + k.  A store then covers 4 pieces of one row with 4 lanes
+// instead of one piece of 32 rows (8 lines an instruction instead of 32).
+template <int N> __device__ inline void transpose4(uint32_t (*v)[N]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int step = 1; step <= 2; step <<= 1) {
+        const bool up = lane & step;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & step)
+                continue;
+            // lanes with the bit clear send piece k + step and keep k; the others the other way
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint32_t send = up ? v[k][e] : v[k + step][e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, step);
+                if (up)
+                    v[k][e] = got;
+                else
+                    v[k + step][e] = got;
+            }
+        }
+    }
+}
+
+// 32 columns of 32 accumulator rows (one row a lane) to memory, whole warp:
+// row `row` (in rows of D elements; -1: this lane's row is not stored), columns
+// from col.
+template <int D>
+__device__ inline void store_rows32(void *out, int dtype, long long row, int col, const float *v) {
+    const int q = threadIdx.x & 3;
+    long long rows[4];  // of the lanes of this group of four
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        rows[k] = __shfl_sync(0xffffffffu, row, (threadIdx.x & 28) + k);
+    if (dtype == PA_F32) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {  // 16 columns: 4 pieces of 16 bytes
+            uint32_t w[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[k][e] = __float_as_uint(v[16 * hf + 4 * k + e]);
+            transpose4<4>(w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (rows[k] >= 0)
+                    store16(static_cast<float *>(out) + rows[k] * D + col + 16 * hf + 4 * q, w[k]);
         }
         return;
     }
-    uint16_t *o = static_cast<uint16_t *>(out) + idx;
+    uint32_t w[4][4];  // 4 pieces of 8 columns
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        uint32_t w[4];
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            w[e] = dtype == PA_F16 ? pack2<__half>(v[i + 2 * e], v[i + 2 * e + 1])
-                                   : pack2<__nv_bfloat16>(v[i + 2 * e], v[i + 2 * e + 1]);
-        if (wide) {
-            *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
+            w[k][e] = dtype == PA_F16 ? pack2<__half>(v[8 * k + 2 * e], v[8 * k + 2 * e + 1])
+                                      : pack2<__nv_bfloat16>(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
+    transpose4<4>(w);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[i + 2 * e] = static_cast<uint16_t>(w[e]), o[i + 2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
-        }
+    for (int k = 0; k < 4; ++k)
+        if (rows[k] >= 0)
+            store16(static_cast<uint16_t *>(out) + rows[k] * D + col + 8 * q, w[k]);
+}
+
+// Half a tile's scores of this thread's row; masked ones become -inf.
+__device__ inline void load_scores(uint32_t s_addr, int half, bool masked, const uint32_t *allow, float *sv) {
+    tmem_ld<32>(s_addr + 64 * half, sv);
+    tmem_ld<32>(s_addr + 64 * half + 32, sv + 32);
+    tmem_wait_ld();
+    if (masked) {
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+            sv[e] = (allow[2 * half + (e >> 5)] >> (e & 31)) & 1u ? sv[e] : -INFINITY;
     }
 }
 
@@ -651,14 +743,27 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 continue;
             const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
             const int tok0 = (it.blk_lo << lbs) + ti * 128;
+            const bool drafts = it.drafted > 0 && tok0 + 128 > it.committed && tok0 < it.len;
+            uint32_t allow[4];  // set and used where the tile is masked
+            if (tok0 + 128 > it.committed)  // (the mask's round trip overlaps the wait for S)
+                tree_bits128(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0, allow);
+            else
+                allow[0] = allow[1] = allow[2] = allow[3] = 0xffffffffu;
             if (!mbar_wait_bounded(&M->sfull[wg], use & 1u))
                 return false;
             ++use;
             tc_fence_after();
             const uint32_t blocks = M->meta[t % kTcMeta];
             const bool whole = blocks == (1u << bpt) - 1u;
-            const bool drafts = it.drafted > 0 && tok0 + 128 > it.committed && tok0 < it.len;
             const bool masked = !whole || tok0 + 128 > it.committed;
+            if (!whole) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
+                        if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
+                            allow[c] &= ~(0xffu << (8 * e));
+            }
             bool poisoned = false;
             const int vstage = static_cast<int>(t % C::kSV);
             char *vrow = smem + C::kOffV + vstage * C::kTile + (row >> 3) * C::kGroup + (row & 7) * 128;
@@ -691,42 +796,19 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     drop = drop || bad;
                 }
             }
-            // the tile's tokens 32 c .. 32 c + 31 that this row attends
-            auto allowed = [&](int c) -> uint32_t {
-                uint32_t a = live ? tree_bits32(p, it, i, tok0 + 32 * c) : 0u;
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
-                        if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
-                            a &= ~(0xffu << (8 * e));
-                }
-                return a;
-            };
-            float sv[128];
             if (warp_live) {
-                // the row's scores, once into registers; their maximum (raw; sc >= 0)
+                // the row's maximum (raw scores; sc >= 0), half a tile at a time
+                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld<32>(s_addr + 32 * c, sv + 32 * c);
-                tmem_wait_ld();
-                if (masked) {
+                for (int hf = 0; hf < 2; ++hf) {
+                    float sv[64];
+                    load_scores(s_addr, hf, masked, allow, sv);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t a = allowed(c);
+                    for (int e = 0; e < 64; e += 8)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            sv[32 * c + e] = (a >> e) & 1u ? sv[32 * c + e] : -INFINITY;
-                    }
+                        for (int c = 0; c < 4; ++c)
+                            m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), sv[e + 4 + c]);
                 }
-                float m4[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    m4[c] = sv[c];
-#pragma unroll
-                for (int e = 4; e < 128; e += 8)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), e + 4 + c < 128 ? sv[e + 4 + c] : m4[c]);
                 float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 mt = mt == -INFINITY ? -INFINITY : mt * sc;
                 // O scales with the maximum in use; it changes only when the row's
@@ -773,7 +855,8 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                             tmem_ld<2>(s_addr + (u & ~1), x);
                             tmem_wait_ld();
                             const float s = u & 1 ? x[1] : x[0];
-                            if ((allowed(u >> 5) >> (u & 31)) & 1u) {
+                            const uint32_t a = u < 64 ? (u < 32 ? allow[0] : allow[1]) : (u < 96 ? allow[2] : allow[3]);
+                            if ((a >> (u & 31)) & 1u) {
                                 const float pw = fast_exp2(fmaf(s, sc, -me));
                                 const char *vr = smem + C::kOffV + vstage * C::kTile + (u >> 3) * C::kGroup +
                                                  (u & 7) * 128 + (c >> 6) * 1024;
@@ -804,13 +887,16 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             if (warp_live) {
                 // (a masked score is -inf: its weight is exactly 0)
                 float2 l2 = make_float2(0.f, 0.f);
+                float sv[64];
                 const float2 sc2 = make_float2(sc, sc), me2 = make_float2(-me, -me);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    if ((c & 1) == 0)
+                        load_scores(s_addr, c >> 1, masked, allow, sv);
                     uint32_t w[16], wl[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = fma2(make_float2(sv[32 * c + e], sv[32 * c + e + 1]), sc2, me2);
+                        float2 x = fma2(make_float2(sv[32 * (c & 1) + e], sv[32 * (c & 1) + e + 1]), sc2, me2);
                         x.x = fast_exp2(x.x), x.y = fast_exp2(x.y);
                         l2 = add2(l2, x);
                         w[e / 2] = pack2<T>(x.x, x.y);
@@ -868,7 +954,9 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
         constexpr int kCols = Units == 1 ? D / 2 : D;
         const int col0 = Units == 1 ? wg * kCols : 0;
         const long long pr = orow * p.max_parts + it.part;
-        for (int c = col0; c < col0 + kCols; c += 32) {
+        // (rows a warp need not write: none of them is stored)
+        const bool any_stored = __any_sync(0xffffffffu, stored);
+        for (int c = any_stored ? col0 : D; c < col0 + kCols; c += 32) {
             float o[32];
             if (ntiles > 0 && warp_live) {
                 if (Units == 1) {
@@ -884,15 +972,13 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     tmem_wait_ld();
                 }
             }
-            if (stored) {
-                if (direct) {
+            if (direct) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = den == 0.f ? 0.f : o[e] * inv;
-                    store_cols32(p.out, p.out_dtype, orow * D + c, o);
-                } else if (den != 0.f) {
-                    store_cols32(p.part_acc, PA_F32, pr * D + c, o);
-                }
+                for (int e = 0; e < 32; ++e)
+                    o[e] = den == 0.f ? 0.f : o[e] * inv;
+                store_rows32<D>(p.out, p.out_dtype, stored ? orow : -1, c, o);
+            } else if (warp_live) {
+                store_rows32<D>(p.part_acc, PA_F32, stored && den != 0.f ? pr : -1, c, o);
             }
         }
         if (stored && !direct && col0 == 0) {
@@ -966,10 +1052,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
-    // registers: 384 x 168 = 128 x 72 + 256 x 216 (a softmax thread holds its row's 128 scores)
+    // registers: 384 x 168 = 128 x 88 + 256 x 208
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             tc_kproducer<D, Units>(p, &tmk, smem, M);
         } else if (warp == 1) {
@@ -989,7 +1075,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
