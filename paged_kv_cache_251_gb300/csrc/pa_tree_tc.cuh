@@ -13,12 +13,14 @@
 // the exponents (weights up to 2^8, fp32 sums), which changes nothing in the
 // quotient.
 //
-// Two softmax warpgroups, two S and two O buffers.  With at most 128 rows
-// (Units = 1) they take alternate tiles, each with its own running state and
-// O, merged once per item; with more (Units = 2) each takes one of two row
-// tiles on every K/V tile.  While one warpgroup computes, the other's P V and
-// next S run on the tensor cores.
-//
+// Work inside an item goes by sub-units of 64 tokens, n = 0, 1, 2, ...:
+// sub-unit n belongs to softmax warpgroup n % 2 and S / P buffer n % 4 (64
+// columns each), so each warpgroup has two buffers: S of its next sub-unit is
+// made while it works on this one, and P V of the last one runs beside both.
+// With at most 128 rows (Units = 1) warpgroup w takes tokens 64 w .. 64 w + 63
+// of every tile, with its own running state and O, merged once per item; with
+// more (Units = 2) each takes one of two row tiles and all tokens.
+
 // P's rounding (Parts): a 16-bit output takes P rounded once to the type of V
 // (the output is rounded as coarsely); an fp32 output takes hi + lo parts
 // (hi = round(p), lo = round(p - hi)), two accumulating products.
@@ -29,9 +31,8 @@
 //               each tile by TMA (one copy per block), and a record of the
 //               tile's blocks for the V producer;
 //   warp 1      V producer, from the records;
-//   warp 2      tensor-memory allocation and the thread that issues MMAs;
-//   warp 3      Q loader (the Q buffer is free once the item before it has
-//               issued and finished its last S);
+//   warp 2      tensor-memory allocation, the queries' TMA, S products;
+//   warp 3      P V products;
 //   warps 4-7, 8-11  softmax and epilogue, warpgroups 0 and 1.
 //
 // Masks.  A tile whose blocks are all valid and whose tokens are all committed
@@ -53,9 +54,10 @@ namespace pa {
 
 constexpr int kTcThreads = 12 * 32;
 constexpr int kTcItems = 4;      // item ring
-constexpr int kTcRecords = 4;    // record ring of the V producer
-// valid-block masks of the last tiles: the K producer of tile t has seen S of tile t - kSK finish, which was issued
-// after the softmax of tile t - kSK - 2 was done, so no reader lags by more than kSK + 1 <= 7 tiles
+constexpr int kTcRecords = 3;    // record ring of the V producer
+// valid-block masks of the last tiles: the K producer of tile t has seen all S of tile t - kSK finish, the last of
+// which was issued after the softmax of the sub-unit four before it was done, so no reader lags by more than
+// kSK + 1 <= 7 tiles
 constexpr int kTcMeta = 8;
 constexpr int kTcNear = 4;       // tiles of an item still to issue when the next one is claimed
 constexpr int kTcMaxBpt = 16;    // blocks per tile at block size 8
@@ -88,7 +90,7 @@ struct TcMisc {
     uint64_t kfull[6], kempty[6], vfull[6], vempty[6];
     uint64_t zfull[kTcRecords], zfree[kTcRecords];
     uint64_t ifull[kTcItems], iempty[kTcItems];
-    uint64_t qfull, qempty, sfull[2], pfull[2], pvdone[2], odone, ofree, xbar, pz[2], fin, done;
+    uint64_t qfull, qempty, sfull[4], pfull[4], pvdone[4], odone, ofree, xbar, pz[2], fin, done;
     TcItem items[kTcItems];
     uint32_t meta[kTcMeta];
     uint32_t zmask[kTcRecords];
@@ -391,98 +393,106 @@ __device__ inline void tc_vproducer(const TreeParams &p, const CUtensorMap *tmv,
     __syncwarp();
 }
 
-// The item's query rows (one thread): row tile(s) of 128 rows = 128 / G drafted
-// tokens x G heads; rows past the last drafted token of the batch read zeros,
-// rows of the next sequence are computed and never stored.
-template <int D, int Units>
-__device__ inline bool tc_qloader(const TreeParams &p, const CUtensorMap *tmq, char *smem, TcMisc *M) {
+// ---------------------------------------------------------------------------
+// The two issuing warps.  Each is converged, one elected lane executing.  The S
+// warp runs up to four sub-units ahead of the P V warp (across items too); one
+// warp issuing both took about 1000 cycles a sub-unit in waits and issue alone.
+
+// S = Q . K^T of every sub-unit, and the item's query rows: row tile(s) of 128
+// rows = 128 / G drafted tokens x G heads; rows past the last drafted token of
+// the batch read zeros, rows of the next sequence are computed and never stored.
+template <typename T, int D, int Units>
+__device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
+    constexpr uint32_t kPerTile = 2 * Units;  // sub-units of a tile
+    // a negative scale is the sign of Q (bit 13: A negated), so the softmax
+    // takes maxima of raw scores
+    const uint32_t id_qk = idesc_f16<T>(128, 64, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t kHalf = 8 * C::kGroup >> 4;  // 64 tokens of a tile, in descriptor units
+    const uint32_t lead = elect_lane();
+    const bool lane0 = (threadIdx.x & 31) == 0;
+    // descriptors of the first Q row tile and the first K stage; steps along a
+    // buffer are added to the address field (16-byte units)
+    const uint64_t q_desc = sdesc(smem, 16, 1024);
+    const uint64_t k_desc = sdesc(smem + C::kOffK, 16, C::kGroup);
+    const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
     const int G = p.num_heads / p.num_kv_heads;
-    prefetch_tensormap(tmq);
-    uint32_t ke = 0;
+    if (lane0)
+        prefetch_tensormap(tmq);
+    uint32_t x = 0;             // sub-units so far
+    uint32_t ke = 0;            // items with tiles
+    uint32_t kst = 0, kph = 0;  // K stage, phase of its use
     for (uint32_t k = 0;; ++k) {
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
             return false;
         const TcItem it = M->items[slot];
-        mbar_arrive(&M->iempty[slot]);
+        __syncwarp();
+        if (lane0)
+            mbar_arrive(&M->iempty[slot]);
         if (it.end)
             return true;
-        if (it.nb == 0)
+        const int ntiles = (it.nb + (1 << lbpt) - 1) >> lbpt;
+        if (ntiles == 0)
             continue;
-        if (!mbar_wait_bounded(&M->qempty, (ke & 1u) ^ 1u))
+        // the Q buffer: free once the last S of the item before has finished
+        if (ke > 0 && !mbar_wait_bounded(&M->qempty, (ke - 1) & 1u))
             return false;
-        mbar_arrive_expect_tx(&M->qfull, Units * C::kQ);
+        if (lane0) {
+            mbar_arrive_expect_tx(&M->qfull, Units * C::kQ);
 #pragma unroll
-        for (int u = 0; u < Units; ++u) {
-            const int z = it.s * p.num_draft + (it.rt * Units + u) * (128 / G);
+            for (int u = 0; u < Units; ++u) {
+                const int z = it.s * p.num_draft + (it.rt * Units + u) * (128 / G);
 #pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-                tma_load_3d(smem + u * C::kQ + hf * (128 * 128), tmq, hf * 64, it.kvh * G, z, &M->qfull);
+                for (int hf = 0; hf < C::kHalves; ++hf)
+                    tma_load_3d(smem + u * C::kQ + hf * (128 * 128), tmq, hf * 64, it.kvh * G, z, &M->qfull);
+            }
+        }
+        __syncwarp();
+        if (!mbar_wait_bounded(&M->qfull, ke & 1u))
+            return false;
+        for (int ti = 0; ti < ntiles; ++ti) {
+            if (!mbar_wait_bounded(&M->kfull[kst], kph))
+                return false;
+#pragma unroll
+            for (uint32_t e = 0; e < kPerTile; ++e, ++x) {
+                const uint32_t b = x & 3u;
+                // S shares its columns with the P of the buffer's last use
+                if (x >= 4 && !mbar_wait_bounded(&M->pvdone[b], ((x >> 2) - 1) & 1u))
+                    return false;
+                tc_fence_after();
+                const uint64_t qd = q_desc + (Units == 2 ? (e & 1u) * (C::kQ >> 4) : 0u);
+                const uint64_t kd = k_desc + kst * (C::kTile >> 4) + (Units == 2 ? e >> 1 : e) * kHalf;
+                const uint32_t d = tmem + b * 64;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_ss(lead, d, qd + ((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
+                              kd + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2), id_qk, kk > 0);
+                tc_commit_lead(lead, &M->sfull[b]);
+            }
+            tc_commit_lead(lead, &M->kempty[kst]);
+            if (ti == ntiles - 1)
+                tc_commit_lead(lead, &M->qempty);
+            if (++kst == C::kSK)
+                kst = 0, kph ^= 1u;
         }
         ++ke;
     }
 }
 
-// ---------------------------------------------------------------------------
-// The MMA-issuing warp.  Unit g (a tile, or a tile and a row tile): S(g) is
-// issued before P V of unit g - 1, so a softmax always overlaps a product.
-
+// O += P . V of every sub-unit.
 template <typename T, int D, int Parts, int Units>
-__device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
+__device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
-    // a negative scale is the sign of Q (bit 13: A negated), so the softmax
-    // takes maxima of raw scores
-    const uint32_t id_qk = idesc_f16<T>(128, 128, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t kPerTile = 2 * Units;
     constexpr uint32_t kIdPV = idesc_f16<T>(128, D, 0, 1);
+    constexpr uint32_t kHalf = 8 * C::kGroup >> 4;
     const uint32_t lead = elect_lane();
     const bool lane0 = (threadIdx.x & 31) == 0;
-    // descriptors of the first Q row tile and the first K and V stages; steps
-    // along a buffer are added to the address field (16-byte units)
-    const uint64_t q_desc = sdesc(smem, 16, 1024);
-    const uint64_t k_desc = sdesc(smem + C::kOffK, 16, C::kGroup);
     // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
     const uint64_t v_desc = sdesc(smem + C::kOffV, 1024, C::kGroup);
     const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
-    uint32_t cnt[2] = {0, 0};  // units issued per buffer
-    uint32_t pvs[2] = {0, 0};  // products issued per buffer
-    uint32_t ke = 0;           // items with tiles
-    uint32_t g = 0, t = 0;     // units, tiles
-    uint32_t kst = 0, kph = 0;  // K stage of tile t, phase of its use
-    uint32_t vst = 0, vph = 0;  // V stage of the next product, phase of its use
-
-    // P V of the unit in buffer b (row tile w); first: the buffer's first of its item
-    auto pv = [&](uint32_t b, int w, bool first) -> bool {
-        if (!mbar_wait_bounded(&M->pfull[b], (b ? pvs[1] : pvs[0]) & 1u))
-            return false;
-        if (b)
-            ++pvs[1];
-        else
-            ++pvs[0];
-        // O is free once the item before has been written out
-        if (first && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
-            return false;
-        if (!mbar_wait_bounded(&M->vfull[vst], vph))
-            return false;
-        tc_fence_after();
-        const int keep = first ? *reinterpret_cast<volatile int *>(&M->oinit[b]) : 1;
-        const uint64_t vd = v_desc + vst * (C::kTile >> 4);
-        const uint32_t o = tmem + 256 + b * D, pt = tmem + b * 128;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-#pragma unroll
-            for (int part = 0; part < Parts; ++part)
-                tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, vd + kk * (2 * C::kGroup >> 4), kIdPV,
-                          (kk | part) ? 1 : keep);
-        tc_commit_lead(lead, &M->pvdone[b]);
-        if (w == Units - 1) {
-            tc_commit_lead(lead, &M->vempty[vst]);
-            if (++vst == C::kSV)
-                vst = 0, vph ^= 1u;
-        }
-        return true;
-    };
-
+    uint32_t x = 0, ke = 0, vst = 0, vph = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
@@ -496,45 +506,33 @@ __device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, u
         const int ntiles = (nb + (1 << lbpt) - 1) >> lbpt;
         if (ntiles == 0)
             continue;
-        if (!mbar_wait_bounded(&M->qfull, ke & 1u))
-            return false;
-        const uint32_t g0 = g;
-        for (int ti = 0; ti < ntiles; ++ti, ++t) {
-            if (!mbar_wait_bounded(&M->kfull[kst], kph))
-                return false;
+        for (int ti = 0; ti < ntiles; ++ti) {
 #pragma unroll
-            for (int w = 0; w < Units; ++w, ++g) {
-                const uint32_t b = g & 1u;
-                // S shares its columns with the P of the buffer's last unit
-                const uint32_t used = b ? cnt[1] : cnt[0];
-                if (used > 0 && !mbar_wait_bounded(&M->pvdone[b], (used - 1) & 1u))
+            for (uint32_t e = 0; e < kPerTile; ++e, ++x) {
+                const uint32_t b = x & 3u, w = e & 1u;
+                if (!mbar_wait_bounded(&M->pfull[b], (x >> 2) & 1u))
+                    return false;
+                // O is free once the item before has been written out
+                if (e == 0 && ti == 0 && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
+                    return false;
+                if (e == 0 && !mbar_wait_bounded(&M->vfull[vst], vph))
                     return false;
                 tc_fence_after();
-                const uint64_t qd = q_desc + w * (C::kQ >> 4), kd = k_desc + kst * (C::kTile >> 4);
+                const int keep = ti == 0 && e < 2 ? *reinterpret_cast<volatile int *>(&M->oinit[w]) : 1;
+                const uint64_t vd = v_desc + vst * (C::kTile >> 4) + (Units == 2 ? e >> 1 : e) * kHalf;
+                const uint32_t o = tmem + 256 + w * D, pt = tmem + b * 64;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_ss(lead, tmem + b * 128, qd + ((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
-                              kd + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2), id_qk, kk > 0);
-                tc_commit_lead(lead, &M->sfull[b]);
-                if (b)
-                    ++cnt[1];
-                else
-                    ++cnt[0];
-                if (w == Units - 1) {
-                    tc_commit_lead(lead, &M->kempty[kst]);
-                    if (ti == ntiles - 1)
-                        tc_commit_lead(lead, &M->qempty);
-                }
-                // the product of the unit before (the first two units of an item are their buffers' first)
-                if (g > g0 && !pv(b ^ 1u, Units == 2 ? 1 - w : 0, g - g0 <= 2))
-                    return false;
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int part = 0; part < Parts; ++part)
+                        tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                                  vd + kk * (2 * C::kGroup >> 4), kIdPV, (kk | part) ? 1 : keep);
+                tc_commit_lead(lead, &M->pvdone[b]);
             }
-            if (++kst == C::kSK)
-                kst = 0, kph ^= 1u;
+            tc_commit_lead(lead, &M->vempty[vst]);
+            if (++vst == C::kSV)
+                vst = 0, vph ^= 1u;
         }
-        // the item's last product before anything of the next item
-        if (!pv((g - 1) & 1u, Units - 1, g - g0 <= 2))
-            return false;
         tc_commit_lead(lead, &M->odone);
         ++ke;
     }
@@ -543,58 +541,27 @@ __device__ inline bool tc_mma_warp(const TreeParams &p, char *smem, TcMisc *M, u
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 
-// The 128 cached tokens [tok, tok + 128) that a row attends, blocks aside:
+// The 64 cached tokens [tok, tok + 64) that a row attends, blocks aside:
 // committed tokens, then the row's drafted ones.  The mask words come in one
-// round trip (three 64-bit words cover 128 bits at any offset).
-__device__ inline uint32_t first_bits(int n) { return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u); }
+// round trip (two 64-bit words cover 64 bits at any offset).
+__device__ inline uint64_t first_bits(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
 
-__device__ inline void tree_bits128(const TreeParams &p, int s, int committed, int drafted, int i, int tok,
-                                    uint32_t *bits) {
+__device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed, int drafted, int i, int tok) {
     const int j = tok - committed;  // drafted index of the first token (negative: committed tokens first)
-    uint64_t w[3] = {0, 0, 0};
-    const int j0 = max(j, 0);
-    if (j > -128 && j < drafted) {
+    const int up = max(-j, 0), j0 = max(j, 0);
+    uint64_t d = 0;  // bit e: drafted token j0 + e
+    if (j > -64 && j < drafted) {
         if (p.mask) {
             const uint64_t *row = p.mask + (static_cast<long long>(s) * p.num_draft + i) * p.words + (j0 >> 6);
-            const int left = p.words - (j0 >> 6);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k < left)
-                    w[k] = row[k];
-        } else {  // a chain: bits 0 .. i
-            const int n = i + 1 - (j0 & ~63);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                w[k] = static_cast<uint64_t>(first_bits(n - 64 * k)) |
-                       static_cast<uint64_t>(first_bits(n - 64 * k - 32)) << 32;
+            const int sh = j0 & 63;
+            const uint64_t lo = row[0], hi = (j0 >> 6) + 1 < p.words ? row[1] : 0ull;
+            d = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+        } else {  // a chain
+            d = first_bits(i + 1 - j0);
         }
+        d &= first_bits(drafted - j0);
     }
-    // bit e of d: drafted token j0 + e
-    const int sh = j0 & 63;
-    uint64_t d[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        d[k] = sh ? (w[k] >> sh) | (w[k + 1] << (64 - sh)) : w[k];
-    uint32_t u[4] = {static_cast<uint32_t>(d[0]), static_cast<uint32_t>(d[0] >> 32), static_cast<uint32_t>(d[1]),
-                     static_cast<uint32_t>(d[1] >> 32)};
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        u[c] &= first_bits(drafted - j0 - 32 * c);
-    // committed tokens below them: the drafted bits start at bit -j
-    const int up = max(-j, 0);  // 0 .. 128 and more
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        uint32_t x = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {  // u[k] lands on bits [32 k + up, + 32)
-            const int at = 32 * k + up - 32 * c;
-            if (at >= 0 && at < 32)
-                x |= u[k] << at;
-            else if (at < 0 && at > -32)
-                x |= u[k] >> -at;
-        }
-        bits[c] = x | first_bits(up - 32 * c);
-    }
+    return up >= 64 ? ~0ull : first_bits(up) | (d << up);
 }
 
 // 16 bytes to an address of any 2-byte alignment.
@@ -682,18 +649,6 @@ __device__ inline void store_rows32(void *out, int dtype, long long row, int col
             store16(static_cast<uint16_t *>(out) + rows[k] * D + col + 8 * q, w[k]);
 }
 
-// Half a tile's scores of this thread's row; masked ones become -inf.
-__device__ inline void load_scores(uint32_t s_addr, int half, bool masked, const uint32_t *allow, float *sv) {
-    tmem_ld<32>(s_addr + 64 * half, sv);
-    tmem_ld<32>(s_addr + 64 * half + 32, sv + 32);
-    tmem_wait_ld();
-    if (masked) {
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-            sv[e] = (allow[2 * half + (e >> 5)] >> (e & 31)) & 1u ? sv[e] : -INFINITY;
-    }
-}
-
 template <typename T, int D, int Parts, int Units>
 __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
@@ -702,7 +657,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;  // row of the 128, and token of a tile
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + wg * 128, o_addr = tmem + lanes + 256 + wg * D;
+    const uint32_t o_addr = tmem + lanes + 256 + wg * D;
     const int bs = p.block_size, bpt = 128 / bs;
     const int G = p.num_heads / p.num_kv_heads;
     const int lg = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
@@ -710,7 +665,12 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
     // (a scale of 0 as one too small to matter: a masked -inf times 0 would be NaN)
     const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
     uint64_t *pzbar = Units == 1 ? &M->pz[wg] : &M->pz[0];
-    uint32_t use = 0, pzc = 0, ke = 0, g = 0;
+    // V rows of a sub-unit: two threads a token
+    const int tk = row & 63, vpart = row >> 6;
+    constexpr int kVChunks = C::kHalves == 2 ? 8 : 4;  // 16-byte chunks of a thread's part of a V row
+    const int vchunk0 = C::kHalves == 2 ? 0 : vpart * 4;
+    uint32_t cnt = 0;  // sub-units of this warpgroup: its cnt-th is sub-unit 2 cnt + wg
+    uint32_t pzc = 0, ke = 0;
 
     auto arrive_wait = [&](uint64_t *bar, uint32_t phase) -> bool {
         __syncwarp();
@@ -738,39 +698,38 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
         const long long orow = (static_cast<long long>(it.s) * p.num_draft + i) * p.num_heads + it.kvh * G + (r & (G - 1));
         float m = -INFINITY, l = 0.f;
         bool first = true;
-        for (int ti = 0; ti < ntiles; ++ti, g += Units) {
-            if (Units == 1 && static_cast<int>(g & 1u) != wg)
-                continue;
+        for (int su = 0; su < ntiles * Units; ++su, ++cnt) {
+            const int ti = Units == 2 ? su >> 1 : su, half = Units == 2 ? su & 1 : wg;
             const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
-            const int tok0 = (it.blk_lo << lbs) + ti * 128;
-            const bool drafts = it.drafted > 0 && tok0 + 128 > it.committed && tok0 < it.len;
-            uint32_t allow[4];  // set and used where the tile is masked
-            if (tok0 + 128 > it.committed)  // (the mask's round trip overlaps the wait for S)
-                tree_bits128(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0, allow);
-            else
-                allow[0] = allow[1] = allow[2] = allow[3] = 0xffffffffu;
-            if (!mbar_wait_bounded(&M->sfull[wg], use & 1u))
+            const uint32_t buf = (2 * cnt + wg) & 3u;
+            const uint32_t s_addr = tmem + lanes + buf * 64;
+            const int tok0 = (it.blk_lo << lbs) + ti * 128 + half * 64;
+            const bool drafts = it.drafted > 0 && tok0 + 64 > it.committed && tok0 < it.len;
+            uint64_t allow = ~0ull;
+            if (tok0 + 64 > it.committed)  // (the mask's round trip overlaps the wait for S)
+                allow = tree_bits64(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0);
+            if (!mbar_wait_bounded(&M->sfull[buf], (cnt >> 1) & 1u))
                 return false;
-            ++use;
             tc_fence_after();
-            const uint32_t blocks = M->meta[t % kTcMeta];
-            const bool whole = blocks == (1u << bpt) - 1u;
-            const bool masked = !whole || tok0 + 128 > it.committed;
+            // the sub-unit's blocks, bit e: block e of it
+            const uint32_t sub_bpt = static_cast<uint32_t>(bpt) >> 1;
+            const uint32_t blocks = (M->meta[t % kTcMeta] >> (half * sub_bpt)) & ((1u << sub_bpt) - 1u);
+            const bool whole = blocks == (1u << sub_bpt) - 1u;
+            const bool masked = !whole || tok0 + 64 > it.committed;
             if (!whole) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)  // 8-token pieces of the chunk
-                        if (!((blocks >> ((32 * c + 8 * e) >> lbs)) & 1u))
-                            allow[c] &= ~(0xffu << (8 * e));
+                for (int e = 0; e < 8; ++e)  // 8-token pieces
+                    if (!((blocks >> ((8 * e) >> lbs)) & 1u))
+                        allow &= ~(0xffull << (8 * e));
             }
-            bool poisoned = false;
+            bool poisoned = false, drop = false;  // drop: this thread's V row must not be multiplied
             const int vstage = static_cast<int>(t % C::kSV);
-            char *vrow = smem + C::kOffV + vstage * C::kTile + (row >> 3) * C::kGroup + (row & 7) * 128;
-            bool drop = false;  // this thread's token has a V row that must not be multiplied
+            const char *vhalf = smem + C::kOffV + vstage * C::kTile + half * (8 * C::kGroup);
+            char *vrow = const_cast<char *>(vhalf) + (tk >> 3) * C::kGroup + (tk & 7) * 128 +
+                         (C::kHalves == 2 ? vpart * 1024 : 0);
             if (masked) {
-                const int tok = tok0 + row;
-                const bool valid = ((blocks >> (row >> lbs)) & 1u) && tok < it.len;
+                const int tok = tok0 + tk;
+                const bool valid = ((blocks >> (tk >> lbs)) & 1u) && tok < it.len;
                 drop = !valid;
                 if (__any_sync(0xffffffffu, drop) || drafts)
                     if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
@@ -779,13 +738,11 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     bool bad = false;
                     if (valid && tok >= it.committed) {
 #pragma unroll
-                        for (int hf = 0; hf < C::kHalves; ++hf)
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const uint4 x = ld_shared_v4(vrow + hf * 1024 + ((c + row) & 7) * 16);
-                                bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
-                                      non_finite2<T>(x.w);
-                            }
+                        for (int c = 0; c < kVChunks; ++c) {
+                            const uint4 x = ld_shared_v4(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16);
+                            bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
+                                  non_finite2<T>(x.w);
+                        }
                     }
                     const uint32_t votes = __ballot_sync(0xffffffffu, bad);
                     if (lane == 0)
@@ -793,22 +750,29 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     if (!arrive_wait(pzbar, pzc++))
                         return false;
                     poisoned = (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
-                    drop = drop || bad;
+                    drop = drop || (((M->poison[wg][tk >> 5] | M->poison[wg][2 + (tk >> 5)]) >> (tk & 31)) & 1u);
                 }
             }
+            float sv[64];
             if (warp_live) {
-                // the row's maximum (raw scores; sc >= 0), half a tile at a time
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                tmem_ld<32>(s_addr, sv);
+                tmem_ld<32>(s_addr + 32, sv + 32);
+                tmem_wait_ld();
+                if (masked) {
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    float sv[64];
-                    load_scores(s_addr, hf, masked, allow, sv);
-#pragma unroll
-                    for (int e = 0; e < 64; e += 8)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), sv[e + 4 + c]);
+                    for (int e = 0; e < 64; ++e)
+                        sv[e] = (allow >> e) & 1u ? sv[e] : -INFINITY;
                 }
+                // the row's maximum (raw scores; sc >= 0)
+                float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int e = 4; e < 60; e += 8)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), sv[e + 4 + c]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    m4[c] = fmaxf(m4[c], sv[60 + c]);
                 float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 mt = mt == -INFINITY ? -INFINITY : mt * sc;
                 // O scales with the maximum in use; it changes only when the row's
@@ -816,6 +780,14 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 const float mn = fmaxf(m, mt);
                 const bool grow = first ? false : mn > m + kTcLazy;
                 if (__any_sync(0xffffffffu, grow)) {
+                    // the products into this O so far are done: the buffer's S came after
+                    // the one of two sub-units before, and the last one is waited for
+                    if (cnt > 0) {
+                        const uint32_t last = (2 * (cnt - 1) + wg) & 3u;
+                        if (!mbar_wait_bounded(&M->pvdone[last], ((cnt - 1) >> 1) & 1u))
+                            return false;
+                        tc_fence_after();
+                    }
                     const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -838,6 +810,12 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             if (poisoned) {
                 // drafted tokens with non-finite V: added here to the rows that attend them
                 if (warp_live) {
+                    if (!first) {
+                        const uint32_t last = (2 * (cnt - 1) + wg) & 3u;
+                        if (!mbar_wait_bounded(&M->pvdone[last], ((cnt - 1) >> 1) & 1u))
+                            return false;
+                        tc_fence_after();
+                    }
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
                         if (first) {
@@ -848,18 +826,16 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                             tmem_ld<16>(o_addr + c, o);
                             tmem_wait_ld();
                         }
-                        for (int u = 0; u < 128; ++u) {
-                            if (!((M->poison[wg][u >> 5] >> (u & 31)) & 1u))
+                        for (int u = 0; u < 64; ++u) {
+                            if (!(((M->poison[wg][u >> 5] | M->poison[wg][2 + (u >> 5)]) >> (u & 31)) & 1u))
                                 continue;
                             float x[2];
                             tmem_ld<2>(s_addr + (u & ~1), x);
                             tmem_wait_ld();
-                            const float s = u & 1 ? x[1] : x[0];
-                            const uint32_t a = u < 64 ? (u < 32 ? allow[0] : allow[1]) : (u < 96 ? allow[2] : allow[3]);
-                            if ((a >> (u & 31)) & 1u) {
-                                const float pw = fast_exp2(fmaf(s, sc, -me));
-                                const char *vr = smem + C::kOffV + vstage * C::kTile + (u >> 3) * C::kGroup +
-                                                 (u & 7) * 128 + (c >> 6) * 1024;
+                            const float sx = u & 1 ? x[1] : x[0];
+                            if ((allow >> u) & 1u) {
+                                const float pw = fast_exp2(fmaf(sx, sc, -me));
+                                const char *vr = vhalf + (u >> 3) * C::kGroup + (u & 7) * 128 + (c >> 6) * 1024;
 #pragma unroll
                                 for (int e = 0; e < 16; e += 2) {
                                     const int ch = ((c & 63) + e) >> 3;  // 16-byte chunk, swizzled by the row
@@ -887,16 +863,13 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             if (warp_live) {
                 // (a masked score is -inf: its weight is exactly 0)
                 float2 l2 = make_float2(0.f, 0.f);
-                float sv[64];
                 const float2 sc2 = make_float2(sc, sc), me2 = make_float2(-me, -me);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if ((c & 1) == 0)
-                        load_scores(s_addr, c >> 1, masked, allow, sv);
+                for (int c = 0; c < 2; ++c) {
                     uint32_t w[16], wl[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        float2 x = fma2(make_float2(sv[32 * (c & 1) + e], sv[32 * (c & 1) + e + 1]), sc2, me2);
+                        float2 x = fma2(make_float2(sv[32 * c + e], sv[32 * c + e + 1]), sc2, me2);
                         x.x = fast_exp2(x.x), x.y = fast_exp2(x.y);
                         l2 = add2(l2, x);
                         w[e / 2] = pack2<T>(x.x, x.y);
@@ -915,17 +888,16 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             }
             if (drop) {
 #pragma unroll
-                for (int hf = 0; hf < C::kHalves; ++hf)
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        *reinterpret_cast<uint4 *>(vrow + hf * 1024 + ((c + row) & 7) * 16) = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < kVChunks; ++c)
+                    *reinterpret_cast<uint4 *>(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16) =
+                        make_uint4(0, 0, 0, 0);
             }
             if (masked)
                 fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&M->pfull[wg]);
+                mbar_arrive(&M->pfull[buf]);
             first = false;
         }
         // ---- the item's output: final rows, or a partial per row
@@ -1026,21 +998,22 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < kTcItems; ++i) {
             mbar_init(&M->ifull[i], 1);
-            mbar_init(&M->iempty[i], 10);  // Q loader, MMA thread, softmax warps
+            mbar_init(&M->iempty[i], 10);  // S warp, P V warp, softmax warps
         }
         mbar_init(&M->qfull, 1);
         mbar_init(&M->qempty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&M->sfull[i], 1);
             mbar_init(&M->pfull[i], 4);
             mbar_init(&M->pvdone[i], 1);
-            mbar_init(&M->pz[i], Units == 1 ? 4 : 8);
         }
+        for (int i = 0; i < 2; ++i)
+            mbar_init(&M->pz[i], Units == 1 ? 4 : 8);
         mbar_init(&M->odone, 1);
         mbar_init(&M->ofree, 8);
         mbar_init(&M->xbar, 8);
         mbar_init(&M->fin, 1);
-        mbar_init(&M->done, 8);
+        mbar_init(&M->done, 9);  // softmax warps, P V warp
         fence_mbar_init();
     }
     if (warp == 2) {
@@ -1052,17 +1025,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
-    // registers: 384 x 168 = 128 x 88 + 256 x 208
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             tc_kproducer<D, Units>(p, &tmk, smem, M);
         } else if (warp == 1) {
             tc_vproducer<D, Units>(p, &tmv, smem, M);
         } else if (warp == 2) {
-            ok = tc_mma_warp<T, D, Parts, Units>(p, smem, M, tmem);
-            // every MMA has finished, and the softmax warps are done with tensor memory, before it goes
+            ok = tc_s_warp<T, D, Units>(p, &tmq, smem, M, tmem);
+            // every S has finished, and everyone is done with tensor memory, before it goes
             tc_commit_lead(elect_lane(), &M->fin);
             (void)mbar_wait_bounded(&M->fin, 0);
             (void)mbar_wait_bounded(&M->done, 0);
@@ -1070,12 +1041,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             tmem_dealloc(tmem, 512);
         } else {
-            if ((threadIdx.x & 31) == 0)
-                ok = tc_qloader<D, Units>(p, &tmq, smem, M);
+            ok = tc_pv_warp<T, D, Parts, Units>(p, smem, M, tmem);
+            // done once its products have finished
+            tc_commit_lead(elect_lane(), &M->done);
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
