@@ -86,11 +86,15 @@ pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t strea
     if (st != PA_OK)
         return st;
     if (p.max_parts > 1) {
-        const long long rows = static_cast<long long>(p.num_seqs) * p.num_draft * p.num_heads;
-        constexpr int kRows = kTreeMergeThreads / 32;
+        const int rows = p.num_draft * (p.num_heads / p.num_kv_heads);
+        const int lrb = tree_merge_log_rows(rows, head_dim);
+        const long long ctas = static_cast<long long>(p.num_seqs) * p.num_kv_heads * ((rows + (1 << lrb) - 1) >> lrb) *
+                               (head_dim / (kTreeMergeCols * (32 >> lrb)));
+        if (ctas > INT_MAX)
+            return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_draft * num_heads too large");
         const void *mf = head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_merge_kernel<64>)
                                         : reinterpret_cast<const void *>(&pa_tree_merge_kernel<128>);
-        e = launch_dependent(mf, dim3(static_cast<unsigned>((rows + kRows - 1) / kRows)), dim3(kTreeMergeThreads),
+        e = launch_dependent(mf, dim3(static_cast<unsigned>(ctas)), dim3(kTreeMergeThreads),
                              args, 0, stream);
         if (e != cudaSuccess)
             return cuda_fail(e, "tree merge launch");

@@ -7,7 +7,9 @@
 // the same K/V rows: cached token t is attended by row r when
 //   t < L - T_s   (committed), or bit t - (L - T_s) of mask[s][i] is set.
 // Work unit: (sequence, kv head, row tile, context partition); partitions are
-// merged by log-sum-exp as in the other decodes.
+// merged by log-sum-exp as in the other decodes.  A partition's partial is
+// column-major over the rows of its (sequence, kv head): accumulators
+// [D][T * G], then (running max, denominator) pairs [T * G] in their own array.
 #pragma once
 
 #include "pa_decode.cuh"
@@ -141,58 +143,116 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             for (int e = 0; e < E; ++e)
                 store_out(p.out, p.out_dtype, orow * D + l8 + 8 * e, l == 0.f ? 0.f : acc[e] / l);
         } else {
-            const long long pr = orow * p.max_parts + part;
+            const long long item = (static_cast<long long>(s) * p.num_kv_heads + kvh) * p.max_parts + part;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                p.part_acc[pr * D + l8 + 8 * e] = acc[e];
-            if (l8 == 0) {
-                p.part_ml[pr * 2] = m;
-                p.part_ml[pr * 2 + 1] = l;
-            }
+                p.part_acc[(item * D + l8 + 8 * e) * rows + r] = acc[e];
+            if (l8 == 0)
+                reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(m, l);
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the partitions of every row of a multi-partition sequence, a warp a
-// row; a partition in which the row attends nothing (l == 0) left no
-// accumulator.
-constexpr int kTreeMergeThreads = 128;
+// Merge of the partitions of every row of a multi-partition sequence.  A CTA
+// takes RB rows of a (sequence, kv head) and 16 * 32 / RB columns (RB: 32, or
+// the next power of two of fewer rows): lane = (row, column), so partials are
+// read as whole lines.  Its 8 warps take every eighth partition each (one round
+// trip of 17 loads a partition, few in sequence however long the context), and
+// their states meet in shared memory.  A partition in which a row attends
+// nothing (l == 0) left no accumulator.
+constexpr int kTreeMergeThreads = 256;
+constexpr int kTreeMergeWarps = kTreeMergeThreads / 32;
+constexpr int kTreeMergeCols = 16;  // columns of a lane
+
+// log2 of RB for `rows` rows: at most 32, and at least what leaves the CTA's columns within D
+__host__ __device__ inline int tree_merge_log_rows(int rows, int D) {
+    int l = D == 64 ? 3 : 2;
+    while (l < 5 && (1 << l) < rows)
+        ++l;
+    return l;
+}
 
 template <int D>
-__global__ void __launch_bounds__(kTreeMergeThreads) pa_tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_merge_kernel(const TreeParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int kPer = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * (kTreeMergeThreads / 32) + (threadIdx.x >> 5);
-    if (row >= static_cast<long long>(p.num_seqs) * p.num_draft * p.num_heads)
-        return;
-    const int s = static_cast<int>(row / (static_cast<long long>(p.num_draft) * p.num_heads));
+    constexpr int E = kTreeMergeCols;
+    __shared__ float acc[kTreeMergeWarps][E][33];  // [warp][element][lane]
+    __shared__ float2 state[kTreeMergeWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = p.num_heads / p.num_kv_heads;
+    const int rows = p.num_draft * G;
+    const int lrb = tree_merge_log_rows(rows, D);
+    const int RB = 1 << lrb, CB = 32 >> lrb;  // rows, and columns a step
+    const int chunks = (rows + RB - 1) >> lrb;
+    const int col_chunks = D / (E * CB);
+    long long f = blockIdx.x;
+    const int col0 = static_cast<int>(f % col_chunks) * (E * CB);
+    f /= col_chunks;
+    const int r0 = static_cast<int>(f % chunks) << lrb;
+    const long long seq_head = f / chunks;
+    const int s = static_cast<int>(seq_head / p.num_kv_heads);
+    const int kvh = static_cast<int>(seq_head - static_cast<long long>(s) * p.num_kv_heads);
+    const int r = r0 + (lane & (RB - 1));
     const SeqSpan sp = seq_span(ld_nc_i32(p.context_lens + s), p.max_len, 0, p.block_size, p.bpp);
     if (sp.nparts <= 1)
         return;
-    const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + row * p.max_parts;
-    const float *a = p.part_acc + row * p.max_parts * D + lane * kPer;
-    float M = -INFINITY, den = 0.f, num[kPer];
+    float M = -INFINITY, den = 0.f, num[E];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
+    for (int e = 0; e < E; ++e)
         num[e] = 0.f;
-    for (int q = 0; q < sp.nparts; ++q) {
-        const float2 v = ml[q];
-        if (v.y == 0.f)
-            continue;
-        const float mn = fmaxf(M, v.x);
-        const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
-        den = den * keep + v.y * add;
+    if (r < rows) {
+        const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + seq_head * p.max_parts * rows + r;
+        const float *a = p.part_acc + (seq_head * p.max_parts * D + col0 + (lane >> lrb)) * rows + r;
+        for (int q = warp; q < sp.nparts; q += kTreeMergeWarps) {
+            const float2 v = ml[static_cast<long long>(q) * rows];
+            const float *aq = a + static_cast<long long>(q) * D * rows;
+            float x[E];
 #pragma unroll
-        for (int e = 0; e < kPer; ++e)
-            num[e] = num[e] * keep + a[static_cast<long long>(q) * D + e] * add;
-        M = mn;
+            for (int e = 0; e < E; ++e)
+                x[e] = aq[static_cast<long long>(e * CB) * rows];
+            if (v.y == 0.f)
+                continue;
+            const float mn = fmaxf(M, v.x);
+            const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
+            den = den * keep + v.y * add;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                num[e] = num[e] * keep + x[e] * add;
+            M = mn;
+        }
     }
+    state[warp][lane] = make_float2(M, den);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e)
-        store_out(p.out, p.out_dtype, row * D + lane * kPer + e, den == 0.f ? 0.f : num[e] / den);
+    for (int e = 0; e < E; ++e)
+        acc[warp][e][lane] = num[e];
+    __syncthreads();
+    // output o of the CTA: row o / (E CB), column o % (E CB)
+    for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
+        const int rr = o / (E * CB), c = o - rr * (E * CB);
+        if (r0 + rr >= rows)
+            break;
+        const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kTreeMergeWarps; ++w)
+            if (state[w][ln].y != 0.f)
+                m = fmaxf(m, state[w][ln].x);
+        float n = 0.f, d = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTreeMergeWarps; ++w) {
+            const float2 v = state[w][ln];
+            if (v.y != 0.f) {
+                const float sc = v.x == m ? 1.f : exp2f(v.x - m);
+                d = fmaf(v.y, sc, d);
+                n = fmaf(acc[w][e][ln], sc, n);
+            }
+        }
+        const int i = (r0 + rr) / G, h = kvh * G + (r0 + rr) % G;
+        const long long orow = (static_cast<long long>(s) * p.num_draft + i) * p.num_heads + h;
+        store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+    }
 }
 
 }  // namespace pa

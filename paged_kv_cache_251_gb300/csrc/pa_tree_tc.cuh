@@ -564,89 +564,67 @@ __device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed
     return up >= 64 ? ~0ull : first_bits(up) | (d << up);
 }
 
-// 16 bytes to an address of any 2-byte alignment.
-template <typename E> __device__ inline void store16(E *p, const uint32_t *w) {
-    if ((reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+// 32 columns of an accumulator row to the output.
+__device__ inline void store_cols32(void *out, int dtype, long long idx, const float *v) {
+    if (dtype == PA_F32) {
+        float *o = static_cast<float *>(out) + idx;
+        if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                o[i] = v[i];
+        }
         return;
     }
-    if constexpr (sizeof(E) == 4) {
+    uint16_t *o = static_cast<uint16_t *>(out) + idx;
+    uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            p[e] = __uint_as_float(w[e]);
+    for (int e = 0; e < 16; ++e)
+        w[e] = dtype == PA_F16 ? pack2<__half>(v[2 * e], v[2 * e + 1]) : pack2<__nv_bfloat16>(v[2 * e], v[2 * e + 1]);
+    if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            p[2 * e] = static_cast<E>(w[e]), p[2 * e + 1] = static_cast<E>(w[e] >> 16);
+        for (int e = 0; e < 16; ++e)
+            o[2 * e] = static_cast<uint16_t>(w[e]), o[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
     }
 }
 
-// Exchange pieces among 4 adjacent lanes: v holds piece k (N words) of this
-// lane's own row; afterwards v holds piece (lane & 3) of the rows of lanes
-// (lane & ~3) + k.  A store then covers 4 pieces of one row with 4 lanes
-// instead of one piece of 32 rows (8 lines an instruction instead of 32).
-template <int N> __device__ inline void transpose4(uint32_t (*v)[N]) {
-    const int lane = threadIdx.x & 31;
+__device__ inline float max32(const float *v) {
+    float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]);
 #pragma unroll
-    for (int step = 1; step <= 2; step <<= 1) {
-        const bool up = lane & step;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (k & step)
-                continue;
-            // lanes with the bit clear send piece k + step and keep k; the others the other way
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const uint32_t send = up ? v[k][e] : v[k + step][e];
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, step);
-                if (up)
-                    v[k][e] = got;
-                else
-                    v[k + step][e] = got;
-            }
-        }
-    }
+    for (int e = 4; e < 32; e += 4)
+        a = fmaxf(fmaxf(a, v[e]), v[e + 1]), b = fmaxf(fmaxf(b, v[e + 2]), v[e + 3]);
+    return fmaxf(a, b);
 }
 
-// 32 columns of 32 accumulator rows (one row a lane) to memory, whole warp:
-// row `row` (in rows of D elements; -1: this lane's row is not stored), columns
-// from col.
-template <int D>
-__device__ inline void store_rows32(void *out, int dtype, long long row, int col, const float *v) {
-    const int q = threadIdx.x & 3;
-    long long rows[4];  // of the lanes of this group of four
+// The weights 2^(s sc - me) of 32 scores of this thread's row: summed, and as
+// the P operand over the columns the scores came from (hi parts in the first
+// 16, lo parts behind them).
+template <typename T, int Parts>
+__device__ inline void weights32(const float *s, float sc, float me, uint32_t addr, float2 &sum) {
+    const float2 sc2 = make_float2(sc, sc), me2 = make_float2(-me, -me);
+    uint32_t w[16], wl[16];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        rows[k] = __shfl_sync(0xffffffffu, row, (threadIdx.x & 28) + k);
-    if (dtype == PA_F32) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {  // 16 columns: 4 pieces of 16 bytes
-            uint32_t w[4][4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[k][e] = __float_as_uint(v[16 * hf + 4 * k + e]);
-            transpose4<4>(w);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (rows[k] >= 0)
-                    store16(static_cast<float *>(out) + rows[k] * D + col + 16 * hf + 4 * q, w[k]);
+    for (int e = 0; e < 32; e += 2) {
+        float2 x = fma2(make_float2(s[e], s[e + 1]), sc2, me2);
+        x.x = fast_exp2(x.x), x.y = fast_exp2(x.y);
+        sum = add2(sum, x);
+        w[e / 2] = pack2<T>(x.x, x.y);
+        if constexpr (Parts == 2) {
+            float h0, h1;
+            unpack2<T>(w[e / 2], h0, h1);
+            wl[e / 2] = pack2<T>(x.x - h0, x.y - h1);
         }
-        return;
     }
-    uint32_t w[4][4];  // 4 pieces of 8 columns
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[k][e] = dtype == PA_F16 ? pack2<__half>(v[8 * k + 2 * e], v[8 * k + 2 * e + 1])
-                                      : pack2<__nv_bfloat16>(v[8 * k + 2 * e], v[8 * k + 2 * e + 1]);
-    transpose4<4>(w);
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (rows[k] >= 0)
-            store16(static_cast<uint16_t *>(out) + rows[k] * D + col + 8 * q, w[k]);
+    tmem_st16(addr, w);
+    if constexpr (Parts == 2)
+        tmem_st16(addr + 16, wl);
 }
 
 template <typename T, int D, int Parts, int Units>
@@ -669,6 +647,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
     const int tk = row & 63, vpart = row >> 6;
     constexpr int kVChunks = C::kHalves == 2 ? 8 : 4;  // 16-byte chunks of a thread's part of a V row
     const int vchunk0 = C::kHalves == 2 ? 0 : vpart * 4;
+    const uint32_t sub_bpt = static_cast<uint32_t>(bpt) >> 1, sub_full = (1u << sub_bpt) - 1u;
     uint32_t cnt = 0;  // sub-units of this warpgroup: its cnt-th is sub-unit 2 cnt + wg
     uint32_t pzc = 0, ke = 0;
 
@@ -695,93 +674,94 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
         const int i = r >> lg;
         const bool stored = i < p.num_draft, live = i < it.drafted;
         const bool warp_live = __any_sync(0xffffffffu, live);
-        const long long orow = (static_cast<long long>(it.s) * p.num_draft + i) * p.num_heads + it.kvh * G + (r & (G - 1));
+        const long long orow =
+            (static_cast<long long>(it.s) * p.num_draft + i) * p.num_heads + it.kvh * G + (r & (G - 1));
         float m = -INFINITY, l = 0.f;
         bool first = true;
-        for (int su = 0; su < ntiles * Units; ++su, ++cnt) {
+        // the scores of the sub-unit at hand, and their maximum; `ready`: loaded
+        // during the one before (interior sub-units only: nothing masked)
+        float sv[64], top = -INFINITY;
+        bool ready = false;
+        const int subs = ntiles * Units;
+        for (int su = 0; su < subs; ++su, ++cnt) {
             const int ti = Units == 2 ? su >> 1 : su, half = Units == 2 ? su & 1 : wg;
             const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
             const uint32_t buf = (2 * cnt + wg) & 3u;
             const uint32_t s_addr = tmem + lanes + buf * 64;
             const int tok0 = (it.blk_lo << lbs) + ti * 128 + half * 64;
-            const bool drafts = it.drafted > 0 && tok0 + 64 > it.committed && tok0 < it.len;
             uint64_t allow = ~0ull;
-            if (tok0 + 64 > it.committed)  // (the mask's round trip overlaps the wait for S)
-                allow = tree_bits64(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0);
-            if (!mbar_wait_bounded(&M->sfull[buf], (cnt >> 1) & 1u))
-                return false;
-            tc_fence_after();
-            // the sub-unit's blocks, bit e: block e of it
-            const uint32_t sub_bpt = static_cast<uint32_t>(bpt) >> 1;
-            const uint32_t blocks = (M->meta[t % kTcMeta] >> (half * sub_bpt)) & ((1u << sub_bpt) - 1u);
-            const bool whole = blocks == (1u << sub_bpt) - 1u;
-            const bool masked = !whole || tok0 + 64 > it.committed;
-            if (!whole) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)  // 8-token pieces
-                    if (!((blocks >> ((8 * e) >> lbs)) & 1u))
-                        allow &= ~(0xffull << (8 * e));
-            }
-            bool poisoned = false, drop = false;  // drop: this thread's V row must not be multiplied
+            bool masked = false, poisoned = false, drop = false;  // drop: this thread's V row must not be multiplied
             const int vstage = static_cast<int>(t % C::kSV);
             const char *vhalf = smem + C::kOffV + vstage * C::kTile + half * (8 * C::kGroup);
             char *vrow = const_cast<char *>(vhalf) + (tk >> 3) * C::kGroup + (tk & 7) * 128 +
                          (C::kHalves == 2 ? vpart * 1024 : 0);
-            if (masked) {
-                const int tok = tok0 + tk;
-                const bool valid = ((blocks >> (tk >> lbs)) & 1u) && tok < it.len;
-                drop = !valid;
-                if (__any_sync(0xffffffffu, drop) || drafts)
-                    if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
-                        return false;
-                if (drafts) {
-                    bool bad = false;
-                    if (valid && tok >= it.committed) {
+            if (!ready) {
+                const bool drafts = it.drafted > 0 && tok0 + 64 > it.committed && tok0 < it.len;
+                if (tok0 + 64 > it.committed)  // (the mask's round trip overlaps the wait for S)
+                    allow = tree_bits64(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0);
+                if (!mbar_wait_bounded(&M->sfull[buf], (cnt >> 1) & 1u))
+                    return false;
+                tc_fence_after();
+                if (warp_live) {
+                    tmem_ld<32>(s_addr, sv);
+                    tmem_ld<32>(s_addr + 32, sv + 32);
+                }
+                // the sub-unit's blocks, bit e: block e of it
+                const uint32_t blocks = (M->meta[t % kTcMeta] >> (half * sub_bpt)) & sub_full;
+                const bool whole = blocks == sub_full;
+                masked = !whole || tok0 + 64 > it.committed;
+                if (!whole) {
 #pragma unroll
-                        for (int c = 0; c < kVChunks; ++c) {
-                            const uint4 x = ld_shared_v4(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16);
-                            bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
-                                  non_finite2<T>(x.w);
+                    for (int e = 0; e < 8; ++e)  // 8-token pieces
+                        if (!((blocks >> ((8 * e) >> lbs)) & 1u))
+                            allow &= ~(0xffull << (8 * e));
+                }
+                if (masked) {
+                    const int tok = tok0 + tk;
+                    const bool valid = ((blocks >> (tk >> lbs)) & 1u) && tok < it.len;
+                    drop = !valid;
+                    if (__any_sync(0xffffffffu, drop) || drafts)
+                        if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
+                            return false;
+                    if (drafts) {
+                        bool bad = false;
+                        if (valid && tok >= it.committed) {
+#pragma unroll
+                            for (int c = 0; c < kVChunks; ++c) {
+                                const uint4 x = ld_shared_v4(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16);
+                                bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
+                                      non_finite2<T>(x.w);
+                            }
                         }
+                        const uint32_t votes = __ballot_sync(0xffffffffu, bad);
+                        if (lane == 0)
+                            M->poison[wg][quarter] = votes;
+                        if (!arrive_wait(pzbar, pzc++))
+                            return false;
+                        poisoned =
+                            (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
+                        drop = drop || (((M->poison[wg][tk >> 5] | M->poison[wg][2 + (tk >> 5)]) >> (tk & 31)) & 1u);
                     }
-                    const uint32_t votes = __ballot_sync(0xffffffffu, bad);
-                    if (lane == 0)
-                        M->poison[wg][quarter] = votes;
-                    if (!arrive_wait(pzbar, pzc++))
-                        return false;
-                    poisoned = (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
-                    drop = drop || (((M->poison[wg][tk >> 5] | M->poison[wg][2 + (tk >> 5)]) >> (tk & 31)) & 1u);
+                }
+                if (warp_live) {
+                    tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            sv[e] = (allow >> e) & 1u ? sv[e] : -INFINITY;
+                    }
+                    top = fmaxf(max32(sv), max32(sv + 32));
                 }
             }
-            float sv[64];
             if (warp_live) {
-                tmem_ld<32>(s_addr, sv);
-                tmem_ld<32>(s_addr + 32, sv + 32);
-                tmem_wait_ld();
-                if (masked) {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e)
-                        sv[e] = (allow >> e) & 1u ? sv[e] : -INFINITY;
-                }
                 // the row's maximum (raw scores; sc >= 0)
-                float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-                for (int e = 4; e < 60; e += 8)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        m4[c] = fmaxf(fmaxf(m4[c], sv[e + c]), sv[e + 4 + c]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    m4[c] = fmaxf(m4[c], sv[60 + c]);
-                float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-                mt = mt == -INFINITY ? -INFINITY : mt * sc;
+                const float mt = top == -INFINITY ? -INFINITY : top * sc;
                 // O scales with the maximum in use; it changes only when the row's
                 // maximum passed it by kTcLazy
                 const float mn = fmaxf(m, mt);
                 const bool grow = first ? false : mn > m + kTcLazy;
                 if (__any_sync(0xffffffffu, grow)) {
-                    // the products into this O so far are done: the buffer's S came after
-                    // the one of two sub-units before, and the last one is waited for
+                    // every product into this O so far is done once the last one is
                     if (cnt > 0) {
                         const uint32_t last = (2 * (cnt - 1) + wg) & 3u;
                         if (!mbar_wait_bounded(&M->pvdone[last], ((cnt - 1) >> 1) & 1u))
@@ -860,30 +840,29 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             }
             if (first && quarter == 0 && lane == 0)
                 M->oinit[wg] = poisoned ? 1 : 0;
+            ready = false;
             if (warp_live) {
                 // (a masked score is -inf: its weight is exactly 0)
                 float2 l2 = make_float2(0.f, 0.f);
-                const float2 sc2 = make_float2(sc, sc), me2 = make_float2(-me, -me);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16], wl[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        float2 x = fma2(make_float2(sv[32 * c + e], sv[32 * c + e + 1]), sc2, me2);
-                        x.x = fast_exp2(x.x), x.y = fast_exp2(x.y);
-                        l2 = add2(l2, x);
-                        w[e / 2] = pack2<T>(x.x, x.y);
-                        if constexpr (Parts == 2) {
-                            float h0, h1;
-                            unpack2<T>(w[e / 2], h0, h1);
-                            wl[e / 2] = pack2<T>(x.x - h0, x.y - h1);
-                        }
-                    }
-                    tmem_st16(s_addr + 32 * c, w);
-                    if constexpr (Parts == 2)
-                        tmem_st16(s_addr + 32 * c + 16, wl);
+                weights32<T, Parts>(sv, sc, me, s_addr, l2);
+                // the next sub-unit's scores replace this one's as they are used up,
+                // when its S is there and nothing of it is masked
+                const int nti = Units == 2 ? (su + 1) >> 1 : su + 1, nhalf = Units == 2 ? (su + 1) & 1 : wg;
+                const uint32_t nbuf = (buf + 2) & 3u;
+                if (su + 1 < subs && (it.blk_lo << lbs) + nti * 128 + nhalf * 64 + 64 <= it.committed)
+                    ready = __all_sync(0xffffffffu, mbar_try_wait(&M->sfull[nbuf], ((cnt + 1) >> 1) & 1u)) &&
+                            ((M->meta[(it.t_first + nti) % kTcMeta] >> (nhalf * sub_bpt)) & sub_full) == sub_full;
+                if (ready) {
+                    tc_fence_after();
+                    tmem_ld<32>(tmem + lanes + nbuf * 64, sv);
                 }
+                weights32<T, Parts>(sv + 32, sc, me, s_addr + 32, l2);
                 l += l2.x + l2.y;
+                if (ready) {
+                    tmem_ld<32>(tmem + lanes + nbuf * 64 + 32, sv + 32);
+                    tmem_wait_ld();
+                    top = fmaxf(max32(sv), max32(sv + 32));
+                }
                 tmem_wait_st();
             }
             if (drop) {
@@ -922,41 +901,54 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 den = a.y * f0 + b.y * f1;
             }
         }
-        const float inv = den == 0.f ? 0.f : 1.f / den;
+        // final rows row by row, partials column by column (the lanes' rows are
+        // adjacent there: whole lines without any exchange)
         constexpr int kCols = Units == 1 ? D / 2 : D;
         const int col0 = Units == 1 ? wg * kCols : 0;
-        const long long pr = orow * p.max_parts + it.part;
-        // (rows a warp need not write: none of them is stored)
-        const bool any_stored = __any_sync(0xffffffffu, stored);
-        for (int c = any_stored ? col0 : D; c < col0 + kCols; c += 32) {
-            float o[32];
-            if (ntiles > 0 && warp_live) {
-                if (Units == 1) {
-                    float x[32];
-                    tmem_ld<32>(tmem + lanes + 256 + c, o);
-                    tmem_ld<32>(tmem + lanes + 256 + D + c, x);
-                    tmem_wait_ld();
+        const int rows = p.num_draft << lg;
+        const long long item = (static_cast<long long>(it.s) * p.num_kv_heads + it.kvh) * p.max_parts + it.part;
+        if (__any_sync(0xffffffffu, stored)) {
+            if (direct) {
+                const float inv = den == 0.f ? 0.f : __fdividef(1.f, den);
+                f0 = den == 0.f ? 0.f : f0 * inv;  // (a factor of 0 is a row that saw nothing: 0, not 0 x garbage)
+                f1 = den == 0.f ? 0.f : f1 * inv;
+            }
+#pragma unroll 1
+            for (int c = col0; c < col0 + kCols; c += 32) {
+                float o[32];
+                if (ntiles > 0 && warp_live) {
+                    tmem_ld<32>(tmem + lanes + 256 + (Units == 1 ? 0 : wg * D) + c, o);
+                    if (Units == 1) {
+                        float x[32];
+                        tmem_ld<32>(tmem + lanes + 256 + D + c, x);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : x[e] * f1);
+                    } else {
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = f0 == 0.f ? 0.f : o[e] * f0;
+                    }
+                } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : x[e] * f1);
-                } else {
-                    tmem_ld<32>(o_addr + c, o);
-                    tmem_wait_ld();
+                        o[e] = 0.f;
+                }
+                if (direct) {
+                    if (stored)
+                        store_cols32(p.out, p.out_dtype, orow * D + c, o);
+                } else if (stored && den != 0.f) {
+                    float *a = p.part_acc + (item * D + c) * rows + r;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        a[static_cast<long long>(e) * rows] = o[e];
                 }
             }
-            if (direct) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    o[e] = den == 0.f ? 0.f : o[e] * inv;
-                store_rows32<D>(p.out, p.out_dtype, stored ? orow : -1, c, o);
-            } else if (warp_live) {
-                store_rows32<D>(p.part_acc, PA_F32, stored && den != 0.f ? pr : -1, c, o);
-            }
         }
-        if (stored && !direct && col0 == 0) {
-            p.part_ml[pr * 2] = mx;
-            p.part_ml[pr * 2 + 1] = den;
-        }
+        if (stored && !direct && col0 == 0)
+            reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(mx, den);
         if (ntiles > 0) {
             tc_fence_before();
             __syncwarp();
@@ -1025,8 +1017,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
+    // registers: 384 x 168 = 128 x 104 + 256 x 200
     bool ok = true;
     if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp == 0) {
             tc_kproducer<D, Units>(p, &tmk, smem, M);
         } else if (warp == 1) {
@@ -1047,6 +1041,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
