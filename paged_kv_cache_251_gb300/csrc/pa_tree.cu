@@ -88,14 +88,18 @@ pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t strea
     if (p.max_parts > 1) {
         const int rows = p.num_draft * (p.num_heads / p.num_kv_heads);
         const int lrb = tree_merge_log_rows(rows, head_dim);
-        const long long ctas = static_cast<long long>(p.num_seqs) * p.num_kv_heads * ((rows + (1 << lrb) - 1) >> lrb) *
-                               (head_dim / (kTreeMergeCols * (32 >> lrb)));
+        const int col_chunks = head_dim / (kTreeMergeCols * (32 >> lrb));  // a power of two
+        const long long groups = static_cast<long long>(p.num_seqs) * p.num_kv_heads * ((rows + (1 << lrb) - 1) >> lrb);
+        int steps = col_chunks;
+        while (steps > 1 && groups * (col_chunks / steps) < 4LL * sms)
+            steps /= 2;
+        const long long ctas = groups * (col_chunks / steps);
         if (ctas > INT_MAX)
             return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_draft * num_heads too large");
         const void *mf = head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_merge_kernel<64>)
                                         : reinterpret_cast<const void *>(&pa_tree_merge_kernel<128>);
-        e = launch_dependent(mf, dim3(static_cast<unsigned>(ctas)), dim3(kTreeMergeThreads),
-                             args, 0, stream);
+        void *margs[] = {&p, &steps};
+        e = launch_dependent(mf, dim3(static_cast<unsigned>(ctas)), dim3(kTreeMergeThreads), margs, 0, stream);
         if (e != cudaSuccess)
             return cuda_fail(e, "tree merge launch");
     }

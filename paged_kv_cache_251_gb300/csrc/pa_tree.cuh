@@ -160,7 +160,9 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
 // read as whole lines.  Its 8 warps take every eighth partition each (one round
 // trip of 17 loads a partition, few in sequence however long the context), and
 // their states meet in shared memory.  A partition in which a row attends
-// nothing (l == 0) left no accumulator.
+// nothing (l == 0) left no accumulator.  `steps` column chunks a CTA: all of them
+// when there are rows enough for every SM (a CTA of a single-partition sequence
+// only reads its length and leaves, and 8192 such cost 20 us), one when few.
 constexpr int kTreeMergeThreads = 256;
 constexpr int kTreeMergeWarps = kTreeMergeThreads / 32;
 constexpr int kTreeMergeCols = 16;  // columns of a lane
@@ -174,7 +176,7 @@ __host__ __device__ inline int tree_merge_log_rows(int rows, int D) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_merge_kernel(const TreeParams p, int steps) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int E = kTreeMergeCols;
@@ -186,10 +188,10 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_merge_kernel(con
     const int lrb = tree_merge_log_rows(rows, D);
     const int RB = 1 << lrb, CB = 32 >> lrb;  // rows, and columns a step
     const int chunks = (rows + RB - 1) >> lrb;
-    const int col_chunks = D / (E * CB);
+    const int col_groups = D / (E * CB * steps);
     long long f = blockIdx.x;
-    const int col0 = static_cast<int>(f % col_chunks) * (E * CB);
-    f /= col_chunks;
+    const int group0 = static_cast<int>(f % col_groups) * (E * CB * steps);
+    f /= col_groups;
     const int r0 = static_cast<int>(f % chunks) << lrb;
     const long long seq_head = f / chunks;
     const int s = static_cast<int>(seq_head / p.num_kv_heads);
@@ -198,60 +200,64 @@ __global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_merge_kernel(con
     const SeqSpan sp = seq_span(ld_nc_i32(p.context_lens + s), p.max_len, 0, p.block_size, p.bpp);
     if (sp.nparts <= 1)
         return;
-    float M = -INFINITY, den = 0.f, num[E];
+    for (int step = 0; step < steps; ++step) {
+        const int col0 = group0 + step * (E * CB);
+        float M = -INFINITY, den = 0.f, num[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        num[e] = 0.f;
-    if (r < rows) {
-        const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + seq_head * p.max_parts * rows + r;
-        const float *a = p.part_acc + (seq_head * p.max_parts * D + col0 + (lane >> lrb)) * rows + r;
-        for (int q = warp; q < sp.nparts; q += kTreeMergeWarps) {
-            const float2 v = ml[static_cast<long long>(q) * rows];
-            const float *aq = a + static_cast<long long>(q) * D * rows;
-            float x[E];
+        for (int e = 0; e < E; ++e)
+            num[e] = 0.f;
+        if (r < rows) {
+            const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + seq_head * p.max_parts * rows + r;
+            const float *a = p.part_acc + (seq_head * p.max_parts * D + col0 + (lane >> lrb)) * rows + r;
+            for (int q = warp; q < sp.nparts; q += kTreeMergeWarps) {
+                const float2 v = ml[static_cast<long long>(q) * rows];
+                const float *aq = a + static_cast<long long>(q) * D * rows;
+                float x[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = aq[static_cast<long long>(e * CB) * rows];
-            if (v.y == 0.f)
-                continue;
-            const float mn = fmaxf(M, v.x);
-            const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
-            den = den * keep + v.y * add;
+                for (int e = 0; e < E; ++e)
+                    x[e] = aq[static_cast<long long>(e * CB) * rows];
+                if (v.y == 0.f)
+                    continue;
+                const float mn = fmaxf(M, v.x);
+                const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
+                den = den * keep + v.y * add;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                num[e] = num[e] * keep + x[e] * add;
-            M = mn;
-        }
-    }
-    state[warp][lane] = make_float2(M, den);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        acc[warp][e][lane] = num[e];
-    __syncthreads();
-    // output o of the CTA: row o / (E CB), column o % (E CB)
-    for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
-        const int rr = o / (E * CB), c = o - rr * (E * CB);
-        if (r0 + rr >= rows)
-            break;
-        const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kTreeMergeWarps; ++w)
-            if (state[w][ln].y != 0.f)
-                m = fmaxf(m, state[w][ln].x);
-        float n = 0.f, d = 0.f;
-#pragma unroll
-        for (int w = 0; w < kTreeMergeWarps; ++w) {
-            const float2 v = state[w][ln];
-            if (v.y != 0.f) {
-                const float sc = v.x == m ? 1.f : exp2f(v.x - m);
-                d = fmaf(v.y, sc, d);
-                n = fmaf(acc[w][e][ln], sc, n);
+                for (int e = 0; e < E; ++e)
+                    num[e] = num[e] * keep + x[e] * add;
+                M = mn;
             }
         }
-        const int i = (r0 + rr) / G, h = kvh * G + (r0 + rr) % G;
-        const long long orow = (static_cast<long long>(s) * p.num_draft + i) * p.num_heads + h;
-        store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+        state[warp][lane] = make_float2(M, den);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[warp][e][lane] = num[e];
+        __syncthreads();
+        // output o of the CTA: row o / (E CB), column o % (E CB)
+        for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
+            const int rr = o / (E * CB), c = o - rr * (E * CB);
+            if (r0 + rr >= rows)
+                break;
+            const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kTreeMergeWarps; ++w)
+                if (state[w][ln].y != 0.f)
+                    m = fmaxf(m, state[w][ln].x);
+            float n = 0.f, d = 0.f;
+#pragma unroll
+            for (int w = 0; w < kTreeMergeWarps; ++w) {
+                const float2 v = state[w][ln];
+                if (v.y != 0.f) {
+                    const float sc = v.x == m ? 1.f : exp2f(v.x - m);
+                    d = fmaf(v.y, sc, d);
+                    n = fmaf(acc[w][e][ln], sc, n);
+                }
+            }
+            const int i = (r0 + rr) / G, h = kvh * G + (r0 + rr) % G;
+            const long long orow = (static_cast<long long>(s) * p.num_draft + i) * p.num_heads + h;
+            store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+        }
+        __syncthreads();
     }
 }
 
