@@ -13,13 +13,14 @@
 // the exponents (weights up to 2^8, fp32 sums), which changes nothing in the
 // quotient.
 //
-// Work inside an item goes by sub-units of 64 tokens, n = 0, 1, 2, ...:
-// sub-unit n belongs to softmax warpgroup n % 2 and S / P buffer n % 4 (64
-// columns each), so each warpgroup has two buffers: S of its next sub-unit is
-// made while it works on this one, and P V of the last one runs beside both.
 // With at most 128 rows (Units = 1) warpgroup w takes tokens 64 w .. 64 w + 63
-// of every tile, with its own running state and O, merged once per item; with
-// more (Units = 2) each takes one of two row tiles and all tokens.
+// of every tile, with its own running state and O, merged once per item; it has
+// two S buffers of 64 columns, so that the next S is made while it works.  With
+// more rows (Units = 2) each warpgroup takes one of two row tiles and all 128
+// tokens of a tile: one S of 128 columns each fills tensor memory (an S of 64
+// tokens would cost three quarters of one of 128, as it rereads Q, and the
+// tensor cores are the scarce part there).  P overwrites S, and goes to its
+// product in halves of 64 tokens.
 
 // P's rounding (Parts): a 16-bit output takes P rounded once to the type of V
 // (the output is rounded as coarsely); an fp32 output takes hi + lo parts
@@ -193,6 +194,20 @@ template <> __device__ inline void unpack2<__half>(uint32_t w, float &lo, float 
     const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
     lo = f.x, hi = f.y;
 }
+// Whether a phase has completed, without waiting (try_wait may suspend the
+// thread for a while when it has not).
+__device__ inline bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // Two fp32 operations of one instruction.
 __device__ inline float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -398,16 +413,24 @@ __device__ inline void tc_vproducer(const TreeParams &p, const CUtensorMap *tmv,
 // warp runs up to four sub-units ahead of the P V warp (across items too); one
 // warp issuing both took about 1000 cycles a sub-unit in waits and issue alone.
 
-// S = Q . K^T of every sub-unit, and the item's query rows: row tile(s) of 128
+// S / P buffer of warpgroup w for tile t, and the phase of that use: Units = 1
+// has two a warpgroup (2 (t & 1) + w), Units = 2 one (w).
+template <int Units> __device__ inline uint32_t tc_buf(uint32_t t, uint32_t w) {
+    return Units == 2 ? w : 2 * (t & 1u) + w;
+}
+template <int Units> __device__ inline uint32_t tc_phase(uint32_t t) { return (Units == 2 ? t : t >> 1) & 1u; }
+// First column of a buffer: a warpgroup's are adjacent.
+__device__ inline uint32_t tc_buf_col(uint32_t b) { return (b & 1u) * 128 + (b >> 1) * 64; }
+
+// S = Q . K^T of every tile, and the item's query rows: row tile(s) of 128
 // rows = 128 / G drafted tokens x G heads; rows past the last drafted token of
 // the batch read zeros, rows of the next sequence are computed and never stored.
 template <typename T, int D, int Units>
 __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
-    constexpr uint32_t kPerTile = 2 * Units;  // sub-units of a tile
     // a negative scale is the sign of Q (bit 13: A negated), so the softmax
     // takes maxima of raw scores
-    const uint32_t id_qk = idesc_f16<T>(128, 64, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
+    const uint32_t id_qk = idesc_f16<T>(128, Units == 2 ? 128 : 64, 0, 0) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t kHalf = 8 * C::kGroup >> 4;  // 64 tokens of a tile, in descriptor units
     const uint32_t lead = elect_lane();
     const bool lane0 = (threadIdx.x & 31) == 0;
@@ -419,7 +442,7 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
     const int G = p.num_heads / p.num_kv_heads;
     if (lane0)
         prefetch_tensormap(tmq);
-    uint32_t x = 0;             // sub-units so far
+    uint32_t t = 0;             // tiles so far
     uint32_t ke = 0;            // items with tiles
     uint32_t kst = 0, kph = 0;  // K stage, phase of its use
     for (uint32_t k = 0;; ++k) {
@@ -455,21 +478,22 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
             if (!mbar_wait_bounded(&M->kfull[kst], kph))
                 return false;
 #pragma unroll
-            for (uint32_t e = 0; e < kPerTile; ++e, ++x) {
-                const uint32_t b = x & 3u;
-                // S shares its columns with the P of the buffer's last use
-                if (x >= 4 && !mbar_wait_bounded(&M->pvdone[b], ((x >> 2) - 1) & 1u))
+            for (uint32_t e = 0; e < 2; ++e) {
+                // S shares its columns with the P of their last use: two tiles ago (Units = 1), or one
+                const uint32_t b = tc_buf<Units>(t, e);
+                if (t >= (Units == 2 ? 1 : 2) && !mbar_wait_bounded(&M->pvdone[b], tc_phase<Units>(t) ^ 1u))
                     return false;
                 tc_fence_after();
-                const uint64_t qd = q_desc + (Units == 2 ? (e & 1u) * (C::kQ >> 4) : 0u);
-                const uint64_t kd = k_desc + kst * (C::kTile >> 4) + (Units == 2 ? e >> 1 : e) * kHalf;
-                const uint32_t d = tmem + b * 64;
+                const uint64_t qd = q_desc + (Units == 2 ? e * (C::kQ >> 4) : 0u);
+                const uint64_t kd = k_desc + kst * (C::kTile >> 4) + (Units == 2 ? 0u : e * kHalf);
+                const uint32_t d = tmem + tc_buf_col(b);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     tc_mma_ss(lead, d, qd + ((kk >> 2) * (128 * 128 >> 4) + (kk & 3) * 2),
                               kd + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2), id_qk, kk > 0);
                 tc_commit_lead(lead, &M->sfull[b]);
             }
+            ++t;
             tc_commit_lead(lead, &M->kempty[kst]);
             if (ti == ntiles - 1)
                 tc_commit_lead(lead, &M->qempty);
@@ -480,11 +504,10 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
     }
 }
 
-// O += P . V of every sub-unit.
+// O += P . V of every tile, 64 tokens at a time.
 template <typename T, int D, int Parts, int Units>
 __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
-    constexpr uint32_t kPerTile = 2 * Units;
     constexpr uint32_t kIdPV = idesc_f16<T>(128, D, 0, 1);
     constexpr uint32_t kHalf = 8 * C::kGroup >> 4;
     const uint32_t lead = elect_lane();
@@ -492,7 +515,7 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
     // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
     const uint64_t v_desc = sdesc(smem + C::kOffV, 1024, C::kGroup);
     const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
-    uint32_t x = 0, ke = 0, vst = 0, vph = 0;
+    uint32_t t = 0, ke = 0, vst = 0, vph = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
@@ -506,11 +529,15 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
         const int ntiles = (nb + (1 << lbpt) - 1) >> lbpt;
         if (ntiles == 0)
             continue;
-        for (int ti = 0; ti < ntiles; ++ti) {
+        for (int ti = 0; ti < ntiles; ++ti, ++t) {
+            // Units = 1: tokens 64 w of the tile, from warpgroup w; Units = 2: both halves
+            // of row tile 0, then of row tile 1 (the warpgroups settle half a tile apart,
+            // one's exponentials beside the other's products)
 #pragma unroll
-            for (uint32_t e = 0; e < kPerTile; ++e, ++x) {
-                const uint32_t b = x & 3u, w = e & 1u;
-                if (!mbar_wait_bounded(&M->pfull[b], (x >> 2) & 1u))
+            for (uint32_t e = 0; e < 2 * Units; ++e) {
+                const uint32_t w = Units == 2 ? e >> 1 : e, half = e & 1u;
+                const uint32_t b = tc_buf<Units>(t, w);
+                if (!mbar_wait_bounded(&M->pfull[Units == 2 ? 2 * half + w : b], tc_phase<Units>(t)))
                     return false;
                 // O is free once the item before has been written out
                 if (e == 0 && ti == 0 && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
@@ -518,16 +545,19 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
                 if (e == 0 && !mbar_wait_bounded(&M->vfull[vst], vph))
                     return false;
                 tc_fence_after();
-                const int keep = ti == 0 && e < 2 ? *reinterpret_cast<volatile int *>(&M->oinit[w]) : 1;
-                const uint64_t vd = v_desc + vst * (C::kTile >> 4) + (Units == 2 ? e >> 1 : e) * kHalf;
-                const uint32_t o = tmem + 256 + w * D, pt = tmem + b * 64;
+                const int keep =
+                    ti == 0 && (Units == 1 || half == 0) ? *reinterpret_cast<volatile int *>(&M->oinit[w]) : 1;
+                const uint64_t vd = v_desc + vst * (C::kTile >> 4) + half * kHalf;
+                const uint32_t o = tmem + 256 + w * D;
+                const uint32_t pt = tmem + tc_buf_col(b) + (Units == 2 ? half * 64 : 0u);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                     for (int part = 0; part < Parts; ++part)
                         tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
                                   vd + kk * (2 * C::kGroup >> 4), kIdPV, (kk | part) ? 1 : keep);
-                tc_commit_lead(lead, &M->pvdone[b]);
+                if (Units == 1 || half == 1)
+                    tc_commit_lead(lead, &M->pvdone[b]);
             }
             tc_commit_lead(lead, &M->vempty[vst]);
             if (++vst == C::kSV)
@@ -595,12 +625,24 @@ __device__ inline void store_cols32(void *out, int dtype, long long idx, const f
     }
 }
 
-__device__ inline float max32(const float *v) {
-    float a = fmaxf(v[0], v[1]), b = fmaxf(v[2], v[3]);
+template <int N> __device__ inline float max_of(const float *v) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int e = 4; e < 32; e += 4)
-        a = fmaxf(fmaxf(a, v[e]), v[e + 1]), b = fmaxf(fmaxf(b, v[e + 2]), v[e + 3]);
-    return fmaxf(a, b);
+    for (int e = 4; e + 8 <= N; e += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            m[c] = fmaxf(fmaxf(m[c], v[e + c]), v[e + 4 + c]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        m[c] = fmaxf(m[c], v[N - 4 + c]);
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Whether token u of the warpgroup's share of a tile has a non-finite V row:
+// word q holds the votes of the warpgroup's warp q (Units = 1: two threads a token).
+template <int Units> __device__ inline bool tc_poison(const uint32_t *votes, int u) {
+    const uint32_t w = Units == 2 ? votes[u >> 5] : votes[u >> 5] | votes[2 + (u >> 5)];
+    return (w >> (u & 31)) & 1u;
 }
 
 // The weights 2^(s sc - me) of 32 scores of this thread's row: summed, and as
@@ -630,10 +672,11 @@ __device__ inline void weights32(const float *s, float sc, float me, uint32_t ad
 template <typename T, int D, int Parts, int Units>
 __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
+    constexpr int kTok = 64 * Units;  // tokens of a tile that a warpgroup takes
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wg = (warp >> 2) - 1;
     const int quarter = warp & 3;
-    const int row = quarter * 32 + lane;  // row of the 128, and token of a tile
+    const int row = quarter * 32 + lane;  // row of the 128
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t o_addr = tmem + lanes + 256 + wg * D;
     const int bs = p.block_size, bpt = 128 / bs;
@@ -643,12 +686,12 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
     // (a scale of 0 as one too small to matter: a masked -inf times 0 would be NaN)
     const float sc = fmaxf(fabsf(p.scale_log2), 1e-30f);
     uint64_t *pzbar = Units == 1 ? &M->pz[wg] : &M->pz[0];
-    // V rows of a sub-unit: two threads a token
-    const int tk = row & 63, vpart = row >> 6;
-    constexpr int kVChunks = C::kHalves == 2 ? 8 : 4;  // 16-byte chunks of a thread's part of a V row
-    const int vchunk0 = C::kHalves == 2 ? 0 : vpart * 4;
-    const uint32_t sub_bpt = static_cast<uint32_t>(bpt) >> 1, sub_full = (1u << sub_bpt) - 1u;
-    uint32_t cnt = 0;  // sub-units of this warpgroup: its cnt-th is sub-unit 2 cnt + wg
+    // V rows of the warpgroup's tokens: 128 / kTok threads a token, each with its
+    // share of the row's 16-byte chunks
+    const int tk = row & (kTok - 1), vpart = row / kTok;
+    constexpr int kShare = C::kHalves * 8 * kTok / 128;  // chunks of a thread: 16, 8 or 4
+    const uint32_t sub_bpt = static_cast<uint32_t>(bpt) / (128 / kTok), sub_full = (1u << sub_bpt) - 1u;
+    uint32_t t = 0;  // tiles so far
     uint32_t pzc = 0, ke = 0;
 
     auto arrive_wait = [&](uint64_t *bar, uint32_t phase) -> bool {
@@ -678,48 +721,59 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             (static_cast<long long>(it.s) * p.num_draft + i) * p.num_heads + it.kvh * G + (r & (G - 1));
         float m = -INFINITY, l = 0.f;
         bool first = true;
-        // the scores of the sub-unit at hand, and their maximum; `ready`: loaded
-        // during the one before (interior sub-units only: nothing masked)
-        float sv[64], top = -INFINITY;
+        // the scores at hand, and their maximum; `ready`: loaded during the tile
+        // before (Units = 1, interior tiles: nothing masked)
+        float sv[kTok], top = -INFINITY;
         bool ready = false;
-        const int subs = ntiles * Units;
-        for (int su = 0; su < subs; ++su, ++cnt) {
-            const int ti = Units == 2 ? su >> 1 : su, half = Units == 2 ? su & 1 : wg;
-            const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
-            const uint32_t buf = (2 * cnt + wg) & 3u;
-            const uint32_t s_addr = tmem + lanes + buf * 64;
+        for (int ti = 0; ti < ntiles; ++ti, ++t) {
+            const int half = Units == 2 ? 0 : wg;
+            const uint32_t buf = tc_buf<Units>(t, wg);
+            const uint32_t s_addr = tmem + lanes + tc_buf_col(buf);
             const int tok0 = (it.blk_lo << lbs) + ti * 128 + half * 64;
-            uint64_t allow = ~0ull;
-            bool masked = false, poisoned = false, drop = false;  // drop: this thread's V row must not be multiplied
-            const int vstage = static_cast<int>(t % C::kSV);
-            const char *vhalf = smem + C::kOffV + vstage * C::kTile + half * (8 * C::kGroup);
-            char *vrow = const_cast<char *>(vhalf) + (tk >> 3) * C::kGroup + (tk & 7) * 128 +
-                         (C::kHalves == 2 ? vpart * 1024 : 0);
+            uint64_t allow[Units];
+            bool masked = false, poisoned = false;
             if (!ready) {
-                const bool drafts = it.drafted > 0 && tok0 + 64 > it.committed && tok0 < it.len;
-                if (tok0 + 64 > it.committed)  // (the mask's round trip overlaps the wait for S)
-                    allow = tree_bits64(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0, tok0);
-                if (!mbar_wait_bounded(&M->sfull[buf], (cnt >> 1) & 1u))
+                const bool drafts = it.drafted > 0 && tok0 + kTok > it.committed && tok0 < it.len;
+#pragma unroll
+                for (int u = 0; u < Units; ++u) {
+                    allow[u] = ~0ull;
+                    if (tok0 + kTok > it.committed)  // (the mask's round trip overlaps the wait for S)
+                        allow[u] = tree_bits64(p, it.s, it.committed, live ? it.drafted : 0, live ? i : 0,
+                                               tok0 + 64 * u);
+                }
+                if (!mbar_wait_bounded(&M->sfull[buf], tc_phase<Units>(t)))
                     return false;
                 tc_fence_after();
                 if (warp_live) {
-                    tmem_ld<32>(s_addr, sv);
-                    tmem_ld<32>(s_addr + 32, sv + 32);
+#pragma unroll
+                    for (int c = 0; c < kTok; c += 32)
+                        tmem_ld<32>(s_addr + c, sv + c);
                 }
-                // the sub-unit's blocks, bit e: block e of it
+                // the tokens' blocks, bit e: block e of them
                 const uint32_t blocks = (M->meta[t % kTcMeta] >> (half * sub_bpt)) & sub_full;
                 const bool whole = blocks == sub_full;
-                masked = !whole || tok0 + 64 > it.committed;
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)  // 8-token pieces
-                        if (!((blocks >> ((8 * e) >> lbs)) & 1u))
-                            allow &= ~(0xffull << (8 * e));
-                }
+                masked = !whole || tok0 + kTok > it.committed;
                 if (masked) {
+                    const int vstage = static_cast<int>(t % C::kSV);
+                    const char *vhalf = smem + C::kOffV + vstage * C::kTile + half * (8 * C::kGroup);
+                    char *vrow = const_cast<char *>(vhalf) + (tk >> 3) * C::kGroup + (tk & 7) * 128;
+                    // chunk c of this thread's share, in an order rotated by the row (the lanes of an access then
+                    // cover all banks)
+                    auto chunk = [&](int c) -> char * {
+                        const int at = vpart * kShare + ((c + tk) & (kShare - 1));
+                        return vrow + (at >> 3) * 1024 + (at & 7) * 16;
+                    };
+                    if (!whole) {
+#pragma unroll
+                        for (int u = 0; u < Units; ++u)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)  // 8-token pieces
+                                if (!((blocks >> ((64 * u + 8 * e) >> lbs)) & 1u))
+                                    allow[u] &= ~(0xffull << (8 * e));
+                    }
                     const int tok = tok0 + tk;
                     const bool valid = ((blocks >> (tk >> lbs)) & 1u) && tok < it.len;
-                    drop = !valid;
+                    bool drop = !valid;  // this token's V row must not be multiplied
                     if (__any_sync(0xffffffffu, drop) || drafts)
                         if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
                             return false;
@@ -727,8 +781,8 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                         bool bad = false;
                         if (valid && tok >= it.committed) {
 #pragma unroll
-                            for (int c = 0; c < kVChunks; ++c) {
-                                const uint4 x = ld_shared_v4(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16);
+                            for (int c = 0; c < kShare; ++c) {
+                                const uint4 x = ld_shared_v4(chunk(c));
                                 bad = bad || non_finite2<T>(x.x) || non_finite2<T>(x.y) || non_finite2<T>(x.z) ||
                                       non_finite2<T>(x.w);
                             }
@@ -740,19 +794,81 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                             return false;
                         poisoned =
                             (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
-                        drop = drop || (((M->poison[wg][tk >> 5] | M->poison[wg][2 + (tk >> 5)]) >> (tk & 31)) & 1u);
+                        drop = drop || tc_poison<Units>(M->poison[wg], tk);
                     }
-                }
-                if (warp_live) {
-                    tmem_wait_ld();
-                    if (masked) {
+                    if (warp_live) {
+                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            sv[e] = (allow >> e) & 1u ? sv[e] : -INFINITY;
+                        for (int e = 0; e < kTok; ++e)
+                            sv[e] = (allow[e >> 6] >> (e & 63)) & 1u ? sv[e] : -INFINITY;
+                        top = max_of<kTok>(sv);
                     }
-                    top = fmaxf(max32(sv), max32(sv + 32));
+                    if (poisoned) {
+                        // drafted tokens with non-finite V: added to the rows that attend them, before
+                        // their V rows are zeroed; the row's maximum in use, and O's scale, are settled first
+                        if (!first && !mbar_wait_bounded(&M->pvdone[tc_buf<Units>(t - 1, wg)], tc_phase<Units>(t - 1)))
+                            return false;
+                        tc_fence_after();
+                        if (warp_live) {
+                            const float mx = fmaxf(m, top == -INFINITY ? -INFINITY : top * sc);
+                            const float mn = first || mx > m + kTcLazy ? mx : m;  // (as below)
+                            const float alpha = first || (m == -INFINITY && mn != m) ? 0.f : fast_exp2(m - mn);
+                            const float me = mn == -INFINITY ? 0.f : mn;
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tmem_ld<16>(o_addr + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = !first && mn == m ? o[e] : (alpha == 0.f ? 0.f : o[e] * alpha);
+                                for (int u = 0; u < kTok; ++u) {
+                                    if (!tc_poison<Units>(M->poison[wg], u))
+                                        continue;
+                                    float x[2];
+                                    tmem_ld<2>(s_addr + (u & ~1), x);
+                                    tmem_wait_ld();
+                                    const float sx = u & 1 ? x[1] : x[0];
+                                    if (((Units == 2 && u >= 64 ? allow[Units - 1] : allow[0]) >> (u & 63)) & 1u) {
+                                        const float pw = fast_exp2(fmaf(sx, sc, -me));
+                                        const char *vr = vhalf + (u >> 3) * C::kGroup + (u & 7) * 128 + (c >> 6) * 1024;
+#pragma unroll
+                                        for (int e = 0; e < 16; e += 2) {
+                                            const int ch = ((c & 63) + e) >> 3;  // 16-byte chunk, swizzled by the row
+                                            float v0, v1;
+                                            unpack2<T>(ld_shared_u32(vr + ((ch ^ (u & 7)) << 4) + (e & 7) * 2), v0, v1);
+                                            o[e] = fmaf(pw, v0, o[e]);
+                                            o[e + 1] = fmaf(pw, v1, o[e + 1]);
+                                        }
+                                    }
+                                }
+                                __syncwarp();
+                                uint32_t w[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    w[e] = __float_as_uint(o[e]);
+                                tmem_st16(o_addr + c, w);
+                            }
+                            l *= mn == m ? 1.f : alpha;
+                            m = mn;
+                            tmem_wait_st();
+                        }
+                        if (!arrive_wait(pzbar, pzc++))  // every row has read the V rows that are zeroed now
+                            return false;
+                    }
+                    if (drop) {
+#pragma unroll
+                        for (int c = 0; c < kShare; ++c)
+                            *reinterpret_cast<uint4 *>(chunk(c)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                } else if (warp_live) {
+                    tmem_wait_ld();
+                    top = max_of<kTok>(sv);
                 }
             }
+            if (first && quarter == 0 && lane == 0)
+                M->oinit[wg] = poisoned ? 1 : 0;
+            ready = false;
             if (warp_live) {
                 // the row's maximum (raw scores; sc >= 0)
                 const float mt = top == -INFINITY ? -INFINITY : top * sc;
@@ -762,12 +878,9 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 const bool grow = first ? false : mn > m + kTcLazy;
                 if (__any_sync(0xffffffffu, grow)) {
                     // every product into this O so far is done once the last one is
-                    if (cnt > 0) {
-                        const uint32_t last = (2 * (cnt - 1) + wg) & 3u;
-                        if (!mbar_wait_bounded(&M->pvdone[last], ((cnt - 1) >> 1) & 1u))
-                            return false;
-                        tc_fence_after();
-                    }
+                    if (!mbar_wait_bounded(&M->pvdone[tc_buf<Units>(t - 1, wg)], tc_phase<Units>(t - 1)))
+                        return false;
+                    tc_fence_after();
                     const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -785,98 +898,47 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 }
                 if (first || grow)
                     m = mn;
-            }
-            const float me = m == -INFINITY ? 0.f : m;
-            if (poisoned) {
-                // drafted tokens with non-finite V: added here to the rows that attend them
-                if (warp_live) {
-                    if (!first) {
-                        const uint32_t last = (2 * (cnt - 1) + wg) & 3u;
-                        if (!mbar_wait_bounded(&M->pvdone[last], ((cnt - 1) >> 1) & 1u))
-                            return false;
-                        tc_fence_after();
-                    }
-                    for (int c = 0; c < D; c += 16) {
-                        float o[16];
-                        if (first) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                o[e] = 0.f;
-                        } else {
-                            tmem_ld<16>(o_addr + c, o);
-                            tmem_wait_ld();
-                        }
-                        for (int u = 0; u < 64; ++u) {
-                            if (!(((M->poison[wg][u >> 5] | M->poison[wg][2 + (u >> 5)]) >> (u & 31)) & 1u))
-                                continue;
-                            float x[2];
-                            tmem_ld<2>(s_addr + (u & ~1), x);
-                            tmem_wait_ld();
-                            const float sx = u & 1 ? x[1] : x[0];
-                            if ((allow >> u) & 1u) {
-                                const float pw = fast_exp2(fmaf(sx, sc, -me));
-                                const char *vr = vhalf + (u >> 3) * C::kGroup + (u & 7) * 128 + (c >> 6) * 1024;
-#pragma unroll
-                                for (int e = 0; e < 16; e += 2) {
-                                    const int ch = ((c & 63) + e) >> 3;  // 16-byte chunk, swizzled by the row
-                                    float v0, v1;
-                                    unpack2<T>(ld_shared_u32(vr + ((ch ^ (u & 7)) << 4) + (e & 7) * 2), v0, v1);
-                                    o[e] = fmaf(pw, v0, o[e]);
-                                    o[e + 1] = fmaf(pw, v1, o[e + 1]);
-                                }
-                            }
-                        }
-                        __syncwarp();
-                        uint32_t w[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            w[e] = __float_as_uint(o[e]);
-                        tmem_st16(o_addr + c, w);
-                    }
-                    tmem_wait_st();
-                }
-                if (!arrive_wait(pzbar, pzc++))  // every row has read the V rows that are zeroed now
-                    return false;
-            }
-            if (first && quarter == 0 && lane == 0)
-                M->oinit[wg] = poisoned ? 1 : 0;
-            ready = false;
-            if (warp_live) {
+                const float me = m == -INFINITY ? 0.f : m;
                 // (a masked score is -inf: its weight is exactly 0)
                 float2 l2 = make_float2(0.f, 0.f);
                 weights32<T, Parts>(sv, sc, me, s_addr, l2);
-                // the next sub-unit's scores replace this one's as they are used up,
-                // when its S is there and nothing of it is masked
-                const int nti = Units == 2 ? (su + 1) >> 1 : su + 1, nhalf = Units == 2 ? (su + 1) & 1 : wg;
-                const uint32_t nbuf = (buf + 2) & 3u;
-                if (su + 1 < subs && (it.blk_lo << lbs) + nti * 128 + nhalf * 64 + 64 <= it.committed)
-                    ready = __all_sync(0xffffffffu, mbar_try_wait(&M->sfull[nbuf], ((cnt + 1) >> 1) & 1u)) &&
-                            ((M->meta[(it.t_first + nti) % kTcMeta] >> (nhalf * sub_bpt)) & sub_full) == sub_full;
-                if (ready) {
-                    tc_fence_after();
-                    tmem_ld<32>(tmem + lanes + nbuf * 64, sv);
+                if constexpr (Units == 2) {
+                    weights32<T, Parts>(sv + 32, sc, me, s_addr + 32, l2);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&M->pfull[wg]);  // the first half
+                    weights32<T, Parts>(sv + 64, sc, me, s_addr + 64, l2);
+                    weights32<T, Parts>(sv + 96, sc, me, s_addr + 96, l2);
+                } else {
+                    // the next tile's scores replace this one's as they are used up, when its
+                    // S is there and nothing of it is masked
+                    const uint32_t nbuf = tc_buf<Units>(t + 1, wg);
+                    const uint32_t n_addr = tmem + lanes + tc_buf_col(nbuf);
+                    if (ti + 1 < ntiles && tok0 + 128 + kTok <= it.committed)
+                        ready = __all_sync(0xffffffffu, mbar_test_wait(&M->sfull[nbuf], tc_phase<Units>(t + 1))) &&
+                                ((M->meta[(t + 1) % kTcMeta] >> (half * sub_bpt)) & sub_full) == sub_full;
+                    if (ready) {
+                        tc_fence_after();
+                        tmem_ld<32>(n_addr, sv);
+                    }
+                    weights32<T, Parts>(sv + 32, sc, me, s_addr + 32, l2);
+                    if (ready) {
+                        tmem_ld<32>(n_addr + 32, sv + 32);
+                        tmem_wait_ld();
+                        top = max_of<kTok>(sv);
+                    }
                 }
-                weights32<T, Parts>(sv + 32, sc, me, s_addr + 32, l2);
                 l += l2.x + l2.y;
-                if (ready) {
-                    tmem_ld<32>(tmem + lanes + nbuf * 64 + 32, sv + 32);
-                    tmem_wait_ld();
-                    top = fmaxf(max32(sv), max32(sv + 32));
-                }
                 tmem_wait_st();
+            } else if (Units == 2 && lane == 0) {
+                mbar_arrive(&M->pfull[wg]);
             }
-            if (drop) {
-#pragma unroll
-                for (int c = 0; c < kVChunks; ++c)
-                    *reinterpret_cast<uint4 *>(vrow + (vchunk0 + ((c + tk) & (kVChunks - 1))) * 16) =
-                        make_uint4(0, 0, 0, 0);
-            }
-            if (masked)
-                fence_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&M->pfull[buf]);
+                mbar_arrive(&M->pfull[Units == 2 ? 2 + wg : buf]);
             first = false;
         }
         // ---- the item's output: final rows, or a partial per row
@@ -1017,10 +1079,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
-    // registers: 384 x 168 = 128 x 104 + 256 x 200
+    // registers: 384 x 168 = 128 x 72 + 256 x 216
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             tc_kproducer<D, Units>(p, &tmk, smem, M);
         } else if (warp == 1) {
@@ -1041,7 +1103,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
