@@ -461,10 +461,15 @@ PA_API pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, co
  *                 from draft_lens[s] on are ignored); NULL: token j <= i, the
  *                 drafted tokens are a chain
  *   num_draft     1 .. 256
- *   partition_size  as pa_decode; 0 = chosen from the batch size and
- *                 max_blocks_per_seq so that every SM has work
  *   workspace     pa_decode_tree_workspace_size() bytes, 16-byte aligned
  *                 (may be NULL when that size is 0)
+ * There is no partition size: fp16 / bf16 caches go through a tensor-core
+ * kernel that splits the whole batch's contexts evenly over the SMs, fp32
+ * caches in 256-token partitions.  The same inputs give the same bits on every
+ * call (a sequence decoded in another batch may differ in the last bits, where
+ * its context is cut elsewhere).  fp16 / bf16 out: the softmax weights are
+ * rounded once to the cache's type before the product with V, like the output
+ * itself; fp32 out: they are carried in two parts.
  * A drafted token that some query does not attend has no influence on it,
  * whatever its K and V hold (infinities and NaN too).  Other arguments and
  * limits as pa_decode (window 0).
@@ -473,14 +478,14 @@ PA_API pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, c
                                 const int32_t *block_tables, const int32_t *context_lens, const int32_t *draft_lens,
                                 const uint64_t *tree_mask, int num_seqs, int num_draft, int num_heads,
                                 int num_kv_heads, int head_dim, int block_size, float scale, pa_dtype dtype,
-                                pa_dtype out_dtype, int max_blocks_per_seq, int num_blocks, int partition_size,
-                                void *workspace, size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
+                                pa_dtype out_dtype, int max_blocks_per_seq, int num_blocks, void *workspace,
+                                size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
 
-/* Bytes of workspace pa_decode_tree needs (0 when no sequence can span more
- * than one partition, and for bad arguments). */
+/* Bytes of workspace pa_decode_tree needs (0 when no context can be cut, and
+ * for bad arguments). */
 PA_API size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num_heads, int num_kv_heads,
                                             int head_dim, int block_size, int max_blocks_per_seq,
-                                            int partition_size);
+                                            pa_dtype dtype);
 
 /*
  * pa_decode that also accumulates how much attention each cached token gets,

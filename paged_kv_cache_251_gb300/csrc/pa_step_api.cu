@@ -95,34 +95,35 @@ void fill_decode(DecodeParams &p, void *out, const void *q, const void *k_cache,
 }
 
 constexpr int kMaxDraft = 256;
-// The default partition of the tree attention: the context split so that the
-// batch gives about two items to each of kTreeSms SMs, in partitions of 256 to
-// 1024 tokens.
-constexpr int kTreeSms = 152;
-constexpr int kTreeMinPartition = 256, kTreeMaxPartition = 1024;
+// The general tree kernel splits contexts into partitions of this many tokens.
+constexpr int kTreePartition = 256;
 
+// The partitions of the general kernel, and the workspace of the kernel that
+// takes the call (`pool`: num_blocks; the workspace size is for pools of up to
+// 2^31 (block, kv head) tiles, which the tensor-core kernel addresses).
 pa_status plan_tree(int num_seqs, int num_draft, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                    int max_blocks_per_seq, int partition_size, DecodePlan *plan) {
+                    int max_blocks_per_seq, int dtype, int pool, DecodePlan *plan) {
     if (num_draft < 1 || num_draft > kMaxDraft)
         return fail(PA_ERR_INVALID_ARGUMENT, "num_draft must be 1 .. 256");
     if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads != 0)
         return fail(PA_ERR_INVALID_ARGUMENT, "num_heads must be a positive multiple of num_kv_heads");
-    if (partition_size == 0 && block_size_ok(block_size) && num_seqs > 0 && max_blocks_per_seq > 0) {
-        const long long rows = static_cast<long long>(num_draft) * (num_heads / num_kv_heads);
-        const long long items = static_cast<long long>(num_seqs) * num_kv_heads * ((rows + 127) / 128);
-        const long long parts = (2 * kTreeSms + items - 1) / items;
-        long long tokens = (static_cast<long long>(max_blocks_per_seq) * block_size + parts - 1) / parts;
-        tokens = tokens < kTreeMinPartition ? kTreeMinPartition : tokens;
-        tokens = tokens > kTreeMaxPartition ? kTreeMaxPartition : tokens;
-        partition_size = static_cast<int>((tokens + 127) / 128 * 128);
-    }
-    const pa_status st = plan_decode(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq, 0, partition_size,
+    if (!dtype_ok(dtype))
+        return fail(PA_ERR_INVALID_ARGUMENT, "unknown dtype");
+    const pa_status st = plan_decode(num_seqs, num_heads, head_dim, block_size, max_blocks_per_seq, 0, kTreePartition,
                                      plan);
-    if (st == PA_OK)
+    if (st != PA_OK)
+        return st;
+    if (tree_tensor_cores(dtype, pool, num_kv_heads)) {
+        const long long max_len = static_cast<long long>(max_blocks_per_seq) * block_size;
+        plan->workspace =
+            tree_tc_workspace(num_seqs, num_kv_heads, num_draft * (num_heads / num_kv_heads), head_dim,
+                              static_cast<int>(max_len < INT_MAX ? max_len : INT_MAX));
+    } else {
         plan->workspace = plan->max_parts > 1 ? static_cast<size_t>(num_seqs) * num_draft * num_heads *
                                                     plan->max_parts * (head_dim + 2) * sizeof(float)
                                               : 0;
-    return st;
+    }
+    return PA_OK;
 }
 
 // Sizes of the scored decode's workspace: partials, every row's (max,
@@ -288,10 +289,10 @@ pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, const voi
 }
 
 size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num_heads, int num_kv_heads, int head_dim,
-                                     int block_size, int max_blocks_per_seq, int partition_size) {
+                                     int block_size, int max_blocks_per_seq, pa_dtype dtype) {
     DecodePlan plan;
-    if (plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                  partition_size, &plan) != PA_OK)
+    if (plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, dtype, 1,
+                  &plan) != PA_OK)
         return 0;
     return plan.workspace;
 }
@@ -300,12 +301,12 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
                          const int32_t *block_tables, const int32_t *context_lens, const int32_t *draft_lens,
                          const uint64_t *tree_mask, int num_seqs, int num_draft, int num_heads, int num_kv_heads,
                          int head_dim, int block_size, float scale, pa_dtype dtype, pa_dtype out_dtype,
-                         int max_blocks_per_seq, int num_blocks, int partition_size, void *workspace,
-                         size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream) {
+                         int max_blocks_per_seq, int num_blocks, void *workspace, size_t workspace_bytes,
+                         uint32_t *err_word, pa_stream_t stream) {
     g_detail.clear();
     DecodePlan plan;
     pa_status st = plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                             partition_size, &plan);
+                             dtype, num_blocks, &plan);
     if (st != PA_OK)
         return st;
     if (num_seqs == 0)
@@ -331,9 +332,10 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
     p.num_draft = num_draft;
     p.words = (num_draft + 63) / 64;
     p.row_tiles = 0;
-    if (plan.max_parts > 1) {
+    if (plan.workspace > 0) {
+        // accumulators, then the (max, denominator) pairs: head_dim : 2 of the workspace
         p.part_acc = static_cast<float *>(workspace);
-        p.part_ml = p.part_acc + rows * plan.max_parts * head_dim;
+        p.part_ml = p.part_acc + plan.workspace / sizeof(float) / (head_dim + 2) * head_dim;
     }
     return launch_tree(p, dtype, head_dim, stream_of(stream));
 }

@@ -63,16 +63,50 @@ pa_status launch_tc(TreeParams &p, int dtype, int head_dim, int dev, int sms, cu
         return cuda_fail(e, "tree kernel set-up");
     if (per_sm < 1)
         return fail(PA_ERR_UNSUPPORTED, "tree kernel does not fit on an SM");
-    const long long items = static_cast<long long>(p.num_seqs) * p.num_kv_heads * p.max_parts * p.row_tiles;
-    const long long grid = items < sms ? (items < 1 ? 1 : items) : sms;
-    if (items > grid)
-        p.work = work_counter(dev, stream);
+    const int grid = tree_tc_ctas(p.num_seqs, p.num_kv_heads, rows, p.max_len, sms);
     void *args[] = {&p, &tmk, &tmv, &tmq};
-    e = launch_dependent(fn, dim3(static_cast<unsigned>(grid)), dim3(kTcThreads), args, smem, stream);
-    return e == cudaSuccess ? PA_OK : cuda_fail(e, "tree launch");
+    e = launch_dependent(fn, dim3(grid), dim3(kTcThreads), args, smem, stream);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "tree launch");
+    // a context of one tile is never cut
+    if (grid > 1 && p.max_len > 128) {
+        const int slot_rows = units == 2 ? tc_slot_rows<2>(rows) : tc_slot_rows<1>(rows);
+        const int lrb = tree_merge_log_rows(slot_rows, head_dim);
+        const dim3 mgrid(grid - 1, (slot_rows + (1 << lrb) - 1) >> lrb, head_dim / (kTreeMergeCols * (32 >> lrb)));
+        const void *mf = head_dim == 64 ? (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 2>)
+                                                      : reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 1>))
+                                        : (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<128, 2>)
+                                                      : reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<128, 1>));
+        int ctas = grid;
+        void *margs[] = {&p, &ctas};
+        e = launch_dependent(mf, mgrid, dim3(kTreeMergeThreads), margs, 0, stream);
+        if (e != cudaSuccess)
+            return cuda_fail(e, "tree merge launch");
+    }
+    return PA_OK;
 }
 
 }  // namespace
+
+bool tree_tensor_cores(int dtype, int num_blocks, int num_kv_heads) {
+    return dtype != PA_F32 && static_cast<long long>(num_blocks) * num_kv_heads <= INT_MAX;
+}
+
+// One CTA per SM, no more than there can be units of work.
+int tree_tc_ctas(int num_seqs, int num_kv_heads, int rows, int max_len, int sms) {
+    const int tile_rows = rows > 128 ? 256 : 128;
+    const long long pairs =
+        static_cast<long long>(num_seqs) * num_kv_heads * ((rows + tile_rows - 1) / tile_rows);
+    const long long tiles = pairs * ((static_cast<long long>(max_len) + 127) / 128);  // (at least)
+    const int most = sms < kTreeSms ? sms : kTreeSms;
+    return static_cast<int>(tiles < most ? (tiles < 1 ? 1 : tiles) : most);
+}
+
+size_t tree_tc_workspace(int num_seqs, int num_kv_heads, int rows, int head_dim, int max_len) {
+    const int ctas = tree_tc_ctas(num_seqs, num_kv_heads, rows, max_len, kTreeSms);
+    const size_t slot_rows = static_cast<size_t>(rows < 256 ? rows : 256);
+    return ctas > 1 && max_len > 128 ? 2 * static_cast<size_t>(ctas) * slot_rows * (head_dim + 2) * sizeof(float) : 0;
+}
 
 pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t stream) {
     int dev = 0, sms = 0;
@@ -80,12 +114,12 @@ pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t strea
     if (e != cudaSuccess)
         return cuda_fail(e, "device query");
     void *args[] = {&p};
-    const pa_status st = dtype != PA_F32 && static_cast<long long>(p.num_blocks) * p.num_kv_heads <= INT_MAX
-                             ? launch_tc(p, dtype, head_dim, dev, sms, stream)
-                             : launch_general(p, dtype, head_dim, dev, stream);
+    const bool tensor_cores = tree_tensor_cores(dtype, p.num_blocks, p.num_kv_heads);
+    const pa_status st = tensor_cores ? launch_tc(p, dtype, head_dim, dev, sms, stream)
+                                      : launch_general(p, dtype, head_dim, dev, stream);
     if (st != PA_OK)
         return st;
-    if (p.max_parts > 1) {
+    if (!tensor_cores && p.max_parts > 1) {
         const int rows = p.num_draft * (p.num_heads / p.num_kv_heads);
         const int lrb = tree_merge_log_rows(rows, head_dim);
         const int col_chunks = head_dim / (kTreeMergeCols * (32 >> lrb));  // a power of two

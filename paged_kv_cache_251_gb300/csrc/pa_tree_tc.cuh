@@ -26,11 +26,20 @@
 // (the output is rounded as coarsely); an fp32 output takes hi + lo parts
 // (hi = round(p), lo = round(p - hi)), two accumulating products.
 //
-// Warp roles (384 threads, one CTA per SM, persistent over items (sequence,
-// partition, kv head, row tile)):
-//   warp 0      K producer: item ring, block-table slice in registers, K of
-//               each tile by TMA (one copy per block), and a record of the
-//               tile's blocks for the V producer;
+// Work is split evenly over the CTAs, one per SM: the tiles of all pairs
+// (sequence, kv head, row tile) in order, each pair counted with kTcPairCost
+// tiles more for what it costs whatever its length, are cut into gridDim.x equal
+// spans.  A CTA's items are the parts of pairs in its span; a pair inside one
+// span is finished there, one cut by a boundary leaves a partial in each CTA it
+// touches (at most two a CTA: the first and the last of its span), merged by a
+// second kernel.  Partials number a few hundred however long the contexts are
+// (fixed partitions of 1024 tokens wrote and read back a quarter of the K/V bytes
+// at 256 rows), and no CTA is left with a long item at the end.
+//
+// Warp roles (384 threads, persistent over the CTA's items):
+//   warp 0      K producer: the items of the span, block-table slices in
+//               registers, K of each tile by TMA (one copy per block), and a
+//               record of the tile's blocks for the V producer;
 //   warp 1      V producer, from the records;
 //   warp 2      tensor-memory allocation, the queries' TMA, S products;
 //   warp 3      P V products;
@@ -60,7 +69,6 @@ constexpr int kTcRecords = 3;    // record ring of the V producer
 // which was issued after the softmax of the sub-unit four before it was done, so no reader lags by more than
 // kSK + 1 <= 7 tiles
 constexpr int kTcMeta = 8;
-constexpr int kTcNear = 4;       // tiles of an item still to issue when the next one is claimed
 constexpr int kTcMaxBpt = 16;    // blocks per tile at block size 8
 constexpr uint32_t kTcEnd = 0xFFFFFFFFu;
 constexpr float kTcLazy = 8.0f;  // growth of a row's maximum (base 2) that rescales its O
@@ -81,8 +89,9 @@ template <int D, int Units> struct TcCfg {
 };
 
 struct TcItem {
-    int s, kvh, rt, part;
-    int nparts, nb, blk_lo, t_first;
+    int s, kvh, rt;
+    int slot;  // -1: the whole context, final rows; else this CTA's partial 0 or 1
+    int tile0, ntiles, t_first;
     int len, committed, drafted, end;
 };
 
@@ -232,7 +241,148 @@ template <typename T> __device__ inline bool non_finite2(uint32_t w) {
 }
 
 // ---------------------------------------------------------------------------
+// The even split
+
+constexpr int kTcPairCost = 2;
+
+__device__ inline int tc_tiles(const TreeParams &p, int s) {
+    const int len = max(0, min(ld_nc_i32(p.context_lens + s), p.max_len));
+    return (len >> 7) + ((len & 127) != 0);
+}
+
+// Span `part` of `parts` (warp-collective): the sequence of its first unit, the
+// units before that sequence, and all units.  No more spans than units: `parts`
+// is cut to that, so no span is empty; a span past it has no sequence.
+struct TcFind {
+    int s;
+    long long before, total, parts;
+    __device__ long long bound(long long b) const { return total * b / parts; }  // first unit of span b
+};
+__device__ inline TcFind tc_find(const TreeParams &p, int pairs_per_seq, int part, int parts) {
+    const int lane = threadIdx.x & 31;
+    TcFind f = {p.num_seqs, 0, 0, 1};
+    long long sum = 0;
+#pragma unroll 4
+    for (int s = lane; s < p.num_seqs; s += 32)
+        sum += tc_tiles(p, s) + kTcPairCost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    f.total = sum * pairs_per_seq;
+    f.parts = min(static_cast<long long>(parts), max(f.total, 1LL));
+    if (part >= f.parts)
+        return f;
+    const long long u = f.bound(part);
+    long long run = 0;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
+        const int s = s0 + lane;
+        const long long mine =
+            s < p.num_seqs ? static_cast<long long>(tc_tiles(p, s) + kTcPairCost) * pairs_per_seq : 0;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const uint32_t hit = __ballot_sync(0xffffffffu, run + incl > u);
+        if (hit) {
+            const int j = __ffs(hit) - 1;
+            f.s = s0 + j;
+            f.before = run + __shfl_sync(0xffffffffu, incl - mine, j);
+            return f;
+        }
+        run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return f;
+}
+
+// Tiles of a pair below unit u (the pair's units start at `start`; its cost
+// comes before its tiles).
+__device__ inline int tc_tiles_below(long long u, long long start, int tiles) {
+    const long long x = u - start - kTcPairCost;
+    return static_cast<int>(x < 0 ? 0 : (x > tiles ? tiles : x));
+}
+
+// ---------------------------------------------------------------------------
 // Producers
+
+// The items of a CTA's span, in chunks whose table slice fits the registers of
+// a warp (256 entries); every call gives the next chunk with its entries loaded.
+struct TcChunk {
+    int s = -1, kvh, rt, slot;
+    int tile0, ntiles;  // of the item
+    int lo, hi;         // of the chunk, in tiles of the sequence
+    int nblk;           // blocks of the sequence
+    int tb[kMaxBpp / 32];
+};
+struct TcWalk {
+    long long u0, u1, start;  // the span; first unit of the pair at hand
+    int s, j, tiles;
+    int lo, hi, at;  // the item at hand (tiles) and the next chunk's first tile
+    bool open;       // an item is being cut into chunks
+
+    __device__ void begin(const TreeParams &p, int pairs_per_seq) {
+        const TcFind f = tc_find(p, pairs_per_seq, blockIdx.x, gridDim.x);
+        u0 = f.bound(blockIdx.x);
+        u1 = f.bound(blockIdx.x + 1);
+        s = f.s;
+        open = false;
+        j = 0;
+        tiles = 0;
+        start = f.before;
+        if (s < p.num_seqs) {
+            tiles = tc_tiles(p, s);
+            j = static_cast<int>((u0 - start) / (tiles + kTcPairCost));
+            start += static_cast<long long>(j) * (tiles + kTcPairCost);
+        }
+    }
+    __device__ void next(const TreeParams &p, int pairs_per_seq, TcChunk &c) {
+        const int lane = threadIdx.x & 31;
+        const int bpt = 128 / p.block_size;
+        c.s = -1;
+        while (!open) {
+            if (s >= p.num_seqs || start >= u1)
+                return;
+            lo = tc_tiles_below(u0, start, tiles);
+            hi = tc_tiles_below(u1, start, tiles);
+            // (an empty context is the item of the CTA that has its first unit)
+            open = hi > lo || (tiles == 0 && start >= u0);
+            if (open)
+                at = lo;
+            else
+                step(p, pairs_per_seq);
+        }
+        c.s = s;
+        c.kvh = j / p.row_tiles;
+        c.rt = j - c.kvh * p.row_tiles;
+        c.slot = hi - lo == tiles ? -1 : (lo > 0 ? 0 : 1);
+        c.tile0 = lo;
+        c.ntiles = hi - lo;
+        c.lo = at;
+        c.hi = min(hi, at + kMaxBpp / bpt);
+        const int len = max(0, min(ld_nc_i32(p.context_lens + s), p.max_len));
+        c.nblk = len / p.block_size + (len % p.block_size != 0);
+        const int32_t *row = p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + c.lo * bpt;
+        const int n = min(c.hi * bpt, c.nblk) - c.lo * bpt;
+#pragma unroll
+        for (int i = 0; i < kMaxBpp / 32; ++i)
+            c.tb[i] = lane + 32 * i < n ? ld_nc_i32(row + lane + 32 * i) : -1;
+        at = c.hi;
+        if (at >= hi) {
+            open = false;
+            step(p, pairs_per_seq);
+        }
+    }
+    __device__ void step(const TreeParams &p, int pairs_per_seq) {
+        start += tiles + kTcPairCost;
+        if (++j == pairs_per_seq) {
+            j = 0;
+            if (++s < p.num_seqs)
+                tiles = tc_tiles(p, s);
+        }
+    }
+};
 
 template <int D, int Units>
 __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk, char *smem, TcMisc *M) {
@@ -243,53 +393,52 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
     const uint64_t policy = policy_evict_first();
     if (lane == 0)
         prefetch_tensormap(tmk);
-    ItemScan scan;
-    ItemClaim claim;
-    claim.start();
-    NextItem cur, nxt;
-    const long long groups = static_cast<long long>(p.num_kv_heads) * p.row_tiles;
-    prepare_item(p, bs, scan, claim.w, groups, cur);
-    uint32_t t = 0;
+    const int pairs_per_seq = p.num_kv_heads * p.row_tiles;
+    TcWalk walk;
+    TcChunk cur, nxt;
+    walk.begin(p, pairs_per_seq);
+    walk.next(p, pairs_per_seq, cur);
+    uint32_t t = 0, k = 0;
     bool ok = true;
-    for (uint32_t k = 0;; ++k) {
-        const int slot = static_cast<int>(k % kTcItems);
-        if (!mbar_wait_bounded(&M->iempty[slot], ((k / kTcItems) & 1u) ^ 1u)) {
-            ok = false;
-            break;
-        }
-        if (cur.s < 0) {
+    for (;;) {
+        if (cur.s < 0 || cur.lo == cur.tile0) {  // an item starts, or the span is done
+            const int slot = static_cast<int>(k % kTcItems);
+            if (!mbar_wait_bounded(&M->iempty[slot], ((k / kTcItems) & 1u) ^ 1u)) {
+                ok = false;
+                break;
+            }
+            ++k;
+            if (cur.s < 0) {
+                if (lane == 0) {
+                    M->items[slot].end = 1;
+                    mbar_arrive(&M->ifull[slot]);
+                }
+                __syncwarp();
+                break;
+            }
             if (lane == 0) {
-                M->items[slot].end = 1;
+                const TreeSeq q = tree_seq(p, cur.s);
+                if (q.bad && cur.tile0 == 0 && cur.kvh == 0 && cur.rt == 0 && p.err)
+                    atomicOr(p.err, PA_DEVERR_BAD_LEN);
+                TcItem it;
+                it.s = cur.s;
+                it.kvh = cur.kvh;
+                it.rt = cur.rt;
+                it.slot = cur.slot;
+                it.tile0 = cur.tile0;
+                it.ntiles = cur.ntiles;
+                it.t_first = static_cast<int>(t);
+                it.len = q.len;
+                it.committed = q.len - q.drafted;
+                it.drafted = q.drafted;
+                it.end = 0;
+                M->items[slot] = it;
                 mbar_arrive(&M->ifull[slot]);
             }
             __syncwarp();
-            break;
         }
-        const int ntiles = (cur.nb + bpt - 1) / bpt;
-        const int kvh = cur.head / p.row_tiles;
-        if (lane == 0) {
-            const TreeSeq q = tree_seq(p, cur.s);
-            if (q.bad && cur.part == 0 && cur.head == 0 && p.err)
-                atomicOr(p.err, PA_DEVERR_BAD_LEN);
-            TcItem it;
-            it.s = cur.s;
-            it.kvh = kvh;
-            it.rt = cur.head - kvh * p.row_tiles;
-            it.part = cur.part;
-            it.nparts = cur.sp.nparts;
-            it.nb = cur.nb;
-            it.blk_lo = cur.blk_lo;
-            it.t_first = static_cast<int>(t);
-            it.len = q.len;
-            it.committed = q.len - q.drafted;
-            it.drafted = q.drafted;
-            it.end = 0;
-            M->items[slot] = it;
-            mbar_arrive(&M->ifull[slot]);
-        }
-        __syncwarp();
-        bool have_next = false;
-        for (int ti = 0; ti < ntiles; ++ti, ++t) {
+        walk.next(p, pairs_per_seq, nxt);  // its entries arrive while this chunk is issued
+        for (int tile = cur.lo; tile < cur.hi; ++tile, ++t) {
             const int stage = static_cast<int>(t % C::kSK), rec = static_cast<int>(t % kTcRecords);
             if (!mbar_wait_bounded(&M->kempty[stage], ((t / C::kSK) & 1u) ^ 1u) ||
                 !mbar_wait_bounded(&M->zfree[rec], ((t / kTcRecords) & 1u) ^ 1u)) {
@@ -297,7 +446,7 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
                 break;
             }
             // lane j takes block j of the tile: its entry is in lane (index % 32) of the slice registers
-            const int b0 = ti * bpt;  // (a tile's entries share one register: bpt divides 32)
+            const int b0 = (tile - cur.lo) * bpt;  // (a tile's entries share one register: bpt divides 32)
             int entry = -1;
 #pragma unroll
             for (int i = 0; i < kMaxBpp / 32; ++i) {
@@ -305,12 +454,12 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
                 if (i == b0 >> 5)
                     entry = e;
             }
-            const bool in = lane < bpt && b0 + lane < cur.nb;
+            const bool in = lane < bpt && tile * bpt + lane < cur.nblk;
             const bool mine = in && entry >= 0 && entry < p.num_blocks;
             if (in && !mine && p.err)
                 atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
             const uint32_t mask = __ballot_sync(0xffffffffu, mine);
-            const int z = mine ? entry * p.num_kv_heads + kvh : 0;
+            const int z = mine ? entry * p.num_kv_heads + cur.kvh : 0;
             if (lane < kTcMaxBpt)
                 M->zid[rec][lane] = z;
             if (lane == 0) {
@@ -327,18 +476,9 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
             if (lane == 0)
                 mbar_arrive(&M->zfull[rec]);
             __syncwarp();
-            if (ti == max(0, ntiles - kTcNear)) {  // the next item, while copies are in flight
-                claim.next(p);
-                prepare_item(p, bs, scan, claim.w, groups, nxt);
-                have_next = true;
-            }
         }
         if (!ok)
             break;
-        if (!have_next) {
-            claim.next(p);
-            prepare_item(p, bs, scan, claim.w, groups, nxt);
-        }
         cur = nxt;
     }
     // no more tiles for the V producer (after a failed wait too)
@@ -356,7 +496,6 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
         for (uint32_t u = first; u < t; ++u)
             (void)mbar_wait_bounded(&M->kfull[u % C::kSK], (u / C::kSK) & 1u);
     }
-    claim.finish(p);
     __syncwarp();
 }
 
@@ -438,7 +577,6 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
     // buffer are added to the address field (16-byte units)
     const uint64_t q_desc = sdesc(smem, 16, 1024);
     const uint64_t k_desc = sdesc(smem + C::kOffK, 16, C::kGroup);
-    const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
     const int G = p.num_heads / p.num_kv_heads;
     if (lane0)
         prefetch_tensormap(tmq);
@@ -455,7 +593,7 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
             mbar_arrive(&M->iempty[slot]);
         if (it.end)
             return true;
-        const int ntiles = (it.nb + (1 << lbpt) - 1) >> lbpt;
+        const int ntiles = it.ntiles;
         if (ntiles == 0)
             continue;
         // the Q buffer: free once the last S of the item before has finished
@@ -514,19 +652,17 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
     const bool lane0 = (threadIdx.x & 31) == 0;
     // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
     const uint64_t v_desc = sdesc(smem + C::kOffV, 1024, C::kGroup);
-    const int lbpt = p.block_size == 8 ? 4 : (p.block_size == 16 ? 3 : 2);
     uint32_t t = 0, ke = 0, vst = 0, vph = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
             return false;
-        const int nb = M->items[slot].nb, end = M->items[slot].end;
+        const int ntiles = M->items[slot].ntiles, end = M->items[slot].end;
         __syncwarp();
         if (lane0)
             mbar_arrive(&M->iempty[slot]);
         if (end)
             return true;
-        const int ntiles = (nb + (1 << lbpt) - 1) >> lbpt;
         if (ntiles == 0)
             continue;
         for (int ti = 0; ti < ntiles; ++ti, ++t) {
@@ -625,6 +761,11 @@ __device__ inline void store_cols32(void *out, int dtype, long long idx, const f
     }
 }
 
+// Rows of a partial: those of the row tile(s) a CTA takes.
+template <int Units> __host__ __device__ inline int tc_slot_rows(int rows) {
+    return rows < 128 * Units ? rows : 128 * Units;
+}
+
 template <int N> __device__ inline float max_of(const float *v) {
     float m[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
@@ -711,7 +852,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             mbar_arrive(&M->iempty[slot]);
         if (it.end)
             return true;
-        const int ntiles = (it.nb + bpt - 1) / bpt;
+        const int ntiles = it.ntiles;
         // this thread's row of the (sequence, kv head)
         const int r = (it.rt * Units + (Units == 2 ? wg : 0)) * 128 + row;
         const int i = r >> lg;
@@ -729,7 +870,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             const int half = Units == 2 ? 0 : wg;
             const uint32_t buf = tc_buf<Units>(t, wg);
             const uint32_t s_addr = tmem + lanes + tc_buf_col(buf);
-            const int tok0 = (it.blk_lo << lbs) + ti * 128 + half * 64;
+            const int tok0 = (it.tile0 + ti) * 128 + half * 64;
             uint64_t allow[Units];
             bool masked = false, poisoned = false;
             if (!ready) {
@@ -942,7 +1083,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             first = false;
         }
         // ---- the item's output: final rows, or a partial per row
-        const bool direct = it.nparts == 1;
+        const bool direct = it.slot < 0;
         if (!live)  // padding rows in a warp with live ones: they attend nothing
             m = -INFINITY, l = 0.f;
         float f0 = 1.f, f1 = 0.f, den = l, mx = m;
@@ -967,8 +1108,9 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
         // adjacent there: whole lines without any exchange)
         constexpr int kCols = Units == 1 ? D / 2 : D;
         const int col0 = Units == 1 ? wg * kCols : 0;
-        const int rows = p.num_draft << lg;
-        const long long item = (static_cast<long long>(it.s) * p.num_kv_heads + it.kvh) * p.max_parts + it.part;
+        const int rows = tc_slot_rows<Units>(p.num_draft << lg);
+        const int ir = r - it.rt * Units * 128;  // row of the row tile(s)
+        const long long item = static_cast<long long>(blockIdx.x) * 2 + it.slot;
         if (__any_sync(0xffffffffu, stored)) {
             if (direct) {
                 const float inv = den == 0.f ? 0.f : __fdividef(1.f, den);
@@ -1002,7 +1144,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     if (stored)
                         store_cols32(p.out, p.out_dtype, orow * D + c, o);
                 } else if (stored && den != 0.f) {
-                    float *a = p.part_acc + (item * D + c) * rows + r;
+                    float *a = p.part_acc + (item * D + c) * rows + ir;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         a[static_cast<long long>(e) * rows] = o[e];
@@ -1010,7 +1152,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
             }
         }
         if (stored && !direct && col0 == 0)
-            reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(mx, den);
+            reinterpret_cast<float2 *>(p.part_ml)[item * rows + ir] = make_float2(mx, den);
         if (ntiles > 0) {
             tc_fence_before();
             __syncwarp();
@@ -1112,8 +1254,102 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     if (!ok && (threadIdx.x & 31) == 0 && p.err)
         atomicOr(p.err, PA_DEVERR_TIMEOUT);
+}
+
+// ---------------------------------------------------------------------------
+// Merge of the pairs that a span boundary cuts.  Boundary b (between the spans
+// of CTAs b - 1 and b of the tree kernel, `ctas` of them) merges its pair when
+// it is the first boundary with tiles of the pair on both sides: the parts are
+// CTA b - 1's second partial and the first partials of the CTAs after it up to
+// the pair's end.  grid: boundary, row chunk, column group; a CTA's lanes are
+// RB rows x 32 / RB columns (whole lines of the column-major partials) with
+// kTreeMergeCols columns each, its 8 warps take every eighth part.
+template <int D, int Units>
+__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_tc_merge_kernel(const TreeParams p, int ctas) {
+    pdl_launch_dependents();
+    pdl_wait();
+    constexpr int E = kTreeMergeCols;
+    __shared__ float acc[kTreeMergeWarps][E][33];  // [warp][element][lane]
+    __shared__ float2 state[kTreeMergeWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int G = p.num_heads / p.num_kv_heads;
+    const int all_rows = p.num_draft * G, rows = tc_slot_rows<Units>(all_rows);
+    const int lrb = tree_merge_log_rows(rows, D);
+    const int RB = 1 << lrb, CB = 32 >> lrb;
+    const int b = blockIdx.x + 1, r0 = blockIdx.y << lrb, col0 = blockIdx.z * (E * CB);
+    const int pairs_per_seq = p.num_kv_heads * p.row_tiles;
+    const TcFind f = tc_find(p, pairs_per_seq, b, ctas);
+    if (f.s >= p.num_seqs)
+        return;
+    const int tiles = tc_tiles(p, f.s);
+    const long long ub = f.bound(b);
+    const int j = static_cast<int>((ub - f.before) / (tiles + kTcPairCost));
+    const long long start = f.before + static_cast<long long>(j) * (tiles + kTcPairCost);
+    const int cut = tc_tiles_below(ub, start, tiles);
+    if (cut == 0 || cut == tiles || tc_tiles_below(f.bound(b - 1), start, tiles) > 0)
+        return;
+    // the CTA of the pair's last tile
+    const long long last_unit = start + kTcPairCost + tiles - 1;
+    const int last = static_cast<int>(((last_unit + 1) * f.parts - 1) / f.total);
+    const int nparts = last - b + 2;
+    const int kvh = j / p.row_tiles, rt = j - kvh * p.row_tiles;
+    const int r = r0 + (lane & (RB - 1));
+    float M = -INFINITY, den = 0.f, num[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        num[e] = 0.f;
+    if (r < rows) {
+        for (int q = warp; q < nparts; q += kTreeMergeWarps) {
+            // part 0: CTA b - 1, partial 1; part q: CTA b - 1 + q, partial 0
+            const long long slot = q == 0 ? 2LL * (b - 1) + 1 : 2LL * (b - 1 + q);
+            const float2 v = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
+            const float *a = p.part_acc + (slot * D + col0 + (lane >> lrb)) * rows + r;
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[e] = a[static_cast<long long>(e * CB) * rows];
+            if (v.y == 0.f)  // it attended nothing there, and left no accumulator
+                continue;
+            const float mn = fmaxf(M, v.x);
+            const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
+            den = den * keep + v.y * add;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                num[e] = num[e] * keep + x[e] * add;
+            M = mn;
+        }
+    }
+    state[warp][lane] = make_float2(M, den);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[warp][e][lane] = num[e];
     __syncthreads();
-    release_claims(p);
+    // output o of the CTA: row o / (E CB), column o % (E CB)
+    for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
+        const int rr = o / (E * CB), c = o - rr * (E * CB);
+        const int full = rt * Units * 128 + r0 + rr;  // row of the (sequence, kv head)
+        if (r0 + rr >= rows || full >= all_rows)
+            break;
+        const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kTreeMergeWarps; ++w)
+            if (state[w][ln].y != 0.f)
+                m = fmaxf(m, state[w][ln].x);
+        float n = 0.f, d = 0.f;
+#pragma unroll
+        for (int w = 0; w < kTreeMergeWarps; ++w) {
+            const float2 v = state[w][ln];
+            if (v.y != 0.f) {
+                const float sc = v.x == m ? 1.f : exp2f(v.x - m);
+                d = fmaf(v.y, sc, d);
+                n = fmaf(acc[w][e][ln], sc, n);
+            }
+        }
+        const long long orow =
+            (static_cast<long long>(f.s) * p.num_draft + full / G) * p.num_heads + kvh * G + full % G;
+        store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+    }
 }
 
 }  // namespace pa

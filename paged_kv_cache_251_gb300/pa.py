@@ -75,7 +75,7 @@ def _load():
     lib.pa_rope.restype = I
     lib.pa_rope_append_kv.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, LL, LL, LL, I, I, I, F, I, P, P]
     lib.pa_rope_append_kv.restype = I
-    lib.pa_decode_tree.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_decode_tree.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P, SZ, P, P]
     lib.pa_decode_tree.restype = I
     lib.pa_decode_tree_workspace_size.argtypes = [I, I, I, I, I, I, I, I]
     lib.pa_decode_tree_workspace_size.restype = SZ
@@ -536,17 +536,16 @@ def pa_rope_append_kv(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
 
 
 def pa_decode_tree_workspace_size(num_seqs: int, num_draft: int, num_heads: int, num_kv_heads: int, head_dim: int,
-                                  block_size: int, max_blocks_per_seq: int, partition_size: int = 0) -> int:
+                                  block_size: int, max_blocks_per_seq: int, dtype: torch.dtype) -> int:
     return int(_lib.pa_decode_tree_workspace_size(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size,
-                                                  max_blocks_per_seq, partition_size))
+                                                  max_blocks_per_seq, DTYPE_CODE[dtype]))
 
 
-def tree_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int,
-                       partition_size: int = 0) -> torch.Tensor | None:
+def tree_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int) -> torch.Tensor | None:
     """A workspace tensor for pa_decode_tree (None if 0 bytes)."""
     n, t, h, d = q.shape
     return _ws(pa_decode_tree_workspace_size(n, t, h, k_cache.shape[1], d, k_cache.shape[2], max_blocks_per_seq,
-                                             partition_size), q.device)
+                                             k_cache.dtype), q.device)
 
 
 def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
@@ -586,7 +585,7 @@ def _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d) -> tu
 
 def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                    block_tables: torch.Tensor, context_lens: torch.Tensor, tree_mask: torch.Tensor | None = None,
-                   draft_lens: torch.Tensor | None = None, scale: float | None = None, partition_size: int = 0,
+                   draft_lens: torch.Tensor | None = None, scale: float | None = None,
                    workspace: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
                    stream=None) -> torch.Tensor:
     """Attention of each sequence's drafted tokens (q, out: [N, T, H, d]) over
@@ -609,11 +608,11 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = tree_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
+        workspace = tree_workspace_for(q, k_cache, block_tables.shape[1])
     _call(_lib.pa_decode_tree, dev, stream, _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
           _ptr(context_lens), _ptr(draft_lens), _ptr(tree_mask), n, t, h, hkv, d, bs, float(scale),
-          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, int(partition_size),
-          _ptr(workspace), _ws_bytes(workspace), _ptr(err_word))
+          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _ptr(workspace),
+          _ws_bytes(workspace), _ptr(err_word))
     return out
 
 

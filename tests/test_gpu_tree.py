@@ -10,18 +10,18 @@ from steplib import attention_bound, check_within, paged, random_parents, tree_o
 pytestmark = pytest.mark.gpu
 
 
-def run(q, k, v, tables, lens, mask, drafts, out_dtype, partition=0, workspace=None, err=None, scale=None):
+def run(q, k, v, tables, lens, mask, drafts, out_dtype, workspace=None, err=None, scale=None):
     from paged_kv_cache_251_gb300 import pa
     out = torch.full(q.shape, float("nan"), dtype=out_dtype, device="cuda")
-    pa.pa_decode_tree(out, q, k, v, tables, lens, tree_mask=mask, draft_lens=drafts, partition_size=partition,
-                      workspace=workspace, err_word=err, scale=scale)
+    pa.pa_decode_tree(out, q, k, v, tables, lens, tree_mask=mask, draft_lens=drafts, workspace=workspace,
+                      err_word=err, scale=scale)
     return out
 
 
-def check(q, k, v, tables, lens, drafts, mask, out_dtype, partition=0, scale=None):
+def check(q, k, v, tables, lens, drafts, mask, out_dtype, scale=None):
     T = q.shape[1]
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = run(q, k, v, tables, lens, mask, drafts, out_dtype, partition, err=err, scale=scale)
+    out = run(q, k, v, tables, lens, mask, drafts, out_dtype, err=err, scale=scale)
     d = drafts if drafts is not None else torch.full((q.shape[0],), T)
     ref, mag, dx = tree_oracle(q, k, v, tables, lens, d, mask, scale or 1 / math.sqrt(q.shape[-1]))
     torch.cuda.synchronize()
@@ -31,17 +31,17 @@ def check(q, k, v, tables, lens, drafts, mask, out_dtype, partition=0, scale=Non
 
 
 CASES = [
-    # H, H_kv, d, block, T, contexts (drafted tokens included), drafted, partition
-    (4, 4, 64, 16, 1, [1, 2, 17, 100], [1, 1, 1, 1], 0),
-    (8, 2, 128, 16, 5, [5, 4, 0, 700], [5, 3, 0, 2], 0),                 # all drafted; an empty sequence
-    (8, 1, 128, 8, 16, [16, 129, 1000], [16, 16, 9], 128),               # 128 rows a kv head
-    (8, 2, 128, 16, 33, [33, 160, 515, 40], [33, 20, 33, 1], 64),        # 132 rows: two row tiles
-    (16, 2, 64, 32, 40, [300, 41, 1025], [40, 40, 31], 0),
-    (4, 4, 128, 32, 64, [64, 200], [64, 64], 0),
-    (4, 2, 128, 16, 70, [500, 71], [70, 70], 256),                       # two mask words
-    (2, 2, 64, 8, 130, [400, 131], [130, 100], 0),                       # three
-    (8, 8, 128, 16, 8, [2048, 1111, 8, 9], [8, 8, 8, 8], 0),
-    (8, 1, 128, 16, 64, [2000], [64], 0),                                # 512 rows
+    # H, H_kv, d, block, T, contexts (drafted tokens included), drafted
+    (4, 4, 64, 16, 1, [1, 2, 17, 100], [1, 1, 1, 1]),
+    (8, 2, 128, 16, 5, [5, 4, 0, 700], [5, 3, 0, 2]),                 # all drafted; an empty sequence
+    (8, 1, 128, 8, 16, [16, 129, 1000], [16, 16, 9]),               # 128 rows a kv head
+    (8, 2, 128, 16, 33, [33, 160, 515, 40], [33, 20, 33, 1]),        # 132 rows: two row tiles
+    (16, 2, 64, 32, 40, [300, 41, 1025], [40, 40, 31]),
+    (4, 4, 128, 32, 64, [64, 200], [64, 64]),
+    (4, 2, 128, 16, 70, [500, 71], [70, 70]),                       # two mask words
+    (2, 2, 64, 8, 130, [400, 131], [130, 100]),                       # three
+    (8, 8, 128, 16, 8, [2048, 1111, 8, 9], [8, 8, 8, 8]),
+    (8, 1, 128, 16, 64, [2000], [64]),                                # 512 rows
 ]
 
 
@@ -50,12 +50,12 @@ CASES = [
 @pytest.mark.parametrize("wide", [False, True])
 def test_tree(case, dtype, wide):
     from paged_kv_cache_251_gb300 import pa
-    h, hkv, d, bs, t, lens, drafted, part = case
+    h, hkv, d, bs, t, lens, drafted = case
     k, v, tables, lens_t = paged(17, lens, hkv, d, bs, dtype)
     q = wl.normal_tensor(9, 3, (len(lens), t, h, d), dtype=dtype).cuda()
     mask = pa.tree_mask_from_parents(random_parents(t, len(lens), t)).cuda()
     check(q, k, v, tables, lens_t, torch.tensor(drafted, dtype=torch.int32, device="cuda"), mask,
-          torch.float32 if wide else dtype, part)
+          torch.float32 if wide else dtype)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -143,7 +143,7 @@ def test_ramps_and_dominant_keys(dtype):
     from paged_kv_cache_251_gb300 import pa
     mask = pa.tree_mask_from_parents(random_parents(2, 3, t)).cuda()
     for out_dtype in (torch.float32, dtype):
-        check(q, k, v, tables, lens_t, None, mask, out_dtype, partition=256)
+        check(q, k, v, tables, lens_t, None, mask, out_dtype)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
@@ -156,7 +156,7 @@ def test_scales(dtype, scale):
     q = wl.normal_tensor(8, 3, (2, t, h, d), dtype=dtype).cuda()
     mask = pa.tree_mask_from_parents(random_parents(2, 2, t)).cuda()
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = run(q, k, v, tables, lens_t, mask, None, torch.float32, partition=128, err=err, scale=scale)
+    out = run(q, k, v, tables, lens_t, mask, None, torch.float32, err=err, scale=scale)
     ref, mag, dx = tree_oracle(q, k, v, tables, lens_t, [t, t], mask, scale)
     assert err.item() == 0
     check_within(out, ref, attention_bound(ref, mag, dx, dtype, torch.float32, 300))
@@ -174,7 +174,7 @@ def test_bad_tables_and_lengths(dtype):
     bad = tables.clone()
     bad[0, 3], bad[0, 4], bad[1, 0], bad[2, :] = -7, k.shape[0], 2 ** 31 - 1, -1
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out = run(q, k, v, bad, lens_t, None, None, torch.float32, partition=128, err=err)
+    out = run(q, k, v, bad, lens_t, None, None, torch.float32, err=err)
     assert err.item() == pa.DEVERR_BAD_BLOCK
     assert (out[2] == 0).all()
     # the same with the tokens of those blocks never attended
@@ -211,13 +211,13 @@ def test_captured_replays_and_two_streams_match():
     k, v, tables, lens_t = paged(31, lens, hkv, d, 16, torch.bfloat16)
     mask = pa.tree_mask_from_parents(random_parents(4, 4, t)).cuda()
     qs = [wl.normal_tensor(40 + i, 3, (4, t, h, d), dtype=torch.bfloat16).cuda() for i in range(3)]
-    want = [run(q, k, v, tables, lens_t, mask, None, torch.bfloat16, partition=256) for q in qs]
-    ws = [pa.tree_workspace_for(qs[0], k, tables.shape[1], 256) for _ in range(2)]
+    want = [run(q, k, v, tables, lens_t, mask, None, torch.bfloat16) for q in qs]
+    ws = [pa.tree_workspace_for(qs[0], k, tables.shape[1]) for _ in range(2)]
     q, out = qs[0].clone(), torch.empty_like(qs[0])
     g = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(g):
-        pa.pa_decode_tree(out, q, k, v, tables, lens_t, tree_mask=mask, partition_size=256, workspace=ws[0])
+        pa.pa_decode_tree(out, q, k, v, tables, lens_t, tree_mask=mask, workspace=ws[0])
     for i in (0, 1, 2, 1):
         q.copy_(qs[i])
         g.replay()
@@ -227,8 +227,8 @@ def test_captured_replays_and_two_streams_match():
     torch.cuda.synchronize()
     for _ in range(4):
         for i in range(2):
-            pa.pa_decode_tree(outs[i], qs[i], k, v, tables, lens_t, tree_mask=mask, partition_size=256,
-                              workspace=ws[i], stream=streams[i])
+            pa.pa_decode_tree(outs[i], qs[i], k, v, tables, lens_t, tree_mask=mask, workspace=ws[i],
+                              stream=streams[i])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
 

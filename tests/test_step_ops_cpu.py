@@ -59,15 +59,15 @@ def test_rope_append_refusals(lib):
 
 def test_tree_refusals(lib):
     call = caller(lib.pa_decode_tree,
-                  [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, I, P, SZ, P, P],
+                  [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P, SZ, P, P],
                   dict(out=0x1000, q=0x2000, k=0x3000, v=0x4000, bt=0x5000, cl=0x6000, dl=None, mask=0x7000, n=4, t=8,
-                       h=8, hkv=2, d=128, bs=16, scale=0.1, dt=2, odt=2, m=8, nb=64, part=0, ws=None, wsb=0, err=None,
+                       h=8, hkv=2, d=128, bs=16, scale=0.1, dt=2, odt=2, m=8, nb=64, ws=None, wsb=0, err=None,
                        st=None))
     assert call(n=0) == 0
     assert call(h=12, hkv=4) == UNS and call(d=96) == UNS and call(bs=24) == UNS
     for bad in (dict(t=0), dict(t=257), dict(n=-1), dict(h=9), dict(hkv=0), dict(q=0), dict(cl=0), dict(k=0x3008),
-                dict(mask=0x7004), dict(scale=float("inf")), dict(dt=4), dict(odt=3), dict(nb=0), dict(part=24),
-                dict(m=0), dict(out=0x1001)):
+                dict(mask=0x7004), dict(scale=float("inf")), dict(dt=4), dict(odt=3), dict(nb=0), dict(m=0),
+                dict(out=0x1001)):
         assert call(**bad) == INV, bad
     assert call(m=1000) == WS
     assert call(m=1000, ws=0x100, wsb=16) == WS
@@ -77,14 +77,16 @@ def test_tree_refusals(lib):
 def test_tree_workspace_size(lib):
     f = lib.pa_decode_tree_workspace_size
     f.restype, f.argtypes = SZ, [I] * 8
-    assert f(4, 8, 8, 2, 128, 16, 8, 0) == 0                       # one partition
-    assert f(4, 8, 8, 2, 128, 16, 64, 256) == 4 * 8 * 8 * 4 * 130 * 4
-    assert f(4, 0, 8, 2, 128, 16, 64, 256) == 0 and f(4, 8, 9, 2, 128, 16, 64, 256) == 0
-    # the chosen partition covers the whole context in whole blocks
-    for n, t, m in ((1, 1, 8192), (64, 16, 512), (4, 64, 8192), (1, 256, 7)):
-        for bs in (8, 16, 32):
-            size = f(n, t, 32, 8, 128, bs, m, 0)
-            assert size % (n * t * 32 * 130 * 4) == 0
+    F32, BF16 = 0, 2
+    assert f(4, 8, 8, 2, 128, 16, 8, BF16) == 0                       # contexts of one 128-token tile are never cut
+    assert f(4, 8, 8, 2, 128, 16, 9, BF16) == 2 * 16 * 32 * 130 * 4   # two partials for each of 16 CTAs, 32 rows
+    assert f(64, 16, 32, 8, 128, 16, 512, BF16) == 2 * 152 * 64 * 130 * 4
+    assert f(4, 64, 32, 8, 128, 16, 8192, BF16) == 2 * 152 * 256 * 130 * 4
+    assert f(4, 256, 64, 8, 64, 16, 8192, BF16) == 2 * 152 * 256 * 66 * 4   # 2048 rows: tiles of 256
+    assert f(4, 8, 8, 2, 128, 16, 16, F32) == 0                       # one 256-token partition
+    assert f(4, 8, 8, 2, 128, 16, 64, F32) == 4 * 8 * 8 * 4 * 130 * 4
+    assert f(4, 0, 8, 2, 128, 16, 64, F32) == 0 and f(4, 8, 9, 2, 128, 16, 64, F32) == 0
+    assert f(4, 8, 8, 2, 128, 16, 64, 3) == 0
 
 
 def test_scored_refusals(lib):
