@@ -332,10 +332,19 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
     p.num_draft = num_draft;
     p.words = (num_draft + 63) / 64;
     p.row_tiles = 0;
+    p.cuts = nullptr;
     if (plan.workspace > 0) {
-        // accumulators, then the (max, denominator) pairs: head_dim : 2 of the workspace
-        p.part_acc = static_cast<float *>(workspace);
-        p.part_ml = p.part_acc + plan.workspace / sizeof(float) / (head_dim + 2) * head_dim;
+        if (tree_tensor_cores(dtype, num_blocks, num_kv_heads)) {
+            // merge records, accumulators, (max, denominator) pairs
+            const int tree_rows = num_draft * (num_heads / num_kv_heads);
+            const size_t ctas = tree_tc_ctas(num_seqs, num_kv_heads, tree_rows, p.max_len, kTreeSms);
+            p.cuts = static_cast<int4 *>(workspace);
+            p.part_acc = reinterpret_cast<float *>(p.cuts + ctas);
+            p.part_ml = p.part_acc + 2 * ctas * (tree_rows < 256 ? tree_rows : 256) * head_dim;
+        } else {
+            p.part_acc = static_cast<float *>(workspace);
+            p.part_ml = p.part_acc + rows * plan.max_parts * head_dim;
+        }
     }
     return launch_tree(p, dtype, head_dim, stream_of(stream));
 }

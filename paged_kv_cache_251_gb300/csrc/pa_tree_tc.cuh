@@ -313,11 +313,13 @@ struct TcChunk {
     int s = -1, kvh, rt, slot;
     int tile0, ntiles;  // of the item
     int lo, hi;         // of the chunk, in tiles of the sequence
+    int parts;          // slot 1: CTAs that hold a part of the pair
     int nblk;           // blocks of the sequence
     int tb[kMaxBpp / 32];
 };
 struct TcWalk {
     long long u0, u1, start;  // the span; first unit of the pair at hand
+    long long total, spans;
     int s, j, tiles;
     int lo, hi, at;  // the item at hand (tiles) and the next chunk's first tile
     bool open;       // an item is being cut into chunks
@@ -326,6 +328,8 @@ struct TcWalk {
         const TcFind f = tc_find(p, pairs_per_seq, blockIdx.x, gridDim.x);
         u0 = f.bound(blockIdx.x);
         u1 = f.bound(blockIdx.x + 1);
+        total = f.total;
+        spans = f.parts;
         s = f.s;
         open = false;
         j = 0;
@@ -357,6 +361,10 @@ struct TcWalk {
         c.kvh = j / p.row_tiles;
         c.rt = j - c.kvh * p.row_tiles;
         c.slot = hi - lo == tiles ? -1 : (lo > 0 ? 0 : 1);
+        if (c.slot == 1) {  // up to the CTA of the pair's last unit
+            const long long last = start + kTcPairCost + tiles - 1;
+            c.parts = static_cast<int>(((last + 1) * spans - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+        }
         c.tile0 = lo;
         c.ntiles = hi - lo;
         c.lo = at;
@@ -397,6 +405,9 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
     TcWalk walk;
     TcChunk cur, nxt;
     walk.begin(p, pairs_per_seq);
+    // the merge's record of this CTA: the pair that its second partial begins,
+    // and the parts that pair is in
+    int4 cut = make_int4(0, 0, 0, 0);
     walk.next(p, pairs_per_seq, cur);
     uint32_t t = 0, k = 0;
     bool ok = true;
@@ -416,6 +427,8 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
                 __syncwarp();
                 break;
             }
+            if (cur.slot == 1)
+                cut = make_int4(cur.s, cur.kvh, cur.rt, cur.parts);
             if (lane == 0) {
                 const TreeSeq q = tree_seq(p, cur.s);
                 if (q.bad && cur.tile0 == 0 && cur.kvh == 0 && cur.rt == 0 && p.err)
@@ -481,6 +494,8 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
             break;
         cur = nxt;
     }
+    if (lane == 0 && p.cuts)
+        p.cuts[blockIdx.x] = cut;
     // no more tiles for the V producer (after a failed wait too)
     if (lane == 0) {
         const int rec = static_cast<int>(t % kTcRecords);
@@ -1177,6 +1192,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (smem_addr(smem) & 1023u) {
         if (threadIdx.x == 0 && p.err)
             atomicOr(p.err, PA_DEVERR_BAD_LAUNCH);
+        if (threadIdx.x == 0 && p.cuts)
+            p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
     TcMisc *M = reinterpret_cast<TcMisc *>(smem + C::kOffMisc);
@@ -1221,10 +1238,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(&M->tmem);
 
-    // registers: 384 x 168 = 128 x 72 + 256 x 216
+    // registers: 384 x 168 = 128 x 88 + 256 x 208
     bool ok = true;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             tc_kproducer<D, Units>(p, &tmk, smem, M);
         } else if (warp == 1) {
@@ -1245,7 +1262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         ok = tc_softmax<T, D, Parts, Units>(p, smem, M, tmem);
         tc_fence_before();
         __syncwarp();
@@ -1257,98 +1274,89 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the pairs that a span boundary cuts.  Boundary b (between the spans
-// of CTAs b - 1 and b of the tree kernel, `ctas` of them) merges its pair when
-// it is the first boundary with tiles of the pair on both sides: the parts are
-// CTA b - 1's second partial and the first partials of the CTAs after it up to
-// the pair's end.  grid: boundary, row chunk, column group; a CTA's lanes are
-// RB rows x 32 / RB columns (whole lines of the column-major partials) with
-// kTreeMergeCols columns each, its 8 warps take every eighth part.
+// Merge of the pairs that a span boundary cuts: CTA c's second partial begins
+// such a pair (its record says which, and in how many parts), the first partials
+// of the CTAs after it continue it.  grid: CTA of the tree kernel, row chunk,
+// column group; a CTA's lanes are RB rows x 32 / RB columns (whole lines of the
+// column-major partials) with kTreeMergeCols columns each, `steps` times over,
+// and its 8 warps take every eighth part.
 template <int D, int Units>
-__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_tc_merge_kernel(const TreeParams p, int ctas) {
+__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_tc_merge_kernel(const TreeParams p, int steps) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int E = kTreeMergeCols;
     __shared__ float acc[kTreeMergeWarps][E][33];  // [warp][element][lane]
     __shared__ float2 state[kTreeMergeWarps][32];
+    const int4 cut = p.cuts[blockIdx.x];
+    const int nparts = cut.w;
+    if (nparts == 0)
+        return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.num_heads / p.num_kv_heads;
     const int all_rows = p.num_draft * G, rows = tc_slot_rows<Units>(all_rows);
     const int lrb = tree_merge_log_rows(rows, D);
     const int RB = 1 << lrb, CB = 32 >> lrb;
-    const int b = blockIdx.x + 1, r0 = blockIdx.y << lrb, col0 = blockIdx.z * (E * CB);
-    const int pairs_per_seq = p.num_kv_heads * p.row_tiles;
-    const TcFind f = tc_find(p, pairs_per_seq, b, ctas);
-    if (f.s >= p.num_seqs)
-        return;
-    const int tiles = tc_tiles(p, f.s);
-    const long long ub = f.bound(b);
-    const int j = static_cast<int>((ub - f.before) / (tiles + kTcPairCost));
-    const long long start = f.before + static_cast<long long>(j) * (tiles + kTcPairCost);
-    const int cut = tc_tiles_below(ub, start, tiles);
-    if (cut == 0 || cut == tiles || tc_tiles_below(f.bound(b - 1), start, tiles) > 0)
-        return;
-    // the CTA of the pair's last tile
-    const long long last_unit = start + kTcPairCost + tiles - 1;
-    const int last = static_cast<int>(((last_unit + 1) * f.parts - 1) / f.total);
-    const int nparts = last - b + 2;
-    const int kvh = j / p.row_tiles, rt = j - kvh * p.row_tiles;
-    const int r = r0 + (lane & (RB - 1));
-    float M = -INFINITY, den = 0.f, num[E];
+    const int r0 = blockIdx.y << lrb;
+    for (int step = 0; step < steps; ++step) {
+        const int col0 = (static_cast<int>(blockIdx.z) * steps + step) * (E * CB);
+        const int r = r0 + (lane & (RB - 1));
+        float M = -INFINITY, den = 0.f, num[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        num[e] = 0.f;
-    if (r < rows) {
-        for (int q = warp; q < nparts; q += kTreeMergeWarps) {
-            // part 0: CTA b - 1, partial 1; part q: CTA b - 1 + q, partial 0
-            const long long slot = q == 0 ? 2LL * (b - 1) + 1 : 2LL * (b - 1 + q);
-            const float2 v = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
-            const float *a = p.part_acc + (slot * D + col0 + (lane >> lrb)) * rows + r;
-            float x[E];
+        for (int e = 0; e < E; ++e)
+            num[e] = 0.f;
+        if (r < rows) {
+            for (int q = warp; q < nparts; q += kTreeMergeWarps) {
+                // part 0: this CTA's partial 1; part q: partial 0 of the q-th CTA after it
+                const long long slot = 2LL * (blockIdx.x + q) + (q == 0);
+                const float2 v = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
+                const float *a = p.part_acc + (slot * D + col0 + (lane >> lrb)) * rows + r;
+                float x[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = a[static_cast<long long>(e * CB) * rows];
-            if (v.y == 0.f)  // it attended nothing there, and left no accumulator
-                continue;
-            const float mn = fmaxf(M, v.x);
-            const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
-            den = den * keep + v.y * add;
+                for (int e = 0; e < E; ++e)
+                    x[e] = a[static_cast<long long>(e * CB) * rows];
+                if (v.y == 0.f)  // it attended nothing there, and left no accumulator
+                    continue;
+                const float mn = fmaxf(M, v.x);
+                const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
+                den = den * keep + v.y * add;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                num[e] = num[e] * keep + x[e] * add;
-            M = mn;
-        }
-    }
-    state[warp][lane] = make_float2(M, den);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        acc[warp][e][lane] = num[e];
-    __syncthreads();
-    // output o of the CTA: row o / (E CB), column o % (E CB)
-    for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
-        const int rr = o / (E * CB), c = o - rr * (E * CB);
-        const int full = rt * Units * 128 + r0 + rr;  // row of the (sequence, kv head)
-        if (r0 + rr >= rows || full >= all_rows)
-            break;
-        const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kTreeMergeWarps; ++w)
-            if (state[w][ln].y != 0.f)
-                m = fmaxf(m, state[w][ln].x);
-        float n = 0.f, d = 0.f;
-#pragma unroll
-        for (int w = 0; w < kTreeMergeWarps; ++w) {
-            const float2 v = state[w][ln];
-            if (v.y != 0.f) {
-                const float sc = v.x == m ? 1.f : exp2f(v.x - m);
-                d = fmaf(v.y, sc, d);
-                n = fmaf(acc[w][e][ln], sc, n);
+                for (int e = 0; e < E; ++e)
+                    num[e] = num[e] * keep + x[e] * add;
+                M = mn;
             }
         }
-        const long long orow =
-            (static_cast<long long>(f.s) * p.num_draft + full / G) * p.num_heads + kvh * G + full % G;
-        store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+        state[warp][lane] = make_float2(M, den);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[warp][e][lane] = num[e];
+        __syncthreads();
+        // output o of the CTA: row o / (E CB), column o % (E CB)
+        for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
+            const int rr = o / (E * CB), c = o - rr * (E * CB);
+            const int full = cut.z * Units * 128 + r0 + rr;  // row of the (sequence, kv head)
+            if (r0 + rr >= rows || full >= all_rows)
+                break;
+            const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kTreeMergeWarps; ++w)
+                if (state[w][ln].y != 0.f)
+                    m = fmaxf(m, state[w][ln].x);
+            float n = 0.f, d = 0.f;
+#pragma unroll
+            for (int w = 0; w < kTreeMergeWarps; ++w) {
+                const float2 v = state[w][ln];
+                if (v.y != 0.f) {
+                    const float sc = v.x == m ? 1.f : exp2f(v.x - m);
+                    d = fmaf(v.y, sc, d);
+                    n = fmaf(acc[w][e][ln], sc, n);
+                }
+            }
+            const long long orow =
+                (static_cast<long long>(cut.x) * p.num_draft + full / G) * p.num_heads + cut.y * G + full % G;
+            store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+        }
+        __syncthreads();
     }
 }
 
