@@ -5,23 +5,31 @@
 // of the C tokens before them the k = budget - recent with the largest
 // scores, of equal scores the lowest index.  A score's order is that of the
 // unsigned image of its bits (sign bit flipped, negatives complemented; -0 as
-// +0, NaN on top).  The k-th largest image is found by a radix search, one
-// byte at a time from the top: a histogram of the next byte over the scores
-// that share the bytes found so far, then the byte whose suffix count passes
-// k.  One ordered pass then writes the kept indices: those above the k-th
-// image, and the first (lowest-index) of those equal to it that are needed.
+// +0, NaN on top).  The k-th largest image is found by a radix search from the
+// top, 11 + 11 + 10 bits: a histogram of the digit over the scores that share
+// the digits found so far, then the digit whose suffix count passes k (2048
+// bins: the first digit holds the exponent and two bits of mantissa, so scores of
+// one magnitude do not all meet in one counter).  One ordered pass then writes
+// the kept indices: the recent ones, those above the k-th image, and the first
+// (lowest-index) of those equal to it that are needed.  A row is shared by the
+// CTAs of a cluster, each holding a slice of it in shared memory (the scores are
+// read from memory once); histograms and counts are exchanged through
+// distributed shared memory.  Few long rows thus use many SMs.
 //
 // Movement.  A row moves to an equal or lower place: place i takes token
-// j >= i.  In place, a CTA owns the same 16-byte columns of every row of a
-// (sequence, kv head) and walks the places upward, a chunk at a time: all
-// loads of a chunk happen before its stores, and a later chunk only reads at
-// or above its own first place, which the stores before it never reach.
-// Into other blocks there is nothing to order, and the rows are split over
-// more CTAs.
+// j >= i.  A warp takes 32 places at a time, one a lane: kept index, both table
+// entries and both addresses are found once a row, then whole rows of K and V
+// go through the warp, addresses by shuffle.  Into other blocks there is nothing
+// to order.  In place, a CTA owns all rows of a (sequence, kv head) of K or of V
+// and walks the places upward, a chunk at a time: all loads of a chunk happen
+// before its stores, and a later chunk only reads at or above its own first
+// place, which the stores before it never reach.
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
 #include "pa_evict.h"
+#include "pa_host.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -65,17 +73,37 @@ __device__ inline uint32_t cta_scan(uint32_t v, uint32_t *warp_sum, uint32_t &to
     return before + x - v;
 }
 
-// grid: (kv heads, sequences)
+constexpr int kSelBins = 2048;
+constexpr int kSelPer = 8;                            // consecutive tokens of a thread in the ordered pass
+constexpr int kSelRound = kSelThreads * kSelPer;      // tokens of a round (below 2^16: packed counts)
+constexpr int kSelMaxSlice = 48 * 1024;               // scores a CTA holds in shared memory
+constexpr int kSelMaxCluster = 8;
+
+struct SelectShared {
+    uint32_t hist[2][kSelBins];
+    uint32_t warp_sum[kSelWarps];
+    uint32_t digit, above;
+    uint32_t count[2];  // of the slice: kept surely, equal to the k-th
+};
+
+// grid: (kv heads x cluster, sequences); a cluster of p.cluster CTAs takes a
+// row.  Cached: the slices are in shared memory.  Otherwise (rows longer than
+// the cluster's shared memory) one CTA reads the row from memory in every pass.
+template <bool Cached>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+    namespace cg = cooperative_groups;
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ uint32_t hist[256];
-    __shared__ uint32_t warp_sum[kSelWarps];
-    __shared__ uint32_t found_byte, found_above;
-    const int s = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+    extern __shared__ __align__(16) char smem[];
+    SelectShared *sh = reinterpret_cast<SelectShared *>(smem);
+    float *slice = reinterpret_cast<float *>(smem + sizeof(SelectShared));
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = Cached ? static_cast<int>(cluster.block_rank()) : 0;
+    const int ranks = Cached ? p.cluster : 1;
+    const int s = blockIdx.y, h = blockIdx.x / ranks, tid = threadIdx.x;
     int L = ld_nc_i32(p.context_lens + s);
     if (L > p.max_len) {
-        if (p.err && tid == 0 && h == 0)
+        if (p.err && tid == 0 && h == 0 && rank == 0)
             atomicOr(p.err, PA_DEVERR_BAD_LEN);
         L = static_cast<int>(p.max_len);
     }
@@ -85,210 +113,357 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const float *in = p.scores + row * p.stride;
     float *out = p.scores_out ? p.scores_out + row * p.stride : nullptr;
     int32_t *keep = p.keep + row * p.budget;
-    if (h == 0 && tid == 0)
+    if (h == 0 && tid == 0 && rank == 0)
         p.new_lens[s] = n;
     const int C = L > p.budget ? L - p.recent : 0;  // candidates
     const int k = L > p.budget ? p.budget - p.recent : 0;
+    // this CTA's tokens [lo, hi)
+    const int per = Cached ? (L + ranks - 1) / ranks : L;
+    const int lo = min(L, rank * per), hi = min(L, lo + per);
+    if (Cached) {
+        if ((reinterpret_cast<uintptr_t>(in + lo) & 15u) == 0) {
+            const int n4 = (hi - lo) / 4;
+            for (int i = tid; i < n4; i += kSelThreads)
+                reinterpret_cast<float4 *>(slice)[i] = reinterpret_cast<const float4 *>(in + lo)[i];
+            for (int i = n4 * 4 + tid; i < hi - lo; i += kSelThreads)
+                slice[i] = in[lo + i];
+        } else {
+            for (int i = tid; i < hi - lo; i += kSelThreads)
+                slice[i] = in[lo + i];
+        }
+    }
+    auto score = [&](int t) -> float { return Cached ? slice[t - lo] : in[t]; };
+
     uint32_t kth = 0, above = 0;  // the k-th largest image, scores above it
     if (k > 0) {
+        const int chi = min(hi, C);
         uint32_t need = k;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelThreads)
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+            const uint32_t high = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
+            const uint32_t digits = pass == 2 ? 1023u : 2047u;
+            uint32_t *hist = sh->hist[pass & 1];
+            for (int i = tid; i < kSelBins; i += kSelThreads)
                 hist[i] = 0;
-            __syncthreads();
-            const uint32_t high = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-            for (int t = tid; t < C; t += kSelThreads) {
-                const uint32_t u = order_of(in[t]);
+            __syncthreads();  // (the slice is loaded, too)
+            for (int t = lo + tid; t < chi; t += kSelThreads) {
+                const uint32_t u = order_of(score(t));
                 if ((u & high) == (kth & high))
-                    atomicAdd(&hist[(u >> shift) & 255], 1u);
+                    atomicAdd(&hist[(u >> shift) & digits], 1u);
+            }
+            if (ranks > 1)
+                cluster.sync();
+            else
+                __syncthreads();
+            // suffix counts over the cluster, 4 bins a thread, from the top
+            uint32_t c[4] = {0, 0, 0, 0};
+            const int top = kSelBins - 1 - 4 * tid;  // thread tid: bins top, top - 1, top - 2, top - 3
+            for (int r = 0; r < ranks; ++r) {
+                const uint32_t *rh = ranks > 1 ? cluster.map_shared_rank(hist, r) : hist;
+                const uint4 v = *reinterpret_cast<const uint4 *>(rh + top - 3);
+                c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
+            }
+            const uint32_t mine = c[0] + c[1] + c[2] + c[3];
+            // (counts up to 2^31: a plain scan, not the packed one)
+            uint32_t x = mine;
+            const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (lane == 31)
+                sh->warp_sum[warp] = x;
+            __syncthreads();
+            uint32_t before = x - mine;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w)
+                before += w < warp ? sh->warp_sum[w] : 0;
+            if (before < need && before + mine >= need) {
+                int b = 0;
+                while (before + c[b] < need)
+                    before += c[b++];
+                sh->digit = static_cast<uint32_t>(top - b);
+                sh->above = before;
             }
             __syncthreads();
-            if (tid < 32) {  // suffix counts of 8 bins a lane, from the top
-                uint32_t mine = 0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mine += hist[255 - tid * 8 - i];
-                uint32_t x = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (tid >= o)
-                        x += y;
-                }
-                uint32_t before = x - mine;
-                if (before < need && x >= need) {
-                    int b = 255 - tid * 8;
-                    while (before + hist[b] < need)
-                        before += hist[b--];
-                    found_byte = static_cast<uint32_t>(b);
-                    found_above = before;
-                }
-            }
-            __syncthreads();
-            kth |= found_byte << shift;
-            above += found_above;
-            need -= found_above;
+            kth |= sh->digit << shift;
+            above += sh->above;
+            need -= sh->above;
             __syncthreads();
         }
     }
     const uint32_t equal = k - above;  // scores equal to the k-th that are kept: the first ones
-    // the ordered pass; a thread takes one token a round.  In place (scores_out
-    // is scores), a score moves to an equal or lower index: a round's loads
-    // come before its stores, and later rounds read higher indices only.
-    uint32_t kept_above = 0, seen_equal = 0;
-    for (int t0 = 0; t0 < C; t0 += kSelThreads) {
-        const int t = t0 + tid;
-        float x = 0.f;
-        uint32_t u = 0;
-        bool gt = false, eq = false;
-        if (t < C) {
-            x = in[t];
-            u = order_of(x);
-            gt = k > 0 && u > kth;
-            eq = k > 0 && u == kth;
+    // a token is kept surely when it is recent (or the context short), or above the k-th
+    auto classify = [&](int t, bool &sure, bool &eq, float &x) {
+        x = 0.f;
+        sure = eq = false;
+        if (t < hi) {
+            x = score(t);
+            const uint32_t u = order_of(x);
+            sure = t >= C || (k > 0 && u > kth);
+            eq = !sure && k > 0 && u == kth;
+        }
+    };
+    uint32_t kept = 0, seen = 0;  // in the slices before this one: kept surely, equal
+    if (ranks > 1) {
+        uint32_t a = 0, e = 0;
+        for (int t = lo + tid; t < hi; t += kSelThreads) {
+            bool sure, eq;
+            float x;
+            classify(t, sure, eq, x);
+            a += sure, e += eq;
+        }
+        if (tid == 0)
+            sh->count[0] = sh->count[1] = 0;
+        __syncthreads();
+        a = __reduce_add_sync(0xffffffffu, a);
+        e = __reduce_add_sync(0xffffffffu, e);
+        if ((tid & 31) == 0) {
+            atomicAdd(&sh->count[0], a);
+            atomicAdd(&sh->count[1], e);
+        }
+        // (also: every slice is in shared memory before any score is written, which may be over them)
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) {
+            const uint32_t *rc = cluster.map_shared_rank(sh->count, r);
+            kept += rc[0];
+            seen += rc[1];
+        }
+    } else {
+        __syncthreads();
+    }
+    // The ordered pass: a thread takes kSelPer consecutive tokens a round.  Without
+    // a cached slice and in place, a score moves to an equal or lower index: a
+    // round's loads come before its stores, and later rounds read higher indices only.
+    for (int t0 = lo; t0 < hi; t0 += kSelRound) {
+        const int t1 = t0 + tid * kSelPer;
+        float x[kSelPer];
+        uint32_t sure_bits = 0, eq_bits = 0;
+#pragma unroll
+        for (int i = 0; i < kSelPer; ++i) {
+            bool sure, eq;
+            classify(t1 + i, sure, eq, x[i]);
+            sure_bits |= (sure ? 1u : 0u) << i;
+            eq_bits |= (eq ? 1u : 0u) << i;
         }
         uint32_t total;
-        const uint32_t pre = cta_scan((gt ? 1u : 0u) | (eq ? 0x10000u : 0u), warp_sum, total);
-        const uint32_t eq_before = seen_equal + (pre >> 16);
-        const uint32_t place = kept_above + (pre & 0xffffu) + min(eq_before, equal);
-        if (gt || (eq && eq_before < equal)) {
-            keep[place] = t;
-            if (out)
-                out[place] = x;
+        const uint32_t pre = cta_scan(__popc(sure_bits) | (__popc(eq_bits) << 16), sh->warp_sum, total);
+        uint32_t place_sure = kept + (pre & 0xffffu), rank_eq = seen + (pre >> 16);
+#pragma unroll
+        for (int i = 0; i < kSelPer; ++i) {
+            const bool sure = (sure_bits >> i) & 1u, eq = (eq_bits >> i) & 1u;
+            if (sure || (eq && rank_eq < equal)) {
+                const uint32_t place = place_sure + min(rank_eq, equal);
+                keep[place] = t1 + i;
+                if (out)
+                    out[place] = x[i];
+            }
+            place_sure += sure;
+            rank_eq += eq;
         }
-        kept_above += total & 0xffffu;
-        seen_equal += total >> 16;
+        kept += total & 0xffffu;
+        seen += total >> 16;
     }
     __syncthreads();
-    // the tokens kept for being recent (or all of a short context)
-    const int from = C, head = k;
-    for (int i0 = 0; i0 < L - from; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        float x = 0.f;
-        if (i < L - from)
-            x = in[from + i];
-        __syncthreads();
-        if (i < L - from) {
-            keep[head + i] = from + i;
-            if (out)
-                out[head + i] = x;
-        }
-    }
-    __syncthreads();
-    for (int i = n + tid; i < p.budget; i += kSelThreads)
+    for (int i = n + rank * kSelThreads + tid; i < p.budget; i += ranks * kSelThreads)
         keep[i] = -1;
     if (out)
-        for (long long i = n + tid; i < p.stride; i += kSelThreads)
+        for (long long i = n + rank * kSelThreads + tid; i < p.stride; i += ranks * kSelThreads)
             out[i] = 0.f;
+    if (ranks > 1)
+        cluster.sync();  // no CTA leaves while another may read its counts
 }
 
 constexpr int kMoveThreads = 256;
+constexpr int kMoveWarps = kMoveThreads / 32;
 constexpr int kMoveUnroll = 4;
 
-// A thread moves one 16-byte column of kMoveUnroll rows a chunk.  grid.x:
-// column segments x row splits, grid.y: kv heads x {K, V}, grid.z: sequences
-// (65535 at a time).
+// The move of place i of (sequence s, kv head h): the 16-byte chunk where the
+// source row starts, and the destination's; -1 when nothing moves.
+struct Move {
+    long long from, to;
+};
 template <bool InPlace>
+__device__ inline Move find_move(const CompactParams &p, int s, int h, int i, int n, long long base, bool report) {
+    Move m = {-1, -1};
+    if (i >= n)
+        return m;
+    const int j = ld_nc_i32(p.keep + (static_cast<long long>(s) * p.keep_heads + (p.keep_heads > 1 ? h : 0)) *
+                                         p.keep_stride + i);
+    const long long src = base + j, dst = base + i;
+    if (j < (InPlace ? i : 0) || base < 0 || src >= static_cast<long long>(p.max_blocks) << p.log_block ||
+        dst >= static_cast<long long>(p.dst_max_blocks) << p.log_block) {
+        if (report)
+            atomicOr(p.err, PA_DEVERR_BAD_INDEX);
+        return m;
+    }
+    if (InPlace && j == i)
+        return m;
+    const int sb = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks + (src >> p.log_block));
+    const int db = ld_nc_i32(p.dst_block_tables + static_cast<long long>(s) * p.dst_max_blocks + (dst >> p.log_block));
+    if (sb < 0 || sb >= p.num_blocks || db < 0 || db >= p.num_blocks) {
+        if (report)
+            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+        return m;
+    }
+    const int mask = (1 << p.log_block) - 1;
+    m.from = ((((static_cast<long long>(sb) * p.num_kv_heads + h) << p.log_block) + (src & mask)) * p.row_chunks);
+    m.to = ((((static_cast<long long>(db) * p.num_kv_heads + h) << p.log_block) + (dst & mask)) * p.row_chunks);
+    return m;
+}
+
+// Into other blocks.  Lpr lanes a row (16 bytes each).  grid.x: 32-row batches
+// (8 a CTA), grid.y: kv heads, grid.z: sequences.
+template <int Lpr>
 __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const CompactParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int s = blockIdx.z;
-    const bool is_v = blockIdx.y >= static_cast<unsigned>(p.num_kv_heads);
-    const int h = static_cast<int>(blockIdx.y) - (is_v ? p.num_kv_heads : 0);
-    const int seg = static_cast<int>(blockIdx.x) % p.segs, split = static_cast<int>(blockIdx.x) / p.segs;
-    const int rows = kMoveThreads / p.seg_chunks;  // rows a pass
-    const int r = threadIdx.x / p.seg_chunks;
-    const int col = seg * p.seg_chunks + threadIdx.x % p.seg_chunks;  // 16-byte column of a row
-    const bool report = p.err && !is_v && seg == 0 && threadIdx.x % p.seg_chunks == 0;
-    uint4 *cache = static_cast<uint4 *>(is_v ? p.v_cache : p.k_cache);
-    const long long max_tok = static_cast<long long>(p.max_blocks) * p.block_size;
-    const long long dst_tok = static_cast<long long>(p.dst_max_blocks) * p.block_size;
+    constexpr int kRows = 32 / Lpr;  // rows of a warp access
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = blockIdx.z, h = blockIdx.y;
     const int n = min(max(ld_nc_i32(p.keep_lens + s), 0), p.keep_stride);
+    const int i0 = (blockIdx.x * kMoveWarps + warp) * 32;
+    if (i0 >= n)
+        return;
     const long long base = p.base_lens ? ld_nc_i32(p.base_lens + s) : 0;
-    const int32_t *keep = p.keep + (static_cast<long long>(s) * p.keep_heads + (p.keep_heads > 1 ? h : 0)) *
-                                       p.keep_stride;
-    const int32_t *src_row = p.block_tables + static_cast<long long>(s) * p.max_blocks;
-    const int32_t *dst_row = p.dst_block_tables + static_cast<long long>(s) * p.dst_max_blocks;
-    // the 16-byte chunk of a token's row in the cache, -1 (flagged) when it has none
-    auto chunk_of = [&](const int32_t *table, long long tok) -> long long {
-        const int blk = static_cast<int>(tok / p.block_size);
-        const int phys = ld_nc_i32(table + blk);
-        if (phys < 0 || phys >= p.num_blocks) {
-            if (report)
-                atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
-            return -1;
-        }
-        const long long tile = static_cast<long long>(phys) * p.num_kv_heads + h;
-        return (tile * p.block_size + (tok - static_cast<long long>(blk) * p.block_size)) * p.row_chunks + col;
-    };
-    const int chunk = rows * kMoveUnroll;
-    for (int i0 = split * chunk; i0 < n; i0 += p.splits * chunk) {
-        uint4 v[kMoveUnroll];
+    const Move m = find_move<false>(p, s, h, i0 + lane, n, base, p.err != nullptr);
+    uint4 *k = static_cast<uint4 *>(p.k_cache), *v = static_cast<uint4 *>(p.v_cache);
+    const int sub = lane / Lpr, col = lane % Lpr;
+#pragma unroll 1
+    for (int r = 0; r < 32; r += kRows * kMoveUnroll) {
+        uint4 kx[kMoveUnroll], vx[kMoveUnroll];
         long long to[kMoveUnroll];
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u) {
-            const int i = i0 + u * rows + r;
-            to[u] = -1;
-            if (r < rows && i < n) {
-                const int j = ld_nc_i32(keep + i);
-                if (j < (InPlace ? i : 0) || base < 0 || base + j >= max_tok || base + i >= dst_tok) {
-                    if (report)
-                        atomicOr(p.err, PA_DEVERR_BAD_INDEX);
-                } else if (!InPlace || j != i) {
-                    const long long from = chunk_of(src_row, base + j);
-                    const long long dst = chunk_of(dst_row, base + i);
-                    if (from >= 0 && dst >= 0) {
-                        v[u] = cache[from];
-                        to[u] = dst;
-                    }
-                }
+            const int rr = r + u * kRows + sub;
+            const long long from = __shfl_sync(0xffffffffu, m.from, rr & 31);
+            to[u] = __shfl_sync(0xffffffffu, m.to, rr & 31);
+            if (rr >= 32 || from < 0)
+                to[u] = -1;
+            if (to[u] >= 0) {
+                kx[u] = k[from + col];
+                vx[u] = v[from + col];
             }
         }
-        if (InPlace)
-            __syncthreads();  // every load of the chunk before its first store
 #pragma unroll
         for (int u = 0; u < kMoveUnroll; ++u)
-            if (to[u] >= 0)
-                cache[to[u]] = v[u];
-        if (InPlace)
-            __syncthreads();  // (the compiler keeps later loads behind this chunk's)
+            if (to[u] >= 0) {
+                k[to[u] + col] = kx[u];
+                v[to[u] + col] = vx[u];
+            }
+    }
+}
+
+// In place.  A CTA takes K or V of a (sequence, kv head), 32 rows a warp and
+// chunk.  grid.x: kv heads, grid.y: {K, V}, grid.z: sequences.
+template <int Lpr>
+__global__ void __launch_bounds__(kMoveThreads) compact_in_place_kernel(const CompactParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    constexpr int kRows = 32 / Lpr;
+    constexpr int kHold = 16;                 // 16-byte pieces a lane holds
+    constexpr int kBatch = kHold * kRows;     // rows of a warp and chunk (at most 32)
+    constexpr int kBatchRows = kBatch < 32 ? kBatch : 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int s = blockIdx.z, h = blockIdx.x;
+    const int n = min(max(ld_nc_i32(p.keep_lens + s), 0), p.keep_stride);
+    const long long base = p.base_lens ? ld_nc_i32(p.base_lens + s) : 0;
+    uint4 *c = static_cast<uint4 *>(blockIdx.y ? p.v_cache : p.k_cache);
+    const int sub = lane / Lpr, col = lane % Lpr;
+    for (int i0 = 0; i0 < n; i0 += kMoveWarps * kBatchRows) {
+        const int i = i0 + warp * kBatchRows + lane;
+        const Move m = lane < kBatchRows ? find_move<true>(p, s, h, i, n, base, p.err && blockIdx.y == 0)
+                                         : Move{-1, -1};
+        uint4 x[kBatchRows / kRows];
+#pragma unroll
+        for (int u = 0; u < kBatchRows / kRows; ++u) {
+            const long long from = __shfl_sync(0xffffffffu, m.from, u * kRows + sub);
+            if (from >= 0)
+                x[u] = c[from + col];
+        }
+        __syncthreads();  // every load of the chunk before its first store
+#pragma unroll
+        for (int u = 0; u < kBatchRows / kRows; ++u) {
+            const long long to = __shfl_sync(0xffffffffu, m.to, u * kRows + sub);
+            if (to >= 0)
+                c[to + col] = x[u];
+        }
+        __syncthreads();  // (later loads stay behind)
     }
 }
 
 }  // namespace
 
-cudaError_t launch_select(SelectParams p, cudaStream_t stream) {
+cudaError_t launch_select(SelectParams p, int num_sms, cudaStream_t stream) {
+    // a cluster a row: enough CTAs that a slice fits shared memory, and (for few
+    // rows) that every SM has one, down to 2048 scores a CTA
+    const long long rows = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
+    int cluster = 1;
+    while (cluster < kSelMaxCluster &&
+           ((p.max_len + cluster - 1) / cluster > kSelMaxSlice ||
+            (rows * cluster < num_sms && (p.max_len + cluster - 1) / cluster > 2048)))
+        cluster *= 2;
+    const bool cached = (p.max_len + cluster - 1) / cluster <= kSelMaxSlice;
+    if (!cached)
+        cluster = 1;
+    p.cluster = cluster;
+    const void *fn = cached ? reinterpret_cast<const void *>(&select_kernel<true>)
+                            : reinterpret_cast<const void *>(&select_kernel<false>);
+    const size_t slice = cached ? static_cast<size_t>((p.max_len + cluster - 1) / cluster + 3) / 4 * 16 : 0;
+    const size_t smem = sizeof(SelectShared) + slice;
+    int dev = 0, sms = 0, per_sm = 0;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e == cudaSuccess)
+        e = prepare_kernel(dev, fn, smem, kSelThreads, &per_sm);
+    if (e != cudaSuccess)
+        return e;
     for (int s0 = 0; s0 < p.num_seqs; s0 += 65535) {
         SelectParams c = p;
         const int n = p.num_seqs - s0 < 65535 ? p.num_seqs - s0 : 65535;
-        const long long rows = static_cast<long long>(s0) * p.num_kv_heads;
+        const long long r0 = static_cast<long long>(s0) * p.num_kv_heads;
         c.context_lens += s0;
         c.new_lens += s0;
-        c.keep += rows * p.budget;
-        c.scores += rows * p.stride;
+        c.keep += r0 * p.budget;
+        c.scores += r0 * p.stride;
         if (c.scores_out)
-            c.scores_out += rows * p.stride;
+            c.scores_out += r0 * p.stride;
         void *args[] = {&c};
-        const cudaError_t e = launch_dependent(reinterpret_cast<const void *>(&select_kernel),
-                                               dim3(p.num_kv_heads, n), dim3(kSelThreads), args, 0, stream);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(p.num_kv_heads * cluster, n);
+        cfg.blockDim = dim3(kSelThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelExC(&cfg, fn, args);
         if (e != cudaSuccess)
             return e;
     }
     return cudaSuccess;
 }
 
-cudaError_t launch_compact(CompactParams p, bool in_place, int num_sms, cudaStream_t stream) {
-    p.seg_chunks = p.row_chunks < 4 ? p.row_chunks : 4;  // 64-byte column segments
-    p.segs = p.row_chunks / p.seg_chunks;
-    p.splits = 1;
-    if (!in_place) {
-        const int chunk = kMoveThreads / p.seg_chunks * kMoveUnroll;
-        p.splits = (p.keep_stride + chunk - 1) / chunk;
-        const long long ctas = static_cast<long long>(p.segs) * p.num_kv_heads * 2 * p.num_seqs;
-        const long long most = (64LL * num_sms + ctas - 1) / ctas;
-        if (p.splits > most)
-            p.splits = static_cast<int>(most);
-    }
+cudaError_t launch_compact(CompactParams p, bool in_place, cudaStream_t stream) {
+    p.log_block = p.block_size == 8 ? 3 : (p.block_size == 16 ? 4 : 5);
+    const void *fn;
+    if (in_place)
+        fn = p.row_chunks == 8    ? reinterpret_cast<const void *>(&compact_in_place_kernel<8>)
+             : p.row_chunks == 16 ? reinterpret_cast<const void *>(&compact_in_place_kernel<16>)
+                                  : reinterpret_cast<const void *>(&compact_in_place_kernel<32>);
+    else
+        fn = p.row_chunks == 8    ? reinterpret_cast<const void *>(&compact_kernel<8>)
+             : p.row_chunks == 16 ? reinterpret_cast<const void *>(&compact_kernel<16>)
+                                  : reinterpret_cast<const void *>(&compact_kernel<32>);
+    const int batches = (p.keep_stride + kMoveWarps * 32 - 1) / (kMoveWarps * 32);
     for (int s0 = 0; s0 < p.num_seqs; s0 += 65535) {
         CompactParams c = p;
         const int n = p.num_seqs - s0 < 65535 ? p.num_seqs - s0 : 65535;
@@ -299,10 +474,8 @@ cudaError_t launch_compact(CompactParams p, bool in_place, int num_sms, cudaStre
         c.block_tables += static_cast<long long>(s0) * p.max_blocks;
         c.dst_block_tables += static_cast<long long>(s0) * p.dst_max_blocks;
         void *args[] = {&c};
-        const void *fn = in_place ? reinterpret_cast<const void *>(&compact_kernel<true>)
-                                  : reinterpret_cast<const void *>(&compact_kernel<false>);
-        const cudaError_t e = launch_dependent(fn, dim3(p.segs * p.splits, 2 * p.num_kv_heads, n), dim3(kMoveThreads),
-                                               args, 0, stream);
+        const dim3 grid = in_place ? dim3(p.num_kv_heads, 2, n) : dim3(batches, p.num_kv_heads, n);
+        const cudaError_t e = launch_dependent(fn, grid, dim3(kMoveThreads), args, 0, stream);
         if (e != cudaSuccess)
             return e;
     }

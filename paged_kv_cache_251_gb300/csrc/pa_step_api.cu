@@ -441,7 +441,11 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores_out, c
     p.num_kv_heads = num_kv_heads;
     p.budget = budget;
     p.recent = recent;
-    const cudaError_t e = launch_select(p, stream_of(stream));
+    int dev = 0, sms = 0;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e != cudaSuccess)
+        return cuda_fail(e, "device query");
+    e = launch_select(p, sms, stream_of(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "select launch");
 }
 
@@ -464,7 +468,7 @@ pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep, const
         return fail(PA_ERR_INVALID_ARGUMENT, "unknown dtype");
     if (dst_block_tables && dst_max_blocks_per_seq <= 0)
         return fail(PA_ERR_INVALID_ARGUMENT, "dst_max_blocks_per_seq must be positive");
-    if (num_kv_heads > 32767)
+    if (num_kv_heads > 65535)
         return fail(PA_ERR_UNSUPPORTED, "num_kv_heads too large");
     if (num_seqs == 0 || keep_stride == 0)
         return PA_OK;
@@ -491,11 +495,7 @@ pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep, const
     p.dst_max_blocks = in_place ? max_blocks_per_seq : dst_max_blocks_per_seq;
     p.num_blocks = num_blocks;
     p.row_chunks = head_dim * elt_bytes(dtype) / 16;
-    int dev = 0, sms = 0;
-    cudaError_t e = device_sms(&dev, &sms);
-    if (e != cudaSuccess)
-        return cuda_fail(e, "device query");
-    e = launch_compact(p, in_place, sms, stream_of(stream));
+    const cudaError_t e = launch_compact(p, in_place, stream_of(stream));
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "compact launch");
 }
 

@@ -180,6 +180,26 @@ def test_select(case, kind, in_place):
     assert torch.equal(torch.nan_to_num(got, nan=1.5), torch.nan_to_num(s_ref, nan=1.5))
 
 
+@pytest.mark.parametrize("L", [3000, 70001, 400003])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_select_over_slices(L, in_place):
+    """Rows shared by several CTAs, and one beyond what they hold: many ties around
+    the cut, against a stable sort."""
+    from paged_kv_cache_251_gb300 import pa
+    K, budget, recent = 2, L // 3, 17
+    sc = (wl.normal_tensor(L, 3, (1, K, L)).abs() * 8).round() / 8
+    dev = sc.cuda()
+    out = dev if in_place else torch.full_like(dev, 9.0)
+    keep = torch.empty((1, K, budget), dtype=torch.int32, device="cuda")
+    new = torch.empty(1, dtype=torch.int32, device="cuda")
+    pa.pa_evict_select(keep, new, out, dev, torch.tensor([L], dtype=torch.int32, device="cuda"), budget, recent)
+    for h in range(K):
+        order = torch.sort(sc[0, h, :L - recent], descending=True, stable=True).indices[:budget - recent]
+        want = torch.cat([order.sort().values, torch.arange(L - recent, L)])
+        assert torch.equal(keep[0, h].cpu().long(), want)
+        assert torch.equal(out[0, h, :budget].cpu(), sc[0, h, want]) and (out[0, h, budget:] == 0).all()
+
+
 def test_select_clamps_long_contexts_and_writes_no_scores_when_asked():
     from paged_kv_cache_251_gb300 import pa
     sc = torch.rand((2, 2, 50), device="cuda")
