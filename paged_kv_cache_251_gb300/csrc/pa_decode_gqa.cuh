@@ -764,6 +764,9 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
         for (int h = 0; h < G; ++h)
             m_run[h] = -INFINITY, l_run[h] = 0.f;
 
+        // (Log) the scores of the item's first head
+        float *logit_row =
+            Log ? p.logits + (static_cast<long long>(it.s) * p.num_heads + it.kvh * G) * p.logits_stride : nullptr;
         for (int ti = 0; ti < ntiles; ++ti, ++g) {
             const uint32_t t = static_cast<uint32_t>(it.t_first + ti);
             const int stage = static_cast<int>(t % S);
@@ -794,7 +797,7 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
                 const float x = valid ? sc[h] * p.scale_log2 : -INFINITY;
                 if constexpr (Log) {
                     if (tok >= it.tok_lo && tok < it.tok_hi)
-                        store_logit(p, static_cast<long long>(it.s) * p.num_heads + it.kvh * G + h, tok, x);
+                        logit_row[h * p.logits_stride + tok] = x;
                 }
                 float mt = x;
 #pragma unroll

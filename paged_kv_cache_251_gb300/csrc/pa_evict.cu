@@ -74,13 +74,13 @@ __device__ inline uint32_t cta_scan(uint32_t v, uint32_t *warp_sum, uint32_t &to
 }
 
 constexpr int kSelBins = 2048;
-constexpr int kSelPer = 8;                            // consecutive tokens of a thread in the ordered pass
-constexpr int kSelRound = kSelThreads * kSelPer;      // tokens of a round (below 2^16: packed counts)
-constexpr int kSelMaxSlice = 48 * 1024;               // scores a CTA holds in shared memory
+constexpr int kSelPer = 4;                        // consecutive tokens of a thread in the ordered pass
+constexpr int kSelRound = kSelThreads * kSelPer;  // tokens of a round (below 2^16: packed counts)
+constexpr int kSelMaxSlice = 48 * 1024;           // scores a CTA holds in shared memory
 constexpr int kSelMaxCluster = 8;
 
 struct SelectShared {
-    uint32_t hist[2][kSelBins];
+    uint32_t hist[2][kSelBins];  // later a round's kept tokens and their scores
     uint32_t warp_sum[kSelWarps];
     uint32_t digit, above;
     uint32_t count[2];  // of the slice: kept surely, equal to the k-th
@@ -235,9 +235,13 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     } else {
         __syncthreads();
     }
-    // The ordered pass: a thread takes kSelPer consecutive tokens a round.  Without
-    // a cached slice and in place, a score moves to an equal or lower index: a
-    // round's loads come before its stores, and later rounds read higher indices only.
+    // The ordered pass: a thread takes kSelPer consecutive tokens a round; a round's
+    // kept tokens meet in shared memory and leave as whole lines.  Without a cached
+    // slice and in place, a score moves to an equal or lower index: a round's loads
+    // come before its stores, and later rounds read higher indices only.
+    static_assert(kSelRound <= kSelBins, "a round's kept tokens fit a histogram");
+    uint32_t *kept_tok = sh->hist[0];
+    float *kept_score = reinterpret_cast<float *>(sh->hist[1]);
     for (int t0 = lo; t0 < hi; t0 += kSelRound) {
         const int t1 = t0 + tid * kSelPer;
         float x[kSelPer];
@@ -251,21 +255,29 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
         uint32_t total;
         const uint32_t pre = cta_scan(__popc(sure_bits) | (__popc(eq_bits) << 16), sh->warp_sum, total);
+        const uint32_t base = kept + min(seen, equal);  // the round's first place
         uint32_t place_sure = kept + (pre & 0xffffu), rank_eq = seen + (pre >> 16);
 #pragma unroll
         for (int i = 0; i < kSelPer; ++i) {
             const bool sure = (sure_bits >> i) & 1u, eq = (eq_bits >> i) & 1u;
             if (sure || (eq && rank_eq < equal)) {
-                const uint32_t place = place_sure + min(rank_eq, equal);
-                keep[place] = t1 + i;
-                if (out)
-                    out[place] = x[i];
+                const uint32_t at = place_sure + min(rank_eq, equal) - base;
+                kept_tok[at] = static_cast<uint32_t>(t1 + i);
+                kept_score[at] = x[i];
             }
             place_sure += sure;
             rank_eq += eq;
         }
         kept += total & 0xffffu;
         seen += total >> 16;
+        __syncthreads();
+        const uint32_t count = kept + min(seen, equal) - base;
+        for (uint32_t i = tid; i < count; i += kSelThreads) {
+            keep[base + i] = static_cast<int32_t>(kept_tok[i]);
+            if (out)
+                out[base + i] = kept_score[i];
+        }
+        // (the next round writes here after the barriers of its scan)
     }
     __syncthreads();
     for (int i = n + rank * kSelThreads + tid; i < p.budget; i += ranks * kSelThreads)

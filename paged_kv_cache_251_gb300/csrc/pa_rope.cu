@@ -10,11 +10,11 @@
 //
 // The rows are read once and written once: HBM-bound, or launch-bound for a
 // decode step.  A CTA takes `tok` tokens.  It first forms their rot / 2
-// (cos, sin) pairs once, in shared memory (every head of a token shares
-// them), then its threads are x lanes by y rows: lane x of a row holds the
-// same E elements of both halves (or E adjacent ones, interleaved) of every
-// row it takes, so its angles of a token stay in registers while it walks the
-// rows.
+// (cos, sin) pairs once, in shared memory (every head of a token shares them).
+// Its threads are x lanes by y rows: lane x of a row holds E elements of both
+// halves (or E adjacent ones, interleaved), or E of the elements past rot.  They
+// walk the CTA's rows (every token's q, k and v rows in order) y at a time,
+// kRopeUnroll rows' loads before the first is used.
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
@@ -65,49 +65,72 @@ template <int E, bool Inter> struct RopeUnit {
     static constexpr int kPairs = Inter ? (E == 1 ? 1 : E / 2) : E;  // pairs of a pair lane
 };
 
-template <typename T, int E, bool Inter>
-__device__ inline void rotate_unit(const T *src, T *dst, int x, int half, const float *c, const float *s) {
-    constexpr int P = RopeUnit<E, Inter>::kPairs;
-    if constexpr (!Inter) {
-        Vec<T, E> a, b;
-        a.load(src + x * E);
-        b.load(src + half + x * E);
-        float fa[E], fb[E], ya[E], yb[E];
-        a.get(fa);
-        b.get(fb);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            ya[i] = fa[i] * c[i] - fb[i] * s[i];
-            yb[i] = fb[i] * c[i] + fa[i] * s[i];
+constexpr int kRopeUnroll = 4;
+
+// A lane's share of a row, loaded; its rotation or copy, stored.
+template <typename T, int E, bool Inter> struct RowUnit {
+    Vec<T, E> a, b;  // b: half layout, the second half's elements; interleaved with E == 1, the odd element
+    __device__ inline void load(const T *src, int x, int half, bool pair, int copy_at) {
+        if (!pair) {
+            a.load(src + copy_at);
+        } else if constexpr (!Inter) {
+            a.load(src + x * E);
+            b.load(src + half + x * E);
+        } else if constexpr (E == 1) {
+            a.load(src + 2 * x);
+            b.load(src + 2 * x + 1);
+        } else {
+            a.load(src + x * E);
         }
-        a.set(ya);
-        b.set(yb);
-        a.store(dst + x * E);
-        b.store(dst + half + x * E);
-    } else if constexpr (E == 1) {
-        const float a = load_f(src + 2 * x), b = load_f(src + 2 * x + 1);
-        store_f(dst + 2 * x, a * c[0] - b * s[0]);
-        store_f(dst + 2 * x + 1, b * c[0] + a * s[0]);
-    } else {
-        Vec<T, E> a;
-        a.load(src + x * E);
-        float f[E], y[E];
-        a.get(f);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            y[2 * i] = f[2 * i] * c[i] - f[2 * i + 1] * s[i];
-            y[2 * i + 1] = f[2 * i + 1] * c[i] + f[2 * i] * s[i];
-        }
-        a.set(y);
-        a.store(dst + x * E);
     }
-}
+    __device__ inline void store(T *dst, int x, int half, bool pair, int copy_at) const {
+        if (!pair) {
+            a.store(dst + copy_at);
+        } else if constexpr (!Inter) {
+            a.store(dst + x * E);
+            b.store(dst + half + x * E);
+        } else if constexpr (E == 1) {
+            a.store(dst + 2 * x);
+            b.store(dst + 2 * x + 1);
+        } else {
+            a.store(dst + x * E);
+        }
+    }
+    // trig: (cos, sin) of the unit's pairs
+    __device__ inline void rotate(const float2 *trig) {
+        constexpr int P = RopeUnit<E, Inter>::kPairs;
+        if constexpr (!Inter || E == 1) {
+            float fa[E], fb[E], ya[E], yb[E];
+            a.get(fa);
+            b.get(fb);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 cs = trig[i];
+                ya[i] = fa[i] * cs.x - fb[i] * cs.y;
+                yb[i] = fb[i] * cs.x + fa[i] * cs.y;
+            }
+            a.set(ya);
+            b.set(yb);
+        } else {
+            float f[E], y[E];
+            a.get(f);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 cs = trig[i];
+                y[2 * i] = f[2 * i] * cs.x - f[2 * i + 1] * cs.y;
+                y[2 * i + 1] = f[2 * i + 1] * cs.x + f[2 * i] * cs.y;
+            }
+            a.set(y);
+        }
+    }
+};
 
 template <typename T, int E, bool Inter>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
     constexpr int P = RopeUnit<E, Inter>::kPairs;
     pdl_launch_dependents();
-    extern __shared__ float2 trig[];  // [tok][rot / 2]
+    extern __shared__ __align__(16) float2 trig[];  // [tok][rot / 2]
+    __shared__ long long place[kRopeMaxTok];        // cache element of a token's first kv head; -1: not appended
     pdl_wait();
     const int half = p.rot / 2;
     const long long tok0 = static_cast<long long>(blockIdx.x) * p.tok;
@@ -125,6 +148,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
                   &cs);
         trig[i] = make_float2(cs * p.mscale, sn * p.mscale);
     }
+    const long long step = static_cast<long long>(p.block_size) * p.head_dim;  // kv head to kv head
+    if (p.num_kv_heads && threadIdx.x < ntok) {
+        const long long slot = p.slots[tok0 + threadIdx.x];
+        long long at = -1;
+        if (slot >= static_cast<long long>(p.num_blocks) * p.block_size) {
+            if (p.err)
+                atomicOr(p.err, PA_DEVERR_BAD_SLOT);
+        } else if (slot >= 0) {
+            const long long phys = slot / p.block_size;
+            at = phys * p.num_kv_heads * step + (slot - phys * p.block_size) * p.head_dim;
+        }
+        place[threadIdx.x] = at;
+    }
     __syncthreads();
     const int pair_lanes = half / P;
     const int lanes = pair_lanes + (p.head_dim - p.rot) / E;  // lanes of a row
@@ -135,56 +171,50 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
         return;
     const bool pair = x < pair_lanes;
     const int copy_at = pair ? 0 : p.rot + (x - pair_lanes) * E;
-    const T *qg = static_cast<const T *>(p.q), *kg = static_cast<const T *>(p.k), *vg = static_cast<const T *>(p.v);
-    T *qo = static_cast<T *>(p.q_out), *kc = static_cast<T *>(p.k_cache), *vc = static_cast<T *>(p.v_cache);
-    const long long pool_slots = static_cast<long long>(p.num_blocks) * p.block_size;
-    for (int t = 0; t < ntok; ++t) {
-        const long long tok = tok0 + t;
-        float c[P], s[P];
-        if (pair) {
+    const int per_tok = p.num_heads + 2 * p.num_kv_heads;  // rows of a token: q, k, v
+    // the thread's next row: r of token t
+    int t = 0, r = y;
+    while (r >= per_tok && t < ntok)
+        r -= per_tok, ++t;
+    while (t < ntok) {
+        RowUnit<T, E, Inter> unit[kRopeUnroll];
+        T *dst[kRopeUnroll];
+        int turn[kRopeUnroll];  // token to rotate by, -1: a copy
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float2 cs = trig[t * half + x * P + i];
-                c[i] = cs.x, s[i] = cs.y;
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            dst[u] = nullptr;
+            turn[u] = -1;
+            if (t < ntok) {
+                const long long tok = tok0 + t;
+                const T *src;
+                if (r < p.num_heads) {
+                    src = static_cast<const T *>(p.q) + tok * p.q_stride + r * p.head_dim;
+                    dst[u] = static_cast<T *>(p.q_out) + tok * p.q_out_stride + r * p.head_dim;
+                    turn[u] = t;
+                } else {
+                    const bool is_v = r >= p.num_heads + p.num_kv_heads;
+                    const int h = r - p.num_heads - (is_v ? p.num_kv_heads : 0);
+                    src = (is_v ? static_cast<const T *>(p.v) + tok * p.v_stride
+                                : static_cast<const T *>(p.k) + tok * p.k_stride) +
+                          h * p.head_dim;
+                    const long long at = place[t];
+                    if (at >= 0)
+                        dst[u] = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + at + h * step;
+                    turn[u] = is_v ? -1 : t;
+                }
+                if (dst[u])
+                    unit[u].load(src, x, half, pair, copy_at);
+                r += rows_at_once;
+                while (r >= per_tok && t < ntok)
+                    r -= per_tok, ++t;
             }
         }
-        auto move = [&](const T *src, T *dst) {
-            if (pair) {
-                rotate_unit<T, E, Inter>(src, dst, x, half, c, s);
-            } else {
-                Vec<T, E> v;
-                v.load(src + copy_at);
-                v.store(dst + copy_at);
-            }
-        };
-#pragma unroll 2
-        for (int h = y; h < p.num_heads; h += rows_at_once)
-            move(qg + tok * p.q_stride + h * p.head_dim, qo + tok * p.q_out_stride + h * p.head_dim);
-        if (p.num_kv_heads == 0)
-            continue;
-        const long long slot = p.slots[tok];
-        if (slot < 0)
-            continue;  // padding
-        if (slot >= pool_slots) {
-            if (p.err && threadIdx.x == 0)
-                atomicOr(p.err, PA_DEVERR_BAD_SLOT);
-            continue;
-        }
-        const long long phys = slot / p.block_size;
-        const long long off = slot - phys * p.block_size;
-        const long long step = static_cast<long long>(p.block_size) * p.head_dim;  // kv head to kv head
-        const long long at = phys * p.num_kv_heads * step + off * p.head_dim;
-#pragma unroll 2
-        for (int h = y; h < p.num_kv_heads; h += rows_at_once)
-            move(kg + tok * p.k_stride + h * p.head_dim, kc + at + h * step);
-#pragma unroll 2
-        for (int h = y; h < p.num_kv_heads; h += rows_at_once) {
-            const T *src = vg + tok * p.v_stride + h * p.head_dim;
-            T *dst = vc + at + h * step;
-            for (int e = x * E; e < p.head_dim; e += lanes * E) {
-                Vec<T, E> v;
-                v.load(src + e);
-                v.store(dst + e);
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+            if (dst[u]) {
+                if (pair && turn[u] >= 0)
+                    unit[u].rotate(trig + turn[u] * half + x * P);
+                unit[u].store(dst[u], x, half, pair, copy_at);
             }
         }
     }

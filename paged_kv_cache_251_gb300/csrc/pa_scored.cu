@@ -17,57 +17,93 @@ namespace pa {
 namespace {
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreTokens = 1024;  // tokens of a CTA
-constexpr int kMaxGroup = 8;
+constexpr int kScorePer = 4;                                // tokens of a thread
+constexpr int kScoreTokens = kScoreThreads * kScorePer;     // tokens of a CTA
 
-// grid: (token chunks, kv heads, sequences)
+// grid: (token chunks, kv heads, sequences).  The scores' loads go out before
+// the row states are formed (two round trips in all: the length, then the rest).
+template <int G>
 __global__ void __launch_bounds__(kScoreThreads) score_kernel(const DecodeParams p, const float *in, float *out,
                                                               long long stride) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ float top[kMaxGroup], inv[kMaxGroup];
+    __shared__ float top[G], inv[G];
     const int s = blockIdx.z, kvh = blockIdx.y;
-    const int G = p.num_heads / p.num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const SeqSpan sp = seq_span(ld_nc_i32(p.context_lens + s), p.max_len, 0, p.block_size, p.bpp);
-    const int t0 = blockIdx.x * kScoreTokens;
-    if (t0 >= sp.end)
+    const int t = blockIdx.x * kScoreTokens + threadIdx.x * kScorePer;
+    if (blockIdx.x * kScoreTokens >= sp.end)
         return;
     const long long row0 = static_cast<long long>(s) * p.num_heads + static_cast<long long>(kvh) * G;
+    // (rows of scores are whole blocks, so four at a time stay inside and aligned)
+    const float *x = p.logits + row0 * p.logits_stride + t;
+    const long long at = (static_cast<long long>(s) * p.num_kv_heads + kvh) * stride + t;
+    const int n = min(kScorePer, sp.end - t);
+    float4 v[G];
+    float w[kScorePer] = {0.f, 0.f, 0.f, 0.f}, base[kScorePer] = {0.f, 0.f, 0.f, 0.f};
+    if (n > 0) {
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+            v[g] = *reinterpret_cast<const float4 *>(x + g * p.logits_stride);
+        if (in) {
+            if (n == kScorePer && (reinterpret_cast<uintptr_t>(in + at) & 15u) == 0) {
+                const float4 b = *reinterpret_cast<const float4 *>(in + at);
+                base[0] = b.x, base[1] = b.y, base[2] = b.z, base[3] = b.w;
+            } else {
+                for (int i = 0; i < n; ++i)
+                    base[i] = in[at + i];
+            }
+        }
+    }
     if (warp < G) {
         const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml) + (row0 + warp) * p.max_parts;
-        float m = -INFINITY;
-        for (int q = lane; q < sp.nparts; q += 32)
-            m = fmaxf(m, ml[q].x);
+        float m = -INFINITY, den = 0.f;
+        for (int q = lane; q < sp.nparts; q += 32) {
+            const float2 a = ml[q];
+            if (a.x == -INFINITY && a.y == 0.f)
+                continue;
+            const float mn = fmaxf(m, a.x);
+            den = (m == -INFINITY ? 0.f : den * exp2f(m - mn)) + a.y * exp2f(a.x - mn);
+            m = mn;
+        }
+        float M = m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float den = 0.f;
-        for (int q = lane; q < sp.nparts; q += 32) {
-            const float2 v = ml[q];
-            den += v.x == -INFINITY ? 0.f : v.y * exp2f(v.x - m);
-        }
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        den = m == -INFINITY ? den : den * exp2f(m - M);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             den += __shfl_xor_sync(0xffffffffu, den, o);
         if (lane == 0) {
-            top[warp] = m == -INFINITY ? 0.f : m;
+            top[warp] = M == -INFINITY ? 0.f : M;
             inv[warp] = den == 0.f ? 0.f : 1.f / den;
         }
     }
     __syncthreads();
-    const float *x = p.logits + row0 * p.logits_stride;
-    const long long at = (static_cast<long long>(s) * p.num_kv_heads + kvh) * stride;
+    if (n <= 0)
+        return;
 #pragma unroll
-    for (int i = 0; i < kScoreTokens / kScoreThreads; ++i) {
-        const int t = t0 + i * kScoreThreads + threadIdx.x;
-        if (t < sp.end) {
-            float w = 0.f;
-            for (int g = 0; g < G; ++g)
-                w += exp2f(x[g * p.logits_stride + t] - top[g]) * inv[g];
-            out[at + t] = in ? in[at + t] + w : w;
-        }
+    for (int g = 0; g < G; ++g) {
+        const float m = top[g], r = inv[g];
+        w[0] += exp2f(v[g].x - m) * r;
+        w[1] += exp2f(v[g].y - m) * r;
+        w[2] += exp2f(v[g].z - m) * r;
+        w[3] += exp2f(v[g].w - m) * r;
     }
+    if (n == kScorePer && (reinterpret_cast<uintptr_t>(out + at) & 15u) == 0) {
+        *reinterpret_cast<float4 *>(out + at) =
+            make_float4(base[0] + w[0], base[1] + w[1], base[2] + w[2], base[3] + w[3]);
+    } else {
+        for (int i = 0; i < n; ++i)
+            out[at + i] = base[i] + w[i];
+    }
+}
+
+const void *score_fn(int G) {
+    return G == 1   ? reinterpret_cast<const void *>(&score_kernel<1>)
+           : G == 2 ? reinterpret_cast<const void *>(&score_kernel<2>)
+           : G == 4 ? reinterpret_cast<const void *>(&score_kernel<4>)
+                    : reinterpret_cast<const void *>(&score_kernel<8>);
 }
 
 }  // namespace
@@ -86,7 +122,7 @@ cudaError_t launch_scores(DecodeParams &p, const float *in, float *out, long lon
         const float *ci = in ? in + at : nullptr;
         float *co = out + at;
         void *args[] = {&c, &ci, &co, &stride};
-        const cudaError_t e = launch_dependent(reinterpret_cast<const void *>(&score_kernel),
+        const cudaError_t e = launch_dependent(score_fn(p.num_heads / p.num_kv_heads),
                                                dim3(chunks, p.num_kv_heads, n), dim3(kScoreThreads), args, 0, stream);
         if (e != cudaSuccess)
             return e;
