@@ -48,40 +48,16 @@ __device__ inline uint32_t order_of(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Exclusive prefix of `v` over the CTA (two packed 16-bit counts), and the total.
-__device__ inline uint32_t cta_scan(uint32_t v, uint32_t *warp_sum, uint32_t &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o)
-            x += y;
-    }
-    __syncthreads();  // the sums of the scan before are read
-    if (lane == 31)
-        warp_sum[warp] = x;
-    __syncthreads();
-    uint32_t before = 0;
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        const uint32_t t = warp_sum[w];
-        before += w < warp ? t : 0;
-        total += t;
-    }
-    return before + x - v;
-}
-
 constexpr int kSelBins = 2048;
-constexpr int kSelPer = 4;                        // consecutive tokens of a thread in the ordered pass
-constexpr int kSelRound = kSelThreads * kSelPer;  // tokens of a round (below 2^16: packed counts)
+constexpr int kSelPer = 8;                        // tokens of a thread and round of the ordered pass
+constexpr int kSelRound = kSelThreads * kSelPer;  // tokens of a round: 256 consecutive ones a warp
 constexpr int kSelMaxSlice = 48 * 1024;           // scores a CTA holds in shared memory
 constexpr int kSelMaxCluster = 8;
 
 struct SelectShared {
-    uint32_t hist[2][kSelBins];  // later a round's kept tokens and their scores
+    uint32_t hist[2][kSelBins];
     uint32_t warp_sum[kSelWarps];
+    uint32_t warp_count[2][kSelWarps];  // by round parity: kept surely | equal << 16
     uint32_t digit, above;
     uint32_t count[2];  // of the slice: kept surely, equal to the k-th
 };
@@ -147,6 +123,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             for (int i = tid; i < kSelBins; i += kSelThreads)
                 hist[i] = 0;
             __syncthreads();  // (the slice is loaded, too)
+#pragma unroll 4
             for (int t = lo + tid; t < chi; t += kSelThreads) {
                 const uint32_t u = order_of(score(t));
                 if ((u & high) == (kth & high))
@@ -159,11 +136,17 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             // suffix counts over the cluster, 4 bins a thread, from the top
             uint32_t c[4] = {0, 0, 0, 0};
             const int top = kSelBins - 1 - 4 * tid;  // thread tid: bins top, top - 1, top - 2, top - 3
-            for (int r = 0; r < ranks; ++r) {
-                const uint32_t *rh = ranks > 1 ? cluster.map_shared_rank(hist, r) : hist;
-                const uint4 v = *reinterpret_cast<const uint4 *>(rh + top - 3);
-                c[0] += v.w, c[1] += v.z, c[2] += v.y, c[3] += v.x;
-            }
+            uint4 v[kSelMaxCluster];  // (all loads before the first sum)
+#pragma unroll
+            for (int r = 0; r < kSelMaxCluster; ++r)
+                if (r < ranks) {
+                    const uint32_t *rh = ranks > 1 ? cluster.map_shared_rank(hist, r) : hist;
+                    v[r] = *reinterpret_cast<const uint4 *>(rh + top - 3);
+                }
+#pragma unroll
+            for (int r = 0; r < kSelMaxCluster; ++r)
+                if (r < ranks)
+                    c[0] += v[r].w, c[1] += v[r].z, c[2] += v[r].y, c[3] += v[r].x;
             const uint32_t mine = c[0] + c[1] + c[2] + c[3];
             // (counts up to 2^31: a plain scan, not the packed one)
             uint32_t x = mine;
@@ -207,9 +190,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             eq = !sure && k > 0 && u == kth;
         }
     };
-    uint32_t kept = 0, seen = 0;  // in the slices before this one: kept surely, equal
+    const int lane = tid & 31, warp = tid >> 5;
+    uint32_t kept = 0, seen = 0;  // in the tokens before: kept surely, equal
     if (ranks > 1) {
         uint32_t a = 0, e = 0;
+#pragma unroll 4
         for (int t = lo + tid; t < hi; t += kSelThreads) {
             bool sure, eq;
             float x;
@@ -221,7 +206,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         __syncthreads();
         a = __reduce_add_sync(0xffffffffu, a);
         e = __reduce_add_sync(0xffffffffu, e);
-        if ((tid & 31) == 0) {
+        if (lane == 0) {
             atomicAdd(&sh->count[0], a);
             atomicAdd(&sh->count[1], e);
         }
@@ -235,49 +220,49 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     } else {
         __syncthreads();
     }
-    // The ordered pass: a thread takes kSelPer consecutive tokens a round; a round's
-    // kept tokens meet in shared memory and leave as whole lines.  Without a cached
-    // slice and in place, a score moves to an equal or lower index: a round's loads
-    // come before its stores, and later rounds read higher indices only.
-    static_assert(kSelRound <= kSelBins, "a round's kept tokens fit a histogram");
-    uint32_t *kept_tok = sh->hist[0];
-    float *kept_score = reinterpret_cast<float *>(sh->hist[1]);
-    for (int t0 = lo; t0 < hi; t0 += kSelRound) {
-        const int t1 = t0 + tid * kSelPer;
+    // The ordered pass: a warp takes 256 consecutive tokens a round, a lane every
+    // 32nd of them, so that places follow from ballots and the kept tokens of a
+    // step go to adjacent places.  One barrier a round: the loads (and counts) of a
+    // round come before it, its stores after it.  Without a cached slice and in
+    // place, a score moves to an equal or lower index, and later rounds read higher
+    // indices only.
+    for (int t0 = lo, round = 0; t0 < hi; t0 += kSelRound, ++round) {
+        const int t1 = t0 + warp * (32 * kSelPer) + lane;
         float x[kSelPer];
-        uint32_t sure_bits = 0, eq_bits = 0;
+        uint32_t sure_bits = 0, eq_bits = 0, mine = 0;
 #pragma unroll
         for (int i = 0; i < kSelPer; ++i) {
             bool sure, eq;
-            classify(t1 + i, sure, eq, x[i]);
+            classify(t1 + 32 * i, sure, eq, x[i]);
             sure_bits |= (sure ? 1u : 0u) << i;
             eq_bits |= (eq ? 1u : 0u) << i;
         }
-        uint32_t total;
-        const uint32_t pre = cta_scan(__popc(sure_bits) | (__popc(eq_bits) << 16), sh->warp_sum, total);
-        const uint32_t base = kept + min(seen, equal);  // the round's first place
-        uint32_t place_sure = kept + (pre & 0xffffu), rank_eq = seen + (pre >> 16);
+        mine = __reduce_add_sync(0xffffffffu, __popc(sure_bits) | (__popc(eq_bits) << 16));
+        uint32_t *count = sh->warp_count[round & 1];
+        if (lane == 0)
+            count[warp] = mine;
+        __syncthreads();
+        const uint32_t c = lane < kSelWarps ? count[lane] : 0;
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
+        const uint32_t total = __reduce_add_sync(0xffffffffu, c);
+        uint32_t place_sure = kept + (before & 0xffffu), rank_eq = seen + (before >> 16);
 #pragma unroll
         for (int i = 0; i < kSelPer; ++i) {
             const bool sure = (sure_bits >> i) & 1u, eq = (eq_bits >> i) & 1u;
-            if (sure || (eq && rank_eq < equal)) {
-                const uint32_t at = place_sure + min(rank_eq, equal) - base;
-                kept_tok[at] = static_cast<uint32_t>(t1 + i);
-                kept_score[at] = x[i];
+            const uint32_t sures = __ballot_sync(0xffffffffu, sure), eqs = __ballot_sync(0xffffffffu, eq);
+            const uint32_t below = (1u << lane) - 1u;
+            const uint32_t my_eq = rank_eq + __popc(eqs & below);
+            if (sure || (eq && my_eq < equal)) {
+                const uint32_t place = place_sure + __popc(sures & below) + min(my_eq, equal);
+                keep[place] = t1 + 32 * i;
+                if (out)
+                    out[place] = x[i];
             }
-            place_sure += sure;
-            rank_eq += eq;
+            place_sure += __popc(sures);
+            rank_eq += __popc(eqs);
         }
         kept += total & 0xffffu;
         seen += total >> 16;
-        __syncthreads();
-        const uint32_t count = kept + min(seen, equal) - base;
-        for (uint32_t i = tid; i < count; i += kSelThreads) {
-            keep[base + i] = static_cast<int32_t>(kept_tok[i]);
-            if (out)
-                out[base + i] = kept_score[i];
-        }
-        // (the next round writes here after the barriers of its scan)
     }
     __syncthreads();
     for (int i = n + rank * kSelThreads + tid; i < p.budget; i += ranks * kSelThreads)
