@@ -39,13 +39,12 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 
-__device__ inline uint32_t order_of(float x) {
-    const uint32_t u = __float_as_uint(x);
-    if ((u & 0x7fffffffu) > 0x7f800000u)
-        return 0xffffffffu;  // NaN
-    if (u == 0x80000000u)
-        return 0x80000000u;  // -0 as +0
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+// A score as it is compared and written: -0 as +0, any NaN as the one whose bits
+// are largest.  Its order is then that of the image below.
+__device__ inline float canonical(float x) { return x != x ? __int_as_float(0x7fffffff) : x + 0.f; }
+__device__ inline uint32_t order_of(float canonical_x) {
+    const int u = __float_as_int(canonical_x);
+    return static_cast<uint32_t>(u ^ ((u >> 31) | static_cast<int>(0x80000000u)));
 }
 
 constexpr int kSelBins = 2048;
@@ -55,7 +54,8 @@ constexpr int kSelMaxSlice = 48 * 1024;           // scores a CTA holds in share
 constexpr int kSelMaxCluster = 8;
 
 struct SelectShared {
-    uint32_t hist[2][kSelBins];
+    uint32_t hist[kSelBins];        // of this CTA's slice
+    uint32_t all[2][kSelBins];      // of the row, by pass parity (clusters)
     uint32_t warp_sum[kSelWarps];
     uint32_t warp_count[2][kSelWarps];  // by round parity: kept surely | equal << 16
     uint32_t digit, above;
@@ -100,15 +100,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         if ((reinterpret_cast<uintptr_t>(in + lo) & 15u) == 0) {
             const int n4 = (hi - lo) / 4;
             for (int i = tid; i < n4; i += kSelThreads)
-                reinterpret_cast<float4 *>(slice)[i] = reinterpret_cast<const float4 *>(in + lo)[i];
+                {
+                const float4 v = reinterpret_cast<const float4 *>(in + lo)[i];
+                reinterpret_cast<float4 *>(slice)[i] =
+                    make_float4(canonical(v.x), canonical(v.y), canonical(v.z), canonical(v.w));
+            }
             for (int i = n4 * 4 + tid; i < hi - lo; i += kSelThreads)
-                slice[i] = in[lo + i];
+                slice[i] = canonical(in[lo + i]);
         } else {
             for (int i = tid; i < hi - lo; i += kSelThreads)
-                slice[i] = in[lo + i];
+                slice[i] = canonical(in[lo + i]);
         }
     }
-    auto score = [&](int t) -> float { return Cached ? slice[t - lo] : in[t]; };
+    if (ranks > 1) {
+        for (int i = tid; i < 2 * kSelBins; i += kSelThreads)
+            sh->all[0][i] = 0;
+        cluster.sync();  // (no CTA adds to another's before it is zero)
+    }
+    auto score = [&](int t) -> float { return Cached ? slice[t - lo] : canonical(in[t]); };
 
     uint32_t kth = 0, above = 0;  // the k-th largest image, scores above it
     if (k > 0) {
@@ -119,7 +128,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t high = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
             const uint32_t digits = pass == 2 ? 1023u : 2047u;
-            uint32_t *hist = sh->hist[pass & 1];
+            uint32_t *hist = sh->hist, *all = ranks > 1 ? sh->all[pass & 1] : hist;
             for (int i = tid; i < kSelBins; i += kSelThreads)
                 hist[i] = 0;
             __syncthreads();  // (the slice is loaded, too)
@@ -129,24 +138,23 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 if ((u & high) == (kth & high))
                     atomicAdd(&hist[(u >> shift) & digits], 1u);
             }
-            if (ranks > 1)
-                cluster.sync();
-            else
-                __syncthreads();
-            // suffix counts over the cluster, 4 bins a thread, from the top
-            uint32_t c[4] = {0, 0, 0, 0};
+            __syncthreads();
             const int top = kSelBins - 1 - 4 * tid;  // thread tid: bins top, top - 1, top - 2, top - 3
-            uint4 v[kSelMaxCluster];  // (all loads before the first sum)
+            if (ranks > 1) {
+                // this slice's counts to every CTA of the row: only the digits it has (a
+                // whole histogram read from 7 others took 7000 cycles)
+                const uint4 v = *reinterpret_cast<const uint4 *>(hist + top - 3);
+                const uint32_t mine4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int r = 0; r < kSelMaxCluster; ++r)
-                if (r < ranks) {
-                    const uint32_t *rh = ranks > 1 ? cluster.map_shared_rank(hist, r) : hist;
-                    v[r] = *reinterpret_cast<const uint4 *>(rh + top - 3);
-                }
-#pragma unroll
-            for (int r = 0; r < kSelMaxCluster; ++r)
-                if (r < ranks)
-                    c[0] += v[r].w, c[1] += v[r].z, c[2] += v[r].y, c[3] += v[r].x;
+                for (int i = 0; i < 4; ++i)
+                    if (mine4[i])
+                        for (int r = 0; r < ranks; ++r)
+                            atomicAdd(cluster.map_shared_rank(all, r) + top - 3 + i, mine4[i]);
+                cluster.sync();
+            }
+            // suffix counts, from the top
+            const uint4 v = *reinterpret_cast<const uint4 *>(all + top - 3);
+            const uint32_t c[4] = {v.w, v.z, v.y, v.x};
             const uint32_t mine = c[0] + c[1] + c[2] + c[3];
             // (counts up to 2^31: a plain scan, not the packed one)
             uint32_t x = mine;
@@ -175,6 +183,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             kth |= sh->digit << shift;
             above += sh->above;
             need -= sh->above;
+            if (ranks > 1)  // for the pass after next: its counts come after another cluster barrier
+                *reinterpret_cast<uint4 *>(all + top - 3) = make_uint4(0, 0, 0, 0);
             __syncthreads();
         }
     }
