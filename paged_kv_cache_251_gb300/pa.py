@@ -416,32 +416,43 @@ def pa_swap_blocks_quant(src_dst_pairs: torch.Tensor, src_k: torch.Tensor, src_v
 # eviction)
 
 
-def _one_device(*ts) -> torch.device:
-    """The tensors' common CUDA device; every tensor must be on it."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("every tensor must be on one device")
+# These calls are short beside their launch, so their checks are written to cost
+# little: one pass over the tensors, addresses passed as integers.
+
+
+def _dense(first: torch.Tensor, *rest) -> int:
+    """The CUDA device index that all tensors share; each must be contiguous."""
+    dev = first.get_device()
+    if dev < 0 or not first.is_contiguous():
+        raise ValueError("every tensor must be a contiguous CUDA tensor")
+    for t in rest:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if t.is_cuda and t.is_contiguous():
+                raise ValueError("every tensor must be on one device")
+            raise ValueError("every tensor must be a contiguous CUDA tensor")
     return dev
 
 
-def _call(fn, device: torch.device, stream, *args) -> None:
+def _call(fn, dev: int, stream, *args) -> None:
     """Run a library call on `stream` (default: the device's current one) with
-    `device` current."""
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream is on another device than the tensors")
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(stream)))
+    device `dev` current."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device_index != dev:
+            raise ValueError("the stream is on another device than the tensors")
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, raw)
+    if status != PA_OK:
+        _check(status)
 
 
 def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -449,6 +460,10 @@ def _int32(**ts) -> None:
     for name, t in ts.items():
         if t is not None and t.dtype != torch.int32:
             raise TypeError(f"{name} must be int32")
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 def _ws_bytes(workspace) -> int:
@@ -487,18 +502,18 @@ def pa_rope(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: 
             interleaved: bool = False, inverse: bool = False, mscale: float = 1.0, stream=None) -> torch.Tensor:
     """out[i, h] = x[i, h] rotated to positions[i] (back by it when inverse:
     the gradient of the rotation).  rot_dim is 2 * freqs.numel(); out may be x."""
-    dev = _one_device(out, x, positions, freqs)
+    dev = _dense(positions, freqs)
+    if x.get_device() != dev or out.get_device() != dev:
+        raise ValueError("every tensor must be a CUDA tensor on one device")
     n, h, d = x.shape
     _shape(out, x.shape, "out")
     _shape(positions, (n,), "positions")
-    _int32(positions=positions)
-    if freqs.dtype != torch.float64 or freqs.dim() != 1:
-        raise TypeError("freqs must be a double vector")
+    if positions.dtype != torch.int32 or freqs.dtype != torch.float64 or freqs.dim() != 1:
+        raise TypeError("positions must be int32 and freqs a double vector")
     if out.dtype != x.dtype:
         raise TypeError("out and x must share one dtype")
-    _cuda(positions, freqs)
-    _call(_lib.pa_rope, dev, stream, _ptr(out), _ptr(x), _ptr(positions), _ptr(freqs), n, h, d, 2 * freqs.numel(),
-          _rows(x, "x"), _rows(out, "out"), int(interleaved), -1 if inverse else 1, float(mscale),
+    _call(_lib.pa_rope, dev, stream, out.data_ptr(), x.data_ptr(), positions.data_ptr(), freqs.data_ptr(), n, h, d,
+          2 * freqs.numel(), _rows(x, "x"), _rows(out, "out"), int(interleaved), -1 if inverse else 1, float(mscale),
           DTYPE_CODE[x.dtype])
     return out
 
@@ -510,7 +525,9 @@ def pa_rope_append_kv(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     """Rotate q into q_out and k into its cache slots, store v in its slots (see
     include/pa.h).  q, k and v may be slices of one projection: their rows may
     be any distance apart."""
-    dev = _one_device(q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, err_word)
+    dev = _dense(q_out, positions, slot_mapping, freqs, k_cache, v_cache, err_word)
+    if q.get_device() != dev or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("every tensor must be a CUDA tensor on one device")
     n, h, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
     _shape(q_out, q.shape, "q_out")
@@ -520,18 +537,17 @@ def pa_rope_append_kv(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     _shape(v_cache, k_cache.shape, "v_cache")
     _shape(positions, (n,), "positions")
     _shape(slot_mapping, (n,), "slot_mapping")
-    _int32(positions=positions)
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
+    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64:
+        raise TypeError("positions must be int32 and slot_mapping int64")
     if freqs.dtype != torch.float64 or freqs.dim() != 1:
         raise TypeError("freqs must be a double vector")
-    if len({q_out.dtype, q.dtype, k.dtype, v.dtype, k_cache.dtype, v_cache.dtype}) != 1:
+    dt = q.dtype
+    if q_out.dtype != dt or k.dtype != dt or v.dtype != dt or k_cache.dtype != dt or v_cache.dtype != dt:
         raise TypeError("q, k, v, q_out and the caches must share one dtype")
-    _cuda(q_out, positions, slot_mapping, freqs, k_cache, v_cache, err_word)
-    _call(_lib.pa_rope_append_kv, dev, stream, _ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _ptr(positions),
-          _ptr(slot_mapping), _ptr(freqs), _ptr(k_cache), _ptr(v_cache), n, h, hkv, d, 2 * freqs.numel(),
-          _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), bs, nb, int(interleaved), float(mscale), DTYPE_CODE[q.dtype],
-          _ptr(err_word))
+    _call(_lib.pa_rope_append_kv, dev, stream, q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          positions.data_ptr(), slot_mapping.data_ptr(), freqs.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), n, h,
+          hkv, d, 2 * freqs.numel(), _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), bs, nb, int(interleaved),
+          float(mscale), DTYPE_CODE[dt], _addr(err_word))
     return q_out
 
 
@@ -592,9 +608,7 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     its committed tokens and the drafted ones its mask names; the drafted
     tokens are the last draft_lens[s] of the context_lens[s] cached ones.
     tree_mask None: a chain (see include/pa.h)."""
-    dev = _one_device(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace,
-                      err_word)
-    _cuda(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, err_word)
+    dev = _dense(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, err_word)
     n, t, h, d = q.shape
     nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
     _shape(out, q.shape, "out")
@@ -609,10 +623,10 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = tree_workspace_for(q, k_cache, block_tables.shape[1])
-    _call(_lib.pa_decode_tree, dev, stream, _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-          _ptr(context_lens), _ptr(draft_lens), _ptr(tree_mask), n, t, h, hkv, d, bs, float(scale),
-          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _ptr(workspace),
-          _ws_bytes(workspace), _ptr(err_word))
+    _call(_lib.pa_decode_tree, dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), context_lens.data_ptr(), _addr(draft_lens), _addr(tree_mask), n, t, h, hkv, d, bs, float(scale),
+          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace),
+          _ws_bytes(workspace), _addr(err_word))
     return out
 
 
@@ -638,27 +652,24 @@ def pa_decode_scored(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tenso
     """pa_decode, and scores_out[s, kvh, t] = scores_in[s, kvh, t] (None: 0) +
     the softmax weights token t gets from the kv head's query heads (see
     include/pa.h).  Scores are fp32 [N, H_kv, at least max_blocks * block_size]."""
-    dev = _one_device(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace,
-                      err_word)
-    _cuda(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace, err_word)
+    dev = _dense(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace, err_word)
     n, h, d = q.shape
     nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
     _shape(out, q.shape, "out")
-    if scores_out.dim() != 3 or tuple(scores_out.shape[:2]) != (n, hkv):
+    if scores_out.dim() != 3 or scores_out.shape[:2] != (n, hkv):
         raise ValueError("scores_out must be [N, H_kv, tokens]")
     if scores_in is not None:
         _shape(scores_in, scores_out.shape, "scores_in")
-    for t in (scores_out, scores_in):
-        if t is not None and t.dtype != torch.float32:
-            raise TypeError("scores must be float32")
+    if scores_out.dtype != torch.float32 or (scores_in is not None and scores_in.dtype != torch.float32):
+        raise TypeError("scores must be float32")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = scored_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
-    _call(_lib.pa_decode_scored, dev, stream, _ptr(out), _ptr(scores_out), _ptr(scores_in), _ptr(q), _ptr(k_cache),
-          _ptr(v_cache), _ptr(block_tables), _ptr(context_lens), n, h, hkv, d, bs, float(scale),
+    _call(_lib.pa_decode_scored, dev, stream, out.data_ptr(), scores_out.data_ptr(), _addr(scores_in), q.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), n, h, hkv, d, bs, float(scale),
           scores_out.shape[2], DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb,
-          int(partition_size), _ptr(workspace), _ws_bytes(workspace), _ptr(err_word))
+          int(partition_size), _addr(workspace), _ws_bytes(workspace), _addr(err_word))
     return out
 
 
@@ -669,8 +680,7 @@ def pa_evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores_out: torc
     the others with the largest scores, `budget` in all, ascending in keep
     [N, H_kv, budget] (-1 past new_lens); their scores move to the front of
     scores_out (which may be scores, or None).  See include/pa.h."""
-    dev = _one_device(keep, new_lens, scores_out, scores, context_lens, err_word)
-    _cuda(keep, new_lens, scores_out, scores, context_lens, err_word)
+    dev = _dense(keep, new_lens, scores_out, scores, context_lens, err_word)
     if scores.dim() != 3 or scores.dtype != torch.float32:
         raise TypeError("scores must be float32 [N, H_kv, tokens]")
     n, hkv, stride = scores.shape
@@ -682,8 +692,8 @@ def pa_evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores_out: torc
     _shape(new_lens, (n,), "new_lens")
     _shape(context_lens, (n,), "context_lens")
     _int32(keep=keep, new_lens=new_lens, context_lens=context_lens)
-    _call(_lib.pa_evict_select, dev, stream, _ptr(keep), _ptr(new_lens), _ptr(scores_out), _ptr(scores),
-          _ptr(context_lens), n, hkv, int(budget), int(recent), stride, _ptr(err_word))
+    _call(_lib.pa_evict_select, dev, stream, keep.data_ptr(), new_lens.data_ptr(), _addr(scores_out),
+          scores.data_ptr(), context_lens.data_ptr(), n, hkv, int(budget), int(recent), stride, _addr(err_word))
     return keep
 
 
@@ -693,8 +703,7 @@ def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tens
     """Token base_lens[s] + i takes the K/V rows of token base_lens[s] +
     keep[s, h, i], for i < keep_lens[s] (keep [N, H_kv or 1, n]): in place, or
     into the blocks of dst_block_tables.  See include/pa.h."""
-    dev = _one_device(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
-    _cuda(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
+    dev = _dense(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
     nb, hkv, bs, d = k_cache.shape
     _shape(v_cache, k_cache.shape, "v_cache")
     if v_cache.dtype != k_cache.dtype:
@@ -704,16 +713,17 @@ def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tens
     n = keep.shape[0]
     _int32(keep=keep, keep_lens=keep_lens, block_tables=block_tables, dst_block_tables=dst_block_tables,
            base_lens=base_lens)
-    for name, t in (("block_tables", block_tables), ("dst_block_tables", dst_block_tables)):
-        if t is not None and (t.dim() != 2 or t.shape[0] != n):
-            raise ValueError(f"{name} must be [N, max_blocks_per_seq]")
-    for name, t in (("keep_lens", keep_lens), ("base_lens", base_lens)):
-        if t is not None:
-            _shape(t, (n,), name)
-    _call(_lib.pa_compact_kv, dev, stream, _ptr(k_cache), _ptr(v_cache), _ptr(keep), _ptr(keep_lens),
-          _ptr(base_lens), _ptr(block_tables), _ptr(dst_block_tables), n, keep.shape[1], keep.shape[2], hkv, d, bs,
-          block_tables.shape[1], 0 if dst_block_tables is None else dst_block_tables.shape[1], nb,
-          DTYPE_CODE[k_cache.dtype], _ptr(err_word))
+    _shape(keep_lens, (n,), "keep_lens")
+    if block_tables.shape[0] != n or (dst_block_tables is not None and
+                                      (dst_block_tables.dim() != 2 or dst_block_tables.shape[0] != n)):
+        raise ValueError("block_tables and dst_block_tables must be [N, max_blocks_per_seq]")
+    if base_lens is not None:
+        _shape(base_lens, (n,), "base_lens")
+    _call(_lib.pa_compact_kv, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), keep.data_ptr(),
+          keep_lens.data_ptr(), _addr(base_lens), block_tables.data_ptr(), _addr(dst_block_tables), n, keep.shape[1],
+          keep.shape[2], hkv, d, bs, block_tables.shape[1],
+          0 if dst_block_tables is None else dst_block_tables.shape[1], nb, DTYPE_CODE[k_cache.dtype],
+          _addr(err_word))
 
 
 def version() -> tuple[int, int, int]:
