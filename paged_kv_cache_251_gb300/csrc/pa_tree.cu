@@ -22,7 +22,7 @@ pa_status launch_general(TreeParams &p, int dtype, int head_dim, int dev, cudaSt
     const void *fn = dtype == PA_F32   ? tree_fn<float>(head_dim)
                      : dtype == PA_F16 ? tree_fn<__half>(head_dim)
                                        : tree_fn<__nv_bfloat16>(head_dim);
-    const size_t smem = static_cast<size_t>(2) * p.block_size * head_dim * sizeof(float);
+    const size_t smem = head_dim == 64 ? sizeof(TreeSmem<64>) : sizeof(TreeSmem<128>);
     int per_sm = 0;
     cudaError_t e = prepare_kernel(dev, fn, smem, kTreeThreads, &per_sm);
     if (e != cudaSuccess)

@@ -39,22 +39,48 @@ __device__ inline TreeSeq tree_seq(const TreeParams &p, int s) {
     return q;
 }
 
-// Whether query i attends drafted token j (both below the sequence's drafted count).
-__device__ inline bool tree_bit(const TreeParams &p, int s, int i, int j) {
-    if (!p.mask)
-        return j <= i;
-    const uint64_t w = p.mask[(static_cast<long long>(s) * p.num_draft + i) * p.words + (j >> 6)];
-    return (w >> (j & 63)) & 1u;
+// The 64 cached tokens [tok, tok + 64) that a row attends, blocks aside:
+// committed tokens, then the row's drafted ones.  The mask words come in one
+// round trip (two 64-bit words cover 64 bits at any offset).
+__device__ inline uint64_t first_bits(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
+
+__device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed, int drafted, int i, int tok) {
+    const int j = tok - committed;  // drafted index of the first token (negative: committed tokens first)
+    const int up = max(-j, 0), j0 = max(j, 0);
+    uint64_t d = 0;  // bit e: drafted token j0 + e
+    if (j > -64 && j < drafted) {
+        if (p.mask) {
+            const uint64_t *row = p.mask + (static_cast<long long>(s) * p.num_draft + i) * p.words + (j0 >> 6);
+            const int sh = j0 & 63;
+            const uint64_t lo = row[0], hi = (j0 >> 6) + 1 < p.words ? row[1] : 0ull;
+            d = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
+        } else {  // a chain
+            d = first_bits(i + 1 - j0);
+        }
+        d &= first_bits(drafted - j0);
+    }
+    return up >= 64 ? ~0ull : first_bits(up) | (d << up);
 }
 
 // ---------------------------------------------------------------------------
 // General kernel: any dtype, on the CUDA cores.  A CTA of 128 threads takes 16
-// rows: 8 lanes a row, lane l holding elements l, l + 8, ... of its query and
-// accumulator.  K and V of one block at a time are widened to fp32 in shared
-// memory; every row then walks the block's tokens with an online softmax.
+// rows, 8 lanes a row, and 64 tokens at a time, widened to fp32 in shared memory
+// (one round trip a tile).  Scores: lane l of a row has tokens l, l + 8, ... with
+// whole dot products, no exchange; one maximum and one rescale a tile; then the
+// weights go through shared memory and lane l sums its D / 8 elements of the
+// output over the attended tokens (others are never multiplied).
 
 constexpr int kTreeRows = 16;
 constexpr int kTreeThreads = kTreeRows * 8;
+constexpr int kTreeTile = 64;
+
+template <int D> struct TreeSmem {
+    float k[kTreeTile][D + 4];  // (+ 4: rows of a lane's tokens on different banks)
+    float v[kTreeTile][D];
+    float q[kTreeRows][D + 4];
+    float w[kTreeRows][kTreeTile + 1];
+    int phys[kTreeTile / 8];  // blocks of the tile, -1: left out
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams p) {
@@ -62,12 +88,13 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
     pdl_wait();
     constexpr int E = D / 8;
     constexpr int V = 16 / sizeof(T);  // elements per 16-byte load
-    extern __shared__ __align__(16) float kv[];
-    float *ks = kv, *vs = kv + p.block_size * D;
+    constexpr int kPer = kTreeTile / 8;  // tokens of a lane
+    extern __shared__ __align__(16) char smem[];
+    TreeSmem<D> *sh = reinterpret_cast<TreeSmem<D> *>(smem);
     const int G = p.num_heads / p.num_kv_heads;
     const int rows = p.num_draft * G;
     const int rl = threadIdx.x >> 3, l8 = threadIdx.x & 7;
-    const int bs = p.block_size;
+    const int bs = p.block_size, tile_blocks = kTreeTile / bs;
     const long long total = static_cast<long long>(p.num_seqs) * p.max_parts * p.num_kv_heads * p.row_tiles;
     for (long long w = blockIdx.x; w < total; w += gridDim.x) {
         long long f = w;
@@ -90,64 +117,115 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
         const int h = kvh * G + (mine ? r % G : 0);
         const bool live = mine && i < q.drafted;
         const long long orow = (static_cast<long long>(s) * p.num_draft + i) * p.num_heads + h;
-        float qf[E], acc[E], m = -INFINITY, l = 0.f;
+        float acc[E], m = -INFINITY, l = 0.f;
+        __syncthreads();  // (the item before is done with shared memory)
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            qf[e] = live ? static_cast<float>(static_cast<const T *>(p.q)[orow * D + l8 + 8 * e]) * p.scale_log2 : 0.f;
+            const int c = l8 + 8 * e;
+            sh->q[rl][c] = live ? static_cast<float>(static_cast<const T *>(p.q)[orow * D + c]) * p.scale_log2 : 0.f;
             acc[e] = 0.f;
         }
         const int b_lo = part * p.bpp, b_hi = min(b_lo + p.bpp, sp.nblk);
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int phys = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b);
-            if (phys < 0 || phys >= p.num_blocks) {  // (uniform over the CTA)
-                if (threadIdx.x == 0 && p.err)
-                    atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
-                continue;
-            }
-            const long long tile = (static_cast<long long>(phys) * p.num_kv_heads + kvh) * bs * D;
+        for (int b = b_lo; b < b_hi; b += tile_blocks) {
             __syncthreads();
-            for (int c = threadIdx.x; c < bs * D / V; c += kTreeThreads) {
-                Elt<T>::unpack(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_cache) + tile)[c],
-                               ks + c * V);
-                Elt<T>::unpack(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_cache) + tile)[c],
-                               vs + c * V);
+            if (threadIdx.x < tile_blocks) {
+                int phys = -1;
+                if (b + static_cast<int>(threadIdx.x) < b_hi) {
+                    phys = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b +
+                                     threadIdx.x);
+                    if (phys < 0 || phys >= p.num_blocks) {
+                        phys = -1;
+                        if (p.err)
+                            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+                    }
+                }
+                sh->phys[threadIdx.x] = phys;
             }
             __syncthreads();
-            const int hi = min(bs, q.len - b * bs);
-            for (int u = 0; u < hi; ++u) {
-                const int j = b * bs + u - committed;
-                const bool ok = live && (j < 0 || tree_bit(p, s, i, j));
-                float x = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    x = fmaf(qf[e], ks[u * D + l8 + 8 * e], x);
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                if (ok) {
-                    const float mn = fmaxf(m, x);
-                    const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
-                    const float pw = x == -INFINITY ? 0.f : exp2f(x - mn);  // (a NaN score stays one)
-                    l = fmaf(l, alpha, pw);
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        acc[e] = fmaf(acc[e], alpha, pw * vs[u * D + l8 + 8 * e]);
-                    m = mn;
+            // 16-byte pieces of the tile's rows
+            for (int c = threadIdx.x; c < kTreeTile * D / V; c += kTreeThreads) {
+                const int t = c / (D / V), e = (c - t * (D / V)) * V;
+                const int phys = sh->phys[t / bs];
+                if (phys >= 0) {
+                    const long long at =
+                        ((static_cast<long long>(phys) * p.num_kv_heads + kvh) * bs + t % bs) * D + e;
+                    Elt<T>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_cache) + at), &sh->k[t][e]);
+                    Elt<T>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_cache) + at), &sh->v[t][e]);
                 }
             }
+            __syncthreads();
+            const int tok0 = b * bs;
+            uint64_t allow = live ? tree_bits64(p, s, committed, q.drafted, i, tok0) : 0ull;
+            for (int k = 0; k < tile_blocks; ++k)
+                if (sh->phys[k] < 0)
+                    allow &= ~(first_bits(bs) << (k * bs));
+            float x[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k)
+                x[k] = 0.f;
+#pragma unroll 4
+            for (int e = 0; e < D; e += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(&sh->q[rl][e]);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const float4 c = *reinterpret_cast<const float4 *>(&sh->k[l8 + 8 * k][e]);
+                    x[k] = fmaf(a.x, c.x, fmaf(a.y, c.y, fmaf(a.z, c.z, fmaf(a.w, c.w, x[k]))));
+                }
+            }
+            float mt = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                x[k] = (allow >> (l8 + 8 * k)) & 1u ? x[k] : -INFINITY;
+                mt = fmaxf(mt, x[k]);
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+            const float mn = fmaxf(m, mt);
+            const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            l *= alpha;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] *= alpha;
+            m = mn;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                // (a NaN score stays one)
+                const float pw = x[k] == -INFINITY ? 0.f : exp2f(x[k] - mn);
+                l += pw;
+                sh->w[rl][l8 + 8 * k] = pw;
+            }
+            __syncwarp();
+            // attended tokens one by one, in order; lane l8 sums elements E l8 .. E l8 + E - 1
+            for (uint64_t left = allow; left; left &= left - 1) {
+                const int t = __ffsll(static_cast<long long>(left)) - 1;
+                const float pw = sh->w[rl][t];
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    const float4 c = *reinterpret_cast<const float4 *>(&sh->v[t][l8 * E + e]);
+                    acc[e] = fmaf(pw, c.x, acc[e]);
+                    acc[e + 1] = fmaf(pw, c.y, acc[e + 1]);
+                    acc[e + 2] = fmaf(pw, c.z, acc[e + 2]);
+                    acc[e + 3] = fmaf(pw, c.w, acc[e + 3]);
+                }
+            }
+            __syncwarp();
         }
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
         if (!mine)
             continue;
         if (sp.nparts == 1) {
             // (a NaN denominator is the row's own: it stays)
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                store_out(p.out, p.out_dtype, orow * D + l8 + 8 * e, l == 0.f ? 0.f : acc[e] / l);
+                store_out(p.out, p.out_dtype, orow * D + l8 * E + e, l == 0.f ? 0.f : acc[e] / l);
         } else {
             const long long item = (static_cast<long long>(s) * p.num_kv_heads + kvh) * p.max_parts + part;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                p.part_acc[(item * D + l8 + 8 * e) * rows + r] = acc[e];
+                p.part_acc[(item * D + l8 * E + e) * rows + r] = acc[e];
             if (l8 == 0)
                 reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(m, l);
         }

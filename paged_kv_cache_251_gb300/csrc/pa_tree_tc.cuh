@@ -722,29 +722,6 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 
-// The 64 cached tokens [tok, tok + 64) that a row attends, blocks aside:
-// committed tokens, then the row's drafted ones.  The mask words come in one
-// round trip (two 64-bit words cover 64 bits at any offset).
-__device__ inline uint64_t first_bits(int n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull); }
-
-__device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed, int drafted, int i, int tok) {
-    const int j = tok - committed;  // drafted index of the first token (negative: committed tokens first)
-    const int up = max(-j, 0), j0 = max(j, 0);
-    uint64_t d = 0;  // bit e: drafted token j0 + e
-    if (j > -64 && j < drafted) {
-        if (p.mask) {
-            const uint64_t *row = p.mask + (static_cast<long long>(s) * p.num_draft + i) * p.words + (j0 >> 6);
-            const int sh = j0 & 63;
-            const uint64_t lo = row[0], hi = (j0 >> 6) + 1 < p.words ? row[1] : 0ull;
-            d = sh ? (lo >> sh) | (hi << (64 - sh)) : lo;
-        } else {  // a chain
-            d = first_bits(i + 1 - j0);
-        }
-        d &= first_bits(drafted - j0);
-    }
-    return up >= 64 ? ~0ull : first_bits(up) | (d << up);
-}
-
 // 32 columns of an accumulator row to the output.
 __device__ inline void store_cols32(void *out, int dtype, long long idx, const float *v) {
     if (dtype == PA_F32) {
