@@ -81,8 +81,8 @@ template <int D, int Units> struct TcCfg {
     static constexpr int kQ = 128 * kRow;              // one row tile of queries
     // measured on the tree over long contexts and the ragged batch: as many
     // tiles as shared memory holds beside the queries
-    static constexpr int kSK = D == 64 ? 6 : 3;
-    static constexpr int kSV = D == 64 ? 6 : (Units == 1 ? 3 : 2);
+    static constexpr int kSK = D == 64 ? 6 : (Units == 1 ? 3 : 2);
+    static constexpr int kSV = D == 64 ? 6 : 3;
     static constexpr int kOffK = Units * kQ;
     static constexpr int kOffV = kOffK + kSK * kTile;
     static constexpr int kOffMisc = kOffV + kSV * kTile;
@@ -243,7 +243,11 @@ template <typename T> __device__ inline bool non_finite2(uint32_t w) {
 // ---------------------------------------------------------------------------
 // The even split
 
-constexpr int kTcPairCost = 2;
+// In tiles.  An item costs its start, its masked last tile and its epilogue beside
+// its tiles; measured on 64 ragged contexts of 16 to 8192 tokens: 108, 88, 80.5,
+// 81.5, 84 and 88 us at 1, 2, 4, 5, 8 and 12 (contexts of 512 to 2048: 249, 238,
+// 239, 242, 251 and 260).
+constexpr int kTcPairCost = 4;
 
 __device__ inline int tc_tiles(const TreeParams &p, int s) {
     const int len = max(0, min(ld_nc_i32(p.context_lens + s), p.max_len));
