@@ -427,7 +427,8 @@ PA_API pa_status pa_rope(void *out, const void *x, const int32_t *positions, con
  *   v_cache[...] = v[i][h][:]
  * with slot = slot_mapping[i]; a negative slot is padding (its query is
  * rotated, nothing is appended), one outside the pool is skipped and flagged,
- * and a slot named twice holds one of its rows, as for pa_append_kv.
+ * as for pa_append_kv.  Two tokens must not name one slot (it would hold parts
+ * of both; nothing else is touched).
  *   q, k, v       rows of num_heads (q) or num_kv_heads (k, v) * head_dim
  *                 elements of dtype, q_stride, k_stride, v_stride elements
  *                 apart (slices of one fused projection, for instance)
@@ -471,7 +472,8 @@ PA_API pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, co
  * rounded once to the cache's type before the product with V, like the output
  * itself; fp32 out: they are carried in two parts.
  * A drafted token that some query does not attend has no influence on it,
- * whatever its K and V hold (infinities and NaN too).  Other arguments and
+ * whatever its K and V hold (infinities and NaN too).  The table holds at most
+ * 2^30 tokens a sequence (max_blocks_per_seq * block_size); other arguments and
  * limits as pa_decode (window 0).
  */
 PA_API pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -502,7 +504,7 @@ PA_API size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num
  *   workspace     pa_decode_scored_workspace_size() bytes, 16-byte aligned
  *                 (the scores of every query head are kept there between the
  *                 passes)
- * Other arguments, limits and results as pa_decode with window 0.
+ * The table holds at most 2^30 tokens a sequence.  Other arguments, limits and results as pa_decode with window 0.
  */
 PA_API pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in, const void *q,
                                   const void *k_cache, const void *v_cache, const int32_t *block_tables,
@@ -526,10 +528,11 @@ PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int h
  *                 tokens in ascending order, then -1
  *   new_lens      int32 [num_seqs] (written): n
  *   scores_out    fp32 [num_seqs][num_kv_heads][scores_stride] (written): the
- *                 kept tokens' scores at 0 .. n - 1, then zeros to the end of
- *                 the row.  May be scores itself; NULL: not written
+ *                 kept tokens' scores at 0 .. n - 1 (-0 as 0, every NaN as one
+ *                 NaN), then zeros to the end of the row.  May be scores
+ *                 itself, and must not overlap it otherwise; NULL: not written
  *   scores        fp32, same shape
- *   budget >= 1, 0 <= recent <= budget; a context longer than scores_stride
+ *   1 <= budget <= 2^30, 0 <= recent <= budget, scores_stride <= 2^30; a context longer than scores_stride
  *   is clamped to it and flagged (PA_DEVERR_BAD_LEN)
  */
 PA_API pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores_out, const float *scores,
@@ -545,7 +548,8 @@ PA_API pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores
  * the commit of accepted drafted tokens (base_lens the committed lengths,
  * keep the accepted drafted tokens of the sequence, keep_heads 1).
  *   keep          int32 [num_seqs][keep_heads][keep_stride], keep_heads
- *                 num_kv_heads or 1 (the same list for every kv head)
+ *                 num_kv_heads or 1 (the same list for every kv head);
+ *                 keep_stride at most 2^30
  *   keep_lens     int32 [num_seqs], clamped to [0, keep_stride]
  *   base_lens     int32 [num_seqs], or NULL (zeros)
  *   dst_block_tables  int32 [num_seqs][dst_max_blocks_per_seq], or NULL: in

@@ -22,6 +22,10 @@ bool elt_aligned(const void *p, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) & (elt_bytes(dtype) - 1)) == 0;
 }
 
+// Positions along a context, a score row or a list of kept tokens are 32 bits in
+// the kernels, with room for a tile past the end.
+constexpr long long kMaxTokens = 1LL << 30;
+
 size_t round16(size_t x) { return (x + 15) & ~static_cast<size_t>(15); }
 
 pa_status rope_args(int num_tokens, int num_heads, int head_dim, int rot_dim, float mscale, int dtype) {
@@ -315,6 +319,8 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
                      out_dtype, num_blocks);
     if (st != PA_OK)
         return st;
+    if (static_cast<long long>(max_blocks_per_seq) * block_size > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size is above 2^30");
     if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)
         return fail(PA_ERR_INVALID_ARGUMENT, "tree_mask must be 8-byte aligned");
     if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
@@ -383,8 +389,8 @@ pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in,
     const long long max_len = static_cast<long long>(max_blocks_per_seq) * block_size;
     if (!scores_out || !elt_aligned(scores_out, PA_F32) || !elt_aligned(scores_in, PA_F32))
         return fail(PA_ERR_INVALID_ARGUMENT, "scores_out is null, or a score array is not 4-byte aligned");
-    if (max_len > INT_MAX)
-        return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size too large");
+    if (max_len > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size is above 2^30");
     if (scores_stride < max_len)
         return fail(PA_ERR_INVALID_ARGUMENT, "scores_stride smaller than max_blocks_per_seq * block_size");
     if (num_kv_heads > 65535)
@@ -421,6 +427,8 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores_out, c
         return fail(PA_ERR_INVALID_ARGUMENT, "num_seqs, num_kv_heads or scores_stride out of range");
     if (budget < 1 || recent < 0 || recent > budget)
         return fail(PA_ERR_INVALID_ARGUMENT, "budget must be positive and recent in [0, budget]");
+    if (scores_stride > kMaxTokens || budget > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "scores_stride or budget is above 2^30");
     if (num_seqs == 0)
         return PA_OK;
     if (!keep || !new_lens || !scores || !context_lens)
@@ -436,7 +444,7 @@ pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores_out, c
     p.context_lens = context_lens;
     p.err = err_word;
     p.stride = scores_stride;
-    p.max_len = scores_stride < INT_MAX ? scores_stride : INT_MAX;
+    p.max_len = scores_stride;
     p.num_seqs = num_seqs;
     p.num_kv_heads = num_kv_heads;
     p.budget = budget;
@@ -470,6 +478,8 @@ pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep, const
         return fail(PA_ERR_INVALID_ARGUMENT, "dst_max_blocks_per_seq must be positive");
     if (num_kv_heads > 65535)
         return fail(PA_ERR_UNSUPPORTED, "num_kv_heads too large");
+    if (keep_stride > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "keep_stride is above 2^30");
     if (num_seqs == 0 || keep_stride == 0)
         return PA_OK;
     if (!k_cache || !v_cache || !keep || !keep_lens || !block_tables)

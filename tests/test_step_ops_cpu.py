@@ -129,6 +129,32 @@ def test_compact_refusals(lib):
         assert call(**bad) == INV, bad
 
 
+def test_long_rows_are_refused(lib):
+    """Above 2^30 tokens a row: 32-bit positions would not leave room for a tile
+    past the end.  At 2^30 the call goes on to its other checks."""
+    tree = caller(lib.pa_decode_tree,
+                  [P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, I, I, I, I, P, SZ, P, P],
+                  dict(out=0x1000, q=0x2000, k=0x3000, v=0x4000, bt=0x5000, cl=0x6000, dl=None, mask=0x7000, n=1, t=8,
+                       h=8, hkv=2, d=128, bs=32, scale=0.1, dt=2, odt=2, m=8, nb=64, ws=None, wsb=0, err=None,
+                       st=None))
+    assert tree(m=1 << 25) == WS and tree(m=(1 << 25) + 1) == UNS and tree(m=(1 << 25) + 1, dt=0, odt=0) == UNS
+    scored = caller(lib.pa_decode_scored,
+                    [P, P, P, P, P, P, P, P, I, I, I, I, I, F, LL, I, I, I, I, I, P, SZ, P, P],
+                    dict(out=0x1000, so=0x8000, si=0x8000, q=0x2000, k=0x3000, v=0x4000, bt=0x5000, cl=0x6000, n=1,
+                         h=8, hkv=2, d=128, bs=32, scale=0.1, stride=1 << 31, dt=1, odt=0, m=8, nb=64, part=0, ws=None,
+                         wsb=0, err=None, st=None))
+    assert scored(m=1 << 25) == WS and scored(m=(1 << 25) + 1) == UNS
+    select = caller(lib.pa_evict_select, [P, P, P, P, P, I, I, I, I, LL, P, P],
+                    dict(keep=None, new=0x2000, so=None, s=0x3000, cl=0x4000, n=2, hkv=2, budget=16, recent=4,
+                         stride=64, err=None, st=None))
+    assert select(stride=1 << 30, budget=1 << 30) == INV
+    assert select(stride=(1 << 30) + 1) == UNS and select(budget=(1 << 30) + 1) == UNS
+    compact = caller(lib.pa_compact_kv, [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P],
+                     dict(k=None, v=0x2000, keep=0x3000, kl=0x4000, bl=None, bt=0x5000, dst=None, n=2, kh=1, ks=8,
+                          hkv=4, d=64, bs=8, m=4, dm=0, nb=16, dt=0, err=None, st=None))
+    assert compact(ks=1 << 30) == INV and compact(ks=(1 << 30) + 1) == UNS
+
+
 def test_binding_refusals():
     """The binding refuses what the C interface cannot see: shapes, types, and
     tensors off the GPU."""
