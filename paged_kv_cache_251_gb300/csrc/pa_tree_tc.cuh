@@ -21,7 +21,7 @@
 // tokens would cost three quarters of one of 128, as it rereads Q, and the
 // tensor cores are the scarce part there).  P overwrites S, and goes to its
 // product in halves of 64 tokens.
-
+//
 // P's rounding (Parts): a 16-bit output takes P rounded once to the type of V
 // (the output is rounded as coarsely); an fp32 output takes hi + lo parts
 // (hi = round(p), lo = round(p - hi)), two accumulating products.
@@ -105,7 +105,9 @@ struct TcMisc {
     uint32_t meta[kTcMeta];
     uint32_t zmask[kTcRecords];
     int32_t zid[kTcRecords][kTcMaxBpt];
-    uint32_t poison[2][4];
+    // votes of the warps of a warpgroup, by tile parity: a warp may be a tile ahead of
+    // another of its warpgroup, not two (the S after next waits for all of them)
+    uint32_t poison[2][2][4];
     int oinit[2];
     uint32_t tmem;
     float2 ml[2][128];
@@ -910,6 +912,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                     }
                     const int tok = tok0 + tk;
                     const bool valid = ((blocks >> (tk >> lbs)) & 1u) && tok < it.len;
+                    uint32_t *poison = M->poison[t & 1u][wg];
                     bool drop = !valid;  // this token's V row must not be multiplied
                     if (__any_sync(0xffffffffu, drop) || drafts)
                         if (!mbar_wait_bounded(&M->vfull[vstage], (t / C::kSV) & 1u))
@@ -926,12 +929,12 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                         }
                         const uint32_t votes = __ballot_sync(0xffffffffu, bad);
                         if (lane == 0)
-                            M->poison[wg][quarter] = votes;
+                            poison[quarter] = votes;
                         if (!arrive_wait(pzbar, pzc++))
                             return false;
                         poisoned =
-                            (M->poison[wg][0] | M->poison[wg][1] | M->poison[wg][2] | M->poison[wg][3]) != 0;
-                        drop = drop || tc_poison<Units>(M->poison[wg], tk);
+                            (poison[0] | poison[1] | poison[2] | poison[3]) != 0;
+                        drop = drop || tc_poison<Units>(poison, tk);
                     }
                     if (warp_live) {
                         tmem_wait_ld();
@@ -959,7 +962,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = !first && mn == m ? o[e] : (alpha == 0.f ? 0.f : o[e] * alpha);
                                 for (int u = 0; u < kTok; ++u) {
-                                    if (!tc_poison<Units>(M->poison[wg], u))
+                                    if (!tc_poison<Units>(poison, u))
                                         continue;
                                     float x[2];
                                     tmem_ld<2>(s_addr + (u & ~1), x);
