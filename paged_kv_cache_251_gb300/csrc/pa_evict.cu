@@ -54,13 +54,24 @@ constexpr int kSelMaxSlice = 48 * 1024;           // scores a CTA holds in share
 constexpr int kSelMaxCluster = 8;
 
 struct SelectShared {
-    uint32_t hist[kSelBins];        // of this CTA's slice
-    uint32_t all[2][kSelBins];      // of the row, by pass parity (clusters)
+    uint32_t hist[kSelBins];  // of this CTA's slice
+    uint32_t all[kSelBins];   // of the row (clusters)
+    uint32_t part[kSelBins];  // every CTA's counts of this CTA's share of the bins (clusters)
     uint32_t warp_sum[kSelWarps];
     uint32_t warp_count[2][kSelWarps];  // by round parity: kept surely | equal << 16
     uint32_t digit, above;
     uint32_t count[2];  // of the slice: kept surely, equal to the k-th
 };
+
+// One count more where `on`, without a branch (a taken branch an element cost 20
+// cycles of a warp's 32, the atomic itself 5).
+__device__ inline void count_if(bool on, uint32_t *bin) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(
+            static_cast<uint32_t>(__cvta_generic_to_shared(bin))),
+        "r"(static_cast<uint32_t>(on))
+        : "memory");
+}
 
 // grid: (kv heads x cluster, sequences); a cluster of p.cluster CTAs takes a
 // row.  Cached: the slices are in shared memory.  Otherwise (rows longer than
@@ -93,68 +104,107 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         p.new_lens[s] = n;
     const int C = L > p.budget ? L - p.recent : 0;  // candidates
     const int k = L > p.budget ? p.budget - p.recent : 0;
-    // this CTA's tokens [lo, hi)
-    const int per = Cached ? (L + ranks - 1) / ranks : L;
+    // this CTA's tokens [lo, hi): slices of whole 16-byte groups
+    const int per = Cached ? ((L + ranks - 1) / ranks + 3) & ~3 : L;
     const int lo = min(L, rank * per), hi = min(L, lo + per);
+    const int chi = max(lo, min(hi, C));  // the slice's candidates: [lo, chi)
+    for (int i = tid; i < kSelBins; i += kSelThreads)
+        sh->hist[i] = 0;
+    __syncthreads();
     if (Cached) {
+        // the slice, canonical; its first histogram on the way (unless nothing is chosen: chi == lo)
+        auto first = [&](int t, float x) { count_if(t < chi, &sh->hist[order_of(x) >> 21]); };
+        int i = tid, n4 = 0;
         if ((reinterpret_cast<uintptr_t>(in + lo) & 15u) == 0) {
-            const int n4 = (hi - lo) / 4;
-            for (int i = tid; i < n4; i += kSelThreads)
-                {
-                const float4 v = reinterpret_cast<const float4 *>(in + lo)[i];
-                reinterpret_cast<float4 *>(slice)[i] =
-                    make_float4(canonical(v.x), canonical(v.y), canonical(v.z), canonical(v.w));
+            n4 = (hi - lo) / 4;
+            constexpr int kAhead = 4;  // loads of a thread in flight
+            const float4 *in4 = reinterpret_cast<const float4 *>(in + lo);
+            for (; i < n4; i += kAhead * kSelThreads) {
+                float4 v[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (i + u * kSelThreads < n4)
+                        v[u] = in4[i + u * kSelThreads];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int j = i + u * kSelThreads;
+                    if (j < n4) {
+                        const float4 c = make_float4(canonical(v[u].x), canonical(v[u].y), canonical(v[u].z),
+                                                     canonical(v[u].w));
+                        reinterpret_cast<float4 *>(slice)[j] = c;
+                        first(lo + 4 * j, c.x);
+                        first(lo + 4 * j + 1, c.y);
+                        first(lo + 4 * j + 2, c.z);
+                        first(lo + 4 * j + 3, c.w);
+                    }
+                }
             }
-            for (int i = n4 * 4 + tid; i < hi - lo; i += kSelThreads)
-                slice[i] = canonical(in[lo + i]);
-        } else {
-            for (int i = tid; i < hi - lo; i += kSelThreads)
-                slice[i] = canonical(in[lo + i]);
         }
-    }
-    if (ranks > 1) {
-        for (int i = tid; i < 2 * kSelBins; i += kSelThreads)
-            sh->all[0][i] = 0;
-        cluster.sync();  // (no CTA adds to another's before it is zero)
+        for (int j = n4 * 4 + tid; j < hi - lo; j += kSelThreads) {
+            const float c = canonical(in[lo + j]);
+            slice[j] = c;
+            first(lo + j, c);
+        }
     }
     auto score = [&](int t) -> float { return Cached ? slice[t - lo] : canonical(in[t]); };
 
-    uint32_t kth = 0, above = 0;  // the k-th largest image, scores above it
+    uint32_t kth = 0, above = 0;     // the k-th largest image, scores above it
+    uint32_t own_above = 0, own_equal = 0;  // this slice's share: of the thread's bins (sums over threads), equal to the k-th
     if (k > 0) {
-        const int chi = min(hi, C);
         uint32_t need = k;
 #pragma unroll
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const uint32_t high = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
             const uint32_t digits = pass == 2 ? 1023u : 2047u;
-            uint32_t *hist = sh->hist, *all = ranks > 1 ? sh->all[pass & 1] : hist;
-            for (int i = tid; i < kSelBins; i += kSelThreads)
-                hist[i] = 0;
-            __syncthreads();  // (the slice is loaded, too)
+            uint32_t *hist = sh->hist, *all = ranks > 1 ? sh->all : hist;
+            auto count = [&](float x) {
+                const uint32_t u = order_of(x);
+                count_if((u & high) == (kth & high), &hist[(u >> shift) & digits]);
+            };
+            if (Cached && pass > 0) {
+                const int n4 = (chi - lo) / 4;
+#pragma unroll 2
+                for (int i = tid; i < n4; i += kSelThreads) {
+                    const float4 x = reinterpret_cast<const float4 *>(slice)[i];
+                    count(x.x);
+                    count(x.y);
+                    count(x.z);
+                    count(x.w);
+                }
+                if (tid < chi - lo - 4 * n4)
+                    count(slice[4 * n4 + tid]);
+            } else if (!Cached) {
 #pragma unroll 4
-            for (int t = lo + tid; t < chi; t += kSelThreads) {
-                const uint32_t u = order_of(score(t));
-                if ((u & high) == (kth & high))
-                    atomicAdd(&hist[(u >> shift) & digits], 1u);
+                for (int t = lo + tid; t < chi; t += kSelThreads)
+                    count(score(t));
             }
-            __syncthreads();
             const int top = kSelBins - 1 - 4 * tid;  // thread tid: bins top, top - 1, top - 2, top - 3
             if (ranks > 1) {
-                // this slice's counts to every CTA of the row: only the digits it has (a
-                // whole histogram read from 7 others took 7000 cycles)
-                const uint4 v = *reinterpret_cast<const uint4 *>(hist + top - 3);
-                const uint32_t mine4[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (mine4[i])
-                        for (int r = 0; r < ranks; ++r)
-                            atomicAdd(cluster.map_shared_rank(all, r) + top - 3 + i, mine4[i]);
+                // The row's histogram in every CTA: rank r sums bins [r, r + 1) 2048 / ranks over the
+                // slices, and gives its sums to all.  One 16-byte access of a thread to another CTA's
+                // memory each way (counts added there by remote atomics took 13000 cycles a pass
+                // with many digits in use).
+                cluster.sync();  // every slice is counted
+                const int quads = kSelThreads / ranks, q = tid % quads, r = tid / quads;
+                const int share = rank * (kSelBins / ranks) + 4 * q;
+                reinterpret_cast<uint4 *>(sh->part)[tid] =
+                    *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(hist, r) + share);
+                __syncthreads();
+                uint4 sum = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < ranks; ++i) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(sh->part)[i * quads + q];
+                    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+                }
+                *reinterpret_cast<uint4 *>(cluster.map_shared_rank(all, r) + share) = sum;
                 cluster.sync();
+            } else {
+                __syncthreads();
             }
             // suffix counts, from the top
             const uint4 v = *reinterpret_cast<const uint4 *>(all + top - 3);
-            const uint32_t c[4] = {v.w, v.z, v.y, v.x};
+            const uint4 ov = *reinterpret_cast<const uint4 *>(hist + top - 3);
+            const uint32_t c[4] = {v.w, v.z, v.y, v.x}, own[4] = {ov.w, ov.z, ov.y, ov.x};
             const uint32_t mine = c[0] + c[1] + c[2] + c[3];
             // (counts up to 2^31: a plain scan, not the packed one)
             uint32_t x = mine;
@@ -174,18 +224,26 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 before += w < warp ? sh->warp_sum[w] : 0;
             if (before < need && before + mine >= need) {
                 int b = 0;
-                while (before + c[b] < need)
-                    before += c[b++];
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (b == i && before + c[i] < need)
+                        before += c[i], b = i + 1;
                 sh->digit = static_cast<uint32_t>(top - b);
                 sh->above = before;
             }
+            if (pass < 2)  // for the next pass (everyone has read the counts)
+                *reinterpret_cast<uint4 *>(hist + top - 3) = make_uint4(0, 0, 0, 0);
             __syncthreads();
-            kth |= sh->digit << shift;
+            const uint32_t digit = sh->digit;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                own_above += static_cast<uint32_t>(top - i) > digit ? own[i] : 0;
+                if (pass == 2 && static_cast<uint32_t>(top - i) == digit)
+                    own_equal = own[i];
+            }
+            kth |= digit << shift;
             above += sh->above;
             need -= sh->above;
-            if (ranks > 1)  // for the pass after next: its counts come after another cluster barrier
-                *reinterpret_cast<uint4 *>(all + top - 3) = make_uint4(0, 0, 0, 0);
-            __syncthreads();
         }
     }
     const uint32_t equal = k - above;  // scores equal to the k-th that are kept: the first ones
@@ -203,23 +261,16 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const int lane = tid & 31, warp = tid >> 5;
     uint32_t kept = 0, seen = 0;  // in the tokens before: kept surely, equal
     if (ranks > 1) {
-        uint32_t a = 0, e = 0;
-#pragma unroll 4
-        for (int t = lo + tid; t < hi; t += kSelThreads) {
-            bool sure, eq;
-            float x;
-            classify(t, sure, eq, x);
-            a += sure, e += eq;
+        if (tid == 0) {
+            sh->count[0] = max(0, hi - max(lo, C));  // recent ones (of a short context: all)
+            sh->count[1] = 0;
         }
-        if (tid == 0)
-            sh->count[0] = sh->count[1] = 0;
         __syncthreads();
-        a = __reduce_add_sync(0xffffffffu, a);
-        e = __reduce_add_sync(0xffffffffu, e);
-        if (lane == 0) {
-            atomicAdd(&sh->count[0], a);
-            atomicAdd(&sh->count[1], e);
-        }
+        own_above = __reduce_add_sync(0xffffffffu, own_above);
+        if (lane == 0 && own_above)
+            atomicAdd(&sh->count[0], own_above);
+        if (own_equal)
+            sh->count[1] = own_equal;
         // (also: every slice is in shared memory before any score is written, which may be over them)
         cluster.sync();
         for (int r = 0; r < rank; ++r) {
@@ -256,8 +307,24 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
         const uint32_t total = __reduce_add_sync(0xffffffffu, c);
         uint32_t place_sure = kept + (before & 0xffffu), rank_eq = seen + (before >> 16);
+        if ((mine >> 16) == 0) {  // (of the warp's tokens none is equal to the k-th: nearly always)
+            place_sure += min(rank_eq, equal);
 #pragma unroll
-        for (int i = 0; i < kSelPer; ++i) {
+            for (int i = 0; i < kSelPer; ++i) {
+                const bool sure = (sure_bits >> i) & 1u;
+                const uint32_t sures = __ballot_sync(0xffffffffu, sure);
+                if (sure) {
+                    const uint32_t place = place_sure + __popc(sures & ((1u << lane) - 1u));
+                    keep[place] = t1 + 32 * i;
+                    if (out)
+                        out[place] = x[i];
+                }
+                place_sure += __popc(sures);
+            }
+            mine = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kSelPer && mine; ++i) {
             const bool sure = (sure_bits >> i) & 1u, eq = (eq_bits >> i) & 1u;
             const uint32_t sures = __ballot_sync(0xffffffffu, sure), eqs = __ballot_sync(0xffffffffu, eq);
             const uint32_t below = (1u << lane) - 1u;
@@ -277,9 +344,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     __syncthreads();
     for (int i = n + rank * kSelThreads + tid; i < p.budget; i += ranks * kSelThreads)
         keep[i] = -1;
-    if (out)
-        for (long long i = n + rank * kSelThreads + tid; i < p.stride; i += ranks * kSelThreads)
-            out[i] = 0.f;
+    if (out) {
+        // up to a 16-byte boundary, four at a time, the rest
+        const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out + n) & 15u)) & 15u) / 4;
+        const long long from = min(static_cast<long long>(n + head), p.stride);
+        const long long n4 = (p.stride - from) / 4, rest = from + 4 * n4;
+        if (rank == 0 && tid < from - n)
+            out[n + tid] = 0.f;
+        for (long long j = rank * kSelThreads + tid; j < n4; j += ranks * kSelThreads)
+            reinterpret_cast<float4 *>(out + from)[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (rank == 0 && tid < p.stride - rest)
+            out[rest + tid] = 0.f;
+    }
     if (ranks > 1)
         cluster.sync();  // no CTA leaves while another may read its counts
 }
