@@ -345,7 +345,7 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
             const int tree_rows = num_draft * (num_heads / num_kv_heads);
             const size_t ctas = tree_tc_ctas(num_seqs, num_kv_heads, tree_rows, p.max_len, kTreeSms);
             p.cuts = static_cast<int4 *>(workspace);
-            p.part_acc = reinterpret_cast<float *>(p.cuts + ctas);
+            p.part_acc = reinterpret_cast<float *>(p.cuts + 2 * ctas);
             p.part_ml = p.part_acc + 2 * ctas * (tree_rows < 256 ? tree_rows : 256) * head_dim;
         } else {
             p.part_acc = static_cast<float *>(workspace);

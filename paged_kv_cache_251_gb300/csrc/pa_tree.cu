@@ -71,20 +71,14 @@ pa_status launch_tc(TreeParams &p, int dtype, int head_dim, int dev, int sms, cu
     // a context of one tile is never cut
     if (grid > 1 && p.max_len > 128) {
         const int slot_rows = units == 2 ? tc_slot_rows<2>(rows) : tc_slot_rows<1>(rows);
-        const int lrb = tree_merge_log_rows(slot_rows, head_dim);
-        const int chunks = (slot_rows + (1 << lrb) - 1) >> lrb;
-        const int col_chunks = head_dim / (kTreeMergeCols * (32 >> lrb));  // a power of two
-        // few enough CTAs that the ones without a record to merge cost little
-        int steps = 1;
-        while (steps < col_chunks && static_cast<long long>(grid) * chunks * (col_chunks / steps) > 16LL * sms)
-            steps *= 2;
-        const dim3 mgrid(grid, chunks, col_chunks / steps);
+        const int lrb = tc_merge_log_rows(slot_rows, head_dim);
+        const dim3 mgrid(grid, (slot_rows + (1 << lrb) - 1) >> lrb);
         const void *mf = head_dim == 64 ? (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 2>)
                                                       : reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 1>))
                                         : (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<128, 2>)
                                                       : reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<128, 1>));
-        void *margs[] = {&p, &steps};
-        e = launch_dependent(mf, mgrid, dim3(kTreeMergeThreads), margs, 0, stream);
+        void *margs[] = {&p};
+        e = launch_dependent(mf, mgrid, dim3(kTcMergeThreads), margs, 0, stream);
         if (e != cudaSuccess)
             return cuda_fail(e, "tree merge launch");
     }
@@ -110,8 +104,10 @@ int tree_tc_ctas(int num_seqs, int num_kv_heads, int rows, int max_len, int sms)
 size_t tree_tc_workspace(int num_seqs, int num_kv_heads, int rows, int head_dim, int max_len) {
     const int ctas = tree_tc_ctas(num_seqs, num_kv_heads, rows, max_len, kTreeSms);
     const size_t slot_rows = static_cast<size_t>(rows < 256 ? rows : 256);
-    // two partials and a merge record a CTA
-    return ctas > 1 && max_len > 128 ? static_cast<size_t>(ctas) * (2 * slot_rows * (head_dim + 2) * sizeof(float) + sizeof(int4)) : 0;
+    // two partials a CTA, each with a merge record
+    return ctas > 1 && max_len > 128
+               ? 2 * static_cast<size_t>(ctas) * (slot_rows * (head_dim + 2) * sizeof(float) + sizeof(int4))
+               : 0;
 }
 
 pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t stream) {

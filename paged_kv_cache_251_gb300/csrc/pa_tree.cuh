@@ -21,7 +21,7 @@ struct TreeParams : DecodeParams {
     const uint64_t *mask;       // [num_seqs][num_draft][words] or nullptr (chain)
     int num_draft, words;
     int row_tiles;  // tiles of rows a (sequence, kv head)
-    int4 *cuts;     // tensor-core kernel: a record per CTA for the merge, or nullptr
+    int4 *cuts;     // tensor-core kernel: two records a CTA for the merge, or nullptr
 };
 
 // Cached tokens and drafted tokens of sequence s, clamped.

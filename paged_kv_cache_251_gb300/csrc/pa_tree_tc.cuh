@@ -319,7 +319,7 @@ struct TcChunk {
     int s = -1, kvh, rt, slot;
     int tile0, ntiles;  // of the item
     int lo, hi;         // of the chunk, in tiles of the sequence
-    int parts;          // slot 1: CTAs that hold a part of the pair
+    int first, parts;   // slots 0 and 1: the CTA that begins the pair, and how many hold a part of it
     int nblk;           // blocks of the sequence
     int tb[kMaxBpp / 32];
 };
@@ -367,9 +367,10 @@ struct TcWalk {
         c.kvh = j / p.row_tiles;
         c.rt = j - c.kvh * p.row_tiles;
         c.slot = hi - lo == tiles ? -1 : (lo > 0 ? 0 : 1);
-        if (c.slot == 1) {  // up to the CTA of the pair's last unit
-            const long long last = start + kTcPairCost + tiles - 1;
-            c.parts = static_cast<int>(((last + 1) * spans - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+        if (c.slot >= 0) {  // from the CTA of the pair's first tile to that of its last
+            const long long one = start + kTcPairCost, last = one + tiles - 1;
+            c.first = static_cast<int>(((one + 1) * spans - 1) / total);
+            c.parts = static_cast<int>(((last + 1) * spans - 1) / total) - c.first + 1;
         }
         c.tile0 = lo;
         c.ntiles = hi - lo;
@@ -411,9 +412,8 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
     TcWalk walk;
     TcChunk cur, nxt;
     walk.begin(p, pairs_per_seq);
-    // the merge's record of this CTA: the pair that its second partial begins,
-    // and the parts that pair is in
-    int4 cut = make_int4(0, 0, 0, 0);
+    // the merge's records of this CTA: the pairs of its partials 0 and 1, or zeros
+    uint32_t cuts = 0;
     walk.next(p, pairs_per_seq, cur);
     uint32_t t = 0, k = 0;
     bool ok = true;
@@ -433,8 +433,12 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
                 __syncwarp();
                 break;
             }
-            if (cur.slot == 1)
-                cut = make_int4(cur.s, cur.kvh, cur.rt, cur.parts);
+            if (cur.slot >= 0) {
+                cuts |= 1u << cur.slot;
+                if (lane == 0)
+                    p.cuts[2 * blockIdx.x + cur.slot] =
+                        make_int4(cur.s, cur.kvh * p.row_tiles + cur.rt, cur.first, cur.parts);
+            }
             if (lane == 0) {
                 const TreeSeq q = tree_seq(p, cur.s);
                 if (q.bad && cur.tile0 == 0 && cur.kvh == 0 && cur.rt == 0 && p.err)
@@ -500,8 +504,8 @@ __device__ inline void tc_kproducer(const TreeParams &p, const CUtensorMap *tmk,
             break;
         cur = nxt;
     }
-    if (lane == 0 && p.cuts)
-        p.cuts[blockIdx.x] = cut;
+    if (p.cuts && lane < 2 && !((cuts >> lane) & 1u))
+        p.cuts[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
     // no more tiles for the V producer (after a failed wait too)
     if (lane == 0) {
         const int rec = static_cast<int>(t % kTcRecords);
@@ -728,33 +732,33 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
 // ---------------------------------------------------------------------------
 // Softmax and epilogue
 
-// 32 columns of an accumulator row to the output.
-__device__ inline void store_cols32(void *out, int dtype, long long idx, const float *v) {
+// N columns of an accumulator row to the output (a multiple of 8).
+template <int N> __device__ inline void store_cols(void *out, int dtype, long long idx, const float *v) {
     if (dtype == PA_F32) {
         float *o = static_cast<float *>(out) + idx;
         if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < N; i += 4)
                 *reinterpret_cast<float4 *>(o + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < N; ++i)
                 o[i] = v[i];
         }
         return;
     }
     uint16_t *o = static_cast<uint16_t *>(out) + idx;
-    uint32_t w[16];
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < N / 2; ++e)
         w[e] = dtype == PA_F16 ? pack2<__half>(v[2 * e], v[2 * e + 1]) : pack2<__nv_bfloat16>(v[2 * e], v[2 * e + 1]);
     if ((reinterpret_cast<uintptr_t>(o) & 15u) == 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < N / 8; ++i)
             reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < N / 2; ++e)
             o[2 * e] = static_cast<uint16_t>(w[e]), o[2 * e + 1] = static_cast<uint16_t>(w[e] >> 16);
     }
 }
@@ -1141,7 +1145,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 }
                 if (direct) {
                     if (stored)
-                        store_cols32(p.out, p.out_dtype, orow * D + c, o);
+                        store_cols<32>(p.out, p.out_dtype, orow * D + c, o);
                 } else if (stored && den != 0.f) {
                     float *a = p.part_acc + (item * D + c) * rows + ir;
 #pragma unroll
@@ -1176,8 +1180,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (smem_addr(smem) & 1023u) {
         if (threadIdx.x == 0 && p.err)
             atomicOr(p.err, PA_DEVERR_BAD_LAUNCH);
-        if (threadIdx.x == 0 && p.cuts)
-            p.cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+        if (threadIdx.x < 2 && p.cuts)
+            p.cuts[2 * blockIdx.x + threadIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
     TcMisc *M = reinterpret_cast<TcMisc *>(smem + C::kOffMisc);
@@ -1258,89 +1262,128 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Merge of the pairs that a span boundary cuts: CTA c's second partial begins
-// such a pair (its record says which, and in how many parts), the first partials
-// of the CTAs after it continue it.  grid: CTA of the tree kernel, row chunk,
-// column group; a CTA's lanes are RB rows x 32 / RB columns (whole lines of the
-// column-major partials) with kTreeMergeCols columns each, `steps` times over,
-// and its 8 warps take every eighth part.
+// Merge of the pairs that a span boundary cuts: CTA f's second partial begins
+// such a pair, the first partials of CTAs f + 1 .. f + P - 1 continue it.  The
+// work goes back to the P CTAs (grid.x) that made the parts: the j-th takes every
+// P-th column group, so each reads about as much as it wrote, in one or two round
+// trips whatever P is (one CTA of a pair for all its columns, or for 16 of them
+// with warps over the parts, took 14 us on the ragged batch and 22 us on
+// the long contexts, against 7 and 13).  grid.y: chunks of RB rows.  A warp's
+// lanes are RB rows x 32 / RB column groups of kTcMergeCols columns (whole
+// lines of the column-major partials); its 8 warps take different groups, or, when
+// a CTA has fewer, share the parts of one and meet in shared memory.
+constexpr int kTcMergeThreads = 256;
+constexpr int kTcMergeWarps = kTcMergeThreads / 32;
+constexpr int kTcMergeCols = 8;
+
+// log2 of RB for `rows` rows: at most 32, and no less than what a warp's columns within D leave
+__host__ __device__ inline int tc_merge_log_rows(int rows, int D) {
+    int l = D == 64 ? 2 : 1;
+    while (l < 5 && (1 << l) < rows)
+        ++l;
+    return l;
+}
+
+// The state of a row over some parts: running maximum, denominator, numerators.
+struct TcMergeState {
+    float m = -INFINITY, den = 0.f, num[kTcMergeCols] = {};
+    // x, v: a part's accumulators and (maximum, denominator); one that attended
+    // nothing (v.y == 0) left no accumulators
+    __device__ inline void add(float2 v, const float *x) {
+        if (v.y == 0.f)
+            return;
+        const float mn = fmaxf(m, v.x);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(v.x - mn);
+        den = den * keep + v.y * w;
+#pragma unroll
+        for (int e = 0; e < kTcMergeCols; ++e)
+            num[e] = num[e] * keep + x[e] * w;
+        m = mn;
+    }
+};
+
 template <int D, int Units>
-__global__ void __launch_bounds__(kTreeMergeThreads, 3) pa_tree_tc_merge_kernel(const TreeParams p, int steps) {
+__global__ void __launch_bounds__(kTcMergeThreads, 4) pa_tree_tc_merge_kernel(const TreeParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int E = kTreeMergeCols;
-    __shared__ float acc[kTreeMergeWarps][E][33];  // [warp][element][lane]
-    __shared__ float2 state[kTreeMergeWarps][32];
-    const int4 cut = p.cuts[blockIdx.x];
-    const int nparts = cut.w;
-    if (nparts == 0)
-        return;
+    constexpr int E = kTcMergeCols;
+    __shared__ float acc[kTcMergeWarps][E + 2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int4 cut[2] = {p.cuts[2 * blockIdx.x], p.cuts[2 * blockIdx.x + 1]};
     const int G = p.num_heads / p.num_kv_heads;
     const int all_rows = p.num_draft * G, rows = tc_slot_rows<Units>(all_rows);
-    const int lrb = tree_merge_log_rows(rows, D);
-    const int RB = 1 << lrb, CB = 32 >> lrb;
-    const int r0 = blockIdx.y << lrb;
-    for (int step = 0; step < steps; ++step) {
-        const int col0 = (static_cast<int>(blockIdx.z) * steps + step) * (E * CB);
-        const int r = r0 + (lane & (RB - 1));
-        float M = -INFINITY, den = 0.f, num[E];
+    const int lrb = tc_merge_log_rows(rows, D);
+    const int groups = (D / E) >> (5 - lrb);  // column groups of a warp's width
+    const int r = (blockIdx.y << lrb) + (lane & ((1 << lrb) - 1));
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            num[e] = 0.f;
-        if (r < rows) {
-            for (int q = warp; q < nparts; q += kTreeMergeWarps) {
-                // part 0: this CTA's partial 1; part q: partial 0 of the q-th CTA after it
-                const long long slot = 2LL * (blockIdx.x + q) + (q == 0);
-                const float2 v = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
-                const float *a = p.part_acc + (slot * D + col0 + (lane >> lrb)) * rows + r;
-                float x[E];
+    for (int job = 0; job < 2; ++job) {
+        const int parts = cut[job].w, first = cut[job].z;
+        if (parts == 0)
+            continue;
+        const int j = static_cast<int>(blockIdx.x) - first;
+        const int mine = groups > j ? (groups - j + parts - 1) / parts : 0;
+        if (mine == 0)
+            continue;
+        int cw = 1;  // warps over column groups; the others over parts
+        while (cw < kTcMergeWarps && cw < mine)
+            cw *= 2;
+        const int pw = kTcMergeWarps / cw;
+        const int full = cut[job].y % p.row_tiles * Units * 128 + r;  // row of the (sequence, kv head)
+        const bool live = r < rows && full < all_rows;
+        const long long orow = (static_cast<long long>(cut[job].x) * p.num_draft + full / G) * p.num_heads +
+                               cut[job].y / p.row_tiles * G + full % G;
+        // (one turn when warps share parts: cw >= mine then)
+        for (int k0 = 0; k0 < mine; k0 += cw) {
+            const int k = k0 + warp % cw;
+            const int col = (((j + k * parts) << (5 - lrb)) + (lane >> lrb)) * E;
+            TcMergeState st;
+            if (live && k < mine) {
+                // part 0: the first CTA's partial 1; part q: partial 0 of the q-th CTA after it
+                for (int q = warp / cw; q < parts; q += 2 * pw) {
+                    float2 v[2];
+                    float x[2][E];
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    x[e] = a[static_cast<long long>(e * CB) * rows];
-                if (v.y == 0.f)  // it attended nothing there, and left no accumulator
-                    continue;
-                const float mn = fmaxf(M, v.x);
-                const float keep = M == -INFINITY ? 0.f : exp2f(M - mn), add = exp2f(v.x - mn);
-                den = den * keep + v.y * add;
+                    for (int u = 0; u < 2; ++u) {
+                        const int part = q + u * pw;
+                        v[u] = make_float2(0.f, 0.f);
+                        if (part < parts) {
+                            const long long slot = 2LL * (first + part) + (part == 0);
+                            v[u] = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
+                            const float *a = p.part_acc + (slot * D + col) * rows + r;
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    num[e] = num[e] * keep + x[e] * add;
-                M = mn;
-            }
-        }
-        state[warp][lane] = make_float2(M, den);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[warp][e][lane] = num[e];
-        __syncthreads();
-        // output o of the CTA: row o / (E CB), column o % (E CB)
-        for (int o = threadIdx.x; o < 32 * E; o += kTreeMergeThreads) {
-            const int rr = o / (E * CB), c = o - rr * (E * CB);
-            const int full = cut.z * Units * 128 + r0 + rr;  // row of the (sequence, kv head)
-            if (r0 + rr >= rows || full >= all_rows)
-                break;
-            const int e = c / CB, ln = ((c - e * CB) << lrb) + rr;
-            float m = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kTreeMergeWarps; ++w)
-                if (state[w][ln].y != 0.f)
-                    m = fmaxf(m, state[w][ln].x);
-            float n = 0.f, d = 0.f;
-#pragma unroll
-            for (int w = 0; w < kTreeMergeWarps; ++w) {
-                const float2 v = state[w][ln];
-                if (v.y != 0.f) {
-                    const float sc = v.x == m ? 1.f : exp2f(v.x - m);
-                    d = fmaf(v.y, sc, d);
-                    n = fmaf(acc[w][e][ln], sc, n);
+                            for (int e = 0; e < E; ++e)
+                                x[u][e] = a[static_cast<long long>(e) * rows];
+                        }
+                    }
+                    st.add(v[0], x[0]);
+                    st.add(v[1], x[1]);
                 }
             }
-            const long long orow =
-                (static_cast<long long>(cut.x) * p.num_draft + full / G) * p.num_heads + cut.y * G + full % G;
-            store_out(p.out, p.out_dtype, orow * D + col0 + c, d == 0.f ? 0.f : n / d);
+            if (pw > 1) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[warp][e][lane] = st.num[e];
+                acc[warp][E][lane] = st.m;
+                acc[warp][E + 1][lane] = st.den;
+                __syncthreads();
+                if (warp < cw)
+                    for (int w = warp + cw; w < kTcMergeWarps; w += cw) {
+                        float x[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            x[e] = acc[w][e][lane];
+                        st.add(make_float2(acc[w][E][lane], acc[w][E + 1][lane]), x);
+                    }
+            }
+            if (live && k < mine && (pw == 1 || warp < cw)) {
+                const float inv = st.den == 0.f ? 0.f : 1.f / st.den;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    st.num[e] = st.den == 0.f ? 0.f : st.num[e] * inv;
+                store_cols<E>(p.out, p.out_dtype, orow * D + col, st.num);
+            }
         }
-        __syncthreads();
+        __syncthreads();  // (before the next job's states)
     }
 }
 

@@ -79,10 +79,10 @@ def test_tree_workspace_size(lib):
     f.restype, f.argtypes = SZ, [I] * 8
     F32, BF16 = 0, 2
     assert f(4, 8, 8, 2, 128, 16, 8, BF16) == 0                       # contexts of one 128-token tile are never cut
-    assert f(4, 8, 8, 2, 128, 16, 9, BF16) == 16 * (2 * 32 * 130 * 4 + 16)   # two partials (32 rows) and a record for each of 16 CTAs
-    assert f(64, 16, 32, 8, 128, 16, 512, BF16) == 152 * (2 * 64 * 130 * 4 + 16)
-    assert f(4, 64, 32, 8, 128, 16, 8192, BF16) == 152 * (2 * 256 * 130 * 4 + 16)
-    assert f(4, 256, 64, 8, 64, 16, 8192, BF16) == 152 * (2 * 256 * 66 * 4 + 16)   # 2048 rows: tiles of 256
+    assert f(4, 8, 8, 2, 128, 16, 9, BF16) == 16 * (2 * 32 * 130 * 4 + 32)   # two partials (32 rows), a record each, for 16 CTAs
+    assert f(64, 16, 32, 8, 128, 16, 512, BF16) == 152 * (2 * 64 * 130 * 4 + 32)
+    assert f(4, 64, 32, 8, 128, 16, 8192, BF16) == 152 * (2 * 256 * 130 * 4 + 32)
+    assert f(4, 256, 64, 8, 64, 16, 8192, BF16) == 152 * (2 * 256 * 66 * 4 + 32)   # 2048 rows: tiles of 256
     assert f(4, 8, 8, 2, 128, 16, 16, F32) == 0                       # one 256-token partition
     assert f(4, 8, 8, 2, 128, 16, 64, F32) == 4 * 8 * 8 * 4 * 130 * 4
     assert f(4, 0, 8, 2, 128, 16, 64, F32) == 0 and f(4, 8, 9, 2, 128, 16, 64, F32) == 0

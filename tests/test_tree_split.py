@@ -15,8 +15,8 @@ COST = int(re.search(r"constexpr int kTcPairCost = (\d+);", SOURCE.read_text()).
 
 
 def split(tiles, pairs_per_seq, ctas):
-    """Every CTA's items (pair, first tile, end, slot) and its merge record
-    (pair, parts) or None."""
+    """Every CTA's items (pair, first tile, end, slot) and its merge records: by
+    slot, (pair, first CTA, parts) or None."""
     pairs = [t for t in tiles for _ in range(pairs_per_seq)]
     starts, total = [], 0
     for t in pairs:
@@ -25,7 +25,7 @@ def split(tiles, pairs_per_seq, ctas):
     spans = min(ctas, max(total, 1))
     items, records = [], []
     for c in range(ctas):
-        mine, record = [], None
+        mine, record = [], [None, None]
         if c < spans:
             u0, u1 = total * c // spans, total * (c + 1) // spans
             for i, (t, start) in enumerate(zip(pairs, starts)):
@@ -33,9 +33,9 @@ def split(tiles, pairs_per_seq, ctas):
                 if start >= u1 or not (hi > lo or (t == 0 and start >= u0)):
                     continue
                 slot = -1 if hi - lo == t else (0 if lo > 0 else 1)
-                if slot == 1:
-                    last = start + COST + t - 1
-                    record = (i, ((last + 1) * spans - 1) // total - c + 1)
+                if slot >= 0:
+                    first = ((start + COST + 1) * spans - 1) // total
+                    record[slot] = (i, first, ((start + COST + t) * spans - 1) // total - first + 1)
                 mine.append((i, lo, hi, slot))
         items.append(mine)
         records.append(record)
@@ -62,12 +62,14 @@ def test_even_split(seed):
             assert len(segs) == 1 or t > 1
             if len(segs) > 1:
                 cut.add(i)
-        merged = [rec for rec in records if rec]
-        assert {i for i, _ in merged} == cut and len(merged) == len(cut)
-        for c, rec in enumerate(records):
-            if rec:                                        # partial 1 of CTA c, partial 0 of those after it
-                want = [(c, 1)] + [(c + q, 0) for q in range(1, rec[1])]
-                assert [(cc, slot) for _, _, cc, slot in sorted(parts[rec[0]])] == want
+        assert {rec[0] for both in records for rec in both if rec} == cut
+        for c, both in enumerate(records):
+            for slot, rec in enumerate(both):
+                if rec:                                    # partial 1 of the first CTA, partial 0 of those after it
+                    i, first, n = rec
+                    want = [(first, 1)] + [(first + q, 0) for q in range(1, n)]
+                    assert [(cc, sl) for _, _, cc, sl in sorted(parts[i])] == want and (c, slot) in want
+        assert sum(rec is not None for both in records for rec in both) == sum(len(parts[i]) for i in cut)
 
 
 def test_spans_are_even():
