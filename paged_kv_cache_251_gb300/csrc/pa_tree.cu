@@ -72,7 +72,7 @@ pa_status launch_tc(TreeParams &p, int dtype, int head_dim, int dev, int sms, cu
     if (grid > 1 && p.max_len > 128) {
         const int slot_rows = units == 2 ? tc_slot_rows<2>(rows) : tc_slot_rows<1>(rows);
         const int lrb = tc_merge_log_rows(slot_rows, head_dim);
-        const dim3 mgrid(grid, (slot_rows + (1 << lrb) - 1) >> lrb);
+        const dim3 mgrid(grid, (slot_rows + (1 << lrb) - 1) >> lrb, 2);
         const void *mf = head_dim == 64 ? (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 2>)
                                                       : reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<64, 1>))
                                         : (units == 2 ? reinterpret_cast<const void *>(&pa_tree_tc_merge_kernel<128, 2>)

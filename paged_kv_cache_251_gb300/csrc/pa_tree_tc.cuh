@@ -1268,10 +1268,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // P-th column group, so each reads about as much as it wrote, in one or two round
 // trips whatever P is (one CTA of a pair for all its columns, or for 16 of them
 // with warps over the parts, took 14 us on the ragged batch and 22 us on
-// the long contexts, against 7 and 13).  grid.y: chunks of RB rows.  A warp's
-// lanes are RB rows x 32 / RB column groups of kTcMergeCols columns (whole
-// lines of the column-major partials); its 8 warps take different groups, or, when
-// a CTA has fewer, share the parts of one and meet in shared memory.
+// the long contexts, against 5 and 13).  grid.y: chunks of RB rows, grid.z: the
+// CTA's first or second partial.  A warp's lanes are RB rows x 32 / RB column
+// groups of kTcMergeCols columns (whole lines of the column-major partials); the 8
+// warps take different groups, or, when there are fewer, share the parts of one
+// and meet in shared memory.
 constexpr int kTcMergeThreads = 256;
 constexpr int kTcMergeWarps = kTcMergeThreads / 32;
 constexpr int kTcMergeCols = 8;
@@ -1309,81 +1310,77 @@ __global__ void __launch_bounds__(kTcMergeThreads, 4) pa_tree_tc_merge_kernel(co
     constexpr int E = kTcMergeCols;
     __shared__ float acc[kTcMergeWarps][E + 2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 cut[2] = {p.cuts[2 * blockIdx.x], p.cuts[2 * blockIdx.x + 1]};
+    const int4 cut = p.cuts[2 * blockIdx.x + blockIdx.z];
+    const int parts = cut.w, first = cut.z;
+    if (parts == 0)
+        return;
     const int G = p.num_heads / p.num_kv_heads;
     const int all_rows = p.num_draft * G, rows = tc_slot_rows<Units>(all_rows);
     const int lrb = tc_merge_log_rows(rows, D);
     const int groups = (D / E) >> (5 - lrb);  // column groups of a warp's width
     const int r = (blockIdx.y << lrb) + (lane & ((1 << lrb) - 1));
+    const int j = static_cast<int>(blockIdx.x) - first;
+    const int mine = groups > j ? (groups - j + parts - 1) / parts : 0;
+    if (mine == 0)
+        return;
+    int cw = 1;  // warps over column groups; the others over parts
+    while (cw < kTcMergeWarps && cw < mine)
+        cw *= 2;
+    const int pw = kTcMergeWarps / cw;
+    const int full = cut.y % p.row_tiles * Units * 128 + r;  // row of the (sequence, kv head)
+    const bool live = r < rows && full < all_rows;
+    const long long orow = (static_cast<long long>(cut.x) * p.num_draft + full / G) * p.num_heads +
+                           cut.y / p.row_tiles * G + full % G;
+    // (one turn when warps share parts: cw >= mine then)
+    for (int k0 = 0; k0 < mine; k0 += cw) {
+        const int k = k0 + warp % cw;
+        const int col = (((j + k * parts) << (5 - lrb)) + (lane >> lrb)) * E;
+        TcMergeState st;
+        if (live && k < mine) {
+            // part 0: the first CTA's partial 1; part q: partial 0 of the q-th CTA after it
+            for (int q = warp / cw; q < parts; q += 2 * pw) {
+                float2 v[2];
+                float x[2][E];
 #pragma unroll
-    for (int job = 0; job < 2; ++job) {
-        const int parts = cut[job].w, first = cut[job].z;
-        if (parts == 0)
-            continue;
-        const int j = static_cast<int>(blockIdx.x) - first;
-        const int mine = groups > j ? (groups - j + parts - 1) / parts : 0;
-        if (mine == 0)
-            continue;
-        int cw = 1;  // warps over column groups; the others over parts
-        while (cw < kTcMergeWarps && cw < mine)
-            cw *= 2;
-        const int pw = kTcMergeWarps / cw;
-        const int full = cut[job].y % p.row_tiles * Units * 128 + r;  // row of the (sequence, kv head)
-        const bool live = r < rows && full < all_rows;
-        const long long orow = (static_cast<long long>(cut[job].x) * p.num_draft + full / G) * p.num_heads +
-                               cut[job].y / p.row_tiles * G + full % G;
-        // (one turn when warps share parts: cw >= mine then)
-        for (int k0 = 0; k0 < mine; k0 += cw) {
-            const int k = k0 + warp % cw;
-            const int col = (((j + k * parts) << (5 - lrb)) + (lane >> lrb)) * E;
-            TcMergeState st;
-            if (live && k < mine) {
-                // part 0: the first CTA's partial 1; part q: partial 0 of the q-th CTA after it
-                for (int q = warp / cw; q < parts; q += 2 * pw) {
-                    float2 v[2];
-                    float x[2][E];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int part = q + u * pw;
-                        v[u] = make_float2(0.f, 0.f);
-                        if (part < parts) {
-                            const long long slot = 2LL * (first + part) + (part == 0);
-                            v[u] = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
-                            const float *a = p.part_acc + (slot * D + col) * rows + r;
-#pragma unroll
-                            for (int e = 0; e < E; ++e)
-                                x[u][e] = a[static_cast<long long>(e) * rows];
-                        }
-                    }
-                    st.add(v[0], x[0]);
-                    st.add(v[1], x[1]);
-                }
-            }
-            if (pw > 1) {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    acc[warp][e][lane] = st.num[e];
-                acc[warp][E][lane] = st.m;
-                acc[warp][E + 1][lane] = st.den;
-                __syncthreads();
-                if (warp < cw)
-                    for (int w = warp + cw; w < kTcMergeWarps; w += cw) {
-                        float x[E];
+                for (int u = 0; u < 2; ++u) {
+                    const int part = q + u * pw;
+                    v[u] = make_float2(0.f, 0.f);
+                    if (part < parts) {
+                        const long long slot = 2LL * (first + part) + (part == 0);
+                        v[u] = reinterpret_cast<const float2 *>(p.part_ml)[slot * rows + r];
+                        const float *a = p.part_acc + (slot * D + col) * rows + r;
 #pragma unroll
                         for (int e = 0; e < E; ++e)
-                            x[e] = acc[w][e][lane];
-                        st.add(make_float2(acc[w][E][lane], acc[w][E + 1][lane]), x);
+                            x[u][e] = a[static_cast<long long>(e) * rows];
                     }
-            }
-            if (live && k < mine && (pw == 1 || warp < cw)) {
-                const float inv = st.den == 0.f ? 0.f : 1.f / st.den;
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    st.num[e] = st.den == 0.f ? 0.f : st.num[e] * inv;
-                store_cols<E>(p.out, p.out_dtype, orow * D + col, st.num);
+                }
+                st.add(v[0], x[0]);
+                st.add(v[1], x[1]);
             }
         }
-        __syncthreads();  // (before the next job's states)
+        if (pw > 1) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[warp][e][lane] = st.num[e];
+            acc[warp][E][lane] = st.m;
+            acc[warp][E + 1][lane] = st.den;
+            __syncthreads();
+            if (warp < cw)
+                for (int w = warp + cw; w < kTcMergeWarps; w += cw) {
+                    float x[E];
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        x[e] = acc[w][e][lane];
+                    st.add(make_float2(acc[w][E][lane], acc[w][E + 1][lane]), x);
+                }
+        }
+        if (live && k < mine && (pw == 1 || warp < cw)) {
+            const float inv = st.den == 0.f ? 0.f : 1.f / st.den;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                st.num[e] = st.den == 0.f ? 0.f : st.num[e] * inv;
+            store_cols<E>(p.out, p.out_dtype, orow * D + col, st.num);
+        }
     }
 }
 
