@@ -11,7 +11,8 @@ struct DecodeParams;
 struct TreeParams;
 
 // The score pass of the scored decode, after the decode and its merge.
-cudaError_t launch_scores(DecodeParams &p, const float *in, float *out, long long stride, cudaStream_t stream);
+cudaError_t launch_scores(DecodeParams &p, const float *in, float *out, long long stride, int sms,
+                          cudaStream_t stream);
 
 // CTAs of the tensor-core tree attention: one per SM, at most this many (the
 // workspace is sized for them).

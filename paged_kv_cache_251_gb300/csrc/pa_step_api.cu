@@ -411,11 +411,12 @@ pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in,
     st = launch_decode_kernel(p, dtype, head_dim, num_heads / num_kv_heads, cs);
     if (st != PA_OK)
         return st;
-    cudaError_t e = cudaSuccess;
-    if (plan.decode.max_parts > 1)
+    int dev = 0, sms = 0;
+    cudaError_t e = device_sms(&dev, &sms);
+    if (e == cudaSuccess && plan.decode.max_parts > 1)
         e = launch_reduce(p, head_dim, static_cast<long long>(num_seqs) * num_heads, cs);
     if (e == cudaSuccess)
-        e = launch_scores(p, scores_in, scores_out, scores_stride, cs);
+        e = launch_scores(p, scores_in, scores_out, scores_stride, sms, cs);
     return e == cudaSuccess ? PA_OK : cuda_fail(e, "score launch");
 }
 
