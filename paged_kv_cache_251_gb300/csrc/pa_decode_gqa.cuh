@@ -792,13 +792,12 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
             const int tok = (it.blk_lo + ti * C::kBpt + j) * BS + (row % BS);
             const bool valid = ((mask >> j) & 1u) && tok >= it.tok_lo && tok < it.tok_hi;
             char *pb = pbuf + b * C::kOpBytes + pbox * 16 * 128;
+            float logit[Log ? G : 1];
 #pragma unroll
             for (int h = 0; h < G; ++h) {
                 const float x = valid ? sc[h] * p.scale_log2 : -INFINITY;
-                if constexpr (Log) {
-                    if (tok >= it.tok_lo && tok < it.tok_hi)
-                        logit_row[h * p.logits_stride + tok] = x;
-                }
+                if constexpr (Log)
+                    logit[h] = x;
                 float mt = x;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
@@ -837,6 +836,13 @@ __device__ inline bool gqa_softmax(const DecodeParams &p, char *smem, const GqaL
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&pfull[b]);
+            if constexpr (Log) {  // (here they delay no product)
+                if (tok >= it.tok_lo && tok < it.tok_hi) {
+#pragma unroll
+                    for (int h = 0; h < G; ++h)
+                        logit_row[h * p.logits_stride + tok] = logit[h];
+                }
+            }
 
             if (pend && !epilogue(pend_g, pend_last, pend_it))
                 return false;
