@@ -246,10 +246,10 @@ template <typename T> __device__ inline bool non_finite2(uint32_t w) {
 // The even split
 
 // In tiles.  An item costs its start, its masked last tile and its epilogue beside
-// its tiles; measured on 64 ragged contexts of 16 to 8192 tokens: 108, 88, 80.5,
-// 81.5, 84 and 88 us at 1, 2, 4, 5, 8 and 12 (contexts of 512 to 2048: 249, 238,
-// 239, 242, 251 and 260).
-constexpr int kTcPairCost = 4;
+// its tiles: 2.8 tiles' time in a fit of the CTAs' end times on contexts of 512 to
+// 2048 tokens, 3.6 on contexts of 16 to 8192.  Those take 234 and 72 us with a cost
+// of 3, 238 and 72 with 4; costs of 1 and 12 lost a third and a tenth on the ragged ones.
+constexpr int kTcPairCost = 3;
 
 __device__ inline int tc_tiles(const TreeParams &p, int s) {
     const int len = max(0, min(ld_nc_i32(p.context_lens + s), p.max_len));
