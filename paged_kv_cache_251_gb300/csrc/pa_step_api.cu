@@ -99,8 +99,6 @@ void fill_decode(DecodeParams &p, void *out, const void *q, const void *k_cache,
 }
 
 constexpr int kMaxDraft = 256;
-// The general tree kernel splits contexts into partitions of this many tokens.
-constexpr int kTreePartition = 256;
 
 // The partitions of the general kernel, and the workspace of the kernel that
 // takes the call (`pool`: num_blocks; the workspace size is for pools of up to

@@ -73,13 +73,14 @@ __device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed
 constexpr int kTreeRows = 16;
 constexpr int kTreeThreads = kTreeRows * 8;
 constexpr int kTreeTile = 64;
+constexpr int kTreePartition = 256;  // tokens of a context partition
 
 template <int D> struct TreeSmem {
     float k[kTreeTile][D + 4];  // (+ 4: rows of a lane's tokens on different banks)
     float v[kTreeTile][D];
     float q[kTreeRows][D + 4];
-    float w[kTreeRows][kTreeTile + 1];
-    int phys[kTreeTile / 8];  // blocks of the tile, -1: left out
+    float w[kTreeRows][kTreeTile + 4];
+    int phys[kTreePartition / 8];  // blocks of the partition, -1: left out
 };
 
 template <typename T, int D>
@@ -126,38 +127,50 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             acc[e] = 0.f;
         }
         const int b_lo = part * p.bpp, b_hi = min(b_lo + p.bpp, sp.nblk);
+        if (static_cast<int>(threadIdx.x) < b_hi - b_lo) {  // (at most 32 blocks a partition)
+            int phys = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b_lo + threadIdx.x);
+            if (phys < 0 || phys >= p.num_blocks) {
+                phys = -1;
+                if (p.err)
+                    atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+            }
+            sh->phys[threadIdx.x] = phys;
+        }
         for (int b = b_lo; b < b_hi; b += tile_blocks) {
             __syncthreads();
-            if (threadIdx.x < tile_blocks) {
-                int phys = -1;
-                if (b + static_cast<int>(threadIdx.x) < b_hi) {
-                    phys = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b +
-                                     threadIdx.x);
-                    if (phys < 0 || phys >= p.num_blocks) {
-                        phys = -1;
-                        if (p.err)
-                            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+            // 16-byte pieces of the tile's rows, the loads of eight of a thread (K and V)
+            // in flight: one after another they took 6000 cycles a tile
+            constexpr int kAhead = 8;
+            for (int c0 = threadIdx.x; c0 < kTreeTile * D / V; c0 += kAhead * kTreeThreads) {
+                uint4 kx[kAhead], vx[kAhead];
+                bool on[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int c = c0 + u * kTreeThreads, t = c / (D / V), e = (c - t * (D / V)) * V;
+                    const int blk = b + t / bs;
+                    const int phys = t < kTreeTile && blk < b_hi ? sh->phys[blk - b_lo] : -1;
+                    on[u] = phys >= 0;
+                    if (on[u]) {
+                        const long long at =
+                            ((static_cast<long long>(phys) * p.num_kv_heads + kvh) * bs + t % bs) * D + e;
+                        kx[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_cache) + at);
+                        vx[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_cache) + at);
                     }
                 }
-                sh->phys[threadIdx.x] = phys;
-            }
-            __syncthreads();
-            // 16-byte pieces of the tile's rows
-            for (int c = threadIdx.x; c < kTreeTile * D / V; c += kTreeThreads) {
-                const int t = c / (D / V), e = (c - t * (D / V)) * V;
-                const int phys = sh->phys[t / bs];
-                if (phys >= 0) {
-                    const long long at =
-                        ((static_cast<long long>(phys) * p.num_kv_heads + kvh) * bs + t % bs) * D + e;
-                    Elt<T>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_cache) + at), &sh->k[t][e]);
-                    Elt<T>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_cache) + at), &sh->v[t][e]);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int c = c0 + u * kTreeThreads, t = c / (D / V), e = (c - t * (D / V)) * V;
+                    if (on[u]) {
+                        Elt<T>::unpack(kx[u], &sh->k[t][e]);
+                        Elt<T>::unpack(vx[u], &sh->v[t][e]);
+                    }
                 }
             }
             __syncthreads();
             const int tok0 = b * bs;
             uint64_t allow = live ? tree_bits64(p, s, committed, q.drafted, i, tok0) : 0ull;
             for (int k = 0; k < tile_blocks; ++k)
-                if (sh->phys[k] < 0)
+                if (b + k >= b_hi || sh->phys[b - b_lo + k] < 0)
                     allow &= ~(first_bits(bs) << (k * bs));
             float x[kPer];
 #pragma unroll
@@ -196,17 +209,29 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
                 sh->w[rl][l8 + 8 * k] = pw;
             }
             __syncwarp();
-            // attended tokens one by one, in order; lane l8 sums elements E l8 .. E l8 + E - 1
-            for (uint64_t left = allow; left; left &= left - 1) {
-                const int t = __ffsll(static_cast<long long>(left)) - 1;
-                const float pw = sh->w[rl][t];
+            // attended tokens in order, eight at a time that some row of the warp attends; lane l8
+            // sums elements 32 c + 4 l8 .. + 3 of the output (a walk over a row's own bits took
+            // 140 cycles a token, this 20)
+#pragma unroll 1
+            for (int t0 = 0; t0 < kTreeTile; t0 += 8) {
+                const uint32_t bits = static_cast<uint32_t>(allow >> t0) & 0xffu;
+                if (!__any_sync(0xffffffffu, bits))
+                    continue;
+                float pw[8];
+                *reinterpret_cast<float4 *>(pw) = *reinterpret_cast<const float4 *>(&sh->w[rl][t0]);
+                *reinterpret_cast<float4 *>(pw + 4) = *reinterpret_cast<const float4 *>(&sh->w[rl][t0 + 4]);
 #pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const float4 c = *reinterpret_cast<const float4 *>(&sh->v[t][l8 * E + e]);
-                    acc[e] = fmaf(pw, c.x, acc[e]);
-                    acc[e + 1] = fmaf(pw, c.y, acc[e + 1]);
-                    acc[e + 2] = fmaf(pw, c.z, acc[e + 2]);
-                    acc[e + 3] = fmaf(pw, c.w, acc[e + 3]);
+                for (int u = 0; u < 8; ++u) {
+#pragma unroll
+                    for (int e = 0; e < E; e += 4) {
+                        const float4 c = *reinterpret_cast<const float4 *>(&sh->v[t0 + u][8 * e + 4 * l8]);
+                        if ((bits >> u) & 1u) {
+                            acc[e] = fmaf(pw[u], c.x, acc[e]);
+                            acc[e + 1] = fmaf(pw[u], c.y, acc[e + 1]);
+                            acc[e + 2] = fmaf(pw[u], c.z, acc[e + 2]);
+                            acc[e + 3] = fmaf(pw[u], c.w, acc[e + 3]);
+                        }
+                    }
                 }
             }
             __syncwarp();
@@ -220,12 +245,12 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             // (a NaN denominator is the row's own: it stays)
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                store_out(p.out, p.out_dtype, orow * D + l8 * E + e, l == 0.f ? 0.f : acc[e] / l);
+                store_out(p.out, p.out_dtype, orow * D + 8 * (e & ~3) + 4 * l8 + (e & 3), l == 0.f ? 0.f : acc[e] / l);
         } else {
             const long long item = (static_cast<long long>(s) * p.num_kv_heads + kvh) * p.max_parts + part;
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                p.part_acc[(item * D + l8 * E + e) * rows + r] = acc[e];
+                p.part_acc[(item * D + 8 * (e & ~3) + 4 * l8 + (e & 3)) * rows + r] = acc[e];
             if (l8 == 0)
                 reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(m, l);
         }
