@@ -11,18 +11,23 @@ namespace pa {
 
 namespace {
 
-template <typename T> const void *tree_fn(int head_dim) {
-    return head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_kernel<T, 64>)
-                          : reinterpret_cast<const void *>(&pa_tree_kernel<T, 128>);
+template <typename T, int R> const void *tree_fn(int head_dim) {
+    return head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_kernel<T, 64, R>)
+                          : reinterpret_cast<const void *>(&pa_tree_kernel<T, 128, R>);
+}
+template <int R> const void *tree_fn_of(int dtype, int head_dim, size_t *smem) {
+    *smem = head_dim == 64 ? sizeof(TreeSmem<64, R>) : sizeof(TreeSmem<128, R>);
+    return dtype == PA_F32   ? tree_fn<float, R>(head_dim)
+           : dtype == PA_F16 ? tree_fn<__half, R>(head_dim)
+                             : tree_fn<__nv_bfloat16, R>(head_dim);
 }
 
 pa_status launch_general(TreeParams &p, int dtype, int head_dim, int dev, cudaStream_t stream) {
-    const int G = p.num_heads / p.num_kv_heads;
-    p.row_tiles = (p.num_draft * G + kTreeRows - 1) / kTreeRows;
-    const void *fn = dtype == PA_F32   ? tree_fn<float>(head_dim)
-                     : dtype == PA_F16 ? tree_fn<__half>(head_dim)
-                                       : tree_fn<__nv_bfloat16>(head_dim);
-    const size_t smem = head_dim == 64 ? sizeof(TreeSmem<64>) : sizeof(TreeSmem<128>);
+    const int rows = p.num_draft * (p.num_heads / p.num_kv_heads);
+    const int R = rows > kTreeRows ? 2 : 1;
+    p.row_tiles = (rows + R * kTreeRows - 1) / (R * kTreeRows);
+    size_t smem = 0;
+    const void *fn = R == 1 ? tree_fn_of<1>(dtype, head_dim, &smem) : tree_fn_of<2>(dtype, head_dim, &smem);
     int per_sm = 0;
     cudaError_t e = prepare_kernel(dev, fn, smem, kTreeThreads, &per_sm);
     if (e != cudaSuccess)

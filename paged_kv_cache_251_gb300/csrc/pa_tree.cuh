@@ -63,27 +63,32 @@ __device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed
 }
 
 // ---------------------------------------------------------------------------
-// General kernel: any dtype, on the CUDA cores.  A CTA of 128 threads takes 16
-// rows, 8 lanes a row, and 64 tokens at a time, widened to fp32 in shared memory
-// (one round trip a tile).  Scores: lane l of a row has tokens l, l + 8, ... with
-// whole dot products, no exchange; one maximum and one rescale a tile; then the
-// weights go through shared memory and lane l sums its D / 8 elements of the
-// output over the attended tokens (others are never multiplied).
+// General kernel: any dtype, on the CUDA cores.  A CTA of 128 threads takes 16 R
+// rows, 8 lanes a row and R rows a thread, and 64 tokens at a time, widened to fp32
+// in shared memory (one round trip a tile).  Scores: lane l of a row has tokens l,
+// l + 8, ... with whole dot products, no exchange; one maximum and one rescale a
+// tile; then the weights go through shared memory and lane l sums its D / 8
+// elements of the output over the attended tokens (others are never multiplied).
+// Shared memory's rate bounds it at many rows: with R = 2 each K or V element read
+// there serves two.  R = 2 above 16 rows (48 rows over 64 contexts of 32 to 2048
+// tokens, fp32, head_dim 128: 787 us, 1018 with R = 1); up to 16 half of its rows
+// would be empty.  fp32, head_dim 64, 4 rows over two contexts of 8000 and 16000
+// tokens: 68 us, 1.45 TB/s; a 5-token tree over a hundred tokens: 11 us.
 
-constexpr int kTreeRows = 16;
-constexpr int kTreeThreads = kTreeRows * 8;
+constexpr int kTreeThreads = 128;
+constexpr int kTreeRows = kTreeThreads / 8;  // rows of a CTA, times R
 constexpr int kTreeTile = 64;
 constexpr int kTreePartition = 256;  // tokens of a context partition
 
-template <int D> struct TreeSmem {
+template <int D, int R> struct TreeSmem {
     float k[kTreeTile][D + 4];  // (+ 4: rows of a lane's tokens on different banks)
     float v[kTreeTile][D];
-    float q[kTreeRows][D + 4];
-    float w[kTreeRows][kTreeTile + 4];
+    float q[R * kTreeRows][D + 4];
+    float w[R * kTreeRows][kTreeTile + 4];
     int phys[kTreePartition / 8];  // blocks of the partition, -1: left out
 };
 
-template <typename T, int D>
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams p) {
     pdl_launch_dependents();
     pdl_wait();
@@ -91,7 +96,7 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
     constexpr int V = 16 / sizeof(T);  // elements per 16-byte load
     constexpr int kPer = kTreeTile / 8;  // tokens of a lane
     extern __shared__ __align__(16) char smem[];
-    TreeSmem<D> *sh = reinterpret_cast<TreeSmem<D> *>(smem);
+    TreeSmem<D, R> *sh = reinterpret_cast<TreeSmem<D, R> *>(smem);
     const int G = p.num_heads / p.num_kv_heads;
     const int rows = p.num_draft * G;
     const int rl = threadIdx.x >> 3, l8 = threadIdx.x & 7;
@@ -112,19 +117,28 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
         if (q.bad && part == 0 && kvh == 0 && rt == 0 && threadIdx.x == 0 && p.err)
             atomicOr(p.err, PA_DEVERR_BAD_LEN);
         const int committed = q.len - q.drafted;
-        const int r = rt * kTreeRows + rl;
-        const bool mine = r < rows;
-        const int i = mine ? r / G : 0;
-        const int h = kvh * G + (mine ? r % G : 0);
-        const bool live = mine && i < q.drafted;
-        const long long orow = (static_cast<long long>(s) * p.num_draft + i) * p.num_heads + h;
-        float acc[E], m = -INFINITY, l = 0.f;
+        // the thread's rows: rl + 16 y of the row tile
+        const int r0 = rt * kTreeRows * R + rl;
+        bool mine[R], live[R];
+        int i[R];
+        long long orow[R];
+        float acc[R][E], m[R], l[R];
         __syncthreads();  // (the item before is done with shared memory)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = l8 + 8 * e;
-            sh->q[rl][c] = live ? static_cast<float>(static_cast<const T *>(p.q)[orow * D + c]) * p.scale_log2 : 0.f;
-            acc[e] = 0.f;
+        for (int y = 0; y < R; ++y) {
+            const int r = r0 + kTreeRows * y;
+            mine[y] = r < rows;
+            i[y] = mine[y] ? r / G : 0;
+            live[y] = mine[y] && i[y] < q.drafted;
+            orow[y] = (static_cast<long long>(s) * p.num_draft + i[y]) * p.num_heads + kvh * G + (mine[y] ? r % G : 0);
+            m[y] = -INFINITY, l[y] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const int c = l8 + 8 * e;
+                sh->q[rl + kTreeRows * y][c] =
+                    live[y] ? static_cast<float>(static_cast<const T *>(p.q)[orow[y] * D + c]) * p.scale_log2 : 0.f;
+                acc[y][e] = 0.f;
+            }
         }
         const int b_lo = part * p.bpp, b_hi = min(b_lo + p.bpp, sp.nblk);
         if (static_cast<int>(threadIdx.x) < b_hi - b_lo) {  // (at most 32 blocks a partition)
@@ -168,68 +182,92 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             }
             __syncthreads();
             const int tok0 = b * bs;
-            uint64_t allow = live ? tree_bits64(p, s, committed, q.drafted, i, tok0) : 0ull;
+            uint64_t allow[R];
+#pragma unroll
+            for (int y = 0; y < R; ++y)
+                allow[y] = live[y] ? tree_bits64(p, s, committed, q.drafted, i[y], tok0) : 0ull;
+            uint64_t blocks = ~0ull;
             for (int k = 0; k < tile_blocks; ++k)
                 if (b + k >= b_hi || sh->phys[b - b_lo + k] < 0)
-                    allow &= ~(first_bits(bs) << (k * bs));
-            float x[kPer];
-#pragma unroll
-            for (int k = 0; k < kPer; ++k)
-                x[k] = 0.f;
+                    blocks &= ~(first_bits(bs) << (k * bs));
+            float x[R][kPer] = {};
 #pragma unroll 4
             for (int e = 0; e < D; e += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&sh->q[rl][e]);
+                float4 a[R];
+#pragma unroll
+                for (int y = 0; y < R; ++y)
+                    a[y] = *reinterpret_cast<const float4 *>(&sh->q[rl + kTreeRows * y][e]);
 #pragma unroll
                 for (int k = 0; k < kPer; ++k) {
                     const float4 c = *reinterpret_cast<const float4 *>(&sh->k[l8 + 8 * k][e]);
-                    x[k] = fmaf(a.x, c.x, fmaf(a.y, c.y, fmaf(a.z, c.z, fmaf(a.w, c.w, x[k]))));
+#pragma unroll
+                    for (int y = 0; y < R; ++y)
+                        x[y][k] = fmaf(a[y].x, c.x,
+                                       fmaf(a[y].y, c.y, fmaf(a[y].z, c.z, fmaf(a[y].w, c.w, x[y][k]))));
                 }
             }
-            float mt = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                x[k] = (allow >> (l8 + 8 * k)) & 1u ? x[k] : -INFINITY;
-                mt = fmaxf(mt, x[k]);
-            }
+            for (int y = 0; y < R; ++y) {
+                allow[y] &= blocks;
+                float mt = -INFINITY;
 #pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-            const float mn = fmaxf(m, mt);
-            const float alpha = mn == -INFINITY ? 1.f : exp2f(m - mn);
-            l *= alpha;
+                for (int k = 0; k < kPer; ++k) {
+                    x[y][k] = (allow[y] >> (l8 + 8 * k)) & 1u ? x[y][k] : -INFINITY;
+                    mt = fmaxf(mt, x[y][k]);
+                }
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                acc[e] *= alpha;
-            m = mn;
+                for (int o = 1; o < 8; o <<= 1)
+                    mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+                const float mn = fmaxf(m[y], mt);
+                const float alpha = mn == -INFINITY ? 1.f : exp2f(m[y] - mn);
+                l[y] *= alpha;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                // (a NaN score stays one)
-                const float pw = x[k] == -INFINITY ? 0.f : exp2f(x[k] - mn);
-                l += pw;
-                sh->w[rl][l8 + 8 * k] = pw;
+                for (int e = 0; e < E; ++e)
+                    acc[y][e] *= alpha;
+                m[y] = mn;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    // (a NaN score stays one)
+                    const float pw = x[y][k] == -INFINITY ? 0.f : exp2f(x[y][k] - mn);
+                    l[y] += pw;
+                    sh->w[rl + kTreeRows * y][l8 + 8 * k] = pw;
+                }
             }
             __syncwarp();
-            // attended tokens in order, eight at a time that some row of the warp attends; lane l8
+            // attended tokens in order, kAtOnce at a time that some row of the warp attends; lane l8
             // sums elements 32 c + 4 l8 .. + 3 of the output (a walk over a row's own bits took
             // 140 cycles a token, this 20)
+            constexpr int kAtOnce = R == 1 ? 8 : 4;
 #pragma unroll 1
-            for (int t0 = 0; t0 < kTreeTile; t0 += 8) {
-                const uint32_t bits = static_cast<uint32_t>(allow >> t0) & 0xffu;
-                if (!__any_sync(0xffffffffu, bits))
-                    continue;
-                float pw[8];
-                *reinterpret_cast<float4 *>(pw) = *reinterpret_cast<const float4 *>(&sh->w[rl][t0]);
-                *reinterpret_cast<float4 *>(pw + 4) = *reinterpret_cast<const float4 *>(&sh->w[rl][t0 + 4]);
+            for (int t0 = 0; t0 < kTreeTile; t0 += kAtOnce) {
+                uint32_t bits[R], any = 0;
+                float pw[R][kAtOnce];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int y = 0; y < R; ++y) {
+                    bits[y] = static_cast<uint32_t>(allow[y] >> t0) & ((1u << kAtOnce) - 1u);
+                    any |= bits[y];
+                }
+                if (!__any_sync(0xffffffffu, any))
+                    continue;
+#pragma unroll
+                for (int y = 0; y < R; ++y)
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; u += 4)
+                        *reinterpret_cast<float4 *>(&pw[y][u]) =
+                            *reinterpret_cast<const float4 *>(&sh->w[rl + kTreeRows * y][t0 + u]);
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
 #pragma unroll
                     for (int e = 0; e < E; e += 4) {
                         const float4 c = *reinterpret_cast<const float4 *>(&sh->v[t0 + u][8 * e + 4 * l8]);
-                        if ((bits >> u) & 1u) {
-                            acc[e] = fmaf(pw[u], c.x, acc[e]);
-                            acc[e + 1] = fmaf(pw[u], c.y, acc[e + 1]);
-                            acc[e + 2] = fmaf(pw[u], c.z, acc[e + 2]);
-                            acc[e + 3] = fmaf(pw[u], c.w, acc[e + 3]);
+#pragma unroll
+                        for (int y = 0; y < R; ++y) {
+                            if ((bits[y] >> u) & 1u) {
+                                acc[y][e] = fmaf(pw[y][u], c.x, acc[y][e]);
+                                acc[y][e + 1] = fmaf(pw[y][u], c.y, acc[y][e + 1]);
+                                acc[y][e + 2] = fmaf(pw[y][u], c.z, acc[y][e + 2]);
+                                acc[y][e + 3] = fmaf(pw[y][u], c.w, acc[y][e + 3]);
+                            }
                         }
                     }
                 }
@@ -237,22 +275,27 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             __syncwarp();
         }
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (!mine)
-            continue;
-        if (sp.nparts == 1) {
-            // (a NaN denominator is the row's own: it stays)
+        for (int y = 0; y < R; ++y) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                store_out(p.out, p.out_dtype, orow * D + 8 * (e & ~3) + 4 * l8 + (e & 3), l == 0.f ? 0.f : acc[e] / l);
-        } else {
-            const long long item = (static_cast<long long>(s) * p.num_kv_heads + kvh) * p.max_parts + part;
+            for (int o = 1; o < 8; o <<= 1)
+                l[y] += __shfl_xor_sync(0xffffffffu, l[y], o);
+            if (!mine[y])
+                continue;
+            if (sp.nparts == 1) {
+                // (a NaN denominator is the row's own: it stays)
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                p.part_acc[(item * D + 8 * (e & ~3) + 4 * l8 + (e & 3)) * rows + r] = acc[e];
-            if (l8 == 0)
-                reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(m, l);
+                for (int e = 0; e < E; ++e)
+                    store_out(p.out, p.out_dtype, orow[y] * D + 8 * (e & ~3) + 4 * l8 + (e & 3),
+                              l[y] == 0.f ? 0.f : acc[y][e] / l[y]);
+            } else {
+                const int r = r0 + kTreeRows * y;
+                const long long item = (static_cast<long long>(s) * p.num_kv_heads + kvh) * p.max_parts + part;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    p.part_acc[(item * D + 8 * (e & ~3) + 4 * l8 + (e & 3)) * rows + r] = acc[y][e];
+                if (l8 == 0)
+                    reinterpret_cast<float2 *>(p.part_ml)[item * rows + r] = make_float2(m[y], l[y]);
+            }
         }
     }
 }
