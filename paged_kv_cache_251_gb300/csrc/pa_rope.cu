@@ -255,7 +255,7 @@ cudaError_t launch_rope(RopeParams p, int dtype, int interleaved, int num_sms, c
     else
         fn = vec ? rope_fn<__nv_bfloat16, 8>(interleaved) : rope_fn<__nv_bfloat16, 1>(interleaved);
     // tokens per CTA: enough CTAs for every SM first, then about 128 rows a CTA (16384
-    // tokens of 80 rows each: 160 us with one, 164 us with three; 65536 tokens of 6
+    // tokens of 120 rows each: 160 us with one a CTA, 164 us with two; 65536 tokens of 6
     // rows: 54 us with eight, 80 us with two)
     long long tok = p.num_tokens / (8LL * num_sms);
     tok = tok < 1 ? 1 : (tok > kRopeMaxTok ? kRopeMaxTok : tok);
