@@ -667,7 +667,10 @@ __device__ inline bool tc_s_warp(const TreeParams &p, const CUtensorMap *tmq, ch
     }
 }
 
-// O += P . V of every tile, 64 tokens at a time.
+// O += P . V of every tile, 64 tokens at a time.  With two row tiles the product of
+// the second is left out where it has no drafted token (its buffers change hands all
+// the same): four contexts of 65536 to 131072 tokens, 24 of 64 queries drafted, 280
+// -> 261 us (leaving out its S as well costs full trees 2 to 5 %).
 template <typename T, int D, int Parts, int Units>
 __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, uint32_t tmem) {
     using C = TcCfg<D, Units>;
@@ -677,12 +680,14 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
     const bool lane0 = (threadIdx.x & 31) == 0;
     // V, MN-major: 64-column halves 1024 bytes apart, 8-token groups kGroup apart
     const uint64_t v_desc = sdesc(smem + C::kOffV, 1024, C::kGroup);
+    const int G = p.num_heads / p.num_kv_heads;
     uint32_t t = 0, ke = 0, vst = 0, vph = 0;
     for (uint32_t k = 0;; ++k) {
         const int slot = static_cast<int>(k % kTcItems);
         if (!mbar_wait_bounded(&M->ifull[slot], (k / kTcItems) & 1u))
             return false;
         const int ntiles = M->items[slot].ntiles, end = M->items[slot].end;
+        const bool both = Units == 1 || M->items[slot].drafted * G > M->items[slot].rt * 256 + 128;
         __syncwarp();
         if (lane0)
             mbar_arrive(&M->iempty[slot]);
@@ -711,12 +716,14 @@ __device__ inline bool tc_pv_warp(const TreeParams &p, char *smem, TcMisc *M, ui
                 const uint64_t vd = v_desc + vst * (C::kTile >> 4) + half * kHalf;
                 const uint32_t o = tmem + 256 + w * D;
                 const uint32_t pt = tmem + tc_buf_col(b) + (Units == 2 ? half * 64 : 0u);
+                if (Units == 1 || w == 0 || both) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                    for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int part = 0; part < Parts; ++part)
-                        tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
-                                  vd + kk * (2 * C::kGroup >> 4), kIdPV, (kk | part) ? 1 : keep);
+                        for (int part = 0; part < Parts; ++part)
+                            tc_mma_ts(lead, o, pt + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                                      vd + kk * (2 * C::kGroup >> 4), kIdPV, (kk | part) ? 1 : keep);
+                }
                 if (Units == 1 || half == 1)
                     tc_commit_lead(lead, &M->pvdone[b]);
             }
