@@ -24,6 +24,12 @@
 // and walks the places upward, a chunk at a time: all loads of a chunk happen
 // before its stores, and a later chunk only reads at or above its own first
 // place, which the stores before it never reach.
+//
+// Measured: 64 contexts of 2049 to 8192 tokens, 8 kv heads of 128, bf16, cut to
+// 2048: selection 26 us (latency of its passes over shared memory), movement 157 us,
+// 6.5 TB/s (HBM).  Two contexts of 65537 to 131072 tokens cut to 16001: selection 28
+// us (8 CTAs a row: 17 us of it loads and counting, the rest cluster barriers),
+// movement 39 us, 6.7 TB/s.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
