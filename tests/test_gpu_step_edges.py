@@ -244,3 +244,77 @@ def test_empty_batches():
     pa.pa_compact_kv(kc, kc.clone(), torch.empty((1, 1, 0), **i32), torch.zeros(1, **i32), torch.zeros((1, 4), **i32))
     torch.cuda.synchronize()
     assert (kc == 0).all() and math.isfinite(float(kc.sum()))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("h,hkv,d,rot,inter", [(1, 1, 64, 64, True), (2, 1, 128, 2, False), (3, 1, 64, 48, False),
+                                               (70, 35, 64, 64, False)])
+def test_many_tokens_a_block_of_threads(dtype, h, hkv, d, rot, inter):
+    """Few heads: up to eight tokens a CTA, the last one ragged; a row that needs
+    nearly all threads of a CTA; more rows a token than a CTA holds at once."""
+    from paged_kv_cache_251_gb300 import pa
+    from test_gpu_rope import check, rotate64
+    n, bs = 12003 if h < 10 else 1500, 16
+    q = wl.normal_tensor(1, 3, (n, h, d), dtype=dtype).cuda()
+    k = wl.normal_tensor(2, 3, (n, hkv, d), dtype=dtype).cuda()
+    v = wl.normal_tensor(3, 3, (n, hkv, d), dtype=dtype).cuda()
+    freqs = pa.pa_rope_frequencies(rot)
+    pos = wl.randint(7, 1, n, 0, 100000).to(torch.int32).cuda()
+    nb = (n + bs - 1) // bs
+    slots = wl.permutation(5, 2, nb * bs)[:n].cuda()
+    kc = torch.zeros((nb, hkv, bs, d), dtype=dtype, device="cuda")
+    vc = torch.zeros_like(kc)
+    out = torch.full_like(q, float("nan"))
+    pa.pa_rope_append_kv(out, q, k, v, pos, slots, freqs.cuda(), kc, vc, interleaved=inter)
+    ref, mag = rotate64(q, pos, freqs, rot, inter, 1.0)
+    check(out, ref, mag, 1.0, 1e5)
+    ref, mag = rotate64(k, pos, freqs, rot, inter, 1.0)
+    check(kc.transpose(1, 2).reshape(nb * bs, hkv, d)[slots], ref, mag, 1.0, 1e5)
+    assert torch.equal(vc.transpose(1, 2).reshape(nb * bs, hkv, d)[slots], v)
+
+
+@pytest.mark.parametrize("L,budget,recent", [(5000, 4999, 0), (33333, 1, 0), (33333, 700, 700), (60001, 20000, 1),
+                                             (20000, 20000, 5)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_select_of_special_values_over_slices(L, budget, recent, in_place):
+    """Infinities, NaN, zeros of both signs and subnormals in rows shared by several
+    CTAs, off the 16-byte boundary; budgets of one, of nearly all, of only recent
+    tokens."""
+    from paged_kv_cache_251_gb300 import pa
+    from test_gpu_evict import select_oracle
+    values = torch.tensor([float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 1e-42, -1e-42, 1.0, 3.5, -2.0, 0.7, 0.71])
+    sc = values[(wl.uniform01(L + budget, 1, 2 * (L + 1)) * 12).floor().long()].view(1, 2, L + 1).contiguous()
+    dev = sc.cuda()
+    out = dev if in_place else torch.full_like(dev, 9.0)
+    keep = torch.empty((1, 2, budget), dtype=torch.int32, device="cuda")
+    new = torch.empty(1, dtype=torch.int32, device="cuda")
+    pa.pa_evict_select(keep, new, out, dev, torch.tensor([L], dtype=torch.int32, device="cuda"), budget, recent)
+    want, n, scores = select_oracle(sc, [L], budget, recent)
+    assert new.tolist() == [min(L, budget)] and torch.equal(keep.cpu(), want)
+    assert torch.equal(torch.nan_to_num(out.cpu(), nan=1.5), torch.nan_to_num(scores, nan=1.5))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h,hkv,t", [(1, 1, 1), (2, 1, 3), (4, 1, 9), (4, 1, 64), (8, 1, 100)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_one_long_context_in_many_parts(dtype, d, h, hkv, t, wide):
+    """A context cut into about 150 parts, from one row to 800: the merge shares a
+    pair's columns among all CTAs, or its parts among warps; and a second sequence
+    of one tile beside it."""
+    from paged_kv_cache_251_gb300 import pa
+    from steplib import tree_oracle
+    lens = [30011, t]
+    k, v, tables, lens_t = paged(t + h, lens, hkv, d, 32, dtype)
+    q = wl.normal_tensor(8, 3, (2, t, h, d), dtype=dtype).cuda()
+    mask = pa.tree_mask_from_parents(random_parents(t, 2, t)).cuda()
+    drafts = torch.tensor([max(t - 1, 1), t], dtype=torch.int32, device="cuda")
+    out_dtype = torch.float32 if wide else dtype
+    out = torch.full(q.shape, float("nan"), dtype=out_dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_decode_tree(out, q, k, v, tables, lens_t, tree_mask=mask, draft_lens=drafts, err_word=err)
+    ref, mag, dx = tree_oracle(q, k, v, tables, lens_t, drafts, mask, 1 / math.sqrt(d))
+    assert err.item() == 0
+    check_within(out, ref, attention_bound(ref, mag, dx, dtype, out_dtype, max(lens)))
+    # rows that are padding are zero
+    assert t == 1 or (out[0, t - 1] == 0).all()
