@@ -154,8 +154,10 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     auto score = [&](int t) -> float { return Cached ? slice[t - lo] : canonical(in[t]); };
 
-    uint32_t kth = 0, above = 0;     // the k-th largest image, scores above it
-    uint32_t own_above = 0, own_equal = 0;  // this slice's share: of the thread's bins (sums over threads), equal to the k-th
+    uint32_t kth = 0, above = 0;  // the k-th largest image, scores above it
+    // of this slice: scores above the k-th (in the thread's bins), and equal to it
+    // (one thread has them)
+    uint32_t own_above = 0, own_equal = 0;
     if (k > 0) {
         uint32_t need = k;
 #pragma unroll

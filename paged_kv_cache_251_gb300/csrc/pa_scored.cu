@@ -141,7 +141,8 @@ cudaError_t launch_scores(DecodeParams &p, const float *in, float *out, long lon
         float *co = out + at;
         void *args[] = {&c, &ci, &co, &stride};
         const cudaError_t e = launch_dependent(score_fn(p.num_heads / p.num_kv_heads),
-                                               dim3(static_cast<unsigned>(chunks), p.num_kv_heads, n), dim3(kScoreThreads), args, 0, stream);
+                                               dim3(static_cast<unsigned>(chunks), p.num_kv_heads, n), dim3(kScoreThreads), args, 0,
+                                               stream);
         if (e != cudaSuccess)
             return e;
     }

@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
         }
         const int b_lo = part * p.bpp, b_hi = min(b_lo + p.bpp, sp.nblk);
         if (static_cast<int>(threadIdx.x) < b_hi - b_lo) {  // (at most 32 blocks a partition)
-            int phys = ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b_lo + threadIdx.x);
+            int phys =
+                ld_nc_i32(p.block_tables + static_cast<long long>(s) * p.max_blocks_per_seq + b_lo + threadIdx.x);
             if (phys < 0 || phys >= p.num_blocks) {
                 phys = -1;
                 if (p.err)

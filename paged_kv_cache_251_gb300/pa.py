@@ -442,7 +442,7 @@ def _call(fn, dev: int, stream, *args) -> None:
         if stream.device_index != dev:
             raise ValueError("the stream is on another device than the tensors")
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -451,15 +451,21 @@ def _call(fn, dev: int, stream, *args) -> None:
         _check(status)
 
 
-def _shape(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _shapes(*checks) -> None:
+    """Tensor, shape, name, and so on: the tensors (None aside) have those shapes."""
+    for i in range(0, len(checks), 3):
+        t = checks[i]
+        if t is not None and t.shape != checks[i + 1]:
+            raise ValueError(f"{checks[i + 2]} has shape {tuple(t.shape)}, expected {tuple(checks[i + 1])}")
 
 
-def _int32(**ts) -> None:
-    for name, t in ts.items():
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError(f"{name} must be int32")
+def _int32(*checks) -> None:
+    """Tensor, name, and so on: the tensors (None aside) are int32."""
+    i32 = torch.int32
+    for i in range(0, len(checks), 2):
+        t = checks[i]
+        if t is not None and t.dtype is not i32:
+            raise TypeError(f"{checks[i + 1]} must be int32")
 
 
 def _addr(t: torch.Tensor | None):
@@ -480,9 +486,10 @@ def _rows(t: torch.Tensor, name: str) -> int:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     n, h, d = t.shape
-    if n and ((h > 1 and t.stride(1) != d) or t.stride(2) != 1):
+    at = t.stride()
+    if n and ((h > 1 and at[1] != d) or at[2] != 1):
         raise ValueError(f"{name}: each token's heads must be dense")
-    return t.stride(0) if n > 1 else h * d
+    return at[0] if n > 1 else h * d
 
 
 def pa_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -506,8 +513,7 @@ def pa_rope(out: torch.Tensor, x: torch.Tensor, positions: torch.Tensor, freqs: 
     if x.get_device() != dev or out.get_device() != dev:
         raise ValueError("every tensor must be a CUDA tensor on one device")
     n, h, d = x.shape
-    _shape(out, x.shape, "out")
-    _shape(positions, (n,), "positions")
+    _shapes(out, x.shape, "out", positions, (n,), "positions")
     if positions.dtype != torch.int32 or freqs.dtype != torch.float64 or freqs.dim() != 1:
         raise TypeError("positions must be int32 and freqs a double vector")
     if out.dtype != x.dtype:
@@ -530,13 +536,8 @@ def pa_rope_append_kv(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         raise ValueError("every tensor must be a CUDA tensor on one device")
     n, h, d = q.shape
     nb, hkv, bs, d2 = k_cache.shape
-    _shape(q_out, q.shape, "q_out")
-    _shape(k, (n, hkv, d), "k")
-    _shape(v, (n, hkv, d), "v")
-    _shape(k_cache, (nb, hkv, bs, d), "k_cache")
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(positions, (n,), "positions")
-    _shape(slot_mapping, (n,), "slot_mapping")
+    _shapes(q_out, q.shape, "q_out", k, (n, hkv, d), "k", v, (n, hkv, d), "v", k_cache, (nb, hkv, bs, d), "k_cache",
+            v_cache, k_cache.shape, "v_cache", positions, (n,), "positions", slot_mapping, (n,), "slot_mapping")
     if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64:
         raise TypeError("positions must be int32 and slot_mapping int64")
     if freqs.dtype != torch.float64 or freqs.dim() != 1:
@@ -588,12 +589,11 @@ def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
 
 def _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d) -> tuple:
     nb, hkv, bs, d2 = k_cache.shape
-    _shape(k_cache, (nb, hkv, bs, d), "k_cache")
-    _shape(v_cache, k_cache.shape, "v_cache")
-    _shape(context_lens, (n,), "context_lens")
+    _shapes(k_cache, (nb, hkv, bs, d), "k_cache", v_cache, k_cache.shape, "v_cache", context_lens, (n,),
+            "context_lens")
     if block_tables.dim() != 2 or block_tables.shape[0] != n:
         raise ValueError("block_tables must be [N, max_blocks_per_seq]")
-    _int32(block_tables=block_tables, context_lens=context_lens)
+    _int32(block_tables, "block_tables", context_lens, "context_lens")
     if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
     return nb, hkv, bs
@@ -611,21 +611,20 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     dev = _dense(out, q, k_cache, v_cache, block_tables, context_lens, tree_mask, draft_lens, workspace, err_word)
     n, t, h, d = q.shape
     nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
-    _shape(out, q.shape, "out")
-    _int32(draft_lens=draft_lens)
-    if draft_lens is not None:
-        _shape(draft_lens, (n,), "draft_lens")
+    _shapes(out, q.shape, "out")
+    _int32(draft_lens, "draft_lens")
+    _shapes(draft_lens, (n,), "draft_lens")
     if tree_mask is not None:
         if tree_mask.dtype != torch.int64:
             raise TypeError("tree_mask must be int64 (64 bits a word)")
-        _shape(tree_mask, (n, t, (t + 63) // 64), "tree_mask")
+        _shapes(tree_mask, (n, t, (t + 63) // 64), "tree_mask")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
         workspace = tree_workspace_for(q, k_cache, block_tables.shape[1])
     _call(_lib.pa_decode_tree, dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), context_lens.data_ptr(), _addr(draft_lens), _addr(tree_mask), n, t, h, hkv, d, bs, float(scale),
-          DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace),
+          block_tables.data_ptr(), context_lens.data_ptr(), _addr(draft_lens), _addr(tree_mask), n, t, h, hkv, d, bs,
+          float(scale), DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace),
           _ws_bytes(workspace), _addr(err_word))
     return out
 
@@ -655,11 +654,11 @@ def pa_decode_scored(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tenso
     dev = _dense(out, scores_out, q, k_cache, v_cache, block_tables, context_lens, scores_in, workspace, err_word)
     n, h, d = q.shape
     nb, hkv, bs = _check_paged(q, k_cache, v_cache, block_tables, context_lens, n, h, d)
-    _shape(out, q.shape, "out")
+    _shapes(out, q.shape, "out")
     if scores_out.dim() != 3 or scores_out.shape[:2] != (n, hkv):
         raise ValueError("scores_out must be [N, H_kv, tokens]")
     if scores_in is not None:
-        _shape(scores_in, scores_out.shape, "scores_in")
+        _shapes(scores_in, scores_out.shape, "scores_in")
     if scores_out.dtype != torch.float32 or (scores_in is not None and scores_in.dtype != torch.float32):
         raise TypeError("scores must be float32")
     if scale is None:
@@ -667,8 +666,8 @@ def pa_decode_scored(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tenso
     if workspace is None:
         workspace = scored_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
     _call(_lib.pa_decode_scored, dev, stream, out.data_ptr(), scores_out.data_ptr(), _addr(scores_in), q.data_ptr(),
-          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), n, h, hkv, d, bs, float(scale),
-          scores_out.shape[2], DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb,
+          k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), n, h, hkv, d, bs,
+          float(scale), scores_out.shape[2], DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb,
           int(partition_size), _addr(workspace), _ws_bytes(workspace), _addr(err_word))
     return out
 
@@ -685,13 +684,11 @@ def pa_evict_select(keep: torch.Tensor, new_lens: torch.Tensor, scores_out: torc
         raise TypeError("scores must be float32 [N, H_kv, tokens]")
     n, hkv, stride = scores.shape
     if scores_out is not None:
-        _shape(scores_out, scores.shape, "scores_out")
+        _shapes(scores_out, scores.shape, "scores_out")
         if scores_out.dtype != torch.float32:
             raise TypeError("scores_out must be float32")
-    _shape(keep, (n, hkv, budget), "keep")
-    _shape(new_lens, (n,), "new_lens")
-    _shape(context_lens, (n,), "context_lens")
-    _int32(keep=keep, new_lens=new_lens, context_lens=context_lens)
+    _shapes(keep, (n, hkv, budget), "keep", new_lens, (n,), "new_lens", context_lens, (n,), "context_lens")
+    _int32(keep, "keep", new_lens, "new_lens", context_lens, "context_lens")
     _call(_lib.pa_evict_select, dev, stream, keep.data_ptr(), new_lens.data_ptr(), _addr(scores_out),
           scores.data_ptr(), context_lens.data_ptr(), n, hkv, int(budget), int(recent), stride, _addr(err_word))
     return keep
@@ -705,20 +702,18 @@ def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tens
     into the blocks of dst_block_tables.  See include/pa.h."""
     dev = _dense(k_cache, v_cache, keep, keep_lens, block_tables, dst_block_tables, base_lens, err_word)
     nb, hkv, bs, d = k_cache.shape
-    _shape(v_cache, k_cache.shape, "v_cache")
+    _shapes(v_cache, k_cache.shape, "v_cache")
     if v_cache.dtype != k_cache.dtype:
         raise TypeError("the caches must share one dtype")
     if keep.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("keep must be [N, H_kv or 1, n] and block_tables [N, max_blocks_per_seq]")
     n = keep.shape[0]
-    _int32(keep=keep, keep_lens=keep_lens, block_tables=block_tables, dst_block_tables=dst_block_tables,
-           base_lens=base_lens)
-    _shape(keep_lens, (n,), "keep_lens")
+    _int32(keep, "keep", keep_lens, "keep_lens", block_tables, "block_tables", dst_block_tables, "dst_block_tables",
+           base_lens, "base_lens")
+    _shapes(keep_lens, (n,), "keep_lens", base_lens, (n,), "base_lens")
     if block_tables.shape[0] != n or (dst_block_tables is not None and
                                       (dst_block_tables.dim() != 2 or dst_block_tables.shape[0] != n)):
         raise ValueError("block_tables and dst_block_tables must be [N, max_blocks_per_seq]")
-    if base_lens is not None:
-        _shape(base_lens, (n,), "base_lens")
     _call(_lib.pa_compact_kv, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), keep.data_ptr(),
           keep_lens.data_ptr(), _addr(base_lens), block_tables.data_ptr(), _addr(dst_block_tables), n, keep.shape[1],
           keep.shape[2], hkv, d, bs, block_tables.shape[1],

@@ -79,7 +79,8 @@ def test_more_sequences_than_a_grid_dimension(dtype):
     out = torch.full((N, 1, d), float("nan"), device="cuda")
     sc = torch.full((N, 1, bs), -1.0, device="cuda")
     pa.pa_decode_scored(out, sc, q, k, v, tables, lens, scale=scale, err_word=err)
-    # a weight: exp of a score off by dx twice over (numerator and denominator), the exponentials' and the sums' roundings
+    # a weight: exp of a score off by dx twice over (numerator and denominator), the
+    # exponentials' and the sums' roundings
     check_within(torch.where(live, sc[:, 0], 0.0), w,
                  w * (2 * dx + 2 * (2.0 ** -21 + 2.0 ** -17) + (bs + 4) * 2.0 ** -24) + 2.0 ** -126, "scores")
     assert (sc[:, 0][~live] == -1).all()
@@ -282,7 +283,8 @@ def test_select_of_special_values_over_slices(L, budget, recent, in_place):
     tokens."""
     from paged_kv_cache_251_gb300 import pa
     from test_gpu_evict import select_oracle
-    values = torch.tensor([float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 1e-42, -1e-42, 1.0, 3.5, -2.0, 0.7, 0.71])
+    values = torch.tensor([float("nan"), float("inf"), float("-inf"), 0.0, -0.0, 1e-42, -1e-42, 1.0, 3.5, -2.0, 0.7,
+                           0.71])
     sc = values[(wl.uniform01(L + budget, 1, 2 * (L + 1)) * 12).floor().long()].view(1, 2, L + 1).contiguous()
     dev = sc.cuda()
     out = dev if in_place else torch.full_like(dev, 9.0)

@@ -79,7 +79,8 @@ def test_tree_workspace_size(lib):
     f.restype, f.argtypes = SZ, [I] * 8
     F32, BF16 = 0, 2
     assert f(4, 8, 8, 2, 128, 16, 8, BF16) == 0                       # contexts of one 128-token tile are never cut
-    assert f(4, 8, 8, 2, 128, 16, 9, BF16) == 16 * (2 * 32 * 130 * 4 + 32)   # two partials (32 rows), a record each, for 16 CTAs
+    # two partials (32 rows), a record each, for 16 CTAs
+    assert f(4, 8, 8, 2, 128, 16, 9, BF16) == 16 * (2 * 32 * 130 * 4 + 32)
     assert f(64, 16, 32, 8, 128, 16, 512, BF16) == 152 * (2 * 64 * 130 * 4 + 32)
     assert f(4, 64, 32, 8, 128, 16, 8192, BF16) == 152 * (2 * 256 * 130 * 4 + 32)
     assert f(4, 256, 64, 8, 64, 16, 8192, BF16) == 152 * (2 * 256 * 66 * 4 + 32)   # 2048 rows: tiles of 256
