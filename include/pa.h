@@ -468,9 +468,12 @@ PA_API pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, co
  * kernel that splits the whole batch's contexts evenly over the SMs, fp32
  * caches in 256-token partitions.  The same inputs give the same bits on every
  * call (a sequence decoded in another batch may differ in the last bits, where
- * its context is cut elsewhere).  fp16 / bf16 out: the softmax weights are
- * rounded once to the cache's type before the product with V, like the output
- * itself; fp32 out: they are carried in two parts.
+ * its context is cut elsewhere).  Over fp16 / bf16 caches the softmax weights go
+ * to the product with V in the cache's type.  fp16 / bf16 out: rounded once, like
+ * the output itself (beside the output's rounding, an error of the same size).
+ * fp32 out: in two parts (hi + lo), for callers who want the weights exact, at 1.2
+ * to 1.4 times the time.  An fp16 weight is off by at most 2^-36 of the row's
+ * largest beside that, however far below it.
  * A drafted token that some query does not attend has no influence on it,
  * whatever its K and V hold (infinities and NaN too).  The table holds at most
  * 2^30 tokens a sequence (max_blocks_per_seq * block_size); other arguments and

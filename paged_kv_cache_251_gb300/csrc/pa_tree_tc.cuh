@@ -9,9 +9,9 @@
 // place), so shared memory feeds one operand of P V only.  A thread owns a row
 // of S: its softmax needs no exchange between lanes.  O accumulates in tensor
 // memory over the tiles of an item; a row whose maximum grows by more than 2^8
-// rescales its O (rare after the first tiles), a smaller growth is left in
-// the exponents (weights up to 2^8, fp32 sums), which changes nothing in the
-// quotient.
+// (fp16: 2^4) rescales its O (rare after the first tiles), a smaller growth is
+// left in the exponents (larger weights, fp32 sums), which changes nothing in
+// the quotient.
 //
 // With at most 128 rows (Units = 1) warpgroup w takes tokens 64 w .. 64 w + 63
 // of every tile, with its own running state and O, merged once per item; it has
@@ -23,8 +23,12 @@
 // product in halves of 64 tokens.
 //
 // P's rounding (Parts): a 16-bit output takes P rounded once to the type of V
-// (the output is rounded as coarsely); an fp32 output takes hi + lo parts
-// (hi = round(p), lo = round(p - hi)), two accumulating products.
+// (the output is rounded as coarsely: against 64 bits 2.2e-3 instead of 1.7e-3 in
+// bf16, 2.9e-4 instead of 2.1e-4 in fp16); an fp32 output takes hi + lo parts
+// (hi = round(p), lo = round(p - hi)), two accumulating products.  Two parts for
+// 16-bit outputs as well cost 234 -> 293, 72 -> 89 and 306 -> 433 us on the three
+// calls measured below; a caller who wants them asks for fp32.  In fp16 weights
+// are lifted above its small numbers (kTcLift).
 //
 // Work is split evenly over the CTAs, one per SM: the tiles of all pairs
 // (sequence, kv head, row tile) in order, each pair counted with kTcPairCost
@@ -79,7 +83,15 @@ constexpr int kTcRecords = 3;    // record ring of the V producer
 constexpr int kTcMeta = 8;
 constexpr int kTcMaxBpt = 16;    // blocks per tile at block size 8
 constexpr uint32_t kTcEnd = 0xFFFFFFFFu;
-constexpr float kTcLazy = 8.0f;  // growth of a row's maximum (base 2) that rescales its O
+// kTcLazy: growth of a row's maximum (base 2) that rescales its O.  kTcLift: weights are
+// carried 2^kTcLift times larger, numerator and denominator alike.  Above the maximum in
+// use they reach 2^(kTcLazy + kTcLift).  fp16 ends at 2^16 and loses what is below 2^-25:
+// lifted, that is 2^-36 of the maximum (not lifted, 2^-25: 131072 tokens behind a dominant
+// one lost up to 2^-8 of the mass from the numerator alone).  bf16 has fp32's exponents.
+template <typename T> constexpr float kTcLazy = 8.0f;
+template <> constexpr float kTcLazy<__half> = 4.0f;
+template <typename T> constexpr float kTcLift = 0.0f;
+template <> constexpr float kTcLift<__half> = 11.0f;
 
 template <int D, int Units> struct TcCfg {
     static constexpr int kHalves = D / 64;
@@ -970,9 +982,9 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                         tc_fence_after();
                         if (warp_live) {
                             const float mx = fmaxf(m, top == -INFINITY ? -INFINITY : top * sc);
-                            const float mn = first || mx > m + kTcLazy ? mx : m;  // (as below)
+                            const float mn = first || mx > m + kTcLazy<T> ? mx : m;  // (as below)
                             const float alpha = first || (m == -INFINITY && mn != m) ? 0.f : fast_exp2(m - mn);
-                            const float me = mn == -INFINITY ? 0.f : mn;
+                            const float me = (mn == -INFINITY ? 0.f : mn) - kTcLift<T>;
                             for (int c = 0; c < D; c += 16) {
                                 float o[16];
                                 tmem_ld<16>(o_addr + c, o);
@@ -1034,7 +1046,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 // O scales with the maximum in use; it changes only when the row's
                 // maximum passed it by kTcLazy
                 const float mn = fmaxf(m, mt);
-                const bool grow = first ? false : mn > m + kTcLazy;
+                const bool grow = first ? false : mn > m + kTcLazy<T>;
                 if (__any_sync(0xffffffffu, grow)) {
                     // every product into this O so far is done once the last one is
                     if (!mbar_wait_bounded(&M->pvdone[tc_buf<Units>(t - 1, wg)], tc_phase<Units>(t - 1)))
@@ -1057,7 +1069,7 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 }
                 if (first || grow)
                     m = mn;
-                const float me = m == -INFINITY ? 0.f : m;
+                const float me = (m == -INFINITY ? 0.f : m) - kTcLift<T>;
                 // (a masked score is -inf: its weight is exactly 0)
                 float2 l2 = make_float2(0.f, 0.f);
                 weights32<T, Parts>(sv, sc, me, s_addr, l2);
