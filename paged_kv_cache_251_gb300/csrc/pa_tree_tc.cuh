@@ -979,6 +979,9 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                         // their V rows are zeroed; the row's maximum in use, and O's scale, are settled first
                         if (!first && !mbar_wait_bounded(&M->pvdone[tc_buf<Units>(t - 1, wg)], tc_phase<Units>(t - 1)))
                             return false;
+                        // (with two row tiles only this warpgroup reads its O)
+                        if (Units == 1 && first && ke > 0 && !mbar_wait_bounded(&M->ofree, (ke - 1) & 1u))
+                            return false;
                         tc_fence_after();
                         if (warp_live) {
                             const float mx = fmaxf(m, top == -INFINITY ? -INFINITY : top * sc);
