@@ -1106,8 +1106,10 @@ __device__ inline bool tc_softmax(const TreeParams &p, char *smem, TcMisc *M, ui
                 }
                 l += l2.x + l2.y;
                 tmem_wait_st();
-            } else if (Units == 2 && lane == 0) {
-                mbar_arrive(&M->pfull[wg]);
+            } else if (Units == 2) {
+                __syncwarp();  // (lanes may have zeroed V rows of the first half)
+                if (lane == 0)
+                    mbar_arrive(&M->pfull[wg]);
             }
             tc_fence_before();
             __syncwarp();

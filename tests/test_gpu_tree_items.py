@@ -42,3 +42,32 @@ def test_neighbours_of_non_finite_drafts_keep_their_bits(dtype, t, h, every):
         assert not torch.isfinite(out[hit][..., 9]).any()
         assert torch.isfinite(out[hit][..., :9]).all() and torch.isfinite(out[hit][..., 10:]).all()
     assert err.item() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("drafted", [1, 8, 16, 20])
+def test_rows_behind_the_context_where_warps_have_no_row(dtype, drafted):
+    """Two row tiles (24 tokens x 8 heads) with few drafted: warps without a live row
+    still zero the V rows behind the context, which hold NaN here."""
+    from paged_kv_cache_251_gb300 import pa
+    t, h, hkv, d, bs, n_seqs = 24, 16, 2, 128, 32, 60
+    lens = [drafted + (5 * s) % 200 for s in range(n_seqs)]
+    k, v, tables, lens_t = paged(44, lens, hkv, d, bs, dtype)
+    q = wl.normal_tensor(45, 3, (n_seqs, t, h, d), dtype=dtype).cuda()
+    drafts = torch.full((n_seqs,), drafted, dtype=torch.int32, device="cuda")
+    ws = pa.tree_workspace_for(q, k, tables.shape[1])
+
+    def run():
+        out = torch.full_like(q, float("nan"))
+        return pa.pa_decode_tree(out, q, k, v, tables, lens_t, draft_lens=drafts, workspace=ws)
+
+    last = tables.gather(1, ((lens_t.long() - 1) // bs)[:, None])[:, 0].long()
+    behind = torch.arange(bs, device="cuda") > ((lens_t - 1) % bs)[:, None]
+    rows = v.permute(0, 2, 1, 3)
+    held = rows[last]
+    rows[last] = torch.where(behind[:, :, None, None], torch.zeros_like(held), held)
+    clean = run()
+    assert torch.isfinite(clean).all()
+    rows[last] = torch.where(behind[:, :, None, None], torch.full_like(held, float("nan")), held)
+    for _ in range(20):
+        assert torch.equal(run(), clean)

@@ -106,3 +106,16 @@ def test_words_of_the_source():
     assert SOURCE.count("if (poisoned) {") == 1
     assert len(re.findall(r"mbar_arrive\(&M->ofree\)", SOURCE)) == 1
     assert "mbar_init(&M->ofree, 8);" in SOURCE
+
+
+def test_arrivals_for_a_warp_come_after_its_lanes():
+    """In the softmax one lane arrives for its warp, whose lanes have all written
+    something (weights, zeroed V rows, an accumulator): each such arrival follows a
+    __syncwarp() directly, and nothing that diverges lies between."""
+    body = SOURCE[SOURCE.index("inline bool tc_softmax("):SOURCE.index("pa_tree_tc_kernel(const TreeParams p")]
+    lines = [x.split("//")[0].strip() for x in body.splitlines()]
+    lines = [x for x in lines if x]
+    at = [i for i, x in enumerate(lines) if x.startswith("mbar_arrive(")]
+    assert len(at) >= 6
+    for i in at:
+        assert lines[i - 1] == "if (lane == 0)" and lines[i - 2] == "__syncwarp();", lines[i - 3:i + 1]
