@@ -113,6 +113,20 @@ def _stream(stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _own_workspace(stream, make, *args) -> torch.Tensor | None:
+    """make(*args) for a call on `stream` that was given no workspace: the memory
+    belongs to that stream (the call's own end is no end for the GPU; memory of
+    another stream could be handed out there while the kernels still use it)."""
+    if stream is None:
+        return make(*args)
+    with torch.cuda.stream(stream):
+        return make(*args)
+
+
+def _bytes(n: int, device) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -154,7 +168,7 @@ def pa_decode(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache
     if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
     if workspace is None:
-        workspace = workspace_for(q, bs, block_tables.shape[1], window, partition_size)
+        workspace = _own_workspace(stream, workspace_for, q, bs, block_tables.shape[1], window, partition_size)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.pa_decode(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                           _ptr(context_lens), N, H, num_kv_heads, d, bs, float(scale), int(window),
@@ -194,7 +208,7 @@ def pa_decode_shared_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.T
     if workspace is None:
         n = pa_decode_shared_prefix_workspace_size(N, H, d, bs, block_tables.shape[1], partition_size, group_size,
                                                    q.dtype)
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=q.device)
+        workspace = _own_workspace(stream, _bytes, max(n, 16), q.device)
     _check(_lib.pa_decode_shared_prefix(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                         _ptr(context_lens), _ptr(shared_lens), int(group_size), N, H, num_kv_heads,
                                         d, bs, float(scale), DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype],
@@ -248,8 +262,7 @@ def pa_decode_contiguous(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
     if q.dtype != k_cache.dtype or v_cache.dtype != k_cache.dtype:
         raise TypeError("q, k_cache and v_cache must share one dtype")
     if workspace is None:
-        n = pa_decode_workspace_size(N, H, d, 16, max(1, L // 16), window, partition_size)
-        workspace = None if n == 0 else torch.empty((n + 15) // 16 * 4, dtype=torch.float32, device=q.device)
+        workspace = _own_workspace(stream, workspace_for, q, 16, max(1, L // 16), window, partition_size)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.pa_decode_contiguous(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(context_lens), N, H,
                                      num_kv_heads, d, L, float(scale), int(window), DTYPE_CODE[q.dtype],
@@ -369,7 +382,7 @@ def pa_decode_quant(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v
     if v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape:
         raise TypeError("k_cache and v_cache must share one code dtype and shape")
     if workspace is None:
-        workspace = workspace_for(q, bs, block_tables.shape[1], window, partition_size)
+        workspace = _own_workspace(stream, workspace_for, q, bs, block_tables.shape[1], window, partition_size)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(_lib.pa_decode_quant(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                                 _ptr(context_lens), N, H, num_kv_heads, d, bs, float(scale), int(window),
@@ -621,7 +634,7 @@ def pa_decode_tree(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = tree_workspace_for(q, k_cache, block_tables.shape[1])
+        workspace = _own_workspace(stream, tree_workspace_for, q, k_cache, block_tables.shape[1])
     _call(_lib.pa_decode_tree, dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_tables.data_ptr(), context_lens.data_ptr(), _addr(draft_lens), _addr(tree_mask), n, t, h, hkv, d, bs,
           float(scale), DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace),
@@ -664,7 +677,7 @@ def pa_decode_scored(out: torch.Tensor, scores_out: torch.Tensor, q: torch.Tenso
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = scored_workspace_for(q, k_cache, block_tables.shape[1], partition_size)
+        workspace = _own_workspace(stream, scored_workspace_for, q, k_cache, block_tables.shape[1], partition_size)
     _call(_lib.pa_decode_scored, dev, stream, out.data_ptr(), scores_out.data_ptr(), _addr(scores_in), q.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), n, h, hkv, d, bs,
           float(scale), scores_out.shape[2], DTYPE_CODE[q.dtype], DTYPE_CODE[out.dtype], block_tables.shape[1], nb,
