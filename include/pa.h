@@ -558,7 +558,9 @@ PA_API pa_status pa_evict_select(int32_t *keep, int32_t *new_lens, float *scores
  *   dst_block_tables  int32 [num_seqs][dst_max_blocks_per_seq], or NULL: in
  *                 place, through block_tables.  In place needs j >= i.  The
  *                 destination blocks must not be read by the call otherwise
- *                 (blocks shared with another sequence are sources only)
+ *                 (blocks shared with another sequence are sources only; blocks
+ *                 that one of its sequences gave up are no destination of
+ *                 another: pa_bm_renew_batch sees to that)
  * An index outside [0, max_blocks_per_seq * block_size - b) or, in place,
  * below i, and a place outside the destination table, move nothing and are
  * flagged (PA_DEVERR_BAD_INDEX); a table entry outside the pool likewise

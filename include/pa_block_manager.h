@@ -79,12 +79,20 @@ PA_API pa_status pa_bm_append(pa_bm *bm, const int32_t *seqs, int n, int64_t *sl
  * rows behind an in-place pa_compact_kv.  Not available for window sequences. */
 PA_API pa_status pa_bm_truncate(pa_bm *bm, int seq, long long length);
 
-/* Give a sequence ceil(length / block_size) blocks from the free list in place
- * of its own, and that length: the destination of a pa_compact_kv into other
- * blocks.  The old blocks lose one reference (export the tables before this
- * call: pa_compact_kv reads them, and nothing else may be enqueued that writes
- * blocks handed out after it).  PA_ERR_NO_BLOCKS, with nothing changed, when
- * the free list is too short.  Not available for window sequences. */
+/* Give each of n different sequences ceil(lengths[i] / block_size) blocks from
+ * the free list in place of its own, and that length: the destinations of one
+ * pa_compact_kv into other blocks.  The old blocks lose one reference, after all
+ * fresh ones were taken, so no destination is a block that the same pa_compact_kv
+ * reads.  (Export the tables before this call: pa_compact_kv reads them, and
+ * nothing else may be enqueued that writes blocks handed out after it.)
+ * PA_ERR_NO_BLOCKS, with nothing changed, when the free list is too short for
+ * all.  Not available for window sequences. */
+PA_API pa_status pa_bm_renew_batch(pa_bm *bm, const int32_t *seqs, const long long *lengths, int n);
+
+/* pa_bm_renew_batch of one sequence, for a pa_compact_kv of that sequence alone:
+ * its old blocks may be handed out by the next call, another pa_bm_renew too, so
+ * enqueue its pa_compact_kv first.  Sequences moved by one pa_compact_kv are
+ * renewed by one pa_bm_renew_batch. */
 PA_API pa_status pa_bm_renew(pa_bm *bm, int seq, long long length);
 
 /* Tokens held by a sequence (-1 if it does not exist). */

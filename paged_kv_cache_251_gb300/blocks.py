@@ -24,6 +24,8 @@ _lib.pa_bm_truncate.argtypes = [P, I, ctypes.c_longlong]
 _lib.pa_bm_truncate.restype = I
 _lib.pa_bm_renew.argtypes = [P, I, ctypes.c_longlong]
 _lib.pa_bm_renew.restype = I
+_lib.pa_bm_renew_batch.argtypes = [P, P, P, I]
+_lib.pa_bm_renew_batch.restype = I
 _lib.pa_bm_length.argtypes = [P, I]
 _lib.pa_bm_length.restype = ctypes.c_longlong
 _lib.pa_bm_tables.argtypes = [P, P, P]
@@ -96,8 +98,20 @@ class BlockManager:
 
     def renew(self, seq: int, length: int) -> None:
         """Replace a sequence's blocks by fresh ones for `length` tokens (the
-        destination of pa_compact_kv); its old blocks are dropped."""
+        destination of a pa_compact_kv of this sequence alone, to be enqueued before
+        the next renew); its old blocks are dropped."""
         _check(_lib.pa_bm_renew(self._h, seq, length))
+
+    def renew_batch(self, seqs, lengths) -> None:
+        """Replace the blocks of different sequences by fresh ones for lengths[i]
+        tokens: the destinations of one pa_compact_kv.  The old blocks are dropped
+        after all fresh ones are taken, so none is both read and written by it."""
+        s = torch.as_tensor(seqs, dtype=torch.int32).contiguous()
+        n = torch.as_tensor(lengths, dtype=torch.int64).contiguous()
+        if s.dim() != 1 or s.shape != n.shape:
+            raise ValueError("seqs and lengths must be lists of one length")
+        _check(_lib.pa_bm_renew_batch(self._h, ctypes.c_void_p(s.data_ptr()), ctypes.c_void_p(n.data_ptr()),
+                                      s.numel()))
 
     def length(self, seq: int) -> int:
         return int(_lib.pa_bm_length(self._h, seq))

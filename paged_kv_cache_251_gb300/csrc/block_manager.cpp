@@ -194,28 +194,54 @@ pa_status pa_bm_truncate(pa_bm *bm, int seq, long long length) {
     return PA_OK;
 }
 
-pa_status pa_bm_renew(pa_bm *bm, int seq, long long length) {
-    if (!bm || !bm->valid(seq) || !bm->seqs[seq].live || bm->seqs[seq].ring || length < 0)
+pa_status pa_bm_renew_batch(pa_bm *bm, const int32_t *seqs, const long long *lengths, int n) {
+    if (!bm || n < 0 || (n > 0 && (!seqs || !lengths)))
         return PA_ERR_INVALID_ARGUMENT;
-    const long long blocks = length / bm->block_size + (length % bm->block_size != 0);
-    if (blocks > bm->max_blocks)
-        return PA_ERR_INVALID_ARGUMENT;
-    if (blocks > static_cast<long long>(bm->free_list.size()))
-        return PA_ERR_NO_BLOCKS;
-    pa_bm::Seq &s = bm->seqs[seq];
-    std::vector<int32_t> fresh;
-    try {
-        fresh.resize(static_cast<size_t>(blocks));
-    } catch (...) {  // no exception crosses the C interface
+    std::vector<std::vector<int32_t>> fresh;
+    std::vector<char> named;
+    try {  // no exception crosses the C interface
+        fresh.resize(static_cast<size_t>(n));
+        named.assign(static_cast<size_t>(bm->max_seqs), 0);
+    } catch (...) {
         return PA_ERR_NO_BLOCKS;
     }
-    for (int32_t &b : fresh)
-        bm->take(&b);
-    for (int32_t b : s.table)
-        bm->drop(b);
-    s.table.swap(fresh);
-    s.length = length;
+    long long need = 0;
+    for (int i = 0; i < n; ++i) {
+        if (!bm->valid(seqs[i]) || !bm->seqs[seqs[i]].live || bm->seqs[seqs[i]].ring || named[seqs[i]] ||
+            lengths[i] < 0)
+            return PA_ERR_INVALID_ARGUMENT;
+        named[seqs[i]] = 1;
+        const long long blocks = lengths[i] / bm->block_size + (lengths[i] % bm->block_size != 0);
+        if (blocks > bm->max_blocks)
+            return PA_ERR_INVALID_ARGUMENT;
+        need += blocks;
+    }
+    if (need > static_cast<long long>(bm->free_list.size()))
+        return PA_ERR_NO_BLOCKS;
+    try {
+        for (int i = 0; i < n; ++i)
+            fresh[i].resize(static_cast<size_t>(lengths[i] / bm->block_size + (lengths[i] % bm->block_size != 0)));
+    } catch (...) {
+        return PA_ERR_NO_BLOCKS;
+    }
+    // every fresh block is taken before the first old one is dropped: none of them
+    // is another sequence's source
+    for (std::vector<int32_t> &table : fresh)
+        for (int32_t &b : table)
+            bm->take(&b);
+    for (int i = 0; i < n; ++i) {
+        pa_bm::Seq &s = bm->seqs[seqs[i]];
+        for (int32_t b : s.table)
+            bm->drop(b);
+        s.table.swap(fresh[i]);
+        s.length = lengths[i];
+    }
     return PA_OK;
+}
+
+pa_status pa_bm_renew(pa_bm *bm, int seq, long long length) {
+    const int32_t one = seq;
+    return pa_bm_renew_batch(bm, &one, &length, 1);
 }
 
 long long pa_bm_length(const pa_bm *bm, int seq) {
