@@ -476,8 +476,9 @@ PA_API pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, co
  * largest beside that, however far below it.
  * A drafted token that some query does not attend has no influence on it,
  * whatever its K and V hold (infinities and NaN too).  The table holds at most
- * 2^30 tokens a sequence (max_blocks_per_seq * block_size); other arguments and
- * limits as pa_decode (window 0).
+ * 2^30 tokens a sequence (max_blocks_per_seq * block_size), a fp16 / bf16 pool
+ * at most 2^31 - 1 (block, kv head) tiles; other arguments and limits as
+ * pa_decode (window 0).
  */
 PA_API pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const void *v_cache,
                                 const int32_t *block_tables, const int32_t *context_lens, const int32_t *draft_lens,

@@ -18,10 +18,8 @@ cudaError_t launch_scores(DecodeParams &p, const float *in, float *out, long lon
 // workspace is sized for them).
 constexpr int kTreeSms = 152;
 
-// Whether the tree attention of 16-bit or fp32 caches takes the tensor-core
-// kernel, how many CTAs that has on a device of `sms` SMs, and its workspace
-// (two partials for each of kTreeSms CTAs).
-bool tree_tensor_cores(int dtype, int num_blocks, int num_kv_heads);
+// How many CTAs the tree attention of 16-bit caches has on a device of `sms`
+// SMs, and its workspace (two partials for each of kTreeSms CTAs).
 int tree_tc_ctas(int num_seqs, int num_kv_heads, int rows, int max_len, int sms);
 size_t tree_tc_workspace(int num_seqs, int num_kv_heads, int rows, int head_dim, int max_len);
 

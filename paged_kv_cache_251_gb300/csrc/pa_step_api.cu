@@ -100,11 +100,10 @@ void fill_decode(DecodeParams &p, void *out, const void *q, const void *k_cache,
 
 constexpr int kMaxDraft = 256;
 
-// The partitions of the general kernel, and the workspace of the kernel that
-// takes the call (`pool`: num_blocks; the workspace size is for pools of up to
-// 2^31 (block, kv head) tiles, which the tensor-core kernel addresses).
+// The partitions of the fp32 kernel, and the workspace of the kernel that takes
+// the call.
 pa_status plan_tree(int num_seqs, int num_draft, int num_heads, int num_kv_heads, int head_dim, int block_size,
-                    int max_blocks_per_seq, int dtype, int pool, DecodePlan *plan) {
+                    int max_blocks_per_seq, int dtype, DecodePlan *plan) {
     if (num_draft < 1 || num_draft > kMaxDraft)
         return fail(PA_ERR_INVALID_ARGUMENT, "num_draft must be 1 .. 256");
     if (num_kv_heads <= 0 || num_heads <= 0 || num_heads % num_kv_heads != 0)
@@ -115,7 +114,7 @@ pa_status plan_tree(int num_seqs, int num_draft, int num_heads, int num_kv_heads
                                      plan);
     if (st != PA_OK)
         return st;
-    if (tree_tensor_cores(dtype, pool, num_kv_heads)) {
+    if (dtype != PA_F32) {
         const long long max_len = static_cast<long long>(max_blocks_per_seq) * block_size;
         plan->workspace =
             tree_tc_workspace(num_seqs, num_kv_heads, num_draft * (num_heads / num_kv_heads), head_dim,
@@ -293,7 +292,7 @@ pa_status pa_rope_append_kv(void *q_out, const void *q, const void *k, const voi
 size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num_heads, int num_kv_heads, int head_dim,
                                      int block_size, int max_blocks_per_seq, pa_dtype dtype) {
     DecodePlan plan;
-    if (plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, dtype, 1,
+    if (plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq, dtype,
                   &plan) != PA_OK)
         return 0;
     return plan.workspace;
@@ -308,7 +307,7 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
     g_detail.clear();
     DecodePlan plan;
     pa_status st = plan_tree(num_seqs, num_draft, num_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                             dtype, num_blocks, &plan);
+                             dtype, &plan);
     if (st != PA_OK)
         return st;
     if (num_seqs == 0)
@@ -319,6 +318,9 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
         return st;
     if (static_cast<long long>(max_blocks_per_seq) * block_size > kMaxTokens)
         return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size is above 2^30");
+    // the tensor maps of 16-bit caches address (block, kv head) tiles by 32 bits
+    if (dtype != PA_F32 && static_cast<long long>(num_blocks) * num_kv_heads > INT_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is above 2^31 - 1");
     if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0)
         return fail(PA_ERR_INVALID_ARGUMENT, "tree_mask must be 8-byte aligned");
     if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
@@ -338,7 +340,7 @@ pa_status pa_decode_tree(void *out, const void *q, const void *k_cache, const vo
     p.row_tiles = 0;
     p.cuts = nullptr;
     if (plan.workspace > 0) {
-        if (tree_tensor_cores(dtype, num_blocks, num_kv_heads)) {
+        if (dtype != PA_F32) {
             // merge records, accumulators, (max, denominator) pairs
             const int tree_rows = num_draft * (num_heads / num_kv_heads);
             const size_t ctas = tree_tc_ctas(num_seqs, num_kv_heads, tree_rows, p.max_len, kTreeSms);

@@ -11,23 +11,18 @@ namespace pa {
 
 namespace {
 
-template <typename T, int R> const void *tree_fn(int head_dim) {
-    return head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_kernel<T, 64, R>)
-                          : reinterpret_cast<const void *>(&pa_tree_kernel<T, 128, R>);
-}
-template <int R> const void *tree_fn_of(int dtype, int head_dim, size_t *smem) {
+template <int R> const void *tree_fn(int head_dim, size_t *smem) {
     *smem = head_dim == 64 ? sizeof(TreeSmem<64, R>) : sizeof(TreeSmem<128, R>);
-    return dtype == PA_F32   ? tree_fn<float, R>(head_dim)
-           : dtype == PA_F16 ? tree_fn<__half, R>(head_dim)
-                             : tree_fn<__nv_bfloat16, R>(head_dim);
+    return head_dim == 64 ? reinterpret_cast<const void *>(&pa_tree_kernel<64, R>)
+                          : reinterpret_cast<const void *>(&pa_tree_kernel<128, R>);
 }
 
-pa_status launch_general(TreeParams &p, int dtype, int head_dim, int dev, cudaStream_t stream) {
+pa_status launch_f32(TreeParams &p, int head_dim, int dev, cudaStream_t stream) {
     const int rows = p.num_draft * (p.num_heads / p.num_kv_heads);
     const int R = rows > kTreeRows ? 2 : 1;
     p.row_tiles = (rows + R * kTreeRows - 1) / (R * kTreeRows);
     size_t smem = 0;
-    const void *fn = R == 1 ? tree_fn_of<1>(dtype, head_dim, &smem) : tree_fn_of<2>(dtype, head_dim, &smem);
+    const void *fn = R == 1 ? tree_fn<1>(head_dim, &smem) : tree_fn<2>(head_dim, &smem);
     int per_sm = 0;
     cudaError_t e = prepare_kernel(dev, fn, smem, kTreeThreads, &per_sm);
     if (e != cudaSuccess)
@@ -92,10 +87,6 @@ pa_status launch_tc(TreeParams &p, int dtype, int head_dim, int dev, int sms, cu
 
 }  // namespace
 
-bool tree_tensor_cores(int dtype, int num_blocks, int num_kv_heads) {
-    return dtype != PA_F32 && static_cast<long long>(num_blocks) * num_kv_heads <= INT_MAX;
-}
-
 // One CTA per SM, no more than there can be units of work.
 int tree_tc_ctas(int num_seqs, int num_kv_heads, int rows, int max_len, int sms) {
     const int tile_rows = rows > 128 ? 256 : 128;
@@ -120,10 +111,9 @@ pa_status launch_tree(TreeParams &p, int dtype, int head_dim, cudaStream_t strea
     cudaError_t e = device_sms(&dev, &sms);
     if (e != cudaSuccess)
         return cuda_fail(e, "device query");
-    void *args[] = {&p};
-    const bool tensor_cores = tree_tensor_cores(dtype, p.num_blocks, p.num_kv_heads);
+    const bool tensor_cores = dtype != PA_F32;
     const pa_status st = tensor_cores ? launch_tc(p, dtype, head_dim, dev, sms, stream)
-                                      : launch_general(p, dtype, head_dim, dev, stream);
+                                      : launch_f32(p, head_dim, dev, stream);
     if (st != PA_OK)
         return st;
     if (!tensor_cores && p.max_parts > 1) {

@@ -1,5 +1,5 @@
-// Tree attention over the paged cache: what its kernels share, the general
-// kernel, and the merge of partitions.
+// Tree attention over the paged cache: what its kernels share, the kernel for
+// fp32 caches, and the merge of its partitions.
 //
 // Sequence s has L = context_lens[s] cached tokens, the last T_s of them
 // drafted.  Row r = i * G + g of a (sequence, kv head) is query head g of
@@ -63,12 +63,12 @@ __device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed
 }
 
 // ---------------------------------------------------------------------------
-// General kernel: any dtype, on the CUDA cores.  A CTA of 128 threads takes 16 R
-// rows, 8 lanes a row and R rows a thread, and 64 tokens at a time, widened to fp32
-// in shared memory (one round trip a tile).  Scores: lane l of a row has tokens l,
-// l + 8, ... with whole dot products, no exchange; one maximum and one rescale a
-// tile; then the weights go through shared memory and lane l sums its D / 8
-// elements of the output over the attended tokens (others are never multiplied).
+// fp32 caches: on the CUDA cores.  A CTA of 128 threads takes 16 R rows, 8 lanes a
+// row and R rows a thread, and 64 tokens at a time in shared memory (one round trip
+// a tile).  Scores: lane l of a row has tokens l, l + 8, ... with whole dot products,
+// no exchange; one maximum and one rescale a tile; then the weights go through shared
+// memory and lane l sums its D / 8 elements of the output over the attended tokens
+// (others are never multiplied).
 // Shared memory's rate bounds it at many rows: with R = 2 each K or V element read
 // there serves two.  R = 2 above 16 rows (48 rows over 64 contexts of 32 to 2048
 // tokens, fp32, head_dim 128: 787 us, 1018 with R = 1); up to 16 half of its rows
@@ -88,12 +88,12 @@ template <int D, int R> struct TreeSmem {
     int phys[kTreePartition / 8];  // blocks of the partition, -1: left out
 };
 
-template <typename T, int D, int R>
+template <int D, int R>
 __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams p) {
     pdl_launch_dependents();
     pdl_wait();
     constexpr int E = D / 8;
-    constexpr int V = 16 / sizeof(T);  // elements per 16-byte load
+    constexpr int V = 4;  // elements per 16-byte load
     constexpr int kPer = kTreeTile / 8;  // tokens of a lane
     extern __shared__ __align__(16) char smem[];
     TreeSmem<D, R> *sh = reinterpret_cast<TreeSmem<D, R> *>(smem);
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             for (int e = 0; e < E; ++e) {
                 const int c = l8 + 8 * e;
                 sh->q[rl + kTreeRows * y][c] =
-                    live[y] ? static_cast<float>(static_cast<const T *>(p.q)[orow[y] * D + c]) * p.scale_log2 : 0.f;
+                    live[y] ? static_cast<const float *>(p.q)[orow[y] * D + c] * p.scale_log2 : 0.f;
                 acc[y][e] = 0.f;
             }
         }
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
             // in flight: one after another they took 6000 cycles a tile
             constexpr int kAhead = 8;
             for (int c0 = threadIdx.x; c0 < kTreeTile * D / V; c0 += kAhead * kTreeThreads) {
-                uint4 kx[kAhead], vx[kAhead];
+                float4 kx[kAhead], vx[kAhead];
                 bool on[kAhead];
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
@@ -168,16 +168,16 @@ __global__ void __launch_bounds__(kTreeThreads) pa_tree_kernel(const TreeParams 
                     if (on[u]) {
                         const long long at =
                             ((static_cast<long long>(phys) * p.num_kv_heads + kvh) * bs + t % bs) * D + e;
-                        kx[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k_cache) + at);
-                        vx[u] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(p.v_cache) + at);
+                        kx[u] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k_cache) + at);
+                        vx[u] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.v_cache) + at);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < kAhead; ++u) {
                     const int c = c0 + u * kTreeThreads, t = c / (D / V), e = (c - t * (D / V)) * V;
                     if (on[u]) {
-                        Elt<T>::unpack(kx[u], &sh->k[t][e]);
-                        Elt<T>::unpack(vx[u], &sh->v[t][e]);
+                        *reinterpret_cast<float4 *>(&sh->k[t][e]) = kx[u];
+                        *reinterpret_cast<float4 *>(&sh->v[t][e]) = vx[u];
                     }
                 }
             }
