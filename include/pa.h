@@ -508,7 +508,9 @@ PA_API size_t pa_decode_tree_workspace_size(int num_seqs, int num_draft, int num
  *   workspace     pa_decode_scored_workspace_size() bytes, 16-byte aligned
  *                 (the scores of every query head are kept there between the
  *                 passes)
- * The table holds at most 2^30 tokens a sequence.  Other arguments, limits and results as pa_decode with window 0.
+ * The table holds at most 2^30 tokens a sequence, the pool at most 2^31 - 1
+ * (block, kv head) tiles.  Other arguments, limits and results as pa_decode with
+ * window 0.
  */
 PA_API pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in, const void *q,
                                   const void *k_cache, const void *v_cache, const int32_t *block_tables,

@@ -48,7 +48,7 @@ const void *decode_gqa_kernel_f16(int block_size, int group);
 const void *decode_gqa_kernel_bf16(int block_size, int group);
 
 // The same kernels with every token's score written out (DecodeParams::logits),
-// for the scored decode.
+// for the scored decode: those that a pool of up to 2^31 - 1 tiles reaches.
 const void *scored_kernel_f32(int head_dim, int group);
 const void *scored_kernel_f16(int head_dim, int group);
 const void *scored_kernel_bf16(int head_dim, int group);

@@ -1,6 +1,6 @@
 // Scored-decode kernel instantiations for __nv_bfloat16 caches: the decode kernels with
-// every token's score written out (general kernel: head_dim 64/128, query
-// groups 2/4/8; one query head per kv head: head_dim 64/128, block 8/16/32;
+// every token's score written out (general kernel: head_dim 64, query groups
+// 2/4/8; one query head per kv head: head_dim 64/128, block 8/16/32;
 // tensor-core grouped heads: head_dim 128, block 8/16/32, query groups 2/4/8).
 #include "pa_decode_gqa.cuh"
 #include "pa_internal.h"
@@ -11,8 +11,7 @@ const void *scored_kernel_bf16(int head_dim, int group) {
 #define PA_CASE(D, G)                                                    \
     if (head_dim == D && group == G)                                     \
         return reinterpret_cast<const void *>(&pa_decode_kernel<__nv_bfloat16, D, G, true>);
-    PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
-    PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
+    PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
 #undef PA_CASE
     return nullptr;
 }

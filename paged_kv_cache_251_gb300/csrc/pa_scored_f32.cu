@@ -10,8 +10,8 @@ const void *scored_kernel_f32(int head_dim, int group) {
 #define PA_CASE(D, G)                                                    \
     if (head_dim == D && group == G)                                     \
         return reinterpret_cast<const void *>(&pa_decode_kernel<float, D, G, true>);
-    PA_CASE(64, 1) PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
-    PA_CASE(128, 1) PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
+    PA_CASE(64, 2) PA_CASE(64, 4) PA_CASE(64, 8)
+    PA_CASE(128, 2) PA_CASE(128, 4) PA_CASE(128, 8)
 #undef PA_CASE
     return nullptr;
 }

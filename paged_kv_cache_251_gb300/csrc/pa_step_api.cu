@@ -395,6 +395,11 @@ pa_status pa_decode_scored(void *out, float *scores_out, const float *scores_in,
         return fail(PA_ERR_INVALID_ARGUMENT, "scores_stride smaller than max_blocks_per_seq * block_size");
     if (num_kv_heads > 65535)
         return fail(PA_ERR_UNSUPPORTED, "num_kv_heads too large");
+    // the tensor maps address (block, kv head) tiles and query rows by 32 bits
+    if (static_cast<long long>(num_blocks) * num_kv_heads > INT_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "num_blocks * num_kv_heads is above 2^31 - 1");
+    if (static_cast<long long>(num_seqs) * num_heads > INT_MAX)
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * num_heads is above 2^31 - 1");
     if (workspace == nullptr || workspace_bytes < need.total())
         return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than pa_decode_scored_workspace_size()");
     if (!aligned16(workspace))
