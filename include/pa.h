@@ -381,8 +381,9 @@ PA_API pa_status pa_swap_blocks_quant(const int64_t *src_dst_pairs, int num_pair
  * for i < rot_dim / 2, with (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1)
  * when interleaved.  Elements from rot_dim on pass through unchanged (mscale
  * does not apply to them).  The angle's fraction of a turn is formed in
- * 64-bit fixed point, so positions up to 2^31 lose nothing; the sine, the
- * cosine and the rotation are fp32, rounded once to dtype.
+ * 64-bit fixed point, within 2^-31 turn of position * freq (of the double
+ * given) at every position; the sine, the cosine and the rotation are fp32,
+ * rounded once to dtype.
  */
 typedef enum {
     PA_ROPE_PLAIN = 0,  /* base^(-2i / rot_dim) */

@@ -2,11 +2,13 @@
 //
 // y_a = m (x_a cos t - x_b sin t), y_b = m (x_b cos t + x_a sin t) with
 // t = position * freq_i.  The angle is kept as a fraction of a turn in 64-bit
-// fixed point: freq_i / 2 pi is a 0.64 fraction (from the caller's double),
-// and position times it wraps modulo one turn exactly, so a far position loses
-// nothing and no 64-bit floating arithmetic runs per position.  Its top 32
-// bits, as a signed fraction in [-1/2, 1/2) turn, go to sincospif: the angle
-// is off by at most 2^-33 turn plus one fp32 rounding.
+// fixed point: freq_i / 2 pi is a 0.64 fraction, formed from the caller's double
+// with 1 / 2 pi in two doubles (one alone is off by 2^-54 relative: 2^-25 turn at
+// position 2^31), and position times it wraps modulo one turn exactly.  No 64-bit
+// floating arithmetic runs per position.  The fraction is off by 2^-64 turn a
+// position (two roundings), its top 32 bits by 2^-33: within 2^-31 turn at every
+// position.  They go to sincospif as a signed fraction in [-1/2, 1/2) turn, with
+// one fp32 rounding.
 //
 // The rows are read once and written once: HBM-bound, or launch-bound for a
 // decode step.  A CTA takes `tok` tokens.  It first forms their rot / 2
@@ -16,7 +18,7 @@
 // walk the CTA's rows (every token's q, k and v rows in order) y at a time,
 // kRopeUnroll rows' loads before the first is used.
 //
-// Measured: 16384 tokens of 40 + 40 heads of 128, fp16, adjacent pairs: 152 us,
+// Measured: 16384 tokens of 40 + 40 heads of 128, fp16, adjacent pairs: 153 us,
 // 6.6 TB/s of the bytes read and written (a plain copy of them takes 148 us).  Small
 // CTAs do best (128 threads, about 128 rows; 256 threads and 8 tokens: 172 us), as
 // do streaming stores (-10 us) and three rows in flight (four: +1 us, six: +7).
@@ -147,10 +149,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     // fraction once: 64-bit floating operations are scarce here)
     const int groups = kRopeThreads / half, j = threadIdx.x % half;
     if (static_cast<int>(threadIdx.x) < groups * half) {
-        // a fraction of a turn per position, in units of 2^-64 turn
-        double turns = p.freqs[j] * 0.15915494309189533577;
-        turns -= floor(turns);
-        const unsigned long long frac = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+        // a fraction of a turn per position, in units of 2^-64 turn: the product with 1 / 2 pi,
+        // its whole turns taken off (exactly), and what its rounding and the constant's left
+        constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18, kUnits = 18446744073709551616.0;
+        const double freq = p.freqs[j], turns = freq * kTurn;
+        const double rest = fma(freq, kTurnRest, fma(freq, kTurn, -turns));
+        const unsigned long long frac = static_cast<unsigned long long>(__double2ll_rn((turns - rint(turns)) * kUnits)) +
+                                        static_cast<unsigned long long>(__double2ll_rn(rest * kUnits));
         for (int t = threadIdx.x / half; t < ntok; t += groups) {
             const long long pos = static_cast<long long>(p.positions[tok0 + t]) * p.direction;
             const unsigned long long angle = frac * static_cast<unsigned long long>(pos);
