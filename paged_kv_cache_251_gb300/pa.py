@@ -446,16 +446,24 @@ def _dense(first: torch.Tensor, *rest) -> int:
     return dev
 
 
+# The current stream's handle and the current device, by torch's inner names where it
+# has them (the public ones make objects on the way, of a call of 11 us), else by the
+# public ones.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
+
+
 def _call(fn, dev: int, stream, *args) -> None:
     """Run a library call on `stream` (default: the device's current one) with
     device `dev` current."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev)
+        raw = _raw_stream(dev)
     else:
         if stream.device_index != dev:
             raise ValueError("the stream is on another device than the tensors")
         raw = stream.cuda_stream
-    if torch._C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
