@@ -520,7 +520,9 @@ PA_API pa_status pa_decode_scored(void *out, float *scores_out, const float *sco
                                   pa_dtype out_dtype, int max_blocks_per_seq, int num_blocks, int partition_size,
                                   void *workspace, size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
 
-/* Bytes of workspace pa_decode_scored needs (0 for bad arguments). */
+/* Bytes of workspace pa_decode_scored needs (0 for bad arguments): above all the
+ * scores, num_seqs * num_heads * max_blocks_per_seq * block_size floats whatever
+ * the contexts hold. */
 PA_API size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int head_dim, int block_size,
                                               int max_blocks_per_seq, int partition_size);
 

@@ -70,10 +70,10 @@ __device__ inline uint64_t tree_bits64(const TreeParams &p, int s, int committed
 // memory and lane l sums its D / 8 elements of the output over the attended tokens
 // (others are never multiplied).
 // Shared memory's rate bounds it at many rows: with R = 2 each K or V element read
-// there serves two.  R = 2 above 16 rows (48 rows over 64 contexts of 32 to 2048
-// tokens, fp32, head_dim 128: 787 us, 1018 with R = 1); up to 16 half of its rows
-// would be empty.  fp32, head_dim 64, 4 rows over two contexts of 8000 and 16000
-// tokens: 68 us, 1.45 TB/s; a 5-token tree over a hundred tokens: 11 us.
+// there serves two.  R = 2 above 16 rows (12 drafted, 32 / 8 heads of 128, 64 contexts
+// spread evenly from 32 to 2048 tokens: 750 us, 992 with R = 1); up to 16 half of its
+// rows would be empty.  4 rows of 64 elements, 8 kv heads, two contexts of 8000 and
+// 16000 tokens: 71 us, 1.4 TB/s; a 5-token tree over a hundred tokens: 11 us.
 
 constexpr int kTreeThreads = 128;
 constexpr int kTreeRows = kTreeThreads / 8;  // rows of a CTA, times R

@@ -27,8 +27,8 @@
 // bf16, 2.9e-4 instead of 2.1e-4 in fp16); an fp32 output takes hi + lo parts
 // (hi = round(p), lo = round(p - hi)), two accumulating products.  Two parts for
 // 16-bit outputs as well cost 234 -> 293, 72 -> 89 and 306 -> 433 us on the three
-// calls measured below; a caller who wants them asks for fp32.  In fp16 weights
-// are lifted above its small numbers (kTcLift).
+// calls measured below (fp32 outputs: 279, 87 and 455); a caller who wants them
+// asks for fp32.  In fp16 weights are lifted above its small numbers (kTcLift).
 //
 // Work is split evenly over the CTAs, one per SM: the tiles of all pairs
 // (sequence, kv head, row tile) in order, each pair counted with kTcPairCost
@@ -64,9 +64,11 @@
 // 512 to 2048 tokens, 8 drafted, 40 heads, fp16: 234 us, 6.3 TB/s of K/V.  64 of 16
 // to 8192 tokens, 16 drafted, 32 / 8 heads, bf16: 72 us, 5.2 TB/s; the CTAs' ends
 // spread over 15 us.  Both are bound by HBM while every CTA works.  4 of 65536 to
-// 131072 tokens, 64 drafted, 32 / 8 heads, bf16: 300 us, 5.2 TB/s and 1.0 PFLOP/s of
-// drafted rows (1.3 with the padding rows of the two row tiles): the two row tiles'
-// chains of S, exponentials and P V on one tensor core, 63 % active.
+// 131072 tokens, 64 drafted, 32 / 8 heads, bf16: 303 us at 2070 MHz, 5.2 TB/s and 1.0
+// PFLOP/s of drafted rows (1.3 with the padding rows of the two row tiles), 332 us
+// (4.7 TB/s) in a long run under the power limit: the two row tiles' chains of S,
+// exponentials and P V on one tensor core, 62 % active.  With 128 drafted (512 rows,
+// K/V read by two pairs of row tiles): 585 us.
 #pragma once
 
 #include "pa_decode_gqa.cuh"

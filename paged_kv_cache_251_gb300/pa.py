@@ -590,7 +590,8 @@ def tree_mask_from_parents(parents: torch.Tensor) -> torch.Tensor:
     """The mask of pa_decode_tree for trees given by parents, an integer tensor
     [N, T]: parents[s, i] < i is the drafted token before token i, or negative
     when it follows the last committed token.  A token attends itself and its
-    ancestors.  Returns int64 [N, T, ceil(T / 64)] on the device of parents."""
+    ancestors.  Returns int64 [N, T, ceil(T / 64)] on the device of parents.  Works
+    on the host: parents on a GPU are waited for and copied, so not during a capture."""
     n, t = parents.shape
     p = parents.to("cpu", torch.int64)
     if bool((p >= torch.arange(t)).any()):
