@@ -19,7 +19,12 @@
  *                      tree), and pa_compact_kv to commit the accepted ones;
  *   pa_decode_scored, pa_evict_select, pa_compact_kv  accumulate the attention
  *                      each cached token gets, choose the tokens to keep, and
- *                      move them together.
+ *                      move them together;
+ *   pa_verify_drafts   accept or reject drafted tokens and draw the next one;
+ *   pa_append_kv_block_quant, pa_decode_block_quant  an 8-bit cache with one
+ *                      scale for each block and kv head;
+ *   pa_pages_update, pa_pages_compact, pa_copy_pages  block tables and
+ *                      reference counts kept on the device.
  *
  * Sources (web pages on PagedAttention):
  *   [A] "PagedAttention: From Operating System Virtual Memory to Large
@@ -117,7 +122,10 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT 0x8u   /* a pipeline wait gave up (about 2 s); the output is not valid */
 #define PA_DEVERR_BAD_LEN 0x10u  /* decode: context_lens[s] > max_blocks_per_seq * block_size; clamped to that */
 #define PA_DEVERR_BAD_LAUNCH 0x20u /* a kernel refused its launch configuration; the output is not valid */
-#define PA_DEVERR_BAD_INDEX 0x40u /* compact: a kept index outside the sequence, or below its place; the row was not moved */
+#define PA_DEVERR_BAD_INDEX 0x40u /* compact: a kept index outside the sequence, or below its place; the row was not moved.
+                                   * verify: a drafted token or parent out of range; the token was left out.
+                                   * pages: a parent row out of range; the row starts empty */
+#define PA_DEVERR_BAD_COUNT 0x80u /* pages: a reference count below 0, or below what the tables hold */
 
 /*
  * Bytes of scratch pa_decode needs for split-context partials (0 when no
@@ -577,6 +585,209 @@ PA_API pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep
                                const int32_t *dst_block_tables, int num_seqs, int keep_heads, int keep_stride,
                                int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq,
                                int dst_max_blocks_per_seq, int num_blocks, pa_dtype dtype, uint32_t *err_word,
+                               pa_stream_t stream);
+
+/*
+ * Verification of drafted tokens, the step of speculative decoding after
+ * pa_decode_tree: which drafted tokens are kept, and the token after them, so
+ * that the kept tokens are distributed as if the target had drawn each.
+ * Random numbers are inputs.  In a sequence's tree the walk stands at a node
+ * (first the last committed token, -1), whose next token has the target
+ * distribution p = target_probs[s][node + 1] and was drafted from
+ * q = draft_probs[s][node + 1].  The drafted tokens i are taken in order; if
+ * parents[s][i] is the present node, token x = draft_tokens[s][i] is
+ *   accepted when  u S q(x) < w(x),  u = uniforms[s][i]: the walk moves to i
+ *   rejected otherwise: a becomes a + S
+ * with w = max(0, p - a q); a = 0 and S = 1 where the walk arrives, S = sum w
+ * after a rejection.  (Children of a node are taken as drawn independently
+ * from q.)  With draft_probs NULL the drafted tokens were chosen, not drawn:
+ * accepted when u S < w(x), w being p without the rejected tokens, and S losing
+ * p(x) of each.  At the end the next token is the first x whose running sum
+ * w(0) + .. + w(x) exceeds uniforms[s][num_draft] sum w (a random number of 1 or
+ * more: the last x with w(x) > 0); if no w is positive, p takes its place; if
+ * no p is, the token is -1.
+ *   accept_lens   int32 [num_seqs] (written): accepted tokens, n
+ *   accepted      int32 [num_seqs][num_draft] (written): their indices, which
+ *                 ascend, then -1: the keep list of pa_compact_kv
+ *                 (keep_heads 1, keep_lens accept_lens)
+ *   tokens        int32 [num_seqs][num_draft + 1] (written): the accepted
+ *                 tokens, the next token, then -1
+ *   target_probs  [num_seqs][num_draft + 1] rows of vocab_size entries of dtype,
+ *                 target_stride elements apart: the target's probabilities after
+ *                 the last committed token, and after each drafted one
+ *   draft_probs   [num_seqs][num_draft] rows, draft_stride elements apart, or
+ *                 NULL: row 0 behind the last committed token, row i behind
+ *                 drafted token i - 1 (in a chain: what token i was drawn from)
+ *   draft_lens    int32 [num_seqs], clamped to [0, num_draft] and flagged
+ *                 (PA_DEVERR_BAD_LEN) outside it; NULL: num_draft everywhere
+ *   parents       int32 [num_seqs][num_draft], parents[s][i] < i, negative behind
+ *                 the last committed token; NULL: i - 1, a chain
+ *   uniforms      fp32 [num_seqs][num_draft + 1], in [0, 1)
+ *   num_draft     1 .. 256;  vocab_size 1 .. 2^30
+ * A drafted token outside the vocabulary, or with a parent that does not come
+ * before it, is left out and flagged (PA_DEVERR_BAD_INDEX).  Probabilities are
+ * taken as given (rows are not normalised); an entry that is NaN in p or q
+ * counts as w = 0; a row with entries outside [0, 1] gives some token of the
+ * vocabulary or -1.  w and its sums are exact to about 2^-46, so a token depends on
+ * no rounding of 32 bits, and the same inputs give the same tokens on every call.
+ * Outputs must not overlap inputs.
+ */
+PA_API pa_status pa_verify_drafts(int32_t *accept_lens, int32_t *accepted, int32_t *tokens, const void *target_probs,
+                                  const void *draft_probs, const int32_t *draft_tokens, const int32_t *draft_lens,
+                                  const int32_t *parents, const float *uniforms, int num_seqs, int num_draft,
+                                  int vocab_size, long long target_stride, long long draft_stride, pa_dtype dtype,
+                                  uint32_t *err_word, pa_stream_t stream);
+
+/*
+ * 8-bit cache with one fp32 scale for each (block, kv head), K and V apart: an
+ * element is code * scale.  (pa_append_kv_quant's pages hold a scale for each
+ * row.)  Layouts:
+ *   k_cache, v_cache    codes [num_blocks][num_kv_heads][block_size][head_dim]
+ *   k_scales, v_scales  fp32 [num_blocks][num_kv_heads]
+ *
+ * Append: token i's K and V rows (dtype PA_F32 / PA_F16 / PA_BF16) go to slot
+ * slot_mapping[i] (padding and out-of-range slots as pa_append_kv).  For every
+ * block that the call writes rows of, and every kv head, of K and of V alike:
+ *   mine  = max |x| of the rows written / Q   (Q = 127 PA_I8, 448 PA_E4M3; one
+ *           fp32 division; infinities and NaN not counted)
+ *   scale = mine, if the call writes row 0 of the block (the block starts anew);
+ *           else the larger of mine and the scale before
+ *   codes of the rows written: x / scale (fp32) rounded as by
+ *           pa_append_kv_quant, infinities saturating, NaN and everything in a
+ *           block of scale 0 coded 0
+ * and where the scale grew, all other rows of the block are coded again:
+ * code * scale before (rounded to fp32) / scale, rounded likewise.  So a
+ * block's values may move by half a step of the new scale whenever a later token
+ * enlarges it.  A block whose row 0 was never written needs a scale (0 will do).
+ * Two tokens must not name one slot (one of them is stored, unspecified which).
+ *   workspace   pa_append_kv_block_quant_workspace_size() bytes, 4-byte
+ *               aligned, of any contents (may be NULL when that size is 0)
+ */
+PA_API pa_status pa_append_kv_block_quant(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,
+                                          void *v_cache, float *k_scales, float *v_scales, int num_tokens,
+                                          int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                                          pa_dtype dtype, pa_dtype cache_dtype, void *workspace,
+                                          size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
+
+/* Bytes of workspace pa_append_kv_block_quant needs: 4 for each slot of the pool
+ * for calls of more than 512 tokens, else 0 (and for bad arguments). */
+PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_size, int num_blocks);
+
+/*
+ * pa_decode over such a cache.  q (dtype PA_F32 / PA_F16 / PA_BF16), out, window
+ * and the other arguments as pa_decode; there is no partition size: the
+ * contexts of the whole batch are cut evenly over the GPU.  The same inputs give the
+ * same bits on every call (a sequence decoded in another batch may differ in the
+ * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
+ * to 2^-40 of a row's largest element, fp32 queries to 2^-33, softmax weights to
+ * 22 bits.  An E4M3 NaN code (which no append writes) reads as +-480.
+ * Entries of the scale arrays for blocks outside the attended ones are not used.
+ * The table holds at most 2^30 tokens a sequence.
+ *   workspace   pa_decode_block_quant_workspace_size() bytes, 16-byte aligned
+ */
+PA_API pa_status pa_decode_block_quant(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                       const float *k_scales, const float *v_scales, const int32_t *block_tables,
+                                       const int32_t *context_lens, int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int block_size, float scale, int window, pa_dtype dtype,
+                                       pa_dtype cache_dtype, pa_dtype out_dtype, int max_blocks_per_seq,
+                                       int num_blocks, void *workspace, size_t workspace_bytes, uint32_t *err_word,
+                                       pa_stream_t stream);
+
+/* Bytes of workspace pa_decode_block_quant needs (0 for bad arguments). */
+PA_API size_t pa_decode_block_quant_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                                   int block_size, int max_blocks_per_seq);
+
+/*
+ * Block tables and reference counts on the device: what the block manager
+ * (pa_block_manager.h) does on the host, for loops that do not return to the host
+ * between steps (captured into a graph, say).  A pool is kept by one of the two.  The
+ * state is ref_counts, int32 [num_blocks] (0: free), and tables; there is no
+ * free list: free blocks are handed out in ascending order.
+ *
+ * The next step's tables.  A row of `tables` holds (one reference each) the
+ * blocks of its first lens[r] tokens.  Row i of new_tables takes over the first
+ * k = min(keep_lens[i], lens[parents[i]]) tokens of row parents[i] (a negative
+ * parent: none), with their blocks, and gets room for g = max(grow_lens[i], k)
+ * tokens: rows are kept (parents[i] = i), cut (keep_lens below lens), forked (named
+ * twice), freed (not named) and grown in one call.  The old rows' references end.
+ * Where g > k and k is not a whole number of blocks, tokens will be written to
+ * the row's last kept block: it is copied into a fresh block (copy-on-write), unless
+ * all its holders are rows that write to it and this row is the first of them.
+ * The blocks that are then free go, ascending, to row 0, 1, .. : first the copy,
+ * then the growth.
+ *   new_tables    int32 [num_rows][max_blocks_per_seq] (written; -1 behind a row's
+ *                 blocks); must not overlap tables
+ *   new_ref_counts  int32 [num_blocks] (written); may be ref_counts
+ *   pairs         int64 [num_rows][2] (written): row i's copy (source,
+ *                 destination), or (-1, -1): for pa_copy_pages, before anything
+ *                 is written to the new blocks or the old ones that were freed
+ *   status        int32 [4] (written): 1, the blocks handed out, the blocks
+ *                 still free, the copies; or, when there are too few free
+ *                 blocks, 0, the blocks needed, the blocks free, 0: then
+ *                 new_tables and new_ref_counts are left as they were and all pairs
+ *                 are (-1, -1)
+ *   tables        int32 [old_rows][max_blocks_per_seq]
+ *   lens          int32 [old_rows], clamped to [0, max_blocks_per_seq * block_size]
+ *                 and flagged (PA_DEVERR_BAD_LEN) outside it
+ *   parents       int32 [num_rows]; NULL: row i continues row i (num_rows <=
+ *                 old_rows).  A parent >= old_rows counts as negative and is
+ *                 flagged (PA_DEVERR_BAD_INDEX)
+ *   keep_lens, grow_lens  int32 [num_rows]; grow_lens above
+ *                 max_blocks_per_seq * block_size is clamped to it and flagged
+ *                 (PA_DEVERR_BAD_LEN)
+ *   workspace     pa_pages_workspace_size(max(num_rows, old_rows), num_blocks)
+ *                 bytes, 4-byte aligned, of any contents
+ * References beyond those of the tables (a prompt cache's) are kept.  Table
+ * entries outside the pool are carried along, hold nothing and are flagged
+ * (PA_DEVERR_BAD_BLOCK).  A count that falls below 0 is flagged
+ * (PA_DEVERR_BAD_COUNT).  block_size is any positive number.
+ */
+PA_API pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t *pairs, int32_t *status,
+                                 const int32_t *tables, const int32_t *ref_counts, const int32_t *lens,
+                                 const int32_t *parents, const int32_t *keep_lens, const int32_t *grow_lens,
+                                 int num_rows, int old_rows, int max_blocks_per_seq, int block_size, int num_blocks,
+                                 void *workspace, size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
+
+/*
+ * Move the used blocks of a pool to its front (to give back the rest, or to find
+ * it in one piece).  With U blocks in use, the highest of them goes to the lowest
+ * free block, the next to the next, until all lie below U or max_moves are made.
+ *   new_tables    int32 [num_rows][max_blocks_per_seq] (written): tables with the
+ *                 blocks' new places, -1 behind lens; may be tables
+ *   new_ref_counts  int32 [num_blocks] (written); may be ref_counts
+ *   remap         int32 [num_blocks] (written): every block's place now, for holders
+ *                 other than the tables
+ *   pairs         int64 [max_moves][2] (written): the moves (source,
+ *                 destination), then (-1, -1): for pa_copy_pages
+ *   status        int32 [4] (written): the moves made, U, 1 + the highest
+ *                 block in use after them, the moves that would have been needed
+ *   workspace     pa_pages_workspace_size(num_rows, num_blocks) bytes, 4-byte
+ *                 aligned, of any contents
+ * lens, and table entries outside the pool, as pa_pages_update.
+ */
+PA_API pa_status pa_pages_compact(int32_t *new_tables, int32_t *new_ref_counts, int32_t *remap, int64_t *pairs,
+                                  int32_t *status, const int32_t *tables, const int32_t *ref_counts,
+                                  const int32_t *lens, int num_rows, int max_blocks_per_seq, int block_size,
+                                  int num_blocks, int max_moves, void *workspace, size_t workspace_bytes,
+                                  uint32_t *err_word, pa_stream_t stream);
+
+/* Bytes of workspace the two need (0 for bad arguments). */
+PA_API size_t pa_pages_workspace_size(int num_rows, int num_blocks);
+
+/*
+ * Copy blocks within each of up to 8 pools (K, V, their scales, of any
+ * number of layers' caches and any type): for every pair (src, dst) with src >= 0
+ * block src goes onto block dst, in every pool.  A negative src is padding; a
+ * pair outside the pool is skipped and flagged (PA_DEVERR_BAD_PAIR).  Sources and
+ * destinations must differ, and no destination may be named twice, as for
+ * pa_copy_blocks.
+ *   src_dst_pairs int64 [num_pairs][2]
+ *   pools         HOST array of num_pools device pointers, 4-byte aligned
+ *   block_bytes   HOST array [num_pools]: bytes of a block, multiples of 4
+ *                 (16 bytes are moved at once where pointer and size allow)
+ */
+PA_API pa_status pa_copy_pages(const int64_t *src_dst_pairs, int num_pairs, void *const *pools,
+                               const long long *block_bytes, int num_pools, int num_blocks, uint32_t *err_word,
                                pa_stream_t stream);
 
 /* Static text for a status code. */

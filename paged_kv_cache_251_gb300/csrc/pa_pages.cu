@@ -1,0 +1,535 @@
+// Block tables and reference counts on the device: the tables of a next step
+// (rows kept, forked, cut, freed and grown, shared last blocks copied on write), the
+// used blocks of a pool moved to its front, and the copies that both ask for.
+// ("PagedAttention — 把 KV cache 当虚拟内存页来管理", 案例 3: reference counts,
+// copy-on-write, one block is the copy unit.)
+//
+// A block is free when its count is 0; free blocks are handed out in ascending
+// order, row by row, so the result is a function of the inputs alone.
+//
+// The first two are bound by latency: a few dependent passes over arrays of some
+// hundred KB, each needing the whole of the one before.  Both are a single kernel of
+// one cluster of CTAs, its barriers between the passes (a launch a pass would cost
+// more than a pass).  Ordered ranks (which free block is the k-th) are a count a CTA,
+// exchanged through shared memory, and a scan within it.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_pages.h"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+
+namespace {
+
+constexpr int kPageThreads = 1024;
+constexpr int kPageWarps = kPageThreads / 32;
+constexpr int kPageCluster = 8;
+constexpr int kCopied = 1 << 31;
+
+struct PagesShared {
+    int warp[kPageWarps];
+    int tile;                      // of block_scan
+    long long total[2][kPageCluster];  // every CTA's counts
+};
+
+// Exclusive prefix of `x` over the CTA's threads; *all gets the sum.
+__device__ inline int block_scan(int x, PagesShared *sh, int *all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o)
+            incl += y;
+    }
+    __syncthreads();  // (the last call's sums were read)
+    if (lane == 31)
+        sh->warp[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        int w = sh->warp[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o)
+                w += y;
+        }
+        sh->warp[lane] = w;
+    }
+    __syncthreads();
+    *all = sh->warp[kPageWarps - 1];
+    return incl - x + (warp ? sh->warp[warp - 1] : 0);
+}
+
+__device__ inline int blocks_of(long long tokens, int block_size) {
+    return static_cast<int>((tokens + block_size - 1) / block_size);
+}
+
+// A row of the update, from its inputs.
+struct Row {
+    int parent;  // -1: none
+    int keep, grow;  // tokens
+    int kept, total;  // blocks
+    int last;  // the last kept block if tokens are written behind its kept ones, else -1
+};
+
+__device__ inline int held_len(const PagesUpdateParams &p, int row) {
+    const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    const int n = p.lens[row];
+    return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
+}
+
+__device__ inline Row row_of(const PagesUpdateParams &p, int i) {
+    const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    Row r;
+    r.parent = p.parents ? p.parents[i] : i;
+    if (r.parent < 0 || r.parent >= p.old_rows)
+        r.parent = -1;
+    const int have = r.parent >= 0 ? held_len(p, r.parent) : 0;
+    const int keep = p.keep[i];
+    r.keep = keep < 0 ? 0 : (keep > have ? have : keep);
+    const long long grow = p.grow[i];
+    r.grow = grow > most ? static_cast<int>(most) : (grow < r.keep ? r.keep : static_cast<int>(grow));
+    r.kept = blocks_of(r.keep, p.block_size);
+    r.total = blocks_of(r.grow, p.block_size);
+    r.last = -1;
+    if (r.grow > r.keep && r.keep % p.block_size != 0) {
+        const int b = p.tables[static_cast<long long>(r.parent) * p.max_blocks + r.kept - 1];
+        if (b >= 0 && b < p.num_blocks)
+            r.last = b;
+    }
+    return r;
+}
+
+// Adds `by` to the counts of entries [j0, j1) of an old row (a warp).
+__device__ inline void count_entries(const PagesUpdateParams &p, int row, int j0, int j1, int by, int lane) {
+    const int32_t *t = p.tables + static_cast<long long>(row) * p.max_blocks;
+    bool bad = false;
+    for (int j = j0 + lane; j < j1; j += 32) {
+        const int b = t[j];
+        if (b >= 0 && b < p.num_blocks)
+            atomicAdd(p.count + b, by);
+        else
+            bad = true;
+    }
+    if (bad && p.err)
+        atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+}
+
+__global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const PagesUpdateParams p) {
+    __shared__ PagesShared shared;
+    PagesShared *sh = &shared;
+    pdl_launch_dependents();
+    pdl_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
+    const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
+
+    // counts to work on, and a clean slate where rows will meet
+    for (int b = gtid; b < p.num_blocks; b += gthreads)
+        p.count[b] = p.refs[b];
+    for (int r = gtid; r < p.old_rows; r += gthreads)
+        p.children[r] = 0;
+    for (int i = gtid; i < p.rows; i += gthreads) {
+        const Row r = row_of(p, i);
+        if (r.last >= 0) {
+            p.first[r.last] = p.rows;
+            p.writers[r.last] = 0;
+        }
+    }
+    cluster.sync();
+
+    // children of the old rows, writers of the last blocks
+    for (int i = gtid; i < p.rows; i += gthreads) {
+        const Row r = row_of(p, i);
+        if (r.parent >= 0) {
+            atomicAdd(p.children + r.parent, 1);
+            atomicExch(p.child + r.parent, i);  // (of use to an only child)
+        }
+        if (r.last >= 0) {
+            atomicMin(p.first + r.last, i);
+            atomicAdd(p.writers + r.last, 1);
+        }
+        const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+        const int given = p.parents ? p.parents[i] : i;
+        if (p.err && given >= p.old_rows)
+            atomicOr(p.err, PA_DEVERR_BAD_INDEX);
+        if (p.err && p.grow[i] > most)
+            atomicOr(p.err, PA_DEVERR_BAD_LEN);
+    }
+    cluster.sync();
+
+    // references: an old row lets go of its blocks, its children hold what they
+    // keep.  What an only child keeps changes nothing.
+    for (int r = gwarp; r < p.old_rows; r += gwarps) {
+        const int n = blocks_of(held_len(p, r), p.block_size);
+        if (lane == 0 && p.err) {
+            const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+            if (p.lens[r] < 0 || p.lens[r] > most)
+                atomicOr(p.err, PA_DEVERR_BAD_LEN);
+        }
+        const int children = __ldcg(p.children + r);
+        const int from = children == 1 ? row_of(p, __ldcg(p.child + r)).kept : 0;
+        count_entries(p, r, from, n, -1, lane);
+    }
+    for (int i = gwarp; i < p.rows; i += gwarps) {
+        const Row r = row_of(p, i);
+        if (r.parent >= 0 && __ldcg(p.children + r.parent) > 1)
+            count_entries(p, r.parent, 0, r.kept, 1, lane);
+    }
+    cluster.sync();
+
+    // what each row needs, and how many blocks are free, a share a CTA
+    const int rows_share = (p.rows + kPageCluster - 1) / kPageCluster;
+    const int i0 = min(rank * rows_share, p.rows), i1 = min(i0 + rows_share, p.rows);
+    const int share = (p.num_blocks + kPageCluster - 1) / kPageCluster;
+    const int b0 = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(p.num_blocks)));
+    const int b1 = p.num_blocks - b0 < share ? p.num_blocks : b0 + share;
+    long long needs = 0;
+    int all;
+    for (int at = i0; at < i1; at += kPageThreads) {
+        const int i = at + tid;
+        int need = 0;
+        if (i < i1) {
+            const Row r = row_of(p, i);
+            // a last block stays where all its holders write to it, with the first of them
+            const bool copied = r.last >= 0 && !(__ldcg(p.writers + r.last) == __ldcg(p.count + r.last) &&
+                                                 __ldcg(p.first + r.last) == i);
+            need = r.total - r.kept + copied;
+            p.need[i] = need | (copied ? kCopied : 0);
+        }
+        const int before = block_scan(need, sh, &all);
+        if (i < i1)
+            p.base[i] = static_cast<int>(needs) + before;  // within the CTA's rows
+        needs += all;
+    }
+    long long spare = 0;
+    {
+        int mine = 0;
+        for (int b = b0 + tid; b < b1; b += kPageThreads)
+            mine += __ldcg(p.count + b) == 0;
+        block_scan(mine, sh, &all);
+        spare = all;
+    }
+    if (tid < kPageCluster) {
+        PagesShared *to = cluster.map_shared_rank(sh, tid);
+        to->total[0][rank] = needs;
+        to->total[1][rank] = spare;
+    }
+    cluster.sync();
+
+    long long needed = 0, free = 0, need_before = 0, free_before = 0;
+    for (int r = 0; r < kPageCluster; ++r) {
+        if (r == rank) {
+            need_before = needed;
+            free_before = free;
+        }
+        needed += sh->total[0][r];
+        free += sh->total[1][r];
+    }
+    const bool done = needed <= free;
+    if (!done) {  // nothing changes
+        for (int i = gtid; i < p.rows; i += gthreads) {
+            p.pairs[2 * i] = -1;
+            p.pairs[2 * i + 1] = -1;
+        }
+        if (gtid == 0) {
+            p.status[0] = 0;
+            p.status[1] = needed > 0x7fffffff ? 0x7fffffff : static_cast<int>(needed);
+            p.status[2] = static_cast<int>(free);
+            p.status[3] = 0;
+        }
+        return;
+    }
+    // the free blocks in order, as far as they are needed; copied blocks lose a holder
+    if (free_before < needed) {
+        long long at = free_before;
+        for (int t0 = b0; t0 < b1; t0 += kPageThreads) {
+            const int b = t0 + tid;
+            const int is = b < b1 && __ldcg(p.count + b) == 0;
+            const long long k = at + block_scan(is, sh, &all);
+            if (is && k < needed)
+                p.free_list[k] = b;
+            at += all;
+        }
+    }
+    cluster.sync();
+    int copies = 0;
+    for (int at = i0; at < i1; at += kPageThreads) {
+        const int i = at + tid;
+        if (i < i1) {
+            const int need = p.need[i];
+            const int base = static_cast<int>(need_before) + p.base[i];
+            p.base[i] = base;
+            int64_t src = -1, dst = -1;
+            if (need & kCopied) {
+                src = row_of(p, i).last;
+                dst = __ldcg(p.free_list + base);
+                atomicAdd(p.count + src, -1);
+                ++copies;
+            }
+            p.pairs[2 * static_cast<long long>(i)] = src;
+            p.pairs[2 * static_cast<long long>(i) + 1] = dst;
+        }
+    }
+    block_scan(copies, sh, &all);
+    if (tid < kPageCluster)
+        cluster.map_shared_rank(sh, tid)->total[0][rank] = all;
+    for (long long k = gtid; k < needed; k += gthreads)
+        p.count[__ldcg(p.free_list + k)] = 1;
+    cluster.sync();
+
+    for (int b = gtid; b < p.num_blocks; b += gthreads) {
+        const int c = __ldcg(p.count + b);
+        p.new_refs[b] = c;
+        if (c < 0 && p.err)
+            atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+    }
+    constexpr int kSegment = 1024;  // entries of a warp
+    const int segments = (p.max_blocks + kSegment - 1) / kSegment;
+    for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
+        const int i = static_cast<int>(u / segments), j0 = static_cast<int>(u % segments) * kSegment;
+        const int j1 = p.max_blocks - j0 < kSegment ? p.max_blocks : j0 + kSegment;
+        const Row r = row_of(p, i);
+        const bool copied = __ldcg(p.need + i) & kCopied;
+        const int base = __ldcg(p.base + i);
+        const int32_t *from = p.tables + static_cast<long long>(r.parent < 0 ? 0 : r.parent) * p.max_blocks;
+        int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
+        bool bad = false;
+#pragma unroll 4
+        for (int j = j0 + lane; j < j1; j += 32) {
+            int b = -1;
+            if (j < r.kept) {
+                b = copied && j == r.kept - 1 ? __ldcg(p.free_list + base) : from[j];
+                bad |= b < 0 || b >= p.num_blocks;
+            } else if (j < r.total && base + copied + (j - r.kept) < needed) {
+                b = __ldcg(p.free_list + base + copied + (j - r.kept));
+            }
+            to[j] = b;
+        }
+        if (bad && p.err)
+            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+    }
+    if (gtid == 0) {
+        long long n = 0;
+        for (int r = 0; r < kPageCluster; ++r)
+            n += sh->total[0][r];
+        p.status[0] = 1;
+        p.status[1] = static_cast<int>(needed);
+        p.status[2] = static_cast<int>(free - needed);
+        p.status[3] = static_cast<int>(n);
+    }
+}
+
+// With U blocks in use, a used block b >= U that has k used blocks above it goes
+// to the k-th free block below U (there are as many).
+__global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const PagesCompactParams p) {
+    __shared__ PagesShared shared;
+    PagesShared *sh = &shared;
+    pdl_launch_dependents();
+    pdl_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
+    const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
+    const int share = (p.num_blocks + kPageCluster - 1) / kPageCluster;
+    const int b0 = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(p.num_blocks)));
+    const int b1 = p.num_blocks - b0 < share ? p.num_blocks : b0 + share;
+    int all;
+    {
+        int mine = 0;
+        for (int b = b0 + tid; b < b1; b += kPageThreads) {
+            const int c = p.refs[b];
+            mine += c > 0;
+            if (c < 0 && p.err)
+                atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+        }
+        block_scan(mine, sh, &all);
+        if (tid < kPageCluster)
+            cluster.map_shared_rank(sh, tid)->total[0][rank] = all;
+    }
+    cluster.sync();
+    long long used = 0, before = 0;
+    for (int r = 0; r < kPageCluster; ++r) {
+        if (r == rank)
+            before = used;
+        used += sh->total[0][r];
+    }
+    int movers = 0;
+    for (int t0 = b0; t0 < b1; t0 += kPageThreads) {
+        const int b = t0 + tid;
+        const int c = b < b1 ? p.refs[b] : 0;
+        const bool is = c > 0;
+        const long long below = before + block_scan(is, sh, &all);  // used blocks below b
+        before += all;
+        if (b < b1) {
+            p.new_refs[b] = c;
+            p.remap[b] = b;
+            if (is && b >= used) {
+                const long long k = used - 1 - below;
+                if (k <= p.max_moves)  // (one more: the highest that stays)
+                    p.src_list[k] = b;
+                ++movers;
+            } else if (!is && b < used && b - below < p.max_moves) {
+                p.dst_list[b - below] = b;
+            }
+        }
+    }
+    block_scan(movers, sh, &all);
+    if (tid < kPageCluster)
+        cluster.map_shared_rank(sh, tid)->total[1][rank] = all;
+    cluster.sync();
+    long long total = 0;
+    for (int r = 0; r < kPageCluster; ++r)
+        total += sh->total[1][r];
+    const int moves = total < p.max_moves ? static_cast<int>(total) : p.max_moves;
+    for (int k = gtid; k < p.max_moves; k += gthreads) {
+        int src = -1, dst = -1;
+        if (k < moves) {
+            src = __ldcg(p.src_list + k);
+            dst = __ldcg(p.dst_list + k);
+            p.remap[src] = dst;
+            p.new_refs[dst] = __ldcg(p.new_refs + src);
+            p.new_refs[src] = 0;
+        }
+        p.pairs[2 * static_cast<long long>(k)] = src;
+        p.pairs[2 * static_cast<long long>(k) + 1] = dst;
+    }
+    cluster.sync();
+    constexpr int kSegment = 1024;
+    const int segments = (p.max_blocks + kSegment - 1) / kSegment;
+    const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
+        const int i = static_cast<int>(u / segments), j0 = static_cast<int>(u % segments) * kSegment;
+        const int j1 = p.max_blocks - j0 < kSegment ? p.max_blocks : j0 + kSegment;
+        int len = p.lens[i];
+        const bool bad_len = len < 0 || len > most;
+        len = len < 0 ? 0 : (len > most ? static_cast<int>(most) : len);
+        const int n = blocks_of(len, p.block_size);
+        const int32_t *from = p.tables + static_cast<long long>(i) * p.max_blocks;
+        int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
+        bool bad = false;
+#pragma unroll 4
+        for (int j = j0 + lane; j < j1; j += 32) {
+            int b = -1;
+            if (j < n) {
+                b = from[j];
+                if (b >= 0 && b < p.num_blocks)
+                    b = __ldcg(p.remap + b);
+                else
+                    bad = true;
+            }
+            to[j] = b;
+        }
+        if (p.err && (bad || bad_len))
+            atomicOr(p.err, (bad ? PA_DEVERR_BAD_BLOCK : 0u) | (bad_len ? PA_DEVERR_BAD_LEN : 0u));
+    }
+    if (gtid == 0) {
+        p.status[0] = moves;
+        p.status[1] = static_cast<int>(used);
+        p.status[2] = total > moves ? __ldcg(p.src_list + moves) + 1 : static_cast<int>(used);
+        p.status[3] = static_cast<int>(total);
+    }
+}
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyFlight = 4;
+
+template <typename V>
+__device__ inline void copy_block(V *dst, const V *src, long long n) {
+    const long long step = static_cast<long long>(gridDim.x) * kCopyThreads * kCopyFlight;
+    for (long long base = static_cast<long long>(blockIdx.x) * kCopyThreads * kCopyFlight + threadIdx.x; base < n;
+         base += step) {
+        V r[kCopyFlight];
+#pragma unroll
+        for (int u = 0; u < kCopyFlight; ++u)
+            if (base + u * kCopyThreads < n)
+                r[u] = __ldcs(src + base + u * kCopyThreads);
+#pragma unroll
+        for (int u = 0; u < kCopyFlight; ++u)
+            if (base + u * kCopyThreads < n)
+                __stcs(dst + base + u * kCopyThreads, r[u]);
+    }
+}
+
+// grid.x: parts of a block, grid.y: pairs (strided), grid.z: pools.
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPagesParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    char *pool = p.pool[blockIdx.z];
+    const long long bytes = p.block_bytes[blockIdx.z];
+    const bool wide = bytes % 16 == 0 && (reinterpret_cast<uintptr_t>(pool) & 15u) == 0;
+    for (int i = blockIdx.y; i < p.num_pairs; i += gridDim.y) {
+        const long long src = p.pairs[2 * static_cast<long long>(i)], dst = p.pairs[2 * static_cast<long long>(i) + 1];
+        if (src < 0)
+            continue;  // padding
+        if (src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+            if (p.err && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+                atomicOr(p.err, PA_DEVERR_BAD_PAIR);
+            continue;
+        }
+        if (wide)
+            copy_block(reinterpret_cast<uint4 *>(pool + dst * bytes), reinterpret_cast<const uint4 *>(pool + src * bytes),
+                       bytes / 16);
+        else
+            copy_block(reinterpret_cast<uint32_t *>(pool + dst * bytes),
+                       reinterpret_cast<const uint32_t *>(pool + src * bytes), bytes / 4);
+    }
+}
+
+cudaError_t launch_cluster(const void *fn, void **args, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kPageCluster);
+    cfg.blockDim = dim3(kPageThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kPageCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_update(PagesUpdateParams p, cudaStream_t stream) {
+    void *args[] = {&p};
+    return launch_cluster(reinterpret_cast<const void *>(&pages_update_kernel), args, stream);
+}
+
+cudaError_t launch_pages_compact(PagesCompactParams p, cudaStream_t stream) {
+    void *args[] = {&p};
+    return launch_cluster(reinterpret_cast<const void *>(&pages_compact_kernel), args, stream);
+}
+
+cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream) {
+    long long most = 0;
+    for (int i = 0; i < p.num_pools; ++i)
+        most = p.block_bytes[i] > most ? p.block_bytes[i] : most;
+    const long long per_cta = 16LL * kCopyThreads * kCopyFlight;
+    long long gx = (most + per_cta - 1) / per_cta;
+    const long long cap = static_cast<long long>(num_sms) * 8;
+    if (gx > cap)
+        gx = cap;
+    long long gy = cap / (gx * p.num_pools);
+    gy = gy < 1 ? 1 : (gy > p.num_pairs ? p.num_pairs : gy);
+    if (gy > 65535)
+        gy = 65535;
+    void *args[] = {&p};
+    return launch_dependent(reinterpret_cast<const void *>(&copy_pages_kernel),
+                            dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy), p.num_pools),
+                            dim3(kCopyThreads), args, 0, stream);
+}
+
+}  // namespace pa

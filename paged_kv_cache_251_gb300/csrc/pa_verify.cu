@@ -1,0 +1,507 @@
+// Verification of drafted tokens: which of a sequence's drafted tokens are kept,
+// and the token after them, from given random numbers, so that what is kept is
+// distributed as if the target had drawn every token itself.
+//
+// At a node of the tree with target p and draft q, after r of its children were
+// rejected, the next token's weights are w_r = max(0, p - a_r q) over S_r = sum w_r,
+// with a_0 = 0, S_0 = 1: rejecting a child drawn from q leaves max(0, w_r / S_r - q),
+// which is max(0, p - (a_r + S_r) q) / S_r, so a_(r+1) = a_r + S_r.  A child x is
+// accepted when u S_r q(x) < w_r(x).  Without q (the drafted tokens were chosen, not
+// drawn) w_r is p without the rejected tokens, and x is accepted when u S_r < p(x).
+// The walk goes over the drafted tokens in order (parents come before children).
+// Where it ends, the next token is the first whose running sum of w exceeds u S.
+//
+// A drawn token must not hang on how a sum was rounded, so weights are summed to
+// about 46 bits: p - q as fp32 value and error, lanes' sums as pairs of floats (their
+// roundings kept), everything past a lane in 64-bit fixed point (2^-54, in smaller
+// units again where that comes to less than 2^-20).  fp64 arithmetic would be the
+// limit here (its rate is 1/64 of fp32's).
+//
+// A sequence is a cluster of CTAs, each taking a share of the vocabulary, a warp a
+// contiguous slice of it.  The first CTA gathers what the walk needs (every drafted
+// token's p, q and u) and hands it to the others, so all walk alike on the same
+// bits.  Only a rejection with q, and the end, read a row; the CTA and the warp
+// that hold the running sum read their slice (a few hundred entries) once more to
+// find the token.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "pa_device.cuh"
+#include "pa_host.h"
+#include "pa_internal.h"
+#include "pa_verify.h"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+
+namespace {
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyMaxCluster = 8;
+constexpr double kFixedOne = 18014398509481984.0;  // 2^54
+// Sums below 2^-20 are taken again in smaller units.
+constexpr unsigned long long kSmallSum = 1ull << 34;
+
+struct VerifyShared {
+    // of every drafted token; tok -1: not a token
+    float p[kVerifyMaxDraft], q[kVerifyMaxDraft], u[kVerifyMaxDraft + 1];
+    int parent[kVerifyMaxDraft], tok[kVerifyMaxDraft];
+    int drafts;
+    unsigned long long total[2][kVerifyMaxCluster];  // of every CTA; two passes' (a slow CTA may still read the last)
+    unsigned long long warp_sum[kVerifyWarps];
+    // the walk
+    double a, s;
+    int node, next, n, ngone, need;
+    bool summed;  // total[] holds the sum of the present weights
+    int path[kVerifyMaxDraft], gone[kVerifyMaxDraft];
+};
+
+enum { kWalkDone = 0, kWalkSum = 1, kWalkEnd = 2 };
+
+// The walk up to a sum that it needs (kWalkSum: of a rejection's weights, kWalkEnd:
+// of the weights it ends with) or to its end (kWalkDone).
+template <bool HasQ> __device__ int walk(VerifyShared *sh) {
+    int node = sh->node, n = sh->n;
+    double a = sh->a, s = sh->s;
+    int ngone = sh->ngone;
+    bool summed = sh->summed;
+    int need = -1;
+    int i = sh->next;
+    for (; i < sh->drafts; ++i) {
+        if (sh->parent[i] != node || sh->tok[i] < 0)
+            continue;
+        double p = sh->p[i];
+        const double u = sh->u[i];
+        bool ok;
+        if (HasQ) {
+            const double q = sh->q[i];
+            const double w = __dsub_rn(p, __dmul_rn(a, q));
+            ok = __dmul_rn(__dmul_rn(u, s), q) < (w > 0 ? w : 0.0);
+        } else {
+            bool again = false;
+            for (int g = 0; g < ngone; ++g)
+                again |= sh->gone[g] == sh->tok[i];
+            ok = !again && __dmul_rn(u, s) < p;
+            if (!ok && !again) {
+                sh->gone[ngone++] = sh->tok[i];
+                s -= p > 0 ? p : 0.0;
+                summed = false;
+            }
+        }
+        if (ok) {
+            sh->path[n++] = i;
+            node = i;
+            a = 0;
+            s = 1;
+            ngone = 0;
+            summed = false;
+        } else if (HasQ) {
+            a += s;
+            summed = false;
+            need = kWalkSum;
+            ++i;
+            break;
+        }
+    }
+    if (need < 0)
+        need = summed ? kWalkDone : kWalkEnd;
+    sh->next = i;
+    sh->node = node;
+    sh->n = n;
+    sh->a = a;
+    sh->s = s;
+    sh->ngone = ngone;
+    sh->summed = summed;
+    return need;
+}
+
+// max(0, p - a q) as value and error; a in two floats.  An entry whose p or q is
+// NaN has no weight.
+struct Weight {
+    float d, e;
+};
+template <bool Unit> __device__ inline Weight weight(float p, float q, float ah, float al) {
+    if (Unit) {  // a = 1
+        const float d = __fsub_rn(p, q);
+        const float e = __fsub_rn(__fsub_rn(p, d), q);
+        return d > 0 ? Weight{d, e} : Weight{0.f, 0.f};
+    }
+    const float h = __fmul_rn(ah, q);
+    const float l = __fmaf_rn(al, q, __fmaf_rn(ah, q, -h));
+    const float d = __fsub_rn(p, h);
+    const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), h), l);
+    return __fadd_rn(d, e) > 0 ? Weight{d, e} : Weight{0.f, 0.f};
+}
+
+__device__ inline float to_f(float x) { return x; }
+__device__ inline float to_f(__half x) { return __half2float(x); }
+__device__ inline float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// E consecutive entries of a row from `at` (a multiple of E below `end`), zeros
+// from `end` on.
+template <typename T, int E> struct Entries {
+    float f[E];
+    __device__ inline void load(const T *row, int at, int end) {
+        if constexpr (E == 1) {
+            f[0] = at < end ? to_f(row[at]) : 0.f;
+        } else {
+            uint4 r = make_uint4(0, 0, 0, 0);
+            if (at < end)  // (rows of this form are whole vectors)
+                r = *reinterpret_cast<const uint4 *>(row + at);
+            Elt<T>::unpack(r, f);
+        }
+    }
+};
+
+__device__ inline unsigned long long warp_add(unsigned long long x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+enum { kRowP = 0, kRowUnit = 1, kRowScaled = 2 };  // p; p - q; p - a q
+
+template <typename T, int E, int Mode>
+__device__ inline Weight entry(const float *p, const float *q, int k, float ah, float al) {
+    if (Mode == kRowP)
+        return p[k] > 0 ? Weight{p[k], 0.f} : Weight{0.f, 0.f};
+    return weight<Mode == kRowUnit>(p[k], q[k], ah, al);
+}
+
+// Entries of gone[] in a warp's next `n` vectors lose their weight.
+template <typename T, int E>
+__device__ inline void leave_out(Entries<T, E> *p, int n, int base, int lane, const int *gone, int ngone) {
+    for (int g = 0; g < ngone; ++g) {
+        const int x = gone[g] - base;
+        if (x < 0 || x >= n * 32 * E)  // the same for the whole warp
+            continue;
+#pragma unroll
+        for (int j = 0; j < n; ++j)
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (x == (j * 32 + lane) * E + k)
+                    p[j].f[k] = 0.f;
+    }
+}
+
+// Sum of the weights of [lo, hi) times `unit` (every lane gets it), entries in
+// gone[] left out (Mode kRowP only).
+template <typename T, int E, int Mode>
+__device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, int hi, float ah, float al,
+                                        const int *gone, int ngone, double unit, int lane) {
+    constexpr int kFlight = E == 1 ? 8 : 16 / E;  // loads in flight of each row
+    float h = 0.f, l = 0.f;
+    for (int base = lo; base < hi; base += 32 * E * kFlight) {
+        Entries<T, E> p[kFlight], q[kFlight];
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j) {
+            const int at = base + (j * 32 + lane) * E;
+            p[j].load(prow, at, hi);
+            if (Mode != kRowP)
+                q[j].load(qrow, at, hi);
+        }
+        if (Mode == kRowP)
+            leave_out<T, E>(p, kFlight, base, lane, gone, ngone);
+#pragma unroll
+        for (int j = 0; j < kFlight; ++j)
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const Weight w = entry<T, E, Mode>(p[j].f, q[j].f, k, ah, al);
+                const float s = __fadd_rn(h, w.d);
+                const float b = __fsub_rn(s, h);
+                const float err = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(w.d, b));
+                h = s;
+                l = __fadd_rn(l, Mode == kRowP ? err : __fadd_rn(err, w.e));
+            }
+    }
+    const double x = (static_cast<double>(h) + static_cast<double>(l)) * unit;
+    return warp_add(static_cast<unsigned long long>(__double2ll_rn(x)));
+}
+
+// The first entry of [lo, hi) whose running sum exceeds t, entries in gone[] left
+// out; the last with any weight where rounding leaves none (-1: no weight at all).
+template <typename T, int E, int Mode>
+__device__ int slice_find(const T *prow, const T *qrow, int lo, int hi, float ah, float al, const int *gone, int ngone,
+                          unsigned long long t, double unit, int lane) {
+    unsigned long long before = 0;
+    int last = -1;
+    for (int base = lo; base < hi; base += 32 * E) {
+        const int at = base + lane * E;
+        Entries<T, E> p, q;
+        p.load(prow, at, hi);
+        if (Mode != kRowP)
+            q.load(qrow, at, hi);
+        if (Mode == kRowP)
+            leave_out<T, E>(&p, 1, base, lane, gone, ngone);
+        unsigned long long w[E], sum = 0;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const Weight we = entry<T, E, Mode>(p.f, q.f, k, ah, al);
+            w[k] = __double2ull_rd((static_cast<double>(we.d) + static_cast<double>(we.e)) * unit);
+            if (we.d > 0)
+                last = at + k;
+            sum += w[k];
+        }
+        unsigned long long incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, before + incl > t);
+        if (hit) {
+            const int who = __ffs(hit) - 1;
+            int x = -1;
+            if (lane == who) {
+                unsigned long long run = before + incl - sum;
+#pragma unroll
+                for (int k = 0; k < E; ++k) {
+                    run += w[k];
+                    if (x < 0 && run > t)
+                        x = at + k;
+                }
+            }
+            return __shfl_sync(0xffffffffu, x, who);
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return __reduce_max_sync(0xffffffffu, last);
+}
+
+template <typename T, int E, bool HasQ>
+__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams p) {
+    __shared__ VerifyShared shared;
+    VerifyShared *sh = &shared;
+    pdl_launch_dependents();
+    pdl_wait();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = p.cluster, rank = ranks > 1 ? static_cast<int>(cluster.block_rank()) : 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const long long s = blockIdx.x / ranks;
+    const int T1 = p.num_draft, V = p.vocab;
+    const T *target = static_cast<const T *>(p.target) + s * (T1 + 1) * p.target_stride;
+    const T *draft = static_cast<const T *>(p.draft) + (HasQ ? s * T1 * p.draft_stride : 0);
+
+    // what the walk needs, gathered once for all CTAs (every one walks on the same bits)
+    if (ranks > 1)
+        cluster.sync();  // every CTA of the cluster has started
+    if (rank == 0) {
+        int drafts = p.draft_lens ? p.draft_lens[s] : T1;
+        uint32_t bad = 0;
+        if (drafts < 0 || drafts > T1) {
+            bad = PA_DEVERR_BAD_LEN;
+            drafts = drafts < 0 ? 0 : T1;
+        }
+        for (int i = tid; i <= T1; i += kVerifyThreads) {
+            const float u = p.uniforms[s * (T1 + 1) + i];
+            float pv = 0.f, qv = 0.f;
+            int parent = -1, tok = -1;
+            if (i < T1) {
+                tok = p.draft_tokens[s * T1 + i];
+                parent = p.parents ? p.parents[s * T1 + i] : i - 1;
+                if (parent < 0)
+                    parent = -1;
+                if (i >= drafts) {
+                    tok = -1;
+                } else if (tok < 0 || tok >= V || parent >= i) {
+                    bad |= PA_DEVERR_BAD_INDEX;
+                    tok = -1;
+                } else {
+                    pv = to_f(target[static_cast<long long>(parent + 1) * p.target_stride + tok]);
+                    if (HasQ)
+                        qv = to_f(draft[static_cast<long long>(parent + 1) * p.draft_stride + tok]);
+                }
+            }
+            for (int r = 0; r < ranks; ++r) {
+                VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, r) : sh;
+                to->u[i] = u;
+                if (i < T1) {
+                    to->p[i] = pv;
+                    to->q[i] = qv;
+                    to->parent[i] = parent;
+                    to->tok[i] = tok;
+                } else {
+                    to->drafts = drafts;
+                }
+            }
+        }
+        if (bad && p.err)
+            atomicOr(p.err, bad);
+    }
+    if (tid == 0) {
+        sh->a = 0;
+        sh->s = 1;
+        sh->node = -1;
+        sh->next = sh->n = sh->ngone = 0;
+        sh->summed = false;
+    }
+    if (ranks > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+
+    const int lo = static_cast<int>(min(static_cast<long long>(rank * kVerifyWarps + warp) * p.slice,
+                                        static_cast<long long>(V)));
+    const int hi = V - lo < p.slice ? V : lo + p.slice;
+    const T *prow, *qrow;
+    float ah, al;
+    int mode, parity = 0;
+    unsigned long long total = 0;
+    double unit = kFixedOne;  // 2^54, times a power of two where the sum is small
+    for (bool again = false, smaller = false;;) {
+        if (tid == 0 && !again && !smaller)
+            sh->need = walk<HasQ>(sh);
+        __syncthreads();
+        const int need = sh->need;
+        if (need != kWalkDone) {
+            if (!smaller)
+                unit = kFixedOne;
+            const int node = sh->node;
+            prow = target + static_cast<long long>(node + 1) * p.target_stride;
+            const double a = sh->a;
+            mode = !HasQ || a == 0 ? kRowP : (a == 1 ? kRowUnit : kRowScaled);
+            qrow = mode == kRowP ? nullptr : draft + static_cast<long long>(node + 1) * p.draft_stride;
+            ah = static_cast<float>(a);
+            al = static_cast<float>(a - static_cast<double>(ah));
+            unsigned long long sum;
+            if (mode == kRowP)
+                sum = slice_sum<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+            else if (mode == kRowUnit)
+                sum = slice_sum<T, E, kRowUnit>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+            else
+                sum = slice_sum<T, E, kRowScaled>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+            if (lane == 0)
+                sh->warp_sum[warp] = sum;
+            __syncthreads();
+            if (tid < ranks) {
+                unsigned long long mine = 0;
+                for (int w = 0; w < kVerifyWarps; ++w)
+                    mine += sh->warp_sum[w];
+                VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, tid) : sh;
+                to->total[parity][rank] = mine;
+            }
+            if (ranks > 1)
+                cluster.sync();
+            else
+                __syncthreads();
+            total = 0;
+            for (int r = 0; r < ranks; ++r)
+                total += sh->total[parity][r];
+            parity ^= 1;
+            smaller = total < kSmallSum && unit < kFixedOne * 1e45;  // (fp32 ends at 1.4e-45)
+            if (smaller) {
+                unit *= total ? 1048576.0 : 1125899906842624.0;  // 2^20, 2^50
+                continue;
+            }
+            if (tid == 0) {
+                sh->s = static_cast<double>(total) / unit;
+                sh->summed = true;
+            }
+        }
+        again = false;
+        if (need == kWalkSum)
+            continue;
+        // nothing is left of p (p and q alike, up to rounding, or every token rejected): p itself
+        if (total == 0 && (sh->a != 0 || sh->ngone != 0)) {
+            __syncthreads();
+            if (tid == 0) {
+                sh->a = 0;
+                sh->ngone = 0;
+                sh->need = kWalkEnd;
+            }
+            again = true;
+            continue;
+        }
+        break;
+    }
+
+    const int n = sh->n;
+    if (rank == 0) {
+        for (int i = tid; i <= T1; i += kVerifyThreads) {
+            const int at = i < n ? sh->path[i] : -1;
+            if (i < T1)
+                p.accepted[s * T1 + i] = at;
+            if (i != n || total == 0)
+                p.tokens[s * (T1 + 1) + i] = i < n ? sh->tok[at] : -1;
+        }
+        if (tid == 0)
+            p.accept_lens[s] = n;
+    }
+    if (total == 0)
+        return;
+    const double x = static_cast<double>(sh->u[T1]) * static_cast<double>(total);
+    unsigned long long t = x > 0 ? static_cast<unsigned long long>(__double2ull_rd(x)) : 0ull;
+    if (t >= total)
+        t = total - 1;
+    int owner = 0;
+    parity ^= 1;
+    // (bounded: entries that are no probabilities may have made the sums wrap)
+    while (owner < ranks - 1 && t >= sh->total[parity][owner])
+        t -= sh->total[parity][owner++];
+    if (rank != owner)
+        return;
+    int w = 0;
+    while (w < kVerifyWarps - 1 && t >= sh->warp_sum[w])
+        t -= sh->warp_sum[w++];
+    if (warp != w)
+        return;
+    int found;
+    if (mode == kRowP)
+        found = slice_find<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+    else if (mode == kRowUnit)
+        found = slice_find<T, E, kRowUnit>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+    else
+        found = slice_find<T, E, kRowScaled>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+    if (lane == 0)
+        p.tokens[s * (T1 + 1) + n] = found;
+}
+
+template <typename T> const void *verify_fn(bool vec, bool has_q) {
+    constexpr int E = 16 / sizeof(T);
+    if (vec)
+        return has_q ? reinterpret_cast<const void *>(&verify_kernel<T, E, true>)
+                     : reinterpret_cast<const void *>(&verify_kernel<T, E, false>);
+    return has_q ? reinterpret_cast<const void *>(&verify_kernel<T, 1, true>)
+                 : reinterpret_cast<const void *>(&verify_kernel<T, 1, false>);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(VerifyParams p, int dtype, int num_sms, cudaStream_t stream) {
+    const int e = 16 / elt_bytes(dtype);
+    const bool vec = p.vocab % e == 0 && p.target_stride % e == 0 && p.draft_stride % e == 0 && aligned16(p.target) &&
+                     aligned16(p.draft);
+    const void *fn = dtype == PA_F32   ? verify_fn<float>(vec, p.draft != nullptr)
+                     : dtype == PA_F16 ? verify_fn<__half>(vec, p.draft != nullptr)
+                                       : verify_fn<__nv_bfloat16>(vec, p.draft != nullptr);
+    // enough CTAs for two an SM, while each has entries for its threads
+    int cluster = 1;
+    while (cluster < kVerifyMaxCluster && static_cast<long long>(p.num_seqs) * cluster < 2LL * num_sms &&
+           p.vocab / (cluster * 2) >= 2 * kVerifyThreads)
+        cluster *= 2;
+    p.cluster = cluster;
+    const int warps = cluster * kVerifyWarps;
+    p.slice = ((p.vocab + warps - 1) / warps + 31) / 32 * 32;
+    // (the grid's first dimension holds 2^31 - 1 CTAs: the caller bounds num_seqs)
+    void *args[] = {&p};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * cluster);
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace pa

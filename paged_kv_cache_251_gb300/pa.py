@@ -18,7 +18,7 @@ LIB_PATH = Path(__file__).resolve().parent / "_lib" / "libpa.so"
 PA_OK, PA_ERR_INVALID_ARGUMENT, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_CUDA = range(5)
 PA_F32, PA_F16, PA_BF16, PA_I8, PA_E4M3 = 0, 1, 2, 3, 4
 DEVERR_BAD_BLOCK, DEVERR_BAD_SLOT, DEVERR_BAD_PAIR, DEVERR_TIMEOUT, DEVERR_BAD_LEN, DEVERR_BAD_LAUNCH = 1, 2, 4, 8, 16, 32
-DEVERR_BAD_INDEX = 64
+DEVERR_BAD_INDEX, DEVERR_BAD_COUNT = 64, 128
 
 DTYPE_CODE = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 # rotary frequency scalings of pa_rope_frequencies
@@ -87,6 +87,24 @@ def _load():
     lib.pa_evict_select.restype = I
     lib.pa_compact_kv.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, P, P]
     lib.pa_compact_kv.restype = I
+    lib.pa_verify_drafts.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, LL, LL, I, P, P]
+    lib.pa_verify_drafts.restype = I
+    lib.pa_append_kv_block_quant.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_append_kv_block_quant.restype = I
+    lib.pa_append_kv_block_quant_workspace_size.argtypes = [I, I, I]
+    lib.pa_append_kv_block_quant_workspace_size.restype = SZ
+    lib.pa_decode_block_quant.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, F, I, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_decode_block_quant.restype = I
+    lib.pa_decode_block_quant_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.pa_decode_block_quant_workspace_size.restype = SZ
+    lib.pa_pages_update.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_pages_update.restype = I
+    lib.pa_pages_compact.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, P, SZ, P, P]
+    lib.pa_pages_compact.restype = I
+    lib.pa_pages_workspace_size.argtypes = [I, I]
+    lib.pa_pages_workspace_size.restype = SZ
+    lib.pa_copy_pages.argtypes = [P, I, P, P, I, I, P, P]
+    lib.pa_copy_pages.restype = I
     lib.pa_status_string.argtypes = [I]
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_last_error_detail.argtypes = []
@@ -740,6 +758,217 @@ def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tens
           keep_lens.data_ptr(), _addr(base_lens), block_tables.data_ptr(), _addr(dst_block_tables), n, keep.shape[1],
           keep.shape[2], hkv, d, bs, block_tables.shape[1],
           0 if dst_block_tables is None else dst_block_tables.shape[1], nb, DTYPE_CODE[k_cache.dtype],
+          _addr(err_word))
+
+
+# ---------------------------------------------------------------------------
+# Verification of drafted tokens, block-scaled 8-bit caches, page tables on the
+# device
+
+
+def _prob_rows(t: torch.Tensor, name: str, n: int, rows: int) -> int:
+    """The row stride, in elements, of [n, rows, vocab] probabilities whose rows are
+    a fixed distance apart (a padded vocabulary cut to size, for instance)."""
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != rows:
+        raise ValueError(f"{name} must be [{n}, {rows}, vocab]")
+    a, b, c = t.stride()
+    v = t.shape[2]
+    if rows == 1:
+        b = a if n > 1 else v
+    if t.numel() and ((c != 1 and v > 1) or (n > 1 and a != rows * b) or b < v):
+        raise ValueError(f"{name}: entries must be dense and rows a fixed distance apart")
+    return b
+
+
+def pa_verify_drafts(accept_lens: torch.Tensor, accepted: torch.Tensor, tokens: torch.Tensor,
+                     target_probs: torch.Tensor, draft_tokens: torch.Tensor, uniforms: torch.Tensor,
+                     draft_probs: torch.Tensor | None = None, draft_lens: torch.Tensor | None = None,
+                     parents: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Which drafted tokens [N, T] are kept, and the token after them, given the
+    target's probabilities [N, T + 1, V] (row i + 1: after drafted token i), the
+    draft's [N, T, V] (row i: behind drafted token i - 1; None: the drafted tokens
+    were chosen, not drawn) and random numbers [N, T + 1].  accepted [N, T] is a
+    keep list of pa_compact_kv, tokens [N, T + 1] the accepted tokens and the
+    next one, -1 behind them.  parents None: a chain (see include/pa.h)."""
+    dev = _dense(accept_lens, accepted, tokens, draft_tokens, uniforms, draft_lens, parents, err_word)
+    if target_probs.get_device() != dev or (draft_probs is not None and draft_probs.get_device() != dev):
+        raise ValueError("every tensor must be a CUDA tensor on one device")
+    if draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be [N, T]")
+    n, t = draft_tokens.shape
+    target_stride = _prob_rows(target_probs, "target_probs", n, t + 1)
+    v = target_probs.shape[2]
+    draft_stride = 0
+    if draft_probs is not None:
+        draft_stride = _prob_rows(draft_probs, "draft_probs", n, t)
+        if draft_probs.shape[2] != v or draft_probs.dtype is not target_probs.dtype:
+            raise ValueError("target_probs and draft_probs must share vocabulary and dtype")
+    _shapes(accept_lens, (n,), "accept_lens", accepted, (n, t), "accepted", tokens, (n, t + 1), "tokens", uniforms,
+            (n, t + 1), "uniforms", draft_lens, (n,), "draft_lens", parents, (n, t), "parents")
+    _int32(accept_lens, "accept_lens", accepted, "accepted", tokens, "tokens", draft_tokens, "draft_tokens", draft_lens,
+           "draft_lens", parents, "parents")
+    if uniforms.dtype is not torch.float32 or target_probs.dtype not in DTYPE_CODE:
+        raise TypeError("uniforms must be float32, the probabilities float32, float16 or bfloat16")
+    _call(_lib.pa_verify_drafts, dev, stream, accept_lens.data_ptr(), accepted.data_ptr(), tokens.data_ptr(),
+          target_probs.data_ptr(), _addr(draft_probs), draft_tokens.data_ptr(), _addr(draft_lens), _addr(parents),
+          uniforms.data_ptr(), n, t, v, target_stride, draft_stride, DTYPE_CODE[target_probs.dtype], _addr(err_word))
+    return tokens
+
+
+def _block_quant_pool(k_cache, v_cache, k_scales, v_scales) -> tuple:
+    """(blocks, kv heads, block size, head_dim, code) of a block-scaled cache."""
+    if k_cache.dim() != 4 or k_cache.dtype not in CODE_DTYPE or v_cache.dtype is not k_cache.dtype:
+        raise TypeError("the caches must be int8 / float8_e4m3fn codes [blocks, H_kv, block_size, head_dim]")
+    nb, hkv, bs, d = k_cache.shape
+    _shapes(v_cache, k_cache.shape, "v_cache", k_scales, (nb, hkv), "k_scales", v_scales, (nb, hkv), "v_scales")
+    if k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32:
+        raise TypeError("k_scales and v_scales must be float32")
+    return nb, hkv, bs, d, CODE_DTYPE[k_cache.dtype]
+
+
+def append_block_quant_workspace_for(slot_mapping: torch.Tensor, k_cache: torch.Tensor) -> torch.Tensor | None:
+    """A workspace tensor for pa_append_kv_block_quant (None if 0 bytes)."""
+    return _ws(int(_lib.pa_append_kv_block_quant_workspace_size(slot_mapping.numel(), k_cache.shape[2],
+                                                                k_cache.shape[0])), k_cache.device)
+
+
+def pa_append_kv_block_quant(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                             v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                             workspace: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
+                             stream=None) -> None:
+    """Store token i's K/V rows (fp32/fp16/bf16) as 8-bit codes at slot_mapping[i];
+    a block's scale for each kv head ([blocks, H_kv]) grows with its rows, and
+    what it held is coded again (see include/pa.h)."""
+    dev = _dense(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales, workspace, err_word)
+    nb, hkv, bs, d, code = _block_quant_pool(k_cache, v_cache, k_scales, v_scales)
+    n = slot_mapping.numel()
+    _shapes(k, (n, hkv, d), "k", v, (n, hkv, d), "v")
+    if slot_mapping.dtype is not torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if k.dtype is not v.dtype or k.dtype not in DTYPE_CODE:
+        raise TypeError("k and v must share one of float32, float16, bfloat16")
+    if workspace is None:
+        workspace = _own_workspace(stream, append_block_quant_workspace_for, slot_mapping, k_cache)
+    _call(_lib.pa_append_kv_block_quant, dev, stream, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, hkv, d, bs, nb,
+          DTYPE_CODE[k.dtype], code, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+
+
+def block_quant_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int) -> torch.Tensor | None:
+    """A workspace tensor for pa_decode_block_quant (None if 0 bytes)."""
+    n, h, d = q.shape
+    return _ws(int(_lib.pa_decode_block_quant_workspace_size(n, h, k_cache.shape[1], d, k_cache.shape[2],
+                                                             max_blocks_per_seq)), q.device)
+
+
+def pa_decode_block_quant(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                          context_lens: torch.Tensor, scale: float | None = None, window: int = 0,
+                          workspace: torch.Tensor | None = None, err_word: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """pa_decode over 8-bit codes [blocks, H_kv, block_size, d] with one scale for
+    each block and kv head (see include/pa.h)."""
+    dev = _dense(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace, err_word)
+    n, h, d = q.shape
+    nb, hkv, bs, d2, code = _block_quant_pool(k_cache, v_cache, k_scales, v_scales)
+    _shapes(out, q.shape, "out", k_cache, (nb, hkv, bs, d), "k_cache", context_lens, (n,), "context_lens")
+    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+        raise ValueError("block_tables must be [N, max_blocks_per_seq]")
+    _int32(block_tables, "block_tables", context_lens, "context_lens")
+    if q.dtype not in DTYPE_CODE or out.dtype not in DTYPE_CODE:
+        raise TypeError("q and out must be float32, float16 or bfloat16")
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        workspace = _own_workspace(stream, block_quant_workspace_for, q, k_cache, block_tables.shape[1])
+    _call(_lib.pa_decode_block_quant, dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+          context_lens.data_ptr(), n, h, hkv, d, bs, float(scale), int(window), DTYPE_CODE[q.dtype], code,
+          DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+    return out
+
+
+def pages_workspace_for(tables: torch.Tensor, ref_counts: torch.Tensor, num_rows: int = 0) -> torch.Tensor:
+    """A workspace tensor for pa_pages_update (to num_rows rows, if more than
+    tables has) and pa_pages_compact."""
+    return _ws(int(_lib.pa_pages_workspace_size(max(num_rows, tables.shape[0]), ref_counts.numel())), tables.device)
+
+
+def _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens) -> None:
+    if tables.dim() != 2 or new_tables.dim() != 2 or new_tables.shape[1] != tables.shape[1]:
+        raise ValueError("tables and new_tables must be [rows, max_blocks_per_seq]")
+    if ref_counts.dim() != 1 or pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("ref_counts must be [blocks] and pairs [n, 2]")
+    _shapes(new_ref_counts, ref_counts.shape, "new_ref_counts", status, (4,), "status", lens, (tables.shape[0],), "lens")
+    _int32(new_tables, "new_tables", new_ref_counts, "new_ref_counts", status, "status", tables, "tables", ref_counts,
+           "ref_counts", lens, "lens")
+    if pairs.dtype is not torch.int64:
+        raise TypeError("pairs must be int64")
+
+
+def pa_pages_update(new_tables: torch.Tensor, new_ref_counts: torch.Tensor, pairs: torch.Tensor,
+                    status: torch.Tensor, tables: torch.Tensor, ref_counts: torch.Tensor, lens: torch.Tensor,
+                    keep_lens: torch.Tensor, grow_lens: torch.Tensor, block_size: int,
+                    parents: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                    err_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The next step's block tables: row i keeps the first keep_lens[i] tokens of
+    row parents[i] (None: i; negative: nothing) and gets blocks for grow_lens[i];
+    pairs [rows, 2] are the copies of shared last blocks, for pa_copy_pages.
+    status[0] is 0, and nothing else changed, if the free blocks do not suffice
+    (see include/pa.h)."""
+    dev = _dense(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens, keep_lens, grow_lens, parents,
+                 workspace, err_word)
+    _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
+    n = new_tables.shape[0]
+    _shapes(pairs, (n, 2), "pairs", keep_lens, (n,), "keep_lens", grow_lens, (n,), "grow_lens", parents, (n,), "parents")
+    _int32(keep_lens, "keep_lens", grow_lens, "grow_lens", parents, "parents")
+    if workspace is None:
+        workspace = _own_workspace(stream, pages_workspace_for, tables, ref_counts, n)
+    _call(_lib.pa_pages_update, dev, stream, new_tables.data_ptr(), new_ref_counts.data_ptr(), pairs.data_ptr(),
+          status.data_ptr(), tables.data_ptr(), ref_counts.data_ptr(), lens.data_ptr(), _addr(parents),
+          keep_lens.data_ptr(), grow_lens.data_ptr(), n, tables.shape[0], tables.shape[1], int(block_size),
+          ref_counts.numel(), _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+    return new_tables
+
+
+def pa_pages_compact(new_tables: torch.Tensor, new_ref_counts: torch.Tensor, remap: torch.Tensor,
+                     pairs: torch.Tensor, status: torch.Tensor, tables: torch.Tensor, ref_counts: torch.Tensor,
+                     lens: torch.Tensor, block_size: int, workspace: torch.Tensor | None = None,
+                     err_word: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Move a pool's used blocks to its front, by at most len(pairs) moves:
+    pairs are the copies, for pa_copy_pages, remap every block's place now (see
+    include/pa.h)."""
+    dev = _dense(new_tables, new_ref_counts, remap, pairs, status, tables, ref_counts, lens, workspace, err_word)
+    _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
+    _shapes(new_tables, tables.shape, "new_tables", remap, ref_counts.shape, "remap")
+    _int32(remap, "remap")
+    if workspace is None:
+        workspace = _own_workspace(stream, pages_workspace_for, tables, ref_counts)
+    _call(_lib.pa_pages_compact, dev, stream, new_tables.data_ptr(), new_ref_counts.data_ptr(), remap.data_ptr(),
+          pairs.data_ptr(), status.data_ptr(), tables.data_ptr(), ref_counts.data_ptr(), lens.data_ptr(),
+          tables.shape[0], tables.shape[1], int(block_size), ref_counts.numel(), pairs.shape[0], _addr(workspace),
+          _ws_bytes(workspace), _addr(err_word))
+    return new_tables
+
+
+def pa_copy_pages(src_dst_pairs: torch.Tensor, pools, err_word: torch.Tensor | None = None, stream=None) -> None:
+    """Copy block src onto block dst, in each of up to 8 pools ([blocks, ...],
+    of any types), for every pair with src >= 0."""
+    dev = _dense(src_dst_pairs, err_word, *pools)
+    if src_dst_pairs.dtype is not torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise TypeError("src_dst_pairs must be int64 [n, 2]")
+    k = len(pools)
+    if not k:
+        raise ValueError("no pool")
+    nb = pools[0].shape[0]
+    for t in pools:
+        if t.shape[0] != nb:
+            raise ValueError("the pools must have the same number of blocks")
+    at = (ctypes.c_void_p * k)(*[t.data_ptr() for t in pools])
+    size = (ctypes.c_longlong * k)(*[t.stride(0) * t.element_size() if nb > 1 else t.numel() * t.element_size()
+                                     for t in pools])
+    _call(_lib.pa_copy_pages, dev, stream, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], at, size, k, nb,
           _addr(err_word))
 
 
