@@ -45,9 +45,9 @@ struct DecodeBqParams {
 
 // CTAs of the block-scaled decode: kDecodeBqCtas an SM, of at most kDecodeBqSms SMs
 // (the workspace is sized for them).
-constexpr int kDecodeBqThreads = 256;
+constexpr int kDecodeBqThreads = 128;
 constexpr int kDecodeBqWarps = kDecodeBqThreads / 32;
-constexpr int kDecodeBqCtas = 2;
+constexpr int kDecodeBqCtas = 4;
 constexpr int kDecodeBqSms = 152;
 constexpr int kDecodeBqMaxCtas = kDecodeBqSms * kDecodeBqCtas;
 

@@ -35,11 +35,10 @@ template <int D> __global__ void __launch_bounds__(kJoinThreads) join_bq_kernel(
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    const float base = top == -INFINITY ? 0.f : top;  // (no token: every partial's sum is 0)
     float sum = 0.f;
     for (int i = lane; i < n; i += 32) {
         const float2 x = ml[part_of(i)];
-        sum = fmaf(ex2(x.x - base), x.y, sum);
+        sum = fmaf(ex2(x.x - top), x.y, sum);
     }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
@@ -51,7 +50,7 @@ template <int D> __global__ void __launch_bounds__(kJoinThreads) join_bq_kernel(
 #pragma unroll 4
     for (int i = sub; i < n; i += subs) {
         const long long part = part_of(i);
-        const float f = ex2(ml[part].x - base);
+        const float f = ex2(ml[part].x - top);
 #pragma unroll
         for (int c = 0; c < C; ++c)
             y[c] = fmaf(f, p.part_acc[part * D + 32 * c + lane], y[c]);

@@ -16,18 +16,18 @@
 // with its register operands is the right one here: tcgen05 wants both operands of
 // 16 bits in shared memory, and the codes are 8.
 //
-// Codes become fp16 exactly: INT8 as the low byte of 1024 + 128 + code, less 1152;
-// E4M3 by moving its bits (the value times 2^-8; a NaN code, which no append
-// writes, reads as 480 times its sign).  So no code is infinite or NaN, and rows
-// behind the context cannot spoil a product with a weight of 0.
+// Codes become fp16 exactly.  K, INT8: code + 128 in the low byte of an fp16 is that
+// times 2^-24, and the scores start at -128 times the queries' sum.  V, INT8: the low
+// byte of 1024 + 128 + code, less 1152.  E4M3: converted by the hardware.
 //
 // The eight columns are four heads twice.  For S both halves hold the same
 // queries, scaled to fp16 by a power of two a row (fp16 and bf16 queries: exact to
 // 2^-40 of the row's largest element); fp32 queries as three fp16 terms, the halves'
 // sums added.  For P the halves hold the weight's fp16 value and 2^11 times what that
 // leaves (22 bits together, down to 2^-50 of the largest weight).  Groups of eight
-// heads take two such column sets.  K scales multiply the scores, V scales each tile's
-// product, in fp32: O += v_scale * (V^T P of the block).
+// heads take two such column sets.  K scales multiply the scores.  V scales multiply
+// the weights before they are rounded, as a power of two that O is kept in, moved when a
+// scale exceeds it or lies 2^10 below, and a factor of at most 1.
 //
 // The running maximum is kept as it was until a score exceeds it by 2^8, so a tile
 // normally needs one vote of the warp and no shuffles.
@@ -53,6 +53,8 @@ constexpr int kMinShare = 8;    // iterations of a warp at least
 constexpr float kMaxSlack = 8;  // log2 by which scores may exceed the running maximum
 constexpr float kPTop = 7;      // weights are at most 2^(kMaxSlack + kPTop): within fp16
 constexpr float kPLow = 2048;   // the low part of a weight is kept times this
+constexpr float kLowScale = 1.f / 1024;  // V scales this far below O's unit move it
+constexpr float kNoMax = -1e30f;  // (finite: less it, a score of -inf stays -inf)
 
 struct BqSpan {
     int start, end;  // attended tokens
@@ -70,45 +72,78 @@ __device__ inline BqSpan bq_span(const DecodeBqParams &p, int L) {
     return sp;
 }
 
-__device__ inline uint4 ld_codes16(const uint8_t *p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
+// 16 bytes to shared memory, asynchronously; the copies so far as a group; until all
+// but the newest N groups are there.
+__device__ inline void copy16(uint32_t to, const uint8_t *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ inline uint2 ld_codes8(const uint8_t *p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
+__device__ inline void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ inline void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// N words (2 or 4) of shared memory.
+template <int N> __device__ inline void ld_words(uint32_t from, uint32_t *r) {
+    if constexpr (N == 4)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(from)
+                     : "memory");
+    else
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(from) : "memory");
 }
 
-// Two codes, the bytes `Lo` and `Lo` + 1 of w, as a pair of fp16 (E4M3: times 2^-8).
-template <int Fmt, int Lo> __device__ inline uint32_t code_pair(uint32_t w) {
+// The two codes of the low (or high) half of w as a pair of fp16.
+__device__ inline uint32_t e4m3_pair(uint32_t w, bool high) {
+    uint32_t y;
+    if (high)
+        asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(y) : "r"(w));
+    else
+        asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(y) : "r"(w));
+    return y;
+}
+
+// K: four adjacent codes as two pairs of fp16.  E4M3: dims (0, 1), (2, 3).  INT8: dims
+// (0, 2), (1, 3), as code + 128 in the low bits of the fp16, which is that times 2^-24
+// (the queries' sums times 128 are taken off where the scores start).
+template <int Fmt> __device__ inline void k_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
     if (Fmt == kFmtI8) {
-        // w's bytes are code + 128 (see code_bias)
-        const uint32_t x = __byte_perm(w, 0x64646464u, Lo == 0 ? 0x4140 : 0x4342);
-        const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&x), __half2(__half_raw{0x6480}, __half_raw{0x6480}));
-        return *reinterpret_cast<const uint32_t *>(&y);
+        a = (w ^ 0x80808080u) & 0x00ff00ffu;
+        b = (w >> 8 ^ 0x00808080u) & 0x00ff00ffu;
+    } else {
+        a = e4m3_pair(w, false);
+        b = e4m3_pair(w, true);
     }
-    const uint32_t x = __byte_perm(w, 0u, Lo == 0 ? 0x1404 : 0x3424);
-    return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
 }
-template <int Fmt> __device__ inline uint32_t code_bias(uint32_t w) { return Fmt == kFmtI8 ? w ^ 0x80808080u : w; }
-template <int Fmt> __host__ __device__ constexpr float code_unit() { return Fmt == kFmtI8 ? 1.f : 256.f; }
+template <int Fmt> __device__ constexpr int k_dim(int pair, int i) {  // dim of pair's element i
+    return Fmt == kFmtI8 ? 2 * i + pair : 2 * pair + i;
+}
+template <int Fmt> __device__ constexpr float k_unit() { return Fmt == kFmtI8 ? 16777216.f : 1.f; }
 
-__device__ inline void mma16(float *c, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
-        "%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// V: dims 2i and 2i + 1 (i = half) of four of tokens a and b, each as the pair (a, b).  INT8 as
+// 1024 + 128 + code less 1152.
+template <int Fmt> __device__ inline void v_pairs(uint32_t wa, uint32_t wb, int half, uint32_t &x, uint32_t &y) {
+    if (Fmt == kFmtI8) {
+        const uint32_t z = __byte_perm(wa, wb, half ? 0x7632 : 0x5410);  // a, a', b, b'
+        const uint32_t even = (z & 0x00ff00ffu) ^ 0x64806480u;
+        const uint32_t odd = (z >> 8 & 0x00ff00ffu) ^ 0x64806480u;
+        const __half2 bias = __half2(__half_raw{0x6480}, __half_raw{0x6480});
+        const __half2 e = __hsub2(*reinterpret_cast<const __half2 *>(&even), bias);
+        const __half2 o = __hsub2(*reinterpret_cast<const __half2 *>(&odd), bias);
+        x = *reinterpret_cast<const uint32_t *>(&e);
+        y = *reinterpret_cast<const uint32_t *>(&o);
+    } else {
+        const uint32_t z = __byte_perm(wa, wb, half ? 0x7362 : 0x5140);  // a, b, a', b'
+        x = e4m3_pair(z, false);
+        y = e4m3_pair(z, true);
+    }
 }
-__device__ inline void mma8(float *c, uint32_t a0, uint32_t a1, uint32_t b) {
+
+// d = a b + c (d may be c).
+__device__ inline void mma16(float *d, const uint32_t *a, uint32_t b0, uint32_t b1, const float *c) {
     asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b));
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+        "%12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 __device__ inline uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -125,6 +160,24 @@ __device__ inline uint32_t pack_half(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// N consecutive query elements from element `at` on, as fp32.
+template <int N> __device__ inline void load_query(const DecodeBqParams &p, long long at, float *x) {
+    if (p.q_dtype == PA_F32) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            Elt<float>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + at + i), x + i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + i);
+            if (p.q_dtype == PA_F16)
+                Elt<__half>::unpack(r, x + i);
+            else
+                Elt<__nv_bfloat16>::unpack(r, x + i);
+        }
+    }
+}
+
 // Units (iterations and piece costs) of a sequence's kv head.
 template <int U> __device__ inline long long bq_units(const BqSpan &sp) { return (sp.tiles + U - 1) / U + kPieceCost; }
 
@@ -137,15 +190,19 @@ struct BqSlot {
 inline __host__ __device__ constexpr int bq_part_floats(int group, int head_dim) {
     return group * head_dim + (2 * group + 3) / 4 * 4;  // (whole float4s)
 }
+// Of a warp: two iterations' codes, 2 KB of K and of V each.
+constexpr int kBqStage = 2048;
+constexpr int kBqStages = 2;
 inline size_t bq_smem(int group, int head_dim) {
-    return static_cast<size_t>(kDecodeBqWarps) * 2 * bq_part_floats(group, head_dim) * sizeof(float);
+    return static_cast<size_t>(kDecodeBqWarps) *
+           (2 * kBqStages * kBqStage + 2 * bq_part_floats(group, head_dim) * sizeof(float));
 }
 
 template <int D, bool B8, int Fmt, int QT, int NG, int U>
-__global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecodeBqCtas : 1)
+__global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecodeBqCtas : (NG == 2 && QT == 3 ? 2 : 3))
     decode_bq_kernel(const DecodeBqParams p) {
-    constexpr int KC = D / 64;       // 16-byte chunks of a K row a lane holds
-    constexpr int KS = D / 16;       // k-steps of S
+    constexpr int KW = D / 16;       // words of a K row a lane holds: one a k-step of S
+    constexpr int KC = D / 64;       // its 16-byte chunks
     constexpr int VW = D / 32;       // words of a V row a lane holds (4 dims each)
     constexpr int MT = D / 16;       // row tiles of O^T
     constexpr int NB = B8 ? 2 : 1;   // blocks of a tile
@@ -154,11 +211,29 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
     __shared__ long long warp_units[kDecodeBqWarps];
     __shared__ BqSlot slots[kDecodeBqWarps][2];
     __shared__ int last_cta[kDecodeBqWarps];  // of a slot 1's piece
-    extern __shared__ float4 parts4[];        // [warps][2]: [group][D] accumulators, [group][2] (max, sum)
+    extern __shared__ __align__(128) float4 dynamic[];  // [warps][stages] codes of K and of V, then
+    // [warps][2]: [group][D] accumulators, [group][2] (max, sum)
+    float *const all_parts = reinterpret_cast<float *>(dynamic) + kDecodeBqWarps * 2 * kBqStages * kBqStage / 4;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    // the lane's place in a K tile (row g) and in a V tile (row 2t)
+    const uint8_t *const k_lane = p.k_cache + lane * 16, *const v_lane = p.v_cache + lane * 16;
+    // A stage is 16 lines of 128 bytes, copied as they lie in the pool (whole lines a warp
+    // instruction), the 16-byte chunks of line i at their place xor i (head_dim 128; a line
+    // is a row) or xor 2 i (64; two rows), modulo 8, so that no fragment's read meets a
+    // bank twice.
+    const uint32_t stages = smem_addr(dynamic) + warp * 2 * kBqStages * kBqStage;
+    const uint32_t copy_to = stages + (lane >> 3) * 128 + ((lane & 7) ^ ((lane >> 3) * (128 / D))) * 16;
+    // (lines 4 on: xor 4, of rows of 128)
+    const uint32_t copy_odd = D == 128 ? copy_to ^ 64 : copy_to;
+    const uint32_t k_read = stages + (D == 128 ? g * 128 + ((2 * t) ^ g) * 16
+                                               : (g >> 1) * 128 + (((g & 1) * 4 + t) ^ (2 * (g >> 1))) * 16);
+    const uint32_t v_read = stages + kBqStages * kBqStage +
+                            (D == 128 ? 2 * t * 128 + (g ^ (2 * t)) * 16
+                                      : t * 128 + ((g >> 1) ^ (2 * t)) * 16 + (g & 1) * 8);
+    const float take = t < 2 ? 0.f : -kPLow, mul = t < 2 ? 1.f : kPLow;
     const int hkv = p.num_kv_heads, G = p.num_heads / hkv;
     const int wid = blockIdx.x * kDecodeBqWarps + warp, nwarps = gridDim.x * kDecodeBqWarps;
 
@@ -246,18 +321,18 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
         }
         if (k0 < k1) {
             // queries as fragments; their power of two
-            uint32_t qf[NG][QS][KS][2];
-            float qs[NG][2];  // of the lane's two columns: scale * log2 e / the power of two
+            uint32_t qf[NG][QS][KW][2];
+            float qs[NG][2];     // of the lane's two columns: scale * log2 e / the power of two
+            float start[NG][4];  // where the scores start
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
                 const int h = 4 * n + (g & 3);
-                const bool there = h < G;
-                const int elt = p.q_dtype == PA_F32 ? 4 : 2;
-                const char *row = static_cast<const char *>(p.q) + (out_row + (there ? h : 0)) * D * elt;
-                float top = 0.f;
-                for (int c = 0; c < KC * 16; ++c) {
-                    const float x = there ? fabsf(load_elt(row, p.q_dtype, (c >> 4) * 64 + t * 16 + (c & 15))) : 0.f;
-                    top = fmaxf(top, x);
+                float x[KW * 4], top = 0.f;
+                load_query<KW * 4>(p, (out_row + (h < G ? h : 0)) * D + t * (KW * 4), x);
+#pragma unroll
+                for (int c = 0; c < KW * 4; ++c) {
+                    x[c] = h < G ? x[c] : 0.f;
+                    top = fmaxf(top, fabsf(x[c]));
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -265,37 +340,49 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                 int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
                 e = e < -100 ? -100 : (e > 100 ? 100 : e);
                 const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-                const float down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2;
-                // the lane's columns 2t, 2t + 1 are the heads of lanes g = 2t, 2t + 1 (modulo 4)
-                qs[n][0] = __shfl_sync(0xffffffffu, down, (2 * (t & 1)) << 2);
-                qs[n][1] = __shfl_sync(0xffffffffu, down, (2 * (t & 1) + 1) << 2);
+                const float down =
+                    __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * (p.scale_log2 * k_unit<Fmt>());
+                float sum = 0.f;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
+                for (int ks = 0; ks < KW; ++ks)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const int d = (ks >> 2) * 64 + t * 16 + (ks & 3) * 4 + 2 * b;
-                        float x[2], y[2];
+                        float y[2], z[2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            x[i] = there ? load_elt(row, p.q_dtype, d + i) * up : 0.f;
-                            y[i] = 0.f;
+                            y[i] = x[ks * 4 + k_dim<Fmt>(b, i)] * up;
+                            z[i] = 0.f;
                             if (QT == 3) {
-                                const float hi = __half2float(__float2half_rn(x[i]));
-                                const float r = x[i] - hi;
+                                const float hi = __half2float(__float2half_rn(y[i]));
+                                const float r = y[i] - hi;
                                 const float mid = __half2float(__float2half_rn(r));
-                                x[i] = g < 4 ? hi : mid;
-                                y[i] = g < 4 ? r - mid : 0.f;
+                                y[i] = g < 4 ? hi : mid;
+                                z[i] = g < 4 ? r - mid : 0.f;
                             }
                         }
-                        qf[n][0][ks][b] = pack_half(x[0], x[1]);
-                        if (QT == 3)
-                            qf[n][QS - 1][ks][b] = pack_half(y[0], y[1]);
+                        qf[n][0][ks][b] = pack_half(y[0], y[1]);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[n][0][ks][b]));
+                        sum += f.x + f.y;
+                        if (QT == 3) {
+                            qf[n][QS - 1][ks][b] = pack_half(z[0], z[1]);
+                            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&qf[n][QS - 1][ks][b]));
+                            sum += l.x + l.y;
+                        }
                     }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum = Fmt == kFmtI8 ? sum * (-128.f / k_unit<Fmt>()) : 0.f;
+                // columns 2t, 2t + 1 are those of lanes g = 2t, 2t + 1 (for heads: modulo 4)
+                qs[n][0] = __shfl_sync(0xffffffffu, down, (2 * (t & 1)) << 2);
+                qs[n][1] = __shfl_sync(0xffffffffu, down, (2 * (t & 1) + 1) << 2);
+                start[n][0] = start[n][2] = __shfl_sync(0xffffffffu, sum, (2 * t) << 2);
+                start[n][1] = start[n][3] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) << 2);
             }
-            float m[NG][2], l[NG][2], o[NG][MT][4];
+            // base: the running maximum less kPTop
+            float base[NG][2], l[NG][2], o[NG][MT][4];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                m[n][0] = m[n][1] = -INFINITY;
+                base[n][0] = base[n][1] = kNoMax;
                 l[n][0] = l[n][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
@@ -304,108 +391,150 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                         o[n][i][c] = 0.f;
             }
 
-            // blocks of the piece, 32 table entries at a time (and the next 32)
+            // Blocks of the piece, a lane an entry, 32 at a time: those in use, with their
+            // scales; the next 32, their scales on the way; and the entries after them.
             const int32_t *table = p.block_tables + static_cast<long long>(seq) * p.max_blocks;
             const int end_block = (sp.end + p.block_size - 1) >> p.log_block;
             const int tile_shift = p.log_block - 4;  // (not B8) tiles of a block: 1 or 2
             const int first = sp.b0 + (B8 ? 2 * k0 * U : (k0 * U) >> tile_shift);
             int group = 0;
-            int entries = first + lane < end_block ? table[first + lane] : -1;
-            int entries_next = first + 32 + lane < end_block ? table[first + 32 + lane] : -1;
+            int phys, phys_next, entry_next;
+            float gks, gvs, gks_next, gvs_next;
+            auto entry = [&](int i) { return first + i + lane < end_block ? table[first + i + lane] : -1; };
+            auto scales = [&](int &e, int i, float &a, float &b) {  // of entry e, the i-th and so on
+                const bool ok = e >= 0 && e < p.num_blocks;
+                if (!ok && first + i + lane < end_block && p.err)
+                    atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+                e = ok ? e : -1;
+                const long long pair = static_cast<long long>(ok ? e : 0) * hkv + head;
+                a = ok ? __ldg(p.k_scales + pair) : 0.f;
+                b = ok ? __ldg(p.v_scales + pair) : 0.f;
+            };
+            phys = entry(0);
+            phys_next = entry(32);
+            entry_next = entry(64);
+            scales(phys, 0, gks, gvs);
+            scales(phys_next, 32, gks_next, gvs_next);
 
-            uint4 kr[U][2][KC];
-            uint32_t vr[U][4][VW];
-            long long off[U][NB];       // of the next tiles: bytes from the pool's start
-            float ks_next[U][NB], vs_next[U][NB];
-            unsigned ok_next = 0;       // bit u * NB + b: the block is in the pool
-
-            auto locate = [&](int it) {  // the tiles of iteration it
-                ok_next = 0;
+            // V scales as a power of two (of o) and a factor of the weights
+            float v_unit = 1.f, v_inv = 1.f;
+            auto set_unit = [&](float top) {
+                if (!(top < INFINITY))
+                    return;
+                int e = static_cast<int>(__float_as_uint(top) >> 23) + 1;  // 2^(e - 127) >= top
+                e = e > 252 ? 252 : (e < 2 ? 2 : e);
+                const float unit = __uint_as_float(static_cast<uint32_t>(e) << 23);
+                const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+                const float f = v_unit * inv;
+                v_unit = unit;
+                v_inv = inv;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                for (int n = 0; n < NG; ++n)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            o[n][i][c] *= f;
+            };
+
+            // The copies run two iterations ahead: K of one is started when K of the one two
+            // before was used, V likewise.  Scales and places of the two on the way:
+            struct Ahead {
+                long long off[U][NB];  // the block's start in either pool, plus the tile's
+                float ks[U][NB], vs[U][NB];
+                unsigned ok;  // bit u * NB + b: the block is in the pool
+            } now, next, after;
+
+            // A stage's lines 0 - 7 and 8 - 15 from `lo` and `hi`.
+            auto copy_stage = [&](uint32_t to, const uint8_t *lo, const uint8_t *hi) {
+                copy16(copy_to + to, lo);
+                copy16(copy_odd + to + 512, lo + 512);
+                copy16(copy_to + to + 1024, hi);
+                copy16(copy_odd + to + 1536, hi + 512);
+            };
+            // Halves of a stage: the blocks or halves of a tile (head_dim 128), two tiles (64; of
+            // blocks of 8 each half is two pieces of 512 bytes).
+            auto copy_halves = [&](uint32_t to, const uint8_t *pool, const Ahead &a) {
+                if constexpr (D == 128) {
+                    copy_stage(to, pool + a.off[0][0], pool + a.off[0][NB - 1] + (B8 ? 0 : 1024));
+                } else {
+                    copy16(copy_to + to, pool + a.off[0][0]);
+                    copy16(copy_to + to + 512, pool + a.off[0][NB - 1] + (B8 ? 0 : 512));
+                    copy16(copy_to + to + 1024, pool + a.off[1][0]);
+                    copy16(copy_to + to + 1536, pool + a.off[1][NB - 1] + (B8 ? 0 : 512));
+                }
+            };
+            auto copy_k = [&](int it) {  // K of iteration it; `after` gets its scales and places
+                after.ok = 0;
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         const int tile = it * U + u;
                         const int e = sp.b0 + (B8 ? 2 * tile + b : tile >> tile_shift) - first;
-                        if ((e >> 5) != group) {  // the same for the whole warp
+                        if ((e >> 5) != group) {  // the same for the whole warp, and all of an iteration
                             ++group;
-                            entries = entries_next;
-                            const int x = first + 32 * (group + 1) + lane;
-                            entries_next = x < end_block ? table[x] : -1;
+                            phys = phys_next, gks = gks_next, gvs = gvs_next;
+                            phys_next = entry_next;
+                            entry_next = entry(32 * (group + 2));
+                            scales(phys_next, 32 * (group + 1), gks_next, gvs_next);
                         }
-                        const int phys = __shfl_sync(0xffffffffu, entries, e & 31);
-                        const bool ok = phys >= 0 && phys < p.num_blocks;
-                        if (!ok && first + e < end_block && lane == 0 && p.err)
-                            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
-                        const long long pair = static_cast<long long>(ok ? phys : 0) * hkv + head;
-                        ks_next[u][b] = __ldg(p.k_scales + pair);
-                        vs_next[u][b] = __ldg(p.v_scales + pair);
-                        off[u][b] = (pair << p.log_block) * D;
+                        const int ph = __shfl_sync(0xffffffffu, phys, e & 31);
+                        after.ks[u][b] = __shfl_sync(0xffffffffu, gks, e & 31);
+                        after.vs[u][b] = __shfl_sync(0xffffffffu, gvs, e & 31);
+                        const long long pair = static_cast<long long>(ph < 0 ? 0 : ph) * hkv + head;
+                        long long off = (pair << p.log_block) * D;
                         if (!B8 && (tile & ((1 << tile_shift) - 1)))
-                            off[u][b] += 16 * D;
-                        ok_next |= static_cast<unsigned>(ok) << (u * NB + b);
+                            off += 16 * D;
+                        after.off[u][b] = off;
+                        after.ok |= static_cast<unsigned>(ph >= 0) << (u * NB + b);
                     }
+                }
+                copy_halves((it & 1) * kBqStage, k_lane, after);
             };
-            auto load_k = [&]() {
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint8_t *row = p.k_cache + off[u][B8 ? r : 0] + (g + (B8 ? 0 : 8 * r)) * D + t * 16;
-#pragma unroll
-                        for (int c = 0; c < KC; ++c)
-                            kr[u][r][c] = ld_codes16(row + c * 64);
-                    }
+            auto copy_v = [&](int it, const Ahead &a) {
+                copy_halves((kBqStages + (it & 1)) * kBqStage, v_lane, a);
             };
-            auto load_v = [&]() {  // tokens 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const uint8_t *row = p.v_cache + off[u][B8 ? r >> 1 : 0] +
-                                             (2 * t + (r & 1) + (B8 ? 0 : 8 * (r >> 1))) * D + g * (D / 8);
-                        if constexpr (VW == 4) {
-                            const uint4 x = ld_codes16(row);
-                            vr[u][r][0] = x.x, vr[u][r][1] = x.y, vr[u][r][2] = x.z, vr[u][r][3] = x.w;
-                        } else {
-                            const uint2 x = ld_codes8(row);
-                            vr[u][r][0] = x.x, vr[u][r][1] = x.y;
-                        }
-                    }
-            };
+            auto inside = [&](int tok, bool ok) { return tok >= sp.start && tok < sp.end && ok; };
 
-            locate(k0);
-            load_k();
-            load_v();
+            copy_k(k0);
+            now = after;
+            copy_commit();
+            copy_v(k0, now);
+            copy_commit();
+            if (k0 + 1 < k1)
+                copy_k(k0 + 1);
+            next = after;
+            copy_commit();
+            if (k0 + 1 < k1)
+                copy_v(k0 + 1, next);
+            copy_commit();
             for (int it = k0; it < k1; ++it) {
-                const unsigned ok = ok_next;
-                float vs[U][NB];
                 float x[U][NG][4];
+                bool full[U];
+                copy_wait<3>();  // K of this iteration is there (V, and K and V of the next, may not be)
+                __syncwarp();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    uint32_t kr[2][KW];
 #pragma unroll
-                    for (int n = 0; n < NG; ++n)
-                        x[u][n][0] = x[u][n][1] = x[u][n][2] = x[u][n][3] = 0.f;
+                    for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        const uint4 r0 = kr[u][0][ks >> 2], r1 = kr[u][1][ks >> 2];
-                        const uint32_t w0 = code_bias<Fmt>((&r0.x)[ks & 3]), w1 = code_bias<Fmt>((&r1.x)[ks & 3]);
-                        const uint32_t a[4] = {code_pair<Fmt, 0>(w0), code_pair<Fmt, 0>(w1), code_pair<Fmt, 2>(w0),
-                                               code_pair<Fmt, 2>(w1)};
+                        for (int c = 0; c < KC; ++c)
+                            ld_words<4>((k_read ^ (c * 16)) + (it & 1) * kBqStage + u * 1024 + r * (8 * D), kr[r] + c * 4);
+#pragma unroll
+                    for (int ks = 0; ks < KW; ++ks) {
+                        uint32_t a[4];
+                        k_pairs<Fmt>(kr[0][ks], a[0], a[2]);
+                        k_pairs<Fmt>(kr[1][ks], a[1], a[3]);
 #pragma unroll
                         for (int n = 0; n < NG; ++n)
 #pragma unroll
                             for (int q = 0; q < QS; ++q)
-                                mma16(x[u][n], a, qf[n][q][ks][0], qf[n][q][ks][1]);
+                                mma16(x[u][n], a, qf[n][q][ks][0], qf[n][q][ks][1],
+                                      ks == 0 && q == 0 ? start[n] : x[u][n]);
                     }
-                    float ks0 = ks_next[u][0] * code_unit<Fmt>(), ks1 = B8 ? ks_next[u][NB - 1] * code_unit<Fmt>() : ks0;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        // (a block outside the pool stands for block 0, whose scale may be anything)
-                        vs[u][b] = (ok >> (u * NB + b) & 1) ? vs_next[u][b] * code_unit<Fmt>() : 0.f;
-                    const int tok = (sp.b0 << p.log_block) + (it * U + u) * 16 + g;
-                    const bool in0 = tok >= sp.start && tok < sp.end && (ok >> (u * NB) & 1);
-                    const bool in1 = tok + 8 >= sp.start && tok + 8 < sp.end && (ok >> (u * NB + NB - 1) & 1);
+                    const float ks0 = now.ks[u][0], ks1 = now.ks[u][NB - 1];
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
                         if (QT == 3) {  // the terms' halves
@@ -413,37 +542,60 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                             for (int c = 0; c < 4; ++c)
                                 x[u][n][c] += __shfl_xor_sync(0xffffffffu, x[u][n][c], 2);
                         }
-                        x[u][n][0] = in0 ? x[u][n][0] * (ks0 * qs[n][0]) : -INFINITY;
-                        x[u][n][1] = in0 ? x[u][n][1] * (ks0 * qs[n][1]) : -INFINITY;
-                        x[u][n][2] = in1 ? x[u][n][2] * (ks1 * qs[n][0]) : -INFINITY;
-                        x[u][n][3] = in1 ? x[u][n][3] * (ks1 * qs[n][1]) : -INFINITY;
+                        x[u][n][0] *= ks0 * qs[n][0];
+                        x[u][n][1] *= ks0 * qs[n][1];
+                        x[u][n][2] *= ks1 * qs[n][0];
+                        x[u][n][3] *= ks1 * qs[n][1];
+                    }
+                    // tokens outside the context, or of blocks outside the pool
+                    const int tok = (sp.b0 << p.log_block) + (it * U + u) * 16;
+                    const unsigned ok = now.ok >> (u * NB);
+                    full[u] = tok >= sp.start && tok + 16 <= sp.end && (ok & ((1 << NB) - 1)) == (1 << NB) - 1;
+                    if (!full[u]) {
+                        const bool in0 = inside(tok + g, ok & 1);
+                        const bool in1 = inside(tok + g + 8, ok >> (NB - 1) & 1);
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
+                            x[u][n][0] = in0 ? x[u][n][0] : -INFINITY;
+                            x[u][n][1] = in0 ? x[u][n][1] : -INFINITY;
+                            x[u][n][2] = in1 ? x[u][n][2] : -INFINITY;
+                            x[u][n][3] = in1 ? x[u][n][3] : -INFINITY;
+                        }
                     }
                 }
-                if (it + 1 < k1) {
-                    locate(it + 1);
-                    load_k();
-                }
+                float top = 0.f;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        top = fmaxf(top, now.vs[u][b]);
+                if (top > v_unit || (top < v_unit * kLowScale && top > 0))
+                    set_unit(top);
+                __syncwarp();  // (every lane has read this iteration's K)
+                if (it + 2 < k1)
+                    copy_k(it + 2);
+                copy_commit();
                 // the running maximum moves only when it is exceeded by kMaxSlack
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {
-                    float t0 = -INFINITY, t1 = -INFINITY;
+                    float t0 = x[0][n][0], t1 = x[0][n][1];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
                         t0 = fmaxf(t0, fmaxf(x[u][n][0], x[u][n][2]));
                         t1 = fmaxf(t1, fmaxf(x[u][n][1], x[u][n][3]));
                     }
-                    if (__any_sync(0xffffffffu, t0 > m[n][0] + kMaxSlack || t1 > m[n][1] + kMaxSlack)) {
+                    if (__any_sync(0xffffffffu, t0 > base[n][0] + (kMaxSlack + kPTop) ||
+                                                    t1 > base[n][1] + (kMaxSlack + kPTop))) {
 #pragma unroll
                         for (int s = 4; s < 32; s <<= 1) {
                             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, s));
                             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, s));
                         }
-                        t0 = fmaxf(t0, m[n][0]);
-                        t1 = fmaxf(t1, m[n][1]);
-                        const float f0 = t0 == -INFINITY ? 1.f : ex2(m[n][0] - t0);
-                        const float f1 = t1 == -INFINITY ? 1.f : ex2(m[n][1] - t1);
-                        m[n][0] = t0;
-                        m[n][1] = t1;
+                        t0 = fmaxf(t0 - kPTop, base[n][0]);
+                        t1 = fmaxf(t1 - kPTop, base[n][1]);
+                        const float f0 = ex2(base[n][0] - t0), f1 = ex2(base[n][1] - t1);
+                        base[n][0] = t0;
+                        base[n][1] = t1;
                         l[n][0] *= f0;
                         l[n][1] *= f1;
 #pragma unroll
@@ -455,64 +607,62 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                         }
                     }
                 }
+                copy_wait<3>();  // V is there
+                __syncwarp();
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
+                    const float r0 = now.vs[u][0] * v_inv, r1 = now.vs[u][NB - 1] * v_inv;
                     uint32_t pf[NG][2];  // weights as the second product's operand: tokens 2t.. and 2t + 8..
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        // (no token yet: every weight of the column is exp2(-inf) = 0)
-                        const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kPTop;
-                        const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kPTop;
-                        const float e0 = ex2(x[u][n][0] - m0), e1 = ex2(x[u][n][1] - m1);
-                        const float e2 = ex2(x[u][n][2] - m0), e3 = ex2(x[u][n][3] - m1);
-                        l[n][0] += e0 + e2;
-                        l[n][1] += e1 + e3;
-                        uint32_t h0 = pack_half(e0, e1), h1 = pack_half(e2, e3);
-                        if (t >= 2) {
-                            const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
-                            const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
-                            h0 = pack_half((e0 - a.x) * kPLow, (e1 - a.y) * kPLow);
-                            h1 = pack_half((e2 - b.x) * kPLow, (e3 - b.y) * kPLow);
-                        }
-                        pf[n][0] = transpose8x8(h0);
-                        pf[n][1] = transpose8x8(h1);
+                        float e[4];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            e[c] = ex2(x[u][n][c] - base[n][c & 1]);
+                        l[n][0] += e[0] + e[2];
+                        l[n][1] += e[1] + e[3];
+                        e[0] *= r0, e[1] *= r0, e[2] *= r1, e[3] *= r1;
+                        const uint32_t h0 = pack_half(e[0], e[1]), h1 = pack_half(e[2], e[3]);
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
+                        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
+                        // columns 0 to 3: the weight itself; 4 to 7: kPLow times what fp16 leaves of it
+                        pf[n][0] = transpose8x8(pack_half(fmaf(a.x, take, e[0] * mul), fmaf(a.y, take, e[1] * mul)));
+                        pf[n][1] = transpose8x8(pack_half(fmaf(b.x, take, e[2] * mul), fmaf(b.y, take, e[3] * mul)));
+                    }
+                    uint32_t vr[4][VW];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        ld_words<VW>((v_read ^ ((r & 1) * (D == 128 ? 16 : 64))) + (D == 128 ? (r & 1) * 128 : 0) +
+                                         (it & 1) * kBqStage + u * 1024 + (r >> 1) * (8 * D),
+                                     vr[r]);
+                    if (Fmt == kFmtE4M3 && !full[u]) {  // (a NaN code outside must not meet its weight of 0)
+                        const int tok = (sp.b0 << p.log_block) + (it * U + u) * 16;
+                        const unsigned ok = now.ok >> (u * NB);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (!inside(tok + 2 * t + (r & 1) + 8 * (r >> 1), ok >> (B8 ? r >> 1 : 0) & 1))
+#pragma unroll
+                                for (int w = 0; w < VW; ++w)
+                                    vr[r][w] = 0;
                     }
 #pragma unroll
-                    for (int w = 0; w < VW; ++w) {
-                        // [token pair][dims 0 and 1, dims 2 and 3]: bytes (a, b, a, b)
-                        uint32_t z[2][2];
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            z[r][0] = code_bias<Fmt>(__byte_perm(vr[u][2 * r][w], vr[u][2 * r + 1][w], 0x5140));
-                            z[r][1] = code_bias<Fmt>(__byte_perm(vr[u][2 * r][w], vr[u][2 * r + 1][w], 0x7362));
-                        }
+                    for (int w = 0; w < VW; ++w)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t a[4] = {code_pair<Fmt, 0>(z[0][i]), code_pair<Fmt, 2>(z[0][i]),
-                                                   code_pair<Fmt, 0>(z[1][i]), code_pair<Fmt, 2>(z[1][i])};
+                            uint32_t a[4];
+                            v_pairs<Fmt>(vr[0][w], vr[1][w], i, a[0], a[1]);
+                            v_pairs<Fmt>(vr[2][w], vr[3][w], i, a[2], a[3]);
 #pragma unroll
-                            for (int n = 0; n < NG; ++n) {
-                                float *acc = o[n][2 * w + i];
-                                float y[4] = {0.f, 0.f, 0.f, 0.f};
-                                if constexpr (B8) {
-                                    float y1[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma8(y, a[0], a[1], pf[n][0]);
-                                    mma8(y1, a[2], a[3], pf[n][1]);
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c)
-                                        acc[c] = fmaf(vs[u][NB - 1], y1[c], acc[c]);
-                                } else {
-                                    mma16(y, a, pf[n][0], pf[n][1]);
-                                }
-#pragma unroll
-                                for (int c = 0; c < 4; ++c)
-                                    acc[c] = fmaf(vs[u][0], y[c], acc[c]);
-                            }
+                            for (int n = 0; n < NG; ++n)
+                                mma16(o[n][2 * w + i], a, pf[n][0], pf[n][1], o[n][2 * w + i]);
                         }
-                    }
                 }
-                if (it + 1 < k1)
-                    load_v();
+                __syncwarp();
+                if (it + 2 < k1)
+                    copy_v(it + 2, after);
+                copy_commit();
+                now = next;
+                next = after;
             }
 
             // The low parts of the weights join the high ones: the lane gets one head,
@@ -528,7 +678,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                     lsum[1] += __shfl_xor_sync(0xffffffffu, lsum[1], s);
                 }
                 const float sum = t < 2 ? lsum[0] : lsum[1];
-                const float top = t < 2 ? m[n][0] : m[n][1];
+                const float top = t < 2 ? base[n][0] : base[n][1];
                 float y[D / 8];
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
@@ -536,8 +686,8 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                     for (int c = 0; c < 2; ++c) {
                         const float send = t < 2 ? o[n][i][2 * c + 1] : o[n][i][2 * c];
                         const float got = __shfl_xor_sync(0xffffffffu, send, 2);
-                        y[2 * i + c] = t < 2 ? fmaf(got, 1.f / kPLow, o[n][i][2 * c])
-                                             : fmaf(o[n][i][2 * c + 1], 1.f / kPLow, got);
+                        y[2 * i + c] = v_unit * (t < 2 ? fmaf(got, 1.f / kPLow, o[n][i][2 * c])
+                                                       : fmaf(o[n][i][2 * c + 1], 1.f / kPLow, got));
                     }
                 const int h = 4 * n + hc;
                 if (h >= G)
@@ -555,7 +705,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                             store_out(p.out, p.out_dtype, to + i, y[i] * inv);
                     }
                 } else {
-                    float *part = reinterpret_cast<float *>(parts4) + (warp * 2 + (k0 == 0)) * bq_part_floats(G, D);
+                    float *part = all_parts + (warp * 2 + (k0 == 0)) * bq_part_floats(G, D);
                     float4 *to = reinterpret_cast<float4 *>(part + h * D + g * (D / 8));
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i)
@@ -596,7 +746,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
         }
         const bool final = from == 1 && ends;
         const int floats = bq_part_floats(G, D);
-        const float *parts = reinterpret_cast<const float *>(parts4) + warp * 2 * floats;
+        const float *parts = all_parts + warp * 2 * floats;
         const long long out_row = static_cast<long long>(slot.seq) * p.num_heads + static_cast<long long>(slot.head) * G;
         if (!final && from == 1 && lane == 0)
             p.records[blockIdx.x] = make_int4(slot.seq, slot.head, last_cta[warp], 1);
@@ -611,7 +761,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecode
                 y[c] = 0.f;
             for (int i = 0; i < n; ++i) {
                 const float *part = parts + (2 * i + (i ? 0 : from)) * floats;
-                const float f = top == -INFINITY ? 1.f : ex2(part[G * D + 2 * h] - top);
+                const float f = ex2(part[G * D + 2 * h] - top);
                 sum = fmaf(f, part[G * D + 2 * h + 1], sum);
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c)
