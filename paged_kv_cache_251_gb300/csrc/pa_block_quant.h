@@ -47,7 +47,7 @@ struct DecodeBqParams {
 // (the workspace is sized for them).
 constexpr int kDecodeBqThreads = 128;
 constexpr int kDecodeBqWarps = kDecodeBqThreads / 32;
-constexpr int kDecodeBqCtas = 4;
+constexpr int kDecodeBqCtas = 3;
 constexpr int kDecodeBqSms = 152;
 constexpr int kDecodeBqMaxCtas = kDecodeBqSms * kDecodeBqCtas;
 

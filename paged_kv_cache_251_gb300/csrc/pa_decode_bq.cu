@@ -29,14 +29,25 @@ template <int D> __global__ void __launch_bounds__(kJoinThreads) join_bq_kernel(
     const int first = blockIdx.x, n = rec.z - first + 1;
     const float2 *ml = reinterpret_cast<const float2 *>(p.part_ml);
     auto part_of = [&](int i) { return (static_cast<long long>(first + i) * 2 + (i == 0)) * G + h; };
-    float top = -INFINITY;
-    for (int i = lane; i < n; i += 32)
+    // the first partials are on their way while the largest maximum is found
+    constexpr int kAhead = 4;
+    float ahead[kAhead][C];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = sub + k * subs;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            ahead[k][c] = i < n ? p.part_acc[part_of(i) * D + 32 * c + lane] : 0.f;
+    }
+    float2 mine = lane < n ? ml[part_of(lane)] : make_float2(kNoMax, 0.f);
+    float top = mine.x;
+    for (int i = lane + 32; i < n; i += 32)
         top = fmaxf(top, ml[part_of(i)].x);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    float sum = 0.f;
-    for (int i = lane; i < n; i += 32) {
+    float sum = ex2(mine.x - top) * mine.y;
+    for (int i = lane + 32; i < n; i += 32) {
         const float2 x = ml[part_of(i)];
         sum = fmaf(ex2(x.x - top), x.y, sum);
     }
@@ -47,8 +58,16 @@ template <int D> __global__ void __launch_bounds__(kJoinThreads) join_bq_kernel(
 #pragma unroll
     for (int c = 0; c < C; ++c)
         y[c] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+        const int i = sub + k * subs;
+        const float f = i < n ? ex2(ml[part_of(i)].x - top) : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            y[c] = fmaf(f, ahead[k][c], y[c]);
+    }
 #pragma unroll 4
-    for (int i = sub; i < n; i += subs) {
+    for (int i = sub + kAhead * subs; i < n; i += subs) {
         const long long part = part_of(i);
         const float f = ex2(ml[part].x - top);
 #pragma unroll

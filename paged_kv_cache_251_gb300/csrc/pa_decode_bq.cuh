@@ -107,7 +107,7 @@ __device__ inline uint32_t e4m3_pair(uint32_t w, bool high) {
 template <int Fmt> __device__ inline void k_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
     if (Fmt == kFmtI8) {
         a = (w ^ 0x80808080u) & 0x00ff00ffu;
-        b = (w >> 8 ^ 0x00808080u) & 0x00ff00ffu;
+        b = __byte_perm(w, 0, 0x4341) ^ 0x00800080u;
     } else {
         a = e4m3_pair(w, false);
         b = e4m3_pair(w, true);
@@ -124,7 +124,7 @@ template <int Fmt> __device__ inline void v_pairs(uint32_t wa, uint32_t wb, int 
     if (Fmt == kFmtI8) {
         const uint32_t z = __byte_perm(wa, wb, half ? 0x7632 : 0x5410);  // a, a', b, b'
         const uint32_t even = (z & 0x00ff00ffu) ^ 0x64806480u;
-        const uint32_t odd = (z >> 8 & 0x00ff00ffu) ^ 0x64806480u;
+        const uint32_t odd = __byte_perm(z, 0, 0x4341) ^ 0x64806480u;
         const __half2 bias = __half2(__half_raw{0x6480}, __half_raw{0x6480});
         const __half2 e = __hsub2(*reinterpret_cast<const __half2 *>(&even), bias);
         const __half2 o = __hsub2(*reinterpret_cast<const __half2 *>(&odd), bias);
@@ -199,7 +199,7 @@ inline size_t bq_smem(int group, int head_dim) {
 }
 
 template <int D, bool B8, int Fmt, int QT, int NG, int U>
-__global__ void __launch_bounds__(kDecodeBqThreads, NG == 1 && QT == 1 ? kDecodeBqCtas : (NG == 2 && QT == 3 ? 2 : 3))
+__global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDecodeBqCtas)
     decode_bq_kernel(const DecodeBqParams p) {
     constexpr int KW = D / 16;       // words of a K row a lane holds: one a k-step of S
     constexpr int KC = D / 64;       // its 16-byte chunks
