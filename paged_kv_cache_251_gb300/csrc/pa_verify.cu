@@ -20,9 +20,8 @@
 // A sequence is a cluster of CTAs, each taking a share of the vocabulary, a warp a
 // contiguous slice of it.  The first CTA gathers what the walk needs (every drafted
 // token's p, q and u) and hands it to the others, so all walk alike on the same
-// bits.  Only a rejection with q, and the end, read a row; the CTA and the warp
-// that hold the running sum read their slice (a few hundred entries) once more to
-// find the token.
+// bits.  Only a rejection with q, and the end, read a row; the slice of the warp whose
+// sum holds the token is read once more, shared by its CTA's warps, to find it.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -40,7 +39,7 @@ namespace {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxCluster = 8;
-constexpr double kFixedOne = 18014398509481984.0;  // 2^54
+constexpr int kFixedBits = 54;
 // Sums below 2^-20 are taken again in smaller units.
 constexpr unsigned long long kSmallSum = 1ull << 34;
 
@@ -48,15 +47,19 @@ struct VerifyShared {
     // of every drafted token; tok -1: not a token
     float p[kVerifyMaxDraft], q[kVerifyMaxDraft], u[kVerifyMaxDraft + 1];
     int parent[kVerifyMaxDraft], tok[kVerifyMaxDraft];
+    int fine[kVerifyMaxDraft];  // accepted if it is the first of its node's to be tried
     int drafts;
     unsigned long long total[2][kVerifyMaxCluster];  // of every CTA; two passes' (a slow CTA may still read the last)
-    unsigned long long warp_sum[kVerifyWarps];
+    unsigned long long warp_sum[kVerifyWarps], part_sum[kVerifyWarps];
     // the walk
     double a, s;
     int node, next, n, ngone, need;
     bool summed;  // total[] holds the sum of the present weights
     int path[kVerifyMaxDraft], gone[kVerifyMaxDraft];
 };
+
+__device__ inline void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ inline void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 enum { kWalkDone = 0, kWalkSum = 1, kWalkEnd = 2 };
 
@@ -67,29 +70,34 @@ template <bool HasQ> __device__ int walk(VerifyShared *sh) {
     double a = sh->a, s = sh->s;
     int ngone = sh->ngone;
     bool summed = sh->summed;
+    bool tried = HasQ ? a != 0 : ngone != 0;  // a child of the node was rejected
     int need = -1;
     int i = sh->next;
     for (; i < sh->drafts; ++i) {
         if (sh->parent[i] != node || sh->tok[i] < 0)
             continue;
-        double p = sh->p[i];
-        const double u = sh->u[i];
-        bool ok;
+        bool ok = sh->fine[i];
         if (HasQ) {
-            const double q = sh->q[i];
-            const double w = __dsub_rn(p, __dmul_rn(a, q));
-            ok = __dmul_rn(__dmul_rn(u, s), q) < (w > 0 ? w : 0.0);
+            if (tried) {
+                const double p = sh->p[i], q = sh->q[i], u = sh->u[i];
+                const double w = __dsub_rn(p, __dmul_rn(a, q));
+                ok = __dmul_rn(__dmul_rn(u, s), q) < (w > 0 ? w : 0.0);
+            }
         } else {
             bool again = false;
-            for (int g = 0; g < ngone; ++g)
-                again |= sh->gone[g] == sh->tok[i];
-            ok = !again && __dmul_rn(u, s) < p;
+            const double p = sh->p[i];
+            if (tried) {
+                for (int g = 0; g < ngone; ++g)
+                    again |= sh->gone[g] == sh->tok[i];
+                ok = !again && __dmul_rn(sh->u[i], s) < p;
+            }
             if (!ok && !again) {
                 sh->gone[ngone++] = sh->tok[i];
                 s -= p > 0 ? p : 0.0;
                 summed = false;
             }
         }
+        tried = !ok;
         if (ok) {
             sh->path[n++] = i;
             node = i;
@@ -133,6 +141,20 @@ template <bool Unit> __device__ inline Weight weight(float p, float q, float ah,
     const float d = __fsub_rn(p, h);
     const float e = __fsub_rn(__fsub_rn(__fsub_rn(p, d), h), l);
     return __fadd_rn(d, e) > 0 ? Weight{d, e} : Weight{0.f, 0.f};
+}
+
+// x >= 0, below 2^9, in units of 2^-bits (54 at least), rounded down.  (Integer
+// arithmetic: fp64 conversions are slow.)
+__device__ inline unsigned long long fixed(float x, int bits) {
+    const uint32_t b = __float_as_uint(x);
+    const int e = static_cast<int>(b >> 23) & 0xff;
+    const unsigned long long m = (b & 0x7fffffu) | (e ? 0x800000u : 0u);
+    const int left = bits - 150 + (e ? e : 1);  // x = m 2^(e - 150)
+    return left >= 0 ? m << (left > 40 ? 40 : left) : m >> (left < -63 ? 63 : -left);
+}
+__device__ inline unsigned long long fixed(float hi, float lo, int bits) {
+    const unsigned long long a = fixed(hi, bits), b = fixed(fabsf(lo), bits);
+    return lo < 0 ? (a > b ? a - b : 0) : a + b;
 }
 
 __device__ inline float to_f(float x) { return x; }
@@ -187,12 +209,12 @@ __device__ inline void leave_out(Entries<T, E> *p, int n, int base, int lane, co
     }
 }
 
-// Sum of the weights of [lo, hi) times `unit` (every lane gets it), entries in
+// Sum of the weights of [lo, hi) in units of 2^-bits (every lane gets it), entries in
 // gone[] left out (Mode kRowP only).
 template <typename T, int E, int Mode>
 __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, int hi, float ah, float al,
-                                        const int *gone, int ngone, double unit, int lane) {
-    constexpr int kFlight = E == 1 ? 8 : 16 / E;  // loads in flight of each row
+                                        const int *gone, int ngone, int bits, int lane) {
+    constexpr int kFlight = 16 / E;  // loads in flight of each row
     float h = 0.f, l = 0.f;
     for (int base = lo; base < hi; base += 32 * E * kFlight) {
         Entries<T, E> p[kFlight], q[kFlight];
@@ -217,15 +239,14 @@ __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, in
                 l = __fadd_rn(l, Mode == kRowP ? err : __fadd_rn(err, w.e));
             }
     }
-    const double x = (static_cast<double>(h) + static_cast<double>(l)) * unit;
-    return warp_add(static_cast<unsigned long long>(__double2ll_rn(x)));
+    return warp_add(fixed(h, l, bits));
 }
 
 // The first entry of [lo, hi) whose running sum exceeds t, entries in gone[] left
 // out; the last with any weight where rounding leaves none (-1: no weight at all).
 template <typename T, int E, int Mode>
 __device__ int slice_find(const T *prow, const T *qrow, int lo, int hi, float ah, float al, const int *gone, int ngone,
-                          unsigned long long t, double unit, int lane) {
+                          unsigned long long t, int bits, int lane) {
     unsigned long long before = 0;
     int last = -1;
     for (int base = lo; base < hi; base += 32 * E) {
@@ -240,7 +261,7 @@ __device__ int slice_find(const T *prow, const T *qrow, int lo, int hi, float ah
 #pragma unroll
         for (int k = 0; k < E; ++k) {
             const Weight we = entry<T, E, Mode>(p.f, q.f, k, ah, al);
-            w[k] = __double2ull_rd((static_cast<double>(we.d) + static_cast<double>(we.e)) * unit);
+            w[k] = fixed(we.d, we.e, bits);
             if (we.d > 0)
                 last = at + k;
             sum += w[k];
@@ -286,51 +307,63 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const T *target = static_cast<const T *>(p.target) + s * (T1 + 1) * p.target_stride;
     const T *draft = static_cast<const T *>(p.draft) + (HasQ ? s * T1 * p.draft_stride : 0);
 
-    // what the walk needs, gathered once for all CTAs (every one walks on the same bits)
+    // what the walk needs, gathered once for all CTAs (every one walks on the same bits):
+    // thread i drafted token i, and one more the last random number
+    static_assert(kVerifyMaxDraft < kVerifyThreads, "a thread a drafted token, and one more");
     if (ranks > 1)
-        cluster.sync();  // every CTA of the cluster has started
-    if (rank == 0) {
-        int drafts = p.draft_lens ? p.draft_lens[s] : T1;
+        cluster_arrive();
+    int drafts = T1, parent = -1, tok = -1;
+    float u = 0.f, pv = 0.f, qv = 0.f;
+    bool fine = false;
+    const int i = tid;
+    if (rank == 0 && i <= T1) {
         uint32_t bad = 0;
-        if (drafts < 0 || drafts > T1) {
-            bad = PA_DEVERR_BAD_LEN;
-            drafts = drafts < 0 ? 0 : T1;
-        }
-        for (int i = tid; i <= T1; i += kVerifyThreads) {
-            const float u = p.uniforms[s * (T1 + 1) + i];
-            float pv = 0.f, qv = 0.f;
-            int parent = -1, tok = -1;
-            if (i < T1) {
-                tok = p.draft_tokens[s * T1 + i];
-                parent = p.parents ? p.parents[s * T1 + i] : i - 1;
-                if (parent < 0)
-                    parent = -1;
-                if (i >= drafts) {
-                    tok = -1;
-                } else if (tok < 0 || tok >= V || parent >= i) {
-                    bad |= PA_DEVERR_BAD_INDEX;
-                    tok = -1;
-                } else {
-                    pv = to_f(target[static_cast<long long>(parent + 1) * p.target_stride + tok]);
-                    if (HasQ)
-                        qv = to_f(draft[static_cast<long long>(parent + 1) * p.draft_stride + tok]);
-                }
+        u = p.uniforms[s * (T1 + 1) + i];
+        if (p.draft_lens) {
+            drafts = p.draft_lens[s];
+            if (drafts < 0 || drafts > T1) {
+                bad = PA_DEVERR_BAD_LEN;
+                drafts = drafts < 0 ? 0 : T1;
             }
-            for (int r = 0; r < ranks; ++r) {
-                VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, r) : sh;
-                to->u[i] = u;
-                if (i < T1) {
-                    to->p[i] = pv;
-                    to->q[i] = qv;
-                    to->parent[i] = parent;
-                    to->tok[i] = tok;
-                } else {
-                    to->drafts = drafts;
-                }
+        }
+        if (i < T1) {
+            tok = p.draft_tokens[s * T1 + i];
+            parent = p.parents ? p.parents[s * T1 + i] : i - 1;
+            if (parent < 0)
+                parent = -1;
+            if (i >= drafts) {
+                tok = -1;
+            } else if (tok < 0 || tok >= V || parent >= i) {
+                bad |= PA_DEVERR_BAD_INDEX;
+                tok = -1;
+            } else {
+                pv = to_f(target[static_cast<long long>(parent + 1) * p.target_stride + tok]);
+                if (HasQ)
+                    qv = to_f(draft[static_cast<long long>(parent + 1) * p.draft_stride + tok]);
+                // u q < p without rounding: the product as value and error
+                const float h = HasQ ? __fmul_rn(u, qv) : u;
+                fine = h < pv || (HasQ && h == pv && __fmaf_rn(u, qv, -h) < 0);
             }
         }
         if (bad && p.err)
             atomicOr(p.err, bad);
+    }
+    if (ranks > 1)
+        cluster_wait();  // every CTA of the cluster has started
+    if (rank == 0 && i <= T1) {
+        for (int r = 0; r < ranks; ++r) {
+            VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, r) : sh;
+            to->u[i] = u;
+            if (i < T1) {
+                to->p[i] = pv;
+                to->q[i] = qv;
+                to->parent[i] = parent;
+                to->tok[i] = tok;
+                to->fine[i] = fine;
+            } else {
+                to->drafts = drafts;
+            }
+        }
     }
     if (tid == 0) {
         sh->a = 0;
@@ -351,7 +384,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     float ah, al;
     int mode, parity = 0;
     unsigned long long total = 0;
-    double unit = kFixedOne;  // 2^54, times a power of two where the sum is small
+    int bits = kFixedBits;  // more where the sum is small
     for (bool again = false, smaller = false;;) {
         if (tid == 0 && !again && !smaller)
             sh->need = walk<HasQ>(sh);
@@ -359,7 +392,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         const int need = sh->need;
         if (need != kWalkDone) {
             if (!smaller)
-                unit = kFixedOne;
+                bits = kFixedBits;
             const int node = sh->node;
             prow = target + static_cast<long long>(node + 1) * p.target_stride;
             const double a = sh->a;
@@ -369,11 +402,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             al = static_cast<float>(a - static_cast<double>(ah));
             unsigned long long sum;
             if (mode == kRowP)
-                sum = slice_sum<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+                sum = slice_sum<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, bits, lane);
             else if (mode == kRowUnit)
-                sum = slice_sum<T, E, kRowUnit>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+                sum = slice_sum<T, E, kRowUnit>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, bits, lane);
             else
-                sum = slice_sum<T, E, kRowScaled>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, unit, lane);
+                sum = slice_sum<T, E, kRowScaled>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, bits, lane);
             if (lane == 0)
                 sh->warp_sum[warp] = sum;
             __syncthreads();
@@ -392,13 +425,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             for (int r = 0; r < ranks; ++r)
                 total += sh->total[parity][r];
             parity ^= 1;
-            smaller = total < kSmallSum && unit < kFixedOne * 1e45;  // (fp32 ends at 1.4e-45)
+            smaller = total < kSmallSum && bits < kFixedBits + 150;  // (fp32 ends at 2^-149)
             if (smaller) {
-                unit *= total ? 1048576.0 : 1125899906842624.0;  // 2^20, 2^50
+                bits += total ? 20 : 50;
                 continue;
             }
             if (tid == 0) {
-                sh->s = static_cast<double>(total) / unit;
+                sh->s = static_cast<double>(total) * scalbn(1.0, -bits);
                 sh->summed = true;
             }
         }
@@ -421,7 +454,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
 
     const int n = sh->n;
     if (rank == 0) {
-        for (int i = tid; i <= T1; i += kVerifyThreads) {
+        if (i <= T1) {
             const int at = i < n ? sh->path[i] : -1;
             if (i < T1)
                 p.accepted[s * T1 + i] = at;
@@ -433,10 +466,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     }
     if (total == 0)
         return;
-    const double x = static_cast<double>(sh->u[T1]) * static_cast<double>(total);
-    unsigned long long t = x > 0 ? static_cast<unsigned long long>(__double2ull_rd(x)) : 0ull;
-    if (t >= total)
-        t = total - 1;
+    // t = floor(u total): u as a fraction of 64 bits
+    u = sh->u[T1];
+    unsigned long long t = u >= 1.f ? total - 1 : (u > 0.f ? __umul64hi(total, fixed(u, 64)) : 0ull);
     int owner = 0;
     parity ^= 1;
     // (bounded: entries that are no probabilities may have made the sums wrap)
@@ -447,15 +479,45 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     int w = 0;
     while (w < kVerifyWarps - 1 && t >= sh->warp_sum[w])
         t -= sh->warp_sum[w++];
-    if (warp != w)
+    // the slice of warp w that holds it, shared by all warps, then the part that does
+    const int begin = (rank * kVerifyWarps + w) * p.slice, end = min(begin + p.slice, V);
+    const int part = (p.slice / kVerifyWarps + 31) / 32 * 32;
+    const int plo = min(begin + warp * part, end), phi = min(plo + part, end);
+    const int *gone = sh->gone;
+    const int ngone = sh->ngone;
+    unsigned long long sum;
+    if (mode == kRowP)
+        sum = slice_sum<T, E, kRowP>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
+    else if (mode == kRowUnit)
+        sum = slice_sum<T, E, kRowUnit>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
+    else
+        sum = slice_sum<T, E, kRowScaled>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
+    if (lane == 0)
+        sh->part_sum[warp] = sum;
+    __syncthreads();
+    int which = -1, last = 0;
+    for (int k = 0; k < kVerifyWarps && which < 0; ++k) {
+        const unsigned long long x = sh->part_sum[k];
+        if (x)
+            last = k;
+        if (t < x)
+            which = k;
+        else
+            t -= x;
+    }
+    if (which < 0) {  // the parts' sums are rounded apart from the slice's
+        which = last;
+        t = ~0ull;
+    }
+    if (warp != which)
         return;
     int found;
     if (mode == kRowP)
-        found = slice_find<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+        found = slice_find<T, E, kRowP>(prow, qrow, plo, phi, ah, al, gone, ngone, t, bits, lane);
     else if (mode == kRowUnit)
-        found = slice_find<T, E, kRowUnit>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+        found = slice_find<T, E, kRowUnit>(prow, qrow, plo, phi, ah, al, gone, ngone, t, bits, lane);
     else
-        found = slice_find<T, E, kRowScaled>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, t, unit, lane);
+        found = slice_find<T, E, kRowScaled>(prow, qrow, plo, phi, ah, al, gone, ngone, t, bits, lane);
     if (lane == 0)
         p.tokens[s * (T1 + 1) + n] = found;
 }
@@ -478,9 +540,9 @@ cudaError_t launch_verify(VerifyParams p, int dtype, int num_sms, cudaStream_t s
     const void *fn = dtype == PA_F32   ? verify_fn<float>(vec, p.draft != nullptr)
                      : dtype == PA_F16 ? verify_fn<__half>(vec, p.draft != nullptr)
                                        : verify_fn<__nv_bfloat16>(vec, p.draft != nullptr);
-    // enough CTAs for two an SM, while each has entries for its threads
+    // as many CTAs as are resident at once (two an SM), while each has entries for its threads
     int cluster = 1;
-    while (cluster < kVerifyMaxCluster && static_cast<long long>(p.num_seqs) * cluster < 2LL * num_sms &&
+    while (cluster < kVerifyMaxCluster && static_cast<long long>(p.num_seqs) * cluster * 2 <= 2LL * num_sms &&
            p.vocab / (cluster * 2) >= 2 * kVerifyThreads)
         cluster *= 2;
     p.cluster = cluster;
