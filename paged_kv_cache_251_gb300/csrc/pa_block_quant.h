@@ -40,6 +40,7 @@ struct DecodeBqParams {
     uint32_t *err;
     int num_seqs, num_heads, num_kv_heads, block_size, log_block, window, max_blocks, max_len, num_blocks;
     int q_dtype, out_dtype;
+    int by_piece;      // a CTA a (sequence, kv head), none cut between CTAs (set by the launch)
     float scale_log2;  // scale * log2 e
 };
 

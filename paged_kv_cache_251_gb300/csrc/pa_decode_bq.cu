@@ -120,12 +120,15 @@ cudaError_t launch_decode_bq(DecodeBqParams p, int cache_dtype, int head_dim, in
     if (per_sm > kDecodeBqCtas)
         per_sm = kDecodeBqCtas;
     const int most = (num_sms < kDecodeBqSms ? num_sms : kDecodeBqSms) * (per_sm < 1 ? 1 : per_sm);
-    int ctas = decode_bq_ctas(p.num_seqs, p.num_kv_heads, p.max_len);
+    const long long pieces = static_cast<long long>(p.num_seqs) * p.num_kv_heads;
+    const int tokens = 16 * (128 / head_dim);  // of an iteration
+    p.by_piece = pieces <= most && p.max_len <= kByPieceIters * tokens;
+    int ctas = p.by_piece ? static_cast<int>(pieces) : decode_bq_ctas(p.num_seqs, p.num_kv_heads, p.max_len);
     if (ctas > most)
         ctas = most;
     void *args[] = {&p};
     e = launch_dependent(fn, dim3(static_cast<unsigned>(ctas)), dim3(kDecodeBqThreads), args, smem, stream);
-    if (e != cudaSuccess || ctas == 1)
+    if (e != cudaSuccess || p.by_piece || ctas == 1)
         return e;
     return launch_dependent(head_dim == 128 ? reinterpret_cast<const void *>(&join_bq_kernel<128>)
                                             : reinterpret_cast<const void *>(&join_bq_kernel<64>),

@@ -36,7 +36,9 @@
 // warps of the grid; a piece counts kPieceCost iterations more (its start and end).
 // A warp whose cut lies inside a piece leaves a partial (O, max, sum) in shared
 // memory, where the CTA's warps join them; what is cut between CTAs goes to
-// the workspace, two partials a CTA at most, and the merge kernel joins those.
+// the workspace, two partials a CTA at most, and the join kernel joins those.  Where
+// every piece can have a CTA and is short (kByPieceIters), each takes one: nothing is
+// cut between CTAs, nothing counted first and no second kernel.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -50,6 +52,7 @@ namespace pa {
 
 constexpr int kPieceCost = 3;   // iterations that a piece costs beside its own
 constexpr int kMinShare = 8;    // iterations of a warp at least
+constexpr int kByPieceIters = 64;  // (16 a warp)
 constexpr float kMaxSlack = 8;  // log2 by which scores may exceed the running maximum
 constexpr float kPTop = 7;      // weights are at most 2^(kMaxSlack + kPTop): within fp16
 constexpr float kPLow = 2048;   // the low part of a weight is kept times this
@@ -237,75 +240,94 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
     const int hkv = p.num_kv_heads, G = p.num_heads / hkv;
     const int wid = blockIdx.x * kDecodeBqWarps + warp, nwarps = gridDim.x * kDecodeBqWarps;
 
-    // every thread's sequences and the units before them
-    const int per = (p.num_seqs + kDecodeBqThreads - 1) / kDecodeBqThreads;
-    long long mine = 0;
-    for (int k = 0; k < per; ++k) {
-        const int s = tid * per + k;
-        if (s < p.num_seqs) {
-            const int L = p.context_lens[s];
-            if (L > p.max_len && p.err && blockIdx.x == 0)
-                atomicOr(p.err, PA_DEVERR_BAD_LEN);
-            mine += hkv * bq_units<U>(bq_span(p, L));
-        }
-    }
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o)
-            incl += y;
-    }
-    if (lane == 31)
-        warp_units[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kDecodeBqWarps; ++w) {
-        if (w < warp)
-            before += warp_units[w];
-        total += warp_units[w];
-    }
-    prefix[tid] = before + incl - mine;
-    if (tid == 0)
-        prefix[kDecodeBqThreads] = total;
-    __syncthreads();
-
-    long long share = (total + nwarps - 1) / nwarps;
-    if (share < kMinShare + kPieceCost)
-        share = kMinShare + kPieceCost;
-    const long long u0 = wid * share, u1 = u0 + share < total ? u0 + share : total;
     if (lane < 2)
         slots[warp][lane].valid = 0;
-    if (tid == 0)
-        p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
     __syncwarp();
-
-    // the sequence that holds unit u0
-    int seq = 0;
-    long long at = 0;  // the first unit of the sequence
-    const bool works = u0 < total;
-    if (works) {
-        int a = 0, b = kDecodeBqThreads;  // prefix[a] <= u0 < prefix[b]
-        while (b - a > 1) {
-            const int m = (a + b) >> 1;
-            if (prefix[m] <= u0)
-                a = m;
-            else
-                b = m;
-        }
-        seq = a * per;
-        at = prefix[a];
-    }
-    BqSpan sp = bq_span(p, p.context_lens[seq]);
-    long long units = bq_units<U>(sp);
-    while (works && at + hkv * units <= u0) {
-        at += hkv * units;
-        sp = bq_span(p, p.context_lens[++seq]);
+    int seq = 0, head = 0;
+    BqSpan sp;
+    long long units, piece = 0;  // of the piece: its units, its first one
+    long long u0, u1, share;     // the warp's units
+    bool works;
+    if (p.by_piece) {
+        // the CTA's piece, its iterations shared by the warps
+        seq = blockIdx.x / hkv;
+        head = blockIdx.x % hkv;
+        const int L = p.context_lens[seq];
+        if (L > p.max_len && p.err && tid == 0)
+            atomicOr(p.err, PA_DEVERR_BAD_LEN);
+        sp = bq_span(p, L);
         units = bq_units<U>(sp);
+        share = (units - kPieceCost + kDecodeBqWarps - 1) / kDecodeBqWarps;
+        u0 = warp == 0 ? 0 : kPieceCost + warp * share;
+        u1 = min(kPieceCost + (warp + 1) * share, units);
+        works = u0 < units;
+    } else {
+        // every thread's sequences and the units before them
+        const int per = (p.num_seqs + kDecodeBqThreads - 1) / kDecodeBqThreads;
+        long long mine = 0;
+        for (int k = 0; k < per; ++k) {
+            const int s = tid * per + k;
+            if (s < p.num_seqs) {
+                const int L = p.context_lens[s];
+                if (L > p.max_len && p.err && blockIdx.x == 0)
+                    atomicOr(p.err, PA_DEVERR_BAD_LEN);
+                mine += hkv * bq_units<U>(bq_span(p, L));
+            }
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += y;
+        }
+        if (lane == 31)
+            warp_units[warp] = incl;
+        __syncthreads();
+        long long before = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kDecodeBqWarps; ++w) {
+            if (w < warp)
+                before += warp_units[w];
+            total += warp_units[w];
+        }
+        prefix[tid] = before + incl - mine;
+        if (tid == 0) {
+            prefix[kDecodeBqThreads] = total;
+            p.records[blockIdx.x] = make_int4(0, 0, 0, 0);
+        }
+        __syncthreads();
+
+        share = (total + nwarps - 1) / nwarps;
+        if (share < kMinShare + kPieceCost)
+            share = kMinShare + kPieceCost;
+        u0 = wid * share;
+        u1 = u0 + share < total ? u0 + share : total;
+        works = u0 < total;
+        // the sequence that holds unit u0
+        long long at = 0;  // the first unit of the sequence
+        if (works) {
+            int a = 0, b = kDecodeBqThreads;  // prefix[a] <= u0 < prefix[b]
+            while (b - a > 1) {
+                const int m = (a + b) >> 1;
+                if (prefix[m] <= u0)
+                    a = m;
+                else
+                    b = m;
+            }
+            seq = a * per;
+            at = prefix[a];
+        }
+        sp = bq_span(p, p.context_lens[seq]);
+        units = bq_units<U>(sp);
+        while (works && at + hkv * units <= u0) {
+            at += hkv * units;
+            sp = bq_span(p, p.context_lens[++seq]);
+            units = bq_units<U>(sp);
+        }
+        head = works ? static_cast<int>((u0 - at) / units) : 0;
+        piece = at + head * units;
     }
-    int head = works ? static_cast<int>((u0 - at) / units) : 0;
-    long long piece = at + head * units;  // first unit of the piece
 
     while (works) {
         // this warp's iterations of the piece

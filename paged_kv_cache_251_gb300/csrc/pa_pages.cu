@@ -27,13 +27,13 @@ namespace {
 
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
+static_assert(kPageWarps == 32, "block_scan: a lane a warp's sum");
 constexpr int kPageCluster = 8;
 constexpr int kCopied = 1 << 31;
 
 struct PagesShared {
     int warp[kPageWarps];
-    int tile;                      // of block_scan
-    long long total[2][kPageCluster];  // every CTA's counts
+    long long total[3][kPageCluster];  // every CTA's counts
 };
 
 // Exclusive prefix of `x` over the CTA's threads; *all gets the sum.
@@ -109,6 +109,7 @@ __device__ inline Row row_of(const PagesUpdateParams &p, int i) {
 __device__ inline void count_entries(const PagesUpdateParams &p, int row, int j0, int j1, int by, int lane) {
     const int32_t *t = p.tables + static_cast<long long>(row) * p.max_blocks;
     bool bad = false;
+#pragma unroll 4
     for (int j = j0 + lane; j < j1; j += 32) {
         const int b = t[j];
         if (b >= 0 && b < p.num_blocks)
@@ -120,6 +121,31 @@ __device__ inline void count_entries(const PagesUpdateParams &p, int row, int j0
         atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
 }
 
+// Four consecutive counts, those from `end` on as `none`.
+__device__ inline void load_counts(const int32_t *from, int b, int end, int none, int *c) {
+    if (b + 4 <= end && (reinterpret_cast<uintptr_t>(from + b) & 15u) == 0) {
+        const int4 x = __ldcg(reinterpret_cast<const int4 *>(from + b));
+        c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            c[k] = b + k < end ? __ldcg(from + b + k) : none;
+    }
+}
+
+constexpr int kTile = 4 * kPageThreads;  // counts of a CTA at once
+
+// A CTA's share of the blocks: whole groups of four.
+__device__ inline void block_share(int num_blocks, int rank, int *b0, int *b1) {
+    const long long share = (static_cast<long long>(num_blocks) + 4 * kPageCluster - 1) / (4 * kPageCluster) * 4;
+    *b0 = static_cast<int>(min(rank * share, static_cast<long long>(num_blocks)));
+    *b1 = static_cast<int>(min((rank + 1) * share, static_cast<long long>(num_blocks)));
+}
+
+// Entries of tables a warp writes at once, and loads before it stores.
+constexpr int kSegment = 1024;
+constexpr int kAhead = 8;
+
 __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const PagesUpdateParams p) {
     __shared__ PagesShared shared;
     PagesShared *sh = &shared;
@@ -130,78 +156,70 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
     const int tid = threadIdx.x, lane = tid & 31;
     const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
     const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
+    const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
 
-    // counts to work on, and a clean slate where rows will meet
-    for (int b = gtid; b < p.num_blocks; b += gthreads)
-        p.count[b] = p.refs[b];
-    for (int r = gtid; r < p.old_rows; r += gthreads)
-        p.children[r] = 0;
+    // counts to work on; what the rows keep and get; a clean slate where writers will meet
     for (int i = gtid; i < p.rows; i += gthreads) {
         const Row r = row_of(p, i);
+        p.kept[i] = r.kept;
+        p.total[i] = r.total;
+        p.base[i] = r.last;  // (until it is known)
         if (r.last >= 0) {
             p.first[r.last] = p.rows;
             p.writers[r.last] = 0;
         }
-    }
-    cluster.sync();
-
-    // children of the old rows, writers of the last blocks
-    for (int i = gtid; i < p.rows; i += gthreads) {
-        const Row r = row_of(p, i);
-        if (r.parent >= 0) {
-            atomicAdd(p.children + r.parent, 1);
-            atomicExch(p.child + r.parent, i);  // (of use to an only child)
-        }
-        if (r.last >= 0) {
-            atomicMin(p.first + r.last, i);
-            atomicAdd(p.writers + r.last, 1);
-        }
-        const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
         const int given = p.parents ? p.parents[i] : i;
         if (p.err && given >= p.old_rows)
             atomicOr(p.err, PA_DEVERR_BAD_INDEX);
         if (p.err && p.grow[i] > most)
             atomicOr(p.err, PA_DEVERR_BAD_LEN);
     }
+#pragma unroll 4
+    for (int b = gtid; b < p.num_blocks; b += gthreads)
+        p.count[b] = p.refs[b];
     cluster.sync();
 
-    // references: an old row lets go of its blocks, its children hold what they
-    // keep.  What an only child keeps changes nothing.
-    for (int r = gwarp; r < p.old_rows; r += gwarps) {
-        const int n = blocks_of(held_len(p, r), p.block_size);
-        if (lane == 0 && p.err) {
-            const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
-            if (p.lens[r] < 0 || p.lens[r] > most)
-                atomicOr(p.err, PA_DEVERR_BAD_LEN);
+    // writers of the last blocks
+    for (int i = gtid; i < p.rows; i += gthreads) {
+        const int last = __ldcg(p.base + i);
+        if (last >= 0) {
+            atomicMin(p.first + last, i);
+            atomicAdd(p.writers + last, 1);
         }
-        const int children = __ldcg(p.children + r);
-        const int from = children == 1 ? row_of(p, __ldcg(p.child + r)).kept : 0;
-        count_entries(p, r, from, n, -1, lane);
     }
-    for (int i = gwarp; i < p.rows; i += gwarps) {
-        const Row r = row_of(p, i);
-        if (r.parent >= 0 && __ldcg(p.children + r.parent) > 1)
-            count_entries(p, r.parent, 0, r.kept, 1, lane);
+    // references: an old row lets go of its blocks, a new row holds what it keeps.  What a
+    // row keeps of its own changes nothing.
+    for (int r = gwarp; r < p.rows || r < p.old_rows; r += gwarps) {
+        const int parent = r < p.rows ? (p.parents ? p.parents[r] : r) : -1;
+        const int kept = r < p.rows ? __ldcg(p.kept + r) : 0;
+        if (r < p.old_rows) {
+            const int len = p.lens[r];
+            if (lane == 0 && p.err && (len < 0 || len > most))
+                atomicOr(p.err, PA_DEVERR_BAD_LEN);
+            count_entries(p, r, parent == r ? kept : 0, blocks_of(held_len(p, r), p.block_size), -1, lane);
+        }
+        if (parent != r && parent >= 0 && parent < p.old_rows)
+            count_entries(p, parent, 0, kept, 1, lane);
     }
     cluster.sync();
 
     // what each row needs, and how many blocks are free, a share a CTA
     const int rows_share = (p.rows + kPageCluster - 1) / kPageCluster;
     const int i0 = min(rank * rows_share, p.rows), i1 = min(i0 + rows_share, p.rows);
-    const int share = (p.num_blocks + kPageCluster - 1) / kPageCluster;
-    const int b0 = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(p.num_blocks)));
-    const int b1 = p.num_blocks - b0 < share ? p.num_blocks : b0 + share;
+    int b0, b1, all;
+    block_share(p.num_blocks, rank, &b0, &b1);
     long long needs = 0;
-    int all;
+    int copies = 0;
     for (int at = i0; at < i1; at += kPageThreads) {
         const int i = at + tid;
         int need = 0;
         if (i < i1) {
-            const Row r = row_of(p, i);
+            const int last = __ldcg(p.base + i);
             // a last block stays where all its holders write to it, with the first of them
-            const bool copied = r.last >= 0 && !(__ldcg(p.writers + r.last) == __ldcg(p.count + r.last) &&
-                                                 __ldcg(p.first + r.last) == i);
-            need = r.total - r.kept + copied;
+            const bool copied = last >= 0 && !(__ldcg(p.writers + last) == __ldcg(p.count + last) &&
+                                               __ldcg(p.first + last) == i);
+            need = __ldcg(p.total + i) - __ldcg(p.kept + i) + copied;
+            copies += copied;
             p.need[i] = need | (copied ? kCopied : 0);
         }
         const int before = block_scan(need, sh, &all);
@@ -209,22 +227,23 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
             p.base[i] = static_cast<int>(needs) + before;  // within the CTA's rows
         needs += all;
     }
-    long long spare = 0;
-    {
-        int mine = 0;
-        for (int b = b0 + tid; b < b1; b += kPageThreads)
-            mine += __ldcg(p.count + b) == 0;
-        block_scan(mine, sh, &all);
-        spare = all;
+    int spare = 0;
+    for (int t0 = b0; t0 < b1; t0 += kTile) {
+        int c[4];
+        load_counts(p.count, t0 + 4 * tid, b1, 1, c);
+        spare += (c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0);
     }
+    block_scan(spare, sh, &spare);
+    block_scan(copies, sh, &copies);
     if (tid < kPageCluster) {
         PagesShared *to = cluster.map_shared_rank(sh, tid);
         to->total[0][rank] = needs;
         to->total[1][rank] = spare;
+        to->total[2][rank] = copies;
     }
     cluster.sync();
 
-    long long needed = 0, free = 0, need_before = 0, free_before = 0;
+    long long needed = 0, free = 0, copied_all = 0, need_before = 0, free_before = 0;
     for (int r = 0; r < kPageCluster; ++r) {
         if (r == rank) {
             need_before = needed;
@@ -232,98 +251,93 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         }
         needed += sh->total[0][r];
         free += sh->total[1][r];
+        copied_all += sh->total[2][r];
     }
     const bool done = needed <= free;
+    if (gtid == 0) {
+        p.status[0] = done;
+        p.status[1] = needed > 0x7fffffff ? 0x7fffffff : static_cast<int>(needed);
+        p.status[2] = static_cast<int>(done ? free - needed : free);
+        p.status[3] = done ? static_cast<int>(copied_all) : 0;
+    }
     if (!done) {  // nothing changes
         for (int i = gtid; i < p.rows; i += gthreads) {
-            p.pairs[2 * i] = -1;
-            p.pairs[2 * i + 1] = -1;
-        }
-        if (gtid == 0) {
-            p.status[0] = 0;
-            p.status[1] = needed > 0x7fffffff ? 0x7fffffff : static_cast<int>(needed);
-            p.status[2] = static_cast<int>(free);
-            p.status[3] = 0;
+            p.pairs[2 * static_cast<long long>(i)] = -1;
+            p.pairs[2 * static_cast<long long>(i) + 1] = -1;
         }
         return;
     }
-    // the free blocks in order, as far as they are needed; copied blocks lose a holder
-    if (free_before < needed) {
+    // the free blocks in order, as far as they are needed, and the counts (copied blocks
+    // lose their holder later)
+    {
         long long at = free_before;
-        for (int t0 = b0; t0 < b1; t0 += kPageThreads) {
-            const int b = t0 + tid;
-            const int is = b < b1 && __ldcg(p.count + b) == 0;
-            const long long k = at + block_scan(is, sh, &all);
-            if (is && k < needed)
-                p.free_list[k] = b;
+        for (int t0 = b0; t0 < b1; t0 += kTile) {
+            const int b = t0 + 4 * tid;
+            int c[4], n = 0;
+            load_counts(p.count, b, b1, 1, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                n += c[k] == 0;
+            long long place = at + block_scan(n, sh, &all);
             at += all;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (b + k < b1) {
+                    if (c[k] < 0 && p.err)
+                        atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+                    if (c[k] == 0 && place++ < needed) {
+                        p.free_list[place - 1] = b + k;
+                        c[k] = 1;
+                    }
+                    p.new_refs[b + k] = c[k];
+                }
         }
     }
-    cluster.sync();
-    int copies = 0;
-    for (int at = i0; at < i1; at += kPageThreads) {
-        const int i = at + tid;
-        if (i < i1) {
-            const int need = p.need[i];
-            const int base = static_cast<int>(need_before) + p.base[i];
-            p.base[i] = base;
-            int64_t src = -1, dst = -1;
-            if (need & kCopied) {
-                src = row_of(p, i).last;
-                dst = __ldcg(p.free_list + base);
-                atomicAdd(p.count + src, -1);
-                ++copies;
-            }
-            p.pairs[2 * static_cast<long long>(i)] = src;
-            p.pairs[2 * static_cast<long long>(i) + 1] = dst;
-        }
-    }
-    block_scan(copies, sh, &all);
-    if (tid < kPageCluster)
-        cluster.map_shared_rank(sh, tid)->total[0][rank] = all;
-    for (long long k = gtid; k < needed; k += gthreads)
-        p.count[__ldcg(p.free_list + k)] = 1;
+    // places in the whole list
+    for (int i = i0 + tid; i < i1; i += kPageThreads)
+        p.base[i] += static_cast<int>(need_before);
     cluster.sync();
 
-    for (int b = gtid; b < p.num_blocks; b += gthreads) {
-        const int c = __ldcg(p.count + b);
-        p.new_refs[b] = c;
-        if (c < 0 && p.err)
-            atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+    for (int i = gtid; i < p.rows; i += gthreads) {
+        int64_t src = -1, dst = -1;
+        if (__ldcg(p.need + i) & kCopied) {
+            dst = __ldcg(p.free_list + __ldcg(p.base + i));
+            src = p.tables[static_cast<long long>(p.parents ? p.parents[i] : i) * p.max_blocks + __ldcg(p.kept + i) - 1];
+            atomicAdd(p.new_refs + src, -1);
+        }
+        p.pairs[2 * static_cast<long long>(i)] = src;
+        p.pairs[2 * static_cast<long long>(i) + 1] = dst;
     }
-    constexpr int kSegment = 1024;  // entries of a warp
     const int segments = (p.max_blocks + kSegment - 1) / kSegment;
     for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
         const int i = static_cast<int>(u / segments), j0 = static_cast<int>(u % segments) * kSegment;
         const int j1 = p.max_blocks - j0 < kSegment ? p.max_blocks : j0 + kSegment;
-        const Row r = row_of(p, i);
+        const int parent = p.parents ? p.parents[i] : i;
+        const int kept = __ldcg(p.kept + i), total = __ldcg(p.total + i), base = __ldcg(p.base + i);
         const bool copied = __ldcg(p.need + i) & kCopied;
-        const int base = __ldcg(p.base + i);
-        const int32_t *from = p.tables + static_cast<long long>(r.parent < 0 ? 0 : r.parent) * p.max_blocks;
+        const int32_t *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
         int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
         bool bad = false;
-#pragma unroll 4
-        for (int j = j0 + lane; j < j1; j += 32) {
-            int b = -1;
-            if (j < r.kept) {
-                b = copied && j == r.kept - 1 ? __ldcg(p.free_list + base) : from[j];
-                bad |= b < 0 || b >= p.num_blocks;
-            } else if (j < r.total && base + copied + (j - r.kept) < needed) {
-                b = __ldcg(p.free_list + base + copied + (j - r.kept));
+        for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
+            int b[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int at = j + 32 * k;
+                b[k] = -1;
+                if (at < j1 && at < kept) {
+                    b[k] = copied && at == kept - 1 ? __ldcg(p.free_list + base) : from[at];
+                    bad |= b[k] < 0 || b[k] >= p.num_blocks;
+                } else if (at < j1 && at < total && base + copied + (at - kept) < needed) {
+                    b[k] = __ldcg(p.free_list + base + copied + (at - kept));
+                }
             }
-            to[j] = b;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (j + 32 * k < j1)
+                    to[j + 32 * k] = b[k];
         }
         if (bad && p.err)
             atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
-    }
-    if (gtid == 0) {
-        long long n = 0;
-        for (int r = 0; r < kPageCluster; ++r)
-            n += sh->total[0][r];
-        p.status[0] = 1;
-        p.status[1] = static_cast<int>(needed);
-        p.status[2] = static_cast<int>(free - needed);
-        p.status[3] = static_cast<int>(n);
     }
 }
 
@@ -339,17 +353,19 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     const int tid = threadIdx.x, lane = tid & 31;
     const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
     const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
-    const int share = (p.num_blocks + kPageCluster - 1) / kPageCluster;
-    const int b0 = static_cast<int>(min(static_cast<long long>(rank) * share, static_cast<long long>(p.num_blocks)));
-    const int b1 = p.num_blocks - b0 < share ? p.num_blocks : b0 + share;
-    int all;
+    int b0, b1, all;
+    block_share(p.num_blocks, rank, &b0, &b1);
     {
         int mine = 0;
-        for (int b = b0 + tid; b < b1; b += kPageThreads) {
-            const int c = p.refs[b];
-            mine += c > 0;
-            if (c < 0 && p.err)
-                atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+        for (int t0 = b0; t0 < b1; t0 += kTile) {
+            int c[4];
+            load_counts(p.refs, t0 + 4 * tid, b1, 0, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                mine += c[k] > 0;
+                if (c[k] < 0 && p.err)
+                    atomicOr(p.err, PA_DEVERR_BAD_COUNT);
+            }
         }
         block_scan(mine, sh, &all);
         if (tid < kPageCluster)
@@ -363,22 +379,31 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         used += sh->total[0][r];
     }
     int movers = 0;
-    for (int t0 = b0; t0 < b1; t0 += kPageThreads) {
-        const int b = t0 + tid;
-        const int c = b < b1 ? p.refs[b] : 0;
-        const bool is = c > 0;
-        const long long below = before + block_scan(is, sh, &all);  // used blocks below b
+    for (int t0 = b0; t0 < b1; t0 += kTile) {
+        const int b = t0 + 4 * tid;
+        int c[4], n = 0;
+        load_counts(p.refs, b, b1, 0, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            n += c[k] > 0;
+        long long below = before + block_scan(n, sh, &all);  // used blocks below b + k
         before += all;
-        if (b < b1) {
-            p.new_refs[b] = c;
-            p.remap[b] = b;
-            if (is && b >= used) {
-                const long long k = used - 1 - below;
-                if (k <= p.max_moves)  // (one more: the highest that stays)
-                    p.src_list[k] = b;
-                ++movers;
-            } else if (!is && b < used && b - below < p.max_moves) {
-                p.dst_list[b - below] = b;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (b + k >= b1)
+                continue;
+            p.new_refs[b + k] = c[k];
+            p.remap[b + k] = b + k;
+            if (c[k] > 0) {
+                if (b + k >= used) {
+                    const long long place = used - 1 - below;
+                    if (place <= p.max_moves)  // (one more: the highest that stays)
+                        p.src_list[place] = b + k;
+                    ++movers;
+                }
+                ++below;
+            } else if (b + k < used && b + k - below < p.max_moves) {
+                p.dst_list[b + k - below] = b + k;
             }
         }
     }
@@ -390,6 +415,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     for (int r = 0; r < kPageCluster; ++r)
         total += sh->total[1][r];
     const int moves = total < p.max_moves ? static_cast<int>(total) : p.max_moves;
+#pragma unroll 2
     for (int k = gtid; k < p.max_moves; k += gthreads) {
         int src = -1, dst = -1;
         if (k < moves) {
@@ -403,7 +429,6 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         p.pairs[2 * static_cast<long long>(k) + 1] = dst;
     }
     cluster.sync();
-    constexpr int kSegment = 1024;
     const int segments = (p.max_blocks + kSegment - 1) / kSegment;
     const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
     for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
@@ -416,17 +441,22 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         const int32_t *from = p.tables + static_cast<long long>(i) * p.max_blocks;
         int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
         bool bad = false;
-#pragma unroll 4
-        for (int j = j0 + lane; j < j1; j += 32) {
-            int b = -1;
-            if (j < n) {
-                b = from[j];
-                if (b >= 0 && b < p.num_blocks)
-                    b = __ldcg(p.remap + b);
+        for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
+            int b[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                b[k] = j + 32 * k < j1 && j + 32 * k < n ? from[j + 32 * k] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (b[k] >= 0 && b[k] < p.num_blocks)
+                    b[k] = __ldcg(p.remap + b[k]);
                 else
-                    bad = true;
+                    bad |= j + 32 * k < j1 && j + 32 * k < n;
             }
-            to[j] = b;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (j + 32 * k < j1)
+                    to[j + 32 * k] = b[k];
         }
         if (p.err && (bad || bad_len))
             atomicOr(p.err, (bad ? PA_DEVERR_BAD_BLOCK : 0u) | (bad_len ? PA_DEVERR_BAD_LEN : 0u));

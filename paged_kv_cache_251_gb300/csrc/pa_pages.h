@@ -14,7 +14,7 @@ struct PagesUpdateParams {
     const int32_t *tables, *refs, *lens, *parents, *keep, *grow;
     // workspace
     int32_t *count, *first, *writers, *free_list;  // [num_blocks]
-    int32_t *children, *child;                     // [old_rows]
+    int32_t *kept, *total;                         // [rows]: blocks kept, blocks in all
     int32_t *need;                                 // [rows]; bit 31: the last kept block is copied
     int32_t *base;                                 // [rows]: the row's first place in free_list
     uint32_t *err;

@@ -299,9 +299,9 @@ pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t 
     p.first = p.count + nb;
     p.writers = p.first + nb;
     p.free_list = p.writers + nb;
-    p.children = p.free_list + nb;
-    p.child = p.children + nr;
-    p.need = p.child + nr;
+    p.kept = p.free_list + nb;
+    p.total = p.kept + nr;
+    p.need = p.total + nr;
     p.base = p.need + nr;
     p.err = err_word;
     p.rows = num_rows;
