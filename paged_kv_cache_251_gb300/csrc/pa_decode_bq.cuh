@@ -25,7 +25,8 @@
 // 2^-40 of the row's largest element); fp32 queries as three fp16 terms, the halves'
 // sums added.  For P the halves hold the weight's fp16 value and 2^11 times what that
 // leaves (22 bits together, down to 2^-50 of the largest weight).  Groups of eight
-// heads take two such column sets.  K scales multiply the scores.  V scales multiply
+// heads fill the columns: fp32 queries are then three sets of them, and what fp16 leaves
+// of a weight is a second product (22 bits, down to 2^-32 of the largest).  K scales multiply the scores.  V scales multiply
 // the weights before they are rounded, as a power of two that O is kept in, moved when a
 // scale exceeds it or lies 2^10 below, and a factor of at most 1.
 //
@@ -201,15 +202,16 @@ inline size_t bq_smem(int group, int head_dim) {
            (2 * kBqStages * kBqStage + 2 * bq_part_floats(group, head_dim) * sizeof(float));
 }
 
-template <int D, bool B8, int Fmt, int QT, int NG, int U>
-__global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDecodeBqCtas)
+template <int D, bool B8, int Fmt, int QT, bool Wide, int U>
+__global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecodeBqCtas)
     decode_bq_kernel(const DecodeBqParams p) {
     constexpr int KW = D / 16;       // words of a K row a lane holds: one a k-step of S
     constexpr int KC = D / 64;       // its 16-byte chunks
     constexpr int VW = D / 32;       // words of a V row a lane holds (4 dims each)
     constexpr int MT = D / 16;       // row tiles of O^T
     constexpr int NB = B8 ? 2 : 1;   // blocks of a tile
-    constexpr int QS = QT == 1 ? 1 : 2;  // column sets of queries: (hi, mid), (lo, 0)
+    // column sets of queries; three terms: (hi, mid), (lo, 0), or a set each where the columns are eight heads
+    constexpr int QS = QT == 1 ? 1 : (Wide ? 3 : 2);
     __shared__ long long prefix[kDecodeBqThreads + 1];
     __shared__ long long warp_units[kDecodeBqWarps];
     __shared__ BqSlot slots[kDecodeBqWarps][2];
@@ -343,12 +345,11 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
         }
         if (k0 < k1) {
             // queries as fragments; their power of two
-            uint32_t qf[NG][QS][KW][2];
-            float qs[NG][2];     // of the lane's two columns: scale * log2 e / the power of two
-            float start[NG][4];  // where the scores start
-#pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                const int h = 4 * n + (g & 3);
+            uint32_t qf[QS][KW][2];
+            float qs[2];     // of the lane's two columns: scale * log2 e / the power of two
+            float start[4];  // where the scores start
+            {
+                const int h = Wide ? g : g & 3;
                 float x[KW * 4], top = 0.f;
                 load_query<KW * 4>(p, (out_row + (h < G ? h : 0)) * D + t * (KW * 4), x);
 #pragma unroll
@@ -369,49 +370,49 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                 for (int ks = 0; ks < KW; ++ks)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        float y[2], z[2];
+                        float y[QS][2];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            y[i] = x[ks * 4 + k_dim<Fmt>(b, i)] * up;
-                            z[i] = 0.f;
-                            if (QT == 3) {
-                                const float hi = __half2float(__float2half_rn(y[i]));
-                                const float r = y[i] - hi;
+                            const float z = x[ks * 4 + k_dim<Fmt>(b, i)] * up;
+                            if constexpr (QT == 1) {
+                                y[0][i] = z;
+                            } else {
+                                const float hi = __half2float(__float2half_rn(z)), r = z - hi;
                                 const float mid = __half2float(__float2half_rn(r));
-                                y[i] = g < 4 ? hi : mid;
-                                z[i] = g < 4 ? r - mid : 0.f;
+                                if constexpr (Wide) {
+                                    y[0][i] = hi;
+                                    y[1][i] = mid;
+                                    y[2][i] = r - mid;
+                                } else {
+                                    y[0][i] = g < 4 ? hi : mid;
+                                    y[1][i] = g < 4 ? r - mid : 0.f;
+                                }
                             }
                         }
-                        qf[n][0][ks][b] = pack_half(y[0], y[1]);
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[n][0][ks][b]));
-                        sum += f.x + f.y;
-                        if (QT == 3) {
-                            qf[n][QS - 1][ks][b] = pack_half(z[0], z[1]);
-                            const float2 l = __half22float2(*reinterpret_cast<const __half2 *>(&qf[n][QS - 1][ks][b]));
-                            sum += l.x + l.y;
+#pragma unroll
+                        for (int q = 0; q < QS; ++q) {
+                            qf[q][ks][b] = pack_half(y[q][0], y[q][1]);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[q][ks][b]));
+                            sum += f.x + f.y;
                         }
                     }
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 sum = Fmt == kFmtI8 ? sum * (-128.f / k_unit<Fmt>()) : 0.f;
-                // columns 2t, 2t + 1 are those of lanes g = 2t, 2t + 1 (for heads: modulo 4)
-                qs[n][0] = __shfl_sync(0xffffffffu, down, (2 * (t & 1)) << 2);
-                qs[n][1] = __shfl_sync(0xffffffffu, down, (2 * (t & 1) + 1) << 2);
-                start[n][0] = start[n][2] = __shfl_sync(0xffffffffu, sum, (2 * t) << 2);
-                start[n][1] = start[n][3] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) << 2);
+                // columns 2t, 2t + 1 are those of lanes g = 2t, 2t + 1 (of four heads: modulo 4)
+                const int from = Wide ? 2 * t : 2 * (t & 1);
+                qs[0] = __shfl_sync(0xffffffffu, down, from << 2);
+                qs[1] = __shfl_sync(0xffffffffu, down, (from + 1) << 2);
+                start[0] = start[2] = __shfl_sync(0xffffffffu, sum, (2 * t) << 2);
+                start[1] = start[3] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) << 2);
             }
             // base: the running maximum less kPTop
-            float base[NG][2], l[NG][2], o[NG][MT][4];
+            float base[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, o[MT][4];
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                base[n][0] = base[n][1] = kNoMax;
-                l[n][0] = l[n][1] = 0.f;
+            for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        o[n][i][c] = 0.f;
-            }
+                for (int c = 0; c < 4; ++c)
+                    o[i][c] = 0.f;
 
             // Blocks of the piece, a lane an entry, 32 at a time: those in use, with their
             // scales; the next 32, their scales on the way; and the entries after them.
@@ -451,12 +452,10 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                 v_unit = unit;
                 v_inv = inv;
 #pragma unroll
-                for (int n = 0; n < NG; ++n)
+                for (int i = 0; i < MT; ++i)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            o[n][i][c] *= f;
+                    for (int c = 0; c < 4; ++c)
+                        o[i][c] *= f;
             };
 
             // The copies run two iterations ahead: K of one is started when K of the one two
@@ -532,7 +531,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                 copy_v(k0 + 1, next);
             copy_commit();
             for (int it = k0; it < k1; ++it) {
-                float x[U][NG][4];
+                float x[U][4];
                 bool full[U];
                 copy_wait<3>();  // K of this iteration is there (V, and K and V of the next, may not be)
                 __syncwarp();
@@ -550,25 +549,19 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                         k_pairs<Fmt>(kr[0][ks], a[0], a[2]);
                         k_pairs<Fmt>(kr[1][ks], a[1], a[3]);
 #pragma unroll
-                        for (int n = 0; n < NG; ++n)
-#pragma unroll
-                            for (int q = 0; q < QS; ++q)
-                                mma16(x[u][n], a, qf[n][q][ks][0], qf[n][q][ks][1],
-                                      ks == 0 && q == 0 ? start[n] : x[u][n]);
+                        for (int q = 0; q < QS; ++q)
+                            mma16(x[u], a, qf[q][ks][0], qf[q][ks][1], ks == 0 && q == 0 ? start : x[u]);
                     }
                     const float ks0 = now.ks[u][0], ks1 = now.ks[u][NB - 1];
+                    if (QT == 3 && !Wide) {  // the terms' halves
 #pragma unroll
-                    for (int n = 0; n < NG; ++n) {
-                        if (QT == 3) {  // the terms' halves
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                x[u][n][c] += __shfl_xor_sync(0xffffffffu, x[u][n][c], 2);
-                        }
-                        x[u][n][0] *= ks0 * qs[n][0];
-                        x[u][n][1] *= ks0 * qs[n][1];
-                        x[u][n][2] *= ks1 * qs[n][0];
-                        x[u][n][3] *= ks1 * qs[n][1];
+                        for (int c = 0; c < 4; ++c)
+                            x[u][c] += __shfl_xor_sync(0xffffffffu, x[u][c], 2);
                     }
+                    x[u][0] *= ks0 * qs[0];
+                    x[u][1] *= ks0 * qs[1];
+                    x[u][2] *= ks1 * qs[0];
+                    x[u][3] *= ks1 * qs[1];
                     // tokens outside the context, or of blocks outside the pool
                     const int tok = (sp.b0 << p.log_block) + (it * U + u) * 16;
                     const unsigned ok = now.ok >> (u * NB);
@@ -576,13 +569,10 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                     if (!full[u]) {
                         const bool in0 = inside(tok + g, ok & 1);
                         const bool in1 = inside(tok + g + 8, ok >> (NB - 1) & 1);
-#pragma unroll
-                        for (int n = 0; n < NG; ++n) {
-                            x[u][n][0] = in0 ? x[u][n][0] : -INFINITY;
-                            x[u][n][1] = in0 ? x[u][n][1] : -INFINITY;
-                            x[u][n][2] = in1 ? x[u][n][2] : -INFINITY;
-                            x[u][n][3] = in1 ? x[u][n][3] : -INFINITY;
-                        }
+                        x[u][0] = in0 ? x[u][0] : -INFINITY;
+                        x[u][1] = in0 ? x[u][1] : -INFINITY;
+                        x[u][2] = in1 ? x[u][2] : -INFINITY;
+                        x[u][3] = in1 ? x[u][3] : -INFINITY;
                     }
                 }
                 float top = 0.f;
@@ -598,35 +588,32 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                     copy_k(it + 2);
                 copy_commit();
                 // the running maximum moves only when it is exceeded by kMaxSlack
+                float t0 = x[0][0], t1 = x[0][1];
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    float t0 = x[0][n][0], t1 = x[0][n][1];
+                for (int u = 0; u < U; ++u) {
+                    t0 = fmaxf(t0, fmaxf(x[u][0], x[u][2]));
+                    t1 = fmaxf(t1, fmaxf(x[u][1], x[u][3]));
+                }
+                if (__any_sync(0xffffffffu,
+                               t0 > base[0] + (kMaxSlack + kPTop) || t1 > base[1] + (kMaxSlack + kPTop))) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        t0 = fmaxf(t0, fmaxf(x[u][n][0], x[u][n][2]));
-                        t1 = fmaxf(t1, fmaxf(x[u][n][1], x[u][n][3]));
+                    for (int s = 4; s < 32; s <<= 1) {
+                        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, s));
+                        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, s));
                     }
-                    if (__any_sync(0xffffffffu, t0 > base[n][0] + (kMaxSlack + kPTop) ||
-                                                    t1 > base[n][1] + (kMaxSlack + kPTop))) {
+                    t0 = fmaxf(t0 - kPTop, base[0]);
+                    t1 = fmaxf(t1 - kPTop, base[1]);
+                    const float f0 = ex2(base[0] - t0), f1 = ex2(base[1] - t1);
+                    base[0] = t0;
+                    base[1] = t1;
+                    l[0] *= f0;
+                    l[1] *= f1;
 #pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) {
-                            t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, s));
-                            t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, s));
-                        }
-                        t0 = fmaxf(t0 - kPTop, base[n][0]);
-                        t1 = fmaxf(t1 - kPTop, base[n][1]);
-                        const float f0 = ex2(base[n][0] - t0), f1 = ex2(base[n][1] - t1);
-                        base[n][0] = t0;
-                        base[n][1] = t1;
-                        l[n][0] *= f0;
-                        l[n][1] *= f1;
-#pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            o[n][i][0] *= f0;
-                            o[n][i][1] *= f1;
-                            o[n][i][2] *= f0;
-                            o[n][i][3] *= f1;
-                        }
+                    for (int i = 0; i < MT; ++i) {
+                        o[i][0] *= f0;
+                        o[i][1] *= f1;
+                        o[i][2] *= f0;
+                        o[i][3] *= f1;
                     }
                 }
                 copy_wait<3>();  // V is there
@@ -634,22 +621,28 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const float r0 = now.vs[u][0] * v_inv, r1 = now.vs[u][NB - 1] * v_inv;
-                    uint32_t pf[NG][2];  // weights as the second product's operand: tokens 2t.. and 2t + 8..
-#pragma unroll
-                    for (int n = 0; n < NG; ++n) {
+                    // weights as the second product's operand: tokens 2t.. and 2t + 8..
+                    uint32_t pf[Wide ? 2 : 1][2];
+                    {
                         float e[4];
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            e[c] = ex2(x[u][n][c] - base[n][c & 1]);
-                        l[n][0] += e[0] + e[2];
-                        l[n][1] += e[1] + e[3];
+                            e[c] = ex2(x[u][c] - base[c & 1]);
+                        l[0] += e[0] + e[2];
+                        l[1] += e[1] + e[3];
                         e[0] *= r0, e[1] *= r0, e[2] *= r1, e[3] *= r1;
                         const uint32_t h0 = pack_half(e[0], e[1]), h1 = pack_half(e[2], e[3]);
                         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
                         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
-                        // columns 0 to 3: the weight itself; 4 to 7: kPLow times what fp16 leaves of it
-                        pf[n][0] = transpose8x8(pack_half(fmaf(a.x, take, e[0] * mul), fmaf(a.y, take, e[1] * mul)));
-                        pf[n][1] = transpose8x8(pack_half(fmaf(b.x, take, e[2] * mul), fmaf(b.y, take, e[3] * mul)));
+                        if constexpr (Wide) {  // what fp16 leaves of a weight, as a product of its own
+                            pf[0][0] = transpose8x8(h0);
+                            pf[0][1] = transpose8x8(h1);
+                            pf[1][0] = transpose8x8(pack_half(e[0] - a.x, e[1] - a.y));
+                            pf[1][1] = transpose8x8(pack_half(e[2] - b.x, e[3] - b.y));
+                        } else {  // columns 0 to 3: the weight itself; 4 to 7: kPLow times what fp16 leaves of it
+                            pf[0][0] = transpose8x8(pack_half(fmaf(a.x, take, e[0] * mul), fmaf(a.y, take, e[1] * mul)));
+                            pf[0][1] = transpose8x8(pack_half(fmaf(b.x, take, e[2] * mul), fmaf(b.y, take, e[3] * mul)));
+                        }
                     }
                     uint32_t vr[4][VW];
 #pragma unroll
@@ -674,9 +667,9 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                             uint32_t a[4];
                             v_pairs<Fmt>(vr[0][w], vr[1][w], i, a[0], a[1]);
                             v_pairs<Fmt>(vr[2][w], vr[3][w], i, a[2], a[3]);
-#pragma unroll
-                            for (int n = 0; n < NG; ++n)
-                                mma16(o[n][2 * w + i], a, pf[n][0], pf[n][1], o[n][2 * w + i]);
+                            mma16(o[2 * w + i], a, pf[0][0], pf[0][1], o[2 * w + i]);
+                            if constexpr (Wide)
+                                mma16(o[2 * w + i], a, pf[1][0], pf[1][1], o[2 * w + i]);
                         }
                 }
                 __syncwarp();
@@ -687,31 +680,32 @@ __global__ void __launch_bounds__(kDecodeBqThreads, NG == 2 && QT == 3 ? 2 : kDe
                 next = after;
             }
 
-            // The low parts of the weights join the high ones: the lane gets one head,
-            // dims g * D / 8 .. + D / 8.
+            // Of four heads: the low parts of the weights join the high ones and the lane gets one
+            // head.  Of eight: the lane has two.  Dims g * D / 8 .. + D / 8.
             const bool whole = k0 == 0 && k1 == iters;
-            const int hc = 2 * (t & 1) + (t >> 1);  // the lane's head of each four
 #pragma unroll
-            for (int n = 0; n < NG; ++n) {
-                float lsum[2] = {l[n][0], l[n][1]};
+            for (int s = 4; s < 32; s <<= 1) {
+                l[0] += __shfl_xor_sync(0xffffffffu, l[0], s);
+                l[1] += __shfl_xor_sync(0xffffffffu, l[1], s);
+            }
 #pragma unroll
-                for (int s = 4; s < 32; s <<= 1) {
-                    lsum[0] += __shfl_xor_sync(0xffffffffu, lsum[0], s);
-                    lsum[1] += __shfl_xor_sync(0xffffffffu, lsum[1], s);
-                }
-                const float sum = t < 2 ? lsum[0] : lsum[1];
-                const float top = t < 2 ? base[n][0] : base[n][1];
+            for (int n = 0; n < (Wide ? 2 : 1); ++n) {
+                const int h = Wide ? 2 * t + n : 2 * (t & 1) + (t >> 1);
+                const float sum = (Wide ? n == 0 : t < 2) ? l[0] : l[1];
+                const float top = (Wide ? n == 0 : t < 2) ? base[0] : base[1];
                 float y[D / 8];
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float send = t < 2 ? o[n][i][2 * c + 1] : o[n][i][2 * c];
-                        const float got = __shfl_xor_sync(0xffffffffu, send, 2);
-                        y[2 * i + c] = v_unit * (t < 2 ? fmaf(got, 1.f / kPLow, o[n][i][2 * c])
-                                                       : fmaf(o[n][i][2 * c + 1], 1.f / kPLow, got));
+                        if constexpr (Wide) {
+                            y[2 * i + c] = v_unit * o[i][2 * c + n];
+                        } else {
+                            const float got = __shfl_xor_sync(0xffffffffu, t < 2 ? o[i][2 * c + 1] : o[i][2 * c], 2);
+                            y[2 * i + c] = v_unit * (t < 2 ? fmaf(got, 1.f / kPLow, o[i][2 * c])
+                                                           : fmaf(o[i][2 * c + 1], 1.f / kPLow, got));
+                        }
                     }
-                const int h = 4 * n + hc;
                 if (h >= G)
                     continue;
                 if (whole) {
@@ -810,16 +804,16 @@ template <int D, int Fmt> const void *decode_bq_kernel(bool wide, bool f32, bool
     constexpr int U = 128 / D;
     if (wide) {
         if (f32)
-            return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 3, 2, U>)
-                      : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 3, 2, U>);
-        return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 1, 2, U>)
-                  : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 1, 2, U>);
+            return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 3, true, U>)
+                      : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 3, true, U>);
+        return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 1, true, U>)
+                  : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 1, true, U>);
     }
     if (f32)
-        return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 3, 1, U>)
-                  : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 3, 1, U>);
-    return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 1, 1, U>)
-              : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 1, 1, U>);
+        return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 3, false, U>)
+                  : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 3, false, U>);
+    return b8 ? reinterpret_cast<const void *>(&decode_bq_kernel<D, true, Fmt, 1, false, U>)
+              : reinterpret_cast<const void *>(&decode_bq_kernel<D, false, Fmt, 1, false, U>);
 }
 
 }  // namespace pa
