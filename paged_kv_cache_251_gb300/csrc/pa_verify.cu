@@ -410,12 +410,12 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             if (lane == 0)
                 sh->warp_sum[warp] = sum;
             __syncthreads();
-            if (tid < ranks) {
-                unsigned long long mine = 0;
-                for (int w = 0; w < kVerifyWarps; ++w)
-                    mine += sh->warp_sum[w];
-                VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, tid) : sh;
-                to->total[parity][rank] = mine;
+            if (warp == 0) {
+                const unsigned long long mine = warp_add(lane < kVerifyWarps ? sh->warp_sum[lane] : 0ull);
+                if (lane < ranks) {
+                    VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, lane) : sh;
+                    to->total[parity][rank] = mine;
+                }
             }
             if (ranks > 1)
                 cluster.sync();
@@ -481,33 +481,38 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         t -= sh->warp_sum[w++];
     // the slice of warp w that holds it, shared by all warps, then the part that does
     const int begin = (rank * kVerifyWarps + w) * p.slice, end = min(begin + p.slice, V);
-    const int part = (p.slice / kVerifyWarps + 31) / 32 * 32;
-    const int plo = min(begin + warp * part, end), phi = min(plo + part, end);
+    const bool shared_out = p.slice > 4 * 32 * E;  // (a few vectors a lane: its warp alone is faster)
+    const int part = shared_out ? (p.slice / kVerifyWarps + 31) / 32 * 32 : p.slice;
+    const int plo = shared_out ? min(begin + warp * part, end) : begin, phi = min(plo + part, end);
     const int *gone = sh->gone;
     const int ngone = sh->ngone;
-    unsigned long long sum;
-    if (mode == kRowP)
-        sum = slice_sum<T, E, kRowP>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
-    else if (mode == kRowUnit)
-        sum = slice_sum<T, E, kRowUnit>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
-    else
-        sum = slice_sum<T, E, kRowScaled>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
-    if (lane == 0)
-        sh->part_sum[warp] = sum;
-    __syncthreads();
-    int which = -1, last = 0;
-    for (int k = 0; k < kVerifyWarps && which < 0; ++k) {
-        const unsigned long long x = sh->part_sum[k];
-        if (x)
-            last = k;
-        if (t < x)
-            which = k;
+    int which = 0;
+    if (shared_out) {
+        unsigned long long sum;
+        if (mode == kRowP)
+            sum = slice_sum<T, E, kRowP>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
+        else if (mode == kRowUnit)
+            sum = slice_sum<T, E, kRowUnit>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
         else
-            t -= x;
-    }
-    if (which < 0) {  // the parts' sums are rounded apart from the slice's
-        which = last;
-        t = ~0ull;
+            sum = slice_sum<T, E, kRowScaled>(prow, qrow, plo, phi, ah, al, gone, ngone, bits, lane);
+        if (lane == 0)
+            sh->part_sum[warp] = sum;
+        __syncthreads();
+        int last = 0;
+        which = -1;
+        for (int k = 0; k < kVerifyWarps && which < 0; ++k) {
+            const unsigned long long x = sh->part_sum[k];
+            if (x)
+                last = k;
+            if (t < x)
+                which = k;
+            else
+                t -= x;
+        }
+        if (which < 0) {  // the parts' sums are rounded apart from the slice's
+            which = last;
+            t = ~0ull;
+        }
     }
     if (warp != which)
         return;
