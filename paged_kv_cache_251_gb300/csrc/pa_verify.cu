@@ -14,8 +14,8 @@
 // A drawn token must not hang on how a sum was rounded, so weights are summed to
 // about 46 bits: p - q as fp32 value and error, lanes' sums as pairs of floats (their
 // roundings kept), everything past a lane in 64-bit fixed point (2^-54, in smaller
-// units again where that comes to less than 2^-20).  fp64 arithmetic would be the
-// limit here (its rate is 1/64 of fp32's).
+// units again where that comes to less than 2^-20), the walk's own numbers again as
+// pairs of floats.  fp64 arithmetic would be the limit here.
 //
 // A sequence is a cluster of CTAs, each taking a share of the vocabulary, a warp a
 // contiguous slice of it.  The first CTA gathers what the walk needs (every drafted
@@ -43,6 +43,44 @@ constexpr int kFixedBits = 54;
 // Sums below 2^-20 are taken again in smaller units.
 constexpr unsigned long long kSmallSum = 1ull << 34;
 
+// A number as two floats, hi + lo with |lo| <= ulp(hi) / 2: about 48 bits.  (One thread's fp64
+// instructions took longer than a pass over a row.)
+struct Pair {
+    float hi, lo;
+};
+__device__ inline Pair quick_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+__device__ inline Pair two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ inline Pair add(Pair a, Pair b) {
+    const Pair s = two_sum(a.hi, b.hi);
+    return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ inline Pair mul(Pair a, float b) {
+    const float h = __fmul_rn(a.hi, b);
+    return quick_sum(h, __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -h)));
+}
+__device__ inline Pair negative(Pair a) { return {-a.hi, -a.lo}; }
+__device__ inline bool less(Pair a, Pair b) {
+    const Pair d = add(a, negative(b));
+    return d.hi < 0;
+}
+// x / 2^bits, rounded down to 48 bits.
+__device__ inline Pair pair_of(unsigned long long x, int bits) {
+    if (x == 0)
+        return {0.f, 0.f};
+    const int lead = __clzll(x);
+    x <<= lead;  // the top 48 bits as two of 24
+    const float hi = static_cast<float>(static_cast<uint32_t>(x >> 40));
+    const float lo = static_cast<float>(static_cast<uint32_t>(x >> 16) & 0xffffffu);
+    const int e = 40 - lead - bits;
+    return quick_sum(ldexpf(hi, e), ldexpf(lo, e - 24));
+}
+
 struct VerifyShared {
     // of every drafted token; tok -1: not a token
     float p[kVerifyMaxDraft], q[kVerifyMaxDraft], u[kVerifyMaxDraft + 1];
@@ -52,7 +90,7 @@ struct VerifyShared {
     unsigned long long total[2][kVerifyMaxCluster];  // of every CTA; two passes' (a slow CTA may still read the last)
     unsigned long long warp_sum[kVerifyWarps], part_sum[kVerifyWarps];
     // the walk
-    double a, s;
+    Pair a, s;
     int node, next, n, ngone, need;
     bool summed;  // total[] holds the sum of the present weights
     int path[kVerifyMaxDraft], gone[kVerifyMaxDraft];
@@ -67,10 +105,10 @@ enum { kWalkDone = 0, kWalkSum = 1, kWalkEnd = 2 };
 // of the weights it ends with) or to its end (kWalkDone).
 template <bool HasQ> __device__ int walk(VerifyShared *sh) {
     int node = sh->node, n = sh->n;
-    double a = sh->a, s = sh->s;
+    Pair a = sh->a, s = sh->s;
     int ngone = sh->ngone;
     bool summed = sh->summed;
-    bool tried = HasQ ? a != 0 : ngone != 0;  // a child of the node was rejected
+    bool tried = HasQ ? a.hi != 0 : ngone != 0;  // a child of the node was rejected
     int need = -1;
     int i = sh->next;
     for (; i < sh->drafts; ++i) {
@@ -79,21 +117,21 @@ template <bool HasQ> __device__ int walk(VerifyShared *sh) {
         bool ok = sh->fine[i];
         if (HasQ) {
             if (tried) {
-                const double p = sh->p[i], q = sh->q[i], u = sh->u[i];
-                const double w = __dsub_rn(p, __dmul_rn(a, q));
-                ok = __dmul_rn(__dmul_rn(u, s), q) < (w > 0 ? w : 0.0);
+                const float p = sh->p[i], q = sh->q[i];
+                const Pair w = add(Pair{p, 0.f}, negative(mul(a, q)));
+                ok = w.hi > 0 && less(mul(mul(s, sh->u[i]), q), w);
             }
         } else {
             bool again = false;
-            const double p = sh->p[i];
+            const float p = sh->p[i];
             if (tried) {
                 for (int g = 0; g < ngone; ++g)
                     again |= sh->gone[g] == sh->tok[i];
-                ok = !again && __dmul_rn(sh->u[i], s) < p;
+                ok = !again && less(mul(s, sh->u[i]), Pair{p, 0.f});
             }
             if (!ok && !again) {
                 sh->gone[ngone++] = sh->tok[i];
-                s -= p > 0 ? p : 0.0;
+                s = add(s, Pair{p > 0 ? -p : 0.f, 0.f});
                 summed = false;
             }
         }
@@ -101,12 +139,12 @@ template <bool HasQ> __device__ int walk(VerifyShared *sh) {
         if (ok) {
             sh->path[n++] = i;
             node = i;
-            a = 0;
-            s = 1;
+            a = Pair{0.f, 0.f};
+            s = Pair{1.f, 0.f};
             ngone = 0;
             summed = false;
         } else if (HasQ) {
-            a += s;
+            a = add(a, s);
             summed = false;
             need = kWalkSum;
             ++i;
@@ -366,8 +404,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         }
     }
     if (tid == 0) {
-        sh->a = 0;
-        sh->s = 1;
+        sh->a = Pair{0.f, 0.f};
+        sh->s = Pair{1.f, 0.f};
         sh->node = -1;
         sh->next = sh->n = sh->ngone = 0;
         sh->summed = false;
@@ -395,11 +433,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 bits = kFixedBits;
             const int node = sh->node;
             prow = target + static_cast<long long>(node + 1) * p.target_stride;
-            const double a = sh->a;
-            mode = !HasQ || a == 0 ? kRowP : (a == 1 ? kRowUnit : kRowScaled);
+            ah = sh->a.hi;
+            al = sh->a.lo;
+            mode = !HasQ || ah == 0 ? kRowP : (ah == 1 && al == 0 ? kRowUnit : kRowScaled);
             qrow = mode == kRowP ? nullptr : draft + static_cast<long long>(node + 1) * p.draft_stride;
-            ah = static_cast<float>(a);
-            al = static_cast<float>(a - static_cast<double>(ah));
             unsigned long long sum;
             if (mode == kRowP)
                 sum = slice_sum<T, E, kRowP>(prow, qrow, lo, hi, ah, al, sh->gone, sh->ngone, bits, lane);
@@ -431,7 +468,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 continue;
             }
             if (tid == 0) {
-                sh->s = static_cast<double>(total) * scalbn(1.0, -bits);
+                sh->s = pair_of(total, bits);
                 sh->summed = true;
             }
         }
@@ -439,10 +476,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         if (need == kWalkSum)
             continue;
         // nothing is left of p (p and q alike, up to rounding, or every token rejected): p itself
-        if (total == 0 && (sh->a != 0 || sh->ngone != 0)) {
+        if (total == 0 && (sh->a.hi != 0 || sh->ngone != 0)) {
             __syncthreads();
             if (tid == 0) {
-                sh->a = 0;
+                sh->a = Pair{0.f, 0.f};
                 sh->ngone = 0;
                 sh->need = kWalkEnd;
             }
