@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                 for (int u = 0; u < U; ++u)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        top = fmaxf(top, now.vs[u][b]);
+                        top = fmaxf(top, fabsf(now.vs[u][b]));
                 if (top > v_unit || (top < v_unit * kLowScale && top > 0))
                     set_unit(top);
                 __syncwarp();  // (every lane has read this iteration's K)

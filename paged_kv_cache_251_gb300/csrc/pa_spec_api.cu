@@ -38,6 +38,12 @@ pa_status pages_args(int num_rows, int max_blocks_per_seq, int block_size, int n
     return PA_OK;
 }
 
+// Whether [a, a + n) and [b, b + m) have bytes in common.
+bool overlap(const void *a, long long n, const void *b, long long m) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return n > 0 && m > 0 && x < y + m && y < x + n;
+}
+
 bool int32_aligned(const void *a, const void *b = nullptr, const void *c = nullptr, const void *d = nullptr,
                    const void *e = nullptr) {
     return aligned(a, 4) && aligned(b, 4) && aligned(c, 4) && aligned(d, 4) && aligned(e, 4);
@@ -276,10 +282,11 @@ pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t 
         return fail(PA_ERR_INVALID_ARGUMENT, "an array is not 4-byte aligned");
     if (!aligned(pairs, 8))
         return fail(PA_ERR_INVALID_ARGUMENT, "pairs must be 8-byte aligned");
-    const char *a = reinterpret_cast<const char *>(new_tables), *b = reinterpret_cast<const char *>(tables);
-    const long long row = 4LL * max_blocks_per_seq;
-    if (num_rows > 0 && old_rows > 0 && a < b + old_rows * row && b < a + num_rows * row)
+    const long long row = 4LL * max_blocks_per_seq, counts = 4LL * num_blocks;
+    if (overlap(new_tables, num_rows * row, tables, old_rows * row))
         return fail(PA_ERR_INVALID_ARGUMENT, "new_tables overlaps tables");
+    if (new_ref_counts != ref_counts && overlap(new_ref_counts, counts, ref_counts, counts))
+        return fail(PA_ERR_INVALID_ARGUMENT, "new_ref_counts overlaps ref_counts and is not the same");
     const int rows = num_rows > old_rows ? num_rows : old_rows;
     if (workspace == nullptr || workspace_bytes < pa_pages_workspace_size(rows, num_blocks))
         return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than pa_pages_workspace_size()");
@@ -331,10 +338,10 @@ pa_status pa_pages_compact(int32_t *new_tables, int32_t *new_ref_counts, int32_t
         return fail(PA_ERR_INVALID_ARGUMENT, "an array is not 4-byte aligned");
     if (!aligned(pairs, 8))
         return fail(PA_ERR_INVALID_ARGUMENT, "pairs must be 8-byte aligned");
-    const char *a = reinterpret_cast<const char *>(new_tables), *b = reinterpret_cast<const char *>(tables);
-    const long long bytes = 4LL * max_blocks_per_seq * num_rows;
-    if (a != b && a < b + bytes && b < a + bytes)
-        return fail(PA_ERR_INVALID_ARGUMENT, "new_tables overlaps tables and is not the same");
+    const long long bytes = 4LL * max_blocks_per_seq * num_rows, counts = 4LL * num_blocks;
+    if ((new_tables != tables && overlap(new_tables, bytes, tables, bytes)) ||
+        (new_ref_counts != ref_counts && overlap(new_ref_counts, counts, ref_counts, counts)))
+        return fail(PA_ERR_INVALID_ARGUMENT, "an output overlaps its input and is not the same");
     if (workspace == nullptr || workspace_bytes < pa_pages_workspace_size(num_rows, num_blocks))
         return fail(PA_ERR_WORKSPACE_TOO_SMALL, "workspace smaller than pa_pages_workspace_size()");
     PagesCompactParams p = {};

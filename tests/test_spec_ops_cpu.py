@@ -73,7 +73,7 @@ def test_pages_refusals(lib):
     for bad in (dict(n=-1), dict(o=-1), dict(m=0), dict(bs=0), dict(nb=0), dict(nt=0), dict(nr=0), dict(pr=0),
                 dict(st=0), dict(t=0), dict(r=0), dict(ln=0), dict(k=0), dict(g=0), dict(pa=0, n=5, wsb=1 << 20),
                 dict(pr=0x3004), dict(nt=0x1002), dict(ws=0x10002), dict(t=0x1000), dict(t=0x1010), dict(nt=0x9070),
-                dict(err=0x1)):
+                dict(nr=0x5010), dict(err=0x1)):
         assert call(**bad) == INV, bad
     call = caller(lib.pa_pages_compact, [P] * 8 + [I] * 5 + [P, SZ, P, P],
                   dict(nt=0x1000, nr=0x2000, rm=0x2800, pr=0x3000, st=0x4000, t=0x9000, r=0x5000, ln=0x6000, n=4, m=8,
@@ -81,7 +81,7 @@ def test_pages_refusals(lib):
     assert call(ws=0) == WS and call(wsb=1663) == WS
     for bad in (dict(n=-1), dict(m=0), dict(bs=-1), dict(nb=0), dict(mv=-1), dict(nt=0), dict(nr=0), dict(rm=0),
                 dict(pr=0), dict(st=0), dict(t=0), dict(r=0), dict(ln=0), dict(pr=0x3004), dict(rm=0x2801),
-                dict(nt=0x9010), dict(err=0x3)):
+                dict(nt=0x9010), dict(nr=0x5004), dict(err=0x3)):
         assert call(**bad) == INV, bad
 
 
