@@ -27,6 +27,7 @@
 
 #include "pa_block_quant.h"
 #include "pa_device.cuh"
+#include "pa_f32x2.cuh"
 #include "pa_internal.h"
 #include "pa_quant.cuh"
 
@@ -93,15 +94,23 @@ template <typename T> __device__ inline float peak_value(uint32_t top) {
 // then lose nothing, unless it is below 2^-40 and coded 0 whatever they do.
 template <int Fmt, bool Plain> __device__ inline uint2 code8(const float *f, float scale, float inv) {
     float y[8];
+    if (Plain) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        if (Plain) {
+        for (int e = 0; e < 8; ++e) {
             y[e] = __fdiv_rn(f[e], scale);
             y[e] = y[e] != y[e] ? 0.f : y[e];
-        } else {
-            float q = __fmul_rn(f[e], inv);
-            q = __fmaf_rn(__fmaf_rn(-q, scale, f[e]), inv, q);
-            y[e] = __fmaf_rn(__fmaf_rn(-q, scale, f[e]), inv, q);
+        }
+    } else {
+        const F2 s = f2(-scale, -scale), r = f2(inv, inv);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            const F2 x = f2(f[e], f[e + 1]);
+            F2 q = f2_mul(x, r);
+            q = f2_fma(f2_fma(q, s, x), r, q);
+            q = f2_fma(f2_fma(q, s, x), r, q);
+            const float2 z = f2_get(q);
+            y[e] = z.x;
+            y[e + 1] = z.y;
         }
     }
     uint32_t w[2];

@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include "pa_device.cuh"
+#include "pa_f32x2.cuh"
 #include "pa_host.h"
 #include "pa_internal.h"
 #include "pa_verify.h"
@@ -253,7 +254,7 @@ template <typename T, int E, int Mode>
 __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, int hi, float ah, float al,
                                         const int *gone, int ngone, int bits, int lane) {
     constexpr int kFlight = 16 / E;  // loads in flight of each row
-    float h = 0.f, l = 0.f;
+    F2 h2 = f2(0.f, 0.f), l2 = h2;  // of even and odd entries
     for (int base = lo; base < hi; base += 32 * E * kFlight) {
         Entries<T, E> p[kFlight], q[kFlight];
 #pragma unroll
@@ -266,17 +267,32 @@ __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, in
         if (Mode == kRowP)
             leave_out<T, E>(p, kFlight, base, lane, gone, ngone);
 #pragma unroll
-        for (int j = 0; j < kFlight; ++j)
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const Weight w = entry<T, E, Mode>(p[j].f, q[j].f, k, ah, al);
-                const float s = __fadd_rn(h, w.d);
-                const float b = __fsub_rn(s, h);
-                const float err = __fadd_rn(__fsub_rn(h, __fsub_rn(s, b)), __fsub_rn(w.d, b));
-                h = s;
-                l = __fadd_rn(l, Mode == kRowP ? err : __fadd_rn(err, w.e));
+        for (int k = 0; k < kFlight * E; k += 2) {
+            F2 d, e = f2(0.f, 0.f);
+            const float px = p[k / E].f[k % E], py = p[(k + 1) / E].f[(k + 1) % E];
+            const float qx = Mode == kRowP ? 0.f : q[k / E].f[k % E], qy = Mode == kRowP ? 0.f : q[(k + 1) / E].f[(k + 1) % E];
+            if (Mode == kRowP) {
+                d = f2(fmaxf(px, 0.f), fmaxf(py, 0.f));
+            } else if (Mode == kRowUnit) {  // max(p, q) - q; a NaN of q as a large number
+                const F2 b = f2(fminf(qx, 1e30f), fminf(qy, 1e30f));
+                const F2 a = f2(fmaxf(px, fminf(qx, 1e30f)), fmaxf(py, fminf(qy, 1e30f)));
+                d = f2_sub(a, b);
+                e = f2_sub(f2_sub(a, d), b);
+            } else {
+                const Weight x = weight<false>(px, qx, ah, al), y = weight<false>(py, qy, ah, al);
+                d = f2(x.d, y.d);
+                e = f2(x.e, y.e);
             }
+            // h + d as value and error
+            const F2 s = f2_add(h2, d), b = f2_sub(s, h2);
+            const F2 err = f2_add(f2_sub(h2, f2_sub(s, b)), f2_sub(d, b));
+            h2 = s;
+            l2 = f2_add(l2, Mode == kRowP ? err : f2_add(err, e));
+        }
     }
+    const float2 hs = f2_get(h2), ls = f2_get(l2);
+    const Pair sum = two_sum(hs.x, hs.y);
+    const float h = sum.hi, l = __fadd_rn(sum.lo, __fadd_rn(ls.x, ls.y));
     return warp_add(fixed(h, l, bits));
 }
 
