@@ -83,12 +83,13 @@ __device__ inline Pair pair_of(unsigned long long x, int bits) {
 }
 
 struct VerifyShared {
-    // of every drafted token; tok -1: not a token
-    float p[kVerifyMaxDraft], q[kVerifyMaxDraft], u[kVerifyMaxDraft + 1];
-    int parent[kVerifyMaxDraft], tok[kVerifyMaxDraft];
-    int fine[kVerifyMaxDraft];  // accepted if it is the first of its node's to be tried
+    // of every drafted token: p, q and u, and the token (its bits; -1: not a token); its parent,
+    // twice, plus 1 if it is accepted where it is the first of its node's to be tried
+    float4 given[kVerifyMaxDraft + 1];
+    int parent2[kVerifyMaxDraft];
     int drafts;
-    unsigned long long total[2][kVerifyMaxCluster];  // of every CTA; two passes' (a slow CTA may still read the last)
+    // of every CTA (0 beyond the last); two passes' (a slow CTA may still read the last)
+    __align__(16) unsigned long long total[2][kVerifyMaxCluster];
     unsigned long long warp_sum[kVerifyWarps], part_sum[kVerifyWarps];
     // the walk
     Pair a, s;
@@ -113,25 +114,29 @@ template <bool HasQ> __device__ int walk(VerifyShared *sh) {
     int need = -1;
     int i = sh->next;
     for (; i < sh->drafts; ++i) {
-        if (sh->parent[i] != node || sh->tok[i] < 0)
+        const int parent2 = sh->parent2[i];
+        if (parent2 >> 1 != node)
             continue;
-        bool ok = sh->fine[i];
+        const float4 given = sh->given[i];
+        const int tok = __float_as_int(given.w);
+        if (tok < 0)
+            continue;
+        const float p = given.x, q = given.y, u = given.z;
+        bool ok = parent2 & 1;
         if (HasQ) {
             if (tried) {
-                const float p = sh->p[i], q = sh->q[i];
                 const Pair w = add(Pair{p, 0.f}, negative(mul(a, q)));
-                ok = w.hi > 0 && less(mul(mul(s, sh->u[i]), q), w);
+                ok = w.hi > 0 && less(mul(mul(s, u), q), w);
             }
         } else {
             bool again = false;
-            const float p = sh->p[i];
             if (tried) {
                 for (int g = 0; g < ngone; ++g)
-                    again |= sh->gone[g] == sh->tok[i];
-                ok = !again && less(mul(s, sh->u[i]), Pair{p, 0.f});
+                    again |= sh->gone[g] == tok;
+                ok = !again && less(mul(s, u), Pair{p, 0.f});
             }
             if (!ok && !again) {
-                sh->gone[ngone++] = sh->tok[i];
+                sh->gone[ngone++] = tok;
                 s = add(s, Pair{p > 0 ? -p : 0.f, 0.f});
                 summed = false;
             }
@@ -407,18 +412,15 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     if (rank == 0 && i <= T1) {
         for (int r = 0; r < ranks; ++r) {
             VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, r) : sh;
-            to->u[i] = u;
-            if (i < T1) {
-                to->p[i] = pv;
-                to->q[i] = qv;
-                to->parent[i] = parent;
-                to->tok[i] = tok;
-                to->fine[i] = fine;
-            } else {
+            to->given[i] = make_float4(pv, qv, u, __int_as_float(tok));
+            if (i < T1)
+                to->parent2[i] = parent * 2 + fine;
+            else
                 to->drafts = drafts;
-            }
         }
     }
+    if (tid < 2 * kVerifyMaxCluster)
+        (&sh->total[0][0])[tid] = 0;  // (before any CTA's first sums: the barrier below)
     if (tid == 0) {
         sh->a = Pair{0.f, 0.f};
         sh->s = Pair{1.f, 0.f};
@@ -475,8 +477,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             else
                 __syncthreads();
             total = 0;
-            for (int r = 0; r < ranks; ++r)
-                total += sh->total[parity][r];
+#pragma unroll
+            for (int r = 0; r < kVerifyMaxCluster; r += 2) {
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(&sh->total[parity][r]);
+                total += x.x + x.y;
+            }
             parity ^= 1;
             smaller = total < kSmallSum && bits < kFixedBits + 150;  // (fp32 ends at 2^-149)
             if (smaller) {
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             if (i < T1)
                 p.accepted[s * T1 + i] = at;
             if (i != n || total == 0)
-                p.tokens[s * (T1 + 1) + i] = i < n ? sh->tok[at] : -1;
+                p.tokens[s * (T1 + 1) + i] = i < n ? __float_as_int(sh->given[at].w) : -1;
         }
         if (tid == 0)
             p.accept_lens[s] = n;
@@ -520,7 +525,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     if (total == 0)
         return;
     // t = floor(u total): u as a fraction of 64 bits
-    u = sh->u[T1];
+    u = sh->given[T1].z;
     unsigned long long t = u >= 1.f ? total - 1 : (u > 0.f ? __umul64hi(total, fixed(u, 64)) : 0ull);
     int owner = 0;
     parity ^= 1;
