@@ -15,6 +15,8 @@
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_pages.h"
@@ -28,12 +30,15 @@ namespace {
 constexpr int kPageThreads = 1024;
 constexpr int kPageWarps = kPageThreads / 32;
 static_assert(kPageWarps == 32, "block_scan: a lane a warp's sum");
-constexpr int kPageCluster = 8;
+constexpr int kPageMaxCluster = 16;  // 8 where the GPU holds no cluster of 16
 constexpr int kCopied = 1 << 31;
+constexpr int kRowsHeld = 2048;  // rows whose parents and kept blocks a CTA holds in shared memory
 
 struct PagesShared {
     int warp[kPageWarps];
-    long long total[3][kPageCluster];  // every CTA's counts
+    int sum;                              // of block_sum
+    long long total[3][kPageMaxCluster];  // every CTA's counts
+    int parent[kRowsHeld], kept[kRowsHeld];
 };
 
 // Exclusive prefix of `x` over the CTA's threads; *all gets the sum.
@@ -63,6 +68,13 @@ __device__ inline int block_scan(int x, PagesShared *sh, int *all) {
     __syncthreads();
     *all = sh->warp[kPageWarps - 1];
     return incl - x + (warp ? sh->warp[warp - 1] : 0);
+}
+
+// Sum of `x` over the CTA's threads, added to sh->sum (zero before; read after a barrier).
+__device__ inline void block_sum(int x, PagesShared *sh) {
+    x = __reduce_add_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0 && x)
+        atomicAdd(&sh->sum, x);
 }
 
 __device__ inline int blocks_of(long long tokens, int block_size) {
@@ -136,8 +148,8 @@ __device__ inline void load_counts(const int32_t *from, int b, int end, int none
 constexpr int kTile = 4 * kPageThreads;  // counts of a CTA at once
 
 // A CTA's share of the blocks: whole groups of four.
-__device__ inline void block_share(int num_blocks, int rank, int *b0, int *b1) {
-    const long long share = (static_cast<long long>(num_blocks) + 4 * kPageCluster - 1) / (4 * kPageCluster) * 4;
+__device__ inline void block_share(int num_blocks, int rank, int ranks, int *b0, int *b1) {
+    const long long share = (static_cast<long long>(num_blocks) + 4 * ranks - 1) / (4 * ranks) * 4;
     *b0 = static_cast<int>(min(rank * share, static_cast<long long>(num_blocks)));
     *b1 = static_cast<int>(min((rank + 1) * share, static_cast<long long>(num_blocks)));
 }
@@ -146,20 +158,43 @@ __device__ inline void block_share(int num_blocks, int rank, int *b0, int *b1) {
 constexpr int kSegment = 1024;
 constexpr int kAhead = 8;
 
+// The children of an old row (a warp): how many, and how many blocks all of them keep.
+struct Children {
+    int count, kept;  // kept 0 without any
+};
+__device__ inline Children children_of(const PagesUpdateParams &p, const PagesShared *sh, int row, int lane) {
+    int n = 0, least = 0x7fffffff;
+    for (int i = lane; i < p.rows; i += 32)
+        if (sh->parent[i] == row) {
+            ++n;
+            least = min(least, sh->kept[i]);
+        }
+    n = __reduce_add_sync(0xffffffffu, n);
+    least = __reduce_min_sync(0xffffffffu, least);
+    return {n, n ? least : 0};
+}
+
 __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const PagesUpdateParams p) {
     __shared__ PagesShared shared;
     PagesShared *sh = &shared;
     pdl_launch_dependents();
     pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
+    const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
     const int tid = threadIdx.x, lane = tid & 31;
-    const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
+    const int gtid = rank * kPageThreads + tid, gthreads = ranks * kPageThreads;
     const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
     const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    const int rows_share = (p.rows + ranks - 1) / ranks;
+    const int i0 = min(rank * rows_share, p.rows), i1 = min(i0 + rows_share, p.rows);
+    int b0, b1, all;
+    block_share(p.num_blocks, rank, ranks, &b0, &b1);
+    const bool one_tile = b1 - b0 <= kTile;
 
     // counts to work on; what the rows keep and get; a clean slate where writers will meet
-    for (int i = gtid; i < p.rows; i += gthreads) {
+    int c[4];
+    load_counts(p.refs, b0 + 4 * tid, b1, 0, c);
+    for (int i = i0 + tid; i < i1; i += kPageThreads) {
         const Row r = row_of(p, i);
         p.kept[i] = r.kept;
         p.total[i] = r.total;
@@ -174,40 +209,62 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         if (p.err && p.grow[i] > most)
             atomicOr(p.err, PA_DEVERR_BAD_LEN);
     }
-#pragma unroll 4
-    for (int b = gtid; b < p.num_blocks; b += gthreads)
-        p.count[b] = p.refs[b];
+    for (int t0 = b0; t0 < b1; t0 += kTile) {
+        const int b = t0 + 4 * tid;
+        if (t0 != b0)
+            load_counts(p.refs, b, b1, 0, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (b + k < b1)
+                p.count[b + k] = c[k];
+    }
+    if (tid == 0)
+        sh->sum = 0;
     cluster.sync();
 
     // writers of the last blocks
-    for (int i = gtid; i < p.rows; i += gthreads) {
+    for (int i = i0 + tid; i < i1; i += kPageThreads) {
         const int last = __ldcg(p.base + i);
         if (last >= 0) {
             atomicMin(p.first + last, i);
             atomicAdd(p.writers + last, 1);
         }
     }
-    // references: an old row lets go of its blocks, a new row holds what it keeps.  What a
-    // row keeps of its own changes nothing.
+    // References: an old row lets go of its blocks, a new row holds what it keeps.  What all
+    // children of a row keep is counted once, with their number: nothing for an only child.
+    const bool held = p.rows <= kRowsHeld;
+    if (held) {
+        for (int i = tid; i < p.rows; i += kPageThreads) {
+            const int parent = p.parents ? p.parents[i] : i;
+            sh->parent[i] = parent < p.old_rows ? parent : -1;
+            sh->kept[i] = __ldcg(p.kept + i);
+        }
+        __syncthreads();
+    }
     for (int r = gwarp; r < p.rows || r < p.old_rows; r += gwarps) {
-        const int parent = r < p.rows ? (p.parents ? p.parents[r] : r) : -1;
-        const int kept = r < p.rows ? __ldcg(p.kept + r) : 0;
         if (r < p.old_rows) {
             const int len = p.lens[r];
             if (lane == 0 && p.err && (len < 0 || len > most))
                 atomicOr(p.err, PA_DEVERR_BAD_LEN);
-            count_entries(p, r, parent == r ? kept : 0, blocks_of(held_len(p, r), p.block_size), -1, lane);
+            const int n = blocks_of(held_len(p, r), p.block_size);
+            Children ch = {0, 0};
+            if (held)
+                ch = children_of(p, sh, r, lane);
+            if (ch.count != 1)
+                count_entries(p, r, 0, ch.kept, ch.count - 1, lane);
+            count_entries(p, r, ch.kept, n, -1, lane);
         }
-        if (parent != r && parent >= 0 && parent < p.old_rows)
-            count_entries(p, parent, 0, kept, 1, lane);
+        if (r < p.rows) {
+            const int parent = held ? sh->parent[r] : (p.parents ? p.parents[r] : r);
+            if (parent >= 0 && parent < p.old_rows) {
+                const int from = held ? children_of(p, sh, parent, lane).kept : 0;
+                count_entries(p, parent, from, held ? sh->kept[r] : __ldcg(p.kept + r), 1, lane);
+            }
+        }
     }
     cluster.sync();
 
     // what each row needs, and how many blocks are free, a share a CTA
-    const int rows_share = (p.rows + kPageCluster - 1) / kPageCluster;
-    const int i0 = min(rank * rows_share, p.rows), i1 = min(i0 + rows_share, p.rows);
-    int b0, b1, all;
-    block_share(p.num_blocks, rank, &b0, &b1);
     long long needs = 0;
     int copies = 0;
     for (int at = i0; at < i1; at += kPageThreads) {
@@ -227,24 +284,25 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
             p.base[i] = static_cast<int>(needs) + before;  // within the CTA's rows
         needs += all;
     }
-    int spare = 0;
+    block_sum(copies, sh);
+    long long spare = 0;
+    int place = 0;  // free blocks of the CTA before the thread's four (of its last tile)
     for (int t0 = b0; t0 < b1; t0 += kTile) {
-        int c[4];
         load_counts(p.count, t0 + 4 * tid, b1, 1, c);
-        spare += (c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0);
+        place = block_scan((c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0), sh, &all);
+        spare += all;
     }
-    block_scan(spare, sh, &spare);
-    block_scan(copies, sh, &copies);
-    if (tid < kPageCluster) {
+    __syncthreads();
+    if (tid < ranks) {
         PagesShared *to = cluster.map_shared_rank(sh, tid);
         to->total[0][rank] = needs;
         to->total[1][rank] = spare;
-        to->total[2][rank] = copies;
+        to->total[2][rank] = sh->sum;
     }
     cluster.sync();
 
     long long needed = 0, free = 0, copied_all = 0, need_before = 0, free_before = 0;
-    for (int r = 0; r < kPageCluster; ++r) {
+    for (int r = 0; r < ranks; ++r) {
         if (r == rank) {
             need_before = needed;
             free_before = free;
@@ -273,20 +331,19 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         long long at = free_before;
         for (int t0 = b0; t0 < b1; t0 += kTile) {
             const int b = t0 + 4 * tid;
-            int c[4], n = 0;
-            load_counts(p.count, b, b1, 1, c);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                n += c[k] == 0;
-            long long place = at + block_scan(n, sh, &all);
+            if (!one_tile) {  // (else the counts and places are those of above)
+                load_counts(p.count, b, b1, 1, c);
+                place = block_scan((c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0), sh, &all);
+            }
+            long long k0 = at + place;
             at += all;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (b + k < b1) {
                     if (c[k] < 0 && p.err)
                         atomicOr(p.err, PA_DEVERR_BAD_COUNT);
-                    if (c[k] == 0 && place++ < needed) {
-                        p.free_list[place - 1] = b + k;
+                    if (c[k] == 0 && k0++ < needed) {
+                        p.free_list[k0 - 1] = b + k;
                         c[k] = 1;
                     }
                     p.new_refs[b + k] = c[k];
@@ -349,12 +406,15 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     pdl_launch_dependents();
     pdl_wait();
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = static_cast<int>(cluster.block_rank());
+    const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
     const int tid = threadIdx.x, lane = tid & 31;
-    const int gtid = rank * kPageThreads + tid, gthreads = kPageCluster * kPageThreads;
+    const int gtid = rank * kPageThreads + tid, gthreads = ranks * kPageThreads;
     const int gwarp = gtid >> 5, gwarps = gthreads >> 5;
     int b0, b1, all;
-    block_share(p.num_blocks, rank, &b0, &b1);
+    block_share(p.num_blocks, rank, ranks, &b0, &b1);
+    if (tid == 0)
+        sh->sum = 0;
+    __syncthreads();
     {
         int mine = 0;
         for (int t0 = b0; t0 < b1; t0 += kTile) {
@@ -367,13 +427,16 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
                     atomicOr(p.err, PA_DEVERR_BAD_COUNT);
             }
         }
-        block_scan(mine, sh, &all);
-        if (tid < kPageCluster)
-            cluster.map_shared_rank(sh, tid)->total[0][rank] = all;
+        block_sum(mine, sh);
+        __syncthreads();
+        if (tid < ranks)
+            cluster.map_shared_rank(sh, tid)->total[0][rank] = sh->sum;
     }
     cluster.sync();
+    if (tid == 0)
+        sh->sum = 0;  // (read before the barrier; added to behind a block_scan's)
     long long used = 0, before = 0;
-    for (int r = 0; r < kPageCluster; ++r) {
+    for (int r = 0; r < ranks; ++r) {
         if (r == rank)
             before = used;
         used += sh->total[0][r];
@@ -407,12 +470,13 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
             }
         }
     }
-    block_scan(movers, sh, &all);
-    if (tid < kPageCluster)
-        cluster.map_shared_rank(sh, tid)->total[1][rank] = all;
+    block_sum(movers, sh);
+    __syncthreads();
+    if (tid < ranks)
+        cluster.map_shared_rank(sh, tid)->total[1][rank] = sh->sum;
     cluster.sync();
     long long total = 0;
-    for (int r = 0; r < kPageCluster; ++r)
+    for (int r = 0; r < ranks; ++r)
         total += sh->total[1][r];
     const int moves = total < p.max_moves ? static_cast<int>(total) : p.max_moves;
 #pragma unroll 2
@@ -514,19 +578,40 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPage
     }
 }
 
-cudaError_t launch_cluster(const void *fn, void **args, cudaStream_t stream) {
+// One cluster of 16 CTAs where the device holds one (asked once a device and kernel), else of 8.
+cudaError_t launch_cluster(const void *fn, int which, void **args, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kPageCluster);
     cfg.blockDim = dim3(kPageThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kPageCluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[2][kDevices];  // 0: not asked yet
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    int size = dev < kDevices ? known[which][dev].load(std::memory_order_relaxed) : 8;
+    if (size == 0) {
+        size = 8;
+        int clusters = 0;
+        attr[0].val.clusterDim.x = kPageMaxCluster;
+        cfg.gridDim = dim3(kPageMaxCluster);
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0)
+            size = kPageMaxCluster;
+        else
+            cudaGetLastError();
+        known[which][dev].store(size, std::memory_order_relaxed);
+    }
+    attr[0].val.clusterDim.x = size;
+    cfg.gridDim = dim3(size);
     cfg.numAttrs = 2;
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
@@ -535,12 +620,12 @@ cudaError_t launch_cluster(const void *fn, void **args, cudaStream_t stream) {
 
 cudaError_t launch_pages_update(PagesUpdateParams p, cudaStream_t stream) {
     void *args[] = {&p};
-    return launch_cluster(reinterpret_cast<const void *>(&pages_update_kernel), args, stream);
+    return launch_cluster(reinterpret_cast<const void *>(&pages_update_kernel), 0, args, stream);
 }
 
 cudaError_t launch_pages_compact(PagesCompactParams p, cudaStream_t stream) {
     void *args[] = {&p};
-    return launch_cluster(reinterpret_cast<const void *>(&pages_compact_kernel), args, stream);
+    return launch_cluster(reinterpret_cast<const void *>(&pages_compact_kernel), 1, args, stream);
 }
 
 cudaError_t launch_copy_pages(CopyPagesParams p, int num_sms, cudaStream_t stream) {
