@@ -117,17 +117,26 @@ __device__ inline Row row_of(const PagesUpdateParams &p, int i) {
     return r;
 }
 
+// Entries that a warp loads before it uses the first.
+constexpr int kAhead = 8;
+
 // Adds `by` to the counts of entries [j0, j1) of an old row (a warp).
 __device__ inline void count_entries(const PagesUpdateParams &p, int row, int j0, int j1, int by, int lane) {
     const int32_t *t = p.tables + static_cast<long long>(row) * p.max_blocks;
     bool bad = false;
-#pragma unroll 4
-    for (int j = j0 + lane; j < j1; j += 32) {
-        const int b = t[j];
-        if (b >= 0 && b < p.num_blocks)
-            atomicAdd(p.count + b, by);
-        else
-            bad = true;
+    for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
+        int b[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            b[k] = j + 32 * k < j1 ? t[j + 32 * k] : 0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (j + 32 * k < j1) {
+                if (b[k] >= 0 && b[k] < p.num_blocks)
+                    atomicAdd(p.count + b[k], by);
+                else
+                    bad = true;
+            }
     }
     if (bad && p.err)
         atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
@@ -154,9 +163,13 @@ __device__ inline void block_share(int num_blocks, int rank, int ranks, int *b0,
     *b1 = static_cast<int>(min((rank + 1) * share, static_cast<long long>(num_blocks)));
 }
 
-// Entries of tables a warp writes at once, and loads before it stores.
-constexpr int kSegment = 1024;
-constexpr int kAhead = 8;
+// Parts of a row of tables, a warp each, such that every warp has one.
+__device__ inline int row_part(int max_blocks, int rows, int warps, int *parts) {
+    const int want = max(1, min(warps / max(rows, 1), (max_blocks + 127) / 128));
+    const int part = ((max_blocks + want - 1) / want + 31) / 32 * 32;
+    *parts = (max_blocks + part - 1) / part;
+    return part;
+}
 
 // The children of an old row (a warp): how many, and how many blocks all of them keep.
 struct Children {
@@ -194,6 +207,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
     // counts to work on; what the rows keep and get; a clean slate where writers will meet
     int c[4];
     load_counts(p.refs, b0 + 4 * tid, b1, 0, c);
+    if (tid < 3 * kPageMaxCluster)
+        (&sh->total[0][0])[tid] = 0;
     for (int i = i0 + tid; i < i1; i += kPageThreads) {
         const Row r = row_of(p, i);
         p.kept[i] = r.kept;
@@ -241,30 +256,36 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         }
         __syncthreads();
     }
-    for (int r = gwarp; r < p.rows || r < p.old_rows; r += gwarps) {
+    const int both = max(p.rows, p.old_rows);
+    int parts;
+    const int part = row_part(p.max_blocks, both, gwarps, &parts);
+    for (long long x = gwarp; x < static_cast<long long>(both) * parts; x += gwarps) {
+        const int r = static_cast<int>(x / parts), j0 = static_cast<int>(x % parts) * part, j1 = j0 + part;
         if (r < p.old_rows) {
             const int len = p.lens[r];
-            if (lane == 0 && p.err && (len < 0 || len > most))
+            if (lane == 0 && j0 == 0 && p.err && (len < 0 || len > most))
                 atomicOr(p.err, PA_DEVERR_BAD_LEN);
             const int n = blocks_of(held_len(p, r), p.block_size);
             Children ch = {0, 0};
             if (held)
                 ch = children_of(p, sh, r, lane);
             if (ch.count != 1)
-                count_entries(p, r, 0, ch.kept, ch.count - 1, lane);
-            count_entries(p, r, ch.kept, n, -1, lane);
+                count_entries(p, r, j0, min(ch.kept, j1), ch.count - 1, lane);
+            count_entries(p, r, max(ch.kept, j0), min(n, j1), -1, lane);
         }
         if (r < p.rows) {
             const int parent = held ? sh->parent[r] : (p.parents ? p.parents[r] : r);
             if (parent >= 0 && parent < p.old_rows) {
                 const int from = held ? children_of(p, sh, parent, lane).kept : 0;
-                count_entries(p, parent, from, held ? sh->kept[r] : __ldcg(p.kept + r), 1, lane);
+                const int kept = held ? sh->kept[r] : __ldcg(p.kept + r);
+                count_entries(p, parent, max(from, j0), min(kept, j1), 1, lane);
             }
         }
     }
     cluster.sync();
 
     // what each row needs, and how many blocks are free, a share a CTA
+    load_counts(p.count, b0 + 4 * tid, b1, 1, c);
     long long needs = 0;
     int copies = 0;
     for (int at = i0; at < i1; at += kPageThreads) {
@@ -288,7 +309,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
     long long spare = 0;
     int place = 0;  // free blocks of the CTA before the thread's four (of its last tile)
     for (int t0 = b0; t0 < b1; t0 += kTile) {
-        load_counts(p.count, t0 + 4 * tid, b1, 1, c);
+        if (t0 != b0)
+            load_counts(p.count, t0 + 4 * tid, b1, 1, c);
         place = block_scan((c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0), sh, &all);
         spare += all;
     }
@@ -302,7 +324,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
     cluster.sync();
 
     long long needed = 0, free = 0, copied_all = 0, need_before = 0, free_before = 0;
-    for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+    for (int r = 0; r < kPageMaxCluster; ++r) {  // (zeros beyond the last CTA)
         if (r == rank) {
             need_before = needed;
             free_before = free;
@@ -365,10 +388,10 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         p.pairs[2 * static_cast<long long>(i)] = src;
         p.pairs[2 * static_cast<long long>(i) + 1] = dst;
     }
-    const int segments = (p.max_blocks + kSegment - 1) / kSegment;
-    for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
-        const int i = static_cast<int>(u / segments), j0 = static_cast<int>(u % segments) * kSegment;
-        const int j1 = p.max_blocks - j0 < kSegment ? p.max_blocks : j0 + kSegment;
+    const int out_part = row_part(p.max_blocks, p.rows, gwarps, &parts);
+    for (long long u = gwarp; u < static_cast<long long>(p.rows) * parts; u += gwarps) {
+        const int i = static_cast<int>(u / parts), j0 = static_cast<int>(u % parts) * out_part;
+        const int j1 = min(p.max_blocks, j0 + out_part);
         const int parent = p.parents ? p.parents[i] : i;
         const int kept = __ldcg(p.kept + i), total = __ldcg(p.total + i), base = __ldcg(p.base + i);
         const bool copied = __ldcg(p.need + i) & kCopied;
@@ -414,7 +437,9 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     block_share(p.num_blocks, rank, ranks, &b0, &b1);
     if (tid == 0)
         sh->sum = 0;
-    __syncthreads();
+    if (tid < 2 * kPageMaxCluster)
+        (&sh->total[0][0])[tid] = 0;
+    cluster.sync();  // (before another CTA's count)
     {
         int mine = 0;
         for (int t0 = b0; t0 < b1; t0 += kTile) {
@@ -436,7 +461,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     if (tid == 0)
         sh->sum = 0;  // (read before the barrier; added to behind a block_scan's)
     long long used = 0, before = 0;
-    for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+    for (int r = 0; r < kPageMaxCluster; ++r) {
         if (r == rank)
             before = used;
         used += sh->total[0][r];
@@ -476,7 +502,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         cluster.map_shared_rank(sh, tid)->total[1][rank] = sh->sum;
     cluster.sync();
     long long total = 0;
-    for (int r = 0; r < ranks; ++r)
+#pragma unroll
+    for (int r = 0; r < kPageMaxCluster; ++r)
         total += sh->total[1][r];
     const int moves = total < p.max_moves ? static_cast<int>(total) : p.max_moves;
 #pragma unroll 2
@@ -493,11 +520,12 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         p.pairs[2 * static_cast<long long>(k) + 1] = dst;
     }
     cluster.sync();
-    const int segments = (p.max_blocks + kSegment - 1) / kSegment;
+    int parts;
+    const int part = row_part(p.max_blocks, p.rows, gwarps, &parts);
     const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
-    for (long long u = gwarp; u < static_cast<long long>(p.rows) * segments; u += gwarps) {
-        const int i = static_cast<int>(u / segments), j0 = static_cast<int>(u % segments) * kSegment;
-        const int j1 = p.max_blocks - j0 < kSegment ? p.max_blocks : j0 + kSegment;
+    for (long long u = gwarp; u < static_cast<long long>(p.rows) * parts; u += gwarps) {
+        const int i = static_cast<int>(u / parts), j0 = static_cast<int>(u % parts) * part;
+        const int j1 = min(p.max_blocks, j0 + part);
         int len = p.lens[i];
         const bool bad_len = len < 0 || len > most;
         len = len < 0 ? 0 : (len > most ? static_cast<int>(most) : len);
