@@ -23,6 +23,11 @@
 // rounded quotient from the correctly rounded reciprocal by two residual corrections
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990), where no step can leave the normal range; else the plain one.
+//
+// Measured: 24000 tokens of ragged prompts, 8 kv heads of 128, bf16 to E4M3: 33 us with the
+// map (2 us), 4.6 TB/s (floor 22 us): a CTA's search for its blocks is three dependent
+// reads, its rows a fourth, and 24 warps an SM do not cover them; plain divisions
+// 72 us (with rows read twice).  64 tokens of a decode step: 3.5 us on the GPU.
 #include <cuda_runtime.h>
 
 #include "pa_block_quant.h"

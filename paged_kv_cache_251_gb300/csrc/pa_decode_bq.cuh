@@ -40,6 +40,15 @@
 // the workspace, two partials a CTA at most, and the join kernel joins those.  Where
 // every piece can have a CTA and is short (kByPieceIters), each takes one: nothing is
 // cut between CTAs, nothing counted first and no second kernel.
+//
+// Measured, 64 x 8192 tokens of 32 / 8 heads of 128, bf16 queries (1.07 GB of codes): E4M3
+// 169 us, INT8 170 us, 6.3 TB/s, 93 % of the copy bandwidth (loads alone by the same
+// copies: 6.8); issue slots half busy, tensor pipe 16 %.  Fragment-shaped loads of 64-byte
+// pieces, to registers or shared memory, end at 4.8 TB/s whatever the occupancy.  16
+// warps an SM (128 registers, spills) 5.8 to 5.9 TB/s, three stages 6.0.  Groups of eight
+// heads: 64 sequences of 1024 to 8192 tokens, 32 / 4 heads, 52 us (two sets of
+// duplicated columns: 68).  A short batch is bound by a piece's start (queries, table,
+// scales, first codes: about 3 us in sequence).
 #pragma once
 
 #include <cuda_fp16.h>

@@ -12,6 +12,11 @@
 // one cluster of CTAs, its barriers between the passes (a launch a pass would cost
 // more than a pass).  Ordered ranks (which free block is the k-th) are a count a CTA,
 // exchanged through shared memory, and a scan within it.
+//
+// Measured on the GPU, copies included: a step of 256 rows over a pool of 25000 blocks
+// 17 us (four barriers 3, the tables' rows 3, the rest dependent reads of 0.4 us), 32
+// prompts of 8 forked beams 18 to 19 us, a pool of 38000 blocks with 12000 moves of 16 KB,
+// K and V, 111 us (the copies 97, 6.3 TB/s; floor of the whole 91).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
