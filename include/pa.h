@@ -741,7 +741,8 @@ PA_API size_t pa_decode_block_quant_workspace_size(int num_seqs, int num_heads, 
  * References beyond those of the tables (a prompt cache's) are kept.  Table
  * entries outside the pool are carried along, hold nothing and are flagged
  * (PA_DEVERR_BAD_BLOCK).  A count that falls below 0 is flagged
- * (PA_DEVERR_BAD_COUNT).  block_size is any positive number.
+ * (PA_DEVERR_BAD_COUNT).  block_size is any positive number; max_blocks_per_seq is
+ * at most 2^21 - 1, its product with block_size, num_rows and num_blocks 2^30.
  */
 PA_API pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t *pairs, int32_t *status,
                                  const int32_t *tables, const int32_t *ref_counts, const int32_t *lens,

@@ -24,6 +24,8 @@ size_t round16(size_t x) { return (x + 15) & ~static_cast<size_t>(15); }
 // Positions along a context or a vocabulary are 32 bits in the kernels, with room
 // for a tile past the end.
 constexpr long long kMaxTokens = 1LL << 30;
+// What 1024 rows need is summed in 32 bits.
+constexpr int kMaxRowBlocks = (1 << 21) - 1;
 
 // Counts of the pages' lists and tables are 32 bits, rows times blocks 64.
 constexpr int kPagesArrays = 4;  // of num_blocks (and as many of num_rows)
@@ -33,6 +35,8 @@ pa_status pages_args(int num_rows, int max_blocks_per_seq, int block_size, int n
         return fail(PA_ERR_INVALID_ARGUMENT, "num_rows, max_blocks_per_seq, block_size or num_blocks out of range");
     if (static_cast<long long>(max_blocks_per_seq) * block_size > kMaxTokens)
         return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size is above 2^30");
+    if (max_blocks_per_seq > kMaxRowBlocks)
+        return fail(PA_ERR_UNSUPPORTED, "max_blocks_per_seq is above 2^21 - 1");
     if (num_rows > kMaxTokens || num_blocks > kMaxTokens)
         return fail(PA_ERR_UNSUPPORTED, "num_rows or num_blocks is above 2^30");
     return PA_OK;
@@ -128,8 +132,10 @@ pa_status pa_append_kv_block_quant(const void *k, const void *v, const int64_t *
         return fail(PA_ERR_INVALID_ARGUMENT, "k and v must be PA_F32, PA_F16 or PA_BF16");
     if (!code_dtype_ok(cache_dtype))
         return fail(PA_ERR_INVALID_ARGUMENT, "cache_dtype must be PA_I8 or PA_E4M3");
-    if (num_kv_heads > kMaxTokens)
-        return fail(PA_ERR_UNSUPPORTED, "num_kv_heads too large");
+    if (num_kv_heads > kMaxTokens / 2)
+        return fail(PA_ERR_UNSUPPORTED, "num_kv_heads is above 2^29");
+    if (num_tokens > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "num_tokens is above 2^30");
     if (num_tokens == 0)
         return PA_OK;
     if (!k || !v || !slot_mapping || !k_cache || !v_cache || !k_scales || !v_scales)
@@ -330,6 +336,8 @@ pa_status pa_pages_compact(int32_t *new_tables, int32_t *new_ref_counts, int32_t
         return st;
     if (max_moves < 0)
         return fail(PA_ERR_INVALID_ARGUMENT, "max_moves must not be negative");
+    if (max_moves > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "max_moves is above 2^30");
     if (!new_ref_counts || !remap || !status || !ref_counts || (num_rows > 0 && (!new_tables || !tables || !lens)) ||
         (max_moves > 0 && !pairs))
         return fail(PA_ERR_INVALID_ARGUMENT, "null pointer");
@@ -372,6 +380,8 @@ pa_status pa_copy_pages(const int64_t *src_dst_pairs, int num_pairs, void *const
         return fail(PA_ERR_INVALID_ARGUMENT, "num_pairs or num_blocks out of range");
     if (num_pools < 1 || num_pools > kMaxPools)
         return fail(PA_ERR_INVALID_ARGUMENT, "num_pools must be 1 .. 8");
+    if (num_pairs > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "num_pairs is above 2^30");
     if (!pools || !block_bytes)
         return fail(PA_ERR_INVALID_ARGUMENT, "null pointer");
     CopyPagesParams p = {};

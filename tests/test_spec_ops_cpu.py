@@ -40,6 +40,7 @@ def test_append_refusals(lib):
     size.restype, size.argtypes = SZ, [I, I, I]
     assert size(512, 16, 10) == 0 and size(513, 16, 10) == 640 and size(513, 12, 10) == 0 and size(513, 16, 0) == 0
     assert size(600, 32, 1 << 30) == 4 << 35
+    assert call(n=(1 << 30) + 1) == UNS and call(hkv=(1 << 29) + 1) == UNS
 
 
 def test_decode_refusals(lib):
@@ -69,7 +70,7 @@ def test_pages_refusals(lib):
                   dict(nt=0x1000, nr=0x2000, pr=0x3000, st=0x4000, t=0x9000, r=0x5000, ln=0x6000, pa=0x7000, k=0x8000,
                        g=0x8800, n=4, o=4, m=8, bs=16, nb=100, ws=0x10000, wsb=1664, err=None, stream=None))
     assert call(ws=0) == WS and call(wsb=1663) == WS and call(o=5) == WS
-    assert call(m=1 << 27) == UNS
+    assert call(m=1 << 27) == UNS and call(bs=1, m=1 << 21) == UNS  # (needs are summed in 32 bits)
     for bad in (dict(n=-1), dict(o=-1), dict(m=0), dict(bs=0), dict(nb=0), dict(nt=0), dict(nr=0), dict(pr=0),
                 dict(st=0), dict(t=0), dict(r=0), dict(ln=0), dict(k=0), dict(g=0), dict(pa=0, n=5, wsb=1 << 20),
                 dict(pr=0x3004), dict(nt=0x1002), dict(ws=0x10002), dict(t=0x1000), dict(t=0x1010), dict(nt=0x9070),
@@ -79,6 +80,7 @@ def test_pages_refusals(lib):
                   dict(nt=0x1000, nr=0x2000, rm=0x2800, pr=0x3000, st=0x4000, t=0x9000, r=0x5000, ln=0x6000, n=4, m=8,
                        bs=16, nb=100, mv=50, ws=0x10000, wsb=1664, err=None, stream=None))
     assert call(ws=0) == WS and call(wsb=1663) == WS
+    assert call(bs=1, m=1 << 21) == UNS and call(mv=(1 << 30) + 1) == UNS and call(n=(1 << 30) + 1) == UNS
     for bad in (dict(n=-1), dict(m=0), dict(bs=-1), dict(nb=0), dict(mv=-1), dict(nt=0), dict(nr=0), dict(rm=0),
                 dict(pr=0), dict(st=0), dict(t=0), dict(r=0), dict(ln=0), dict(pr=0x3004), dict(rm=0x2801),
                 dict(nt=0x9010), dict(nr=0x5004), dict(err=0x3)):
@@ -94,7 +96,7 @@ def test_copy_pages_refusals(lib):
         return fn(pairs, n, at, size, len(pools) if k is None else k, nb, err, None)
 
     assert call(n=0) == 0
-    assert call(sizes=(1 << 62, 4)) == UNS
+    assert call(sizes=(1 << 62, 4)) == UNS and call(n=(1 << 30) + 1) == UNS
     for bad in (dict(n=-1), dict(nb=0), dict(k=0), dict(k=9), dict(pairs=0), dict(pairs=0x1004), dict(pools=(0x2000, 0)),
                 dict(pools=(0x2002, 0x3000)), dict(sizes=(6, 4)), dict(sizes=(0, 4)), dict(sizes=(-4, 4)), dict(err=0x1)):
         assert call(**bad) == INV, bad
