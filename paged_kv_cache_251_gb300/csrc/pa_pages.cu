@@ -351,6 +351,17 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
             p.pairs[2 * static_cast<long long>(i)] = -1;
             p.pairs[2 * static_cast<long long>(i) + 1] = -1;
         }
+        // (kept entries outside the pool are flagged all the same)
+        if (p.err)
+            for (int i = gwarp; i < p.rows; i += gwarps) {
+                const int parent = p.parents ? p.parents[i] : i, kept = __ldcg(p.kept + i);
+                const int32_t *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
+                bool bad = false;
+                for (int j = lane; j < kept; j += 32)
+                    bad |= from[j] < 0 || from[j] >= p.num_blocks;
+                if (bad)
+                    atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
+            }
         return;
     }
     // the free blocks in order, as far as they are needed, and the counts (copied blocks

@@ -121,6 +121,19 @@ def test_update_blocks_held_elsewhere_are_copied():
     assert got[2] == [[-1, -1]]
 
 
+def test_update_flags_bad_contents_in_a_shortage():
+    """Nothing changes, but the entry outside the pool that a row would have kept is told of."""
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = check_update([[9, 1, -1]], [0, 1, 1, 1], [8], [0], [8], [12], 4, err=err)
+    assert got[3][0] == 1 and err.item() == pa.DEVERR_BAD_BLOCK  # (block 0 is free: it suffices)
+    err.zero_()
+    got = check_update([[9, 1, -1]], [1, 1, 1, 1], [8], [0], [8], [12], 4, err=err)
+    assert got[3] == [0, 1, 0, 0] and err.item() == pa.DEVERR_BAD_BLOCK
+    err.zero_()
+    got = check_update([[3, 1, -1]], [1, 1, 1, 1], [8], [0], [8], [12], 4, err=err)
+    assert got[3] == [0, 1, 0, 0] and err.item() == 0
+
+
 def test_update_bad_contents():
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     check_update([[9, 1, -1], [2, -4, -1]], [0, 1, 1, 0], [6, 5], [0, 1], [6, 5], [6, 5], 4, err=err)
