@@ -680,9 +680,9 @@ PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_
  * same bits on every call (a sequence decoded in another batch may differ in the
  * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
  * to 2^-40 of a row's largest element, fp32 queries to 2^-33, softmax weights to
- * 22 bits (at worst 2^-32 of the largest of their (query head, block)).  What codes
- * and scales hold outside the attended tokens has no influence, E4M3 NaN codes (which
- * no append writes) among it.
+ * 22 bits (at worst 2^-32 of the largest of their (query head, block)); q and
+ * q * scale may be as large as 2^100.  What codes and scales hold outside the
+ * attended tokens has no influence, E4M3 NaN codes (which no append writes) among it.
  * The table holds at most 2^30 tokens a sequence.
  *   workspace   pa_decode_block_quant_workspace_size() bytes, 16-byte aligned
  */

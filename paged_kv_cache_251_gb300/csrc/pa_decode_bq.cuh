@@ -67,7 +67,7 @@ constexpr float kMaxSlack = 8;  // log2 by which scores may exceed the running m
 constexpr float kPTop = 7;      // weights are at most 2^(kMaxSlack + kPTop): within fp16
 constexpr float kPLow = 2048;   // the low part of a weight is kept times this
 constexpr float kLowScale = 1.f / 1024;  // V scales this far below O's unit move it
-constexpr float kNoMax = -1e30f;  // (finite: less it, a score of -inf stays -inf)
+constexpr float kNoMax = -3.4028234e38f;  // (finite: less it, a score of -inf stays -inf)
 
 struct BqSpan {
     int start, end;  // attended tokens

@@ -281,6 +281,29 @@ def test_decode_peaked_and_ramped_scores(group):
         check_decode(q, (kc, vc, ks, vs, tables, lens), out_dtype=torch.float32, scale=1.0)
 
 
+@pytest.mark.parametrize("code", [I8, E4M3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lens", [[40], [5000, 40]])
+def test_decode_scores_far_below_zero(code, dtype, lens):
+    """All scores at or below -1e30: the largest of them, 1e30 above the next, takes all the weight."""
+    kc, vc, ks, vs, tables, _ = cache = paged(torch.Generator().manual_seed(40), lens, 1, 16, 64, code)
+    kc.zero_()
+    kc[:, :, :, 0] = 2
+    ks.fill_(1.0)
+    q = torch.zeros((len(lens), 4, 64))
+    q[:, :, 0] = -1e30
+    best = [n * 2 // 3 for n in lens]
+    for s, at in enumerate(best):
+        kc[int(tables[s, at // 16]), 0, at % 16, 0] = 1
+    out = check_decode_raw(q.to(dtype), cache, scale=1.0)
+    for s, at in enumerate(best):
+        b = int(tables[s, at // 16])
+        want = vc[b, 0, at % 16].double() * vs[b, 0].double()
+        # (the weight is 1 exactly; it and V's scale are rounded to 22 bits, the result to dtype)
+        bound = want.abs() * (2.0 ** -20 + torch.finfo(dtype).eps / 2)
+        assert ((out[s].cpu().double() - want).abs() <= bound).all()
+
+
 def test_decode_small_weights_add_up():
     """8192 tokens 20 powers of two below one: together they weigh 2^-7 of it."""
     kc, vc, ks, vs, tables, lens = paged(torch.Generator().manual_seed(26), [8193], 1, 16, 64, I8)
