@@ -335,9 +335,8 @@ cudaError_t launch_append_bq(AppendBqParams p, int dtype, int cache_dtype, int h
         if (e != cudaSuccess)
             return e;
     }
-    // windows as long as they leave eight CTAs an SM (four: 37 us instead of 35 for a prompt
-    // of 24000 tokens); CTAs share a window's heads
-    // where there are still too few
+    // windows as long as they leave eight CTAs an SM (24000 tokens: 33 us; four or sixteen CTAs
+    // 36 to 37); CTAs share a window's heads where there are still too few
     const int want = 8 * num_sms;
     p.window = 1;
     while (p.window < kBqMaxWindow && p.num_tokens / (p.window * 2) >= want)

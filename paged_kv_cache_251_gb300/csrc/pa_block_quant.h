@@ -21,7 +21,9 @@ struct AppendBqParams {
 };
 
 // Tokens up to which an append finds the tokens of a block by looking at all of
-// them (no workspace).
+// them (no workspace, one kernel less).  bf16, 8 heads of 128, on the GPU, so and with the
+// map: 64 single rows 3.6 and 4.4 us, 256 6.3 and 6.9, 512 10.5 and 9.7, 1024 20.4 and
+// 15.3; a prompt of 512 6.8 and 6.4, of 2048 14.8 and 11.4.
 constexpr int kAppendBqFew = 512;
 
 cudaError_t launch_append_bq(AppendBqParams p, int dtype, int cache_dtype, int head_dim, int num_sms,

@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const CopyPage
     }
 }
 
-// One cluster of 16 CTAs where the device holds one (asked once a device and kernel), else of 8.
+// One cluster of 16 CTAs where the device holds one (asked once a device and kernel), else of 8
+// (a step of 256 rows: 18 us instead of 21).
 cudaError_t launch_cluster(const void *fn, int which, void **args, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kPageThreads);

@@ -546,7 +546,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         t -= sh->warp_sum[w++];
     // the slice of warp w that holds it, shared by all warps, then the part that does
     const int begin = (rank * kVerifyWarps + w) * p.slice, end = min(begin + p.slice, V);
-    const bool shared_out = p.slice > 4 * 32 * E;  // (a few vectors a lane: its warp alone is faster)
+    // (a few vectors a lane: its warp alone is faster.  fp32, shared and not: slices of 256
+    // entries 7.5 and 7.0 us, of 416 10.0 and 9.1, of 1024 8.3 and 8.6, of 2016 15.2 and 18.9,
+    // of 8000 46 and 90)
+    const bool shared_out = p.slice > 4 * 32 * E;
     const int part = shared_out ? (p.slice / kVerifyWarps + 31) / 32 * 32 : p.slice;
     const int plo = shared_out ? min(begin + warp * part, end) : begin, phi = min(plo + part, end);
     const int *gone = sh->gone;
@@ -605,15 +608,20 @@ template <typename T> const void *verify_fn(bool vec, bool has_q) {
 
 cudaError_t launch_verify(VerifyParams p, int dtype, int num_sms, cudaStream_t stream) {
     const int e = 16 / elt_bytes(dtype);
+    // (whole vectors of 16 bytes; else entry by entry: 32 trees over 50257 bf16 entries 18 us,
+    // over 50256 16)
     const bool vec = p.vocab % e == 0 && p.target_stride % e == 0 && p.draft_stride % e == 0 && aligned16(p.target) &&
                      aligned16(p.draft);
     const void *fn = dtype == PA_F32   ? verify_fn<float>(vec, p.draft != nullptr)
                      : dtype == PA_F16 ? verify_fn<__half>(vec, p.draft != nullptr)
                                        : verify_fn<__nv_bfloat16>(vec, p.draft != nullptr);
-    // as many CTAs as are resident at once (two an SM), while each has entries for its threads
+    // As many CTAs as are resident at once (two an SM), while each has eight entries a thread:
+    // 8 and 4 CTAs for a chain of 128000 entries 8.3 and 9.3 us, for 32 chains of 50256 9.2 and
+    // 10.6, for one of 32000 7.0 and 6.8; 4 and 1 for one of 8000 5.7 and 5.2, for 32 of 8000 8.0
+    // and 6.6.  More than are resident: 64 chains of 128000 24 us instead of 15.
     int cluster = 1;
     while (cluster < kVerifyMaxCluster && static_cast<long long>(p.num_seqs) * cluster * 2 <= 2LL * num_sms &&
-           p.vocab / (cluster * 2) >= 2 * kVerifyThreads)
+           p.vocab / (cluster * 2) >= 8 * kVerifyThreads)
         cluster *= 2;
     p.cluster = cluster;
     const int warps = cluster * kVerifyWarps;
