@@ -669,8 +669,9 @@ PA_API pa_status pa_append_kv_block_quant(const void *k, const void *v, const in
                                           pa_dtype dtype, pa_dtype cache_dtype, void *workspace,
                                           size_t workspace_bytes, uint32_t *err_word, pa_stream_t stream);
 
-/* Bytes of workspace pa_append_kv_block_quant needs: 4 for each slot of the pool
- * for calls of more than 512 tokens, else 0 (and for bad arguments). */
+/* Bytes of workspace pa_append_kv_block_quant needs: for calls of more than 512
+ * tokens 4 for each slot of the pool and each block that the call may write, and 4
+ * more; else 0 (and for bad arguments). */
 PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_size, int num_blocks);
 
 /*

@@ -12,18 +12,19 @@ struct AppendBqParams {
     const int64_t *slots;
     uint8_t *k_cache, *v_cache;  // [num_blocks][num_kv_heads][block_size][head_dim]
     float *k_scales, *v_scales;  // [num_blocks][num_kv_heads]
-    int32_t *token_of;           // workspace, [num_blocks * block_size] (many tokens only)
+    // workspace (many tokens only)
+    int32_t *token_of;      // [num_blocks * block_size]
+    int32_t *list, *listed;  // [min(num_tokens, num_blocks)] blocks that the call writes; their number
     uint32_t *err;
     long long pool_slots;
     int num_tokens, num_kv_heads, block_size;
-    int window;      // tokens of a CTA (set by the launch)
-    int unit_split;  // CTAs that share a window's (kv head, K or V) units (set by the launch)
+    int parts;  // (few tokens) warps that share a token's (kv head, K or V) units (set by the launch)
 };
 
 // Tokens up to which an append finds the tokens of a block by looking at all of
-// them (no workspace, one kernel less).  bf16, 8 heads of 128, on the GPU, so and with the
-// map: 64 single rows 3.6 and 4.4 us, 256 6.3 and 6.9, 512 10.5 and 9.7, 1024 20.4 and
-// 15.3; a prompt of 512 6.8 and 6.4, of 2048 14.8 and 11.4.
+// them (no workspace, two kernels less).  bf16, 8 heads of 128, on the GPU, so and with the
+// list: 64 single rows 3.3 and 8.0 us, 256 5.6 and 9.4, 512 10.2 and 11.1, 1024 18.3 and
+// 14.4; a prompt of 512 6.0 and 6.5, of 1024 8.8 and 7.0.
 constexpr int kAppendBqFew = 512;
 
 cudaError_t launch_append_bq(AppendBqParams p, int dtype, int cache_dtype, int head_dim, int num_sms,

@@ -114,7 +114,8 @@ pa_status pa_verify_drafts(int32_t *accept_lens, int32_t *accepted, int32_t *tok
 size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_size, int num_blocks) {
     if (num_tokens <= kAppendBqFew || !block_size_ok(block_size) || num_blocks <= 0)
         return 0;
-    return static_cast<size_t>(num_blocks) * block_size * sizeof(int32_t);
+    const size_t blocks = num_tokens < num_blocks ? num_tokens : num_blocks;
+    return (static_cast<size_t>(num_blocks) * block_size + blocks + 1) * sizeof(int32_t);
 }
 
 pa_status pa_append_kv_block_quant(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache,
@@ -157,7 +158,11 @@ pa_status pa_append_kv_block_quant(const void *k, const void *v, const int64_t *
     p.v_cache = static_cast<uint8_t *>(v_cache);
     p.k_scales = k_scales;
     p.v_scales = v_scales;
-    p.token_of = static_cast<int32_t *>(workspace);
+    if (need > 0) {
+        p.token_of = static_cast<int32_t *>(workspace);
+        p.listed = p.token_of + static_cast<size_t>(num_blocks) * block_size;
+        p.list = p.listed + 1;
+    }
     p.err = err_word;
     p.pool_slots = static_cast<long long>(num_blocks) * block_size;
     p.num_tokens = num_tokens;

@@ -149,9 +149,9 @@ def test_append_workspace_of_any_contents():
     slots[100:200] = -1
     want = speclib.append_block_quant(k, k, slots, *cache)
     for fill in (0, -1, 899, 2**31 - 1, -2**31):
-        ws = torch.full((nb * 16,), fill, dtype=torch.int32, device="cuda")
+        ws = torch.full((nb * 16 + nb + 1,), fill, dtype=torch.int32, device="cuda")
         same_cache(append(k, k, slots, *cache, workspace=ws), want)
-    ws = torch.arange(nb * 16, dtype=torch.int32, device="cuda") % n
+    ws = torch.arange(nb * 17 + 1, dtype=torch.int32, device="cuda") % n
     same_cache(append(k, k, slots, *cache, workspace=ws), want)
 
 

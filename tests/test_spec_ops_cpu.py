@@ -32,14 +32,14 @@ def test_append_refusals(lib):
                        bs=16, nb=10, dt=1, cdt=3, ws=0, wsb=0, err=None, st=None))
     assert call(n=0) == 0
     assert call(d=96) == UNS and call(bs=12) == UNS
-    assert call(n=513) == WS and call(n=513, ws=0x8000, wsb=639) == WS
+    assert call(n=513) == WS and call(n=513, ws=0x8000, wsb=683) == WS
     for bad in (dict(n=-1), dict(hkv=0), dict(nb=0), dict(dt=3), dict(cdt=1), dict(k=0), dict(v=0x2008), dict(sl=0x3004),
                 dict(kc=0x4008), dict(vc=0), dict(ks=0x6002), dict(vs=0), dict(ws=0x8002), dict(err=0x1001)):
         assert call(**bad) == INV, bad
     size = lib.pa_append_kv_block_quant_workspace_size
     size.restype, size.argtypes = SZ, [I, I, I]
-    assert size(512, 16, 10) == 0 and size(513, 16, 10) == 640 and size(513, 12, 10) == 0 and size(513, 16, 0) == 0
-    assert size(600, 32, 1 << 30) == 4 << 35
+    assert size(512, 16, 10) == 0 and size(513, 16, 10) == 684 and size(513, 12, 10) == 0 and size(513, 16, 0) == 0
+    assert size(600, 32, 1 << 30) == (4 << 35) + 4 * 601
     assert call(n=(1 << 30) + 1) == UNS and call(hkv=(1 << 29) + 1) == UNS
 
 
