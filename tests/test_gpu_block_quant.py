@@ -155,6 +155,60 @@ def test_append_workspace_of_any_contents():
     same_cache(append(k, k, slots, *cache, workspace=ws), want)
 
 
+@pytest.mark.parametrize("n,hkv", [(40, 300), (520, 1900)])
+def test_append_more_heads_than_warps(n, hkv):
+    """Units beyond the warps that share them: each head's codes are those of a call with it alone."""
+    gen = torch.Generator().manual_seed(41)
+    nb = 40
+    cache = pool(gen, nb, 1, 16, 64, I8)
+    cache = [x.expand(-1, hkv, *x.shape[2:]).contiguous() for x in cache]
+    k, v = (rows(gen, n, 1, 64, torch.bfloat16).expand(n, hkv, 64).clone() for _ in range(2))
+    some = [0, 1, hkv // 2, hkv - 2, hkv - 1]
+    for h in some:
+        k[:, h], v[:, h] = rows(gen, n, 1, 64, torch.bfloat16)[:, 0], rows(gen, n, 1, 64, torch.bfloat16)[:, 0]
+    slots = torch.randperm(nb * 16, generator=gen)[:n]
+    got = append(k, v, slots, *cache)
+    for part in (some, [2]):
+        sub = [x[:, part].contiguous() for x in cache]
+        same_cache([x[:, part] for x in got],
+                   speclib.append_block_quant(k[:, part].contiguous(), v[:, part].contiguous(), slots, *sub))
+    rest = [h for h in range(hkv) if h not in some]  # (all alike)
+    for x in got:
+        assert (x[:, rest] == x[:, [2]]).all()
+
+
+def test_append_streams_graphs_and_one_workspace_after_another():
+    gen = torch.Generator().manual_seed(42)
+    nb, n = 150, 2000
+    cache = [x.cuda() for x in pool(gen, nb, 3, 32, 128, E4M3)]
+    slots = torch.randperm(nb * 32, generator=gen)[:n]
+    slots[::9] = -1
+    k, v = rows(gen, n, 3, 128, torch.float16), rows(gen, n, 3, 128, torch.float16)
+    want = speclib.append_block_quant(k, v, slots, *[x.cpu() for x in cache])
+    dev = [k.cuda(), v.cuda(), slots.cuda()]
+    ws = pa.append_block_quant_workspace_for(dev[2], cache[0])
+    copies = [[x.clone() for x in cache] for _ in range(4)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    pa.pa_append_kv_block_quant(*dev, *copies[0], workspace=ws)
+    pa.pa_append_kv_block_quant(*dev, *copies[1], stream=side)
+    other = slots.flip(0).contiguous().cuda()  # the workspace holds another call's map
+    pa.pa_append_kv_block_quant(dev[0].flip(0).contiguous(), dev[1].flip(0).contiguous(), other, *copies[2], workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_append_kv_block_quant(*dev, *copies[3], workspace=ws)
+    ws.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    for got in copies:
+        same_cache(got, want)
+    graph.replay()  # the same rows again: scales stay or, where row 0 is among them, are set anew alike
+    torch.cuda.synchronize()
+    again = speclib.append_block_quant(k, v, slots, *[x.cpu() for x in copies[0]])
+    same_cache(copies[3], again)
+
+
 # ---------------------------------------------------------------------------
 # Decode.  Beside half a step of the output's type, an output row's error is bounded
 # by the arithmetic: scores are fp32 sums of d products (relative to sum |q k|: about
