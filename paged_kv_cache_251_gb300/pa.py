@@ -8,6 +8,7 @@ non-OK status.  There is no CPU path: the library must be built
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from pathlib import Path
 
@@ -512,7 +513,7 @@ def _addr(t: torch.Tensor | None):
 
 
 def _ws_bytes(workspace) -> int:
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return 0 if workspace is None else workspace.nbytes
 
 
 def _ws(nbytes: int, device) -> torch.Tensor | None:
@@ -769,8 +770,11 @@ def pa_compact_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, keep: torch.Tens
 def _prob_rows(t: torch.Tensor, name: str, n: int, rows: int) -> int:
     """The row stride, in elements, of [n, rows, vocab] probabilities whose rows are
     a fixed distance apart (a padded vocabulary cut to size, for instance)."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != rows:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[1] != rows:
         raise ValueError(f"{name} must be [{n}, {rows}, vocab]")
+    if t.is_contiguous():
+        return shape[2]
     a, b, c = t.stride()
     v = t.shape[2]
     if rows == 1:
@@ -818,13 +822,14 @@ def pa_verify_drafts(accept_lens: torch.Tensor, accepted: torch.Tensor, tokens: 
 
 def _block_quant_pool(k_cache, v_cache, k_scales, v_scales) -> tuple:
     """(blocks, kv heads, block size, head_dim, code) of a block-scaled cache."""
-    if k_cache.dim() != 4 or k_cache.dtype not in CODE_DTYPE or v_cache.dtype is not k_cache.dtype:
+    shape, code = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or code not in CODE_DTYPE or v_cache.dtype is not code:
         raise TypeError("the caches must be int8 / float8_e4m3fn codes [blocks, H_kv, block_size, head_dim]")
-    nb, hkv, bs, d = k_cache.shape
-    _shapes(v_cache, k_cache.shape, "v_cache", k_scales, (nb, hkv), "k_scales", v_scales, (nb, hkv), "v_scales")
+    per_head = shape[:2]
+    _shapes(v_cache, shape, "v_cache", k_scales, per_head, "k_scales", v_scales, per_head, "v_scales")
     if k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32:
         raise TypeError("k_scales and v_scales must be float32")
-    return nb, hkv, bs, d, CODE_DTYPE[k_cache.dtype]
+    return *shape, CODE_DTYPE[code]
 
 
 def append_block_quant_workspace_for(slot_mapping: torch.Tensor, k_cache: torch.Tensor) -> torch.Tensor | None:
@@ -843,16 +848,18 @@ def pa_append_kv_block_quant(k: torch.Tensor, v: torch.Tensor, slot_mapping: tor
     dev = _dense(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales, workspace, err_word)
     nb, hkv, bs, d, code = _block_quant_pool(k_cache, v_cache, k_scales, v_scales)
     n = slot_mapping.numel()
-    _shapes(k, (n, hkv, d), "k", v, (n, hkv, d), "v")
+    rows = (n, hkv, d)
+    _shapes(k, rows, "k", v, rows, "v")
     if slot_mapping.dtype is not torch.int64:
         raise TypeError("slot_mapping must be int64")
-    if k.dtype is not v.dtype or k.dtype not in DTYPE_CODE:
+    dtype = k.dtype
+    if v.dtype is not dtype or dtype not in DTYPE_CODE:
         raise TypeError("k and v must share one of float32, float16, bfloat16")
     if workspace is None:
         workspace = _own_workspace(stream, append_block_quant_workspace_for, slot_mapping, k_cache)
     _call(_lib.pa_append_kv_block_quant, dev, stream, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n, hkv, d, bs, nb,
-          DTYPE_CODE[k.dtype], code, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+          DTYPE_CODE[dtype], code, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
 
 
 def block_quant_workspace_for(q: torch.Tensor, k_cache: torch.Tensor, max_blocks_per_seq: int) -> torch.Tensor | None:
@@ -870,22 +877,26 @@ def pa_decode_block_quant(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Ten
     """pa_decode over 8-bit codes [blocks, H_kv, block_size, d] with one scale for
     each block and kv head (see include/pa.h)."""
     dev = _dense(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace, err_word)
-    n, h, d = q.shape
+    shape, table = q.shape, block_tables.shape
+    n, h, d = shape
     nb, hkv, bs, d2, code = _block_quant_pool(k_cache, v_cache, k_scales, v_scales)
-    _shapes(out, q.shape, "out", k_cache, (nb, hkv, bs, d), "k_cache", context_lens, (n,), "context_lens")
-    if block_tables.dim() != 2 or block_tables.shape[0] != n:
+    if d2 != d:
+        raise ValueError(f"k_cache has head_dim {d2}, expected {d}")
+    _shapes(out, shape, "out", context_lens, (n,), "context_lens")
+    if len(table) != 2 or table[0] != n:
         raise ValueError("block_tables must be [N, max_blocks_per_seq]")
     _int32(block_tables, "block_tables", context_lens, "context_lens")
-    if q.dtype not in DTYPE_CODE or out.dtype not in DTYPE_CODE:
+    dtype, out_dtype = DTYPE_CODE.get(q.dtype), DTYPE_CODE.get(out.dtype)
+    if dtype is None or out_dtype is None:
         raise TypeError("q and out must be float32, float16 or bfloat16")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if workspace is None:
-        workspace = _own_workspace(stream, block_quant_workspace_for, q, k_cache, block_tables.shape[1])
+        workspace = _own_workspace(stream, block_quant_workspace_for, q, k_cache, table[1])
     _call(_lib.pa_decode_block_quant, dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-          context_lens.data_ptr(), n, h, hkv, d, bs, float(scale), int(window), DTYPE_CODE[q.dtype], code,
-          DTYPE_CODE[out.dtype], block_tables.shape[1], nb, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+          context_lens.data_ptr(), n, h, hkv, d, bs, float(scale), int(window), dtype, code, out_dtype, table[1], nb,
+          _addr(workspace), _ws_bytes(workspace), _addr(err_word))
     return out
 
 
@@ -895,16 +906,19 @@ def pages_workspace_for(tables: torch.Tensor, ref_counts: torch.Tensor, num_rows
     return _ws(int(_lib.pa_pages_workspace_size(max(num_rows, tables.shape[0]), ref_counts.numel())), tables.device)
 
 
-def _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens) -> None:
-    if tables.dim() != 2 or new_tables.dim() != 2 or new_tables.shape[1] != tables.shape[1]:
+def _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens) -> tuple:
+    """(old rows, max_blocks_per_seq, new rows, blocks, pairs)."""
+    old, new, blocks, moves = tables.shape, new_tables.shape, ref_counts.shape, pairs.shape
+    if len(old) != 2 or len(new) != 2 or new[1] != old[1]:
         raise ValueError("tables and new_tables must be [rows, max_blocks_per_seq]")
-    if ref_counts.dim() != 1 or pairs.dim() != 2 or pairs.shape[1] != 2:
+    if len(blocks) != 1 or len(moves) != 2 or moves[1] != 2:
         raise ValueError("ref_counts must be [blocks] and pairs [n, 2]")
-    _shapes(new_ref_counts, ref_counts.shape, "new_ref_counts", status, (4,), "status", lens, (tables.shape[0],), "lens")
+    _shapes(new_ref_counts, blocks, "new_ref_counts", status, (4,), "status", lens, old[:1], "lens")
     _int32(new_tables, "new_tables", new_ref_counts, "new_ref_counts", status, "status", tables, "tables", ref_counts,
            "ref_counts", lens, "lens")
     if pairs.dtype is not torch.int64:
         raise TypeError("pairs must be int64")
+    return *old, new[0], blocks[0], moves[0]
 
 
 def pa_pages_update(new_tables: torch.Tensor, new_ref_counts: torch.Tensor, pairs: torch.Tensor,
@@ -919,16 +933,18 @@ def pa_pages_update(new_tables: torch.Tensor, new_ref_counts: torch.Tensor, pair
     (see include/pa.h)."""
     dev = _dense(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens, keep_lens, grow_lens, parents,
                  workspace, err_word)
-    _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
-    n = new_tables.shape[0]
-    _shapes(pairs, (n, 2), "pairs", keep_lens, (n,), "keep_lens", grow_lens, (n,), "grow_lens", parents, (n,), "parents")
+    old, m, n, nb, moves = _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
+    if moves != n:
+        raise ValueError(f"pairs has shape {tuple(pairs.shape)}, expected {(n, 2)}")
+    rows = (n,)
+    _shapes(keep_lens, rows, "keep_lens", grow_lens, rows, "grow_lens", parents, rows, "parents")
     _int32(keep_lens, "keep_lens", grow_lens, "grow_lens", parents, "parents")
     if workspace is None:
         workspace = _own_workspace(stream, pages_workspace_for, tables, ref_counts, n)
     _call(_lib.pa_pages_update, dev, stream, new_tables.data_ptr(), new_ref_counts.data_ptr(), pairs.data_ptr(),
           status.data_ptr(), tables.data_ptr(), ref_counts.data_ptr(), lens.data_ptr(), _addr(parents),
-          keep_lens.data_ptr(), grow_lens.data_ptr(), n, tables.shape[0], tables.shape[1], int(block_size),
-          ref_counts.numel(), _addr(workspace), _ws_bytes(workspace), _addr(err_word))
+          keep_lens.data_ptr(), grow_lens.data_ptr(), n, old, m, int(block_size), nb, _addr(workspace),
+          _ws_bytes(workspace), _addr(err_word))
     return new_tables
 
 
@@ -940,15 +956,16 @@ def pa_pages_compact(new_tables: torch.Tensor, new_ref_counts: torch.Tensor, rem
     pairs are the copies, for pa_copy_pages, remap every block's place now (see
     include/pa.h)."""
     dev = _dense(new_tables, new_ref_counts, remap, pairs, status, tables, ref_counts, lens, workspace, err_word)
-    _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
-    _shapes(new_tables, tables.shape, "new_tables", remap, ref_counts.shape, "remap")
+    n, m, new_rows, nb, moves = _check_pages(new_tables, new_ref_counts, pairs, status, tables, ref_counts, lens)
+    if new_rows != n:
+        raise ValueError(f"new_tables has shape {tuple(new_tables.shape)}, expected {(n, m)}")
+    _shapes(remap, (nb,), "remap")
     _int32(remap, "remap")
     if workspace is None:
         workspace = _own_workspace(stream, pages_workspace_for, tables, ref_counts)
     _call(_lib.pa_pages_compact, dev, stream, new_tables.data_ptr(), new_ref_counts.data_ptr(), remap.data_ptr(),
           pairs.data_ptr(), status.data_ptr(), tables.data_ptr(), ref_counts.data_ptr(), lens.data_ptr(),
-          tables.shape[0], tables.shape[1], int(block_size), ref_counts.numel(), pairs.shape[0], _addr(workspace),
-          _ws_bytes(workspace), _addr(err_word))
+          n, m, int(block_size), nb, moves, _addr(workspace), _ws_bytes(workspace), _addr(err_word))
     return new_tables
 
 
@@ -956,20 +973,26 @@ def pa_copy_pages(src_dst_pairs: torch.Tensor, pools, err_word: torch.Tensor | N
     """Copy block src onto block dst, in each of up to 8 pools ([blocks, ...],
     of any types), for every pair with src >= 0."""
     dev = _dense(src_dst_pairs, err_word, *pools)
-    if src_dst_pairs.dtype is not torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+    n = src_dst_pairs.shape
+    if src_dst_pairs.dtype is not torch.int64 or len(n) != 2 or n[1] != 2:
         raise TypeError("src_dst_pairs must be int64 [n, 2]")
     k = len(pools)
     if not k:
         raise ValueError("no pool")
     nb = pools[0].shape[0]
+    at, size = [], []
     for t in pools:
         if t.shape[0] != nb:
             raise ValueError("the pools must have the same number of blocks")
-    at = (ctypes.c_void_p * k)(*[t.data_ptr() for t in pools])
-    size = (ctypes.c_longlong * k)(*[t.stride(0) * t.element_size() if nb > 1 else t.numel() * t.element_size()
-                                     for t in pools])
-    _call(_lib.pa_copy_pages, dev, stream, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], at, size, k, nb,
-          _addr(err_word))
+        at.append(t.data_ptr())
+        size.append(t.nbytes // (nb or 1))
+    _call(_lib.pa_copy_pages, dev, stream, src_dst_pairs.data_ptr(), n[0], _array(ctypes.c_void_p, k)(*at),
+          _array(ctypes.c_longlong, k)(*size), k, nb, _addr(err_word))
+
+
+@functools.cache
+def _array(kind, n: int):
+    return kind * n
 
 
 def version() -> tuple[int, int, int]:
