@@ -2,8 +2,9 @@
 // kv head, K and V apart).
 //
 // HBM-bound: a code byte is worth 2 G flops (G query heads a kv head).  What it needs
-// beside the bytes in flight is few instructions a byte: codes go from global
-// memory straight to the registers of mma fragments, no shared memory between.
+// beside the bytes in flight is few instructions a byte: codes go to shared memory by
+// asynchronous copies of whole lines, two iterations ahead, and from there straight to the
+// registers of mma fragments.
 // A warp works alone on a run of 16-token tiles of one (sequence, kv head):
 //
 //   S = K Q^T    m16n8k16, rows = tokens, columns = heads.  The contraction runs over
