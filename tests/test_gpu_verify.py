@@ -91,6 +91,26 @@ def test_siblings_and_repeated_tokens(with_q):
     check(pr)
 
 
+@pytest.mark.parametrize("v,dtype", [(8200, torch.float32), (17001, torch.bfloat16), (40000, torch.float16),
+                                     (40003, torch.float32)])
+@pytest.mark.parametrize("with_q", [True, False])
+@pytest.mark.parametrize("same", [False, True])
+def test_rejections_over_long_rows(v, dtype, with_q, same):
+    """Many sums of a row that several CTAs share; same: where p and q are alike nothing is left of p."""
+    if same and not with_q:
+        pytest.skip("without q nothing is alike")
+    n, t = 3, 9
+    pr = problem(40, n, t, v, True, with_q, dtype)
+    if same:
+        pr["draft"] = pr["target"][:, :t].clone()
+        pr["uniforms"][:, :t] = 1.0  # (every draft rejected)
+    else:
+        pr["uniforms"][:, :t].clamp_(min=0.9, max=1 - 2.0 ** -24)
+    pr["parents"] = torch.tensor([-1, -1, -1, -1, 0, 0, 1, 2, 2], dtype=torch.int32).expand(n, t).contiguous()
+    pr["lens"] = torch.full((n,), t, dtype=torch.int32)
+    check(pr)
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_equal_distributions_keep_everything(dtype):
     pr = problem(5, 6, 5, 999, False, True, dtype)
