@@ -125,7 +125,7 @@ typedef enum {
 #define PA_DEVERR_BAD_INDEX 0x40u /* compact: a kept index outside the sequence, or below its place; the row was not moved.
                                    * verify: a drafted token or parent out of range; the token was left out.
                                    * pages: a parent row out of range; the row starts empty */
-#define PA_DEVERR_BAD_COUNT 0x80u /* pages: a reference count below 0, or below what the tables hold */
+#define PA_DEVERR_BAD_COUNT 0x80u /* pages: a reference count below 0, or 0 for a block that a row holds */
 
 /*
  * Bytes of scratch pa_decode needs for split-context partials (0 when no
@@ -741,8 +741,9 @@ PA_API size_t pa_decode_block_quant_workspace_size(int num_seqs, int num_heads, 
  *                 bytes, 4-byte aligned, of any contents
  * References beyond those of the tables (a prompt cache's) are kept.  Table
  * entries outside the pool are carried along, hold nothing and are flagged
- * (PA_DEVERR_BAD_BLOCK).  A count that falls below 0 is flagged
- * (PA_DEVERR_BAD_COUNT).  block_size is any positive number; max_blocks_per_seq is
+ * (PA_DEVERR_BAD_BLOCK).  Counts are taken as given: a count that falls below 0, and
+ * a block that a row keeps while its count falls to 0 (it goes out as a free one, too),
+ * are flagged (PA_DEVERR_BAD_COUNT), with or without enough free blocks.  block_size is any positive number; max_blocks_per_seq is
  * at most 2^21 - 1, its product with block_size, num_rows and num_blocks 2^30.
  */
 PA_API pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t *pairs, int32_t *status,
@@ -766,7 +767,9 @@ PA_API pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, i
  *                 block in use after them, the moves that would have been needed
  *   workspace     pa_pages_workspace_size(num_rows, num_blocks) bytes, 4-byte
  *                 aligned, of any contents
- * lens, and table entries outside the pool, as pa_pages_update.
+ * lens, and table entries outside the pool, as pa_pages_update.  A count below 0,
+ * or of 0 for a block that a row holds, makes its block a free one and is flagged
+ * (PA_DEVERR_BAD_COUNT).
  */
 PA_API pa_status pa_pages_compact(int32_t *new_tables, int32_t *new_ref_counts, int32_t *remap, int64_t *pairs,
                                   int32_t *status, const int32_t *tables, const int32_t *ref_counts,

@@ -14,7 +14,7 @@
 // exchanged through shared memory, and a scan within it.
 //
 // Measured on the GPU, copies included: a step of 256 rows over a pool of 25000 blocks
-// 17 us (four barriers 3, the tables' rows 3, the rest dependent reads of 0.4 us), 32
+// 16 us (four barriers 3, the tables' rows 3, the rest dependent reads of 0.4 us), 32
 // prompts of 8 forked beams 18 to 19 us, a pool of 38000 blocks with 12000 moves of 16 KB,
 // K and V, 111 us (the copies 97, 6.3 TB/s; floor of the whole 91).
 #include <cooperative_groups.h>
@@ -38,8 +38,8 @@ static_assert(kPageWarps == 32, "block_scan: a lane a warp's sum");
 constexpr int kPageMaxCluster = 16;  // 8 where the GPU holds no cluster of 16
 constexpr int kCopied = 1 << 31;
 // Rows up to which a CTA holds their parents and kept blocks in shared memory, and looks for an old
-// row's children there: a step of 256 rows 13.8 us, else 15.9; of 1024 22.9 and 24.2; of 2048
-// 38.8 and 29.7; 2048 forked beams 36.6 and 27.5.
+// row's children there: a step of 256 rows 13.4 us, else 15.9; of 1024 22.4 and 24.2; of 2048
+// 38.8 and 29.2; 2048 forked beams 36.6 and 26.9.
 constexpr int kRowsHeld = 1024;
 
 struct PagesShared {
@@ -180,6 +180,40 @@ __device__ inline int row_part(int max_blocks, int rows, int warps, int *parts) 
     return part;
 }
 
+// What the entries that rows hold tell of: blocks outside the pool, and blocks that no reference
+// counts, which go out as free ones, too.  row_at(i, &from): how many entries row i holds, and where.
+// The warps of a CTA take rows from the last warp on (in the update the first have needs to find
+// meanwhile).  Only calls with an error word pay for it: an update of 256 rows 0.6 to 1.0 us, of 2048
+// rows 5.0 us.
+template <typename RowAt>
+__device__ inline uint32_t entry_errors(const int32_t *count, int num_blocks, int max_blocks, int rows, int rank,
+                                        int ranks, int warp, int lane, RowAt row_at) {
+    uint32_t bad = 0;
+    int parts;
+    const int warps = ranks * kPageWarps, part = row_part(max_blocks, rows, warps, &parts);
+    const long long items = static_cast<long long>(rows) * parts;
+    for (long long u = rank + ranks * (kPageWarps - 1 - warp); u < items; u += warps) {
+        const int32_t *from;
+        const int j0 = static_cast<int>(u % parts) * part, j1 = min(row_at(static_cast<int>(u / parts), &from), j0 + part);
+        for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
+            int b[kAhead], c[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                b[k] = j + 32 * k < j1 ? from[j + 32 * k] : -1;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const bool inside = b[k] >= 0 && b[k] < num_blocks;
+                bad |= inside || j + 32 * k >= j1 ? 0u : PA_DEVERR_BAD_BLOCK;
+                c[k] = inside ? __ldcg(count + b[k]) : 1;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                bad |= c[k] > 0 ? 0u : PA_DEVERR_BAD_COUNT;
+        }
+    }
+    return bad;
+}
+
 // The children of an old row (a warp): how many, and how many blocks all of them keep.
 struct Children {
     int count, kept;  // kept 0 without any
@@ -295,6 +329,14 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
 
     // what each row needs, and how many blocks are free, a share a CTA
     load_counts(p.count, b0 + 4 * tid, b1, 1, c);
+    uint32_t bad = 0;
+    if (p.err)
+        bad = entry_errors(p.count, p.num_blocks, p.max_blocks, p.rows, rank, ranks, tid >> 5, lane,
+                           [&](int i, const int32_t **from) {
+                               const int kept = __ldcg(p.kept + i), parent = p.parents ? p.parents[i] : i;
+                               *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
+                               return kept;
+                           });
     long long needs = 0;
     int copies = 0;
     for (int at = i0; at < i1; at += kPageThreads) {
@@ -303,8 +345,12 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         if (i < i1) {
             const int last = __ldcg(p.base + i);
             // a last block stays where all its holders write to it, with the first of them
-            const bool copied = last >= 0 && !(__ldcg(p.writers + last) == __ldcg(p.count + last) &&
-                                               __ldcg(p.first + last) == i);
+            bool copied = false;
+            if (last >= 0) {
+                const int writers = __ldcg(p.writers + last), holders = __ldcg(p.count + last);
+                copied = !(writers == holders && __ldcg(p.first + last) == i);
+                bad |= writers > holders ? PA_DEVERR_BAD_COUNT : 0u;
+            }
             need = __ldcg(p.total + i) - __ldcg(p.kept + i) + copied;
             copies += copied;
             p.need[i] = need | (copied ? kCopied : 0);
@@ -322,7 +368,10 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
             load_counts(p.count, t0 + 4 * tid, b1, 1, c);
         place = block_scan((c[0] == 0) + (c[1] == 0) + (c[2] == 0) + (c[3] == 0), sh, &all);
         spare += all;
+        bad |= min(min(c[0], c[1]), min(c[2], c[3])) < 0 ? PA_DEVERR_BAD_COUNT : 0u;
     }
+    if (bad && p.err)
+        atomicOr(p.err, bad);
     __syncthreads();
     if (tid < ranks) {
         PagesShared *to = cluster.map_shared_rank(sh, tid);
@@ -355,17 +404,6 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
             p.pairs[2 * static_cast<long long>(i)] = -1;
             p.pairs[2 * static_cast<long long>(i) + 1] = -1;
         }
-        // (kept entries outside the pool are flagged all the same)
-        if (p.err)
-            for (int i = gwarp; i < p.rows; i += gwarps) {
-                const int parent = p.parents ? p.parents[i] : i, kept = __ldcg(p.kept + i);
-                const int32_t *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
-                bool bad = false;
-                for (int j = lane; j < kept; j += 32)
-                    bad |= from[j] < 0 || from[j] >= p.num_blocks;
-                if (bad)
-                    atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
-            }
         return;
     }
     // the free blocks in order, as far as they are needed, and the counts (copied blocks
@@ -383,8 +421,6 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 if (b + k < b1) {
-                    if (c[k] < 0 && p.err)
-                        atomicOr(p.err, PA_DEVERR_BAD_COUNT);
                     if (c[k] == 0 && k0++ < needed) {
                         p.free_list[k0 - 1] = b + k;
                         c[k] = 1;
@@ -417,28 +453,29 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
         const bool copied = __ldcg(p.need + i) & kCopied;
         const int32_t *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
         int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
-        bool bad = false;
         for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
             int b[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int at = j + 32 * k;
                 b[k] = -1;
-                if (at < j1 && at < kept) {
+                if (at < j1 && at < kept)
                     b[k] = copied && at == kept - 1 ? __ldcg(p.free_list + base) : from[at];
-                    bad |= b[k] < 0 || b[k] >= p.num_blocks;
-                } else if (at < j1 && at < total && base + copied + (at - kept) < needed) {
+                else if (at < j1 && at < total && base + copied + (at - kept) < needed)
                     b[k] = __ldcg(p.free_list + base + copied + (at - kept));
-                }
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (j + 32 * k < j1)
                     to[j + 32 * k] = b[k];
         }
-        if (bad && p.err)
-            atomicOr(p.err, PA_DEVERR_BAD_BLOCK);
     }
+}
+
+__device__ inline int held_len(const PagesCompactParams &p, int row) {
+    const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    const int n = p.lens[row];
+    return n < 0 ? 0 : (n > most ? static_cast<int>(most) : n);
 }
 
 // With U blocks in use, a used block b >= U that has k used blocks above it goes
@@ -459,6 +496,15 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         sh->sum = 0;
     if (tid < 2 * kPageMaxCluster)
         (&sh->total[0][0])[tid] = 0;
+    if (p.err) {  // (before tables and counts change in place)
+        const uint32_t bad = entry_errors(p.refs, p.num_blocks, p.max_blocks, p.rows, rank, ranks, tid >> 5, lane,
+                                          [&](int i, const int32_t **from) {
+                                              *from = p.tables + static_cast<long long>(i) * p.max_blocks;
+                                              return blocks_of(held_len(p, i), p.block_size);
+                                          });
+        if (bad)
+            atomicOr(p.err, bad);
+    }
     cluster.sync();  // (before another CTA's count)
     {
         int mine = 0;
@@ -546,32 +592,25 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     for (long long u = gwarp; u < static_cast<long long>(p.rows) * parts; u += gwarps) {
         const int i = static_cast<int>(u / parts), j0 = static_cast<int>(u % parts) * part;
         const int j1 = min(p.max_blocks, j0 + part);
-        int len = p.lens[i];
-        const bool bad_len = len < 0 || len > most;
-        len = len < 0 ? 0 : (len > most ? static_cast<int>(most) : len);
-        const int n = blocks_of(len, p.block_size);
+        const int len = p.lens[i], n = blocks_of(held_len(p, i), p.block_size);
         const int32_t *from = p.tables + static_cast<long long>(i) * p.max_blocks;
         int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
-        bool bad = false;
         for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
             int b[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 b[k] = j + 32 * k < j1 && j + 32 * k < n ? from[j + 32 * k] : -1;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
+            for (int k = 0; k < kAhead; ++k)
                 if (b[k] >= 0 && b[k] < p.num_blocks)
                     b[k] = __ldcg(p.remap + b[k]);
-                else
-                    bad |= j + 32 * k < j1 && j + 32 * k < n;
-            }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (j + 32 * k < j1)
                     to[j + 32 * k] = b[k];
         }
-        if (p.err && (bad || bad_len))
-            atomicOr(p.err, (bad ? PA_DEVERR_BAD_BLOCK : 0u) | (bad_len ? PA_DEVERR_BAD_LEN : 0u));
+        if (p.err && lane == 0 && (len < 0 || len > most))
+            atomicOr(p.err, PA_DEVERR_BAD_LEN);
     }
     if (gtid == 0) {
         p.status[0] = moves;
