@@ -626,10 +626,12 @@ PA_API pa_status pa_compact_kv(void *k_cache, void *v_cache, const int32_t *keep
  *   num_draft     1 .. 256;  vocab_size 1 .. 2^30
  * A drafted token outside the vocabulary, or with a parent that does not come
  * before it, is left out and flagged (PA_DEVERR_BAD_INDEX).  Probabilities are
- * taken as given (rows are not normalised); an entry that is NaN in p or q
- * counts as w = 0; a row with entries outside [0, 1] gives some token of the
- * vocabulary or -1.  w and its sums are exact to about 2^-46, so a token depends on
- * no rounding of 32 bits, and the same inputs give the same tokens on every call.
+ * taken as given (rows are not normalised, and may have any sum up to 2^100); an
+ * entry that is NaN in p, or in q while a > 0, counts as w = 0, and a drafted token
+ * of such an entry is rejected; a row with negative or infinite entries gives some token
+ * of the vocabulary or -1.  w and its sums are exact to about 2^-46 (of the sum, where
+ * that is 16 or more), so a token depends on no rounding of 32 bits, and the same
+ * inputs give the same tokens on every call.
  * Outputs must not overlap inputs.
  */
 PA_API pa_status pa_verify_drafts(int32_t *accept_lens, int32_t *accepted, int32_t *tokens, const void *target_probs,

@@ -14,8 +14,8 @@
 // A drawn token must not hang on how a sum was rounded, so weights are summed to
 // about 46 bits: p - q as fp32 value and error, lanes' sums as pairs of floats (their
 // roundings kept), everything past a lane in 64-bit fixed point (2^-54, in smaller
-// units again where that comes to less than 2^-20), the walk's own numbers again as
-// pairs of floats.  fp64 arithmetic would be the limit here.
+// units again where that comes to less than 2^-20, in larger ones where a row that is not
+// normalised comes to 16 or more), the walk's own numbers again as pairs of floats.  fp64 arithmetic would be the limit here.
 //
 // A sequence is a cluster of CTAs, each taking a share of the vocabulary, a warp a
 // contiguous slice of it.  The first CTA gathers what the walk needs (every drafted
@@ -50,6 +50,11 @@ constexpr int kVerifyMaxCluster = 8;
 constexpr int kFixedBits = 54;
 // Sums below 2^-20 are taken again in smaller units.
 constexpr unsigned long long kSmallSum = 1ull << 34;
+// From 2^58 units (16) on they are taken again in units 2^12 times larger.  Every lane's, warp's and
+// CTA's sum counts about this much at most, so none wraps, and a total below it has not been cut.
+constexpr unsigned long long kLargeSum = 1ull << 58;
+constexpr int kLargeStep = 12;
+constexpr int kLeastBits = kFixedBits - 10 * kLargeStep;  // sums up to 2^124
 
 // A number as two floats, hi + lo with |lo| <= ulp(hi) / 2: about 48 bits.  (One thread's fp64
 // instructions took longer than a pass over a row.)
@@ -194,8 +199,8 @@ template <bool Unit> __device__ inline Weight weight(float p, float q, float ah,
     return __fadd_rn(d, e) > 0 ? Weight{d, e} : Weight{0.f, 0.f};
 }
 
-// x >= 0, below 2^9, in units of 2^-bits (54 at least), rounded down.  (Integer
-// arithmetic: fp64 conversions are slow.)
+// x >= 0 in units of 2^-bits, rounded down; 2^63 or more where it is not below that (NaN and
+// infinities among it).  (Integer arithmetic: fp64 conversions are slow.)
 __device__ inline unsigned long long fixed(float x, int bits) {
     const uint32_t b = __float_as_uint(x);
     const int e = static_cast<int>(b >> 23) & 0xff;
@@ -206,6 +211,10 @@ __device__ inline unsigned long long fixed(float x, int bits) {
 __device__ inline unsigned long long fixed(float hi, float lo, int bits) {
     const unsigned long long a = fixed(hi, bits), b = fixed(fabsf(lo), bits);
     return lo < 0 ? (a > b ? a - b : 0) : a + b;
+}
+// Of a lane's sum; kLargeSum where hi is not below that (or, in units that no such sum asks for, 2^-126).
+__device__ inline unsigned long long fixed_sum(float hi, float lo, int bits) {
+    return static_cast<int>(__float_as_uint(hi) >> 23) < max(127 + 58 - bits, 1) ? fixed(hi, lo, bits) : kLargeSum;
 }
 
 __device__ inline float to_f(float x) { return x; }
@@ -261,7 +270,7 @@ __device__ inline void leave_out(Entries<T, E> *p, int n, int base, int lane, co
 }
 
 // Sum of the weights of [lo, hi) in units of 2^-bits (every lane gets it), entries in
-// gone[] left out (Mode kRowP only).
+// gone[] left out (Mode kRowP only); a lane's counts kLargeSum at most.
 template <typename T, int E, int Mode>
 __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, int hi, float ah, float al,
                                         const int *gone, int ngone, int bits, int lane) {
@@ -305,7 +314,7 @@ __device__ unsigned long long slice_sum(const T *prow, const T *qrow, int lo, in
     const float2 hs = f2_get(h2), ls = f2_get(l2);
     const Pair sum = two_sum(hs.x, hs.y);
     const float h = sum.hi, l = __fadd_rn(sum.lo, __fadd_rn(ls.x, ls.y));
-    return warp_add(fixed(h, l, bits));
+    return warp_add(fixed_sum(h, l, bits));
 }
 
 // The first entry of [lo, hi) whose running sum exceeds t, entries in gone[] left
@@ -447,14 +456,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     float ah, al;
     int mode, parity = 0;
     unsigned long long total = 0;
-    int bits = kFixedBits;  // more where the sum is small
-    for (bool again = false, smaller = false;;) {
-        if (tid == 0 && !again && !smaller)
+    int bits = kFixedBits;  // more where the sum is small, less where it is large
+    for (bool again = false, rescaled = false;;) {
+        if (tid == 0 && !again && !rescaled)
             sh->need = walk<HasQ>(sh);
         __syncthreads();
         const int need = sh->need;
         if (need != kWalkDone) {
-            if (!smaller)
+            if (!rescaled)
                 bits = kFixedBits;
             const int node = sh->node;
             prow = target + static_cast<long long>(node + 1) * p.target_stride;
@@ -473,7 +482,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 sh->warp_sum[warp] = sum;
             __syncthreads();
             if (warp == 0) {
-                const unsigned long long mine = warp_add(lane < kVerifyWarps ? sh->warp_sum[lane] : 0ull);
+                const unsigned long long of_warp = lane < kVerifyWarps ? sh->warp_sum[lane] : 0ull;
+                const unsigned long long mine = min(warp_add(min(of_warp, kLargeSum)), kLargeSum);
                 if (lane < ranks) {
                     VerifyShared *to = ranks > 1 ? cluster.map_shared_rank(sh, lane) : sh;
                     to->total[parity][rank] = mine;
@@ -490,10 +500,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 total += x.x + x.y;
             }
             parity ^= 1;
-            smaller = total < kSmallSum && bits < kFixedBits + 150;  // (fp32 ends at 2^-149)
-            if (smaller) {
-                bits += total ? 20 : 50;
-                continue;
+            rescaled = false;
+            if (total - kSmallSum >= kLargeSum - kSmallSum) {  // below kSmallSum, or kLargeSum and more
+                const bool large = total >= kLargeSum;
+                rescaled = large ? bits > kLeastBits : bits < kFixedBits + 150;  // (fp32 ends at 2^-149)
+                if (rescaled) {
+                    bits += large ? -kLargeStep : (total ? 20 : 50);
+                    continue;
+                }
             }
             if (tid == 0) {
                 sh->s = pair_of(total, bits);
@@ -536,7 +550,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     unsigned long long t = u >= 1.f ? total - 1 : (u > 0.f ? __umul64hi(total, fixed(u, 64)) : 0ull);
     int owner = 0;
     parity ^= 1;
-    // (bounded: entries that are no probabilities may have made the sums wrap)
+    // (bounded: sums of infinite entries are cut)
     while (owner < ranks - 1 && t >= sh->total[parity][owner])
         t -= sh->total[parity][owner++];
     if (rank != owner)
