@@ -684,7 +684,9 @@ PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_
  * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
  * to 2^-40 of a row's largest element, fp32 queries to 2^-33, softmax weights to
  * 22 bits (at worst 2^-32 of the largest of their (query head, block)); q and
- * q * scale may be as large as 2^100.  What codes and scales hold outside the
+ * q * scale may be as large as 2^100, V (code * scale) as 2^80, and V scales of any
+ * sizes may follow one another; of a sequence's kv head what lies below 2^-80 of its
+ * largest |V| need not be kept.  What codes and scales hold outside the
  * attended tokens has no influence, E4M3 NaN codes (which no append writes) among it.
  * The table holds at most 2^30 tokens a sequence.
  *   workspace   pa_decode_block_quant_workspace_size() bytes, 16-byte aligned

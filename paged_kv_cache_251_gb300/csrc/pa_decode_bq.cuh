@@ -29,7 +29,8 @@
 // heads fill the columns: fp32 queries are then three sets of them, and what fp16 leaves
 // of a weight is a second product (22 bits, down to 2^-32 of the largest).  K scales multiply the scores.  V scales multiply
 // the weights before they are rounded, as a power of two that O is kept in, moved when a
-// scale exceeds it or lies 2^10 below, and a factor of at most 1.
+// scale exceeds it or lies 2^10 below (down only while O stays below 2^120), and a factor of
+// at most 1.  Blocks of one iteration whose scales lie further apart are taken one by one.
 //
 // The running maximum is kept as it was until a score exceeds it by 2^8, so a tile
 // normally needs one vote of the warp and no shuffles.
@@ -457,21 +458,42 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
 
             // V scales as a power of two (of o) and a factor of the weights
             float v_unit = 1.f, v_inv = 1.f;
+            auto unit_for = [](float top) {  // its exponent: 2^(e - 127) >= top
+                const int e = static_cast<int>(__float_as_uint(top) >> 23) + 1;
+                return e > 252 ? 252 : (e < 2 ? 2 : e);
+            };
+            // (lowered no further than O stays below 2^120, whatever its heads hold)
             auto set_unit = [&](float top) {
                 if (!(top < INFINITY))
                     return;
-                int e = static_cast<int>(__float_as_uint(top) >> 23) + 1;  // 2^(e - 127) >= top
-                e = e > 252 ? 252 : (e < 2 ? 2 : e);
-                const float unit = __uint_as_float(static_cast<uint32_t>(e) << 23);
-                const float inv = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                const float f = v_unit * inv;
-                v_unit = unit;
-                v_inv = inv;
+                const int e = unit_for(top);
+                const int from = static_cast<int>(__float_as_uint(v_unit) >> 23);
+                int shift = from - e;  // log2 of O's factor
+                uint32_t most = 0;  // (a head that is NaN or infinite must not hold the others)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t x = __float_as_uint(o[i][c]) & 0x7fffffffu;
+                        most = max(most, x < 0x7f800000u ? x : 1u);
+                    }
+                most = __reduce_max_sync(0xffffffffu, most);
+                const int room = 127 + 120 - static_cast<int>(most >> 23);
+                if (most >= 0x00800000u && shift > room)
+                    shift = room > 0 ? room : 0;
+                v_unit = __uint_as_float(static_cast<uint32_t>(from - shift) << 23);
+                v_inv = __uint_as_float(static_cast<uint32_t>(254 - from + shift) << 23);
+                if (most == 0)
+                    return;
+                // (in two steps: fp32 holds no 2^250)
+                const int half = shift / 2;
+                const float f0 = __uint_as_float(static_cast<uint32_t>(127 + half) << 23);
+                const float f1 = __uint_as_float(static_cast<uint32_t>(127 + shift - half) << 23);
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        o[i][c] *= f;
+                        o[i][c] = o[i][c] * f0 * f1;
             };
 
             // The copies run two iterations ahead: K of one is started when K of the one two
@@ -532,6 +554,18 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
             auto copy_v = [&](int it, const Ahead &a) {
                 copy_halves((kBqStages + (it & 1)) * kBqStage, v_lane, a);
             };
+            auto scale_range = [&](float &top, float &low) {  // of the present iteration's V scales but 0
+                top = 0.f, low = INFINITY;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        const float vs = fabsf(now.vs[u][b]);
+                        top = fmaxf(top, vs);
+                        if (U * NB > 1)
+                            low = fminf(low, vs > 0 ? vs : INFINITY);
+                    }
+            };
             auto inside = [&](int tok, bool ok) { return tok >= sp.start && tok < sp.end && ok; };
 
             copy_k(k0);
@@ -546,7 +580,20 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
             if (k0 + 1 < k1)
                 copy_v(k0 + 1, next);
             copy_commit();
-            for (int it = k0; it < k1; ++it) {
+            {
+                float top, low;
+                scale_range(top, low);
+                if (top > 0 && top < INFINITY) {
+                    v_unit = __uint_as_float(static_cast<uint32_t>(unit_for(top)) << 23);
+                    v_inv = __uint_as_float(static_cast<uint32_t>(254 - unit_for(top)) << 23);
+                }
+            }
+            // Of an iteration whose blocks' V scales lie so far apart that one's weights would be lost
+            // beside another's: the block of this pass over it; else -1.  (A second copy of the loop's
+            // body for them costs all other iterations 2 to 4 %, a loop around half of it 3 to 16, this 0 to 2.)
+            constexpr int kBlocks = U * NB;
+            int only = -1;
+            for (int it = k0; it < k1;) {
                 float x[U][4];
                 bool full[U];
                 copy_wait<3>();  // K of this iteration is there (V, and K and V of the next, may not be)
@@ -591,16 +638,20 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                         x[u][3] = in1 ? x[u][3] : -INFINITY;
                     }
                 }
-                float top = 0.f;
+                // V scales: whether O's unit has to move
+                float top, low;
+                scale_range(top, low);
+                const bool apart = kBlocks > 1 && low < top * kLowScale;
+                if (apart) {
+                    only = only < 0 ? 0 : only;
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        top = fmaxf(top, fabsf(now.vs[u][b]));
-                if (top > v_unit || (top < v_unit * kLowScale && top > 0))
-                    set_unit(top);
+                    for (int i = 0; i < kBlocks; ++i)
+                        top = only == i ? fabsf(now.vs[i / NB][i % NB]) : top;
+                }
+                const bool moves = top > v_unit || (top < v_unit * kLowScale && top > 0);
+                const bool last = !apart || only == kBlocks - 1;  // pass over the iteration
                 __syncwarp();  // (every lane has read this iteration's K)
-                if (it + 2 < k1)
+                if (it + 2 < k1 && last)
                     copy_k(it + 2);
                 copy_commit();
                 // the running maximum moves only when it is exceeded by kMaxSlack
@@ -634,9 +685,15 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                 }
                 copy_wait<3>();  // V is there
                 __syncwarp();
+                if (moves)  // (behind the maximum: O has lost what that makes nothing of)
+                    set_unit(top);
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const float r0 = now.vs[u][0] * v_inv, r1 = now.vs[u][NB - 1] * v_inv;
+                    float r0 = now.vs[u][0] * v_inv, r1 = now.vs[u][NB - 1] * v_inv;
+                    if (kBlocks > 1 && only >= 0) {
+                        r0 = only == u * NB ? r0 : 0.f;
+                        r1 = only == u * NB + NB - 1 ? r1 : 0.f;
+                    }
                     // weights as the second product's operand: tokens 2t.. and 2t + 8..
                     uint32_t pf[Wide ? 2 : 1][2];
                     {
@@ -644,8 +701,10 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             e[c] = ex2(x[u][c] - base[c & 1]);
-                        l[0] += e[0] + e[2];
-                        l[1] += e[1] + e[3];
+                        if (kBlocks == 1 || only <= 0) {
+                            l[0] += e[0] + e[2];
+                            l[1] += e[1] + e[3];
+                        }
                         e[0] *= r0, e[1] *= r0, e[2] *= r1, e[3] *= r1;
                         const uint32_t h0 = pack_half(e[0], e[1]), h1 = pack_half(e[2], e[3]);
                         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
@@ -689,11 +748,17 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                         }
                 }
                 __syncwarp();
-                if (it + 2 < k1)
+                if (it + 2 < k1 && last)
                     copy_v(it + 2, after);
                 copy_commit();
+                if (!last) {
+                    ++only;
+                    continue;
+                }
+                only = -1;
                 now = next;
                 next = after;
+                ++it;
             }
 
             // Of four heads: the low parts of the weights join the high ones and the lane gets one
