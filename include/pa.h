@@ -683,7 +683,7 @@ PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_
  * same bits on every call (a sequence decoded in another batch may differ in the
  * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
  * to 2^-40 of a row's largest element, fp32 queries to 2^-33, softmax weights to
- * 22 bits (at worst 2^-32 of the largest of their (query head, block)); q and
+ * 2^-22 of themselves or 2^-34 of their query head's largest, whichever is more; q and
  * q * scale may be as large as 2^100, V (code * scale) as 2^80, and V scales of any
  * sizes may follow one another; of a sequence's kv head what lies below 2^-80 of its
  * largest |V| need not be kept.  What codes and scales hold outside the

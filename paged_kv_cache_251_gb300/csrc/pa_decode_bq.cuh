@@ -25,15 +25,17 @@
 // queries, scaled to fp16 by a power of two a row (fp16 and bf16 queries: exact to
 // 2^-40 of the row's largest element); fp32 queries as three fp16 terms, the halves'
 // sums added.  For P the halves hold the weight's fp16 value and 2^11 times what that
-// leaves (22 bits together, down to 2^-50 of the largest weight).  Groups of eight
-// heads fill the columns: fp32 queries are then three sets of them, and what fp16 leaves
-// of a weight is a second product (22 bits, down to 2^-32 of the largest).  K scales multiply the scores.  V scales multiply
-// the weights before they are rounded, as a power of two that O is kept in, moved when a
-// scale exceeds it or lies 2^10 below (down only while O stays below 2^120), and a factor of
-// at most 1.  Blocks of one iteration whose scales lie further apart are taken one by one.
+// leaves.  Groups of eight heads fill the columns: fp32 queries are then three sets of
+// them, and what fp16 leaves of a weight is a second product.  K scales multiply the scores.
+// V scales multiply the weights before they are rounded, as a power of two that O is kept
+// in, moved when a scale exceeds it or lies 2^4 below (down only while O stays below 2^120),
+// and a factor of at most 1.  Blocks of one iteration whose scales lie further apart are
+// taken one by one.  So a weight is off by 2^-22 of itself, or, being small, by 2^-39 of the
+// largest so far (four heads: steps of 2^-35 below 2^7, a scale 2^-4 of the unit) or 2^-34
+// (eight: of 2^-24 below 2^13).
 //
-// The running maximum is kept as it was until a score exceeds it by 2^8, so a tile
-// normally needs one vote of the warp and no shuffles.
+// The running maximum is kept as it was until a score exceeds it by 2^8 (eight heads: 2^2),
+// so a tile normally needs one vote of the warp and no shuffles.
 //
 // Work: the tiles of all (sequence, kv head) pieces in one line, cut evenly over all
 // warps of the grid; a piece counts kPieceCost iterations more (its start and end).
@@ -69,10 +71,13 @@ constexpr int kMinShare = 8;    // iterations of a warp at least
 // tokens 6 and 10 us, of 1024 14 and 17, of 2048 23 and 19, of 8192 76 and 22; 40 of 512 14
 // and 22, of 1024 22 and 25, of 2048 39 and 39, up to 2048 32 and 23.
 constexpr int kByPieceIters = 64;
-constexpr float kMaxSlack = 8;  // log2 by which scores may exceed the running maximum
-constexpr float kPTop = 7;      // weights are at most 2^(kMaxSlack + kPTop): within fp16
+// log2 by which scores may exceed the running maximum, and of the weight at the running maximum (groups of
+// four heads and of eight): together 15, so weights are within fp16.  What fp16 leaves of eight heads'
+// weights is not scaled up, ends at 2^-25, and needs them large.
+constexpr float kMaxSlack4 = 8, kMaxSlack8 = 2;
+constexpr float kPTop4 = 7, kPTop8 = 13;
 constexpr float kPLow = 2048;   // the low part of a weight is kept times this
-constexpr float kLowScale = 1.f / 1024;  // V scales this far below O's unit move it
+constexpr float kLowScale = 1.f / 16;    // V scales this far below O's unit move it
 constexpr float kNoMax = -3.4028234e38f;  // (finite: less it, a score of -inf stays -inf)
 
 struct BqSpan {
@@ -423,6 +428,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                 start[0] = start[2] = __shfl_sync(0xffffffffu, sum, (2 * t) << 2);
                 start[1] = start[3] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) << 2);
             }
+            constexpr float kMaxSlack = Wide ? kMaxSlack8 : kMaxSlack4, kPTop = Wide ? kPTop8 : kPTop4;
             // base: the running maximum less kPTop
             float base[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, o[MT][4];
 #pragma unroll

@@ -108,3 +108,27 @@ def test_heads_of_their_own(code, bs, d, group, pattern):
     q[:, ::2, 0] = -40.0
     check_rows(q, cache)
     check_rows(q.to(torch.float16), cache)
+
+
+@pytest.mark.parametrize("code", [I8, E4M3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bs,d,group", [(16, 64, 4), (16, 64, 8), (8, 64, 8), (32, 128, 8), (16, 128, 2)])
+@pytest.mark.parametrize("size", [1.0, 0.13, 0.0021, 1e-5])
+def test_small_weights_of_small_scales_add_up(code, dtype, bs, d, group, size):
+    """One token of weight one, then 8192 of 2^-16 to 2^-18.6 in blocks whose V scales are `size` times its own,
+    and an element of V that only they have.  Its error: a weight is off by 2^-22 of itself or 2^-34 of the
+    largest (2^-15 of these), a score of 20 by 2^-19, sums of some 64 steps by 2^-17; together below 2^-14.
+    (2^-25 of a weight of 2^7 that a scale of 2^-10 of the unit multiplies is 2^-22 of the largest.)"""
+    kc, vc, ks, vs, tables, lens = paged(torch.Generator().manual_seed(26), [bs + 8192], 1, bs, d, code)
+    first = int(tables[0, 0])
+    kc, vc = kc.float().zero_(), vc.float().zero_()
+    ks.fill_(1.0), vs.fill_(size)
+    vs[first] = 1.0
+    kc[first, 0, 0, 0] = 16
+    vc[:, :, :, 1] = 64
+    vc[first] = 0
+    q = torch.zeros((1, group, d))
+    q[0, :, 0] = 0.6931 * (1.0 + 0.023 * torch.arange(group))
+    q, cache = q.to(dtype), [kc.to(code), vc.to(code), ks, vs, tables, lens]
+    got, want = decode(q, cache, scale=1.0), speclib.decode_block_quant(q, *cache, scale=1.0)
+    assert ((got - want)[0, :, 1].abs() <= 2.0 ** -14 * want[0, :, 1]).all(), ((got - want) / want)[0, :, 1]
