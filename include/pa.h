@@ -682,8 +682,9 @@ PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_
  * contexts of the whole batch are cut evenly over the GPU.  The same inputs give the
  * same bits on every call (a sequence decoded in another batch may differ in the
  * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
- * to 2^-40 of a row's largest element, fp32 queries to 2^-33, softmax weights to
- * 2^-22 of themselves or 2^-34 of their query head's largest, whichever is more; q and
+ * to 2^-40 of a row's largest element, fp32 queries to 2^-33; products with the codes
+ * are exact and summed in fp32 (a score is off by 20 * 2^-24 of scale * sum |q k| at
+ * most); softmax weights are good to 2^-22 of themselves or 2^-34 of their query head's largest, whichever is more; q and
  * q * scale may be as large as 2^100, V (code * scale) as 2^80, and V scales of any
  * sizes may follow one another; of a sequence's kv head what lies below 2^-80 of its
  * largest |V| need not be kept.  What codes and scales hold outside the

@@ -17,9 +17,8 @@
 // with its register operands is the right one here: tcgen05 wants both operands of
 // 16 bits in shared memory, and the codes are 8.
 //
-// Codes become fp16 exactly.  K, INT8: code + 128 in the low byte of an fp16 is that
-// times 2^-24, and the scores start at -128 times the queries' sum.  V, INT8: the low
-// byte of 1024 + 128 + code, less 1152.  E4M3: converted by the hardware.
+// Codes become fp16 exactly.  INT8: the low byte of 1024 + 128 + code, less 1152.  E4M3:
+// converted by the hardware.
 //
 // The eight columns are four heads twice.  For S both halves hold the same
 // queries, scaled to fp16 by a power of two a row (fp16 and bf16 queries: exact to
@@ -125,13 +124,19 @@ __device__ inline uint32_t e4m3_pair(uint32_t w, bool high) {
     return y;
 }
 
+// Codes + 128 in the low bytes of two fp16 of 1024 + 128, to the codes, exactly.
+__device__ inline uint32_t unbias(uint32_t w) {
+    const __half2 bias = __half2(__half_raw{0x6480}, __half_raw{0x6480});
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&w), bias);
+    return *reinterpret_cast<const uint32_t *>(&x);
+}
+
 // K: four adjacent codes as two pairs of fp16.  E4M3: dims (0, 1), (2, 3).  INT8: dims
-// (0, 2), (1, 3), as code + 128 in the low bits of the fp16, which is that times 2^-24
-// (the queries' sums times 128 are taken off where the scores start).
+// (0, 2), (1, 3).
 template <int Fmt> __device__ inline void k_pairs(uint32_t w, uint32_t &a, uint32_t &b) {
     if (Fmt == kFmtI8) {
-        a = (w ^ 0x80808080u) & 0x00ff00ffu;
-        b = __byte_perm(w, 0, 0x4341) ^ 0x00800080u;
+        a = unbias((w & 0x00ff00ffu) ^ 0x64806480u);
+        b = unbias(__byte_perm(w, 0, 0x4341) ^ 0x64806480u);
     } else {
         a = e4m3_pair(w, false);
         b = e4m3_pair(w, true);
@@ -140,20 +145,13 @@ template <int Fmt> __device__ inline void k_pairs(uint32_t w, uint32_t &a, uint3
 template <int Fmt> __device__ constexpr int k_dim(int pair, int i) {  // dim of pair's element i
     return Fmt == kFmtI8 ? 2 * i + pair : 2 * pair + i;
 }
-template <int Fmt> __device__ constexpr float k_unit() { return Fmt == kFmtI8 ? 16777216.f : 1.f; }
 
-// V: dims 2i and 2i + 1 (i = half) of four of tokens a and b, each as the pair (a, b).  INT8 as
-// 1024 + 128 + code less 1152.
+// V: dims 2i and 2i + 1 (i = half) of four of tokens a and b, each as the pair (a, b).
 template <int Fmt> __device__ inline void v_pairs(uint32_t wa, uint32_t wb, int half, uint32_t &x, uint32_t &y) {
     if (Fmt == kFmtI8) {
         const uint32_t z = __byte_perm(wa, wb, half ? 0x7632 : 0x5410);  // a, a', b, b'
-        const uint32_t even = (z & 0x00ff00ffu) ^ 0x64806480u;
-        const uint32_t odd = __byte_perm(z, 0, 0x4341) ^ 0x64806480u;
-        const __half2 bias = __half2(__half_raw{0x6480}, __half_raw{0x6480});
-        const __half2 e = __hsub2(*reinterpret_cast<const __half2 *>(&even), bias);
-        const __half2 o = __hsub2(*reinterpret_cast<const __half2 *>(&odd), bias);
-        x = *reinterpret_cast<const uint32_t *>(&e);
-        y = *reinterpret_cast<const uint32_t *>(&o);
+        x = unbias((z & 0x00ff00ffu) ^ 0x64806480u);
+        y = unbias(__byte_perm(z, 0, 0x4341) ^ 0x64806480u);
     } else {
         const uint32_t z = __byte_perm(wa, wb, half ? 0x7362 : 0x5140);  // a, b, a', b'
         x = e4m3_pair(z, false);
@@ -369,7 +367,6 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
             // queries as fragments; their power of two
             uint32_t qf[QS][KW][2];
             float qs[2];     // of the lane's two columns: scale * log2 e / the power of two
-            float start[4];  // where the scores start
             {
                 const int h = Wide ? g : g & 3;
                 float x[KW * 4], top = 0.f;
@@ -386,8 +383,7 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                 e = e < -100 ? -100 : (e > 100 ? 100 : e);
                 const float up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
                 const float down =
-                    __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * (p.scale_log2 * k_unit<Fmt>());
-                float sum = 0.f;
+                    __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23) * p.scale_log2;
 #pragma unroll
                 for (int ks = 0; ks < KW; ++ks)
 #pragma unroll
@@ -412,21 +408,13 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
                             }
                         }
 #pragma unroll
-                        for (int q = 0; q < QS; ++q) {
+                        for (int q = 0; q < QS; ++q)
                             qf[q][ks][b] = pack_half(y[q][0], y[q][1]);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qf[q][ks][b]));
-                            sum += f.x + f.y;
-                        }
                     }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                sum = Fmt == kFmtI8 ? sum * (-128.f / k_unit<Fmt>()) : 0.f;
                 // columns 2t, 2t + 1 are those of lanes g = 2t, 2t + 1 (of four heads: modulo 4)
                 const int from = Wide ? 2 * t : 2 * (t & 1);
                 qs[0] = __shfl_sync(0xffffffffu, down, from << 2);
                 qs[1] = __shfl_sync(0xffffffffu, down, (from + 1) << 2);
-                start[0] = start[2] = __shfl_sync(0xffffffffu, sum, (2 * t) << 2);
-                start[1] = start[3] = __shfl_sync(0xffffffffu, sum, (2 * t + 1) << 2);
             }
             constexpr float kMaxSlack = Wide ? kMaxSlack8 : kMaxSlack4, kPTop = Wide ? kPTop8 : kPTop4;
             // base: the running maximum less kPTop
@@ -615,11 +603,13 @@ __global__ void __launch_bounds__(kDecodeBqThreads, Wide && QT == 3 ? 2 : kDecod
 #pragma unroll
                     for (int ks = 0; ks < KW; ++ks) {
                         uint32_t a[4];
+                        if (ks == 0)
+                            x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
                         k_pairs<Fmt>(kr[0][ks], a[0], a[2]);
                         k_pairs<Fmt>(kr[1][ks], a[1], a[3]);
 #pragma unroll
                         for (int q = 0; q < QS; ++q)
-                            mma16(x[u], a, qf[q][ks][0], qf[q][ks][1], ks == 0 && q == 0 ? start : x[u]);
+                            mma16(x[u], a, qf[q][ks][0], qf[q][ks][1], x[u]);
                     }
                     const float ks0 = now.ks[u][0], ks1 = now.ks[u][NB - 1];
                     if (QT == 3 && !Wide) {  // the terms' halves
