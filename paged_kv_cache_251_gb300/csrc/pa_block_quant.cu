@@ -239,8 +239,11 @@ __device__ inline void store_unit(const AppendBqParams &p, long long block, int 
                 Q8<Fmt>::widen4(before.x, f);
                 Q8<Fmt>::widen4(before.y, f + 4);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+                for (int e = 0; e < 8; ++e) {
                     f[e] = __fmul_rn(f[e], old);
+                    if (Fmt == kFmtE4M3)  // (NaN codes, which only a pool of any contents holds)
+                        f[e] = f[e] != f[e] ? 0.f : f[e];
+                }
                 *at = code(f);
             }
     }
