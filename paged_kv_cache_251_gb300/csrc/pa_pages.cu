@@ -162,6 +162,22 @@ __device__ inline void load_counts(const int32_t *from, int b, int end, int none
     }
 }
 
+// Of four consecutive blocks with counts c: where they are, ~ that of those without a count.
+__device__ inline void store_places(int32_t *to, int b, int end, const int *c) {
+    int x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        x[k] = c[k] > 0 ? b + k : ~(b + k);
+    if (b + 4 <= end && (reinterpret_cast<uintptr_t>(to + b) & 15u) == 0) {
+        *reinterpret_cast<int4 *>(to + b) = make_int4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (b + k < end)
+                to[b + k] = x[k];
+    }
+}
+
 constexpr int kTile = 4 * kPageThreads;  // counts of a CTA at once
 
 // A CTA's share of the blocks: whole groups of four.
@@ -180,21 +196,19 @@ __device__ inline int row_part(int max_blocks, int rows, int warps, int *parts) 
     return part;
 }
 
-// What the entries that rows hold tell of: blocks outside the pool, and blocks that no reference
-// counts, which go out as free ones, too.  row_at(i, &from): how many entries row i holds, and where.
-// The warps of a CTA take rows from the last warp on (in the update the first have needs to find
-// meanwhile).  Only calls with an error word pay for it: an update of 256 rows 0.6 to 1.0 us, of 2048
-// rows 5.0 us.
-template <typename RowAt>
-__device__ inline uint32_t entry_errors(const int32_t *count, int num_blocks, int max_blocks, int rows, int rank,
-                                        int ranks, int warp, int lane, RowAt row_at) {
+// What the entries that the update's rows keep tell of: blocks outside the pool, and blocks that no
+// reference counts any more, which go out as free ones, too.  The warps of a CTA take rows from the
+// last warp on (the first have needs to find meanwhile).  Only calls with an error word pay for it:
+// with 256 rows 0.6 to 1 us, with 1024 or 2048 4 to 5 (a gather of every entry's count).
+__device__ inline uint32_t kept_errors(const PagesUpdateParams &p, int rank, int ranks, int warp, int lane) {
     uint32_t bad = 0;
     int parts;
-    const int warps = ranks * kPageWarps, part = row_part(max_blocks, rows, warps, &parts);
-    const long long items = static_cast<long long>(rows) * parts;
+    const int warps = ranks * kPageWarps, part = row_part(p.max_blocks, p.rows, warps, &parts);
+    const long long items = static_cast<long long>(p.rows) * parts;
     for (long long u = rank + ranks * (kPageWarps - 1 - warp); u < items; u += warps) {
-        const int32_t *from;
-        const int j0 = static_cast<int>(u % parts) * part, j1 = min(row_at(static_cast<int>(u / parts), &from), j0 + part);
+        const int i = static_cast<int>(u / parts), j0 = static_cast<int>(u % parts) * part;
+        const int kept = __ldcg(p.kept + i), parent = p.parents ? p.parents[i] : i, j1 = min(kept, j0 + part);
+        const int32_t *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
         for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
             int b[kAhead], c[kAhead];
 #pragma unroll
@@ -202,9 +216,9 @@ __device__ inline uint32_t entry_errors(const int32_t *count, int num_blocks, in
                 b[k] = j + 32 * k < j1 ? from[j + 32 * k] : -1;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const bool inside = b[k] >= 0 && b[k] < num_blocks;
+                const bool inside = b[k] >= 0 && b[k] < p.num_blocks;
                 bad |= inside || j + 32 * k >= j1 ? 0u : PA_DEVERR_BAD_BLOCK;
-                c[k] = inside ? __ldcg(count + b[k]) : 1;
+                c[k] = inside ? __ldcg(p.count + b[k]) : 1;
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
@@ -331,12 +345,7 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_update_kernel(const Pag
     load_counts(p.count, b0 + 4 * tid, b1, 1, c);
     uint32_t bad = 0;
     if (p.err)
-        bad = entry_errors(p.count, p.num_blocks, p.max_blocks, p.rows, rank, ranks, tid >> 5, lane,
-                           [&](int i, const int32_t **from) {
-                               const int kept = __ldcg(p.kept + i), parent = p.parents ? p.parents[i] : i;
-                               *from = p.tables + static_cast<long long>(kept ? parent : 0) * p.max_blocks;
-                               return kept;
-                           });
+        bad = kept_errors(p, rank, ranks, tid >> 5, lane);
     long long needs = 0;
     int copies = 0;
     for (int at = i0; at < i1; at += kPageThreads) {
@@ -496,15 +505,6 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         sh->sum = 0;
     if (tid < 2 * kPageMaxCluster)
         (&sh->total[0][0])[tid] = 0;
-    if (p.err) {  // (before tables and counts change in place)
-        const uint32_t bad = entry_errors(p.refs, p.num_blocks, p.max_blocks, p.rows, rank, ranks, tid >> 5, lane,
-                                          [&](int i, const int32_t **from) {
-                                              *from = p.tables + static_cast<long long>(i) * p.max_blocks;
-                                              return blocks_of(held_len(p, i), p.block_size);
-                                          });
-        if (bad)
-            atomicOr(p.err, bad);
-    }
     cluster.sync();  // (before another CTA's count)
     {
         int mine = 0;
@@ -538,6 +538,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
         const int b = t0 + 4 * tid;
         int c[4], n = 0;
         load_counts(p.refs, b, b1, 0, c);
+        if (p.err)
+            store_places(p.place, b, b1, c);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             n += c[k] > 0;
@@ -579,6 +581,8 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
             src = __ldcg(p.src_list + k);
             dst = __ldcg(p.dst_list + k);
             p.remap[src] = dst;
+            if (p.err)
+                p.place[src] = dst;
             p.new_refs[dst] = __ldcg(p.new_refs + src);
             p.new_refs[src] = 0;
         }
@@ -589,28 +593,46 @@ __global__ void __launch_bounds__(kPageThreads, 1) pages_compact_kernel(const Pa
     int parts;
     const int part = row_part(p.max_blocks, p.rows, gwarps, &parts);
     const long long most = static_cast<long long>(p.max_blocks) * p.block_size;
+    // (with an error word: blocks without a count, free ones to all others, are told of where a row holds them;
+    // 0.5 us with 256 rows)
+    const int32_t *place = p.err ? p.place : p.remap;
     for (long long u = gwarp; u < static_cast<long long>(p.rows) * parts; u += gwarps) {
         const int i = static_cast<int>(u / parts), j0 = static_cast<int>(u % parts) * part;
         const int j1 = min(p.max_blocks, j0 + part);
         const int len = p.lens[i], n = blocks_of(held_len(p, i), p.block_size);
+        uint32_t bad = len < 0 || len > most ? PA_DEVERR_BAD_LEN : 0u;
         const int32_t *from = p.tables + static_cast<long long>(i) * p.max_blocks;
         int32_t *to = p.new_tables + static_cast<long long>(i) * p.max_blocks;
         for (int j = j0 + lane; j < j1; j += 32 * kAhead) {
             int b[kAhead];
+            unsigned inside = 0;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 b[k] = j + 32 * k < j1 && j + 32 * k < n ? from[j + 32 * k] : -1;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (b[k] >= 0 && b[k] < p.num_blocks)
-                    b[k] = __ldcg(p.remap + b[k]);
+            for (int k = 0; k < kAhead; ++k) {
+                if (b[k] >= 0 && b[k] < p.num_blocks) {
+                    b[k] = __ldcg(place + b[k]);
+                    inside |= 1u << k;
+                } else if (j + 32 * k < j1 && j + 32 * k < n) {
+                    bad |= PA_DEVERR_BAD_BLOCK;
+                }
+            }
+            if (p.err) {
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (inside >> k & 1 && b[k] < 0) {
+                        b[k] = ~b[k];
+                        bad |= PA_DEVERR_BAD_COUNT;
+                    }
+            }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (j + 32 * k < j1)
                     to[j + 32 * k] = b[k];
         }
-        if (p.err && lane == 0 && (len < 0 || len > most))
-            atomicOr(p.err, PA_DEVERR_BAD_LEN);
+        if (p.err && bad)
+            atomicOr(p.err, bad);
     }
     if (gtid == 0) {
         p.status[0] = moves;

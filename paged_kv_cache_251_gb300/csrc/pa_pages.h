@@ -29,6 +29,7 @@ struct PagesCompactParams {
     int32_t *status;      // [4]
     const int32_t *tables, *refs, *lens;
     int32_t *src_list, *dst_list;  // workspace, [num_blocks] each
+    int32_t *place;                // workspace, [num_blocks] (with err): remap, ~b of blocks without a count
     uint32_t *err;
     int rows, max_blocks, num_blocks, block_size, max_moves;
 };

@@ -368,6 +368,7 @@ pa_status pa_pages_compact(int32_t *new_tables, int32_t *new_ref_counts, int32_t
     p.lens = lens;
     p.src_list = static_cast<int32_t *>(workspace);
     p.dst_list = p.src_list + num_blocks;
+    p.place = p.dst_list + num_blocks;
     p.err = err_word;
     p.rows = num_rows;
     p.max_blocks = max_blocks_per_seq;
