@@ -660,7 +660,8 @@ PA_API pa_status pa_verify_drafts(int32_t *accept_lens, int32_t *accepted, int32
  * and where the scale grew, all other rows of the block are coded again:
  * code * scale before (rounded to fp32) / scale, rounded likewise.  So a
  * block's values may move by half a step of the new scale whenever a later token
- * enlarges it.  A block whose row 0 was never written needs a scale (0 will do).
+ * enlarges it: a drafted token that is rejected and written over, too, for the scale
+ * stays until row 0 is written again.  A block whose row 0 was never written needs a scale (0 will do).
  * Two tokens must not name one slot (one of them is stored, unspecified which).
  *   workspace   pa_append_kv_block_quant_workspace_size() bytes, 4-byte
  *               aligned, of any contents (may be NULL when that size is 0)
@@ -684,12 +685,14 @@ PA_API size_t pa_append_kv_block_quant_workspace_size(int num_tokens, int block_
  * last bits, where its context is cut elsewhere).  fp16 / bf16 queries are exact
  * to 2^-40 of a row's largest element, fp32 queries to 2^-33; products with the codes
  * are exact and summed in fp32 (a score is off by 20 * 2^-24 of scale * sum |q k| at
- * most); softmax weights are good to 2^-22 of themselves or 2^-34 of their query head's largest, whichever is more; q and
- * q * scale may be as large as 2^100, V (code * scale) as 2^80, and V scales of any
- * sizes may follow one another; of a sequence's kv head what lies below 2^-80 of its
- * largest |V| need not be kept.  What codes and scales hold outside the
- * attended tokens has no influence, E4M3 NaN codes (which no append writes) among it.
- * The table holds at most 2^30 tokens a sequence.
+ * most); softmax weights are good to 2^-22 of themselves or 2^-34 of their query head's
+ * largest, whichever is more; q and q * scale may be as large as 2^100, V (code *
+ * scale) as 2^80, and V scales of any sizes may follow one another; of a sequence's kv
+ * head what lies below 2^-80 of its largest |V| need not be kept.  What codes and
+ * scales hold outside the attended tokens has no influence, E4M3 NaN codes (which no
+ * append writes) among it.  The table holds at most 2^30 tokens a sequence.
+ * Drafted tokens: each as a sequence of its own, with its sequence's table
+ * (pa_decode_tree and pa_compact_kv take 16- and 32-bit caches only).
  *   workspace   pa_decode_block_quant_workspace_size() bytes, 16-byte aligned
  */
 PA_API pa_status pa_decode_block_quant(void *out, const void *q, const void *k_cache, const void *v_cache,
