@@ -23,10 +23,10 @@
 // bits.  Only a rejection with q, and the end, read a row; the slice of the warp whose
 // sum holds the token is read once more, shared by its CTA's warps, to find it.
 //
-// Measured (fp32, with q, on the GPU): 256 chains over 128000 entries 42 us, 6.2 TB/s of the
-// two rows each; 64 chains 15 us (floor 9.7: the gather, two cluster barriers and the
+// Measured (fp32, with q, on the GPU): 256 chains over 128000 entries 46 us, 5.7 TB/s of the
+// two rows each (without q 27, a row each); 64 chains 15 us (floor 9.7: the gather, two cluster barriers and the
 // search are 6); one chain over 32000 entries 7 us, all latency.  32 trees of 24
-// drafted tokens over 50257 entries, bf16: 18 us; a rejection's sum costs 3 to 4 us (two
+// drafted tokens over 50257 entries, bf16: 19 us (without q 11); a rejection's sum costs 3 to 4 us (two
 // thirds arithmetic and its barriers).  Loads held a step ahead (64 chains 19 us) and
 // twice the loads at once (19 us: one CTA an SM) were slower.
 #include <cooperative_groups.h>
