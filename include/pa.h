@@ -661,7 +661,8 @@ PA_API pa_status pa_verify_drafts(int32_t *accept_lens, int32_t *accepted, int32
  * code * scale before (rounded to fp32) / scale, rounded likewise.  So a
  * block's values may move by half a step of the new scale whenever a later token
  * enlarges it: a drafted token that is rejected and written over, too, for the scale
- * stays until row 0 is written again.  A block whose row 0 was never written needs a scale (0 will do).
+ * stays until row 0 is written again.  A block whose row 0 was never written needs a
+ * scale (0 will do).
  * Two tokens must not name one slot (one of them is stored, unspecified which).
  *   workspace   pa_append_kv_block_quant_workspace_size() bytes, 4-byte
  *               aligned, of any contents (may be NULL when that size is 0)
@@ -751,8 +752,9 @@ PA_API size_t pa_decode_block_quant_workspace_size(int num_seqs, int num_heads, 
  * entries outside the pool are carried along, hold nothing and are flagged
  * (PA_DEVERR_BAD_BLOCK).  Counts are taken as given: a count that falls below 0, and
  * a block that a row keeps while its count falls to 0 (it goes out as a free one, too),
- * are flagged (PA_DEVERR_BAD_COUNT), with or without enough free blocks.  block_size is any positive number; max_blocks_per_seq is
- * at most 2^21 - 1, its product with block_size, num_rows and num_blocks 2^30.
+ * are flagged (PA_DEVERR_BAD_COUNT), with or without enough free blocks.  block_size is
+ * any positive number; max_blocks_per_seq is at most 2^21 - 1, its product with
+ * block_size, num_rows and num_blocks 2^30.
  */
 PA_API pa_status pa_pages_update(int32_t *new_tables, int32_t *new_ref_counts, int64_t *pairs, int32_t *status,
                                  const int32_t *tables, const int32_t *ref_counts, const int32_t *lens,

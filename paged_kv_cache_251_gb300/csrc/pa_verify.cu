@@ -15,7 +15,8 @@
 // about 46 bits: p - q as fp32 value and error, lanes' sums as pairs of floats (their
 // roundings kept), everything past a lane in 64-bit fixed point (2^-54, in smaller
 // units again where that comes to less than 2^-20, in larger ones where a row that is not
-// normalised comes to 16 or more), the walk's own numbers again as pairs of floats.  fp64 arithmetic would be the limit here.
+// normalised comes to 16 or more), the walk's own numbers again as pairs of floats.  fp64
+// arithmetic would be the limit here.
 //
 // A sequence is a cluster of CTAs, each taking a share of the vocabulary, a warp a
 // contiguous slice of it.  The first CTA gathers what the walk needs (every drafted
@@ -24,11 +25,11 @@
 // sum holds the token is read once more, shared by its CTA's warps, to find it.
 //
 // Measured (fp32, with q, on the GPU): 256 chains over 128000 entries 46 us, 5.7 TB/s of the
-// two rows each (without q 27, a row each); 64 chains 15 us (floor 9.7: the gather, two cluster barriers and the
-// search are 6); one chain over 32000 entries 7 us, all latency.  32 trees of 24
-// drafted tokens over 50257 entries, bf16: 19 us (without q 11); a rejection's sum costs 3 to 4 us (two
-// thirds arithmetic and its barriers).  Loads held a step ahead (64 chains 19 us) and
-// twice the loads at once (19 us: one CTA an SM) were slower.
+// two rows each (without q 27, a row each); 64 chains 15 us (floor 9.7: the gather, two
+// cluster barriers and the search are 6); one chain over 32000 entries 7 us, all latency.
+// 32 trees of 24 drafted tokens over 50257 entries, bf16: 19 us (without q 11); a
+// rejection's sum costs 3 to 4 us (two thirds arithmetic and its barriers).  Loads held a
+// step ahead (64 chains 19 us) and twice the loads at once (19 us: one CTA an SM) were slower.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
